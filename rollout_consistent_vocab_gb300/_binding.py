@@ -62,13 +62,43 @@ class ShardArgs(ctypes.Structure):
     ]
 
 
+class KVCache(ctypes.Structure):
+    """rlk_kv_cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("B", ctypes.c_int64),
+        ("lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p),
+        ("n", ctypes.c_int32),
+        ("err_count", ctypes.c_void_p),
+    ]
+
+
+class BTHStrides(ctypes.Structure):
+    """rlk_bth_strides."""
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
 COMPUTE = ("rlk_logp_full", "rlk_logp_restricted", "rlk_logp_pair", "rlk_logp_kl", "rlk_logp_kl_ref",
            "rlk_logp_kl_host",
            "rlk_logp_backward", "rlk_logp_pair_save", "rlk_logp_backward_saved", "rlk_sample",
            "rlk_sample_noalloc", "rlk_linear_logp", "rlk_linear_logp_pair",
            "rlk_logp_shard_summary", "rlk_logp_shard_counts", "rlk_logp_merge",
            "rlk_logp_merge_resumable", "rlk_logp_shard_counts_window",
-           "rlk_sqnorm_accumulate", "rlk_sqnorm_finalize", "rlk_grad_norm")
+           "rlk_sqnorm_accumulate", "rlk_sqnorm_finalize", "rlk_grad_norm",
+           "rlk_kv_append", "rlk_paged_attention", "rlk_paged_attention_workspace")
 RLK_GRAD_BF16, RLK_GRAD_F32 = 0, 1
 EXPORTS = COMPUTE + ("rlk_status_string", "rlk_last_error", "rlk_abi_version")
 
@@ -113,6 +143,10 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.rlk_sqnorm_accumulate.argtypes = [VP, i64, i32, VP, VP]
     lib.rlk_sqnorm_finalize.argtypes = [VP, VP, VP]
     lib.rlk_grad_norm.argtypes = [VP, i64, i32, VP, VP, VP]
+    KC, BS = P(KVCache), P(BTHStrides)
+    lib.rlk_kv_append.argtypes = [KC, VP, BS, VP, BS, VP]
+    lib.rlk_paged_attention.argtypes = [KC, VP, BS, i32, f32, i32, i32, VP, BS, VP, VP, VP]
+    lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i64, P(ctypes.c_size_t)]
     for f in COMPUTE:
         getattr(lib, f).restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
@@ -755,3 +789,113 @@ def grad_norm(tensors, *, distributed=False, group=None, bins=None, out=None, st
     if distributed:
         reduce_bins_(bins, group)
     return sqnorm_finalize(bins, out, stream)
+
+
+# ----------------------------------------------------------------- paged key-value cache
+
+def _cache_dtype(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return RLK_DT_BF16
+    if t.dtype == torch.float16:
+        return RLK_DT_F16
+    raise ValueError(f"the cache's dtype {t.dtype} must be bfloat16 or float16")
+
+
+def _bth(t, shape, dtype, name) -> BTHStrides:
+    """Strides of a [B, n, heads, head_dim] tensor with unit stride in the last place."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have unit stride in its last place")
+    # a place of extent 1 is never stepped over: its stride is of no account
+    return BTHStrides(sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+
+
+def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> KVCache:
+    torch = _torch()
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim] tensors of one dtype")
+    strides = k_cache.stride()
+    if strides[3] != 1 or v_cache.stride() != strides:
+        raise ValueError("k_cache and v_cache must have the same strides, 1 in the last place")
+    if not (k_cache.is_cuda and v_cache.is_cuda):
+        raise ValueError("k_cache and v_cache must live on the GPU")
+    B = lens.shape[0]
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or not page_table.is_cuda or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
+    for t, name in ((lens, "lens"), (new_lens, "new_lens")):
+        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda):
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape [{B}]")
+    pages, page_size, heads, dim = k_cache.shape
+    width = page_table.shape[1]
+    return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, strides[0] if pages > 1 else 0,
+                   strides[1] if page_size > 1 else 0, strides[2] if heads > 1 else 0, page_size, heads, dim,
+                   _cache_dtype(k_cache), page_table.data_ptr(), page_table.stride(0) if B > 1 else width, width,
+                   B, lens.data_ptr(), _ptr(new_lens), n, _ptr(err_count))
+
+
+def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_count=None, stream=None):
+    """Write the new tokens' keys and values into their pages, in place.
+
+    k_cache, v_cache: bf16 or f16 [pages, page_size, kv_heads, head_dim], any
+    strides (a transposed view for pages ordered by head), the same for both.
+    page_table: int32 [B, pages per sequence]; lens: int32 [B], tokens of each
+    sequence with the new ones; k, v: [B, n, kv_heads, head_dim], any strides;
+    new_lens: int32 [B] (None: n each), the tokens of k and v that count."""
+    lib = load_library()
+    B, n = (lens.shape[0], k.shape[1]) if k.dim() == 4 else (0, -1)
+    shape = (B, n, k_cache.shape[2], k_cache.shape[3])
+    ks = _bth(k, shape, k_cache.dtype, "k")
+    vs = _bth(v, shape, k_cache.dtype, "v")
+    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
+    check(lib.rlk_kv_append(ctypes.byref(c), k.data_ptr(), ctypes.byref(ks), v.data_ptr(), ctypes.byref(vs),
+                            _stream(stream)))
+
+
+def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, head_dim: int, max_tokens: int) -> int:
+    """rlk_paged_attention_workspace: scratch bytes for max_tokens = pages per sequence * page_size."""
+    return 0
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, scale=None, window=0, sinks=0,
+                    out=None, out_lse=None, workspace=None, err_count=None, stream=None):
+    """Attention of the new tokens over the cache that already holds them
+    (kv_append): query i of sequence b is its token lens[b] - new_lens[b] + i
+    and sees the tokens up to itself; with ``window`` > 0 the last ``window``
+    of those and the first ``sinks`` of the sequence.
+
+    q: [B, n, q_heads, head_dim], any strides; the rest as in kv_append;
+    scale: 1 / sqrt(head_dim) unless given.  ``workspace``: uint8
+    [paged_attention_workspace_bytes(...)] scratch (allocated here if not
+    given).  Returns (out like q, lse float32 [B, n, q_heads]); a query that
+    sees nothing gets 0 and -inf."""
+    lib = load_library()
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, q_heads, head_dim]")
+    B, n, heads = lens.shape[0], q.shape[1], q.shape[2]
+    dim = k_cache.shape[-1]
+    shape = (B, n, heads, dim)
+    qs = _bth(q, shape, k_cache.dtype, "q")
+    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        os_ = BTHStrides(n * heads * dim, heads * dim, dim)
+    else:
+        os_ = _bth(out, shape, q.dtype, "out")
+    if out_lse is None:
+        out_lse = torch.empty((B, n, heads), dtype=torch.float32, device=q.device)
+    elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
+        raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
+    need = paged_attention_workspace_bytes(B, n, heads, dim, c.max_pages * c.page_size)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
+    check(lib.rlk_paged_attention(ctypes.byref(c), q.data_ptr(), ctypes.byref(qs), heads,
+                                  dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+                                  ctypes.byref(os_), out_lse.data_ptr(), _ptr(workspace), _stream(stream)))
+    return out, out_lse

@@ -1,0 +1,96 @@
+"""The rollout operators' C entry points refuse bad arguments on the host
+before anything is enqueued (runs without a GPU)."""
+
+import ctypes
+import math
+
+import pytest
+
+import rollout_consistent_vocab_gb300 as pkg
+from rollout_consistent_vocab_gb300 import _binding as b
+from rollout_consistent_vocab_gb300.build import build_library
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_library()
+    return pkg.load_library()
+
+
+def cache(**kw):
+    c = b.KVCache(0x10000, 0x20000, 8, 4096, 256, 128, 16, 2, 128, b.RLK_DT_BF16, 0x30000, 4, 4, 3, 0x40000,
+                  None, 2, None)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+BAD = [
+    (dict(k=None), b.RLK_EINVAL), (dict(v=None), b.RLK_EINVAL), (dict(page_table=None), b.RLK_EINVAL),
+    (dict(lens=None), b.RLK_EINVAL), (dict(B=-1), b.RLK_EINVAL), (dict(B=1 << 16), b.RLK_EINVAL),
+    (dict(n=-1), b.RLK_EINVAL), (dict(n=1 << 16), b.RLK_EINVAL), (dict(head_dim=96), b.RLK_EINVAL),
+    (dict(dtype=b.RLK_DT_F32), b.RLK_EINVAL), (dict(kv_heads=0), b.RLK_EINVAL), (dict(page_size=0), b.RLK_EINVAL),
+    (dict(max_pages=-1), b.RLK_EINVAL), (dict(table_stride=3), b.RLK_EINVAL), (dict(num_pages=-1), b.RLK_EINVAL),
+    (dict(page_size=1 << 30, max_pages=4), b.RLK_EINVAL), (dict(kv_heads=1025), b.RLK_EINVAL),
+    (dict(k=0x10008), b.RLK_EALIGN), (dict(page_stride=4100), b.RLK_EALIGN), (dict(token_stride=4), b.RLK_EALIGN),
+    (dict(head_stride=130), b.RLK_EALIGN), (dict(lens=0x40002), b.RLK_EALIGN), (dict(page_table=0x30001), b.RLK_EALIGN),
+    (dict(new_lens=0x50002), b.RLK_EALIGN), (dict(err_count=0x50001), b.RLK_EALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD)
+def test_cache_is_checked(lib, kw, status):
+    st = b.BTHStrides(512, 256, 128)
+    c = cache(**kw)
+    s = ctypes.byref(st)
+    assert lib.rlk_kv_append(ctypes.byref(c), 0x60000, s, 0x70000, s, None) == status
+    assert lib.rlk_paged_attention(ctypes.byref(c), 0x60000, s, 4, 0.1, 0, 0, 0x70000, s, None, 0x80000, None) == status
+    assert lib.rlk_last_error()
+
+
+def test_calls_are_checked(lib):
+    c, st = cache(), b.BTHStrides(512, 256, 128)
+
+    def append(k=0x60000, ks=st, v=0x70000, vs=st, c=c):
+        return lib.rlk_kv_append(None if c is None else ctypes.byref(c), k, None if ks is None else ctypes.byref(ks), v,
+                                 None if vs is None else ctypes.byref(vs), None)
+
+    assert append(c=None) == b.RLK_EINVAL
+    assert append(k=None) == b.RLK_EINVAL
+    assert append(vs=None) == b.RLK_EINVAL
+    assert append(v=0x70004) == b.RLK_EALIGN
+    assert append(ks=b.BTHStrides(512, 250, 128)) == b.RLK_EALIGN
+
+    def attend(q=0x60000, qs=st, heads=4, scale=0.1, window=0, sinks=0, out=0x70000, os=st, lse=None, ws=0x80000):
+        return lib.rlk_paged_attention(ctypes.byref(c), q, ctypes.byref(qs), heads, scale, window, sinks, out,
+                                       ctypes.byref(os), lse, ws, None)
+
+    assert attend(q=None) == b.RLK_EINVAL
+    assert attend(out=None) == b.RLK_EINVAL
+    for heads in (0, 3, -2, 2 * 128 + 2):
+        assert attend(heads=heads) == b.RLK_EINVAL
+    for scale in (math.inf, math.nan):
+        assert attend(scale=scale) == b.RLK_EINVAL
+    assert attend(window=-1) == b.RLK_EINVAL
+    assert attend(sinks=-1) == b.RLK_EINVAL
+    assert attend(q=0x60008) == b.RLK_EALIGN
+    assert attend(os=b.BTHStrides(512, 256, 132)) == b.RLK_EALIGN
+    assert attend(lse=0x90002) == b.RLK_EALIGN
+
+
+def test_empty_calls_are_no_ops(lib):
+    st = b.BTHStrides(0, 0, 0)
+    s = ctypes.byref(st)
+    for c in (cache(B=0), cache(n=0), cache(B=0, k=None, lens=None, page_table=None)):
+        assert lib.rlk_kv_append(ctypes.byref(c), None, s, None, s, None) == b.RLK_OK
+        assert lib.rlk_paged_attention(ctypes.byref(c), None, s, 4, 0.1, 0, 0, None, s, None, None, None) == b.RLK_OK
+
+
+def test_workspace_formula(lib):
+    size = ctypes.c_size_t()
+    for B, n, heads, dim, tokens in ((1, 1, 8, 128, 16), (1, 1, 8, 64, 256), (3, 2, 4, 128, 257), (2, 1, 32, 128, 16384),
+                                     (2, 1, 32, 128, 16385), (1, 5, 7, 64, 131072), (1, 1, 1, 64, 2**31 - 1), (0, 1, 1, 64, 500)):
+        assert lib.rlk_paged_attention_workspace(B, n, heads, dim, tokens, ctypes.byref(size)) == b.RLK_OK
+        assert b.paged_attention_workspace_bytes(B, n, heads, dim, tokens) == size.value
+    assert lib.rlk_paged_attention_workspace(-1, 1, 1, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
+    assert lib.rlk_paged_attention_workspace(1, 1, 1, 64, 1, None) == b.RLK_EINVAL
