@@ -115,6 +115,62 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
 rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t head_dim,
                                          int64_t max_tokens, size_t* bytes);
 
+/* Verification of drafted tokens by rejection sampling: what comes out is
+ * distributed as the target's own tokens, whatever the draft model.
+ *
+ * Row b * (n + 1) + i of `logits` is the target model's at the place of draft i
+ * of sequence b (i = n, or num_drafts[b]: the place after the last draft); row
+ * b * n + i of `draft_logits` is the draft model's.  p_i and q_i are their
+ * distributions as rlk_sample draws from them: temperature, top-k then top-p,
+ * renormalised; temperature 0 puts all on the argmax.  Without draft_logits the
+ * drafts are point masses: q_i is 1 at draft_token[b][i].  With
+ * u_i = (accept_uniform[b][i] >> 8) / 2^24, for i = 0, 1, ...:
+ *   draft i is accepted iff u_i q_i(d_i) < p_i(d_i);
+ *   at the first one that is not (a), the token there is drawn from
+ *     max(p_a - q_a, 0), renormalised (from p_a, where that has no mass);
+ *   if all num_drafts[b] are accepted (a = num_drafts[b]), it is drawn from p_a.
+ * The draw is the sampler's: the first column, in column order, at which the
+ * running fixed-point mass exceeds U = draw_uniform[b] / 2^32 of the total.  A
+ * filtered row's p_a draw is the token that rlk_sample gives for that word. */
+typedef struct rlk_verify_args {
+  int64_t B;                    /* sequences; B * (2 n + 1) < 2^28 */
+  int32_t n;                    /* drafts per sequence at most, 0 .. 1024 */
+  int32_t vocab_real;           /* must be RLK_VOCAB_REAL */
+  int32_t vocab_padded;         /* must be RLK_VOCAB_PADDED */
+  const void* logits;           /* bf16 [B * (n + 1)][row_stride], as in rlk_logp_args */
+  int64_t row_stride;
+  const void* draft_logits;     /* bf16 [B * n][draft_row_stride], or NULL: point masses */
+  int64_t draft_row_stride;
+  const int32_t* draft_token;   /* [B][n] */
+  const int32_t* num_drafts;    /* [B], 0 .. n, or NULL: n each; rows past them are not read */
+  /* the target's sampling parameters: by sequence [B], or NULL for the scalar */
+  const float* temperature;  float temperature_scalar;
+  const float* top_p;        float top_p_scalar;
+  const int32_t* top_k;      int32_t top_k_scalar;
+  /* the draft model's (ignored without draft_logits) */
+  const float* draft_temperature;  float draft_temperature_scalar;
+  const float* draft_top_p;        float draft_top_p_scalar;
+  const int32_t* draft_top_k;      int32_t draft_top_k_scalar;
+  const uint32_t* accept_uniform;   /* [B][n] random words */
+  const uint32_t* draw_uniform;     /* [B] random words */
+  int32_t* err_count;           /* optional device counter of rejected sequences */
+} rlk_verify_args;
+
+#define RLK_VERIFY_WORKSPACE_BYTES(B, n) ((size_t)(B) * (((size_t)(n) + 1u) * 2464u + (size_t)(n) * 32u))
+
+/* out_token: int32 [B][n + 1], the accepted drafts, then the drawn token, then
+ *   -1; out_accepted: int32 [B], a.
+ * out_restr, out_full (optional): float [B][n + 1], the target's restricted and
+ *   full logprobs of those tokens (bit-identical to rlk_logp_pair), then 0.
+ * workspace: RLK_VERIFY_WORKSPACE_BYTES(B, n) bytes of device scratch, 16-byte
+ *   aligned.
+ * A sequence that comes to a row it cannot use (parameters or drafted token out
+ * of their domains, logits that rlk_logp_pair answers with NaN, num_drafts[b]
+ * out of range: then at place 0) stops there: token -1 and NaN logprobs at place
+ * a, and err_count is raised by one.  Rows it does not come to are of no account. */
+rlk_status rlk_verify_drafts(const rlk_verify_args* args, int32_t* out_token, int32_t* out_accepted,
+                             float* out_restr, float* out_full, void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,8 @@ import math
 
 import numpy as np
 
+from . import logp_oracle as lo
+
 
 def token_place(table_row, t: int, page_size: int):
     return int(table_row[t // page_size]), t % page_size
@@ -74,3 +76,53 @@ def paged_attention(q, k_cache, v_cache, table, lens, new, scale: float, window:
                 o, z, (w, x) = attend(q[b, i, h], keys[j, h // group], values[j, h // group], scale)
                 out[b, i, h], lse[b, i, h], wb[b, i, h], sb[b, i, h] = o, z, w, x
     return out, lse, wb, sb
+
+
+# ------------------------------------------------------------ verification of drafts
+
+def restricted_row(bits_row, tau: float, top_p: float, top_k: int):
+    """(probabilities, restricted logprobs, full logprobs) of a row's real tokens; None for
+    a row that has no distribution (NaN or +inf logits, all -inf)."""
+    x = lo.bf16_bits_to_f32(np.asarray(bits_row, dtype=np.uint16)[:lo.VREAL])
+    if np.any(np.isnan(x)) or np.any(np.isposinf(x)) or np.all(np.isneginf(x)):
+        return None
+    if tau == 0.0:
+        p = np.zeros(lo.VREAL)
+        p[int(np.argmax(x))] = 1.0
+        with np.errstate(divide="ignore"):
+            return p, np.log(p), np.log(p)
+    full, restr, S = lo.row_logprobs_all(bits_row, tau, top_p, top_k)
+    return np.where(S, np.exp(restr), 0.0), restr, full
+
+
+def draw_set(mass, word: int, eps: float):
+    """Columns that the inverse CDF at U = word / 2^32 may give when the CDF is known to
+    ``eps``: the first column whose running mass exceeds U of the total, and those whose
+    interval comes within eps of it."""
+    cols = np.nonzero(mass > 0)[0]
+    cdf = np.cumsum(mass[cols]) / math.fsum(mass[cols])
+    u = word / 2.0**32
+    before = np.concatenate([[0.0], cdf[:-1]])
+    return {int(c) for c in cols[(before - eps <= u) & (u < cdf + eps)]}
+
+
+def verify_outcomes(target_rows, draft_rows, drafts, accept_words, draw_word: int, eps: float = 0.0):
+    """Every (accepted, token) that rejection sampling may give with probabilities known to
+    a relative ``eps`` (0: the one outcome).  target_rows: len(drafts) + 1 probability
+    vectors; draft_rows: as many as drafts, or None (point masses at the drafts)."""
+    out = set()
+    for i, d in enumerate(drafts):
+        q = np.zeros_like(target_rows[i])
+        q[d] = 1.0
+        q = q if draft_rows is None else draft_rows[i]
+        left, right = (accept_words[i] >> 8) / 2.0**24 * q[d], target_rows[i][d]
+        gap = eps * max(left, right)
+        if left >= right - gap:                                 # may be refused
+            r = np.maximum(target_rows[i] - q, 0.0)
+            mass = math.fsum(r)
+            # what is left after a cancellation is known to eps of p, not of itself
+            out |= {(i, c) for c in (draw_set(r, draw_word, eps / mass) if mass > eps else
+                                     draw_set(target_rows[i], draw_word, eps))}
+            if left >= right + gap:                             # is refused
+                return out
+    return out | {(len(drafts), c) for c in draw_set(target_rows[-1], draw_word, eps)}

@@ -13,7 +13,7 @@ from ._binding import (VOCAB_PADDED, VOCAB_REAL, NUM_SHARDS, SHARD_WIDTH, RlkErr
                        logp_merge_resumable, merge_state, sample, linear_logp, linear_logp_pair,
                        NORM_BINS, norm_bins, sqnorm_accumulate, sqnorm_finalize, reduce_bins_,
                        grad_norm, KVCache, BTHStrides, kv_append, paged_attention,
-                       paged_attention_workspace_bytes)
+                       paged_attention_workspace_bytes, VerifyArgs, verify_drafts, verify_workspace_bytes)
 
 __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError", "LogpArgs",
            "ShardArgs",
@@ -22,4 +22,5 @@ __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError"
            "logp_backward", "logp_pair_save", "logp_backward_saved", "logp_autograd", "shard_summary", "shard_counts", "logp_merge", "shard_counts_window", "logp_merge_resumable", "merge_state",
            "logp_sharded", "sample", "linear_logp", "linear_logp_pair", "NORM_BINS", "norm_bins", "sqnorm_accumulate",
            "sqnorm_finalize", "reduce_bins_", "grad_norm",
-           "KVCache", "BTHStrides", "kv_append", "paged_attention", "paged_attention_workspace_bytes"]
+           "KVCache", "BTHStrides", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
+           "VerifyArgs", "verify_drafts", "verify_workspace_bytes"]

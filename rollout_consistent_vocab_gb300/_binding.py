@@ -91,6 +91,37 @@ class BTHStrides(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
+class VerifyArgs(ctypes.Structure):
+    """rlk_verify_args."""
+    _fields_ = [
+        ("B", ctypes.c_int64),
+        ("n", ctypes.c_int32),
+        ("vocab_real", ctypes.c_int32),
+        ("vocab_padded", ctypes.c_int32),
+        ("logits", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("draft_logits", ctypes.c_void_p),
+        ("draft_row_stride", ctypes.c_int64),
+        ("draft_token", ctypes.c_void_p),
+        ("num_drafts", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p),
+        ("temperature_scalar", ctypes.c_float),
+        ("top_p", ctypes.c_void_p),
+        ("top_p_scalar", ctypes.c_float),
+        ("top_k", ctypes.c_void_p),
+        ("top_k_scalar", ctypes.c_int32),
+        ("draft_temperature", ctypes.c_void_p),
+        ("draft_temperature_scalar", ctypes.c_float),
+        ("draft_top_p", ctypes.c_void_p),
+        ("draft_top_p_scalar", ctypes.c_float),
+        ("draft_top_k", ctypes.c_void_p),
+        ("draft_top_k_scalar", ctypes.c_int32),
+        ("accept_uniform", ctypes.c_void_p),
+        ("draw_uniform", ctypes.c_void_p),
+        ("err_count", ctypes.c_void_p),
+    ]
+
+
 COMPUTE = ("rlk_logp_full", "rlk_logp_restricted", "rlk_logp_pair", "rlk_logp_kl", "rlk_logp_kl_ref",
            "rlk_logp_kl_host",
            "rlk_logp_backward", "rlk_logp_pair_save", "rlk_logp_backward_saved", "rlk_sample",
@@ -98,7 +129,7 @@ COMPUTE = ("rlk_logp_full", "rlk_logp_restricted", "rlk_logp_pair", "rlk_logp_kl
            "rlk_logp_shard_summary", "rlk_logp_shard_counts", "rlk_logp_merge",
            "rlk_logp_merge_resumable", "rlk_logp_shard_counts_window",
            "rlk_sqnorm_accumulate", "rlk_sqnorm_finalize", "rlk_grad_norm",
-           "rlk_kv_append", "rlk_paged_attention", "rlk_paged_attention_workspace")
+           "rlk_kv_append", "rlk_paged_attention", "rlk_paged_attention_workspace", "rlk_verify_drafts")
 RLK_GRAD_BF16, RLK_GRAD_F32 = 0, 1
 EXPORTS = COMPUTE + ("rlk_status_string", "rlk_last_error", "rlk_abi_version")
 
@@ -147,6 +178,7 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.rlk_kv_append.argtypes = [KC, VP, BS, VP, BS, VP]
     lib.rlk_paged_attention.argtypes = [KC, VP, BS, i32, f32, i32, i32, VP, BS, VP, VP, VP]
     lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i64, P(ctypes.c_size_t)]
+    lib.rlk_verify_drafts.argtypes = [P(VerifyArgs), VP, VP, VP, VP, VP, VP]
     for f in COMPUTE:
         getattr(lib, f).restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
@@ -899,3 +931,74 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
                                   dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
                                   ctypes.byref(os_), out_lse.data_ptr(), _ptr(workspace), _stream(stream)))
     return out, out_lse
+
+
+# ----------------------------------------------------------------- draft verification
+
+def verify_workspace_bytes(B: int, n: int) -> int:
+    """RLK_VERIFY_WORKSPACE_BYTES(B, n)."""
+    return B * ((n + 1) * 2464 + n * 32)
+
+
+def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, draft_logits=None,
+                  draft_temperature=None, draft_top_p=None, draft_top_k=None, num_drafts=None, accept_uniform,
+                  draw_uniform, out_token=None, out_accepted=None, out_restr=None, out_full=None, workspace=None,
+                  err_count=None, stream=None):
+    """Which of the drafted tokens stand, and the token that follows them.
+
+    logits: bf16 [B * (n + 1), >=152576], row b * (n + 1) + i the target model's
+    at the place of draft i; draft_token: int32 [B, n]; draft_logits: bf16
+    [B * n, >=152576] (None: the drafts are point masses).  temperature, top_p,
+    top_k: scalars or [B] tensors; the draft model's are the same unless given.
+    num_drafts: int32 [B] (None: n each).  Random words, as uint32 bits in int32
+    tensors: accept_uniform [B, n], draw_uniform [B].  ``workspace``: uint8
+    [verify_workspace_bytes(B, n)] scratch (allocated here if not given).
+
+    Returns (token [B, n + 1]: the accepted drafts, the drawn token, then -1;
+    accepted [B]; restricted and full logprobs of the tokens [B, n + 1])."""
+    lib = load_library()
+    torch = _torch()
+    if draft_token.dim() != 2:
+        raise ValueError("draft_token must be int32 [B, n]")
+    B, n = draft_token.shape
+    for t, rows, name in ((logits, B * (n + 1), "logits"), (draft_logits, B * n, "draft_logits")):
+        if t is not None and (t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != rows
+                              or t.shape[1] < VOCAB_PADDED or t.stride(1) != 1 or not t.is_cuda):
+            raise ValueError(f"{name} must be a bf16 CUDA [{rows}, >={VOCAB_PADDED}] tensor with unit column stride")
+    for t, shape, name in ((draft_token, (B, n), "draft_token"), (accept_uniform, (B, n), "accept_uniform"),
+                           (draw_uniform, (B,), "draw_uniform"), (num_drafts, (B,), "num_drafts")):
+        if t is None and name == "num_drafts":
+            continue
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {list(shape)}")
+    tp, ts = _param(temperature, B, torch.float32, "temperature")
+    pp, ps = _param(top_p, B, torch.float32, "top_p")
+    kp, ks = _param(top_k, B, torch.int32, "top_k")
+    dtp, dts = (tp, ts) if draft_temperature is None else _param(draft_temperature, B, torch.float32, "draft_temperature")
+    dpp, dps = (pp, ps) if draft_top_p is None else _param(draft_top_p, B, torch.float32, "draft_top_p")
+    dkp, dks = (kp, ks) if draft_top_k is None else _param(draft_top_k, B, torch.int32, "draft_top_k")
+    dev = logits.device
+    outs = []
+    for t, shape, dtype, name in ((out_token, (B, n + 1), torch.int32, "out_token"),
+                                  (out_accepted, (B,), torch.int32, "out_accepted"),
+                                  (out_restr, (B, n + 1), torch.float32, "out_restr"),
+                                  (out_full, (B, n + 1), torch.float32, "out_full")):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+        outs.append(t)
+    need = verify_workspace_bytes(B, n)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor of at least verify_workspace_bytes(B, n) bytes")
+    a = VerifyArgs(B, n, VOCAB_REAL, VOCAB_PADDED, logits.data_ptr() if B else None,
+                   logits.stride(0) if B * (n + 1) > 1 else VOCAB_PADDED,
+                   draft_logits.data_ptr() if draft_logits is not None and B * n else None,
+                   draft_logits.stride(0) if draft_logits is not None and B * n > 1 else VOCAB_PADDED,
+                   draft_token.data_ptr(), _ptr(num_drafts), tp, ts, pp, ps, kp, ks, dtp, dts, dpp, dps, dkp, dks,
+                   accept_uniform.data_ptr(), draw_uniform.data_ptr(), _ptr(err_count))
+    check(lib.rlk_verify_drafts(ctypes.byref(a), *[t.data_ptr() for t in outs], workspace.data_ptr() if B else None,
+                                _stream(stream)))
+    return tuple(outs)

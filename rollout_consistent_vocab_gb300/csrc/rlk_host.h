@@ -102,6 +102,41 @@ inline rlk_status check_grad_args(const float* grad_full, const float* grad_rest
   return RLK_OK;
 }
 
+// Flags of a resolved row's record: SAMP_SEL: filtered by top-k or top-p;
+// SAMP_BITS: its support lies in the chunks that its bitmap marks; and the
+// sampler's own (SAMP_DRAW, SAMP_WORDS) and the verification's (VER_OK: the
+// row was resolved; VER_GREEDY: temperature 0).
+enum : uint32_t { SAMP_DRAW = 1u, SAMP_SEL = 2u, SAMP_BITS = 4u, SAMP_WORDS = 8u, VER_OK = 16u, VER_GREEDY = 32u };
+
+// rlk_verify_drafts: a row's resolution, from the pass over both models' rows
+// to the kernel that accepts and draws (32 bytes).
+struct alignas(16) VerifyMsg {
+  float M, Z;          // the row's maximum; sum exp((x - M) / tau) over the vocabulary
+  float zs;            // the same over the support
+  float p_t;           // probability of the drafted token under the restricted distribution
+  float full_t, restr_t;   // its logprobs
+  int32_t min_key;     // lowest order key of the support; greedy rows: the argmax
+  uint32_t flags;
+};
+struct VerifyPass {
+  int64_t B;           // 0 for every other pass
+  int n;
+  const int32_t* token;   // [B][n]
+  const int32_t* num;     // [B] or NULL
+  const float* tau_arr;   // the draft model's parameters, by sequence or one for all
+  const float* p_arr;
+  const int32_t* k_arr;
+  float tau_s, p_s;
+  int32_t k_s;
+  VerifyMsg* rec;         // [B][n + 1]
+  VerifyMsg* rec_draft;   // [B][n]
+};
+
+// One launch over the rows of both models (draft_logits NULL: the target's
+// alone); `bits`: the chunk bitmaps of the target's rows.
+rlk_status verify_pass(const rlk_logp_args* args, const void* draft_logits, int64_t draft_stride,
+                       const VerifyPass& ver, uint32_t* bits, void* stream);
+
 // The sampler behind rlk_sample and rlk_sample_noalloc: `workspace` holds
 // the 16-byte per-row records; `bits` (NULL: not kept) the per-row, per-shard
 // chunk bitmaps that let rows whose support lies in the first candidate

@@ -132,13 +132,14 @@ struct KParams {
   const uint16_t* ref_logits;
   int64_t ref_stride;
   float* out_full_ref;
+  // rlk_verify_drafts: the rows of both models, their parameters by sequence
+  VerifyPass ver;
 };
 
-enum { MODE_FWD = 0, MODE_BWD = 1, MODE_SAMPLE = 2 };
+enum { MODE_FWD = 0, MODE_BWD = 1, MODE_SAMPLE = 2, MODE_VERIFY = 3 };
 
 // Sampler: per-row record of the resolved row, written by the leader of the
 // pair pass and read by the draw kernel (16 bytes).
-enum : uint32_t { SAMP_DRAW = 1u, SAMP_SEL = 2u, SAMP_BITS = 4u, SAMP_WORDS = 8u };
 struct __align__(16) SampMsg {
   float M, Z;
   int32_t min_key;
@@ -194,6 +195,7 @@ __global__ void __cluster_dims__(NSHARD, 1, 1) __launch_bounds__(NTHR, CTAS_PER_
 logp_kernel(const KParams P) {
   constexpr bool BWD = MODE == MODE_BWD;
   constexpr bool SAMPLE = MODE == MODE_SAMPLE;
+  constexpr bool VERIFY = MODE == MODE_VERIFY;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x;
@@ -204,14 +206,31 @@ logp_kernel(const KParams P) {
   const int64_t cid = blockIdx.x / NSHARD;
   const bool pair_kl = MODE == MODE_FWD && P.ref_logits != nullptr;
   const bool is_ref = pair_kl && (cid & 1);
-  const int64_t row = pair_kl ? (cid >> 1) : cid;
+  int64_t row = pair_kl ? (cid >> 1) : cid;
+  // rlk_verify_drafts: the target's B (n + 1) rows, then the draft model's B n;
+  // `row` counts within its model, rows past a sequence's drafts are skipped
+  bool is_draft = false, has_t = true;
+  int64_t seq = row;                    // what the parameter arrays go by
+  int t_ver = 0;
+  if constexpr (VERIFY) {
+    const int64_t nt = P.ver.B * (P.ver.n + 1);
+    is_draft = cid >= nt;
+    row = is_draft ? cid - nt : cid;
+    const int per = is_draft ? P.ver.n : P.ver.n + 1;
+    seq = row / per;
+    const int pos = static_cast<int>(row - seq * per);
+    const int num = P.ver.num ? P.ver.num[seq] : P.ver.n;
+    if (num < 0 || num > P.ver.n || pos > num - (is_draft ? 1 : 0)) return;   // the whole cluster
+    has_t = pos < num;
+    if (has_t) t_ver = P.ver.token[seq * P.ver.n + pos];
+  }
   float* const o_full = is_ref ? P.out_full_ref : P.out_full;
   float* const o_restr = is_ref ? nullptr : P.out_restr;
   int32_t* const o_support = is_ref ? nullptr : P.out_support;
   int32_t* const o_err = is_ref ? nullptr : P.err;
 
   const int nchunks = (r == NSHARD - 1) ? LAST_CHUNKS : SHARD_CHUNKS;
-  const uint16_t* rowp = is_ref ? P.ref_logits + row * P.ref_stride : P.logits + row * P.stride;
+  const uint16_t* rowp = (is_ref || is_draft) ? P.ref_logits + row * P.ref_stride : P.logits + row * P.stride;
   const uint32_t bar_load = smem_addr(&S.bar_load);
   const uint32_t bar_mid = smem_addr(&S.bar_mid);
   const uint32_t bar_mid2 = smem_addr(&S.bar_mid2);
@@ -240,10 +259,14 @@ logp_kernel(const KParams P) {
   }
 
   // ---- row parameters (every CTA of the cluster takes the same decisions)
-  const float tau = P.tau_arr ? P.tau_arr[row] : P.tau_s;
-  const float p = (RESTR && !is_ref) ? (P.p_arr ? P.p_arr[row] : P.p_s) : 1.0f;
-  const int k = (RESTR && !is_ref) ? (P.k_arr ? P.k_arr[row] : P.k_s) : -1;
-  const int t = SAMPLE ? 0 : P.target[row];     // the sampler's pass has no target
+  const float* const tau_arr = is_draft ? P.ver.tau_arr : P.tau_arr;
+  const float* const p_arr = is_draft ? P.ver.p_arr : P.p_arr;
+  const int32_t* const k_arr = is_draft ? P.ver.k_arr : P.k_arr;
+  const float tau = tau_arr ? tau_arr[seq] : (is_draft ? P.ver.tau_s : P.tau_s);
+  const float p = (RESTR && !is_ref) ? (p_arr ? p_arr[seq] : (is_draft ? P.ver.p_s : P.p_s)) : 1.0f;
+  const int k = (RESTR && !is_ref) ? (k_arr ? k_arr[seq] : (is_draft ? P.ver.k_s : P.k_s)) : -1;
+  // the sampler's pass has no target; the verification's is the drafted token
+  const int t = SAMPLE ? 0 : (VERIFY ? t_ver : P.target[row]);
   const bool valid = (tau >= 0.0f) && (tau <= 3.402823466e38f) && (p > 0.0f) && (p <= 1.0f) &&
                      (k == -1 || (k >= 1 && k <= VREAL)) && (t >= 0) && (t < VREAL);
   if (!valid) {
@@ -260,6 +283,7 @@ logp_kernel(const KParams P) {
           P.out_token[row] = -1;
           P.out_samp[row] = SampMsg{};     // nothing to draw
         }
+        if (VERIFY) (is_draft ? P.ver.rec_draft : P.ver.rec)[row] = VerifyMsg{};   // not resolved
         if (o_err) atomicAdd(o_err, 1);
       }
     }
@@ -437,7 +461,7 @@ logp_kernel(const KParams P) {
       for (int i = 0; i < MAXCH; ++i)
         if ((i < MAXCH - 1 || tid + i * NTHR < nchunks) && __hge2_mask(cm[i], vlo2) != 0u)
           hitmask |= 1u << i;
-      if (SAMPLE && P.samp_bits) {
+      if ((SAMPLE || VERIFY) && P.samp_bits && !is_draft) {
         // the draw reads only these chunks when the support lies in the window
         uint32_t* wb = P.samp_bits + (row * NSHARD + r) * SAMP_BITWORDS;
 #pragma unroll
@@ -559,7 +583,7 @@ logp_kernel(const KParams P) {
           ++sent;
         }
       }
-      if (SAMPLE && P.samp_bits) {
+      if ((SAMPLE || VERIFY) && P.samp_bits && !is_draft) {
         // no element of this shard reaches the window with any mass
         uint32_t* wb = P.samp_bits + (row * NSHARD + r) * SAMP_BITWORDS;
         for (int i = tid; i < SAMP_BITWORDS; i += NTHR) wb[i] = 0u;
@@ -687,7 +711,7 @@ logp_kernel(const KParams P) {
     }
   }
 
-  if (tid == 0 && !SAMPLE) {
+  if (tid == 0 && !SAMPLE && !VERIFY) {
     if (o_full) o_full[row] = full;
     if (RESTR && o_restr) o_restr[row] = restr;
     if (RESTR && o_support) o_support[row] = support;
@@ -721,6 +745,26 @@ logp_kernel(const KParams P) {
                                      (RESTR && P.g_restr) ? P.g_restr[row] : 0.0f);
     write_grad_shard(shard_reused ? reinterpret_cast<const uint4*>(rowp) : sh, shard_reused, nchunks,
                      0, t, m, gshard, P.grad_f32 != 0);
+  }
+
+  if (VERIFY && tid == 0) {
+    // the row's resolution and its drafted token's probability and logprobs
+    VerifyMsg m{};
+    if (!bad) {
+      m.M = M;
+      m.Z = Z;
+      m.zs = zs;
+      m.min_key = greedy ? static_cast<int32_t>(amax) : (sel ? sr.min_key : 0);
+      m.flags = VER_OK | (greedy ? VER_GREEDY : 0u) | (sel ? SAMP_SEL : 0u) |
+                (sel && !shard_reused ? SAMP_BITS : 0u);
+      if (has_t) {
+        m.full_t = full;
+        m.restr_t = restr;
+        m.p_t = greedy ? (static_cast<uint32_t>(t) == amax ? 1.0f : 0.0f)
+                       : (in_s ? __fdiv_rn(ex2((xt - M) * c), zs) : 0.0f);
+      }
+    }
+    (is_draft ? P.ver.rec_draft : P.ver.rec)[row] = m;
   }
 
   if (SAMPLE && tid == 0) {
@@ -1200,6 +1244,18 @@ rlk_status rlk_sample(const rlk_logp_args* args, unsigned long long seed,
 }  // extern "C"
 
 namespace rlk {
+
+rlk_status verify_pass(const rlk_logp_args* args, const void* draft_logits, int64_t draft_stride,
+                       const VerifyPass& ver, uint32_t* bits, void* stream) {
+  KParams P = make_params(args);
+  P.ref_logits = static_cast<const uint16_t*>(draft_logits);
+  P.ref_stride = draft_stride;
+  P.ver = ver;
+  P.err = nullptr;               // sequences are counted where they come to a bad row
+  P.samp_bits = bits;
+  const int64_t rows = ver.B * (ver.n + 1 + (draft_logits ? ver.n : 0));
+  return launch<true, MODE_VERIFY>(P, rows, static_cast<cudaStream_t>(stream));
+}
 
 rlk_status sample_impl(const rlk_logp_args* args, unsigned long long seed,
                        const unsigned long long* counter, const uint32_t* uniform,

@@ -92,3 +92,89 @@ def test_planted_mistakes_are_caught(monkeypatch, name):
     with pytest.raises((AssertionError, IndexError)):
         for w, s in ((0, 0), (3, 2)):
             test_attention_against_a_masked_softmax(w, s)
+
+
+# ------------------------------------------------------------ verification
+
+def _probs(r, n, zeros=0):
+    p = r.random(n) + 0.05
+    p[r.permutation(n)[:zeros]] = 0.0
+    return p / p.sum()
+
+
+def _accept_word(u):
+    return int(u * 2**24) << 8
+
+
+def test_verification_emits_the_target_distribution():
+    """Summed over a grid of random numbers and over drafts weighted by q, the first token has
+    the target's probabilities: the identity min(p, q) + max(p - q, 0) = p."""
+    r = np.random.default_rng(3)
+    n, grid = 5, 400
+    p, q = _probs(r, n, 1), _probs(r, n, 1)
+    got = np.zeros(n)
+    for d in range(n):
+        if q[d] == 0:
+            continue
+        for a in range(grid):
+            u = (a + 0.5) / grid
+            word = [_accept_word(u)]
+            if u * q[d] < p[d]:
+                assert {x for x, _ in ro.verify_outcomes([p, p], [q], [d], word, 0)} == {1}
+                got[d] += q[d] / grid
+                continue
+            for c in range(20):
+                (res,) = ro.verify_outcomes([p, p], [q], [d], word, int((c + 0.5) / 20 * 2**32))
+                assert res[0] == 0
+                got[res[1]] += q[d] / grid / 20
+    assert np.abs(got - p).max() < 0.03
+    assert got[p == 0].sum() == 0
+
+
+def test_verification_by_hand():
+    p = np.array([0.5, 0.25, 0.25, 0.0])
+    q = np.array([0.25, 0.25, 0.25, 0.25])
+    w = lambda u: [_accept_word(u)] * 2                                  # noqa: E731
+    # p >= q: accepted at every u; the bonus token by the inverse CDF
+    assert ro.verify_outcomes([p, p, p], [q, q], [0, 1], w(0.999), int(0.6 * 2**32)) == {(2, 1)}
+    # p = 0: refused at every u, and the residual is all at column 0
+    assert ro.verify_outcomes([p, p, p], [q, q], [3, 1], w(0.0), int(0.9 * 2**32)) == {(0, 0)}
+    # a point mass: refused at u >= p(d), the rest renormalised over the others
+    assert ro.verify_outcomes([p, p], None, [0], w(0.4999)[:1], 0) == {(1, 0)}
+    assert ro.verify_outcomes([p, p], None, [0], w(0.5)[:1], int(0.49 * 2**32)) == {(0, 1)}
+    assert ro.verify_outcomes([p, p], None, [0], w(0.5)[:1], int(0.51 * 2**32)) == {(0, 2)}
+    # no drafts: a plain draw, the word at an edge goes to the next column
+    assert ro.verify_outcomes([p], None, [], [], 0) == {(0, 0)}
+    assert ro.verify_outcomes([p], None, [], [], 2**31) == {(0, 1)}
+    assert ro.verify_outcomes([p], None, [], [], 2**31, eps=1e-6) == {(0, 0), (0, 1)}
+
+
+def test_verification_mutants(monkeypatch):
+    src = ro.verify_outcomes
+    mutants = {
+        "accepts on >": lambda t, q, d, a, w, eps=0.0: src(t, q, d, [2**32 - 1 - x for x in a], w, eps),
+        "draws from p": lambda t, q, d, a, w, eps=0.0: {(i, next(iter(ro.draw_set(t[i], w, 0)))) for i, _ in src(t, q, d, a, w, eps)},
+        "bonus from the last draft's row": lambda t, q, d, a, w, eps=0.0: src(t[:-1] + [1 - t[-1]], q, d, a, w, eps),
+    }
+    for name, m in mutants.items():
+        monkeypatch.setattr(ro, "verify_outcomes", m)
+        with pytest.raises(AssertionError):
+            test_verification_by_hand()
+    monkeypatch.setattr(ro, "verify_outcomes", src)
+    test_verification_by_hand()
+
+
+def test_restricted_row_is_the_pinned_one():
+    from oracle import logp_oracle as lo
+    x = np.full(lo.VPAD, -4.0, dtype=np.float32)
+    x[[3, 10, 11]] = [2.0, 1.0, 1.0]
+    x[lo.VREAL:] = np.nan
+    bits = (x.view(np.uint32) >> 16).astype(np.uint16)
+    p, lr, lf = ro.restricted_row(bits, 1.0, 1.0, 2)                     # ties at the k-th value are kept
+    e = np.exp(-1.0)
+    assert np.count_nonzero(p) == 3 and abs(p[3] - 1 / (1 + 2 * e)) < 1e-12 and abs(p[10] - e / (1 + 2 * e)) < 1e-12
+    assert abs(lr[3] - np.log(p[3])) < 1e-12 and lr[5] == -np.inf and np.isfinite(lf[5])
+    p, lr, lf = ro.restricted_row(bits, 0.0, 1.0, -1)
+    assert p[3] == 1.0 and p.sum() == 1.0 and lr[3] == lf[3] == 0.0
+    x[0] = np.nan
+    assert ro.restricted_row((x.view(np.uint32) >> 16).astype(np.uint16), 1.0, 1.0, -1) is None

@@ -94,3 +94,52 @@ def test_workspace_formula(lib):
         assert b.paged_attention_workspace_bytes(B, n, heads, dim, tokens) == size.value
     assert lib.rlk_paged_attention_workspace(-1, 1, 1, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
     assert lib.rlk_paged_attention_workspace(1, 1, 1, 64, 1, None) == b.RLK_EINVAL
+
+
+def verify_args(**kw):
+    a = b.VerifyArgs(3, 2, b.VOCAB_REAL, b.VOCAB_PADDED, 0x10000, b.VOCAB_PADDED, 0x20000, b.VOCAB_PADDED, 0x30000, None,
+                     None, 0.7, None, 0.95, None, 50, None, 0.7, None, 0.95, None, 50, 0x40000, 0x50000, None)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), b.RLK_EINVAL), (dict(n=-1), b.RLK_EINVAL), (dict(n=1025), b.RLK_EINVAL), (dict(B=1 << 28), b.RLK_EINVAL),
+    (dict(B=1 << 27), b.RLK_EINVAL), (dict(vocab_real=7), b.RLK_EINVAL), (dict(logits=None), b.RLK_EINVAL),
+    (dict(logits=0x10008), b.RLK_EALIGN), (dict(row_stride=100), b.RLK_EINVAL), (dict(draft_logits=0x20004), b.RLK_EALIGN),
+    (dict(draft_row_stride=152580), b.RLK_EALIGN), (dict(draft_token=None), b.RLK_EINVAL), (dict(accept_uniform=None), b.RLK_EINVAL),
+    (dict(draw_uniform=None), b.RLK_EINVAL), (dict(draw_uniform=0x50002), b.RLK_EALIGN), (dict(num_drafts=0x60001), b.RLK_EALIGN),
+    (dict(temperature_scalar=-1.0), b.RLK_EINVAL), (dict(top_p_scalar=0.0), b.RLK_EINVAL), (dict(top_k_scalar=0), b.RLK_EINVAL),
+    (dict(draft_temperature_scalar=math.inf), b.RLK_EINVAL), (dict(draft_top_p_scalar=1.5), b.RLK_EINVAL),
+    (dict(draft_top_k_scalar=-2), b.RLK_EINVAL), (dict(temperature=0x70002), b.RLK_EALIGN), (dict(draft_top_k=0x70002), b.RLK_EALIGN),
+    (dict(err_count=0x70002), b.RLK_EALIGN),
+])
+def test_verify_is_checked(lib, kw, status):
+    a = verify_args(**kw)
+    assert lib.rlk_verify_drafts(ctypes.byref(a), 0x80000, 0x90000, None, None, 0xA0000, None) == status
+    assert lib.rlk_last_error()
+
+
+def test_verify_outputs_are_checked(lib):
+    def call(token=0x80000, accepted=0x90000, restr=None, full=None, ws=0xA0000, a=verify_args()):
+        return lib.rlk_verify_drafts(None if a is None else ctypes.byref(a), token, accepted, restr, full, ws, None)
+
+    assert call(a=None) == b.RLK_EINVAL
+    assert call(token=None) == b.RLK_EINVAL
+    assert call(accepted=None) == b.RLK_EINVAL
+    assert call(ws=None) == b.RLK_EINVAL
+    assert call(ws=0xA0008) == b.RLK_EALIGN
+    assert call(restr=0x81002) == b.RLK_EALIGN
+    assert call(full=0x81001) == b.RLK_EALIGN
+    # the draft model's parameters are of no account without its logits; an empty batch is a no-op
+    assert call(a=verify_args(B=0, draft_logits=None, draft_top_p_scalar=9.0)) == b.RLK_OK
+
+
+def test_verify_workspace_macro():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "rlk_rollout.h")).read()
+    m = re.search(r"#define\s+RLK_VERIFY_WORKSPACE_BYTES\(B, n\)\s+(.+)", text).group(1)
+    for B, n in ((1, 0), (3, 4), (128, 7)):
+        assert eval(re.sub(r"\(size_t\)|(?<=\d)u\b", "", m), {"B": B, "n": n}) == b.verify_workspace_bytes(B, n)
