@@ -95,24 +95,25 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
  *   scale: finite.  window: 0 (off) or > 0.  sinks: >= 0, ignored without a
  *     window.
  *   workspace: device scratch of the size that rlk_paged_attention_workspace
- *     gives for max_tokens = max_pages * page_size, 16-byte aligned (NULL where
- *     that is 0).  No contents are expected or kept; calls that overlap on the
- *     GPU need one each.
+ *     gives for max_tokens = max_pages * page_size, 16-byte aligned.  No
+ *     contents are expected or kept; calls that overlap on the GPU need one
+ *     each.
  * Places i >= new_lens[b], and queries that see no token, get out = 0 and
  * lse = -inf.  NaN and infinite keys, values or queries spread to the outputs
  * that see them only (the value of a masked token is never used).  A rejected
- * sequence (as in rlk_kv_append; or a visible token's page number out of
- * range) gets NaN in out and lse for its places i < n.
+ * sequence gets NaN in out and lse: for all its places if its lengths are at
+ * fault (as in rlk_kv_append), for its places i < new_lens[b] if the page
+ * number of a visible token is out of range.
  * Scores, softmax statistics and output sums are held in float32; the weights
- * exp(s_j - max) are rounded to the cache's dtype for the product with V, and
- * out is rounded once at the end. */
+ * exp(s_j - max) go into the product with V as the sum of two elements of the
+ * cache's dtype (16 bits or more), and out is rounded once at the end. */
 rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides,
                                int32_t q_heads, float scale, int32_t window, int32_t sinks, void* out,
                                const rlk_bth_strides* out_strides, float* out_lse, void* workspace,
                                void* stream);
 
 /* *bytes = the scratch that rlk_paged_attention needs for these sizes. */
-rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t head_dim,
+rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int64_t max_tokens, size_t* bytes);
 
 /* Verification of drafted tokens by rejection sampling: what comes out is

@@ -177,7 +177,7 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     KC, BS = P(KVCache), P(BTHStrides)
     lib.rlk_kv_append.argtypes = [KC, VP, BS, VP, BS, VP]
     lib.rlk_paged_attention.argtypes = [KC, VP, BS, i32, f32, i32, i32, VP, BS, VP, VP, VP]
-    lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i64, P(ctypes.c_size_t)]
+    lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i32, i64, P(ctypes.c_size_t)]
     lib.rlk_verify_drafts.argtypes = [P(VerifyArgs), VP, VP, VP, VP, VP, VP]
     for f in COMPUTE:
         getattr(lib, f).restype = ctypes.c_int
@@ -887,9 +887,17 @@ def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_co
                             _stream(stream)))
 
 
-def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, head_dim: int, max_tokens: int) -> int:
+def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int, head_dim: int,
+                                    max_tokens: int) -> int:
     """rlk_paged_attention_workspace: scratch bytes for max_tokens = pages per sequence * page_size."""
-    return 0
+    if B == 0 or n == 0 or q_heads == 0:
+        return 0
+    rows = n * (q_heads // kv_heads)
+    tiles = -(-rows // 32)
+    nt = -(-rows // (8 * tiles))
+    entries, units = B * kv_heads * tiles, -(-max_tokens // 64)
+    parts = (min(entries * units, 1216 if nt <= 2 else 608) * 32 + entries * -(-units // 16)) * nt * 8
+    return ((B + 1) * 8 + 15) // 16 * 16 + parts * (8 + head_dim * 4)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, scale=None, window=0, sinks=0,
@@ -922,9 +930,9 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
         out_lse = torch.empty((B, n, heads), dtype=torch.float32, device=q.device)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
-    need = paged_attention_workspace_bytes(B, n, heads, dim, c.max_pages * c.page_size)
+    need = paged_attention_workspace_bytes(B, n, heads, c.kv_heads, dim, c.max_pages * c.page_size)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
     check(lib.rlk_paged_attention(ctypes.byref(c), q.data_ptr(), ctypes.byref(qs), heads,

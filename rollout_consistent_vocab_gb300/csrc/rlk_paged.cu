@@ -74,72 +74,767 @@ __global__ void append_kernel(const AppendParams P) {
 }
 
 // ------------------------------------------------------------ attention
+//
+// The tokens of a sequence go in units of 64, at fixed places.  A unit is one
+// warp's: its keys and values come in slices through the warp's own ring in
+// shared memory (cp.async), S^T = K Q^T and O^T += V^T P^T run on the tensor
+// cores with the slice's 16 tokens (or dims) as rows and 8 query rows as
+// columns, and a running maximum and sum per query row.  What a row gets from
+// a unit therefore does not depend on the other rows, nor on anything outside
+// the unit.  The units of a group (16 units, 1024 tokens, at fixed places too)
+// are folded in order; the groups of a sequence are joined in a fixed tree.
+// Who folds is free: the units of the whole batch are dealt out in equal runs,
+// and a run that holds all of a group folds it itself, otherwise the units'
+// results go to the workspace and the join folds them, with the same
+// arithmetic.  So no result depends on the batch.
+
+constexpr int UNIT = 64;                 // tokens of a unit
+constexpr int GROUP = 16;                // units of a group
+constexpr int AW = 4;                    // warps of a CTA
+constexpr int NUM_SMS = 152;
+
+// Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in
+// tiles of 8 NT.
+template <int D, int NT>
+struct Shape {
+  static constexpr int CTAS = NT <= 2 ? 2 : 1;               // per SM
+  static constexpr int SL = D == 128 ? 16 : 32;              // tokens of a slice
+  static constexpr int MT = SL / 16;
+  static constexpr int STAGES = NT == 1 ? 3 : NT == 2 ? 2 : 4;
+  static constexpr int ROWB = D * 2;                         // bytes of a head row
+  static constexpr int STAGE = 2 * SL * ROWB;                // keys, then values
+  static constexpr int ACC = NT * 8 * D * 4;                 // the group's running result
+  static constexpr int WARP = STAGES * STAGE + ACC;
+  static constexpr int SMEM = AW * WARP;
+};
+constexpr int workers_of(int nt) { return NUM_SMS * AW * (nt <= 2 ? 2 : 1); }
 
 struct AttnParams {
   PagedParams c;
   const void* q;
   void* out;
   rlk_bth_strides qs, os;       // elements
-  int q_heads;
-  float scale;
+  int q_heads, group;           // group: query heads of a kv head
+  int rows;                     // n * group
+  int tiles;                    // row tiles
+  int64_t B;
+  float c2;                     // scale * log2(e)
   int window, sinks;
   float* lse;
+  int64_t* base;                // [B + 1] units of the sequences before, per kv head and tile
+  float2* unit_ml;              // [workers * 2 GROUP][8 NT]: maximum, sum
+  float* unit_o;                // ... and the weighted sum of values [D]
+  float2* group_ml;             // [B * kv_heads * tiles * groups][8 NT]
+  float* group_o;
+  int groups;                   // groups of the longest sequence that the table can hold
+  int workers;
 };
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+// What of a sequence is visible to its new tokens: units [0, us) for the sinks
+// and [ul, ul + nu - us) up to the end.
+struct Seq {
+  int len, nnew, low, us, ul, nu;
+  bool ok;
+  __device__ __forceinline__ int unit(int li) const { return li < us ? li : ul + (li - us); }
+  // the units of group g, by their place in the sequence's list
+  __device__ __forceinline__ int first(int g) const { return g * GROUP < us ? g * GROUP : us + max(0, g * GROUP - ul); }
+  __device__ __forceinline__ int past(int g) const {
+    const int e = (g + 1) * GROUP;
+    return e <= ul ? min(us, e) : us + min(e - ul, nu - us);
+  }
+};
+__device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
+  Seq s;
+  s.ok = seq_lens(P.c, b, s.len, s.nnew);
+  s.low = s.us = s.ul = s.nu = 0;
+  if (s.ok && s.nnew > 0) {
+    if (P.window > 0) {
+      s.low = max(0, s.len - s.nnew - P.window + 1);
+      s.ul = s.low / UNIT;
+      s.us = min((min(P.sinks, s.len) + UNIT - 1) / UNIT, s.ul);
+    }
+    s.nu = s.us + (s.len + UNIT - 1) / UNIT - s.ul;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int64_t run_start(int64_t k, int64_t units, int64_t workers) { return k * units / workers; }
+__device__ __forceinline__ int64_t run_of(int64_t u, int64_t units, int64_t workers) {
+  return ((u + 1) * workers - 1) / units;
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One more part of a row, of maximum m: the factors of what is there and of the
+// part, with the new maximum in M.  A part that saw nothing (its sum is 0: a
+// part's largest weight is 1) is left out by the caller; one whose scores are all
+// NaN has a NaN sum and m = -inf, and stays NaN.
+struct Factors { float a, b; };
+__device__ __forceinline__ Factors fold_factors(float& M, float m) {
+  const float mx = fmaxf(M, m);
+  const Factors f{M == -INFINITY ? 0.0f : ex2f(M - mx), ex2f(m - mx)};
+  M = mx;
+  return f;
+}
+__device__ __forceinline__ float fold(float x, float part, Factors f) { return __fmaf_rn(part, f.b, __fmul_rn(x, f.a)); }
+
+template <class T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr float OFF = 0.0f;
+  static constexpr uint32_t EXP = 0x7F807F80u;
+  static constexpr float TINY = 9.094947017729282e-13f;      // 2^-40
+  // The weights (a, b) >= 0 as the sum of two pairs of elements.  Both parts of a
+  // weight above 0 are above 0 (hi is rounded down, lo raised to 2^-40 of the
+  // weight), so that an infinite value comes through as itself.
+  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const float x = __uint_as_float(hi << 16), y = __uint_as_float(hi & 0xFFFF0000u);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(fmaxf(a - x, a * TINY), fmaxf(b - y, b * TINY));
+    lo = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+// f16 holds weights in units of 2^-12, so that the smallest ones keep their bits
+template <> struct Elem<__half> {
+  static constexpr float OFF = 12.0f;
+  static constexpr uint32_t EXP = 0x7C007C00u;
+  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16: 2^-36 of the row's largest weight
+  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const __half2 r = __floats2half2_rn(a > 0.0f ? fmaxf(a - h.x, TINY) : a, b > 0.0f ? fmaxf(b - h.y, TINY) : b);
+    lo = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
 __device__ __forceinline__ void from_float(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_float(float x, __half& y) { y = __float2half_rn(x); }
 
-// One warp per query and head: every lane holds head_dim / 32 elements, the
-// visible tokens go by one at a time with a running maximum and sum.
-template <class T, int D>
-__global__ void __launch_bounds__(128) attn_kernel(const AttnParams P, int64_t warps) {
-  constexpr int E = D / 32;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  if (w >= warps) return;
-  const int lane = threadIdx.x & 31;
-  const int hq = static_cast<int>(w % P.q_heads);
-  const int i = static_cast<int>(w / P.q_heads % P.c.n);
-  const int b = static_cast<int>(w / P.q_heads / P.c.n);
-  const int hk = hq / (P.q_heads / P.c.kv_heads);
-  T* out = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
-  const float nan = __int_as_float(0x7fc00000);
-  int len, nnew;
-  bool ok = seq_lens(P.c, b, len, nnew);
-  float m = -INFINITY, l = 0.0f, o[E] = {}, qv[E];
-  if (ok && i < nnew) {
-    const int pos = len - nnew + i;
-    const T* qp = static_cast<const T*>(P.q) + b * P.qs.batch + i * P.qs.token + hq * P.qs.head + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) qv[e] = to_float(qp[e]);
-    const int low = P.window > 0 ? max(0, pos - P.window + 1) : 0;
-    for (int j = P.sinks > 0 ? 0 : low; j <= pos; ++j) {
-      if (j < low && j >= P.sinks) j = low;
-      const int page = P.c.table[b * P.c.table_stride + j / P.c.page_size];
-      if (page < 0 || page >= P.c.num_pages) {
-        ok = false;
-        break;
-      }
-      const int64_t at = page * P.c.page_stride + (j % P.c.page_size) * P.c.token_stride + hk * P.c.head_stride + lane * E;
-      float s = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s += qv[e] * to_float(static_cast<const T*>(P.c.k)[at + e]);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= P.scale;
-      const float mn = fmaxf(m, s);
-      const float f = mn == -INFINITY ? 1.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(s - mn);
-      m = mn;
-      l = l * f + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_float(static_cast<const T*>(P.c.v)[at + e]);
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// 16 bytes into shared memory; zeros where !there (src is then not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A place in a worker's run: the sequence, kv head and tile, the unit in the
+// sequence's list, the slice in the unit.
+struct Place {
+  Seq s;
+  int b, ht, li, slice;
+  int left;                              // units of the run from this one on
+};
+// The unit's first slice from p.slice on that some new token sees, or false.
+template <int SL>
+__device__ __forceinline__ bool seek_slice(const AttnParams& P, Place& p) {
+  for (; p.slice < UNIT / SL; ++p.slice) {
+    const int t0 = p.s.unit(p.li) * UNIT + p.slice * SL;
+    if (t0 < p.s.len && (t0 + SL > p.s.low || t0 < P.sinks)) return true;
+  }
+  return false;
+}
+// The next unit of the run (every unit holds a slice that is seen); false at its end.
+template <int SL>
+__device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
+  if (--p.left <= 0) return false;
+  if (++p.li == p.s.nu) {
+    p.li = 0;
+    if (++p.ht == P.c.kv_heads * P.tiles) {
+      p.ht = 0;
+      do {
+        if (++p.b >= P.B) return false;  // (the lengths changed under the call)
+        p.s = load_seq(P, p.b);
+      } while (p.s.nu == 0);
     }
   }
-  if (!ok && lane == 0 && i == 0 && hq == 0 && P.c.err) atomicAdd(P.c.err, 1);
+  p.slice = 0;
+  return seek_slice<SL>(P, p);
+}
+
+// Where the result of a row goes: out and lse, from the weighted sum o (this
+// lane's share), the sum l and the maximum m (base 2).
+template <class T>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + (log2f(l) - Elem<T>::OFF)) * 0.6931471805599453f;
+}
+
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const AttnParams P) {
+  using S_ = Shape<D, NT>;
+  using E = Elem<T>;
+  constexpr int SL = S_::SL, MT = S_::MT, KK = D / 16, DT = D / 16;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  __shared__ uint8_t bad_slice[AW][8];
+  // until the runs are dealt out, the front of the rings holds the block sums
+  int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [AW * 32], then the total
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- where this warp's run starts: units of the batch, by block of sequences
+  const int per = static_cast<int>((P.B + AW * 32 - 1) / (AW * 32));
+  const int b_lo = static_cast<int>(min(P.B, static_cast<int64_t>(tid) * per));
+  const int b_hi = static_cast<int>(min(P.B, static_cast<int64_t>(b_lo) + per));
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += load_seq(P, b).nu;
+  scan[tid] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t v[AW], sum = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) from_float(!ok ? nan : l == 0.0f ? 0.0f : o[e] / l, out[e]);
-  if (lane == 0 && P.lse) P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] = !ok ? nan : m + logf(l);
+    for (int j = 0; j < AW; ++j) { v[j] = scan[lane * AW + j]; sum += v[j]; }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int64_t run = incl - sum;
+#pragma unroll
+    for (int j = 0; j < AW; ++j) { scan[lane * AW + j] = run; run += v[j]; }
+    if (lane == 31) scan[AW * 32] = incl;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    int64_t run = scan[tid];
+    for (int b = b_lo; b < b_hi; ++b) {
+      P.base[b] = run;
+      run += load_seq(P, b).nu;
+    }
+    if (tid == 0) P.base[P.B] = scan[AW * 32];
+  }
+  const int HT = P.c.kv_heads * P.tiles;
+  const int64_t units = scan[AW * 32] * HT;
+  if (units == 0) return;                // every thread
+  const int64_t workers = min(static_cast<int64_t>(P.workers), units);
+  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t start = run_start(me, units, workers);
+  Place cons;
+  cons.left = 0;
+  int blk = 0;
+  int64_t blk_base = 0;
+  if (me < workers) {
+    // the last block of sequences that begins at or before the run
+#pragma unroll
+    for (int j = 0; j < AW; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= start / HT));
+    blk -= 1;
+    blk_base = scan[blk];
+  }
+  __syncthreads();                       // the rings are free
+  if (me >= workers) return;
+  cons.left = static_cast<int>(run_start(me + 1, units, workers) - start);
+  {
+    const int64_t at = start / HT;       // the sequence that holds it: [run, run + nu)
+    int b = blk * per;
+    int64_t run = blk_base;
+    Seq s = load_seq(P, b);
+    while (run + s.nu <= at && b + 1 < P.B) {
+      run += s.nu;
+      s = load_seq(P, ++b);
+    }
+    if (s.nu == 0) return;               // (the lengths changed under the call)
+    const int64_t rest = start - run * HT;
+    cons.s = s;
+    cons.b = b;
+    cons.ht = static_cast<int>(rest / s.nu);
+    cons.li = static_cast<int>(rest - static_cast<int64_t>(cons.ht) * s.nu);
+    cons.slice = 0;
+  }
+  Place prod = cons;
+
+  unsigned char* const wmem = smem_raw + warp * S_::WARP;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(wmem));
+  float4* const acc = reinterpret_cast<float4*>(wmem + S_::STAGES * S_::STAGE) + lane;
+
+  // ---- the producing side: slice after slice into the ring
+  const T* const kbase = static_cast<const T*>(P.c.k);
+  const T* const vbase = static_cast<const T*>(P.c.v);
+  bool more = seek_slice<SL>(P, prod);
+  int issued = 0;
+  auto issue = [&]() {
+    const int stage = issued % S_::STAGES;
+    ++issued;
+    const int t0 = prod.s.unit(prod.li) * UNIT + prod.slice * SL;
+    // lane j looks token t0 + j (mod SL) up
+    const int t = t0 + (lane & (SL - 1));
+    const bool seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
+    bool there = false;
+    int64_t off = 0;
+    if (seen) {
+      const int page = P.c.table[prod.b * P.c.table_stride + t / P.c.page_size];
+      there = page >= 0 && page < P.c.num_pages;
+      if (there) off = page * P.c.page_stride + (t % P.c.page_size) * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride;
+    }
+    const bool bad = __any_sync(0xffffffffu, seen && !there);
+    if (lane == 0) bad_slice[warp][stage] = bad;
+    const uint32_t there_mask = __ballot_sync(0xffffffffu, there);
+    constexpr int CH = D / 8;            // 16-byte pieces of a row
+    constexpr int RPI = 32 / CH;         // rows per instruction
+    const int piece = lane % CH;
+    const uint32_t dst = ring + stage * S_::STAGE;
+#pragma unroll
+    for (int j = 0; j < SL / RPI; ++j) {
+      const int r = j * RPI + lane / CH;
+      const int64_t o = __shfl_sync(0xffffffffu, off, r) + piece * 8;
+      const bool ok = (there_mask >> r) & 1u;
+      const uint32_t d = dst + r * S_::ROWB + ((piece ^ (r & 7)) * 16);
+      copy16(d, kbase + o, ok);
+      copy16(d + SL * S_::ROWB, vbase + o, ok);
+    }
+    copy_commit();
+    ++prod.slice;
+    more = seek_slice<SL>(P, prod) || next_unit<SL>(P, prod);
+  };
+  for (int i = 0; i < S_::STAGES - 1 && more; ++i) issue();
+
+  // ---- the consuming side
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lch = lane >> 4;      // ldmatrix, keys
+  const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;      // ldmatrix, values
+  uint32_t qf[NT][KK][2];
+  float o[DT][NT][4], m[NT][2], l[NT][2], GM[NT][2], GL[NT][2];
+  int consumed = 0;
+  bool fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false;
+  int64_t at = start;                    // the unit's number in the batch
+  auto clear_unit = [&]() {
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][x][e] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
+    unit_bad = false;
+  };
+  clear_unit();
+  seek_slice<SL>(P, cons);
+  for (;;) {
+    const int u = cons.s.unit(cons.li);
+    const int tile0 = (cons.ht % P.tiles) * NT * 8;
+    if (fresh_head) {
+      // the queries of this kv head and tile, as B operands
+      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + (cons.ht / P.tiles) * P.group * P.qs.head;
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        const int row = tile0 + x * 8 + g8;
+        const int i = row / P.group;
+        const bool real = row < P.rows && i < cons.s.nnew;
+        const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+          qf[x][k][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) : 0u;
+          qf[x][k][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) : 0u;
+        }
+      }
+      fresh_head = false;
+      fresh_group = true;
+    }
+    if (fresh_group) {
+      const int g = u / GROUP, e = cons.s.past(g);
+      folding = cons.li == cons.s.first(g) && e - cons.li <= cons.left;
+      head_part = start >= at - (cons.li - cons.s.first(g));
+#pragma unroll
+      for (int x = 0; x < NT; ++x) GM[x][0] = GM[x][1] = -INFINITY, GL[x][0] = GL[x][1] = 0.0f;
+      fresh_group = false;
+    }
+    // ---- one slice
+    if (more) issue();
+    if (issued - consumed >= S_::STAGES) copy_wait<S_::STAGES - 1>(); else copy_wait<0>();
+    __syncwarp();
+    const int stage = consumed % S_::STAGES;
+    const uint32_t sk = ring + stage * S_::STAGE, sv = sk + SL * S_::ROWB;
+    unit_bad |= bad_slice[warp][stage] != 0;
+    const int t0 = u * UNIT + cons.slice * SL;
+    float s[MT][NT][4];
+#pragma unroll
+    for (int y = 0; y < MT; ++y) {
+      float s2[NT][4];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[y][x][e] = s2[x][e] = 0.0f;
+      const int row = y * 16 + lrow;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        uint32_t a[4];
+        ldsm(a, sk + row * S_::ROWB + (((2 * k + lch) ^ (row & 7)) * 16));
+#pragma unroll
+        for (int x = 0; x < NT; ++x) E::mma((k & 1) ? s2[x] : s[y][x], a, qf[x][k][0], qf[x][k][1]);
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[y][x][e] = (s[y][x][e] + s2[x][e]) * P.c2;
+    }
+    // masks: the queries stand at p0 .. len - 1
+    const int p0 = cons.s.len - cons.s.nnew;
+    const bool masked = t0 + SL - 1 > p0 ||
+                        (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 + SL > P.sinks);
+    if (masked) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int pos = p0 + (tile0 + x * 8 + 2 * t4 + e) / P.group;
+#pragma unroll
+          for (int y = 0; y < MT; ++y)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int t = t0 + y * 16 + g8 + 8 * f;
+              if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks))
+                s[y][x][2 * f + e] = -INFINITY;
+            }
+        }
+    }
+    // running maximum and sum of each query row (the lanes of equal t4 share a row's tokens)
+    uint32_t pf[MT][NT][4];              // weights: two halves of the dtype's bits each, tokens 0-7 and 8-15
+    bool scaled = false;
+    float fac[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = m[x][e];
+#pragma unroll
+        for (int y = 0; y < MT; ++y) mx = fmaxf(mx, fmaxf(s[y][x][e], s[y][x][2 + e]));
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        fac[x][e] = mx == m[x][e] ? 1.0f : ex2f(m[x][e] - mx);
+        scaled |= fac[x][e] != 1.0f;
+        m[x][e] = mx;
+        const float sub = mx == -INFINITY ? 0.0f : mx - E::OFF;
+        float sum = 0.0f;
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          s[y][x][e] = ex2f(s[y][x][e] - sub);
+          s[y][x][2 + e] = ex2f(s[y][x][2 + e] - sub);
+          sum += s[y][x][e] + s[y][x][2 + e];
+        }
+        l[x][e] = l[x][e] * fac[x][e] + sum;
+      }
+    if (__any_sync(0xffffffffu, scaled)) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
+    }
+#pragma unroll
+    for (int y = 0; y < MT; ++y)
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        E::split(s[y][x][0], s[y][x][1], pf[y][x][0], pf[y][x][2]);
+        E::split(s[y][x][2], s[y][x][3], pf[y][x][1], pf[y][x][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pf[y][x][e] = movm(pf[y][x][e]);
+      }
+    // values: a masked token's must not come in even as 0 * inf
+    uint32_t odd = 0;
+    if (masked) {
+#pragma unroll
+      for (int y = 0; y < MT; ++y) {
+        const int row = y * 16 + vrow;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint32_t a[4];
+          ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            odd |= ((a[e] & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) | ((a[e] & E::EXP & 0xFFFF0000u) == (E::EXP & 0xFFFF0000u));
+        }
+      }
+    }
+    if (!__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+      for (int y = 0; y < MT; ++y) {
+        const int row = y * 16 + vrow;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint32_t a[4];
+          ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            E::mma(o[d][x], a, pf[y][x][2], pf[y][x][3]);
+            E::mma(o[d][x], a, pf[y][x][0], pf[y][x][1]);
+          }
+        }
+      }
+    } else {
+      // query by query, with zeros in the place of the values that it does not see:
+      // for its rows the same products as above, had those values been finite
+      const int i0 = tile0 / P.group, i1 = min(P.c.n - 1, (tile0 + NT * 8 - 1) / P.group);
+      for (int i = i0; i <= i1; ++i) {
+        const int pos = p0 + i;
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          uint32_t keep[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            keep[f] = 0u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = t0 + y * 16 + 8 * f + 2 * t4 + e;
+              if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) keep[f] |= 0xFFFFu << (16 * e);
+            }
+          }
+          const int row = y * 16 + vrow;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
+            a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              float r[4] = {o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]};
+              E::mma(r, a, pf[y][x][2], pf[y][x][3]);
+              E::mma(r, a, pf[y][x][0], pf[y][x][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((tile0 + x * 8 + 2 * t4 + (e & 1)) / P.group == i) o[d][x][e] = r[e];
+            }
+          }
+        }
+      }
+    }
+    ++consumed;
+    __syncwarp();                        // the stage may be filled again
+
+    // ---- on to the next slice; at the end of the unit, its result
+    ++cons.slice;
+    if (seek_slice<SL>(P, cons)) continue;
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
+        if (unit_bad) m[x][e] = 0.0f, l[x][e] = __int_as_float(0x7fc00000);
+      }
+    if (unit_bad && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+    const int g = u / GROUP;
+    const bool head_ends = cons.li + 1 == cons.s.nu;
+    const bool group_ends = cons.li + 1 == cons.s.past(g);
+    bool store = true, direct = false;
+    int64_t slot = me * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
+    float2* ml = P.unit_ml;
+    float* po = P.unit_o;
+    if (folding) {
+      const bool first = cons.li == cons.s.first(g);
+      Factors f[NT][2];
+      bool none[NT][2];                  // the row saw nothing in the unit
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f[x][e] = Factors{1.0f, 0.0f};
+          none[x][e] = l[x][e] == 0.0f;
+          if (!none[x][e]) {
+            f[x][e] = fold_factors(GM[x][e], m[x][e]);
+            GL[x][e] = fold(GL[x][e], l[x][e], f[x][e]);
+          }
+          m[x][e] = GM[x][e];
+          l[x][e] = GL[x][e];
+        }
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          const float4 v = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : acc[(d * NT + x) * 32];
+          o[d][x][0] = none[x][0] ? v.x : fold(v.x, o[d][x][0], f[x][0]);
+          o[d][x][1] = none[x][1] ? v.y : fold(v.y, o[d][x][1], f[x][1]);
+          o[d][x][2] = none[x][0] ? v.z : fold(v.z, o[d][x][2], f[x][0]);
+          o[d][x][3] = none[x][1] ? v.w : fold(v.w, o[d][x][3], f[x][1]);
+          if (!group_ends) acc[(d * NT + x) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
+        }
+      store = group_ends;
+      direct = cons.s.past(g) - cons.s.first(g) == cons.s.nu;
+      slot = (static_cast<int64_t>(cons.b) * HT + cons.ht) * P.groups + g;
+      ml = P.group_ml;
+      po = P.group_o;
+    }
+    if (store) {
+      const int kh = cons.ht / P.tiles;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = row / P.group;
+          if (row >= P.rows || i >= cons.s.nnew) continue;
+          if (direct) {
+            const int hq = kh * P.group + (row - i * P.group);
+            T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
+            const bool none = l[x][e] == 0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              from_float(none ? 0.0f : __fdiv_rn(o[d][x][e], l[x][e]), op[d * 16]);
+              from_float(none ? 0.0f : __fdiv_rn(o[d][x][2 + e], l[x][e]), op[d * 16 + 8]);
+            }
+            if (P.lse && g8 == 0)
+              P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(m[x][e], l[x][e]);
+          } else {
+            float* dst = po + (slot * (NT * 8) + r) * D + g8;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              dst[d * 16] = o[d][x][e];
+              dst[d * 16 + 8] = o[d][x][2 + e];
+            }
+            if (g8 == 0) ml[slot * (NT * 8) + r] = make_float2(m[x][e], l[x][e]);
+          }
+        }
+    }
+    clear_unit();
+    fresh_group |= group_ends;
+    fresh_head |= head_ends;
+    ++at;
+    if (!next_unit<SL>(P, cons)) break;
+  }
+}
+
+// ------------------------------------------------------------ the join
+
+constexpr int JW = 8;                    // warps of a join CTA, and chains of the tree
+
+// A row of a sequence whose groups are not all in one run: group g goes to
+// chain g mod 8, each chain folds its groups in order, and the chains are
+// folded in order.  Up to 8 groups that is one fold over the groups, which a
+// single warp does.  The same CTA fills the rows without a query, and those of
+// rejected sequences.
+template <class T, int D>
+struct JoinRow {
+  static constexpr int E = D / 32;       // elements of a lane
+  float M = -INFINITY, L = 0.0f, o[E] = {};
+  __device__ __forceinline__ void add(float m, float l, const float (&v)[E]) {
+    if (l == 0.0f) return;
+    const Factors f = fold_factors(M, m);
+    L = fold(L, l, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fold(o[e], v[e], f);
+  }
+};
+template <int E>
+__device__ __forceinline__ void load_part(const float2* ml, const float* po, int64_t at, int D, int lane, float2& h, float (&v)[E]) {
+  h = ml[at];
+  const float* src = po + at * D + lane * E;
+  if constexpr (E == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(src);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(src);
+    v[0] = x.x, v[1] = x.y;
+  }
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int block_rows, int64_t items) {
+  constexpr int E = D / 32;
+  using Row = JoinRow<T, D>;
+  __shared__ float2 chain_ml[JW];
+  __shared__ float chain_o[JW][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int HT = P.c.kv_heads * P.tiles;
+  const int64_t units = P.base[P.B] * HT;
+  const int64_t workers = min(static_cast<int64_t>(P.workers), units);
+  const int blocks = (tile_rows + block_rows - 1) / block_rows;
+  const float nan = __int_as_float(0x7fc00000);
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int rb = static_cast<int>(it % blocks);
+    const int64_t entry = it / blocks;
+    const int b = static_cast<int>(entry / HT), ht = static_cast<int>(entry - static_cast<int64_t>(b) * HT);
+    const Seq s = load_seq(P, b);
+    if (!s.ok && ht == 0 && rb == 0 && threadIdx.x == 0 && P.c.err) atomicAdd(P.c.err, 1);
+    const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
+    const int64_t u0 = P.base[b] * HT + static_cast<int64_t>(ht) * s.nu;
+    const bool one_group = s.nu > 0 && s.first(glast) == 0;
+    const bool direct = one_group && run_of(u0, units, workers) == run_of(u0 + s.nu - 1, units, workers);
+    const int tile0 = (ht % P.tiles) * tile_rows;
+    const bool wide = glast >= JW;       // more groups than chains: all warps on one row
+    for (int j = wide ? 0 : warp; j < block_rows; j += wide ? 1 : JW) {
+      const int r = rb * block_rows + j, row = tile0 + r, i = row / P.group;
+      if (r >= tile_rows || row >= P.rows) continue;
+      const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
+      const bool query = s.ok && i < s.nnew;
+      if (query && direct) continue;
+      Row acc;
+      if (query) {
+        const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;   // groups [0, gs) and [gl, glast]
+        const int step = wide ? JW : 1;
+        for (int g = wide ? warp : 0; g <= glast; g += step) {
+          if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
+          if (g > glast) break;
+          const int f = s.first(g), e = s.past(g);
+          if (f >= e) continue;
+          const int64_t ua = u0 + f;
+          if (run_of(ua, units, workers) == run_of(u0 + e - 1, units, workers)) {
+            float2 h;
+            float v[E];
+            load_part<E>(P.group_ml, P.group_o, (entry * P.groups + g) * tile_rows + r, D, lane, h, v);
+            acc.add(h.x, h.y, v);
+            continue;
+          }
+          Row part;
+          for (int k = f; k < e; ++k) {
+            const int64_t w = run_of(u0 + k, units, workers);
+            const int64_t slot = w * (2 * GROUP) + (run_start(w, units, workers) >= ua ? 0 : GROUP) + s.unit(k) % GROUP;
+            float2 h;
+            float v[E];
+            load_part<E>(P.unit_ml, P.unit_o, slot * tile_rows + r, D, lane, h, v);
+            part.add(h.x, h.y, v);
+          }
+          acc.add(part.M, part.L, part.o);
+        }
+      }
+      if (query && wide) {
+        if (lane == 0) chain_ml[warp] = make_float2(acc.M, acc.L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) chain_o[warp][lane * E + e] = acc.o[e];
+        __syncthreads();
+        if (warp == 0) {
+          acc = Row();
+          for (int c = 0; c < JW; ++c) {
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = chain_o[c][lane * E + e];
+            acc.add(chain_ml[c].x, chain_ml[c].y, v);
+          }
+        }
+        __syncthreads();
+      }
+      if (wide && warp != 0) continue;
+      T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        from_float(!s.ok ? nan : acc.L == 0.0f ? 0.0f : __fdiv_rn(acc.o[e], acc.L), op[e]);
+      if (P.lse && lane == 0)
+        P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] = !s.ok ? nan : lse_of<T>(acc.M, acc.L);
+    }
+  }
 }
 
 // ------------------------------------------------------------ host side
@@ -201,10 +896,81 @@ PagedParams paged_params(const rlk_kv_cache* c) {
   return P;
 }
 
+// Row tiles of a call: as few as hold the rows in 32 each, then as narrow as they can be.
+struct Tiling { int rows, tiles, nt; };
+Tiling tiling_of(int64_t n, int64_t group) {
+  const int64_t rows = n * group, tiles = (rows + 31) / 32;
+  return {static_cast<int>(rows), static_cast<int>(tiles), static_cast<int>((rows + 8 * tiles - 1) / (8 * tiles))};
+}
+
+// The workspace, in this order: units of the sequences before (int64 [B + 1]),
+// maxima and sums of units and of groups, their weighted sums.
+struct Layout {
+  size_t base, unit_ml, group_ml, unit_o, group_o, bytes;
+  int64_t groups;
+};
+Layout layout_of(int64_t B, int64_t n, int64_t kv_heads, int64_t group, int64_t D, int64_t max_tokens) {
+  const Tiling t = tiling_of(n, group);
+  const int64_t entries = B * kv_heads * t.tiles, units = (max_tokens + UNIT - 1) / UNIT;
+  const int64_t unit_slots = (entries * units < workers_of(t.nt) ? entries * units : workers_of(t.nt)) * 2 * GROUP;
+  Layout y{};
+  y.groups = (units + GROUP - 1) / GROUP;
+  const size_t ur = static_cast<size_t>(unit_slots) * t.nt * 8, gr = static_cast<size_t>(entries * y.groups) * t.nt * 8;
+  y.base = 0;
+  y.unit_ml = (static_cast<size_t>(B + 1) * 8 + 15) / 16 * 16;
+  y.group_ml = y.unit_ml + ur * 8;
+  y.unit_o = y.group_ml + gr * 8;
+  y.group_o = y.unit_o + ur * D * 4;
+  y.bytes = y.group_o + gr * D * 4;
+  return y;
+}
+
+// Function attributes are set once per device and kernel.
+template <class K>
+rlk_status allow_smem(K kernel, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (dev >= 0 && dev < 64 && done[dev]) return RLK_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (dev >= 0 && dev < 64) done[dev] = true;
+  return RLK_OK;
+}
+
+template <class T, int D, int NT>
+rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
+  static bool done[64] = {};
+  rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, done);
+  if (s != RLK_OK) return s;
+  attn_kernel<T, D, NT><<<P.workers / AW, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
+  // the join is launched while the units are at work, and waits for them
+  const int block_rows = P.groups <= JW ? JW : 1;
+  const int64_t items = P.B * P.c.kv_heads * P.tiles * ((NT * 8 + block_rows - 1) / block_rows);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items < NUM_SMS * 8 ? items : NUM_SMS * 8));
+  cfg.blockDim = dim3(JW * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, NT * 8, block_rows, items);
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
+  return RLK_OK;
+}
 template <class T, int D>
-void launch_attn(const AttnParams& P, int64_t B, cudaStream_t st) {
-  const int64_t warps = B * P.c.n * P.q_heads;
-  attn_kernel<T, D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(P, warps);
+rlk_status launch_rows(const AttnParams& P, int nt, cudaStream_t st) {
+  switch (nt) {
+    case 1: return launch_attn<T, D, 1>(P, st);
+    case 2: return launch_attn<T, D, 2>(P, st);
+    case 3: return launch_attn<T, D, 3>(P, st);
+    default: return launch_attn<T, D, 4>(P, st);
+  }
 }
 
 }  // namespace rlk
@@ -235,11 +1001,13 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
   return RLK_OK;
 }
 
-rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t head_dim,
+rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int64_t max_tokens, size_t* bytes) {
   if (B < 0 || n < 0 || q_heads < 0 || head_dim < 0 || max_tokens < 0) return fail(RLK_EINVAL, "a size is negative");
   if (!bytes) return fail(RLK_EINVAL, "bytes is NULL");
-  *bytes = 0;
+  if (kv_heads < 1 || q_heads % kv_heads) return fail(RLK_EINVAL, "q_heads %d must be a multiple of kv_heads %d", q_heads, kv_heads);
+  *bytes = B == 0 || n == 0 || q_heads == 0
+               ? 0 : layout_of(B, n, kv_heads, q_heads / kv_heads, head_dim, max_tokens).bytes;
   return RLK_OK;
 }
 
@@ -257,7 +1025,13 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
   if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
   if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
-  (void)workspace;
+  if (!workspace) return fail(RLK_EINVAL, "workspace is NULL");
+  if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
+  const int group = q_heads / cache->kv_heads;
+  const Tiling t = tiling_of(cache->n, group);
+  const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
+                             static_cast<int64_t>(cache->max_pages) * cache->page_size);
+  char* ws = static_cast<char*>(workspace);
   AttnParams P{};
   P.c = paged_params(cache);
   P.q = q;
@@ -265,19 +1039,26 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.qs = *q_strides;
   P.os = *out_strides;
   P.q_heads = q_heads;
-  P.scale = scale;
+  P.group = group;
+  P.rows = t.rows;
+  P.tiles = t.tiles;
+  P.B = cache->B;
+  P.c2 = scale * 1.4426950408889634f;
   P.window = window;
-  P.sinks = sinks;
+  P.sinks = window > 0 ? sinks : 0;
   P.lse = out_lse;
+  P.base = reinterpret_cast<int64_t*>(ws + y.base);
+  P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
+  P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
+  P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
+  P.group_o = reinterpret_cast<float*>(ws + y.group_o);
+  P.groups = static_cast<int>(y.groups);
+  P.workers = workers_of(t.nt);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = cache->dtype == RLK_DT_BF16, wide = cache->head_dim == 128;
-  if (bf && wide) launch_attn<__nv_bfloat16, 128>(P, cache->B, st);
-  else if (bf) launch_attn<__nv_bfloat16, 64>(P, cache->B, st);
-  else if (wide) launch_attn<__half, 128>(P, cache->B, st);
-  else launch_attn<__half, 64>(P, cache->B, st);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  return RLK_OK;
+  const bool bf = cache->dtype == RLK_DT_BF16;
+  if (cache->head_dim == 128)
+    return bf ? launch_rows<__nv_bfloat16, 128>(P, t.nt, st) : launch_rows<__half, 128>(P, t.nt, st);
+  return bf ? launch_rows<__nv_bfloat16, 64>(P, t.nt, st) : launch_rows<__half, 64>(P, t.nt, st);
 }
 
 }  // extern "C"

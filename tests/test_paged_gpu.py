@@ -1,12 +1,13 @@
 """GPU: the paged key-value cache (append, attention) against the float64 oracle.
 
-Tolerances, from the formats and not from a run.  With u the cache dtype's unit
-roundoff (2^-9 bf16, 2^-12 f16), A = sum_j p_j |v_j| and X the largest
+Tolerances, from the formats and not from a run.  With u half the cache dtype's
+unit roundoff (2^-9 bf16, 2^-12 f16), A = sum_j p_j |v_j| and X the largest
 scale * sum_d |q_d k_jd|:
   * a score carries at most (D + 4) 2^-24 X of float32 rounding, so a weight's
     relative error is at most ds = 2 (D + 4) 2^-24 X + 2^-18 (maximum and
     normaliser; ex2 and the rescalings of the join);
-  * weights are rounded to the dtype: u A; the result once: u |out|;
+  * the result is rounded to the dtype once: 2 u |out| <= u |out| + u A, which leaves no
+    room for weights of the dtype's precision: they have to carry twice its bits;
   * f16: results below its normal range are rounded at 2^-25 (weights are held
     scaled up, so that theirs is 2^-37 per token of the largest): 2^-24 in all.
   lse: ds alone (its sum is of unrounded weights).
@@ -294,7 +295,7 @@ def test_on_another_stream_and_in_a_graph():
     st.synchronize()
     assert torch.equal(o, want) and torch.equal(z, wl)
     out, lse = torch.empty_like(want), torch.empty_like(wl)
-    ws = torch.empty(max(1, pkg.paged_attention_workspace_bytes(2, 2, 8, 128, 16 * c["table"].shape[1])),
+    ws = torch.empty(max(1, pkg.paged_attention_workspace_bytes(2, 2, 8, 2, 128, 16 * c["table"].shape[1])),
                      dtype=torch.uint8, device=DEV)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -88,12 +88,16 @@ def test_empty_calls_are_no_ops(lib):
 
 def test_workspace_formula(lib):
     size = ctypes.c_size_t()
-    for B, n, heads, dim, tokens in ((1, 1, 8, 128, 16), (1, 1, 8, 64, 256), (3, 2, 4, 128, 257), (2, 1, 32, 128, 16384),
-                                     (2, 1, 32, 128, 16385), (1, 5, 7, 64, 131072), (1, 1, 1, 64, 2**31 - 1), (0, 1, 1, 64, 500)):
-        assert lib.rlk_paged_attention_workspace(B, n, heads, dim, tokens, ctypes.byref(size)) == b.RLK_OK
-        assert b.paged_attention_workspace_bytes(B, n, heads, dim, tokens) == size.value
-    assert lib.rlk_paged_attention_workspace(-1, 1, 1, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
-    assert lib.rlk_paged_attention_workspace(1, 1, 1, 64, 1, None) == b.RLK_EINVAL
+    for B, n, heads, kv, dim, tokens in ((1, 1, 8, 8, 128, 16), (1, 1, 8, 1, 64, 256), (3, 2, 4, 2, 128, 257),
+                                         (2, 1, 32, 8, 128, 16384), (2, 9, 32, 8, 128, 16385), (1, 5, 7, 7, 64, 131072),
+                                         (1, 1, 1, 1, 64, 2**31 - 1), (0, 1, 1, 1, 64, 500), (4, 8, 64, 8, 128, 1),
+                                         (4, 17, 64, 8, 128, 5000), (65535, 1, 32, 4, 128, 70000)):
+        assert lib.rlk_paged_attention_workspace(B, n, heads, kv, dim, tokens, ctypes.byref(size)) == b.RLK_OK
+        assert b.paged_attention_workspace_bytes(B, n, heads, kv, dim, tokens) == size.value
+    assert lib.rlk_paged_attention_workspace(-1, 1, 1, 1, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
+    assert lib.rlk_paged_attention_workspace(1, 1, 3, 2, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
+    assert lib.rlk_paged_attention_workspace(1, 1, 3, 0, 64, 1, ctypes.byref(size)) == b.RLK_EINVAL
+    assert lib.rlk_paged_attention_workspace(1, 1, 1, 1, 64, 1, None) == b.RLK_EINVAL
 
 
 def verify_args(**kw):
