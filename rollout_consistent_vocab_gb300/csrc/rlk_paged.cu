@@ -75,21 +75,22 @@ __global__ void append_kernel(const AppendParams P) {
 
 // ------------------------------------------------------------ attention
 //
-// The tokens of a sequence go in units of 64, at fixed places.  A unit is one
-// warp's: its keys and values come in slices through the warp's own ring in
-// shared memory (cp.async), S^T = K Q^T and O^T += V^T P^T run on the tensor
-// cores with the slice's 16 tokens (or dims) as rows and 8 query rows as
-// columns, and a running maximum and sum per query row.  What a row gets from
-// a unit therefore does not depend on the other rows, nor on anything outside
-// the unit.  The units of a group (16 units, 1024 tokens, at fixed places too)
-// are folded in order; the groups of a sequence are joined in a fixed tree.
-// Who folds is free: the units of the whole batch are dealt out in equal runs,
-// and a run that holds all of a group folds it itself, otherwise the units'
-// results go to the workspace and the join folds them, with the same
-// arithmetic.  So no result depends on the batch.
+// The tokens of a sequence go in units of 256, at fixed places.  A unit is one
+// CTA's: its four warps take the unit's slices in turn, keys and values come
+// through each warp's own ring in shared memory (cp.async), S^T = K Q^T and
+// O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims) as
+// rows and 8 query rows as columns, with a running maximum and sum per query
+// row; then the warps' shares are folded in order.  What a row gets from a unit
+// therefore does not depend on the other rows, nor on anything outside the unit.
+// The units of a group (4 units, 1024 tokens, at fixed places too) are folded in
+// order; the groups of a sequence are joined in a fixed tree.  Who folds is
+// free: the units of the whole batch are dealt out in equal runs, and a run that
+// holds all of a group folds it itself, otherwise the units' results go to the
+// workspace and the join folds them, with the same arithmetic.  So no result
+// depends on the batch.
 
-constexpr int UNIT = 64;                 // tokens of a unit
-constexpr int GROUP = 16;                // units of a group
+constexpr int UNIT = 256;                // tokens of a unit
+constexpr int GROUP = 4;                 // units of a group
 constexpr int AW = 4;                    // warps of a CTA
 constexpr int NUM_SMS = 152;
 
@@ -103,11 +104,12 @@ struct Shape {
   static constexpr int STAGES = NT == 1 ? 3 : NT == 2 ? 2 : 4;
   static constexpr int ROWB = D * 2;                         // bytes of a head row
   static constexpr int STAGE = 2 * SL * ROWB;                // keys, then values
-  static constexpr int ACC = NT * 8 * D * 4;                 // the group's running result
-  static constexpr int WARP = STAGES * STAGE + ACC;
-  static constexpr int SMEM = AW * WARP;
+  static constexpr int XCH = NT * 8 * D * 4;                 // a warp's share of a unit's result
+  static constexpr int WARP = STAGES * STAGE + XCH;
+  static constexpr bool QS = NT >= 3;                        // queries in shared memory, not in registers
+  static constexpr int SMEM = AW * WARP + (QS ? NT * (D / 16) * 32 * 8 : 0);
 };
-constexpr int workers_of(int nt) { return NUM_SMS * AW * (nt <= 2 ? 2 : 1); }
+constexpr int workers_of(int nt) { return NUM_SMS * (nt <= 2 ? 2 : 1); }
 
 struct AttnParams {
   PagedParams c;
@@ -126,6 +128,7 @@ struct AttnParams {
   float* unit_o;                // ... and the weighted sum of values [D]
   float2* group_ml;             // [B * kv_heads * tiles * groups][8 NT]
   float* group_o;
+  uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
   int groups;                   // groups of the longest sequence that the table can hold
   int workers;
 };
@@ -170,9 +173,9 @@ __device__ __forceinline__ float ex2f(float x) {
 }
 
 // One more part of a row, of maximum m: the factors of what is there and of the
-// part, with the new maximum in M.  A part that saw nothing (its sum is 0: a
-// part's largest weight is 1) is left out by the caller; one whose scores are all
-// NaN has a NaN sum and m = -inf, and stays NaN.
+// part, with the new maximum in M.  A part that saw nothing (its sum is 0, since
+// a part's largest weight is 1) is left out; one whose scores are all NaN has a
+// NaN sum and m = -inf, and stays NaN.
 struct Factors { float a, b; };
 __device__ __forceinline__ Factors fold_factors(float& M, float m) {
   const float mx = fmaxf(M, m);
@@ -180,7 +183,33 @@ __device__ __forceinline__ Factors fold_factors(float& M, float m) {
   M = mx;
   return f;
 }
-__device__ __forceinline__ float fold(float x, float part, Factors f) { return __fmaf_rn(part, f.b, __fmul_rn(x, f.a)); }
+// (b = 0: the part weighs nothing beside what is there, or is left out; a is then 1)
+__device__ __forceinline__ float fold(float x, float part, Factors f) {
+  return f.b == 0.0f ? x : __fmaf_rn(part, f.b, __fmul_rn(x, f.a));
+}
+// The part's maximum and sum into (M, L).
+__device__ __forceinline__ Factors add_part(float& M, float& L, float m, float l) {
+  if (l == 0.0f) return Factors{1.0f, 0.0f};
+  Factors f = fold_factors(M, m);
+  if (l != l) f.b = l;
+  L = fold(L, l, f);
+  return f;
+}
+// Four elements of a fragment: two each of its rows of even and odd number.
+__device__ __forceinline__ void fold4(float4& x, const float4& part, Factors even, Factors odd) {
+  x.x = fold(x.x, part.x, even);
+  x.y = fold(x.y, part.y, odd);
+  x.z = fold(x.z, part.z, even);
+  x.w = fold(x.w, part.w, odd);
+}
+template <int NT>
+__device__ __forceinline__ Factors pick(const Factors (&f)[NT][2], int x, int e) {
+  Factors r = f[0][e];
+#pragma unroll
+  for (int i = 1; i < NT; ++i)
+    if (x == i) r = f[i][e];
+  return r;
+}
 
 template <class T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
@@ -249,17 +278,16 @@ struct Place {
   int b, ht, li, slice;
   int left;                              // units of the run from this one on
 };
-// The unit's first slice from p.slice on that some new token sees, or false.
+// This warp's first slice of the unit from p.slice on that some new token sees, or false.
 template <int SL>
 __device__ __forceinline__ bool seek_slice(const AttnParams& P, Place& p) {
-  for (; p.slice < UNIT / SL; ++p.slice) {
+  for (; p.slice < UNIT / SL; p.slice += AW) {
     const int t0 = p.s.unit(p.li) * UNIT + p.slice * SL;
     if (t0 < p.s.len && (t0 + SL > p.s.low || t0 < P.sinks)) return true;
   }
   return false;
 }
-// The next unit of the run (every unit holds a slice that is seen); false at its end.
-template <int SL>
+// The next unit of the run; false at its end.
 __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
   if (--p.left <= 0) return false;
   if (++p.li == p.s.nu) {
@@ -272,8 +300,7 @@ __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
       } while (p.s.nu == 0);
     }
   }
-  p.slice = 0;
-  return seek_slice<SL>(P, p);
+  return true;
 }
 
 // Where the result of a row goes: out and lse, from the weighted sum o (this
@@ -290,6 +317,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   constexpr int SL = S_::SL, MT = S_::MT, KK = D / 16, DT = D / 16;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ uint8_t bad_slice[AW][8];
+  __shared__ float2 share[AW][NT * 8];   // maximum and sum of each warp's share
   // until the runs are dealt out, the front of the rings holds the block sums
   int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [AW * 32], then the total
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -331,7 +359,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   const int64_t units = scan[AW * 32] * HT;
   if (units == 0) return;                // every thread
   const int64_t workers = min(static_cast<int64_t>(P.workers), units);
-  const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t me = blockIdx.x;
   const int64_t start = run_start(me, units, workers);
   Place cons;
   cons.left = 0;
@@ -362,33 +390,43 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     cons.b = b;
     cons.ht = static_cast<int>(rest / s.nu);
     cons.li = static_cast<int>(rest - static_cast<int64_t>(cons.ht) * s.nu);
-    cons.slice = 0;
+    cons.slice = warp;
   }
   Place prod = cons;
 
-  unsigned char* const wmem = smem_raw + warp * S_::WARP;
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(wmem));
-  float4* const acc = reinterpret_cast<float4*>(wmem + S_::STAGES * S_::STAGE) + lane;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) + warp * (S_::STAGES * S_::STAGE);
+  // [slot of a fragment][warp][lane]: four floats of a warp's share
+  float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE) + lane;
 
-  // ---- the producing side: slice after slice into the ring
+  // ---- the producing side: this warp's slices into its ring, each looked up in the
+  // page table (lane j: token t0 + j mod SL) one slice before it is copied
   const T* const kbase = static_cast<const T*>(P.c.k);
   const T* const vbase = static_cast<const T*>(P.c.v);
-  bool more = seek_slice<SL>(P, prod);
-  int issued = 0;
+  int issued = 0, page = 0, place = 0;
+  bool seen = false;
+  auto look_up = [&]() {
+    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + (lane & (SL - 1));
+    seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
+    uint32_t p = __umulhi(static_cast<uint32_t>(t), P.page_magic);
+    place = static_cast<int>(static_cast<uint32_t>(t) - p * static_cast<uint32_t>(P.c.page_size));
+    if (place < 0) place += P.c.page_size, --p;            // the quotient is one off at most
+    if (place >= P.c.page_size) place -= P.c.page_size, ++p;
+    page = seen ? __ldg(P.c.table + prod.b * P.c.table_stride + p) : 0;
+  };
+  auto seek = [&]() {
+    while (!seek_slice<SL>(P, prod)) {
+      if (!next_unit(P, prod)) return false;
+      prod.slice = warp;
+    }
+    look_up();
+    return true;
+  };
+  bool more = seek();
   auto issue = [&]() {
     const int stage = issued % S_::STAGES;
     ++issued;
-    const int t0 = prod.s.unit(prod.li) * UNIT + prod.slice * SL;
-    // lane j looks token t0 + j (mod SL) up
-    const int t = t0 + (lane & (SL - 1));
-    const bool seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
-    bool there = false;
-    int64_t off = 0;
-    if (seen) {
-      const int page = P.c.table[prod.b * P.c.table_stride + t / P.c.page_size];
-      there = page >= 0 && page < P.c.num_pages;
-      if (there) off = page * P.c.page_stride + (t % P.c.page_size) * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride;
-    }
+    const bool there = seen && page >= 0 && page < P.c.num_pages;
+    const int64_t off = there ? page * P.c.page_stride + place * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride : 0;
     const bool bad = __any_sync(0xffffffffu, seen && !there);
     if (lane == 0) bad_slice[warp][stage] = bad;
     const uint32_t there_mask = __ballot_sync(0xffffffffu, there);
@@ -406,8 +444,8 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       copy16(d + SL * S_::ROWB, vbase + o, ok);
     }
     copy_commit();
-    ++prod.slice;
-    more = seek_slice<SL>(P, prod) || next_unit<SL>(P, prod);
+    prod.slice += AW;
+    more = seek();
   };
   for (int i = 0; i < S_::STAGES - 1 && more; ++i) issue();
 
@@ -415,12 +453,51 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   const int g8 = lane >> 2, t4 = lane & 3;
   const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lch = lane >> 4;      // ldmatrix, keys
   const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;      // ldmatrix, values
-  uint32_t qf[NT][KK][2];
+  uint32_t qf[S_::QS ? 1 : NT][KK][2];
+  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + AW * S_::WARP) + lane;      // [NT][KK][lane]
+  constexpr int SLOTS = DT * NT, MINE = SLOTS / AW;     // fragments of a share, and those that this warp folds
   float o[DT][NT][4], m[NT][2], l[NT][2], GM[NT][2], GL[NT][2];
+  float4 gacc[MINE];
   int consumed = 0;
-  bool fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false;
+  bool fresh_head = true, fresh_group = true, folding = false, head_part = false;
   int64_t at = start;                    // the unit's number in the batch
-  auto clear_unit = [&]() {
+  for (;;) {
+    const int u = cons.s.unit(cons.li);
+    const int tile0 = (cons.ht % P.tiles) * NT * 8;
+    if (fresh_head) {
+      // the queries of this kv head and tile, as B operands
+      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + (cons.ht / P.tiles) * P.group * P.qs.head;
+      if (S_::QS) __syncthreads();       // every warp is done with the head before
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        if (S_::QS && x != warp) continue;
+        const int row = tile0 + x * 8 + g8;
+        const int i = row / P.group;
+        const bool real = row < P.rows && i < cons.s.nnew;
+        const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+          const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) : 0u;
+          const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) : 0u;
+          if constexpr (S_::QS) qsm[(x * KK + k) * 32] = make_uint2(lo, hi);
+          else qf[x][k][0] = lo, qf[x][k][1] = hi;
+        }
+      }
+      if (S_::QS) __syncthreads();
+      fresh_head = false;
+      fresh_group = true;
+    }
+    const int g = u / GROUP;
+    if (fresh_group) {
+      const int f = cons.s.first(g), e = cons.s.past(g);
+      folding = cons.li == f && e - cons.li <= cons.left;
+      head_part = start >= at - (cons.li - f);
+#pragma unroll
+      for (int x = 0; x < NT; ++x) GM[x][0] = GM[x][1] = -INFINITY, GL[x][0] = GL[x][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) gacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      fresh_group = false;
+    }
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -429,39 +506,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         for (int e = 0; e < 4; ++e) o[d][x][e] = 0.0f;
 #pragma unroll
     for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
-    unit_bad = false;
-  };
-  clear_unit();
-  seek_slice<SL>(P, cons);
-  for (;;) {
-    const int u = cons.s.unit(cons.li);
-    const int tile0 = (cons.ht % P.tiles) * NT * 8;
-    if (fresh_head) {
-      // the queries of this kv head and tile, as B operands
-      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + (cons.ht / P.tiles) * P.group * P.qs.head;
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        const int row = tile0 + x * 8 + g8;
-        const int i = row / P.group;
-        const bool real = row < P.rows && i < cons.s.nnew;
-        const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-          qf[x][k][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) : 0u;
-          qf[x][k][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) : 0u;
-        }
-      }
-      fresh_head = false;
-      fresh_group = true;
-    }
-    if (fresh_group) {
-      const int g = u / GROUP, e = cons.s.past(g);
-      folding = cons.li == cons.s.first(g) && e - cons.li <= cons.left;
-      head_part = start >= at - (cons.li - cons.s.first(g));
-#pragma unroll
-      for (int x = 0; x < NT; ++x) GM[x][0] = GM[x][1] = -INFINITY, GL[x][0] = GL[x][1] = 0.0f;
-      fresh_group = false;
-    }
+    bool unit_bad = false;
+
+    for (cons.slice = warp; seek_slice<SL>(P, cons); cons.slice += AW) {
     // ---- one slice
     if (more) issue();
     if (issued - consumed >= S_::STAGES) copy_wait<S_::STAGES - 1>(); else copy_wait<0>();
@@ -484,7 +531,12 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         uint32_t a[4];
         ldsm(a, sk + row * S_::ROWB + (((2 * k + lch) ^ (row & 7)) * 16));
 #pragma unroll
-        for (int x = 0; x < NT; ++x) E::mma((k & 1) ? s2[x] : s[y][x], a, qf[x][k][0], qf[x][k][1]);
+        for (int x = 0; x < NT; ++x) {
+          uint2 b;
+          if constexpr (S_::QS) b = qsm[(x * KK + k) * 32];
+          else b = make_uint2(qf[x][k][0], qf[x][k][1]);
+          E::mma((k & 1) ? s2[x] : s[y][x], a, b.x, b.y);
+        }
       }
 #pragma unroll
       for (int x = 0; x < NT; ++x)
@@ -625,9 +677,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     ++consumed;
     __syncwarp();                        // the stage may be filled again
 
-    // ---- on to the next slice; at the end of the unit, its result
-    ++cons.slice;
-    if (seek_slice<SL>(P, cons)) continue;
+    }
+
+    // ---- the unit's result: the warps' shares, folded in order
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -635,9 +687,40 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
         if (unit_bad) m[x][e] = 0.0f, l[x][e] = __int_as_float(0x7fc00000);
+        if (g8 == 0) share[warp][x * 8 + 2 * t4 + e] = make_float2(m[x][e], l[x][e]);
       }
     if (unit_bad && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    const int g = u / GROUP;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+        xch[((d * NT + x) * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
+    __syncthreads();
+    float UM[NT][2], UL[NT][2];
+    float4 uacc[MINE];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) UM[x][0] = UM[x][1] = -INFINITY, UL[x][0] = UL[x][1] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) uacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < AW; ++w) {
+      Factors f[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 h = share[w][x * 8 + 2 * t4 + e];
+          f[x][e] = add_part(UM[x][e], UL[x][e], h.x, h.y);
+        }
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) {
+        const int x = (j * AW + warp) % NT;
+        fold4(uacc[j], xch[((j * AW + warp) * AW + w) * 32], pick<NT>(f, x, 0), pick<NT>(f, x, 1));
+      }
+    }
+    __syncthreads();                     // the shares may be written again
+
+    // ---- into the group, where this run holds all of it; otherwise out
     const bool head_ends = cons.li + 1 == cons.s.nu;
     const bool group_ends = cons.li + 1 == cons.s.past(g);
     bool store = true, direct = false;
@@ -645,33 +728,21 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     float2* ml = P.unit_ml;
     float* po = P.unit_o;
     if (folding) {
-      const bool first = cons.li == cons.s.first(g);
       Factors f[NT][2];
-      bool none[NT][2];                  // the row saw nothing in the unit
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          f[x][e] = Factors{1.0f, 0.0f};
-          none[x][e] = l[x][e] == 0.0f;
-          if (!none[x][e]) {
-            f[x][e] = fold_factors(GM[x][e], m[x][e]);
-            GL[x][e] = fold(GL[x][e], l[x][e], f[x][e]);
-          }
-          m[x][e] = GM[x][e];
-          l[x][e] = GL[x][e];
+          f[x][e] = add_part(GM[x][e], GL[x][e], UM[x][e], UL[x][e]);
+          UM[x][e] = GM[x][e];
+          UL[x][e] = GL[x][e];
         }
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          const float4 v = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : acc[(d * NT + x) * 32];
-          o[d][x][0] = none[x][0] ? v.x : fold(v.x, o[d][x][0], f[x][0]);
-          o[d][x][1] = none[x][1] ? v.y : fold(v.y, o[d][x][1], f[x][1]);
-          o[d][x][2] = none[x][0] ? v.z : fold(v.z, o[d][x][2], f[x][0]);
-          o[d][x][3] = none[x][1] ? v.w : fold(v.w, o[d][x][3], f[x][1]);
-          if (!group_ends) acc[(d * NT + x) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
-        }
+      for (int j = 0; j < MINE; ++j) {
+        const int x = (j * AW + warp) % NT;
+        fold4(gacc[j], uacc[j], pick<NT>(f, x, 0), pick<NT>(f, x, 1));
+        uacc[j] = gacc[j];
+      }
       store = group_ends;
       direct = cons.s.past(g) - cons.s.first(g) == cons.s.nu;
       slot = (static_cast<int64_t>(cons.b) * HT + cons.ht) * P.groups + g;
@@ -686,74 +757,61 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         for (int e = 0; e < 2; ++e) {
           const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = row / P.group;
           if (row >= P.rows || i >= cons.s.nnew) continue;
-          if (direct) {
-            const int hq = kh * P.group + (row - i * P.group);
-            T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
-            const bool none = l[x][e] == 0.0f;
+          const bool none = UL[x][e] == 0.0f;
+          const int hq = kh * P.group + (row - i * P.group);
+          T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
+          float* dst = po + (slot * (NT * 8) + r) * D + g8;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              from_float(none ? 0.0f : __fdiv_rn(o[d][x][e], l[x][e]), op[d * 16]);
-              from_float(none ? 0.0f : __fdiv_rn(o[d][x][2 + e], l[x][e]), op[d * 16 + 8]);
+          for (int j = 0; j < MINE; ++j) {
+            const int f = j * AW + warp;
+            if (f % NT != x) continue;
+            const int d = f / NT;
+            const float lo = e ? uacc[j].y : uacc[j].x, hi = e ? uacc[j].w : uacc[j].z;
+            if (direct) {
+              from_float(none ? 0.0f : __fdiv_rn(lo, UL[x][e]), op[d * 16]);
+              from_float(none ? 0.0f : __fdiv_rn(hi, UL[x][e]), op[d * 16 + 8]);
+            } else {
+              dst[d * 16] = lo;
+              dst[d * 16 + 8] = hi;
             }
-            if (P.lse && g8 == 0)
-              P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(m[x][e], l[x][e]);
-          } else {
-            float* dst = po + (slot * (NT * 8) + r) * D + g8;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              dst[d * 16] = o[d][x][e];
-              dst[d * 16 + 8] = o[d][x][2 + e];
-            }
-            if (g8 == 0) ml[slot * (NT * 8) + r] = make_float2(m[x][e], l[x][e]);
+          }
+          if (warp == 0 && g8 == 0) {
+            if (!direct) ml[slot * (NT * 8) + r] = make_float2(UM[x][e], UL[x][e]);
+            else if (P.lse) P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(UM[x][e], UL[x][e]);
           }
         }
     }
-    clear_unit();
     fresh_group |= group_ends;
     fresh_head |= head_ends;
     ++at;
-    if (!next_unit<SL>(P, cons)) break;
+    if (!next_unit(P, cons)) break;
   }
 }
 
 // ------------------------------------------------------------ the join
 
-constexpr int JW = 8;                    // warps of a join CTA, and chains of the tree
+constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
+constexpr int JB = 8;                    // parts in flight
 
 // A row of a sequence whose groups are not all in one run: group g goes to
-// chain g mod 8, each chain folds its groups in order, and the chains are
-// folded in order.  Up to 8 groups that is one fold over the groups, which a
+// chain g mod 16, each chain folds its groups in order, and the chains are
+// folded in order.  Up to 16 groups that is one fold over the groups, which a
 // single warp does.  The same CTA fills the rows without a query, and those of
 // rejected sequences.
-template <class T, int D>
+template <int D>
 struct JoinRow {
   static constexpr int E = D / 32;       // elements of a lane
   float M = -INFINITY, L = 0.0f, o[E] = {};
   __device__ __forceinline__ void add(float m, float l, const float (&v)[E]) {
-    if (l == 0.0f) return;
-    const Factors f = fold_factors(M, m);
-    L = fold(L, l, f);
+    const Factors f = add_part(M, L, m, l);
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fold(o[e], v[e], f);
   }
 };
-template <int E>
-__device__ __forceinline__ void load_part(const float2* ml, const float* po, int64_t at, int D, int lane, float2& h, float (&v)[E]) {
-  h = ml[at];
-  const float* src = po + at * D + lane * E;
-  if constexpr (E == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(src);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(src);
-    v[0] = x.x, v[1] = x.y;
-  }
-}
 
 template <class T, int D>
 __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int block_rows, int64_t items) {
   constexpr int E = D / 32;
-  using Row = JoinRow<T, D>;
   __shared__ float2 chain_ml[JW];
   __shared__ float chain_o[JW][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -773,41 +831,91 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
     const int64_t u0 = P.base[b] * HT + static_cast<int64_t>(ht) * s.nu;
     const bool one_group = s.nu > 0 && s.first(glast) == 0;
     const bool direct = one_group && run_of(u0, units, workers) == run_of(u0 + s.nu - 1, units, workers);
+    if (direct && s.nnew == P.c.n) continue;
     const int tile0 = (ht % P.tiles) * tile_rows;
     const bool wide = glast >= JW;       // more groups than chains: all warps on one row
+    const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;       // groups [0, gs) and [gl, glast]
     for (int j = wide ? 0 : warp; j < block_rows; j += wide ? 1 : JW) {
       const int r = rb * block_rows + j, row = tile0 + r, i = row / P.group;
       if (r >= tile_rows || row >= P.rows) continue;
       const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
       const bool query = s.ok && i < s.nnew;
       if (query && direct) continue;
-      Row acc;
+      JoinRow<D> acc;
       if (query) {
-        const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;   // groups [0, gs) and [gl, glast]
+        // The parts in order, JB of them in flight: a whole group is a part, a group
+        // that runs share is its units.
+        JoinRow<D> inner;
         const int step = wide ? JW : 1;
-        for (int g = wide ? warp : 0; g <= glast; g += step) {
-          if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
-          if (g > glast) break;
-          const int f = s.first(g), e = s.past(g);
-          if (f >= e) continue;
-          const int64_t ua = u0 + f;
-          if (run_of(ua, units, workers) == run_of(u0 + e - 1, units, workers)) {
-            float2 h;
-            float v[E];
-            load_part<E>(P.group_ml, P.group_o, (entry * P.groups + g) * tile_rows + r, D, lane, h, v);
-            acc.add(h.x, h.y, v);
-            continue;
+        int g = wide ? warp : 0, k = -1, f = 0, e = 0;       // k >= 0: the next unit of a shared group
+        int64_t w = 0, w_past = 0, ua = 0;
+        bool in_slot0 = false;
+        auto next_part = [&](const float*& po, float2& h, int& kind) {
+          // kind 0: none left; 1: a group; 2: a unit; 3: the last unit of its group
+          if (k < 0) {
+            for (;; g += step) {
+              if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
+              if (g > glast) return kind = 0, void();
+              f = s.first(g), e = s.past(g);
+              if (f < e) break;
+            }
+            ua = u0 + f;
+            w = run_of(ua, units, workers);
+            w_past = run_start(w + 1, units, workers);
+            if (w_past >= u0 + e) {
+              const int64_t at = (entry * P.groups + g) * tile_rows + r;
+              h = P.group_ml[at];
+              po = P.group_o + at * D;
+              g += step;
+              return kind = 1, void();
+            }
+            k = f;
+            in_slot0 = run_start(w, units, workers) >= ua;
+          } else if (u0 + k >= w_past) {
+            ++w;
+            w_past = run_start(w + 1, units, workers);
+            in_slot0 = true;             // this run starts in the group
           }
-          Row part;
-          for (int k = f; k < e; ++k) {
-            const int64_t w = run_of(u0 + k, units, workers);
-            const int64_t slot = w * (2 * GROUP) + (run_start(w, units, workers) >= ua ? 0 : GROUP) + s.unit(k) % GROUP;
-            float2 h;
-            float v[E];
-            load_part<E>(P.unit_ml, P.unit_o, slot * tile_rows + r, D, lane, h, v);
-            part.add(h.x, h.y, v);
+          const int64_t at = (w * (2 * GROUP) + (in_slot0 ? 0 : GROUP) + s.unit(k) % GROUP) * tile_rows + r;
+          h = P.unit_ml[at];
+          po = P.unit_o + at * D;
+          kind = 2;
+          if (++k == e) {
+            k = -1;
+            g += step;
+            kind = 3;
           }
-          acc.add(part.M, part.L, part.o);
+        };
+        for (;;) {
+          float2 h[JB];
+          float v[JB][E];
+          int kind[JB];
+          bool any = false;
+#pragma unroll
+          for (int q = 0; q < JB; ++q) {
+            const float* po = nullptr;
+            next_part(po, h[q], kind[q]);
+            if (kind[q]) {
+              any = true;
+              if constexpr (E == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(po + lane * E);
+                v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(po + lane * E);
+                v[q][0] = x.x, v[q][1] = x.y;
+              }
+            }
+          }
+          if (!any) break;
+#pragma unroll
+          for (int q = 0; q < JB; ++q) {
+            if (kind[q] == 1) acc.add(h[q].x, h[q].y, v[q]);
+            if (kind[q] >= 2) inner.add(h[q].x, h[q].y, v[q]);
+            if (kind[q] == 3) {
+              acc.add(inner.M, inner.L, inner.o);
+              inner = JoinRow<D>();
+            }
+          }
         }
       }
       if (query && wide) {
@@ -816,7 +924,7 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
         for (int e = 0; e < E; ++e) chain_o[warp][lane * E + e] = acc.o[e];
         __syncthreads();
         if (warp == 0) {
-          acc = Row();
+          acc = JoinRow<D>();
           for (int c = 0; c < JW; ++c) {
             float v[E];
 #pragma unroll
@@ -944,14 +1052,14 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   static bool done[64] = {};
   rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, done);
   if (s != RLK_OK) return s;
-  attn_kernel<T, D, NT><<<P.workers / AW, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
+  attn_kernel<T, D, NT><<<P.workers, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them
-  const int block_rows = P.groups <= JW ? JW : 1;
+  const int block_rows = P.groups <= JW ? 8 : 1;
   const int64_t items = P.B * P.c.kv_heads * P.tiles * ((NT * 8 + block_rows - 1) / block_rows);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < NUM_SMS * 8 ? items : NUM_SMS * 8));
+  cfg.gridDim = dim3(static_cast<unsigned>(items < NUM_SMS * 4 ? items : NUM_SMS * 4));
   cfg.blockDim = dim3(JW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -1052,6 +1160,8 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
   P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
   P.group_o = reinterpret_cast<float*>(ws + y.group_o);
+  P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
+                                       : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
   P.groups = static_cast<int>(y.groups);
   P.workers = workers_of(t.nt);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
