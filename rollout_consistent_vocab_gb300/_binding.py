@@ -896,7 +896,7 @@ def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int,
     tiles = -(-rows // 32)
     nt = -(-rows // (8 * tiles))
     entries, units = B * kv_heads * tiles, -(-max_tokens // 256)
-    parts = (min(entries * units, 304 if nt <= 2 else 152) * 8 + entries * -(-units // 4)) * nt * 8
+    parts = (min(entries * units, 304) * 8 + entries * -(-units // 4)) * nt * 8
     return ((B + 1) * 8 + 15) // 16 * 16 + parts * (8 + head_dim * 4)
 
 

@@ -95,21 +95,25 @@ constexpr int AW = 4;                    // warps of a CTA
 constexpr int NUM_SMS = 152;
 
 // Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in
-// tiles of 8 NT.
+// tiles of 8 NT.  A warp works on slices of 32 tokens; they are copied in halves
+// of 16, STAGES halves in its ring.
+constexpr int SL = 32;
+constexpr int HALF = SL / 2;
 template <int D, int NT>
 struct Shape {
-  static constexpr int CTAS = NT <= 2 ? 2 : 1;               // per SM
-  static constexpr int SL = D == 128 ? 16 : 32;              // tokens of a slice
-  static constexpr int MT = SL / 16;
-  static constexpr int STAGES = NT == 1 ? 3 : NT == 2 ? 2 : 4;
+  static constexpr int CTAS = 2;                             // per SM
   static constexpr int ROWB = D * 2;                         // bytes of a head row
-  static constexpr int STAGE = 2 * SL * ROWB;                // keys, then values
-  static constexpr int XCH = NT * 8 * D * 4;                 // a warp's share of a unit's result
-  static constexpr int WARP = STAGES * STAGE + XCH;
-  static constexpr bool QS = NT >= 3;                        // queries in shared memory, not in registers
-  static constexpr int SMEM = AW * WARP + (QS ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr int STAGE = 2 * HALF * ROWB;              // keys, then values
+  static constexpr int STAGES = D == 64 ? 6 : NT == 4 ? 2 : 3;
+  static constexpr int SLOTS = D / 16 * NT;                  // fragments (four floats a lane) of a warp's result
+  static constexpr int PASSES = D == 64 && NT == 2 ? 1 : NT;
+  static constexpr int XCH = SLOTS / PASSES * 512;           // ... exchanged in so many passes
+  static constexpr bool QS = D == 128 && NT == 4;            // queries in shared memory, not in registers
+  static constexpr int SMEM = AW * (STAGES * STAGE + XCH) + (QS ? NT * (D / 16) * 32 * 8 : 0);
+  static_assert(SLOTS % PASSES == 0 && SLOTS / PASSES % AW == 0, "every warp folds as many fragments in each pass");
+  static_assert(2 * (SMEM + AW * NT * 64 + 64 + 1024) <= 228 * 1024, "two CTAs in the shared memory of an SM");
 };
-constexpr int workers_of(int nt) { return NUM_SMS * (nt <= 2 ? 2 : 1); }
+constexpr int WORKERS = NUM_SMS * 2;
 
 struct AttnParams {
   PagedParams c;
@@ -120,7 +124,9 @@ struct AttnParams {
   int rows;                     // n * group
   int tiles;                    // row tiles
   int64_t B;
-  float c2;                     // scale * log2(e)
+  float c2;                     // |scale| * log2(e)
+  uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
+  bool page16;                  // 16 tokens from a multiple of 16 on lie in one page
   int window, sinks;
   float* lse;
   int64_t* base;                // [B + 1] units of the sequences before, per kv head and tile
@@ -130,7 +136,6 @@ struct AttnParams {
   float* group_o;
   uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
   int groups;                   // groups of the longest sequence that the table can hold
-  int workers;
 };
 
 // What of a sequence is visible to its new tokens: units [0, us) for the sinks
@@ -161,10 +166,20 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
   return s;
 }
 
-__device__ __forceinline__ int64_t run_start(int64_t k, int64_t units, int64_t workers) { return k * units / workers; }
-__device__ __forceinline__ int64_t run_of(int64_t u, int64_t units, int64_t workers) {
-  return ((u + 1) * workers - 1) / units;
-}
+// The units of the batch (fewer than 2^31) in equal runs, the first ones one longer.
+struct Runs {
+  uint32_t len, more, workers;
+  __device__ __forceinline__ Runs(uint32_t units, uint32_t most) {
+    workers = min(units, most);
+    len = workers ? units / workers : 0;
+    more = workers ? units - len * workers : 0;
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t k) const { return k * len + min(k, more); }
+  __device__ __forceinline__ uint32_t of(uint32_t u) const {
+    const uint32_t cut = more * (len + 1);
+    return u < cut ? u / (len + 1) : more + (u - cut) / len;
+  }
+};
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -213,7 +228,7 @@ __device__ __forceinline__ Factors pick(const Factors (&f)[NT][2], int x, int e)
 
 template <class T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
-  static constexpr float OFF = 0.0f;
+  static constexpr float OFF = 0.0f, SLACK = 8.0f;
   static constexpr uint32_t EXP = 0x7F807F80u;
   static constexpr float TINY = 9.094947017729282e-13f;      // 2^-40
   // The weights (a, b) >= 0 as the sum of two pairs of elements.  Both parts of a
@@ -231,11 +246,11 @@ template <> struct Elem<__nv_bfloat16> {
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
-// f16 holds weights in units of 2^-12, so that the smallest ones keep their bits
+// f16 holds weights in units of 2^-8, so that the smallest ones keep their bits
 template <> struct Elem<__half> {
-  static constexpr float OFF = 12.0f;
+  static constexpr float OFF = 8.0f, SLACK = 6.0f;
   static constexpr uint32_t EXP = 0x7C007C00u;
-  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16: 2^-36 of the row's largest weight
+  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16: 2^-32 of the row's largest weight
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
     const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
@@ -264,8 +279,12 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// 16 bytes into shared memory; zeros where !there (src is then not read)
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+// 16 bytes into shared memory
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// ... zeros where !there (src is then not read)
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -279,7 +298,6 @@ struct Place {
   int left;                              // units of the run from this one on
 };
 // This warp's first slice of the unit from p.slice on that some new token sees, or false.
-template <int SL>
 __device__ __forceinline__ bool seek_slice(const AttnParams& P, Place& p) {
   for (; p.slice < UNIT / SL; p.slice += AW) {
     const int t0 = p.s.unit(p.li) * UNIT + p.slice * SL;
@@ -314,9 +332,9 @@ template <class T, int D, int NT>
 __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const AttnParams P) {
   using S_ = Shape<D, NT>;
   using E = Elem<T>;
-  constexpr int SL = S_::SL, MT = S_::MT, KK = D / 16, DT = D / 16;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ uint8_t bad_slice[AW][8];
+  constexpr int KK = D / 16, DT = D / 16, SLOTS = S_::SLOTS, MINE = SLOTS / AW;
+  extern __shared__ __align__(256) unsigned char smem_raw[];
+  __shared__ uint8_t bad_half[AW][8];
   __shared__ float2 share[AW][NT * 8];   // maximum and sum of each warp's share
   // until the runs are dealt out, the front of the rings holds the block sums
   int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [AW * 32], then the total
@@ -356,36 +374,28 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     if (tid == 0) P.base[P.B] = scan[AW * 32];
   }
   const int HT = P.c.kv_heads * P.tiles;
-  const int64_t units = scan[AW * 32] * HT;
-  if (units == 0) return;                // every thread
-  const int64_t workers = min(static_cast<int64_t>(P.workers), units);
-  const int64_t me = blockIdx.x;
-  const int64_t start = run_start(me, units, workers);
+  const Runs runs(static_cast<uint32_t>(scan[AW * 32] * HT), WORKERS);
+  const uint32_t me = blockIdx.x;
+  if (me >= runs.workers) return;        // every thread
+  const uint32_t start = runs.start(me);
   Place cons;
-  cons.left = 0;
-  int blk = 0;
-  int64_t blk_base = 0;
-  if (me < workers) {
-    // the last block of sequences that begins at or before the run
-#pragma unroll
-    for (int j = 0; j < AW; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= start / HT));
-    blk -= 1;
-    blk_base = scan[blk];
-  }
-  __syncthreads();                       // the rings are free
-  if (me >= workers) return;
-  cons.left = static_cast<int>(run_start(me + 1, units, workers) - start);
+  cons.left = static_cast<int>(runs.start(me + 1) - start);
   {
     const int64_t at = start / HT;       // the sequence that holds it: [run, run + nu)
+    int blk = 0;                         // the last block of sequences that begins at or before it
+#pragma unroll
+    for (int j = 0; j < AW; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
+    blk -= 1;
     int b = blk * per;
-    int64_t run = blk_base;
+    int64_t run = scan[blk];
+    __syncthreads();                     // the rings are free
     Seq s = load_seq(P, b);
     while (run + s.nu <= at && b + 1 < P.B) {
       run += s.nu;
       s = load_seq(P, ++b);
     }
     if (s.nu == 0) return;               // (the lengths changed under the call)
-    const int64_t rest = start - run * HT;
+    const int64_t rest = static_cast<int64_t>(start) - run * HT;
     cons.s = s;
     cons.b = b;
     cons.ht = static_cast<int>(rest / s.nu);
@@ -398,14 +408,15 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   // [slot of a fragment][warp][lane]: four floats of a warp's share
   float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE) + lane;
 
-  // ---- the producing side: this warp's slices into its ring, each looked up in the
-  // page table (lane j: token t0 + j mod SL) one slice before it is copied
+  // ---- the producing side: this warp's halves into its ring, each looked up in the
+  // page table (lane j: token t0 + j mod 16) one half before it is copied
   const T* const kbase = static_cast<const T*>(P.c.k);
   const T* const vbase = static_cast<const T*>(P.c.v);
-  int issued = 0, page = 0, place = 0;
+  uint32_t issued = 0, consumed = 0;     // halves
+  int issue_stage = 0, use_stage = 0, half = 0, page = 0, place = 0;
   bool seen = false;
   auto look_up = [&]() {
-    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + (lane & (SL - 1));
+    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + half * HALF + (lane & (HALF - 1));
     seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
     uint32_t p = __umulhi(static_cast<uint32_t>(t), P.page_magic);
     place = static_cast<int>(static_cast<uint32_t>(t) - p * static_cast<uint32_t>(P.c.page_size));
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     page = seen ? __ldg(P.c.table + prod.b * P.c.table_stride + p) : 0;
   };
   auto seek = [&]() {
-    while (!seek_slice<SL>(P, prod)) {
+    while (!seek_slice(P, prod)) {
       if (!next_unit(P, prod)) return false;
       prod.slice = warp;
     }
@@ -422,45 +433,64 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     return true;
   };
   bool more = seek();
+  constexpr int CH = D / 8;              // 16-byte pieces of a row
+  constexpr int RPI = 32 / CH;           // rows that one instruction of the warp copies
+  const int piece = lane % CH, crow = lane / CH;
   auto issue = [&]() {
-    const int stage = issued % S_::STAGES;
-    ++issued;
     const bool there = seen && page >= 0 && page < P.c.num_pages;
     const int64_t off = there ? page * P.c.page_stride + place * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride : 0;
-    const bool bad = __any_sync(0xffffffffu, seen && !there);
-    if (lane == 0) bad_slice[warp][stage] = bad;
     const uint32_t there_mask = __ballot_sync(0xffffffffu, there);
-    constexpr int CH = D / 8;            // 16-byte pieces of a row
-    constexpr int RPI = 32 / CH;         // rows per instruction
-    const int piece = lane % CH;
-    const uint32_t dst = ring + stage * S_::STAGE;
+    const bool bad = __any_sync(0xffffffffu, seen && !there);
+    if (lane == 0) bad_half[warp][issue_stage] = bad;
+    const uint32_t dst = ring + issue_stage * S_::STAGE;
+    if (P.page16 && there_mask == 0xffffffffu) {
+      // 16 tokens of one page: rows a constant stride apart
+      const int64_t o = __shfl_sync(0xffffffffu, off, 0) + crow * P.c.token_stride + piece * 8;
+      const T* ks = kbase + o;
+      const T* vs = vbase + o;
 #pragma unroll
-    for (int j = 0; j < SL / RPI; ++j) {
-      const int r = j * RPI + lane / CH;
-      const int64_t o = __shfl_sync(0xffffffffu, off, r) + piece * 8;
-      const bool ok = (there_mask >> r) & 1u;
-      const uint32_t d = dst + r * S_::ROWB + ((piece ^ (r & 7)) * 16);
-      copy16(d, kbase + o, ok);
-      copy16(d + SL * S_::ROWB, vbase + o, ok);
+      for (int j = 0; j < HALF / RPI; ++j) {
+        const int rr = j * RPI + crow;
+        const uint32_t d = dst + rr * S_::ROWB + ((piece ^ (rr & 7)) * 16);
+        copy16(d, ks);
+        copy16(d + HALF * S_::ROWB, vs);
+        ks += RPI * P.c.token_stride;
+        vs += RPI * P.c.token_stride;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < HALF / RPI; ++j) {
+        const int rr = j * RPI + crow;
+        const int64_t o = __shfl_sync(0xffffffffu, off, rr) + piece * 8;
+        const bool ok = (there_mask >> rr) & 1u;
+        const uint32_t d = dst + rr * S_::ROWB + ((piece ^ (rr & 7)) * 16);
+        copy16_if(d, kbase + o, ok);
+        copy16_if(d + HALF * S_::ROWB, vbase + o, ok);
+      }
     }
     copy_commit();
-    prod.slice += AW;
-    more = seek();
+    ++issued;
+    if (++issue_stage == S_::STAGES) issue_stage = 0;
+    if ((half ^= 1) == 0) {
+      prod.slice += AW;
+      more = seek();
+    } else {
+      look_up();
+    }
   };
-  for (int i = 0; i < S_::STAGES - 1 && more; ++i) issue();
+  for (int i = 0; i < S_::STAGES && more; ++i) issue();
 
   // ---- the consuming side
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lch = lane >> 4;      // ldmatrix, keys
-  const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;      // ldmatrix, values
+  // this lane's row of an ldmatrix, with the swizzle of its first piece; piece 2 k is at that ^ 32 k
+  const uint32_t klane = (((lane >> 3) & 1) * 8 + (lane & 7)) * S_::ROWB + (((lane >> 4) ^ (lane & 7)) * 16);
+  const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * S_::ROWB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
   uint32_t qf[S_::QS ? 1 : NT][KK][2];
-  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + AW * S_::WARP) + lane;      // [NT][KK][lane]
-  constexpr int SLOTS = DT * NT, MINE = SLOTS / AW;     // fragments of a share, and those that this warp folds
+  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + AW * (S_::STAGES * S_::STAGE + S_::XCH)) + lane;      // [NT][KK][lane]
   float o[DT][NT][4], m[NT][2], l[NT][2], GM[NT][2], GL[NT][2];
   float4 gacc[MINE];
-  int consumed = 0;
   bool fresh_head = true, fresh_group = true, folding = false, head_part = false;
-  int64_t at = start;                    // the unit's number in the batch
+  uint32_t at = start;                   // the unit's number in the batch
   for (;;) {
     const int u = cons.s.unit(cons.li);
     const int tile0 = (cons.ht % P.tiles) * NT * 8;
@@ -477,8 +507,8 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
-          const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) : 0u;
-          const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) : 0u;
+          const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.q_sign : 0u;
+          const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.q_sign : 0u;
           if constexpr (S_::QS) qsm[(x * KK + k) * 32] = make_uint2(lo, hi);
           else qf[x][k][0] = lo, qf[x][k][1] = hi;
         }
@@ -508,214 +538,258 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
     bool unit_bad = false;
 
-    for (cons.slice = warp; seek_slice<SL>(P, cons); cons.slice += AW) {
-    // ---- one slice
-    if (more) issue();
-    if (issued - consumed >= S_::STAGES) copy_wait<S_::STAGES - 1>(); else copy_wait<0>();
-    __syncwarp();
-    const int stage = consumed % S_::STAGES;
-    const uint32_t sk = ring + stage * S_::STAGE, sv = sk + SL * S_::ROWB;
-    unit_bad |= bad_slice[warp][stage] != 0;
-    const int t0 = u * UNIT + cons.slice * SL;
-    float s[MT][NT][4];
+    for (cons.slice = warp; seek_slice(P, cons); cons.slice += AW) {
+      // ---- one slice: its two halves have landed
+      if (issued - consumed == S_::STAGES) copy_wait<S_::STAGES - 2>(); else copy_wait<0>();
+      __syncwarp();
+      uint32_t sk[2];
 #pragma unroll
-    for (int y = 0; y < MT; ++y) {
-      float s2[NT][4];
+      for (int y = 0; y < 2; ++y) {
+        sk[y] = ring + use_stage * S_::STAGE;
+        unit_bad |= bad_half[warp][use_stage] != 0;
+        if (++use_stage == S_::STAGES) use_stage = 0;
+      }
+      const int t0 = u * UNIT + cons.slice * SL;
+      float s[2][NT][4];
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[y][x][e] = s2[x][e] = 0.0f;
-      const int row = y * 16 + lrow;
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][x][e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
-        uint32_t a[4];
-        ldsm(a, sk + row * S_::ROWB + (((2 * k + lch) ^ (row & 7)) * 16));
+        uint2 bq[NT];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          uint2 b;
-          if constexpr (S_::QS) b = qsm[(x * KK + k) * 32];
-          else b = make_uint2(qf[x][k][0], qf[x][k][1]);
-          E::mma((k & 1) ? s2[x] : s[y][x], a, b.x, b.y);
+          if constexpr (S_::QS) bq[x] = qsm[(x * KK + k) * 32];
+          else bq[x] = make_uint2(qf[x][k][0], qf[x][k][1]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t a[4];
+          ldsm(a, (sk[y] + klane) ^ (32 * k));
+#pragma unroll
+          for (int x = 0; x < NT; ++x) E::mma(s[y][x], a, bq[x].x, bq[x].y);
         }
       }
+      // masks: the queries stand at p0 .. len - 1
+      const int p0 = cons.s.len - cons.s.nnew;
+      const bool masked = t0 + SL - 1 > p0 ||
+                          (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 + SL > P.sinks);
+      uint32_t hidden = 0;               // bit (y NT + x) 4 + e (of the lane's scores)
+      if (masked) {
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[y][x][e] = (s[y][x][e] + s2[x][e]) * P.c2;
-    }
-    // masks: the queries stand at p0 .. len - 1
-    const int p0 = cons.s.len - cons.s.nnew;
-    const bool masked = t0 + SL - 1 > p0 ||
-                        (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 + SL > P.sinks);
-    if (masked) {
+          for (int e = 0; e < 2; ++e) {
+            const int pos = p0 + (tile0 + x * 8 + 2 * t4 + e) / P.group;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const int t = t0 + y * HALF + g8 + 8 * f;
+                if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks)) {
+                  s[y][x][2 * f + e] = -INFINITY;
+                  hidden |= 1u << ((y * NT + x) * 4 + 2 * f + e);
+                }
+              }
+          }
+      }
+      // each query row's reference m (the lanes of equal t4 share a row's tokens): it follows
+      // the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
+      bool scaled = false;
+      float fac[NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int pos = p0 + (tile0 + x * 8 + 2 * t4 + e) / P.group;
+          float mx = fmaxf(fmaxf(s[0][x][e], s[0][x][2 + e]), fmaxf(s[1][x][e], s[1][x][2 + e]));
 #pragma unroll
-          for (int y = 0; y < MT; ++y)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int t = t0 + y * 16 + g8 + 8 * f;
-              if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks))
-                s[y][x][2 * f + e] = -INFINITY;
+          for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          mx *= P.c2;
+          fac[x][e] = 1.0f;
+          if (mx > m[x][e] + E::SLACK) {
+            if (m[x][e] != -INFINITY) {
+              fac[x][e] = ex2f(m[x][e] - mx);
+              scaled = true;
             }
-        }
-    }
-    // running maximum and sum of each query row (the lanes of equal t4 share a row's tokens)
-    uint32_t pf[MT][NT][4];              // weights: two halves of the dtype's bits each, tokens 0-7 and 8-15
-    bool scaled = false;
-    float fac[NT][2];
-#pragma unroll
-    for (int x = 0; x < NT; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = m[x][e];
-#pragma unroll
-        for (int y = 0; y < MT; ++y) mx = fmaxf(mx, fmaxf(s[y][x][e], s[y][x][2 + e]));
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        fac[x][e] = mx == m[x][e] ? 1.0f : ex2f(m[x][e] - mx);
-        scaled |= fac[x][e] != 1.0f;
-        m[x][e] = mx;
-        const float sub = mx == -INFINITY ? 0.0f : mx - E::OFF;
-        float sum = 0.0f;
-#pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          s[y][x][e] = ex2f(s[y][x][e] - sub);
-          s[y][x][2 + e] = ex2f(s[y][x][2 + e] - sub);
-          sum += s[y][x][e] + s[y][x][2 + e];
-        }
-        l[x][e] = l[x][e] * fac[x][e] + sum;
-      }
-    if (__any_sync(0xffffffffu, scaled)) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
-    }
-#pragma unroll
-    for (int y = 0; y < MT; ++y)
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        E::split(s[y][x][0], s[y][x][1], pf[y][x][0], pf[y][x][2]);
-        E::split(s[y][x][2], s[y][x][3], pf[y][x][1], pf[y][x][3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pf[y][x][e] = movm(pf[y][x][e]);
-      }
-    // values: a masked token's must not come in even as 0 * inf
-    uint32_t odd = 0;
-    if (masked) {
-#pragma unroll
-      for (int y = 0; y < MT; ++y) {
-        const int row = y * 16 + vrow;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          uint32_t a[4];
-          ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            odd |= ((a[e] & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) | ((a[e] & E::EXP & 0xFFFF0000u) == (E::EXP & 0xFFFF0000u));
-        }
-      }
-    }
-    if (!__any_sync(0xffffffffu, odd)) {
-#pragma unroll
-      for (int y = 0; y < MT; ++y) {
-        const int row = y * 16 + vrow;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          uint32_t a[4];
-          ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
-#pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            E::mma(o[d][x], a, pf[y][x][2], pf[y][x][3]);
-            E::mma(o[d][x], a, pf[y][x][0], pf[y][x][1]);
+            m[x][e] = mx;
           }
         }
-      }
-    } else {
-      // query by query, with zeros in the place of the values that it does not see:
-      // for its rows the same products as above, had those values been finite
-      const int i0 = tile0 / P.group, i1 = min(P.c.n - 1, (tile0 + NT * 8 - 1) / P.group);
-      for (int i = i0; i <= i1; ++i) {
-        const int pos = p0 + i;
+      if (__any_sync(0xffffffffu, scaled)) {
 #pragma unroll
-        for (int y = 0; y < MT; ++y) {
+        for (int x = 0; x < NT; ++x) l[x][0] *= fac[x][0], l[x][1] *= fac[x][1];
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float sub = m[x][e] == -INFINITY ? E::OFF : E::OFF - m[x][e];
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int f = 0; f < 4; f += 2) s[y][x][f + e] = ex2f(__fmaf_rn(s[y][x][f + e], P.c2, sub));
+        }
+      if (masked) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((hidden >> ((y * NT + x) * 4 + e)) & 1u) s[y][x][e] = 0.0f;
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          l[x][e] += (s[0][x][e] + s[0][x][2 + e]) + (s[1][x][e] + s[1][x][2 + e]);
+      // values: a masked token's must not come in even as 0 * inf
+      uint32_t odd = 0;
+      if (masked) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, (sk[y] + HALF * S_::ROWB + vlane) ^ (32 * d));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              odd |= ((a[e] & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) | ((a[e] & E::EXP & 0xFFFF0000u) == (E::EXP & 0xFFFF0000u));
+          }
+      }
+      const bool careful = __any_sync(0xffffffffu, odd);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t pf[NT][4];              // weights: tokens 0-7 and 8-15, then what the dtype dropped of them
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          E::split(s[y][x][0], s[y][x][1], pf[x][0], pf[x][2]);
+          E::split(s[y][x][2], s[y][x][3], pf[x][1], pf[x][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
+        }
+        const uint32_t sv = sk[y] + HALF * S_::ROWB + vlane;
+        if (!careful) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, sv ^ (32 * d));
+#pragma unroll
+            for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][2], pf[x][3]);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][0], pf[x][1]);
+          }
+          continue;
+        }
+        // query by query, with zeros in the place of the values that it does not see:
+        // for its rows the same products as above, had those values been finite
+        const int i0 = tile0 / P.group, i1 = min(P.c.n - 1, (tile0 + NT * 8 - 1) / P.group);
+        for (int i = i0; i <= i1; ++i) {
+          const int pos = p0 + i;
           uint32_t keep[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             keep[f] = 0u;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int t = t0 + y * 16 + 8 * f + 2 * t4 + e;
+              const int t = t0 + y * HALF + 8 * f + 2 * t4 + e;
               if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) keep[f] |= 0xFFFFu << (16 * e);
             }
           }
-          const int row = y * 16 + vrow;
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
             uint32_t a[4];
-            ldsm_t(a, sv + row * S_::ROWB + (((2 * d + vch) ^ (row & 7)) * 16));
+            ldsm_t(a, sv ^ (32 * d));
             a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-              float r[4] = {o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]};
-              E::mma(r, a, pf[y][x][2], pf[y][x][3]);
-              E::mma(r, a, pf[y][x][0], pf[y][x][1]);
+              float v[4] = {o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]};
+              E::mma(v, a, pf[x][2], pf[x][3]);
+              E::mma(v, a, pf[x][0], pf[x][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if ((tile0 + x * 8 + 2 * t4 + (e & 1)) / P.group == i) o[d][x][e] = r[e];
+                if ((tile0 + x * 8 + 2 * t4 + (e & 1)) / P.group == i) o[d][x][e] = v[e];
             }
           }
         }
       }
+      consumed += 2;
+      __syncwarp();                      // the stages may be filled again
+      while (more && issued - consumed < S_::STAGES) issue();
     }
-    ++consumed;
-    __syncwarp();                        // the stage may be filled again
 
-    }
-
-    // ---- the unit's result: the warps' shares, folded in order
+    // ---- the unit's result: the warps' shares brought to one maximum and summed in order
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
+        if (l[x][e] == 0.0f) {           // nothing seen: no trace, whatever the values were
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d][x][e] = o[d][x][2 + e] = 0.0f;
+        }
         if (unit_bad) m[x][e] = 0.0f, l[x][e] = __int_as_float(0x7fc00000);
         if (g8 == 0) share[warp][x * 8 + 2 * t4 + e] = make_float2(m[x][e], l[x][e]);
       }
     if (unit_bad && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-        xch[((d * NT + x) * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
-    __syncthreads();
-    float UM[NT][2], UL[NT][2];
+    float UM[NT][2], UL[NT][2], wt[NT][2][AW];
     float4 uacc[MINE];
+    constexpr int PER_PASS = MINE / S_::PASSES;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) UM[x][0] = UM[x][1] = -INFINITY, UL[x][0] = UL[x][1] = 0.0f;
+    for (int pass = 0; pass < S_::PASSES; ++pass) {
+      if (pass > 0) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < MINE; ++j) uacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int f = 0; f < PER_PASS * AW; ++f) {
+        const int d = (pass * PER_PASS * AW + f) / NT, x = (pass * PER_PASS * AW + f) % NT;
+        xch[(f * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
+      }
+      __syncthreads();
+      if (pass == 0) {
 #pragma unroll
-    for (int w = 0; w < AW; ++w) {
-      Factors f[NT][2];
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+          for (int e = 0; e < 2; ++e) {
+            float2 h[AW];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 h = share[w][x * 8 + 2 * t4 + e];
-          f[x][e] = add_part(UM[x][e], UL[x][e], h.x, h.y);
+            for (int w = 0; w < AW; ++w) h[w] = share[w][x * 8 + 2 * t4 + e];
+            float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < AW; ++w) mx = fmaxf(mx, h[w].x);
+#pragma unroll
+            for (int w = 0; w < AW; ++w) {
+              wt[x][e][w] = h[w].y == 0.0f ? 0.0f : ex2f(h[w].x - mx);
+              sum = __fmaf_rn(h[w].y, wt[x][e][w], sum);
+            }
+            UM[x][e] = mx;
+            UL[x][e] = sum;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < PER_PASS; ++j) {
+        const int x = ((pass * PER_PASS + j) * AW + warp) % NT;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < AW; ++w) {
+          const float4 z = xch[((j * AW + warp) * AW + w) * 32];
+          float w0 = wt[0][0][w], w1 = wt[0][1][w];
+#pragma unroll
+          for (int i = 1; i < NT; ++i)
+            if (x == i) w0 = wt[i][0][w], w1 = wt[i][1][w];
+          v.x = __fmaf_rn(z.x, w0, v.x);
+          v.y = __fmaf_rn(z.y, w1, v.y);
+          v.z = __fmaf_rn(z.z, w0, v.z);
+          v.w = __fmaf_rn(z.w, w1, v.w);
         }
-#pragma unroll
-      for (int j = 0; j < MINE; ++j) {
-        const int x = (j * AW + warp) % NT;
-        fold4(uacc[j], xch[((j * AW + warp) * AW + w) * 32], pick<NT>(f, x, 0), pick<NT>(f, x, 1));
+        uacc[pass * PER_PASS + j] = v;
       }
     }
     __syncthreads();                     // the shares may be written again
@@ -724,7 +798,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     const bool head_ends = cons.li + 1 == cons.s.nu;
     const bool group_ends = cons.li + 1 == cons.s.past(g);
     bool store = true, direct = false;
-    int64_t slot = me * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
+    int64_t slot = static_cast<int64_t>(me) * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
     float2* ml = P.unit_ml;
     float* po = P.unit_o;
     if (folding) {
@@ -791,7 +865,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 // ------------------------------------------------------------ the join
 
 constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
-constexpr int JB = 8;                    // parts in flight
+constexpr int JG = 2;                    // groups in flight
 
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, each chain folds its groups in order, and the chains are
@@ -817,8 +891,7 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HT = P.c.kv_heads * P.tiles;
-  const int64_t units = P.base[P.B] * HT;
-  const int64_t workers = min(static_cast<int64_t>(P.workers), units);
+  const Runs runs(static_cast<uint32_t>(P.base[P.B] * HT), WORKERS);
   const int blocks = (tile_rows + block_rows - 1) / block_rows;
   const float nan = __int_as_float(0x7fc00000);
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -828,9 +901,9 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
     const Seq s = load_seq(P, b);
     if (!s.ok && ht == 0 && rb == 0 && threadIdx.x == 0 && P.c.err) atomicAdd(P.c.err, 1);
     const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
-    const int64_t u0 = P.base[b] * HT + static_cast<int64_t>(ht) * s.nu;
+    const uint32_t u0 = static_cast<uint32_t>(P.base[b] * HT) + static_cast<uint32_t>(ht) * s.nu;
     const bool one_group = s.nu > 0 && s.first(glast) == 0;
-    const bool direct = one_group && run_of(u0, units, workers) == run_of(u0 + s.nu - 1, units, workers);
+    const bool direct = one_group && runs.of(u0) == runs.of(u0 + s.nu - 1);
     if (direct && s.nnew == P.c.n) continue;
     const int tile0 = (ht % P.tiles) * tile_rows;
     const bool wide = glast >= JW;       // more groups than chains: all warps on one row
@@ -843,78 +916,48 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
       if (query && direct) continue;
       JoinRow<D> acc;
       if (query) {
-        // The parts in order, JB of them in flight: a whole group is a part, a group
-        // that runs share is its units.
-        JoinRow<D> inner;
+        // JG groups at a time, their loads in flight together: a group that one run
+        // holds is one part, another is its units, folded on their own first
         const int step = wide ? JW : 1;
-        int g = wide ? warp : 0, k = -1, f = 0, e = 0;       // k >= 0: the next unit of a shared group
-        int64_t w = 0, w_past = 0, ua = 0;
-        bool in_slot0 = false;
-        auto next_part = [&](const float*& po, float2& h, int& kind) {
-          // kind 0: none left; 1: a group; 2: a unit; 3: the last unit of its group
-          if (k < 0) {
-            for (;; g += step) {
-              if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
-              if (g > glast) return kind = 0, void();
-              f = s.first(g), e = s.past(g);
-              if (f < e) break;
-            }
-            ua = u0 + f;
-            w = run_of(ua, units, workers);
-            w_past = run_start(w + 1, units, workers);
-            if (w_past >= u0 + e) {
-              const int64_t at = (entry * P.groups + g) * tile_rows + r;
-              h = P.group_ml[at];
-              po = P.group_o + at * D;
-              g += step;
-              return kind = 1, void();
-            }
-            k = f;
-            in_slot0 = run_start(w, units, workers) >= ua;
-          } else if (u0 + k >= w_past) {
-            ++w;
-            w_past = run_start(w + 1, units, workers);
-            in_slot0 = true;             // this run starts in the group
-          }
-          const int64_t at = (w * (2 * GROUP) + (in_slot0 ? 0 : GROUP) + s.unit(k) % GROUP) * tile_rows + r;
-          h = P.unit_ml[at];
-          po = P.unit_o + at * D;
-          kind = 2;
-          if (++k == e) {
-            k = -1;
-            g += step;
-            kind = 3;
-          }
-        };
-        for (;;) {
-          float2 h[JB];
-          float v[JB][E];
-          int kind[JB];
-          bool any = false;
+        int g = wide ? warp : 0;
+        while (g <= glast) {
+          float2 h[JG][GROUP];
+          float v[JG][GROUP][E];
+          int parts[JG];
+          bool whole[JG];
 #pragma unroll
-          for (int q = 0; q < JB; ++q) {
-            const float* po = nullptr;
-            next_part(po, h[q], kind[q]);
-            if (kind[q]) {
-              any = true;
+          for (int q = 0; q < JG; ++q) {
+            if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
+            const int f = g <= glast ? s.first(g) : 0, e = g <= glast ? s.past(g) : 0;
+            const uint32_t ua = u0 + f;
+            whole[q] = e > f && runs.of(ua) == runs.of(u0 + e - 1);
+            parts[q] = whole[q] ? 1 : e - f;
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k) {
+              if (k >= parts[q]) continue;
+              const uint32_t w = runs.of(ua + k);
+              const int64_t at = (whole[q] ? entry * P.groups + g
+                                           : static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) +
+                                                 s.unit(f + k) % GROUP) * tile_rows + r;
+              h[q][k] = (whole[q] ? P.group_ml : P.unit_ml)[at];
+              const float* po = (whole[q] ? P.group_o : P.unit_o) + at * D + lane * E;
               if constexpr (E == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(po + lane * E);
-                v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+                const float4 x = *reinterpret_cast<const float4*>(po);
+                v[q][k][0] = x.x, v[q][k][1] = x.y, v[q][k][2] = x.z, v[q][k][3] = x.w;
               } else {
-                const float2 x = *reinterpret_cast<const float2*>(po + lane * E);
-                v[q][0] = x.x, v[q][1] = x.y;
+                const float2 x = *reinterpret_cast<const float2*>(po);
+                v[q][k][0] = x.x, v[q][k][1] = x.y;
               }
             }
+            g += step;
           }
-          if (!any) break;
 #pragma unroll
-          for (int q = 0; q < JB; ++q) {
-            if (kind[q] == 1) acc.add(h[q].x, h[q].y, v[q]);
-            if (kind[q] >= 2) inner.add(h[q].x, h[q].y, v[q]);
-            if (kind[q] == 3) {
-              acc.add(inner.M, inner.L, inner.o);
-              inner = JoinRow<D>();
-            }
+          for (int q = 0; q < JG; ++q) {
+            JoinRow<D> inner;
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k)
+              if (k < parts[q]) inner.add(h[q][k].x, h[q][k].y, v[q][k]);
+            acc.add(inner.M, inner.L, inner.o);
           }
         }
       }
@@ -1020,7 +1063,7 @@ struct Layout {
 Layout layout_of(int64_t B, int64_t n, int64_t kv_heads, int64_t group, int64_t D, int64_t max_tokens) {
   const Tiling t = tiling_of(n, group);
   const int64_t entries = B * kv_heads * t.tiles, units = (max_tokens + UNIT - 1) / UNIT;
-  const int64_t unit_slots = (entries * units < workers_of(t.nt) ? entries * units : workers_of(t.nt)) * 2 * GROUP;
+  const int64_t unit_slots = (entries * units < WORKERS ? entries * units : WORKERS) * 2 * GROUP;
   Layout y{};
   y.groups = (units + GROUP - 1) / GROUP;
   const size_t ur = static_cast<size_t>(unit_slots) * t.nt * 8, gr = static_cast<size_t>(entries * y.groups) * t.nt * 8;
@@ -1052,7 +1095,7 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   static bool done[64] = {};
   rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, done);
   if (s != RLK_OK) return s;
-  attn_kernel<T, D, NT><<<P.workers, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
+  attn_kernel<T, D, NT><<<WORKERS, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them
@@ -1137,6 +1180,9 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
   const int group = q_heads / cache->kv_heads;
   const Tiling t = tiling_of(cache->n, group);
+  const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
+  if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
+    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 256 must be below 2^31");
   const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
                              static_cast<int64_t>(cache->max_pages) * cache->page_size);
   char* ws = static_cast<char*>(workspace);
@@ -1151,7 +1197,8 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.rows = t.rows;
   P.tiles = t.tiles;
   P.B = cache->B;
-  P.c2 = scale * 1.4426950408889634f;
+  P.c2 = fabsf(scale) * 1.4426950408889634f;
+  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
   P.window = window;
   P.sinks = window > 0 ? sinks : 0;
   P.lse = out_lse;
@@ -1163,7 +1210,7 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
                                        : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
   P.groups = static_cast<int>(y.groups);
-  P.workers = workers_of(t.nt);
+  P.page16 = cache->page_size % HALF == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == RLK_DT_BF16;
   if (cache->head_dim == 128)
