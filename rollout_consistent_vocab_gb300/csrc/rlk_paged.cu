@@ -175,9 +175,19 @@ struct Runs {
     more = workers ? units - len * workers : 0;
   }
   __device__ __forceinline__ uint32_t start(uint32_t k) const { return k * len + min(k, more); }
+};
+// ... and the run that a unit is in, by multiplication: u d for a 32-bit u and
+// d = ceil(2^64 / divisor) has the quotient in its upper 64 bits.
+struct RunOf : Runs {
+  unsigned long long inv, inv1;          // of len (0: len is 1) and of len + 1
+  __device__ __forceinline__ RunOf(uint32_t units, uint32_t most) : Runs(units, most) {
+    inv = len > 1 ? ~0ull / len + 1 : 0ull;
+    inv1 = ~0ull / (len + 1) + 1;        // len + 1 >= 2 where it is used
+  }
   __device__ __forceinline__ uint32_t of(uint32_t u) const {
     const uint32_t cut = more * (len + 1);
-    return u < cut ? u / (len + 1) : more + (u - cut) / len;
+    if (u < cut) return static_cast<uint32_t>(__umul64hi(u, inv1));
+    return more + (inv ? static_cast<uint32_t>(__umul64hi(u - cut, inv)) : u - cut);
   }
 };
 
@@ -865,13 +875,13 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 // ------------------------------------------------------------ the join
 
 constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
-constexpr int JG = 2;                    // groups in flight
+constexpr int JR = 2;                    // rows that a warp joins at once
 
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, each chain folds its groups in order, and the chains are
 // folded in order.  Up to 16 groups that is one fold over the groups, which a
-// single warp does.  The same CTA fills the rows without a query, and those of
-// rejected sequences.
+// single warp does; beyond, a CTA's 16 warps take a chain each.  The join also
+// fills the rows without a query, and those of rejected sequences.
 template <int D>
 struct JoinRow {
   static constexpr int E = D / 32;       // elements of a lane
@@ -882,109 +892,150 @@ struct JoinRow {
     for (int e = 0; e < E; ++e) o[e] = fold(o[e], v[e], f);
   }
 };
+template <int E>
+__device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
+  if constexpr (E == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x, v[1] = x.y;
+  }
+}
+
+// Rows [r, r + JR) of an entry (a sequence, kv head and tile).
+struct JoinItem {
+  Seq s;
+  int b, ht, r, glast;
+  bool direct, wide;
+};
 
 template <class T, int D>
-__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int block_rows, int64_t items) {
+__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int per_cta, int64_t items) {
   constexpr int E = D / 32;
-  __shared__ float2 chain_ml[JW];
-  __shared__ float chain_o[JW][D];
+  __shared__ float2 chain_ml[JW][JR];
+  __shared__ float chain_o[JW][JR][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HT = P.c.kv_heads * P.tiles;
-  const Runs runs(static_cast<uint32_t>(P.base[P.B] * HT), WORKERS);
-  const int blocks = (tile_rows + block_rows - 1) / block_rows;
-  const float nan = __int_as_float(0x7fc00000);
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int rb = static_cast<int>(it % blocks);
+  const RunOf runs(static_cast<uint32_t>(P.base[P.B] * HT), WORKERS);
+  const int blocks = (min(tile_rows, P.rows) + JR - 1) / JR;
+  auto item = [&](int64_t it) {
+    JoinItem x;
     const int64_t entry = it / blocks;
-    const int b = static_cast<int>(entry / HT), ht = static_cast<int>(entry - static_cast<int64_t>(b) * HT);
-    const Seq s = load_seq(P, b);
-    if (!s.ok && ht == 0 && rb == 0 && threadIdx.x == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
-    const uint32_t u0 = static_cast<uint32_t>(P.base[b] * HT) + static_cast<uint32_t>(ht) * s.nu;
-    const bool one_group = s.nu > 0 && s.first(glast) == 0;
-    const bool direct = one_group && runs.of(u0) == runs.of(u0 + s.nu - 1);
-    if (direct && s.nnew == P.c.n) continue;
-    const int tile0 = (ht % P.tiles) * tile_rows;
-    const bool wide = glast >= JW;       // more groups than chains: all warps on one row
-    const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;       // groups [0, gs) and [gl, glast]
-    for (int j = wide ? 0 : warp; j < block_rows; j += wide ? 1 : JW) {
-      const int r = rb * block_rows + j, row = tile0 + r, i = row / P.group;
-      if (r >= tile_rows || row >= P.rows) continue;
-      const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
-      const bool query = s.ok && i < s.nnew;
-      if (query && direct) continue;
-      JoinRow<D> acc;
-      if (query) {
-        // JG groups at a time, their loads in flight together: a group that one run
-        // holds is one part, another is its units, folded on their own first
-        const int step = wide ? JW : 1;
-        int g = wide ? warp : 0;
-        while (g <= glast) {
-          float2 h[JG][GROUP];
-          float v[JG][GROUP][E];
-          int parts[JG];
-          bool whole[JG];
+    x.r = static_cast<int>(it - entry * blocks) * JR;
+    x.b = static_cast<int>(entry / HT);
+    x.ht = static_cast<int>(entry - static_cast<int64_t>(x.b) * HT);
+    x.s = load_seq(P, x.b);
+    x.glast = x.s.nu > 0 ? x.s.unit(x.s.nu - 1) / GROUP : -1;
+    x.wide = x.glast >= JW;
+    const uint32_t u0 = static_cast<uint32_t>(P.base[x.b] * HT) + static_cast<uint32_t>(x.ht) * x.s.nu;
+    x.direct = x.s.nu > 0 && x.s.first(x.glast) == 0 && runs.of(u0) == runs.of(u0 + x.s.nu - 1);
+    return x;
+  };
+  // groups g0, g0 + step, ... into acc
+  auto gather = [&](const JoinItem& x, int g0, int step, JoinRow<D> (&acc)[JR]) {
+    const int64_t entry = static_cast<int64_t>(x.b) * HT + x.ht;
+    const uint32_t u0 = static_cast<uint32_t>(P.base[x.b] * HT) + static_cast<uint32_t>(x.ht) * x.s.nu;
+    const int gl = x.s.ul / GROUP, gs = (x.s.us + GROUP - 1) / GROUP;      // groups [0, gs) and [gl, glast]
+    for (int g = g0; g <= x.glast; g += step) {
+      if (g >= gs && g < gl) {
+        g += (gl - g + step - 1) / step * step;
+        if (g > x.glast) break;
+      }
+      const int f = x.s.first(g), e = x.s.past(g);
+      if (f >= e) continue;
+      const uint32_t ua = u0 + f, w0 = runs.of(ua);
+      // one part, where one run holds the group, or its units
+      const bool whole = runs.start(w0 + 1) >= u0 + e;
+      const int parts = whole ? 1 : e - f;
+      const float2* ml = whole ? P.group_ml : P.unit_ml;
+      const float* po = whole ? P.group_o : P.unit_o;
+      float2 h[GROUP][JR];
+      float v[GROUP][JR][E];
 #pragma unroll
-          for (int q = 0; q < JG; ++q) {
-            if (g >= gs && g < gl) g += (gl - g + step - 1) / step * step;
-            const int f = g <= glast ? s.first(g) : 0, e = g <= glast ? s.past(g) : 0;
-            const uint32_t ua = u0 + f;
-            whole[q] = e > f && runs.of(ua) == runs.of(u0 + e - 1);
-            parts[q] = whole[q] ? 1 : e - f;
+      for (int k = 0; k < GROUP; ++k) {
+        if (k >= parts) continue;
+        int64_t at = entry * P.groups + g;
+        if (!whole) {
+          const uint32_t w = runs.of(ua + k);
+          at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + x.s.unit(f + k) % GROUP;
+        }
+        at = at * tile_rows + x.r;
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k) {
-              if (k >= parts[q]) continue;
-              const uint32_t w = runs.of(ua + k);
-              const int64_t at = (whole[q] ? entry * P.groups + g
-                                           : static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) +
-                                                 s.unit(f + k) % GROUP) * tile_rows + r;
-              h[q][k] = (whole[q] ? P.group_ml : P.unit_ml)[at];
-              const float* po = (whole[q] ? P.group_o : P.unit_o) + at * D + lane * E;
-              if constexpr (E == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(po);
-                v[q][k][0] = x.x, v[q][k][1] = x.y, v[q][k][2] = x.z, v[q][k][3] = x.w;
-              } else {
-                const float2 x = *reinterpret_cast<const float2*>(po);
-                v[q][k][0] = x.x, v[q][k][1] = x.y;
-              }
-            }
-            g += step;
-          }
-#pragma unroll
-          for (int q = 0; q < JG; ++q) {
-            JoinRow<D> inner;
-#pragma unroll
-            for (int k = 0; k < GROUP; ++k)
-              if (k < parts[q]) inner.add(h[q][k].x, h[q][k].y, v[q][k]);
-            acc.add(inner.M, inner.L, inner.o);
-          }
+        for (int j = 0; j < JR; ++j) {
+          h[k][j] = ml[at + j];
+          load_row<E>(po + (at + j) * D + lane * E, v[k][j]);
         }
       }
-      if (query && wide) {
-        if (lane == 0) chain_ml[warp] = make_float2(acc.M, acc.L);
 #pragma unroll
-        for (int e = 0; e < E; ++e) chain_o[warp][lane * E + e] = acc.o[e];
-        __syncthreads();
-        if (warp == 0) {
-          acc = JoinRow<D>();
-          for (int c = 0; c < JW; ++c) {
-            float v[E];
+      for (int j = 0; j < JR; ++j) {
+        JoinRow<D> inner;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = chain_o[c][lane * E + e];
-            acc.add(chain_ml[c].x, chain_ml[c].y, v);
-          }
-        }
-        __syncthreads();
+        for (int k = 0; k < GROUP; ++k)
+          if (k < parts) inner.add(h[k][j].x, h[k][j].y, v[k][j]);
+        acc[j].add(inner.M, inner.L, inner.o);
       }
-      if (wide && warp != 0) continue;
-      T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
+    }
+  };
+  auto write = [&](const JoinItem& x, const JoinRow<D> (&acc)[JR]) {
+#pragma unroll
+    for (int j = 0; j < JR; ++j) {
+      const int row = (x.ht % P.tiles) * tile_rows + x.r + j, i = row / P.group;
+      if (row >= P.rows || (x.direct && i < x.s.nnew)) continue;
+      const int hq = (x.ht / P.tiles) * P.group + (row - i * P.group);
+      const bool query = i < x.s.nnew;
+      const float nan = __int_as_float(0x7fc00000);
+      T* op = static_cast<T*>(P.out) + x.b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        from_float(!s.ok ? nan : acc.L == 0.0f ? 0.0f : __fdiv_rn(acc.o[e], acc.L), op[e]);
+        from_float(!x.s.ok ? nan : !query || acc[j].L == 0.0f ? 0.0f : __fdiv_rn(acc[j].o[e], acc[j].L), op[e]);
       if (P.lse && lane == 0)
-        P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] = !s.ok ? nan : lse_of<T>(acc.M, acc.L);
+        P.lse[(static_cast<int64_t>(x.b) * P.c.n + i) * P.q_heads + hq] =
+            !x.s.ok ? nan : !query ? -INFINITY : lse_of<T>(acc[j].M, acc[j].L);
     }
+  };
+
+  // a CTA takes per_cta items: a warp each, and all warps together for the long ones
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta;
+  bool wide = false;
+  if (warp < per_cta && first + warp < items) {
+    const JoinItem x = item(first + warp);
+    wide = x.wide && !x.direct;
+    if (!x.s.ok && x.ht == 0 && x.r == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+    if (!wide && !(x.direct && x.s.nnew == P.c.n)) {
+      JoinRow<D> acc[JR];
+      if (!x.direct) gather(x, 0, 1, acc);
+      write(x, acc);
+    }
+  }
+  if (!__syncthreads_or(wide)) return;
+  for (int j = 0; j < per_cta && first + j < items; ++j) {
+    const JoinItem x = item(first + j);
+    if (!x.wide || x.direct) continue;   // the same in every warp
+    JoinRow<D> acc[JR];
+    gather(x, warp, JW, acc);
+#pragma unroll
+    for (int q = 0; q < JR; ++q) {
+      if (lane == 0) chain_ml[warp][q] = make_float2(acc[q].M, acc[q].L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) chain_o[warp][q][lane * E + e] = acc[q].o[e];
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int q = 0; q < JR; ++q) {
+        acc[q] = JoinRow<D>();
+        for (int c = 0; c < JW; ++c) {
+          float v[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = chain_o[c][q][lane * E + e];
+          acc[q].add(chain_ml[c][q].x, chain_ml[c][q].y, v);
+        }
+      }
+      write(x, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -1099,10 +1150,15 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them
-  const int block_rows = P.groups <= JW ? 8 : 1;
-  const int64_t items = P.B * P.c.kv_heads * P.tiles * ((NT * 8 + block_rows - 1) / block_rows);
+  const int tile_rows = NT * 8, blocks = ((tile_rows < P.rows ? tile_rows : P.rows) + JR - 1) / JR;
+  const int64_t items = P.B * P.c.kv_heads * P.tiles * blocks;
+  // few items: a CTA each, for the long ones; many: as many to a CTA as keep two rounds of CTAs
+  int64_t per_cta = (items + 2 * NUM_SMS - 1) / (2 * NUM_SMS);
+  per_cta = per_cta > JW ? JW : per_cta;
+  const int64_t ctas = (items + per_cta - 1) / per_cta;
+  if (ctas >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n * q_heads is too large for one call");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < NUM_SMS * 4 ? items : NUM_SMS * 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(JW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -1110,7 +1166,7 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, NT * 8, block_rows, items);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, tile_rows, static_cast<int>(per_cta), items);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
