@@ -111,7 +111,7 @@ struct Shape {
   static constexpr bool QS = D == 128 && NT == 4;            // queries in shared memory, not in registers
   static constexpr int SMEM = AW * (STAGES * STAGE + XCH) + (QS ? NT * (D / 16) * 32 * 8 : 0);
   static_assert(SLOTS % PASSES == 0 && SLOTS / PASSES % AW == 0, "every warp folds as many fragments in each pass");
-  static_assert(2 * (SMEM + AW * NT * 64 + 64 + 1024) <= 228 * 1024, "two CTAs in the shared memory of an SM");
+  static_assert(2 * (SMEM + (AW + 1) * NT * 64 + 64 + 1024) <= 228 * 1024, "two CTAs in the shared memory of an SM");
 };
 constexpr int WORKERS = NUM_SMS * 2;
 
@@ -135,6 +135,7 @@ struct AttnParams {
   float2* group_ml;             // [B * kv_heads * tiles * groups][8 NT]
   float* group_o;
   uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
+  uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
   int groups;                   // groups of the longest sequence that the table can hold
 };
 
@@ -191,6 +192,11 @@ struct RunOf : Runs {
   }
 };
 
+// The new token that a query row belongs to (row * group < 2^32: exact).
+__device__ __forceinline__ int query_of(const AttnParams& P, int row) {
+  return P.group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), P.group_magic)) : row;
+}
+
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -227,19 +233,11 @@ __device__ __forceinline__ void fold4(float4& x, const float4& part, Factors eve
   x.z = fold(x.z, part.z, even);
   x.w = fold(x.w, part.w, odd);
 }
-template <int NT>
-__device__ __forceinline__ Factors pick(const Factors (&f)[NT][2], int x, int e) {
-  Factors r = f[0][e];
-#pragma unroll
-  for (int i = 1; i < NT; ++i)
-    if (x == i) r = f[i][e];
-  return r;
-}
-
 template <class T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
   static constexpr float OFF = 0.0f, SLACK = 8.0f;
-  static constexpr uint32_t EXP = 0x7F807F80u;
+  static constexpr uint32_t EXP = 0x7F807F80u, ONE = 0x00800080u;
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   static constexpr float TINY = 9.094947017729282e-13f;      // 2^-40
   // The weights (a, b) >= 0 as the sum of two pairs of elements.  Both parts of a
   // weight above 0 are above 0 (hi is rounded down, lo raised to 2^-40 of the
@@ -259,7 +257,8 @@ template <> struct Elem<__nv_bfloat16> {
 // f16 holds weights in units of 2^-8, so that the smallest ones keep their bits
 template <> struct Elem<__half> {
   static constexpr float OFF = 8.0f, SLACK = 6.0f;
-  static constexpr uint32_t EXP = 0x7C007C00u;
+  static constexpr uint32_t EXP = 0x7C007C00u, ONE = 0x04000400u;
+  static __device__ __forceinline__ float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
   static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16: 2^-32 of the row's largest weight
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
@@ -283,6 +282,19 @@ __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t y;
@@ -344,8 +356,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   using E = Elem<T>;
   constexpr int KK = D / 16, DT = D / 16, SLOTS = S_::SLOTS, MINE = SLOTS / AW;
   extern __shared__ __align__(256) unsigned char smem_raw[];
-  __shared__ uint8_t bad_half[AW][8];
+  __shared__ uint8_t bad_slice[AW][4];
   __shared__ float2 share[AW][NT * 8];   // maximum and sum of each warp's share
+  __shared__ float2 group_ml[NT * 8];    // ... and of the group so far
   // until the runs are dealt out, the front of the rings holds the block sums
   int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [AW * 32], then the total
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -418,15 +431,25 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   // [slot of a fragment][warp][lane]: four floats of a warp's share
   float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE) + lane;
 
-  // ---- the producing side: this warp's halves into its ring, each looked up in the
-  // page table (lane j: token t0 + j mod 16) one half before it is copied
+  // ---- the producing side: this warp's slices into its ring by halves; a slice is
+  // looked up in the page table (lane j: token j) while the one before is worked on
   const T* const kbase = static_cast<const T*>(P.c.k);
   const T* const vbase = static_cast<const T*>(P.c.v);
   uint32_t issued = 0, consumed = 0;     // halves
-  int issue_stage = 0, use_stage = 0, half = 0, page = 0, place = 0;
-  bool seen = false;
-  auto look_up = [&]() {
-    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + half * HALF + (lane & (HALF - 1));
+  int issue_stage = 0, use_stage = 0, page = 0, place = 0;
+  bool seen = false, more = true;
+  constexpr int CH = D / 8;              // 16-byte pieces of a row
+  constexpr int RPI = 32 / CH;           // rows that one instruction of the warp copies
+  const int piece = lane % CH, crow = lane / CH;
+  auto seek = [&]() {
+    while (!seek_slice(P, prod)) {
+      if (!next_unit(P, prod)) {
+        more = false;
+        return;
+      }
+      prod.slice = warp;
+    }
+    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + lane;
     seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
     uint32_t p = __umulhi(static_cast<uint32_t>(t), P.page_magic);
     place = static_cast<int>(static_cast<uint32_t>(t) - p * static_cast<uint32_t>(P.c.page_size));
@@ -434,28 +457,19 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     if (place >= P.c.page_size) place -= P.c.page_size, ++p;
     page = seen ? __ldg(P.c.table + prod.b * P.c.table_stride + p) : 0;
   };
-  auto seek = [&]() {
-    while (!seek_slice(P, prod)) {
-      if (!next_unit(P, prod)) return false;
-      prod.slice = warp;
-    }
-    look_up();
-    return true;
-  };
-  bool more = seek();
-  constexpr int CH = D / 8;              // 16-byte pieces of a row
-  constexpr int RPI = 32 / CH;           // rows that one instruction of the warp copies
-  const int piece = lane % CH, crow = lane / CH;
   auto issue = [&]() {
+    const int half = issued & 1;
     const bool there = seen && page >= 0 && page < P.c.num_pages;
     const int64_t off = there ? page * P.c.page_stride + place * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride : 0;
-    const uint32_t there_mask = __ballot_sync(0xffffffffu, there);
-    const bool bad = __any_sync(0xffffffffu, seen && !there);
-    if (lane == 0) bad_half[warp][issue_stage] = bad;
+    const uint32_t there_mask = __ballot_sync(0xffffffffu, there) >> (half * HALF);
+    if (half == 0) {
+      const bool bad = __any_sync(0xffffffffu, seen && !there);
+      if (lane == 0) bad_slice[warp][(issued >> 1) & 3] = bad;
+    }
     const uint32_t dst = ring + issue_stage * S_::STAGE;
-    if (P.page16 && there_mask == 0xffffffffu) {
+    if (P.page16 && (there_mask & 0xFFFFu) == 0xFFFFu) {
       // 16 tokens of one page: rows a constant stride apart
-      const int64_t o = __shfl_sync(0xffffffffu, off, 0) + crow * P.c.token_stride + piece * 8;
+      const int64_t o = __shfl_sync(0xffffffffu, off, half * HALF) + crow * P.c.token_stride + piece * 8;
       const T* ks = kbase + o;
       const T* vs = vbase + o;
 #pragma unroll
@@ -468,10 +482,10 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         vs += RPI * P.c.token_stride;
       }
     } else {
-#pragma unroll
+#pragma unroll 2
       for (int j = 0; j < HALF / RPI; ++j) {
         const int rr = j * RPI + crow;
-        const int64_t o = __shfl_sync(0xffffffffu, off, rr) + piece * 8;
+        const int64_t o = __shfl_sync(0xffffffffu, off, half * HALF + rr) + piece * 8;
         const bool ok = (there_mask >> rr) & 1u;
         const uint32_t d = dst + rr * S_::ROWB + ((piece ^ (rr & 7)) * 16);
         copy16_if(d, kbase + o, ok);
@@ -481,14 +495,12 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     copy_commit();
     ++issued;
     if (++issue_stage == S_::STAGES) issue_stage = 0;
-    if ((half ^= 1) == 0) {
+    if (half) {
       prod.slice += AW;
-      more = seek();
-    } else {
-      look_up();
+      seek();
     }
   };
-  for (int i = 0; i < S_::STAGES && more; ++i) issue();
+  seek();
 
   // ---- the consuming side
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -497,13 +509,14 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * S_::ROWB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
   uint32_t qf[S_::QS ? 1 : NT][KK][2];
   uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + AW * (S_::STAGES * S_::STAGE + S_::XCH)) + lane;      // [NT][KK][lane]
-  float o[DT][NT][4], m[NT][2], l[NT][2], GM[NT][2], GL[NT][2];
+  float o[DT][NT][4], m[NT][2], l[NT][2];
   float4 gacc[MINE];
-  bool fresh_head = true, fresh_group = true, folding = false, head_part = false;
+  bool fresh_unit = true, fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false;
   uint32_t at = start;                   // the unit's number in the batch
   for (;;) {
-    const int u = cons.s.unit(cons.li);
-    const int tile0 = (cons.ht % P.tiles) * NT * 8;
+    while (more && issued - consumed < S_::STAGES) issue();
+    const int u = cons.s.unit(cons.li), g = u / GROUP;
+    const int tile0 = P.tiles == 1 ? 0 : (cons.ht % P.tiles) * NT * 8;
     if (fresh_head) {
       // the queries of this kv head and tile, as B operands
       const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + (cons.ht / P.tiles) * P.group * P.qs.head;
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       for (int x = 0; x < NT; ++x) {
         if (S_::QS && x != warp) continue;
         const int row = tile0 + x * 8 + g8;
-        const int i = row / P.group;
+        const int i = query_of(P, row);
         const bool real = row < P.rows && i < cons.s.nnew;
         const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
 #pragma unroll
@@ -525,38 +538,37 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       }
       if (S_::QS) __syncthreads();
       fresh_head = false;
-      fresh_group = true;
     }
-    const int g = u / GROUP;
-    if (fresh_group) {
+    if (fresh_unit && fresh_group) {
       const int f = cons.s.first(g), e = cons.s.past(g);
       folding = cons.li == f && e - cons.li <= cons.left;
       head_part = start >= at - (cons.li - f);
 #pragma unroll
-      for (int x = 0; x < NT; ++x) GM[x][0] = GM[x][1] = -INFINITY, GL[x][0] = GL[x][1] = 0.0f;
-#pragma unroll
       for (int j = 0; j < MINE; ++j) gacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      fresh_group = false;
     }
+    if (fresh_unit) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][x][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) o[d][x][e] = 0.0f;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
-    bool unit_bad = false;
+      for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
+      unit_bad = false;
+      fresh_unit = false;
+      cons.slice = warp;
+    }
 
-    for (cons.slice = warp; seek_slice(P, cons); cons.slice += AW) {
+    if (seek_slice(P, cons)) {
       // ---- one slice: its two halves have landed
       if (issued - consumed == S_::STAGES) copy_wait<S_::STAGES - 2>(); else copy_wait<0>();
       __syncwarp();
+      unit_bad |= bad_slice[warp][(consumed >> 1) & 3] != 0;
       uint32_t sk[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         sk[y] = ring + use_stage * S_::STAGE;
-        unit_bad |= bad_half[warp][use_stage] != 0;
         if (++use_stage == S_::STAGES) use_stage = 0;
       }
       const int t0 = u * UNIT + cons.slice * SL;
@@ -593,7 +605,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int pos = p0 + (tile0 + x * 8 + 2 * t4 + e) / P.group;
+            const int pos = p0 + query_of(P, tile0 + x * 8 + 2 * t4 + e);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -661,21 +673,48 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           l[x][e] += (s[0][x][e] + s[0][x][2 + e]) + (s[1][x][e] + s[1][x][2 + e]);
-      // values: a masked token's must not come in even as 0 * inf
-      uint32_t odd = 0;
+      // A masked token's value must not come in even as 0 * inf: where a masked slice
+      // holds values that are not finite, they go straight into the rows that see them
+      // (which they leave infinite or NaN), and zeros take their place.
       if (masked) {
+        bool odd = false;
+        const uint32_t vat = lane * 16;
+        for (int j = 0; j < 2 * HALF * S_::ROWB / 512; ++j) {
+          const uint32_t z = j * 512 + vat;
+          const uint4 w = lds128((z < HALF * S_::ROWB ? sk[0] : sk[1] - HALF * S_::ROWB) + HALF * S_::ROWB + z);
+          odd |= (((w.x & E::EXP) + E::ONE) | ((w.y & E::EXP) + E::ONE) | ((w.z & E::EXP) + E::ONE) | ((w.w & E::EXP) + E::ONE)) & 0x80008000u;
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          for (int r = 0; r < SL; ++r) {
+            const int t = t0 + r;
+            const uint32_t row = (r < HALF ? sk[0] : sk[1]) + HALF * S_::ROWB + (r & (HALF - 1)) * S_::ROWB;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            uint32_t a[4];
-            ldsm_t(a, (sk[y] + HALF * S_::ROWB + vlane) ^ (32 * d));
+              for (int f = 0; f < 2; ++f) {
+                const uint32_t cell = row + (((2 * d + f) ^ (r & 7)) * 16) + g8 * 2;
+                const uint32_t bits = lds16(cell);
+                if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              odd |= ((a[e] & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) | ((a[e] & E::EXP & 0xFFFF0000u) == (E::EXP & 0xFFFF0000u));
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int pos = p0 + query_of(P, tile0 + x * 8 + 2 * t4 + e);
+                    if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) o[d][x][2 * f + e] += E::value(bits);
+                  }
+              }
           }
+          __syncwarp();
+          for (int r = 0; r < SL; ++r) {
+            const uint32_t row = (r < HALF ? sk[0] : sk[1]) + HALF * S_::ROWB + (r & (HALF - 1)) * S_::ROWB;
+            for (int c = lane; c < D; c += 32) {
+              const uint32_t bits = lds16(row + c * 2);
+              if ((bits & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) sts16(row + c * 2, 0u);
+            }
+          }
+          __syncwarp();
+        }
       }
-      const bool careful = __any_sync(0xffffffffu, odd);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         uint32_t pf[NT][4];              // weights: tokens 0-7 and 8-15, then what the dtype dropped of them
@@ -687,53 +726,20 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
           for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
         }
         const uint32_t sv = sk[y] + HALF * S_::ROWB + vlane;
-        if (!careful) {
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            uint32_t a[4];
-            ldsm_t(a, sv ^ (32 * d));
+        for (int d = 0; d < DT; ++d) {
+          uint32_t a[4];
+          ldsm_t(a, sv ^ (32 * d));
 #pragma unroll
-            for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][2], pf[x][3]);
+          for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][2], pf[x][3]);
 #pragma unroll
-            for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][0], pf[x][1]);
-          }
-          continue;
-        }
-        // query by query, with zeros in the place of the values that it does not see:
-        // for its rows the same products as above, had those values been finite
-        const int i0 = tile0 / P.group, i1 = min(P.c.n - 1, (tile0 + NT * 8 - 1) / P.group);
-        for (int i = i0; i <= i1; ++i) {
-          const int pos = p0 + i;
-          uint32_t keep[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            keep[f] = 0u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = t0 + y * HALF + 8 * f + 2 * t4 + e;
-              if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) keep[f] |= 0xFFFFu << (16 * e);
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            uint32_t a[4];
-            ldsm_t(a, sv ^ (32 * d));
-            a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-              float v[4] = {o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]};
-              E::mma(v, a, pf[x][2], pf[x][3]);
-              E::mma(v, a, pf[x][0], pf[x][1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((tile0 + x * 8 + 2 * t4 + (e & 1)) / P.group == i) o[d][x][e] = v[e];
-            }
-          }
+          for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][0], pf[x][1]);
         }
       }
       consumed += 2;
       __syncwarp();                      // the stages may be filled again
-      while (more && issued - consumed < S_::STAGES) issue();
+      cons.slice += AW;
+      continue;
     }
 
     // ---- the unit's result: the warps' shares brought to one maximum and summed in order
@@ -752,6 +758,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       }
     if (unit_bad && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
     float UM[NT][2], UL[NT][2], wt[NT][2][AW];
+    float2 gml[NT][2];
     float4 uacc[MINE];
     constexpr int PER_PASS = MINE / S_::PASSES;
 #pragma unroll
@@ -759,7 +766,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       if (pass > 0) __syncthreads();
 #pragma unroll
       for (int f = 0; f < PER_PASS * AW; ++f) {
-        const int d = (pass * PER_PASS * AW + f) / NT, x = (pass * PER_PASS * AW + f) % NT;
+        const int x = (pass * PER_PASS * AW + f) / DT, d = (pass * PER_PASS * AW + f) % DT;
         xch[(f * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
       }
       __syncthreads();
@@ -781,23 +788,20 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
             }
             UM[x][e] = mx;
             UL[x][e] = sum;
+            gml[x][e] = fresh_group ? make_float2(-INFINITY, 0.0f) : group_ml[x * 8 + 2 * t4 + e];
           }
       }
 #pragma unroll
       for (int j = 0; j < PER_PASS; ++j) {
-        const int x = ((pass * PER_PASS + j) * AW + warp) % NT;
+        const int x = (pass * PER_PASS + j) * AW / DT;     // of fragments j AW .. j AW + 3
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < AW; ++w) {
           const float4 z = xch[((j * AW + warp) * AW + w) * 32];
-          float w0 = wt[0][0][w], w1 = wt[0][1][w];
-#pragma unroll
-          for (int i = 1; i < NT; ++i)
-            if (x == i) w0 = wt[i][0][w], w1 = wt[i][1][w];
-          v.x = __fmaf_rn(z.x, w0, v.x);
-          v.y = __fmaf_rn(z.y, w1, v.y);
-          v.z = __fmaf_rn(z.z, w0, v.z);
-          v.w = __fmaf_rn(z.w, w1, v.w);
+          v.x = __fmaf_rn(z.x, wt[x][0][w], v.x);
+          v.y = __fmaf_rn(z.y, wt[x][1][w], v.y);
+          v.z = __fmaf_rn(z.z, wt[x][0][w], v.z);
+          v.w = __fmaf_rn(z.w, wt[x][1][w], v.w);
         }
         uacc[pass * PER_PASS + j] = v;
       }
@@ -817,14 +821,14 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          f[x][e] = add_part(GM[x][e], GL[x][e], UM[x][e], UL[x][e]);
-          UM[x][e] = GM[x][e];
-          UL[x][e] = GL[x][e];
+          f[x][e] = add_part(gml[x][e].x, gml[x][e].y, UM[x][e], UL[x][e]);
+          UM[x][e] = gml[x][e].x;
+          UL[x][e] = gml[x][e].y;
+          if (warp == 0 && g8 == 0) group_ml[x * 8 + 2 * t4 + e] = gml[x][e];
         }
 #pragma unroll
       for (int j = 0; j < MINE; ++j) {
-        const int x = (j * AW + warp) % NT;
-        fold4(gacc[j], uacc[j], pick<NT>(f, x, 0), pick<NT>(f, x, 1));
+        fold4(gacc[j], uacc[j], f[j * AW / DT][0], f[j * AW / DT][1]);
         uacc[j] = gacc[j];
       }
       store = group_ends;
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = row / P.group;
+          const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = query_of(P, row);
           if (row >= P.rows || i >= cons.s.nnew) continue;
           const bool none = UL[x][e] == 0.0f;
           const int hq = kh * P.group + (row - i * P.group);
@@ -847,9 +851,8 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
           float* dst = po + (slot * (NT * 8) + r) * D + g8;
 #pragma unroll
           for (int j = 0; j < MINE; ++j) {
-            const int f = j * AW + warp;
-            if (f % NT != x) continue;
-            const int d = f / NT;
+            if (j * AW / DT != x) continue;
+            const int d = j * AW % DT + warp;
             const float lo = e ? uacc[j].y : uacc[j].x, hi = e ? uacc[j].w : uacc[j].z;
             if (direct) {
               from_float(none ? 0.0f : __fdiv_rn(lo, UL[x][e]), op[d * 16]);
@@ -865,8 +868,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
           }
         }
     }
-    fresh_group |= group_ends;
-    fresh_head |= head_ends;
+    fresh_unit = true;
+    fresh_group = group_ends;
+    fresh_head = head_ends;
     ++at;
     if (!next_unit(P, cons)) break;
   }
@@ -1266,6 +1270,7 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
                                        : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
   P.groups = static_cast<int>(y.groups);
+  P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
   P.page16 = cache->page_size % HALF == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == RLK_DT_BF16;
