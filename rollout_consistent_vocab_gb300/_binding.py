@@ -895,9 +895,9 @@ def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int,
     rows = n * (q_heads // kv_heads)
     tiles = -(-rows // 32)
     nt = -(-rows // (8 * tiles))
-    entries, units = B * kv_heads * tiles, -(-max_tokens // 256)
+    entries, units = B * kv_heads * tiles, -(-max_tokens // 512)
     parts = (min(entries * units, 304) * 8 + entries * -(-units // 4)) * nt * 8
-    return ((B + 1) * 8 + 15) // 16 * 16 + parts * (8 + head_dim * 4)
+    return parts * (8 + head_dim * 4)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, scale=None, window=0, sinks=0,

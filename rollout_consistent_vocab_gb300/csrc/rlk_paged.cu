@@ -75,21 +75,21 @@ __global__ void append_kernel(const AppendParams P) {
 
 // ------------------------------------------------------------ attention
 //
-// The tokens of a sequence go in units of 256, at fixed places.  A unit is one
+// The tokens of a sequence go in units of 512, at fixed places.  A unit is one
 // CTA's: its four warps take the unit's slices in turn, keys and values come
 // through each warp's own ring in shared memory (cp.async), S^T = K Q^T and
 // O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims) as
 // rows and 8 query rows as columns, with a running maximum and sum per query
 // row; then the warps' shares are folded in order.  What a row gets from a unit
 // therefore does not depend on the other rows, nor on anything outside the unit.
-// The units of a group (4 units, 1024 tokens, at fixed places too) are folded in
+// The units of a group (4 units, 2048 tokens, at fixed places too) are folded in
 // order; the groups of a sequence are joined in a fixed tree.  Who folds is
 // free: the units of the whole batch are dealt out in equal runs, and a run that
 // holds all of a group folds it itself, otherwise the units' results go to the
 // workspace and the join folds them, with the same arithmetic.  So no result
 // depends on the batch.
 
-constexpr int UNIT = 256;                // tokens of a unit
+constexpr int UNIT = 512;                // tokens of a unit
 constexpr int GROUP = 4;                 // units of a group
 constexpr int AW = 4;                    // warps of a CTA
 constexpr int NUM_SMS = 152;
@@ -129,8 +129,7 @@ struct AttnParams {
   bool page16;                  // 16 tokens from a multiple of 16 on lie in one page
   int window, sinks;
   float* lse;
-  int64_t* base;                // [B + 1] units of the sequences before, per kv head and tile
-  float2* unit_ml;              // [workers * 2 GROUP][8 NT]: maximum, sum
+  float2* unit_ml;              // [workers][2 GROUP][8 NT]: maximum, sum
   float* unit_o;                // ... and the weighted sum of values [D]
   float2* group_ml;             // [B * kv_heads * tiles * groups][8 NT]
   float* group_o;
@@ -192,6 +191,48 @@ struct RunOf : Runs {
   }
 };
 
+// Units (per kv head and tile) of the sequences before each block of sequences,
+// thread by thread, into scan[THREADS], and of them all; the whole CTA.
+template <int THREADS>
+__device__ __forceinline__ int seqs_per(const AttnParams& P) { return static_cast<int>((P.B + THREADS - 1) / THREADS); }
+template <int THREADS>
+__device__ __forceinline__ int64_t unit_sums(const AttnParams& P, int64_t* scan) {
+  const int tid = threadIdx.x, lane = tid & 31, per = seqs_per<THREADS>(P);
+  const int lo = static_cast<int>(min(P.B, static_cast<int64_t>(tid) * per));
+  const int hi = static_cast<int>(min(P.B, static_cast<int64_t>(lo) + per));
+  int64_t mine = 0;
+  for (int b = lo; b < hi; ++b) mine += load_seq(P, b).nu;
+  scan[tid] = mine;
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int N = THREADS / 32;
+    int64_t sum = 0;
+    for (int j = 0; j < N; ++j) sum += scan[lane * N + j];
+    int64_t run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (lane == 31) scan[THREADS] = run;
+    run -= sum;
+    for (int j = 0; j < N; ++j) {
+      const int64_t v = scan[lane * N + j];
+      scan[lane * N + j] = run;
+      run += v;
+    }
+  }
+  __syncthreads();
+  return scan[THREADS];
+}
+template <int THREADS>
+__device__ __forceinline__ int64_t units_before(const AttnParams& P, const int64_t* scan, int b) {
+  const int per = seqs_per<THREADS>(P), blk = b / per;
+  int64_t run = scan[blk];
+  for (int i = blk * per; i < b; ++i) run += load_seq(P, i).nu;
+  return run;
+}
+
 // The new token that a query row belongs to (row * group < 2^32: exact).
 __device__ __forceinline__ int query_of(const AttnParams& P, int row) {
   return P.group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), P.group_magic)) : row;
@@ -238,14 +279,16 @@ template <> struct Elem<__nv_bfloat16> {
   static constexpr float OFF = 0.0f, SLACK = 8.0f;
   static constexpr uint32_t EXP = 0x7F807F80u, ONE = 0x00800080u;
   static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
-  static constexpr float TINY = 9.094947017729282e-13f;      // 2^-40
-  // The weights (a, b) >= 0 as the sum of two pairs of elements.  Both parts of a
-  // weight above 0 are above 0 (hi is rounded down, lo raised to 2^-40 of the
-  // weight), so that an infinite value comes through as itself.
+  static constexpr float MORE = 1.0f + 2.384185791015625e-07f;   // 1 + 2^-22
+  // The weights (a, b) >= 0 as the sum of two pairs of elements: hi is cut off, lo
+  // is the rest and 2^-22 of the weight, a bias far below the result's own
+  // rounding.  So both parts of a weight above 0 are above 0, and an infinite value
+  // comes through as itself.
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-    const float x = __uint_as_float(hi << 16), y = __uint_as_float(hi & 0xFFFF0000u);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(fmaxf(a - x, a * TINY), fmaxf(b - y, b * TINY));
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    hi = __byte_perm(x, y, 0x7632);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(a, MORE, -__uint_as_float(x & 0xFFFF0000u)),
+                                                   __fmaf_rn(b, MORE, -__uint_as_float(y & 0xFFFF0000u)));
     lo = *reinterpret_cast<const uint32_t*>(&r);
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -364,40 +407,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- where this warp's run starts: units of the batch, by block of sequences
-  const int per = static_cast<int>((P.B + AW * 32 - 1) / (AW * 32));
-  const int b_lo = static_cast<int>(min(P.B, static_cast<int64_t>(tid) * per));
-  const int b_hi = static_cast<int>(min(P.B, static_cast<int64_t>(b_lo) + per));
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += load_seq(P, b).nu;
-  scan[tid] = mine;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t v[AW], sum = 0;
-#pragma unroll
-    for (int j = 0; j < AW; ++j) { v[j] = scan[lane * AW + j]; sum += v[j]; }
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int64_t run = incl - sum;
-#pragma unroll
-    for (int j = 0; j < AW; ++j) { scan[lane * AW + j] = run; run += v[j]; }
-    if (lane == 31) scan[AW * 32] = incl;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0) {
-    int64_t run = scan[tid];
-    for (int b = b_lo; b < b_hi; ++b) {
-      P.base[b] = run;
-      run += load_seq(P, b).nu;
-    }
-    if (tid == 0) P.base[P.B] = scan[AW * 32];
-  }
+  const int64_t total = unit_sums<AW * 32>(P, scan);
   const int HT = P.c.kv_heads * P.tiles;
-  const Runs runs(static_cast<uint32_t>(scan[AW * 32] * HT), WORKERS);
+  const Runs runs(static_cast<uint32_t>(total * HT), WORKERS);
   const uint32_t me = blockIdx.x;
   if (me >= runs.workers) return;        // every thread
   const uint32_t start = runs.start(me);
@@ -409,7 +421,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 #pragma unroll
     for (int j = 0; j < AW; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
     blk -= 1;
-    int b = blk * per;
+    int b = blk * seqs_per<AW * 32>(P);
     int64_t run = scan[blk];
     __syncthreads();                     // the rings are free
     Seq s = load_seq(P, b);
@@ -620,34 +632,44 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       }
       // each query row's reference m (the lanes of equal t4 share a row's tokens): it follows
       // the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
-      bool scaled = false;
-      float fac[NT][2];
+      float top[NT][2];
+      bool ahead = false;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(fmaxf(s[0][x][e], s[0][x][2 + e]), fmaxf(s[1][x][e], s[1][x][2 + e]));
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          mx *= P.c2;
-          fac[x][e] = 1.0f;
-          if (mx > m[x][e] + E::SLACK) {
-            if (m[x][e] != -INFINITY) {
-              fac[x][e] = ex2f(m[x][e] - mx);
-              scaled = true;
-            }
-            m[x][e] = mx;
-          }
+          top[x][e] = fmaxf(fmaxf(s[0][x][e], s[0][x][2 + e]), fmaxf(s[1][x][e], s[1][x][2 + e])) * P.c2;
+          ahead |= top[x][e] > m[x][e] + E::SLACK;
         }
-      if (__any_sync(0xffffffffu, scaled)) {
+      if (__any_sync(0xffffffffu, ahead)) {
+        bool scaled = false;
+        float fac[NT][2];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) l[x][0] *= fac[x][0], l[x][1] *= fac[x][1];
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+          for (int e = 0; e < 2; ++e) {
+            float mx = top[x][e];
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            fac[x][e] = 1.0f;
+            if (mx > m[x][e] + E::SLACK) {
+              if (m[x][e] != -INFINITY) {
+                fac[x][e] = ex2f(m[x][e] - mx);
+                scaled = true;
+              }
+              m[x][e] = mx;
+            }
+          }
+        if (__any_sync(0xffffffffu, scaled)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
+          for (int x = 0; x < NT; ++x) l[x][0] *= fac[x][0], l[x][1] *= fac[x][1];
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
+        }
       }
 #pragma unroll
       for (int x = 0; x < NT; ++x)
@@ -879,13 +901,13 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 // ------------------------------------------------------------ the join
 
 constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
-constexpr int JR = 2;                    // rows that a warp joins at once
+constexpr int JR = 4;                    // rows that a warp joins at once
 
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, each chain folds its groups in order, and the chains are
-// folded in order.  Up to 16 groups that is one fold over the groups, which a
-// single warp does; beyond, a CTA's 16 warps take a chain each.  The join also
-// fills the rows without a query, and those of rejected sequences.
+// folded in order.  A chain is a warp's; where the table has room for fewer
+// groups than 16, fewer warps work on a row, and a CTA on several.  The join
+// also fills the rows without a query, and those of rejected sequences.
 template <int D>
 struct JoinRow {
   static constexpr int E = D / 32;       // elements of a lane
@@ -907,51 +929,49 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
   }
 }
 
-// Rows [r, r + JR) of an entry (a sequence, kv head and tile).
-struct JoinItem {
-  Seq s;
-  int b, ht, r, glast;
-  bool direct, wide;
-};
-
 template <class T, int D>
-__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int per_cta, int64_t items) {
+__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
   constexpr int E = D / 32;
+  __shared__ int64_t scan[JW * 32 + 1];
   __shared__ float2 chain_ml[JW][JR];
   __shared__ float chain_o[JW][JR][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int HT = P.c.kv_heads * P.tiles;
-  const RunOf runs(static_cast<uint32_t>(P.base[P.B] * HT), WORKERS);
   const int blocks = (min(tile_rows, P.rows) + JR - 1) / JR;
-  auto item = [&](int64_t it) {
-    JoinItem x;
-    const int64_t entry = it / blocks;
-    x.r = static_cast<int>(it - entry * blocks) * JR;
-    x.b = static_cast<int>(entry / HT);
-    x.ht = static_cast<int>(entry - static_cast<int64_t>(x.b) * HT);
-    x.s = load_seq(P, x.b);
-    x.glast = x.s.nu > 0 ? x.s.unit(x.s.nu - 1) / GROUP : -1;
-    x.wide = x.glast >= JW;
-    const uint32_t u0 = static_cast<uint32_t>(P.base[x.b] * HT) + static_cast<uint32_t>(x.ht) * x.s.nu;
-    x.direct = x.s.nu > 0 && x.s.first(x.glast) == 0 && runs.of(u0) == runs.of(u0 + x.s.nu - 1);
-    return x;
-  };
-  // groups g0, g0 + step, ... into acc
-  auto gather = [&](const JoinItem& x, int g0, int step, JoinRow<D> (&acc)[JR]) {
-    const int64_t entry = static_cast<int64_t>(x.b) * HT + x.ht;
-    const uint32_t u0 = static_cast<uint32_t>(P.base[x.b] * HT) + static_cast<uint32_t>(x.ht) * x.s.nu;
-    const int gl = x.s.ul / GROUP, gs = (x.s.us + GROUP - 1) / GROUP;      // groups [0, gs) and [gl, glast]
-    for (int g = g0; g <= x.glast; g += step) {
+
+  // ---- before the units are done: where everything is.  An item is rows [r, r + JR) of
+  // an entry (a sequence, kv head and tile), and `width` warps'
+  const int64_t it = static_cast<int64_t>(blockIdx.x) * (JW / width) + warp / width;
+  const int w0 = warp % width;           // this warp's first chain
+  const bool mine = it < items;
+  const int64_t entry = mine ? it / blocks : 0;
+  const int r0 = static_cast<int>(it - entry * blocks) * JR;
+  const int b = static_cast<int>(entry / HT), ht = static_cast<int>(entry - static_cast<int64_t>(b) * HT);
+  const int64_t total = unit_sums<JW * 32>(P, scan);
+  const RunOf runs(static_cast<uint32_t>(total * HT), WORKERS);
+  const Seq s = load_seq(P, b);
+  const uint32_t u0 = static_cast<uint32_t>(units_before<JW * 32>(P, scan, b) * HT) + static_cast<uint32_t>(ht) * s.nu;
+  const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
+  const bool direct = s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
+  const bool work = mine && !(direct && s.nnew == P.c.n);
+  if (mine && !s.ok && ht == 0 && r0 == 0 && w0 == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!__syncthreads_or(work)) return;
+
+  // ---- this warp's chains: c, c + 16, ... each on its own; those from `width` on follow
+  const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
+  JoinRow<D> acc[JR];
+  if (work && !direct) {
+    for (int g = w0; g <= glast; g += JW) {
       if (g >= gs && g < gl) {
-        g += (gl - g + step - 1) / step * step;
-        if (g > x.glast) break;
+        g += (gl - g + JW - 1) / JW * JW;
+        if (g > glast) break;
       }
-      const int f = x.s.first(g), e = x.s.past(g);
+      const int f = s.first(g), e = s.past(g);
       if (f >= e) continue;
-      const uint32_t ua = u0 + f, w0 = runs.of(ua);
+      const uint32_t ua = u0 + f;
       // one part, where one run holds the group, or its units
-      const bool whole = runs.start(w0 + 1) >= u0 + e;
+      const bool whole = runs.start(runs.of(ua) + 1) >= u0 + e;
       const int parts = whole ? 1 : e - f;
       const float2* ml = whole ? P.group_ml : P.unit_ml;
       const float* po = whole ? P.group_o : P.unit_o;
@@ -963,9 +983,9 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
         int64_t at = entry * P.groups + g;
         if (!whole) {
           const uint32_t w = runs.of(ua + k);
-          at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + x.s.unit(f + k) % GROUP;
+          at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + s.unit(f + k) % GROUP;
         }
-        at = at * tile_rows + x.r;
+        at = at * tile_rows + r0;
 #pragma unroll
         for (int j = 0; j < JR; ++j) {
           h[k][j] = ml[at + j];
@@ -981,65 +1001,36 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
         acc[j].add(inner.M, inner.L, inner.o);
       }
     }
-  };
-  auto write = [&](const JoinItem& x, const JoinRow<D> (&acc)[JR]) {
-#pragma unroll
-    for (int j = 0; j < JR; ++j) {
-      const int row = (x.ht % P.tiles) * tile_rows + x.r + j, i = row / P.group;
-      if (row >= P.rows || (x.direct && i < x.s.nnew)) continue;
-      const int hq = (x.ht / P.tiles) * P.group + (row - i * P.group);
-      const bool query = i < x.s.nnew;
-      const float nan = __int_as_float(0x7fc00000);
-      T* op = static_cast<T*>(P.out) + x.b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        from_float(!x.s.ok ? nan : !query || acc[j].L == 0.0f ? 0.0f : __fdiv_rn(acc[j].o[e], acc[j].L), op[e]);
-      if (P.lse && lane == 0)
-        P.lse[(static_cast<int64_t>(x.b) * P.c.n + i) * P.q_heads + hq] =
-            !x.s.ok ? nan : !query ? -INFINITY : lse_of<T>(acc[j].M, acc[j].L);
-    }
-  };
-
-  // a CTA takes per_cta items: a warp each, and all warps together for the long ones
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta;
-  bool wide = false;
-  if (warp < per_cta && first + warp < items) {
-    const JoinItem x = item(first + warp);
-    wide = x.wide && !x.direct;
-    if (!x.s.ok && x.ht == 0 && x.r == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    if (!wide && !(x.direct && x.s.nnew == P.c.n)) {
-      JoinRow<D> acc[JR];
-      if (!x.direct) gather(x, 0, 1, acc);
-      write(x, acc);
-    }
   }
-  if (!__syncthreads_or(wide)) return;
-  for (int j = 0; j < per_cta && first + j < items; ++j) {
-    const JoinItem x = item(first + j);
-    if (!x.wide || x.direct) continue;   // the same in every warp
-    JoinRow<D> acc[JR];
-    gather(x, warp, JW, acc);
 #pragma unroll
-    for (int q = 0; q < JR; ++q) {
-      if (lane == 0) chain_ml[warp][q] = make_float2(acc[q].M, acc[q].L);
+  for (int j = 0; j < JR; ++j) {
+    if (lane == 0) chain_ml[warp][j] = make_float2(acc[j].M, acc[j].L);
 #pragma unroll
-      for (int e = 0; e < E; ++e) chain_o[warp][q][lane * E + e] = acc[q].o[e];
+    for (int e = 0; e < E; ++e) chain_o[warp][j][lane * E + e] = acc[j].o[e];
+  }
+  __syncthreads();
+  if (!work) return;
+  // ---- the chains in order, and the result: a row to a warp
+  for (int j = w0; j < JR; j += width) {
+    const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
+    if (row >= P.rows || (direct && i < s.nnew)) continue;
+    JoinRow<D> all;
+    for (int c = 0; c < width; ++c) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = chain_o[warp - w0 + c][j][lane * E + e];
+      all.add(chain_ml[warp - w0 + c][j].x, chain_ml[warp - w0 + c][j].y, v);
     }
-    __syncthreads();
-    if (warp == 0) {
+    const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
+    const bool query = i < s.nnew;
+    const float nan = __int_as_float(0x7fc00000);
+    T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
 #pragma unroll
-      for (int q = 0; q < JR; ++q) {
-        acc[q] = JoinRow<D>();
-        for (int c = 0; c < JW; ++c) {
-          float v[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] = chain_o[c][q][lane * E + e];
-          acc[q].add(chain_ml[c][q].x, chain_ml[c][q].y, v);
-        }
-      }
-      write(x, acc);
-    }
-    __syncthreads();
+    for (int e = 0; e < E; ++e)
+      from_float(!s.ok ? nan : !query || all.L == 0.0f ? 0.0f : __fdiv_rn(all.o[e], all.L), op[e]);
+    if (P.lse && lane == 0)
+      P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] =
+          !s.ok ? nan : !query ? -INFINITY : lse_of<T>(all.M, all.L);
   }
 }
 
@@ -1109,10 +1100,10 @@ Tiling tiling_of(int64_t n, int64_t group) {
   return {static_cast<int>(rows), static_cast<int>(tiles), static_cast<int>((rows + 8 * tiles - 1) / (8 * tiles))};
 }
 
-// The workspace, in this order: units of the sequences before (int64 [B + 1]),
-// maxima and sums of units and of groups, their weighted sums.
+// The workspace, in this order: maxima and sums of units and of groups, their
+// weighted sums.
 struct Layout {
-  size_t base, unit_ml, group_ml, unit_o, group_o, bytes;
+  size_t unit_ml, group_ml, unit_o, group_o, bytes;
   int64_t groups;
 };
 Layout layout_of(int64_t B, int64_t n, int64_t kv_heads, int64_t group, int64_t D, int64_t max_tokens) {
@@ -1122,8 +1113,7 @@ Layout layout_of(int64_t B, int64_t n, int64_t kv_heads, int64_t group, int64_t 
   Layout y{};
   y.groups = (units + GROUP - 1) / GROUP;
   const size_t ur = static_cast<size_t>(unit_slots) * t.nt * 8, gr = static_cast<size_t>(entries * y.groups) * t.nt * 8;
-  y.base = 0;
-  y.unit_ml = (static_cast<size_t>(B + 1) * 8 + 15) / 16 * 16;
+  y.unit_ml = 0;
   y.group_ml = y.unit_ml + ur * 8;
   y.unit_o = y.group_ml + gr * 8;
   y.group_o = y.unit_o + ur * D * 4;
@@ -1156,10 +1146,9 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   // the join is launched while the units are at work, and waits for them
   const int tile_rows = NT * 8, blocks = ((tile_rows < P.rows ? tile_rows : P.rows) + JR - 1) / JR;
   const int64_t items = P.B * P.c.kv_heads * P.tiles * blocks;
-  // few items: a CTA each, for the long ones; many: as many to a CTA as keep two rounds of CTAs
-  int64_t per_cta = (items + 2 * NUM_SMS - 1) / (2 * NUM_SMS);
-  per_cta = per_cta > JW ? JW : per_cta;
-  const int64_t ctas = (items + per_cta - 1) / per_cta;
+  int width = 1;
+  while (width < JW && width < P.groups) width *= 2;
+  const int64_t ctas = (items * width + JW - 1) / JW;
   if (ctas >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n * q_heads is too large for one call");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -1170,7 +1159,7 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, tile_rows, static_cast<int>(per_cta), items);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, tile_rows, width, items);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
@@ -1242,7 +1231,7 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   const Tiling t = tiling_of(cache->n, group);
   const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
   if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
-    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 256 must be below 2^31");
+    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
   const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
                              static_cast<int64_t>(cache->max_pages) * cache->page_size);
   char* ws = static_cast<char*>(workspace);
@@ -1262,7 +1251,6 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   P.window = window;
   P.sinks = window > 0 ? sinks : 0;
   P.lse = out_lse;
-  P.base = reinterpret_cast<int64_t*>(ws + y.base);
   P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
   P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
   P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
