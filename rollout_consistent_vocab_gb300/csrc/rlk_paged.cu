@@ -901,13 +901,14 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 // ------------------------------------------------------------ the join
 
 constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
-constexpr int JR = 4;                    // rows that a warp joins at once
+constexpr int JB = 4;                    // chains of a block
+constexpr int JR = 2;                    // rows that a warp joins at once
 
 // A row of a sequence whose groups are not all in one run: group g goes to
-// chain g mod 16, each chain folds its groups in order, and the chains are
-// folded in order.  A chain is a warp's; where the table has room for fewer
-// groups than 16, fewer warps work on a row, and a CTA on several.  The join
-// also fills the rows without a query, and those of rejected sequences.
+// chain g mod 16, a chain folds its groups in order, a block its four chains,
+// and the row its four blocks.  By how many rows there are, a chain, a block or
+// a row is a warp's; it is the same tree.  The join also fills the rows without
+// a query, and those of rejected sequences.
 template <int D>
 struct JoinRow {
   static constexpr int E = D / 32;       // elements of a lane
@@ -917,6 +918,7 @@ struct JoinRow {
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fold(o[e], v[e], f);
   }
+  __device__ __forceinline__ void add(const JoinRow& r) { add(r.M, r.L, r.o); }
 };
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
@@ -943,6 +945,7 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
   // an entry (a sequence, kv head and tile), and `width` warps'
   const int64_t it = static_cast<int64_t>(blockIdx.x) * (JW / width) + warp / width;
   const int w0 = warp % width;           // this warp's first chain
+  const bool chainwise = P.groups <= width || width == JW;
   const bool mine = it < items;
   const int64_t entry = mine ? it / blocks : 0;
   const int r0 = static_cast<int>(it - entry * blocks) * JR;
@@ -958,47 +961,64 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!__syncthreads_or(work)) return;
 
-  // ---- this warp's chains: c, c + 16, ... each on its own; those from `width` on follow
+  // ---- this warp's chains, in order
   const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
-  JoinRow<D> acc[JR];
+  JoinRow<D> acc[JR], blk[JR];
   if (work && !direct) {
-    for (int g = w0; g <= glast; g += JW) {
-      if (g >= gs && g < gl) {
-        g += (gl - g + JW - 1) / JW * JW;
-        if (g > glast) break;
-      }
-      const int f = s.first(g), e = s.past(g);
-      if (f >= e) continue;
-      const uint32_t ua = u0 + f;
-      // one part, where one run holds the group, or its units
-      const bool whole = runs.start(runs.of(ua) + 1) >= u0 + e;
-      const int parts = whole ? 1 : e - f;
-      const float2* ml = whole ? P.group_ml : P.unit_ml;
-      const float* po = whole ? P.group_o : P.unit_o;
-      float2 h[GROUP][JR];
-      float v[GROUP][JR][E];
-#pragma unroll
-      for (int k = 0; k < GROUP; ++k) {
-        if (k >= parts) continue;
-        int64_t at = entry * P.groups + g;
-        if (!whole) {
-          const uint32_t w = runs.of(ua + k);
-          at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + s.unit(f + k) % GROUP;
+    const int chains = chainwise ? 1 : JW / width;
+    for (int c = w0 * chains; c < (w0 + 1) * chains && c <= glast; ++c) {     // (chainwise: chain w0)
+      JoinRow<D> chain[JR];
+      for (int g = c; g <= glast; g += JW) {
+        if (g >= gs && g < gl) {
+          g += (gl - g + JW - 1) / JW * JW;
+          if (g > glast) break;
         }
-        at = at * tile_rows + r0;
+        const int f = s.first(g), e = s.past(g);
+        if (f >= e) continue;
+        const uint32_t ua = u0 + f;
+        // one part, where one run holds the group, or its units
+        const bool whole = runs.start(runs.of(ua) + 1) >= u0 + e;
+        const int parts = whole ? 1 : e - f;
+        const float2* ml = whole ? P.group_ml : P.unit_ml;
+        const float* po = whole ? P.group_o : P.unit_o;
+        float2 h[GROUP][JR];
+        float v[GROUP][JR][E];
 #pragma unroll
-        for (int j = 0; j < JR; ++j) {
-          h[k][j] = ml[at + j];
-          load_row<E>(po + (at + j) * D + lane * E, v[k][j]);
+        for (int k = 0; k < GROUP; ++k) {
+          int64_t at = entry * P.groups + g;
+          if (!whole) {
+            const uint32_t w = runs.of(min(ua + k, u0 + e - 1));
+            at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + s.unit(min(f + k, e - 1)) % GROUP;
+          }
+          at = at * tile_rows + r0;
+          // (past the last part: its place again)
+#pragma unroll
+          for (int j = 0; j < JR; ++j) {
+            h[k][j] = ml[at + j];
+            load_row<E>(po + (at + j) * D + lane * E, v[k][j]);
+          }
         }
+        JoinRow<D> inner[JR];
+#pragma unroll
+        for (int k = 0; k < GROUP; ++k)
+          if (k < parts) {
+#pragma unroll
+            for (int j = 0; j < JR; ++j) inner[j].add(h[k][j].x, h[k][j].y, v[k][j]);
+          }
+#pragma unroll
+        for (int j = 0; j < JR; ++j) chain[j].add(inner[j]);
       }
 #pragma unroll
       for (int j = 0; j < JR; ++j) {
-        JoinRow<D> inner;
-#pragma unroll
-        for (int k = 0; k < GROUP; ++k)
-          if (k < parts) inner.add(h[k][j].x, h[k][j].y, v[k][j]);
-        acc[j].add(inner.M, inner.L, inner.o);
+        if (chainwise) {
+          acc[j] = chain[j];
+        } else {
+          blk[j].add(chain[j]);
+          if (c % JB == JB - 1 || c == glast) {
+            acc[j].add(blk[j]);
+            blk[j] = JoinRow<D>();
+          }
+        }
       }
     }
   }
@@ -1010,16 +1030,25 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
   }
   __syncthreads();
   if (!work) return;
-  // ---- the chains in order, and the result: a row to a warp
+  // ---- the item's warps in order, and the result: a row to a warp
   for (int j = w0; j < JR; j += width) {
     const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
     if (row >= P.rows || (direct && i < s.nnew)) continue;
-    JoinRow<D> all;
+    JoinRow<D> all, part;
     for (int c = 0; c < width; ++c) {
       float v[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = chain_o[warp - w0 + c][j][lane * E + e];
-      all.add(chain_ml[warp - w0 + c][j].x, chain_ml[warp - w0 + c][j].y, v);
+      const float2 h = chain_ml[warp - w0 + c][j];
+      if (!chainwise) {
+        all.add(h.x, h.y, v);
+        continue;
+      }
+      part.add(h.x, h.y, v);
+      if (c % JB == JB - 1 || c == width - 1) {
+        all.add(part);
+        part = JoinRow<D>();
+      }
     }
     const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
     const bool query = i < s.nnew;
@@ -1146,8 +1175,10 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   // the join is launched while the units are at work, and waits for them
   const int tile_rows = NT * 8, blocks = ((tile_rows < P.rows ? tile_rows : P.rows) + JR - 1) / JR;
   const int64_t items = P.B * P.c.kv_heads * P.tiles * blocks;
+  // a chain to a warp, as far as one round of CTAs (one per SM) has the warps
   int width = 1;
   while (width < JW && width < P.groups) width *= 2;
+  if (items * width > NUM_SMS * JW) width = width > JB && items * JB <= NUM_SMS * JW ? JB : 1;
   const int64_t ctas = (items * width + JW - 1) / JW;
   if (ctas >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n * q_heads is too large for one call");
   cudaLaunchConfig_t cfg{};
