@@ -213,6 +213,7 @@ logp_kernel(const KParams P) {
   int64_t seq = row;                    // what the parameter arrays go by
   int t_ver = 0;
   if constexpr (VERIFY) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the draw's CTAs may line up
     const int64_t nt = P.ver.B * (P.ver.n + 1);
     is_draft = cid >= nt;
     row = is_draft ? cid - nt : cid;

@@ -23,9 +23,10 @@
 
 namespace rlk {
 
-constexpr int VT = 512;                                   // threads of a draw CTA
+constexpr int VT = 128;                                   // threads of a draw CTA
 constexpr int VW = VT / 32;
-constexpr int VPER = (SAMP_BITWORDS + VW - 1) / VW;       // bitmap words per warp
+constexpr int ROUNDS = (SHARD_CHUNKS + VT - 1) / VT;      // of a chunk to a thread, at most
+static_assert(SAMP_BITWORDS <= VT, "a bitmap word to a thread");
 
 struct DrawParams {
   VerifyPass ver;
@@ -89,11 +90,32 @@ __device__ __forceinline__ unsigned long long chunk_masses(const Masses& m, uint
   return sum;
 }
 
+// Sums over the CTA in thread order: this thread's exclusive prefix, and the total.
+__device__ __forceinline__ unsigned long long cta_scan(unsigned long long v, unsigned long long (&part)[VW],
+                                                       unsigned long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned long long incl = warp_incl_scan_u64(v);
+  __syncthreads();                     // the parts of an earlier scan have been read
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  unsigned long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < VW; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  return before + incl - v;
+}
+
 __global__ void __cluster_dims__(NSHARD, 1, 1) __launch_bounds__(VT)
 verify_draw_kernel(const DrawParams P) {
-  __shared__ unsigned long long warp_mass[VW];
+  __shared__ unsigned long long part[VW];
+  __shared__ unsigned long long round_mass[ROUNDS];
   __shared__ unsigned long long shard_mass[2][NSHARD];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint16_t list[SHARD_CHUNKS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31;
   const int r = static_cast<int>(cluster_rank());
   const int64_t b = blockIdx.x / NSHARD;
   const int n = P.ver.n;
@@ -154,26 +176,23 @@ verify_draw_kernel(const DrawParams P) {
   }
   cluster_arrive_relaxed();            // met before the first store into a peer: every CTA is running
 
-  // ---- this warp's chunks, of both rows
+  // ---- the chunks that hold the support, in column order: those that the pass marked,
+  // or all of the shard's
   const uint4* rowp = reinterpret_cast<const uint4*>(P.logits + slot * P.stride) + r * SHARD_CHUNKS;
   const bool with_y = residual && recq;
   const uint4* rowq = with_y ? reinterpret_cast<const uint4*>(P.draft + (b * n + a) * P.draft_stride) + r * SHARD_CHUNKS
                              : nullptr;
-  const int nchunks = r == NSHARD - 1 ? LAST_CHUNKS : SHARD_CHUNKS;
-  uint4 x[VPER], y[VPER];
-  uint32_t have = 0;
-#pragma unroll
-  for (int i = 0; i < VPER; ++i) {
-    const int w = warp * VPER + i, g = w * 32 + lane;
-    bool marked = w < SAMP_BITWORDS && g < nchunks;
-    if (marked && (rr.flags & SAMP_BITS)) marked = (P.bits[(slot * NSHARD + r) * SAMP_BITWORDS + w] >> lane) & 1u;
-    x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (marked) {
-      have |= 1u << i;
-      x[i] = __ldg(rowp + g);
-      if (with_y) y[i] = __ldg(rowq + g);
-    }
+  int chunks = r == NSHARD - 1 ? LAST_CHUNKS : SHARD_CHUNKS;
+  const bool marked = (rr.flags & SAMP_BITS) != 0;
+  if (marked) {
+    uint32_t word = tid < SAMP_BITWORDS ? P.bits[(slot * NSHARD + r) * SAMP_BITWORDS + tid] : 0u;
+    unsigned long long total;
+    int at = static_cast<int>(cta_scan(static_cast<unsigned long long>(__popc(word)), part, total));
+    chunks = static_cast<int>(total);
+    for (; word; word &= word - 1) list[at++] = static_cast<uint16_t>(tid * 32 + __ffs(word) - 1);
   }
+  for (int i = tid; i < ROUNDS; i += VT) round_mass[i] = 0ull;
+  __syncthreads();
   Masses m{};
   const float tau = P.tau_arr ? P.tau_arr[b] : P.tau_s;
   m.M = rr.M;
@@ -198,34 +217,34 @@ verify_draw_kernel(const DrawParams P) {
     }
   }
 
-  // ---- masses; where a residual has none anywhere, once more for p itself
-  unsigned long long mc[VPER], mine = 0, prefix = 0, total = 0;
-  for (int round = 0; round < 2; ++round) {
-    mine = 0;
-#pragma unroll
-    for (int i = 0; i < VPER; ++i) {
+  // ---- masses, a chunk to a thread in each round; where a residual has none anywhere,
+  // once more for p itself
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  unsigned long long prefix = 0, total = 0, mine = 0;
+  for (int turn = 0; turn < 2; ++turn) {
+    unsigned long long sum = 0;
+#pragma unroll 4
+    for (int c = tid; c < chunks; c += VT) {
+      const int g = marked ? list[c] : c;
+      const uint4 x = __ldg(rowp + g), y = m.with_q ? __ldg(rowq + g) : none;
       unsigned long long e[8];
-      mc[i] = (have >> i) & 1u ? chunk_masses(m, x[i], y[i], r * SW + ((warp * VPER + i) * 32 + lane) * 8, e) : 0ull;
-      mine += mc[i];
+      const unsigned long long v = chunk_masses(m, x, y, r * SW + g * 8, e);
+      if (v) atomicAdd(&round_mass[c / VT], v);            // integers: any order
+      sum += v;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) warp_mass[warp] = mine;
-    __syncthreads();
-    if (round == 0) cluster_wait();
+    cta_scan(sum, part, mine);
+    if (turn == 0) cluster_wait();
     if (tid < NSHARD) {
-      unsigned long long s = 0;
-      for (int w = 0; w < VW; ++w) s += warp_mass[w];
-      const uint32_t dst = map_rank(smem_addr(&shard_mass[round][r]), tid);
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(s) : "memory");
+      const uint32_t dst = map_rank(smem_addr(&shard_mass[turn][r]), tid);
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(mine) : "memory");
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     cluster_wait();
     prefix = total = 0;
 #pragma unroll
     for (int q = 0; q < NSHARD; ++q) {
-      if (q < r) prefix += shard_mass[round][q];
-      total += shard_mass[round][q];
+      if (q < r) prefix += shard_mass[turn][q];
+      total += shard_mass[turn][q];
     }
     if (total != 0) break;             // the same in every CTA
     m.with_q = false;
@@ -236,47 +255,43 @@ verify_draw_kernel(const DrawParams P) {
     return;
   }
 
-  // ---- the shard, the warp, the word, the chunk and the column that hold the draw
+  // ---- the shard, the round, the chunk and the column that hold the draw
   const unsigned long long t = scale_draw(P.draw[b], total);
-  unsigned long long before = prefix;
-  for (int w = 0; w < warp; ++w) before += warp_mass[w];
-  if (t < before || t - before >= mine) return;      // uniform over the warp
-  unsigned long long left = t - before;
+  if (t < prefix || t - prefix >= mine) return;      // another CTA's
+  unsigned long long left = t - prefix;
+  int round = 0;
+  while (left >= round_mass[round]) left -= round_mass[round++];
+  const int c = round * VT + tid;
+  const bool here = c < chunks;
+  const int g = here ? (marked ? list[c] : c) : 0;
+  unsigned long long e[8], mass = 0, all;
+  uint4 x = none;
+  if (here) {
+    x = __ldg(rowp + g);
+    mass = chunk_masses(m, x, m.with_q ? __ldg(rowq + g) : none, r * SW + g * 8, e);
+  }
+  const unsigned long long ex = cta_scan(mass, part, all);
+  if (!here || left < ex || left - ex >= mass) return;
+  left -= ex;
+  const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+  int jstar = -1;
+  float xa = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VPER; ++i) {
-    const unsigned long long incl = warp_incl_scan_u64(mc[i]);
-    const unsigned long long word = __shfl_sync(0xffffffffu, incl, 31);
-    if (left >= word) {
-      left -= word;
-      continue;
-    }
-    const unsigned long long ex = incl - mc[i];
-    if (left < ex || left - ex >= mc[i]) return;     // another lane's chunk
-    left -= ex;
-    unsigned long long e[8];
-    const int col0 = r * SW + ((warp * VPER + i) * 32 + lane) * 8;
-    chunk_masses(m, x[i], y[i], col0, e);
-    const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    int jstar = -1;
-    float xa = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (jstar < 0) {
-        if (left < e[j]) {
-          jstar = j;
-          xa = (j & 1) ? bf16_hi(w4[j >> 1]) : bf16_lo(w4[j >> 1]);
-        } else {
-          left -= e[j];
-        }
+  for (int j = 0; j < 8; ++j) {
+    if (jstar < 0) {
+      if (left < e[j]) {
+        jstar = j;
+        xa = (j & 1) ? bf16_hi(w4[j >> 1]) : bf16_lo(w4[j >> 1]);
+      } else {
+        left -= e[j];
       }
     }
-    const float d = __fdiv_rn(xa - rr.M, tau);
-    const float full = d - logf(rr.Z);
-    P.out_token[slot] = col0 + jstar;
-    if (P.out_full) P.out_full[slot] = full;
-    if (P.out_restr) P.out_restr[slot] = (rr.flags & SAMP_SEL) ? d - logf(rr.zs) : full;
-    return;
   }
+  const float d = __fdiv_rn(xa - rr.M, tau);
+  const float full = d - logf(rr.Z);
+  P.out_token[slot] = r * SW + g * 8 + jstar;
+  if (P.out_full) P.out_full[slot] = full;
+  if (P.out_restr) P.out_restr[slot] = (rr.flags & SAMP_SEL) ? d - logf(rr.zs) : full;
 }
 
 }  // namespace rlk
@@ -353,8 +368,17 @@ extern "C" rlk_status rlk_verify_drafts(const rlk_verify_args* a, int32_t* out_t
   P.out_restr = out_restr;
   P.out_full = out_full;
   P.err = a->err_count;
-  verify_draw_kernel<<<static_cast<unsigned>(a->B * NSHARD), VT, 0, static_cast<cudaStream_t>(stream)>>>(P);
-  const cudaError_t e = cudaGetLastError();
+  // launched while the pass's last rows are at work, and waits for them
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a->B * NSHARD));
+  cfg.blockDim = dim3(VT);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_draw_kernel, P);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
