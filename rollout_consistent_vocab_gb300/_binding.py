@@ -248,9 +248,13 @@ def make_args(logits, target, temperature=1.0, top_p=1.0, top_k=-1, err_count=No
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the same handle, without building a Stream
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
 def _empty(T, dtype, like):
@@ -825,18 +829,9 @@ def grad_norm(tensors, *, distributed=False, group=None, bins=None, out=None, st
 
 # ----------------------------------------------------------------- paged key-value cache
 
-def _cache_dtype(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return RLK_DT_BF16
-    if t.dtype == torch.float16:
-        return RLK_DT_F16
-    raise ValueError(f"the cache's dtype {t.dtype} must be bfloat16 or float16")
-
-
 def _bth(t, shape, dtype, name) -> BTHStrides:
     """Strides of a [B, n, heads, head_dim] tensor with unit stride in the last place."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)}")
     sb, st, sh, sd = t.stride()
     if sd != 1:
@@ -847,25 +842,36 @@ def _bth(t, shape, dtype, name) -> BTHStrides:
 
 def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> KVCache:
     torch = _torch()
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim] tensors of one dtype")
-    strides = k_cache.stride()
     if strides[3] != 1 or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same strides, 1 in the last place")
     if not (k_cache.is_cuda and v_cache.is_cuda):
         raise ValueError("k_cache and v_cache must live on the GPU")
+    if dtype == torch.bfloat16:
+        code = RLK_DT_BF16
+    elif dtype == torch.float16:
+        code = RLK_DT_F16
+    else:
+        raise ValueError(f"the cache's dtype {dtype} must be bfloat16 or float16")
+    i32 = torch.int32
+    if lens.dtype != i32 or lens.dim() != 1 or not lens.is_contiguous() or not lens.is_cuda:
+        raise ValueError("lens must be a contiguous int32 CUDA tensor of shape [B]")
     B = lens.shape[0]
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
-            or not page_table.is_cuda or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    if page_table.dtype != i32 or page_table.dim() != 2 or page_table.shape[0] != B or not page_table.is_cuda:
         raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
-    for t, name in ((lens, "lens"), (new_lens, "new_lens")):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda):
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape [{B}]")
-    pages, page_size, heads, dim = k_cache.shape
     width = page_table.shape[1]
+    row, col = page_table.stride()
+    if width > 1 and col != 1:
+        raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
+    if new_lens is not None and (new_lens.dtype != i32 or new_lens.shape != (B,) or not new_lens.is_contiguous()
+                                 or not new_lens.is_cuda):
+        raise ValueError(f"new_lens must be a contiguous int32 CUDA tensor of shape [{B}]")
+    pages, page_size, heads, dim = shape
     return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, strides[0] if pages > 1 else 0,
                    strides[1] if page_size > 1 else 0, strides[2] if heads > 1 else 0, page_size, heads, dim,
-                   _cache_dtype(k_cache), page_table.data_ptr(), page_table.stride(0) if B > 1 else width, width,
+                   code, page_table.data_ptr(), row if B > 1 else width, width,
                    B, lens.data_ptr(), _ptr(new_lens), n, _ptr(err_count))
 
 
@@ -878,13 +884,14 @@ def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_co
     sequence with the new ones; k, v: [B, n, kv_heads, head_dim], any strides;
     new_lens: int32 [B] (None: n each), the tokens of k and v that count."""
     lib = load_library()
-    B, n = (lens.shape[0], k.shape[1]) if k.dim() == 4 else (0, -1)
-    shape = (B, n, k_cache.shape[2], k_cache.shape[3])
-    ks = _bth(k, shape, k_cache.dtype, "k")
-    vs = _bth(v, shape, k_cache.dtype, "v")
+    if k.dim() != 4:
+        raise ValueError("k must be [B, n, kv_heads, head_dim]")
+    n = k.shape[1]
     c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
-    check(lib.rlk_kv_append(ctypes.byref(c), k.data_ptr(), ctypes.byref(ks), v.data_ptr(), ctypes.byref(vs),
-                            _stream(stream)))
+    shape, dtype = (c.B, n, c.kv_heads, c.head_dim), k_cache.dtype
+    ks = _bth(k, shape, dtype, "k")
+    vs = _bth(v, shape, dtype, "v")
+    check(lib.rlk_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)))
 
 
 def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -916,11 +923,11 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
     torch = _torch()
     if q.dim() != 4:
         raise ValueError("q must be [B, n, q_heads, head_dim]")
-    B, n, heads = lens.shape[0], q.shape[1], q.shape[2]
-    dim = k_cache.shape[-1]
+    _, n, heads, _ = q.shape
+    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
+    B, dim, kv_heads = c.B, c.head_dim, c.kv_heads
     shape = (B, n, heads, dim)
     qs = _bth(q, shape, k_cache.dtype, "q")
-    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
     if out is None:
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
         os_ = BTHStrides(n * heads * dim, heads * dim, dim)
@@ -930,14 +937,14 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
         out_lse = torch.empty((B, n, heads), dtype=torch.float32, device=q.device)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
-    need = paged_attention_workspace_bytes(B, n, heads, c.kv_heads, dim, c.max_pages * c.page_size)
+    need = paged_attention_workspace_bytes(B, n, heads, kv_heads, dim, c.max_pages * c.page_size) \
+        if heads > 0 and heads % kv_heads == 0 else 0
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
-    check(lib.rlk_paged_attention(ctypes.byref(c), q.data_ptr(), ctypes.byref(qs), heads,
-                                  dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-                                  ctypes.byref(os_), out_lse.data_ptr(), _ptr(workspace), _stream(stream)))
+    check(lib.rlk_paged_attention(c, q.data_ptr(), qs, heads, dim ** -0.5 if scale is None else scale, window, sinks,
+                                  out.data_ptr(), os_, out_lse.data_ptr(), workspace.data_ptr(), _stream(stream)))
     return out, out_lse
 
 
@@ -1007,6 +1014,6 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
                    draft_logits.stride(0) if draft_logits is not None and B * n > 1 else VOCAB_PADDED,
                    draft_token.data_ptr(), _ptr(num_drafts), tp, ts, pp, ps, kp, ks, dtp, dts, dpp, dps, dkp, dks,
                    accept_uniform.data_ptr(), draw_uniform.data_ptr(), _ptr(err_count))
-    check(lib.rlk_verify_drafts(ctypes.byref(a), *[t.data_ptr() for t in outs], workspace.data_ptr() if B else None,
+    check(lib.rlk_verify_drafts(a, *[t.data_ptr() for t in outs], workspace.data_ptr() if B else None,
                                 _stream(stream)))
     return tuple(outs)
