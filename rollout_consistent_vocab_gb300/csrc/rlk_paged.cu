@@ -1,6 +1,7 @@
 // rlk_paged.cu -- the paged key-value cache: append, and the attention of new
 // tokens over it.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -8,6 +9,7 @@
 #include <stdint.h>
 
 #include "rlk_rollout.h"
+#include "rlk_device.cuh"
 #include "rlk_host.h"
 
 namespace rlk {
@@ -76,11 +78,11 @@ __global__ void append_kernel(const AppendParams P) {
 // ------------------------------------------------------------ attention
 //
 // The tokens of a sequence go in units of 512, at fixed places.  A unit is one
-// CTA's: its four warps take the unit's slices in turn, keys and values come
-// through each warp's own ring in shared memory (cp.async), S^T = K Q^T and
-// O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims) as
-// rows and 8 query rows as columns, with a running maximum and sum per query
-// row; then the warps' shares are folded in order.  What a row gets from a unit
+// CTA's: its four working warps take the unit's slices in turn, and each has a
+// copying warp that brings keys and values into its ring in shared memory (TMA).  S^T = K Q^T
+// and O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims)
+// as rows and 8 query rows as columns, with a running maximum and sum per query
+// row; then the warps' shares are summed in order.  What a row gets from a unit
 // therefore does not depend on the other rows, nor on anything outside the unit.
 // The units of a group (4 units, 2048 tokens, at fixed places too) are folded in
 // order; the groups of a sequence are joined in a fixed tree.  Who folds is
@@ -91,7 +93,12 @@ __global__ void append_kernel(const AppendParams P) {
 
 constexpr int UNIT = 512;                // tokens of a unit
 constexpr int GROUP = 4;                 // units of a group
-constexpr int AW = 4;                    // warps of a CTA
+constexpr int AW = 4;                    // working warps of a CTA, and copying warps
+constexpr int ATHREADS = 2 * AW * 32;
+// Registers of a thread: 128 each at the launch (two CTAs on an SM), then what the
+// copying warps give back goes to the working ones.
+constexpr int REGS_COPY = 40, REGS_WORK = 216;
+static_assert(REGS_COPY + REGS_WORK == 256, "the launch's 2 x 128");
 constexpr int NUM_SMS = 152;
 
 // Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in
@@ -102,16 +109,23 @@ constexpr int HALF = SL / 2;
 template <int D, int NT>
 struct Shape {
   static constexpr int CTAS = 2;                             // per SM
-  static constexpr int ROWB = D * 2;                         // bytes of a head row
-  static constexpr int STAGE = 2 * HALF * ROWB;              // keys, then values
+  // A half in shared memory: D / 64 panels of 16 rows of 128 bytes, the pieces of 16
+  // bytes swizzled (piece p of row r at p ^ (r & 7)); keys, then values.
+  static constexpr int PANEL = HALF * 128;
+  static constexpr int KEYS = D / 64 * PANEL;
+  static constexpr int STAGE = 2 * KEYS;
   static constexpr int STAGES = D == 64 ? 6 : NT == 4 ? 2 : 3;
   static constexpr int SLOTS = D / 16 * NT;                  // fragments (four floats a lane) of a warp's result
-  static constexpr int PASSES = D == 64 && NT == 2 ? 1 : NT;
+  static constexpr int PASSES = D == 128 && NT == 3 ? 6 : NT;
   static constexpr int XCH = SLOTS / PASSES * 512;           // ... exchanged in so many passes
-  static constexpr bool QS = D == 128 && NT == 4;            // queries in shared memory, not in registers
-  static constexpr int SMEM = AW * (STAGES * STAGE + XCH) + (QS ? NT * (D / 16) * 32 * 8 : 0);
-  static_assert(SLOTS % PASSES == 0 && SLOTS / PASSES % AW == 0, "every warp folds as many fragments in each pass");
-  static_assert(2 * (SMEM + (AW + 1) * NT * 64 + 64 + 1024) <= 228 * 1024, "two CTAs in the shared memory of an SM");
+  static constexpr bool QS = D == 128 && NT >= 3;            // queries in shared memory, not in registers
+  static constexpr bool GS = D == 128 && NT == 4;            // ... and the group's result
+  static constexpr int Q_AT = AW * (STAGES * STAGE + XCH);
+  static constexpr int G_AT = Q_AT + (QS ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr int SMEM = G_AT + (GS ? SLOTS * 512 : 0);
+  static_assert(SLOTS % PASSES == 0 && SLOTS / PASSES % AW == 0, "every warp sums as many fragments in each pass");
+  static_assert(2 * (SMEM + (AW + 1) * NT * 64 + AW * STAGES * 16 + 128 + 1024) <= 228 * 1024,
+                "two CTAs in the shared memory of an SM");
 };
 constexpr int WORKERS = NUM_SMS * 2;
 
@@ -126,7 +140,8 @@ struct AttnParams {
   int64_t B;
   float c2;                     // |scale| * log2(e)
   uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
-  bool page16;                  // 16 tokens from a multiple of 16 on lie in one page
+  int box;                      // tokens of a copy: the largest power of 2, up to 16, that divides page_size
+  bool head_first;              // the tensor maps' second place is the head, not the token
   int window, sinks;
   float* lse;
   float2* unit_ml;              // [workers][2 GROUP][8 NT]: maximum, sum
@@ -136,6 +151,9 @@ struct AttnParams {
   uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
   uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
   int groups;                   // groups of the longest sequence that the table can hold
+};
+struct AttnMaps {
+  CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
 };
 
 // What of a sequence is visible to its new tokens: units [0, us) for the sinks
@@ -344,25 +362,32 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// 16 bytes into shared memory
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap& map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
 }
-// ... zeros where !there (src is then not read)
-__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Waits for a phase of a barrier, at most TIMEOUT_NS twice over.
+__device__ __forceinline__ bool mbar_wait_phase(uint32_t bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = global_timer();
+  while (!mbar_try(bar, parity))
+    if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
+  return true;
+}
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(AW * 32) : "memory"); }
 
 // A place in a worker's run: the sequence, kv head and tile, the unit in the
 // sequence's list, the slice in the unit.
 struct Place {
   Seq s;
-  int b, ht, li, slice;
+  int b, head, tile, li, slice;
   int left;                              // units of the run from this one on
 };
-// This warp's first slice of the unit from p.slice on that some new token sees, or false.
+// A warp's first slice of the unit from p.slice on that some new token sees, or false.
 __device__ __forceinline__ bool seek_slice(const AttnParams& P, Place& p) {
   for (; p.slice < UNIT / SL; p.slice += AW) {
     const int t0 = p.s.unit(p.li) * UNIT + p.slice * SL;
@@ -375,8 +400,9 @@ __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
   if (--p.left <= 0) return false;
   if (++p.li == p.s.nu) {
     p.li = 0;
-    if (++p.ht == P.c.kv_heads * P.tiles) {
-      p.ht = 0;
+    if (++p.tile == P.tiles) p.tile = 0, ++p.head;
+    if (p.head == P.c.kv_heads) {
+      p.head = 0;
       do {
         if (++p.b >= P.B) return false;  // (the lengths changed under the call)
         p.s = load_seq(P, p.b);
@@ -393,21 +419,91 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + (log2f(l) - Elem<T>::OFF)) * 0.6931471805599453f;
 }
 
+// A copying warp: the slices of its working warp, by halves of 16 tokens, each half
+// in boxes of P.box tokens that lie in one page.  Lane j looks token j of a slice
+// up, while the slice before is copied.
+template <int D, int NT>
+__device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& maps, Place p, uint32_t ring, uint32_t full,
+                                         uint32_t empty, uint8_t* bad_slice) {
+  using S_ = Shape<D, NT>;
+  const int lane = threadIdx.x & 31;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings' front held the block sums
+  int page = 0, place = 0;
+  bool seen = false;
+  auto seek = [&]() {
+    while (!seek_slice(P, p)) {
+      if (!next_unit(P, p)) return false;
+      p.slice = (threadIdx.x >> 5) - AW;
+    }
+    const int t = p.s.unit(p.li) * UNIT + p.slice * SL + lane;
+    seen = t < p.s.len && (t >= p.s.low || t < P.sinks);
+    uint32_t n = __umulhi(static_cast<uint32_t>(t), P.page_magic);
+    place = static_cast<int>(static_cast<uint32_t>(t) - n * static_cast<uint32_t>(P.c.page_size));
+    if (place < 0) place += P.c.page_size, --n;            // the quotient is one off at most
+    if (place >= P.c.page_size) place -= P.c.page_size, ++n;
+    page = seen ? __ldg(P.c.table + p.b * P.c.table_stride + n) : -1;
+    return true;
+  };
+  int stage = 0, phase = 1, number = 0;
+  bool more = seek();
+  while (more) {
+    const int head = p.head, from = place;
+    // the first lane of a box speaks for it: its page is that of any token seen in it
+    const uint32_t in_box = (__ballot_sync(0xffffffffu, seen) >> lane) & ((1u << P.box) - 1u);
+    const int at = __shfl_sync(0xffffffffu, page, in_box ? lane + __ffs(in_box) - 1 : lane);
+    const bool speaks = lane % P.box == 0 && in_box;
+    const bool copies = speaks && at >= 0 && at < P.c.num_pages;
+    const bool bad = __any_sync(0xffffffffu, speaks && !copies);
+    const uint32_t boxes = __ballot_sync(0xffffffffu, copies);
+    p.slice += AW;
+    more = seek();
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t bar = full + stage * 8;
+      if (!mbar_wait_phase(empty + stage * 8, phase)) return;      // (the working warp gives up too)
+      if (lane == 0) {
+        if (h == 0) bad_slice[number & 3] = bad;
+        mbar_arrive_expect_tx(bar, __popc((boxes >> (h * HALF)) & 0xFFFFu) * P.box * D * 4);
+      }
+      __syncwarp();
+      if (copies && lane / HALF == h) {
+        const uint32_t dst = ring + stage * S_::STAGE + (lane & (HALF - 1)) * 128;
+        const int c1 = P.head_first ? head : from, c2 = P.head_first ? from : head;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          copy_box(dst + c * S_::PANEL, maps.k, c * 64, c1, c2, at, bar);
+          copy_box(dst + S_::KEYS + c * S_::PANEL, maps.v, c * 64, c1, c2, at, bar);
+        }
+      }
+      if (++stage == S_::STAGES) stage = 0, phase ^= 1;
+    }
+    ++number;
+  }
+}
+
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(ATHREADS, Shape<D, NT>::CTAS)
+attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMaps maps) {
   using S_ = Shape<D, NT>;
   using E = Elem<T>;
   constexpr int KK = D / 16, DT = D / 16, SLOTS = S_::SLOTS, MINE = SLOTS / AW;
-  extern __shared__ __align__(256) unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ uint8_t bad_slice[AW][4];
   __shared__ float2 share[AW][NT * 8];   // maximum and sum of each warp's share
   __shared__ float2 group_ml[NT * 8];    // ... and of the group so far
+  __shared__ uint64_t bars[2][AW][S_::STAGES];               // full, empty
   // until the runs are dealt out, the front of the rings holds the block sums
-  int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [AW * 32], then the total
+  int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [ATHREADS], then the total
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t full = smem_addr(&bars[0][0][0]), empty = smem_addr(&bars[1][0][0]);
+  if (tid < 2 * AW * S_::STAGES) {
+    mbar_init(full + tid * 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
 
-  const int64_t total = unit_sums<AW * 32>(P, scan);
+  const int64_t total = unit_sums<ATHREADS>(P, scan);
   const int HT = P.c.kv_heads * P.tiles;
   const Runs runs(static_cast<uint32_t>(total * HT), WORKERS);
   const uint32_t me = blockIdx.x;
@@ -419,9 +515,9 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     const int64_t at = start / HT;       // the sequence that holds it: [run, run + nu)
     int blk = 0;                         // the last block of sequences that begins at or before it
 #pragma unroll
-    for (int j = 0; j < AW; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
+    for (int j = 0; j < ATHREADS / 32; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
     blk -= 1;
-    int b = blk * seqs_per<AW * 32>(P);
+    int b = blk * seqs_per<ATHREADS>(P);
     int64_t run = scan[blk];
     __syncthreads();                     // the rings are free
     Seq s = load_seq(P, b);
@@ -431,108 +527,46 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     }
     if (s.nu == 0) return;               // (the lengths changed under the call)
     const int64_t rest = static_cast<int64_t>(start) - run * HT;
+    const int ht = static_cast<int>(rest / s.nu);
     cons.s = s;
     cons.b = b;
-    cons.ht = static_cast<int>(rest / s.nu);
-    cons.li = static_cast<int>(rest - static_cast<int64_t>(cons.ht) * s.nu);
-    cons.slice = warp;
+    cons.head = ht / P.tiles;
+    cons.tile = ht - cons.head * P.tiles;
+    cons.li = static_cast<int>(rest - static_cast<int64_t>(ht) * s.nu);
+    cons.slice = warp % AW;
   }
-  Place prod = cons;
+  const uint32_t ring = smem_addr(smem_raw) + warp % AW * (S_::STAGES * S_::STAGE);
+  const uint32_t my_full = full + warp % AW * S_::STAGES * 8, my_empty = empty + warp % AW * S_::STAGES * 8;
+  if (warp >= AW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+    copy_run<D, NT>(P, maps, cons, ring, my_full, my_empty, bad_slice[warp - AW]);
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_WORK));
 
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) + warp * (S_::STAGES * S_::STAGE);
+  // ---- a working warp
   // [slot of a fragment][warp][lane]: four floats of a warp's share
   float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE) + lane;
-
-  // ---- the producing side: this warp's slices into its ring by halves; a slice is
-  // looked up in the page table (lane j: token j) while the one before is worked on
-  const T* const kbase = static_cast<const T*>(P.c.k);
-  const T* const vbase = static_cast<const T*>(P.c.v);
-  uint32_t issued = 0, consumed = 0;     // halves
-  int issue_stage = 0, use_stage = 0, page = 0, place = 0;
-  bool seen = false, more = true;
-  constexpr int CH = D / 8;              // 16-byte pieces of a row
-  constexpr int RPI = 32 / CH;           // rows that one instruction of the warp copies
-  const int piece = lane % CH, crow = lane / CH;
-  auto seek = [&]() {
-    while (!seek_slice(P, prod)) {
-      if (!next_unit(P, prod)) {
-        more = false;
-        return;
-      }
-      prod.slice = warp;
-    }
-    const int t = prod.s.unit(prod.li) * UNIT + prod.slice * SL + lane;
-    seen = t < prod.s.len && (t >= prod.s.low || t < P.sinks);
-    uint32_t p = __umulhi(static_cast<uint32_t>(t), P.page_magic);
-    place = static_cast<int>(static_cast<uint32_t>(t) - p * static_cast<uint32_t>(P.c.page_size));
-    if (place < 0) place += P.c.page_size, --p;            // the quotient is one off at most
-    if (place >= P.c.page_size) place -= P.c.page_size, ++p;
-    page = seen ? __ldg(P.c.table + prod.b * P.c.table_stride + p) : 0;
-  };
-  auto issue = [&]() {
-    const int half = issued & 1;
-    const bool there = seen && page >= 0 && page < P.c.num_pages;
-    const int64_t off = there ? page * P.c.page_stride + place * P.c.token_stride + (prod.ht / P.tiles) * P.c.head_stride : 0;
-    const uint32_t there_mask = __ballot_sync(0xffffffffu, there) >> (half * HALF);
-    if (half == 0) {
-      const bool bad = __any_sync(0xffffffffu, seen && !there);
-      if (lane == 0) bad_slice[warp][(issued >> 1) & 3] = bad;
-    }
-    const uint32_t dst = ring + issue_stage * S_::STAGE;
-    if (P.page16 && (there_mask & 0xFFFFu) == 0xFFFFu) {
-      // 16 tokens of one page: rows a constant stride apart
-      const int64_t o = __shfl_sync(0xffffffffu, off, half * HALF) + crow * P.c.token_stride + piece * 8;
-      const T* ks = kbase + o;
-      const T* vs = vbase + o;
-#pragma unroll
-      for (int j = 0; j < HALF / RPI; ++j) {
-        const int rr = j * RPI + crow;
-        const uint32_t d = dst + rr * S_::ROWB + ((piece ^ (rr & 7)) * 16);
-        copy16(d, ks);
-        copy16(d + HALF * S_::ROWB, vs);
-        ks += RPI * P.c.token_stride;
-        vs += RPI * P.c.token_stride;
-      }
-    } else {
-#pragma unroll 2
-      for (int j = 0; j < HALF / RPI; ++j) {
-        const int rr = j * RPI + crow;
-        const int64_t o = __shfl_sync(0xffffffffu, off, half * HALF + rr) + piece * 8;
-        const bool ok = (there_mask >> rr) & 1u;
-        const uint32_t d = dst + rr * S_::ROWB + ((piece ^ (rr & 7)) * 16);
-        copy16_if(d, kbase + o, ok);
-        copy16_if(d + HALF * S_::ROWB, vbase + o, ok);
-      }
-    }
-    copy_commit();
-    ++issued;
-    if (++issue_stage == S_::STAGES) issue_stage = 0;
-    if (half) {
-      prod.slice += AW;
-      seek();
-    }
-  };
-  seek();
-
-  // ---- the consuming side
+  int use_stage = 0, use_phase = 0, number = 0;
+  bool dead = false;                     // a copy did not come
   const int g8 = lane >> 2, t4 = lane & 3;
   // this lane's row of an ldmatrix, with the swizzle of its first piece; piece 2 k is at that ^ 32 k
-  const uint32_t klane = (((lane >> 3) & 1) * 8 + (lane & 7)) * S_::ROWB + (((lane >> 4) ^ (lane & 7)) * 16);
-  const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * S_::ROWB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
+  const uint32_t klane = (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
+  const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
   uint32_t qf[S_::QS ? 1 : NT][KK][2];
-  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + AW * (S_::STAGES * S_::STAGE + S_::XCH)) + lane;      // [NT][KK][lane]
+  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + S_::Q_AT) + lane;      // [NT][KK][lane]
+  float4* const gsm = reinterpret_cast<float4*>(smem_raw + S_::G_AT) + warp * 32 + lane;       // [MINE][warp][lane]
   float o[DT][NT][4], m[NT][2], l[NT][2];
-  float4 gacc[MINE];
+  float4 gacc[S_::GS ? 1 : MINE];
   bool fresh_unit = true, fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false;
   uint32_t at = start;                   // the unit's number in the batch
   for (;;) {
-    while (more && issued - consumed < S_::STAGES) issue();
     const int u = cons.s.unit(cons.li), g = u / GROUP;
-    const int tile0 = P.tiles == 1 ? 0 : (cons.ht % P.tiles) * NT * 8;
+    const int tile0 = cons.tile * NT * 8;
     if (fresh_head) {
       // the queries of this kv head and tile, as B operands
-      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + (cons.ht / P.tiles) * P.group * P.qs.head;
-      if (S_::QS) __syncthreads();       // every warp is done with the head before
+      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + cons.head * P.group * P.qs.head;
+      if (S_::QS) workers_sync();        // every warp is done with the head before
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
         if (S_::QS && x != warp) continue;
@@ -548,7 +582,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
           else qf[x][k][0] = lo, qf[x][k][1] = hi;
         }
       }
-      if (S_::QS) __syncthreads();
+      if (S_::QS) workers_sync();
       fresh_head = false;
     }
     if (fresh_unit && fresh_group) {
@@ -556,7 +590,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       folding = cons.li == f && e - cons.li <= cons.left;
       head_part = start >= at - (cons.li - f);
 #pragma unroll
-      for (int j = 0; j < MINE; ++j) gacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j = 0; j < MINE; ++j) (S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j]) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     if (fresh_unit) {
 #pragma unroll
@@ -573,16 +607,17 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     }
 
     if (seek_slice(P, cons)) {
-      // ---- one slice: its two halves have landed
-      if (issued - consumed == S_::STAGES) copy_wait<S_::STAGES - 2>(); else copy_wait<0>();
-      __syncwarp();
-      unit_bad |= bad_slice[warp][(consumed >> 1) & 3] != 0;
-      uint32_t sk[2];
+      // ---- one slice: its two halves, when they have landed
+      uint32_t sk[2], done[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         sk[y] = ring + use_stage * S_::STAGE;
-        if (++use_stage == S_::STAGES) use_stage = 0;
+        done[y] = my_empty + use_stage * 8;
+        if (!dead && !mbar_wait_phase(my_full + use_stage * 8, use_phase)) dead = true;
+        if (++use_stage == S_::STAGES) use_stage = 0, use_phase ^= 1;
       }
+      unit_bad |= dead || bad_slice[warp][number & 3] != 0;
+      ++number;
       const int t0 = u * UNIT + cons.slice * SL;
       float s[2][NT][4];
 #pragma unroll
@@ -602,7 +637,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint32_t a[4];
-          ldsm(a, (sk[y] + klane) ^ (32 * k));
+          ldsm(a, (sk[y] + k / 4 * S_::PANEL + klane) ^ (32 * (k % 4)));
 #pragma unroll
           for (int x = 0; x < NT; ++x) E::mma(s[y][x], a, bq[x].x, bq[x].y);
         }
@@ -700,21 +735,19 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
       // (which they leave infinite or NaN), and zeros take their place.
       if (masked) {
         bool odd = false;
-        const uint32_t vat = lane * 16;
-        for (int j = 0; j < 2 * HALF * S_::ROWB / 512; ++j) {
-          const uint32_t z = j * 512 + vat;
-          const uint4 w = lds128((z < HALF * S_::ROWB ? sk[0] : sk[1] - HALF * S_::ROWB) + HALF * S_::ROWB + z);
+        for (int z = lane * 16; z < 2 * S_::KEYS; z += 512) {
+          const uint4 w = lds128(z < S_::KEYS ? sk[0] + S_::KEYS + z : sk[1] + z);
           odd |= (((w.x & E::EXP) + E::ONE) | ((w.y & E::EXP) + E::ONE) | ((w.z & E::EXP) + E::ONE) | ((w.w & E::EXP) + E::ONE)) & 0x80008000u;
         }
         if (__any_sync(0xffffffffu, odd)) {
           for (int r = 0; r < SL; ++r) {
             const int t = t0 + r;
-            const uint32_t row = (r < HALF ? sk[0] : sk[1]) + HALF * S_::ROWB + (r & (HALF - 1)) * S_::ROWB;
+            const uint32_t row = (r < HALF ? sk[0] : sk[1]) + S_::KEYS + (r & (HALF - 1)) * 128;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
-                const uint32_t cell = row + (((2 * d + f) ^ (r & 7)) * 16) + g8 * 2;
+                const uint32_t cell = row + d / 4 * S_::PANEL + (((2 * (d % 4) + f) ^ (r & 7)) * 16) + g8 * 2;
                 const uint32_t bits = lds16(cell);
                 if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
 #pragma unroll
@@ -727,13 +760,11 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
               }
           }
           __syncwarp();
-          for (int r = 0; r < SL; ++r) {
-            const uint32_t row = (r < HALF ? sk[0] : sk[1]) + HALF * S_::ROWB + (r & (HALF - 1)) * S_::ROWB;
-            for (int c = lane; c < D; c += 32) {
-              const uint32_t bits = lds16(row + c * 2);
-              if ((bits & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) sts16(row + c * 2, 0u);
-            }
+          for (int z = lane * 2; z < 2 * S_::KEYS; z += 64) {
+            const uint32_t cell = z < S_::KEYS ? sk[0] + S_::KEYS + z : sk[1] + z;
+            if ((lds16(cell) & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) sts16(cell, 0u);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy into it comes after
           __syncwarp();
         }
       }
@@ -747,19 +778,18 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
 #pragma unroll
           for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
         }
-        const uint32_t sv = sk[y] + HALF * S_::ROWB + vlane;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           uint32_t a[4];
-          ldsm_t(a, sv ^ (32 * d));
+          ldsm_t(a, (sk[y] + S_::KEYS + d / 4 * S_::PANEL + vlane) ^ (32 * (d % 4)));
 #pragma unroll
           for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][2], pf[x][3]);
 #pragma unroll
           for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][0], pf[x][1]);
         }
       }
-      consumed += 2;
       __syncwarp();                      // the stages may be filled again
+      if (lane == 0) mbar_arrive(done[0]), mbar_arrive(done[1]);
       cons.slice += AW;
       continue;
     }
@@ -785,13 +815,13 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
     constexpr int PER_PASS = MINE / S_::PASSES;
 #pragma unroll
     for (int pass = 0; pass < S_::PASSES; ++pass) {
-      if (pass > 0) __syncthreads();
+      if (pass > 0) workers_sync();
 #pragma unroll
       for (int f = 0; f < PER_PASS * AW; ++f) {
         const int x = (pass * PER_PASS * AW + f) / DT, d = (pass * PER_PASS * AW + f) % DT;
         xch[(f * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
       }
-      __syncthreads();
+      workers_sync();
       if (pass == 0) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -828,7 +858,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         uacc[pass * PER_PASS + j] = v;
       }
     }
-    __syncthreads();                     // the shares may be written again
+    workers_sync();                     // the shares may be written again
 
     // ---- into the group, where this run holds all of it; otherwise out
     const bool head_ends = cons.li + 1 == cons.s.nu;
@@ -850,17 +880,18 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
         }
 #pragma unroll
       for (int j = 0; j < MINE; ++j) {
-        fold4(gacc[j], uacc[j], f[j * AW / DT][0], f[j * AW / DT][1]);
-        uacc[j] = gacc[j];
+        float4 v = S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j];
+        fold4(v, uacc[j], f[j * AW / DT][0], f[j * AW / DT][1]);
+        uacc[j] = v;
+        (S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j]) = v;
       }
       store = group_ends;
       direct = cons.s.past(g) - cons.s.first(g) == cons.s.nu;
-      slot = (static_cast<int64_t>(cons.b) * HT + cons.ht) * P.groups + g;
+      slot = (static_cast<int64_t>(cons.b) * HT + cons.head * P.tiles + cons.tile) * P.groups + g;
       ml = P.group_ml;
       po = P.group_o;
     }
     if (store) {
-      const int kh = cons.ht / P.tiles;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -868,7 +899,7 @@ __global__ void __launch_bounds__(AW * 32, Shape<D, NT>::CTAS) attn_kernel(const
           const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = query_of(P, row);
           if (row >= P.rows || i >= cons.s.nnew) continue;
           const bool none = UL[x][e] == 0.0f;
-          const int hq = kh * P.group + (row - i * P.group);
+          const int hq = cons.head * P.group + (row - i * P.group);
           T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
           float* dst = po + (slot * (NT * 8) + r) * D + g8;
 #pragma unroll
@@ -1164,12 +1195,54 @@ rlk_status allow_smem(K kernel, int bytes, bool (&done)[64]) {
   return RLK_OK;
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The cache's keys or values as a tensor of (element, token of the page, head, page),
+// the middle two in the order of their strides; a copy takes 64 elements of
+// P.box tokens of a head.
+rlk_status map_cache(CUtensorMap* map, const AttnParams& P, const void* base, int D, bool bf16) {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !p)
+      return fail(RLK_ECUDA, "cuTensorMapEncodeTiled is not available");
+    fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  // a place of extent 1 is never stepped over: any stride does
+  const cuuint64_t any = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t token = P.c.page_size > 1 ? static_cast<cuuint64_t>(P.c.token_stride) * 2 : any;
+  const cuuint64_t head = P.c.kv_heads > 1 ? static_cast<cuuint64_t>(P.c.head_stride) * 2 : any;
+  const cuuint64_t page = P.c.num_pages > 1 ? static_cast<cuuint64_t>(P.c.page_stride) * 2 : any;
+  const cuuint64_t tokens = P.c.page_size, heads = P.c.kv_heads, pages = P.c.num_pages;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), P.head_first ? heads : tokens, P.head_first ? tokens : heads, pages};
+  const cuuint64_t strides[3] = {P.head_first ? head : token, P.head_first ? token : head, page};
+  const cuuint32_t box = static_cast<cuuint32_t>(P.box);
+  const cuuint32_t boxes[4] = {64, P.head_first ? 1 : box, P.head_first ? box : 1, 1}, ones[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(RLK_EINVAL, "the cache's strides have no tensor map (%d): they must be positive and below 2^39 elements",
+                static_cast<int>(r));
+  return RLK_OK;
+}
+
 template <class T, int D, int NT>
 rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   static bool done[64] = {};
   rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, done);
   if (s != RLK_OK) return s;
-  attn_kernel<T, D, NT><<<WORKERS, AW * 32, Shape<D, NT>::SMEM, st>>>(P);
+  AttnMaps maps;
+  constexpr bool bf16 = sizeof(T) == 2 && Elem<T>::EXP == 0x7F807F80u;
+  if (P.c.num_pages > 0) {
+    if ((s = map_cache(&maps.k, P, P.c.k, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P, P.c.v, D, bf16)) != RLK_OK) return s;
+  }
+  attn_kernel<T, D, NT><<<WORKERS, ATHREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them
@@ -1290,7 +1363,9 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
                                        : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
   P.groups = static_cast<int>(y.groups);
   P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
-  P.page16 = cache->page_size % HALF == 0;
+  P.box = 1;
+  while (P.box < HALF && cache->page_size % (2 * P.box) == 0) P.box *= 2;
+  P.head_first = cache->kv_heads > 1 && (cache->page_size == 1 || cache->head_stride < cache->token_stride);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == RLK_DT_BF16;
   if (cache->head_dim == 128)
