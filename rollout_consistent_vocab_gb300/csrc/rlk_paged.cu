@@ -1,6 +1,7 @@
 // rlk_paged.cu -- the paged key-value cache: append, and the attention of new
 // tokens over it.
 
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -78,11 +79,12 @@ __global__ void append_kernel(const AppendParams P) {
 // ------------------------------------------------------------ attention
 //
 // The tokens of a sequence go in units of 512, at fixed places.  A unit is one
-// CTA's: its four working warps take the unit's slices in turn, and each has a
-// copying warp that brings keys and values into its ring in shared memory (TMA).  S^T = K Q^T
-// and O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims)
-// as rows and 8 query rows as columns, with a running maximum and sum per query
-// row; then the warps' shares are summed in order.  What a row gets from a unit
+// CTA's: its four lanes take the unit's slices in turn.  A lane is a copying warp, which
+// brings keys and values into the lane's ring in shared memory (TMA), and a working
+// warp for each 8 query rows, all of which read what it brought.  S^T = K Q^T and
+// O^T += V^T P^T run on the tensor cores with the slice's 16 tokens (or dims) as rows
+// and 8 query rows as columns, with a running maximum and sum per query row; then
+// the lanes' shares are summed in order.  What a row gets from a unit
 // therefore does not depend on the other rows, nor on anything outside the unit.
 // The units of a group (4 units, 2048 tokens, at fixed places too) are folded in
 // order; the groups of a sequence are joined in a fixed tree.  Who folds is
@@ -93,41 +95,40 @@ __global__ void append_kernel(const AppendParams P) {
 
 constexpr int UNIT = 512;                // tokens of a unit
 constexpr int GROUP = 4;                 // units of a group
-constexpr int AW = 4;                    // working warps of a CTA, and copying warps
-constexpr int ATHREADS = 2 * AW * 32;
-// Registers of a thread: 128 each at the launch (two CTAs on an SM), then what the
-// copying warps give back goes to the working ones.
-constexpr int REGS_COPY = 40, REGS_WORK = 216;
-static_assert(REGS_COPY + REGS_WORK == 256, "the launch's 2 x 128");
+constexpr int AW = 4;                    // lanes of a CTA: every fourth slice of a unit is one's
 constexpr int NUM_SMS = 152;
 
-// Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in
-// tiles of 8 NT.  A warp works on slices of 32 tokens; they are copied in halves
-// of 16, STAGES halves in its ring.
+// Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in tiles of
+// 8 NT.  A lane is a copying warp and NT working warps of 8 rows each, which share
+// what it copies: slices of 32 tokens, in halves of 16, STAGES halves in its ring.
 constexpr int SL = 32;
 constexpr int HALF = SL / 2;
 template <int D, int NT>
 struct Shape {
-  static constexpr int CTAS = 2;                             // per SM
+  static constexpr int CTAS = NT <= 2 ? 2 : 1;               // per SM
+  static constexpr int WORKERS = NUM_SMS * CTAS;
+  static constexpr int THREADS = (NT + 1) * AW * 32;
+  // Registers of a thread: as many at the launch as an SM has for its CTAs, then what
+  // the copying warps give back goes to the working ones.
+  static constexpr int REGS = 65536 / (CTAS * THREADS) / 8 * 8;
+  static constexpr int REGS_COPY = 40, REGS_WORK = (REGS * (NT + 1) - REGS_COPY) / NT / 8 * 8;
   // A half in shared memory: D / 64 panels of 16 rows of 128 bytes, the pieces of 16
   // bytes swizzled (piece p of row r at p ^ (r & 7)); keys, then values.
   static constexpr int PANEL = HALF * 128;
   static constexpr int KEYS = D / 64 * PANEL;
   static constexpr int STAGE = 2 * KEYS;
-  static constexpr int STAGES = D == 64 ? 6 : NT == 4 ? 2 : 3;
-  static constexpr int SLOTS = D / 16 * NT;                  // fragments (four floats a lane) of a warp's result
-  static constexpr int PASSES = D == 128 && NT == 3 ? 6 : NT;
-  static constexpr int XCH = SLOTS / PASSES * 512;           // ... exchanged in so many passes
-  static constexpr bool QS = D == 128 && NT >= 3;            // queries in shared memory, not in registers
-  static constexpr bool GS = D == 128 && NT == 4;            // ... and the group's result
-  static constexpr int Q_AT = AW * (STAGES * STAGE + XCH);
-  static constexpr int G_AT = Q_AT + (QS ? NT * (D / 16) * 32 * 8 : 0);
-  static constexpr int SMEM = G_AT + (GS ? SLOTS * 512 : 0);
+  static constexpr int STAGES = CTAS == 1 ? 5 * 128 / D : D == 128 ? 3 : NT == 1 ? 6 : 5;
+  static constexpr int SLOTS = D / 16;                       // fragments (four floats a thread) of a warp's result
+  static constexpr int PASSES = D == 128 && NT % 2 == 0 ? 2 : 1;
+  static constexpr int XCH = SLOTS / PASSES * AW * 512;      // ... of 8 rows, exchanged in so many passes
+  static constexpr bool QS = D == 128 && NT == 4;            // queries in shared memory, not in registers
+  static constexpr int Q_AT = AW * STAGES * STAGE + NT * XCH;
+  static constexpr int SMEM = Q_AT + (QS ? NT * SLOTS * 32 * 8 : 0);
   static_assert(SLOTS % PASSES == 0 && SLOTS / PASSES % AW == 0, "every warp sums as many fragments in each pass");
-  static_assert(2 * (SMEM + (AW + 1) * NT * 64 + AW * STAGES * 16 + 128 + 1024) <= 228 * 1024,
-                "two CTAs in the shared memory of an SM");
+  static_assert(CTAS * (SMEM + (AW + 1) * NT * 64 + AW * STAGES * 16 + 128 + 1024) <= 228 * 1024,
+                "as many CTAs in the shared memory of an SM");
 };
-constexpr int WORKERS = NUM_SMS * 2;
+constexpr int WORKERS = NUM_SMS * 2;     // at most
 
 struct AttnParams {
   PagedParams c;
@@ -150,6 +151,7 @@ struct AttnParams {
   float* group_o;
   uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
   uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
+  uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
 };
 struct AttnMaps {
@@ -292,10 +294,19 @@ __device__ __forceinline__ void fold4(float4& x, const float4& part, Factors eve
   x.z = fold(x.z, part.z, even);
   x.w = fold(x.w, part.w, odd);
 }
+template <uint32_t EXP, uint32_t ONE>
+struct OddElem {                         // which of a pair of elements are not finite: bits 15 and 31
+  static __device__ __forceinline__ uint32_t of(uint32_t w) { return ((w & EXP) + ONE) & 0x80008000u; }
+  static __device__ __forceinline__ bool odd(const uint4& w) { return (of(w.x) | of(w.y) | of(w.z) | of(w.w)) != 0; }
+  static __device__ __forceinline__ void clear_odd(uint32_t (&a)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] &= ~((of(a[j]) >> 15) * 0xFFFFu);
+  }
+};
 template <class T> struct Elem;
-template <> struct Elem<__nv_bfloat16> {
+template <> struct Elem<__nv_bfloat16> : OddElem<0x7F807F80u, 0x00800080u> {
   static constexpr float OFF = 0.0f, SLACK = 8.0f;
-  static constexpr uint32_t EXP = 0x7F807F80u, ONE = 0x00800080u;
+  static constexpr uint32_t EXP = 0x7F807F80u;
   static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   static constexpr float MORE = 1.0f + 2.384185791015625e-07f;   // 1 + 2^-22
   // The weights (a, b) >= 0 as the sum of two pairs of elements: hi is cut off, lo
@@ -316,9 +327,9 @@ template <> struct Elem<__nv_bfloat16> {
   }
 };
 // f16 holds weights in units of 2^-8, so that the smallest ones keep their bits
-template <> struct Elem<__half> {
+template <> struct Elem<__half> : OddElem<0x7C007C00u, 0x04000400u> {
   static constexpr float OFF = 8.0f, SLACK = 6.0f;
-  static constexpr uint32_t EXP = 0x7C007C00u, ONE = 0x04000400u;
+  static constexpr uint32_t EXP = 0x7C007C00u;
   static __device__ __forceinline__ float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
   static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16: 2^-32 of the row's largest weight
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -378,7 +389,22 @@ __device__ __forceinline__ bool mbar_wait_phase(uint32_t bar, uint32_t parity) {
     if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
   return true;
 }
-__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(AW * 32) : "memory"); }
+// ... for a copying warp: it looks now and then, and leaves the issue slots to the
+// working ones.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok) return true;
+    if (t0 == 0) t0 = global_timer();
+    else if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
+    __nanosleep(100);
+  }
+}
+// the four working warps of the tile's rows 8 x .. 8 x + 7
+__device__ __forceinline__ void rows_sync(int x) { asm volatile("bar.sync %0, %1;" ::"r"(x + 1), "n"(AW * 32) : "memory"); }
 
 // A place in a worker's run: the sequence, kv head and tile, the unit in the
 // sequence's list, the slice in the unit.
@@ -419,7 +445,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + (log2f(l) - Elem<T>::OFF)) * 0.6931471805599453f;
 }
 
-// A copying warp: the slices of its working warp, by halves of 16 tokens, each half
+// A copying warp: the slices of its lane, by halves of 16 tokens, each half
 // in boxes of P.box tokens that lie in one page.  Lane j looks token j of a slice
 // up, while the slice before is copied.
 template <int D, int NT>
@@ -433,7 +459,7 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
   auto seek = [&]() {
     while (!seek_slice(P, p)) {
       if (!next_unit(P, p)) return false;
-      p.slice = (threadIdx.x >> 5) - AW;
+      p.slice = (threadIdx.x >> 5) % AW;
     }
     const int t = p.s.unit(p.li) * UNIT + p.slice * SL + lane;
     seen = t < p.s.len && (t >= p.s.low || t < P.sinks);
@@ -460,9 +486,9 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       const uint32_t bar = full + stage * 8;
-      if (!mbar_wait_phase(empty + stage * 8, phase)) return;      // (the working warp gives up too)
+      if (!mbar_wait_phase(empty + stage * 8, phase)) return;      // (the working warps give up too)
       if (lane == 0) {
-        if (h == 0) bad_slice[number & 3] = bad;
+        if (h == 0) bad_slice[number & 7] = bad;
         mbar_arrive_expect_tx(bar, __popc((boxes >> (h * HALF)) & 0xFFFFu) * P.box * D * 4);
       }
       __syncwarp();
@@ -482,30 +508,30 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
 }
 
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(ATHREADS, Shape<D, NT>::CTAS)
+__global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::CTAS)
 attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMaps maps) {
   using S_ = Shape<D, NT>;
   using E = Elem<T>;
-  constexpr int KK = D / 16, DT = D / 16, SLOTS = S_::SLOTS, MINE = SLOTS / AW;
+  constexpr int KK = D / 16, DT = D / 16, MINE = S_::SLOTS / AW, THREADS = S_::THREADS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ uint8_t bad_slice[AW][4];
-  __shared__ float2 share[AW][NT * 8];   // maximum and sum of each warp's share
+  __shared__ uint8_t bad_slice[AW][8];
+  __shared__ float2 share[AW][NT * 8];   // maximum and sum of each lane's share
   __shared__ float2 group_ml[NT * 8];    // ... and of the group so far
   __shared__ uint64_t bars[2][AW][S_::STAGES];               // full, empty
   // until the runs are dealt out, the front of the rings holds the block sums
-  int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [ATHREADS], then the total
+  int64_t* const scan = reinterpret_cast<int64_t*>(smem_raw);      // [THREADS], then the total
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t full = smem_addr(&bars[0][0][0]), empty = smem_addr(&bars[1][0][0]);
   if (tid < 2 * AW * S_::STAGES) {
-    mbar_init(full + tid * 8, 1);
+    mbar_init(full + tid * 8, tid < AW * S_::STAGES ? 1 : NT);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
 
-  const int64_t total = unit_sums<ATHREADS>(P, scan);
+  const int64_t total = unit_sums<THREADS>(P, scan);
   const int HT = P.c.kv_heads * P.tiles;
-  const Runs runs(static_cast<uint32_t>(total * HT), WORKERS);
+  const Runs runs(static_cast<uint32_t>(total * HT), S_::WORKERS);
   const uint32_t me = blockIdx.x;
   if (me >= runs.workers) return;        // every thread
   const uint32_t start = runs.start(me);
@@ -515,9 +541,9 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     const int64_t at = start / HT;       // the sequence that holds it: [run, run + nu)
     int blk = 0;                         // the last block of sequences that begins at or before it
 #pragma unroll
-    for (int j = 0; j < ATHREADS / 32; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
+    for (int j = 0; j < THREADS / 32; ++j) blk += __popc(__ballot_sync(0xffffffffu, scan[j * 32 + lane] <= at));
     blk -= 1;
-    int b = blk * seqs_per<ATHREADS>(P);
+    int b = blk * seqs_per<THREADS>(P);
     int64_t run = scan[blk];
     __syncthreads();                     // the rings are free
     Seq s = load_seq(P, b);
@@ -535,54 +561,54 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     cons.li = static_cast<int>(rest - static_cast<int64_t>(ht) * s.nu);
     cons.slice = warp % AW;
   }
-  const uint32_t ring = smem_addr(smem_raw) + warp % AW * (S_::STAGES * S_::STAGE);
-  const uint32_t my_full = full + warp % AW * S_::STAGES * 8, my_empty = empty + warp % AW * S_::STAGES * 8;
-  if (warp >= AW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
-    copy_run<D, NT>(P, maps, cons, ring, my_full, my_empty, bad_slice[warp - AW]);
+  const int w = warp % AW, x = warp / AW;      // the lane; the working warp's rows, 8 x .. 8 x + 7 of a tile
+  const uint32_t ring = smem_addr(smem_raw) + w * (S_::STAGES * S_::STAGE);
+  const uint32_t my_full = full + w * S_::STAGES * 8, my_empty = empty + w * S_::STAGES * 8;
+  if (x == NT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S_::REGS_COPY));
+    copy_run<D, NT>(P, maps, cons, ring, my_full, my_empty, bad_slice[w]);
     return;
   }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_WORK));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S_::REGS_WORK));
 
   // ---- a working warp
-  // [slot of a fragment][warp][lane]: four floats of a warp's share
-  float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE) + lane;
+  // [fragment][lane of the CTA][thread]: four floats of a warp's result
+  float4* const xch = reinterpret_cast<float4*>(smem_raw + AW * S_::STAGES * S_::STAGE + x * S_::XCH) + lane;
   int use_stage = 0, use_phase = 0, number = 0;
   bool dead = false;                     // a copy did not come
   const int g8 = lane >> 2, t4 = lane & 3;
-  // this lane's row of an ldmatrix, with the swizzle of its first piece; piece 2 k is at that ^ 32 k
+  // this lane's row of an ldmatrix, with the swizzle of its first piece; pieces 2 k are at that ^ 32 k
   const uint32_t klane = (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
   const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
-  uint32_t qf[S_::QS ? 1 : NT][KK][2];
-  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + S_::Q_AT) + lane;      // [NT][KK][lane]
-  float4* const gsm = reinterpret_cast<float4*>(smem_raw + S_::G_AT) + warp * 32 + lane;       // [MINE][warp][lane]
-  float o[DT][NT][4], m[NT][2], l[NT][2];
-  float4 gacc[S_::GS ? 1 : MINE];
-  bool fresh_unit = true, fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false;
+  uint32_t kswz[4], vswz[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) kswz[k] = klane ^ (32 * k), vswz[k] = (vlane ^ (32 * k)) + S_::KEYS;
+  uint32_t qf[S_::QS ? 1 : KK][2];
+  uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + S_::Q_AT) + x * KK * 32 + lane;       // [KK][thread]
+  float o[DT][4], m[2], l[2];
+  float4 gacc[MINE];
+  bool fresh_unit = true, fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false, idle = false;
   uint32_t at = start;                   // the unit's number in the batch
   for (;;) {
     const int u = cons.s.unit(cons.li), g = u / GROUP;
-    const int tile0 = cons.tile * NT * 8;
+    const int row0 = (cons.tile * NT + x) * 8;
     if (fresh_head) {
       // the queries of this kv head and tile, as B operands
       const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + cons.head * P.group * P.qs.head;
-      if (S_::QS) workers_sync();        // every warp is done with the head before
+      idle = row0 >= P.rows || query_of(P, row0) >= cons.s.nnew;
+      const int row = row0 + g8, i = query_of(P, row);
+      const bool real = row < P.rows && i < cons.s.nnew;
+      const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
+      if (S_::QS) rows_sync(x);          // every warp is done with the head before
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        if (S_::QS && x != warp) continue;
-        const int row = tile0 + x * 8 + g8;
-        const int i = query_of(P, row);
-        const bool real = row < P.rows && i < cons.s.nnew;
-        const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-          const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.q_sign : 0u;
-          const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.q_sign : 0u;
-          if constexpr (S_::QS) qsm[(x * KK + k) * 32] = make_uint2(lo, hi);
-          else qf[x][k][0] = lo, qf[x][k][1] = hi;
-        }
+      for (int k = 0; k < KK; ++k) {
+        if (S_::QS && k % AW != w) continue;
+        const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.q_sign : 0u;
+        const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.q_sign : 0u;
+        if constexpr (S_::QS) qsm[k * 32] = make_uint2(lo, hi);
+        else qf[k][0] = lo, qf[k][1] = hi;
       }
-      if (S_::QS) workers_sync();
+      if (S_::QS) rows_sync(x);
       fresh_head = false;
     }
     if (fresh_unit && fresh_group) {
@@ -590,20 +616,17 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       folding = cons.li == f && e - cons.li <= cons.left;
       head_part = start >= at - (cons.li - f);
 #pragma unroll
-      for (int j = 0; j < MINE; ++j) (S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j]) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j = 0; j < MINE; ++j) gacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     if (fresh_unit) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[d][x][e] = 0.0f;
-#pragma unroll
-      for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+      m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
       unit_bad = false;
       fresh_unit = false;
-      cons.slice = warp;
+      cons.slice = w;
     }
 
     if (seek_slice(P, cons)) {
@@ -616,130 +639,109 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
         if (!dead && !mbar_wait_phase(my_full + use_stage * 8, use_phase)) dead = true;
         if (++use_stage == S_::STAGES) use_stage = 0, use_phase ^= 1;
       }
-      unit_bad |= dead || bad_slice[warp][number & 3] != 0;
+      unit_bad |= dead || bad_slice[w][number & 7] != 0;
       ++number;
       const int t0 = u * UNIT + cons.slice * SL;
-      float s[2][NT][4];
+      cons.slice += AW;
+      if (idle) {                        // no query among the warp's rows
+        if (lane == 0) mbar_arrive(done[0]), mbar_arrive(done[1]);
+        continue;
+      }
+      float s[2][4];
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[y][x][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) s[y][e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
-        uint2 bq[NT];
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          if constexpr (S_::QS) bq[x] = qsm[(x * KK + k) * 32];
-          else bq[x] = make_uint2(qf[x][k][0], qf[x][k][1]);
-        }
+        uint2 bq;
+        if constexpr (S_::QS) bq = qsm[k * 32];
+        else bq = make_uint2(qf[k][0], qf[k][1]);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint32_t a[4];
-          ldsm(a, (sk[y] + k / 4 * S_::PANEL + klane) ^ (32 * (k % 4)));
-#pragma unroll
-          for (int x = 0; x < NT; ++x) E::mma(s[y][x], a, bq[x].x, bq[x].y);
+          ldsm(a, sk[y] + kswz[k % 4] + k / 4 * S_::PANEL);
+          E::mma(s[y], a, bq.x, bq.y);
         }
       }
       // masks: the queries stand at p0 .. len - 1
       const int p0 = cons.s.len - cons.s.nnew;
       const bool masked = t0 + SL - 1 > p0 ||
                           (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 + SL > P.sinks);
-      uint32_t hidden = 0;               // bit (y NT + x) 4 + e (of the lane's scores)
+      uint32_t hidden = 0;               // bit 4 y + e (of the thread's scores)
       if (masked) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int pos = p0 + query_of(P, tile0 + x * 8 + 2 * t4 + e);
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                const int t = t0 + y * HALF + g8 + 8 * f;
-                if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks)) {
-                  s[y][x][2 * f + e] = -INFINITY;
-                  hidden |= 1u << ((y * NT + x) * 4 + 2 * f + e);
-                }
-              }
-          }
-      }
-      // each query row's reference m (the lanes of equal t4 share a row's tokens): it follows
-      // the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
-      float top[NT][2];
-      bool ahead = false;
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
         for (int e = 0; e < 2; ++e) {
-          top[x][e] = fmaxf(fmaxf(s[0][x][e], s[0][x][2 + e]), fmaxf(s[1][x][e], s[1][x][2 + e])) * P.c2;
-          ahead |= top[x][e] > m[x][e] + E::SLACK;
-        }
-      if (__any_sync(0xffffffffu, ahead)) {
-        bool scaled = false;
-        float fac[NT][2];
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = top[x][e];
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            fac[x][e] = 1.0f;
-            if (mx > m[x][e] + E::SLACK) {
-              if (m[x][e] != -INFINITY) {
-                fac[x][e] = ex2f(m[x][e] - mx);
-                scaled = true;
-              }
-              m[x][e] = mx;
-            }
-          }
-        if (__any_sync(0xffffffffu, scaled)) {
-#pragma unroll
-          for (int x = 0; x < NT; ++x) l[x][0] *= fac[x][0], l[x][1] *= fac[x][1];
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[d][x][e] *= fac[x][e & 1];
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float sub = m[x][e] == -INFINITY ? E::OFF : E::OFF - m[x][e];
+          const int pos = p0 + query_of(P, row0 + 2 * t4 + e);
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int f = 0; f < 4; f += 2) s[y][x][f + e] = ex2f(__fmaf_rn(s[y][x][f + e], P.c2, sub));
+            for (int f = 0; f < 2; ++f) {
+              const int t = t0 + y * HALF + g8 + 8 * f;
+              if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks)) {
+                s[y][2 * f + e] = -INFINITY;
+                hidden |= 1u << (y * 4 + 2 * f + e);
+              }
+            }
         }
+      }
+      // each query row's reference m (the threads of equal t4 share a row's tokens): it follows
+      // the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
+      float top[2];
+      bool ahead = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e])) * P.c2;
+        ahead |= top[e] > m[e] + E::SLACK;
+      }
+      if (__any_sync(0xffffffffu, ahead)) {
+        bool scaled = false;
+        float fac[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = top[e];
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+          fac[e] = 1.0f;
+          if (mx > m[e] + E::SLACK) {
+            if (m[e] != -INFINITY) {
+              fac[e] = ex2f(m[e] - mx);
+              scaled = true;
+            }
+            m[e] = mx;
+          }
+        }
+        if (__any_sync(0xffffffffu, scaled)) {
+          l[0] *= fac[0], l[1] *= fac[1];
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] *= fac[e & 1];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sub = m[e] == -INFINITY ? E::OFF : E::OFF - m[e];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int f = 0; f < 4; f += 2) s[y][f + e] = ex2f(__fmaf_rn(s[y][f + e], P.c2, sub));
+      }
+      // A masked token's value must not come in even as 0 * inf: where a masked slice
+      // holds values that are not finite, they go straight into the rows that see them
+      // (which they leave infinite or NaN), and the product takes zeros for them.
+      bool odd = false;
       if (masked) {
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((hidden >> ((y * NT + x) * 4 + e)) & 1u) s[y][x][e] = 0.0f;
-      }
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          l[x][e] += (s[0][x][e] + s[0][x][2 + e]) + (s[1][x][e] + s[1][x][2 + e]);
-      // A masked token's value must not come in even as 0 * inf: where a masked slice
-      // holds values that are not finite, they go straight into the rows that see them
-      // (which they leave infinite or NaN), and zeros take their place.
-      if (masked) {
-        bool odd = false;
-        for (int z = lane * 16; z < 2 * S_::KEYS; z += 512) {
-          const uint4 w = lds128(z < S_::KEYS ? sk[0] + S_::KEYS + z : sk[1] + z);
-          odd |= (((w.x & E::EXP) + E::ONE) | ((w.y & E::EXP) + E::ONE) | ((w.z & E::EXP) + E::ONE) | ((w.w & E::EXP) + E::ONE)) & 0x80008000u;
-        }
-        if (__any_sync(0xffffffffu, odd)) {
+          for (int e = 0; e < 4; ++e)
+            if ((hidden >> (y * 4 + e)) & 1u) s[y][e] = 0.0f;
+#pragma unroll 8
+        for (int z = lane * 16; z < 2 * S_::KEYS; z += 512) odd |= E::odd(lds128(z < S_::KEYS ? sk[0] + S_::KEYS + z : sk[1] + z));
+        odd = __any_sync(0xffffffffu, odd);
+        if (odd) {
+#pragma unroll 1
           for (int r = 0; r < SL; ++r) {
             const int t = t0 + r;
             const uint32_t row = (r < HALF ? sk[0] : sk[1]) + S_::KEYS + (r & (HALF - 1)) * 128;
@@ -747,118 +749,119 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
             for (int d = 0; d < DT; ++d)
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
-                const uint32_t cell = row + d / 4 * S_::PANEL + (((2 * (d % 4) + f) ^ (r & 7)) * 16) + g8 * 2;
-                const uint32_t bits = lds16(cell);
+                const uint32_t bits = lds16(row + d / 4 * S_::PANEL + (((2 * (d % 4) + f) ^ (r & 7)) * 16) + g8 * 2);
                 if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int pos = p0 + query_of(P, tile0 + x * 8 + 2 * t4 + e);
-                    if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) o[d][x][2 * f + e] += E::value(bits);
-                  }
+                for (int e = 0; e < 2; ++e) {
+                  const int pos = p0 + query_of(P, row0 + 2 * t4 + e);
+                  if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) o[d][2 * f + e] += E::value(bits);
+                }
               }
           }
-          __syncwarp();
-          for (int z = lane * 2; z < 2 * S_::KEYS; z += 64) {
-            const uint32_t cell = z < S_::KEYS ? sk[0] + S_::KEYS + z : sk[1] + z;
-            if ((lds16(cell) & E::EXP & 0xFFFFu) == (E::EXP & 0xFFFFu)) sts16(cell, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy into it comes after
-          __syncwarp();
         }
       }
 #pragma unroll
+      for (int e = 0; e < 2; ++e) l[e] += (s[0][e] + s[0][2 + e]) + (s[1][e] + s[1][2 + e]);
+      uint32_t pf[2][4];                 // weights: tokens 0-7 and 8-15 of a half, then what the dtype dropped of them
+#pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t pf[NT][4];              // weights: tokens 0-7 and 8-15, then what the dtype dropped of them
+        E::split(s[y][0], s[y][1], pf[y][0], pf[y][2]);
+        E::split(s[y][2], s[y][3], pf[y][1], pf[y][3]);
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          E::split(s[y][x][0], s[y][x][1], pf[x][0], pf[x][2]);
-          E::split(s[y][x][2], s[y][x][3], pf[x][1], pf[x][3]);
+        for (int e = 0; e < 4; ++e) pf[y][e] = movm(pf[y][e]);
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t base = y ? sk[1] : sk[0];
+          uint32_t w4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
+          for (int e = 0; e < 4; ++e) w4[e] = y ? pf[1][e] : pf[0][e];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, base + vswz[d % 4] + d / 4 * S_::PANEL);
+            E::clear_odd(a);
+            E::mma(o[d], a, w4[2], w4[3]);
+            E::mma(o[d], a, w4[0], w4[1]);
+          }
         }
+      } else {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          uint32_t a[4];
-          ldsm_t(a, (sk[y] + S_::KEYS + d / 4 * S_::PANEL + vlane) ^ (32 * (d % 4)));
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][2], pf[x][3]);
-#pragma unroll
-          for (int x = 0; x < NT; ++x) E::mma(o[d][x], a, pf[x][0], pf[x][1]);
-        }
+          for (int d = 0; d < DT; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, sk[y] + vswz[d % 4] + d / 4 * S_::PANEL);
+            E::mma(o[d], a, pf[y][2], pf[y][3]);
+            E::mma(o[d], a, pf[y][0], pf[y][1]);
+          }
       }
       __syncwarp();                      // the stages may be filled again
       if (lane == 0) mbar_arrive(done[0]), mbar_arrive(done[1]);
-      cons.slice += AW;
       continue;
     }
 
-    // ---- the unit's result: the warps' shares brought to one maximum and summed in order
+    // ---- the unit's result: the lanes' shares brought to one maximum and summed in order
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int z = 4; z < 32; z <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], z);
+      if (l[e] == 0.0f) {                // nothing seen: no trace, whatever the values were
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
-        if (l[x][e] == 0.0f) {           // nothing seen: no trace, whatever the values were
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d][x][e] = o[d][x][2 + e] = 0.0f;
-        }
-        if (unit_bad) m[x][e] = 0.0f, l[x][e] = __int_as_float(0x7fc00000);
-        if (g8 == 0) share[warp][x * 8 + 2 * t4 + e] = make_float2(m[x][e], l[x][e]);
+        for (int d = 0; d < DT; ++d) o[d][e] = o[d][2 + e] = 0.0f;
       }
-    if (unit_bad && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    float UM[NT][2], UL[NT][2], wt[NT][2][AW];
-    float2 gml[NT][2];
+      if (unit_bad) m[e] = 0.0f, l[e] = __int_as_float(0x7fc00000);
+      if (g8 == 0) share[w][x * 8 + 2 * t4 + e] = make_float2(m[e], l[e]);
+    }
+    if (unit_bad && x == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+    float UM[2], UL[2], wt[2][AW];
+    float2 gml[2];
     float4 uacc[MINE];
     constexpr int PER_PASS = MINE / S_::PASSES;
 #pragma unroll
     for (int pass = 0; pass < S_::PASSES; ++pass) {
-      if (pass > 0) workers_sync();
+      if (pass > 0) rows_sync(x);
 #pragma unroll
       for (int f = 0; f < PER_PASS * AW; ++f) {
-        const int x = (pass * PER_PASS * AW + f) / DT, d = (pass * PER_PASS * AW + f) % DT;
-        xch[(f * AW + warp) * 32] = make_float4(o[d][x][0], o[d][x][1], o[d][x][2], o[d][x][3]);
+        const int d = pass * PER_PASS * AW + f;
+        xch[(f * AW + w) * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
       }
-      workers_sync();
+      rows_sync(x);
       if (pass == 0) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+        for (int e = 0; e < 2; ++e) {
+          float2 h[AW];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float2 h[AW];
+          for (int z = 0; z < AW; ++z) h[z] = share[z][x * 8 + 2 * t4 + e];
+          float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < AW; ++w) h[w] = share[w][x * 8 + 2 * t4 + e];
-            float mx = -INFINITY, sum = 0.0f;
+          for (int z = 0; z < AW; ++z) mx = fmaxf(mx, h[z].x);
 #pragma unroll
-            for (int w = 0; w < AW; ++w) mx = fmaxf(mx, h[w].x);
-#pragma unroll
-            for (int w = 0; w < AW; ++w) {
-              wt[x][e][w] = h[w].y == 0.0f ? 0.0f : ex2f(h[w].x - mx);
-              sum = __fmaf_rn(h[w].y, wt[x][e][w], sum);
-            }
-            UM[x][e] = mx;
-            UL[x][e] = sum;
-            gml[x][e] = fresh_group ? make_float2(-INFINITY, 0.0f) : group_ml[x * 8 + 2 * t4 + e];
+          for (int z = 0; z < AW; ++z) {
+            wt[e][z] = h[z].y == 0.0f ? 0.0f : ex2f(h[z].x - mx);
+            sum = __fmaf_rn(h[z].y, wt[e][z], sum);
           }
+          UM[e] = mx;
+          UL[e] = sum;
+          gml[e] = fresh_group ? make_float2(-INFINITY, 0.0f) : group_ml[x * 8 + 2 * t4 + e];
+        }
       }
 #pragma unroll
       for (int j = 0; j < PER_PASS; ++j) {
-        const int x = (pass * PER_PASS + j) * AW / DT;     // of fragments j AW .. j AW + 3
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < AW; ++w) {
-          const float4 z = xch[((j * AW + warp) * AW + w) * 32];
-          v.x = __fmaf_rn(z.x, wt[x][0][w], v.x);
-          v.y = __fmaf_rn(z.y, wt[x][1][w], v.y);
-          v.z = __fmaf_rn(z.z, wt[x][0][w], v.z);
-          v.w = __fmaf_rn(z.w, wt[x][1][w], v.w);
+        for (int z = 0; z < AW; ++z) {
+          const float4 part = xch[((j * AW + w) * AW + z) * 32];
+          v.x = __fmaf_rn(part.x, wt[0][z], v.x);
+          v.y = __fmaf_rn(part.y, wt[1][z], v.y);
+          v.z = __fmaf_rn(part.z, wt[0][z], v.z);
+          v.w = __fmaf_rn(part.w, wt[1][z], v.w);
         }
         uacc[pass * PER_PASS + j] = v;
       }
     }
-    workers_sync();                     // the shares may be written again
+    rows_sync(x);                        // the shares may be written again
 
     // ---- into the group, where this run holds all of it; otherwise out
     const bool head_ends = cons.li + 1 == cons.s.nu;
@@ -868,22 +871,18 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     float2* ml = P.unit_ml;
     float* po = P.unit_o;
     if (folding) {
-      Factors f[NT][2];
+      Factors f[2];
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f[x][e] = add_part(gml[x][e].x, gml[x][e].y, UM[x][e], UL[x][e]);
-          UM[x][e] = gml[x][e].x;
-          UL[x][e] = gml[x][e].y;
-          if (warp == 0 && g8 == 0) group_ml[x * 8 + 2 * t4 + e] = gml[x][e];
-        }
+      for (int e = 0; e < 2; ++e) {
+        f[e] = add_part(gml[e].x, gml[e].y, UM[e], UL[e]);
+        UM[e] = gml[e].x;
+        UL[e] = gml[e].y;
+        if (w == 0 && g8 == 0) group_ml[x * 8 + 2 * t4 + e] = gml[e];
+      }
 #pragma unroll
       for (int j = 0; j < MINE; ++j) {
-        float4 v = S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j];
-        fold4(v, uacc[j], f[j * AW / DT][0], f[j * AW / DT][1]);
-        uacc[j] = v;
-        (S_::GS ? gsm[j * AW * 32] : gacc[S_::GS ? 0 : j]) = v;
+        fold4(gacc[j], uacc[j], f[0], f[1]);
+        uacc[j] = gacc[j];
       }
       store = group_ends;
       direct = cons.s.past(g) - cons.s.first(g) == cons.s.nu;
@@ -893,33 +892,30 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     }
     if (store) {
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+      for (int e = 0; e < 2; ++e) {
+        const int r = x * 8 + 2 * t4 + e, row = row0 + 2 * t4 + e, i = query_of(P, row);
+        if (row >= P.rows || i >= cons.s.nnew) continue;
+        const bool none = UL[e] == 0.0f;
+        const int hq = cons.head * P.group + (row - i * P.group);
+        T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
+        float* dst = po + (slot * (NT * 8) + r) * D + g8;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = x * 8 + 2 * t4 + e, row = tile0 + r, i = query_of(P, row);
-          if (row >= P.rows || i >= cons.s.nnew) continue;
-          const bool none = UL[x][e] == 0.0f;
-          const int hq = cons.head * P.group + (row - i * P.group);
-          T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
-          float* dst = po + (slot * (NT * 8) + r) * D + g8;
-#pragma unroll
-          for (int j = 0; j < MINE; ++j) {
-            if (j * AW / DT != x) continue;
-            const int d = j * AW % DT + warp;
-            const float lo = e ? uacc[j].y : uacc[j].x, hi = e ? uacc[j].w : uacc[j].z;
-            if (direct) {
-              from_float(none ? 0.0f : __fdiv_rn(lo, UL[x][e]), op[d * 16]);
-              from_float(none ? 0.0f : __fdiv_rn(hi, UL[x][e]), op[d * 16 + 8]);
-            } else {
-              dst[d * 16] = lo;
-              dst[d * 16 + 8] = hi;
-            }
-          }
-          if (warp == 0 && g8 == 0) {
-            if (!direct) ml[slot * (NT * 8) + r] = make_float2(UM[x][e], UL[x][e]);
-            else if (P.lse) P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(UM[x][e], UL[x][e]);
+        for (int j = 0; j < MINE; ++j) {
+          const int d = j * AW + w;
+          const float lo = e ? uacc[j].y : uacc[j].x, hi = e ? uacc[j].w : uacc[j].z;
+          if (direct) {
+            from_float(none ? 0.0f : __fdiv_rn(lo, UL[e]), op[d * 16]);
+            from_float(none ? 0.0f : __fdiv_rn(hi, UL[e]), op[d * 16 + 8]);
+          } else {
+            dst[d * 16] = lo;
+            dst[d * 16 + 8] = hi;
           }
         }
+        if (w == 0 && g8 == 0) {
+          if (!direct) ml[slot * (NT * 8) + r] = make_float2(UM[e], UL[e]);
+          else if (P.lse) P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(UM[e], UL[e]);
+        }
+      }
     }
     fresh_unit = true;
     fresh_group = group_ends;
@@ -933,7 +929,6 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 
 constexpr int JW = 16;                   // warps of a join CTA, and chains of the tree
 constexpr int JB = 4;                    // chains of a block
-constexpr int JR = 2;                    // rows that a warp joins at once
 
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, a chain folds its groups in order, a block its four chains,
@@ -962,8 +957,8 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
   }
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
+template <class T, int D, int JR>        // JR: rows that a warp joins at once
+__global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
   constexpr int E = D / 32;
   __shared__ int64_t scan[JW * 32 + 1];
   __shared__ float2 chain_ml[JW][JR];
@@ -972,125 +967,129 @@ __global__ void __launch_bounds__(JW * 32) join_kernel(const AttnParams P, int t
   const int HT = P.c.kv_heads * P.tiles;
   const int blocks = (min(tile_rows, P.rows) + JR - 1) / JR;
 
-  // ---- before the units are done: where everything is.  An item is rows [r, r + JR) of
-  // an entry (a sequence, kv head and tile), and `width` warps'
-  const int64_t it = static_cast<int64_t>(blockIdx.x) * (JW / width) + warp / width;
-  const int w0 = warp % width;           // this warp's first chain
   const bool chainwise = P.groups <= width || width == JW;
-  const bool mine = it < items;
-  const int64_t entry = mine ? it / blocks : 0;
-  const int r0 = static_cast<int>(it - entry * blocks) * JR;
-  const int b = static_cast<int>(entry / HT), ht = static_cast<int>(entry - static_cast<int64_t>(b) * HT);
+  const int w0 = warp % width;           // this warp's first chain
   const int64_t total = unit_sums<JW * 32>(P, scan);
-  const RunOf runs(static_cast<uint32_t>(total * HT), WORKERS);
-  const Seq s = load_seq(P, b);
-  const uint32_t u0 = static_cast<uint32_t>(units_before<JW * 32>(P, scan, b) * HT) + static_cast<uint32_t>(ht) * s.nu;
-  const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
-  const bool direct = s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
-  const bool work = mine && !(direct && s.nnew == P.c.n);
-  if (mine && !s.ok && ht == 0 && r0 == 0 && w0 == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!__syncthreads_or(work)) return;
+  const RunOf runs(static_cast<uint32_t>(total * HT), P.workers);
+  bool waited = false;
+  for (int64_t round = blockIdx.x; round * (JW / width) < items; round += gridDim.x) {
+    // ---- where everything is (the first time before the units are done).  An item is rows
+    // [r, r + JR) of an entry (a sequence, kv head and tile), and `width` warps'
+    const int64_t it = round * (JW / width) + warp / width;
+    const bool mine = it < items;
+    const int64_t entry = mine ? it / blocks : 0;
+    const int r0 = static_cast<int>(it - entry * blocks) * JR;
+    const int b = static_cast<int>(entry / HT), ht = static_cast<int>(entry - static_cast<int64_t>(b) * HT);
+    const Seq s = load_seq(P, b);
+    const uint32_t u0 = static_cast<uint32_t>(units_before<JW * 32>(P, scan, b) * HT) + static_cast<uint32_t>(ht) * s.nu;
+    const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
+    const bool direct = s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
+    const bool work = mine && !(direct && s.nnew == P.c.n);
+    if (mine && !s.ok && ht == 0 && r0 == 0 && w0 == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+    if (!__syncthreads_or(work)) continue;
 
-  // ---- this warp's chains, in order
-  const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
-  JoinRow<D> acc[JR], blk[JR];
-  if (work && !direct) {
-    const int chains = chainwise ? 1 : JW / width;
-    for (int c = w0 * chains; c < (w0 + 1) * chains && c <= glast; ++c) {     // (chainwise: chain w0)
-      JoinRow<D> chain[JR];
-      for (int g = c; g <= glast; g += JW) {
-        if (g >= gs && g < gl) {
-          g += (gl - g + JW - 1) / JW * JW;
-          if (g > glast) break;
+    // ---- this warp's chains, in order
+    const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
+    JoinRow<D> acc[JR], blk[JR];
+    if (work && !direct) {
+      const int chains = chainwise ? 1 : JW / width;
+      for (int c = w0 * chains; c < (w0 + 1) * chains && c <= glast; ++c) {     // (chainwise: chain w0)
+        JoinRow<D> chain[JR];
+        for (int g = c; g <= glast; g += JW) {
+          if (g >= gs && g < gl) {
+            g += (gl - g + JW - 1) / JW * JW;
+            if (g > glast) break;
+          }
+          const int f = s.first(g), e = s.past(g);
+          if (f >= e) continue;
+          const uint32_t ua = u0 + f;
+          // one part, where one run holds the group, or its units
+          const bool whole = runs.start(runs.of(ua) + 1) >= u0 + e;
+          const int parts = whole ? 1 : e - f;
+          const float2* ml = whole ? P.group_ml : P.unit_ml;
+          const float* po = whole ? P.group_o : P.unit_o;
+          float2 h[GROUP][JR];
+          float v[GROUP][JR][E];
+#pragma unroll
+          for (int k = 0; k < GROUP; ++k) {
+            int64_t at = entry * P.groups + g;
+            if (!whole) {
+              const uint32_t w = runs.of(min(ua + k, u0 + e - 1));
+              at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + s.unit(min(f + k, e - 1)) % GROUP;
+            }
+            at = at * tile_rows + r0;
+            // (past the last part: its place again)
+#pragma unroll
+            for (int j = 0; j < JR; ++j) {
+              h[k][j] = ml[at + j];
+              load_row<E>(po + (at + j) * D + lane * E, v[k][j]);
+            }
+          }
+          JoinRow<D> inner[JR];
+#pragma unroll
+          for (int k = 0; k < GROUP; ++k)
+            if (k < parts) {
+#pragma unroll
+              for (int j = 0; j < JR; ++j) inner[j].add(h[k][j].x, h[k][j].y, v[k][j]);
+            }
+#pragma unroll
+          for (int j = 0; j < JR; ++j) chain[j].add(inner[j]);
         }
-        const int f = s.first(g), e = s.past(g);
-        if (f >= e) continue;
-        const uint32_t ua = u0 + f;
-        // one part, where one run holds the group, or its units
-        const bool whole = runs.start(runs.of(ua) + 1) >= u0 + e;
-        const int parts = whole ? 1 : e - f;
-        const float2* ml = whole ? P.group_ml : P.unit_ml;
-        const float* po = whole ? P.group_o : P.unit_o;
-        float2 h[GROUP][JR];
-        float v[GROUP][JR][E];
 #pragma unroll
-        for (int k = 0; k < GROUP; ++k) {
-          int64_t at = entry * P.groups + g;
-          if (!whole) {
-            const uint32_t w = runs.of(min(ua + k, u0 + e - 1));
-            at = static_cast<int64_t>(w) * (2 * GROUP) + (runs.start(w) >= ua ? 0 : GROUP) + s.unit(min(f + k, e - 1)) % GROUP;
-          }
-          at = at * tile_rows + r0;
-          // (past the last part: its place again)
-#pragma unroll
-          for (int j = 0; j < JR; ++j) {
-            h[k][j] = ml[at + j];
-            load_row<E>(po + (at + j) * D + lane * E, v[k][j]);
-          }
-        }
-        JoinRow<D> inner[JR];
-#pragma unroll
-        for (int k = 0; k < GROUP; ++k)
-          if (k < parts) {
-#pragma unroll
-            for (int j = 0; j < JR; ++j) inner[j].add(h[k][j].x, h[k][j].y, v[k][j]);
-          }
-#pragma unroll
-        for (int j = 0; j < JR; ++j) chain[j].add(inner[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < JR; ++j) {
-        if (chainwise) {
-          acc[j] = chain[j];
-        } else {
-          blk[j].add(chain[j]);
-          if (c % JB == JB - 1 || c == glast) {
-            acc[j].add(blk[j]);
-            blk[j] = JoinRow<D>();
+        for (int j = 0; j < JR; ++j) {
+          if (chainwise) {
+            acc[j] = chain[j];
+          } else {
+            blk[j].add(chain[j]);
+            if (c % JB == JB - 1 || c == glast) {
+              acc[j].add(blk[j]);
+              blk[j] = JoinRow<D>();
+            }
           }
         }
       }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < JR; ++j) {
-    if (lane == 0) chain_ml[warp][j] = make_float2(acc[j].M, acc[j].L);
+    for (int j = 0; j < JR; ++j) {
+      if (lane == 0) chain_ml[warp][j] = make_float2(acc[j].M, acc[j].L);
 #pragma unroll
-    for (int e = 0; e < E; ++e) chain_o[warp][j][lane * E + e] = acc[j].o[e];
-  }
-  __syncthreads();
-  if (!work) return;
-  // ---- the item's warps in order, and the result: a row to a warp
-  for (int j = w0; j < JR; j += width) {
-    const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
-    if (row >= P.rows || (direct && i < s.nnew)) continue;
-    JoinRow<D> all, part;
-    for (int c = 0; c < width; ++c) {
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = chain_o[warp - w0 + c][j][lane * E + e];
-      const float2 h = chain_ml[warp - w0 + c][j];
-      if (!chainwise) {
-        all.add(h.x, h.y, v);
-        continue;
-      }
-      part.add(h.x, h.y, v);
-      if (c % JB == JB - 1 || c == width - 1) {
-        all.add(part);
-        part = JoinRow<D>();
-      }
+      for (int e = 0; e < E; ++e) chain_o[warp][j][lane * E + e] = acc[j].o[e];
     }
-    const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
-    const bool query = i < s.nnew;
-    const float nan = __int_as_float(0x7fc00000);
-    T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
+    __syncthreads();
+    if (!work) continue;
+    // ---- the item's warps in order, and the result: a row to a warp
+    for (int j = w0; j < JR; j += width) {
+      const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
+      if (row >= P.rows || (direct && i < s.nnew)) continue;
+      JoinRow<D> all, part;
+      for (int c = 0; c < width; ++c) {
+        float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      from_float(!s.ok ? nan : !query || all.L == 0.0f ? 0.0f : __fdiv_rn(all.o[e], all.L), op[e]);
-    if (P.lse && lane == 0)
-      P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] =
-          !s.ok ? nan : !query ? -INFINITY : lse_of<T>(all.M, all.L);
+        for (int e = 0; e < E; ++e) v[e] = chain_o[warp - w0 + c][j][lane * E + e];
+        const float2 h = chain_ml[warp - w0 + c][j];
+        if (!chainwise) {
+          all.add(h.x, h.y, v);
+          continue;
+        }
+        part.add(h.x, h.y, v);
+        if (c % JB == JB - 1 || c == width - 1) {
+          all.add(part);
+          part = JoinRow<D>();
+        }
+      }
+      const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
+      const bool query = i < s.nnew;
+      const float nan = __int_as_float(0x7fc00000);
+      T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        from_float(!s.ok ? nan : !query || all.L == 0.0f ? 0.0f : __fdiv_rn(all.o[e], all.L), op[e]);
+      if (P.lse && lane == 0)
+        P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] =
+            !s.ok ? nan : !query ? -INFINITY : lse_of<T>(all.M, all.L);
+    }
   }
 }
 
@@ -1183,14 +1182,18 @@ Layout layout_of(int64_t B, int64_t n, int64_t kv_heads, int64_t group, int64_t 
 
 // Function attributes are set once per device and kernel.
 template <class K>
-rlk_status allow_smem(K kernel, int bytes, bool (&done)[64]) {
+rlk_status allow_smem(K kernel, int bytes, int regs, bool (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
   if (dev >= 0 && dev < 64 && done[dev]) return RLK_OK;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return fail(RLK_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  cudaFuncAttributes attr{};
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "function attributes: %s", cudaGetErrorString(e));
+  // (with fewer, the working warps would wait for registers without end)
+  if (attr.numRegs != regs) return fail(RLK_ECUDA, "the kernel was built for %d registers, not %d", attr.numRegs, regs);
   if (dev >= 0 && dev < 64) done[dev] = true;
   return RLK_OK;
 }
@@ -1232,9 +1235,9 @@ rlk_status map_cache(CUtensorMap* map, const AttnParams& P, const void* base, in
 }
 
 template <class T, int D, int NT>
-rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
+rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   static bool done[64] = {};
-  rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, done);
+  rlk_status s = allow_smem(attn_kernel<T, D, NT>, Shape<D, NT>::SMEM, Shape<D, NT>::REGS, done);
   if (s != RLK_OK) return s;
   AttnMaps maps;
   constexpr bool bf16 = sizeof(T) == 2 && Elem<T>::EXP == 0x7F807F80u;
@@ -1242,20 +1245,22 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
     if ((s = map_cache(&maps.k, P, P.c.k, D, bf16)) != RLK_OK) return s;
     if ((s = map_cache(&maps.v, P, P.c.v, D, bf16)) != RLK_OK) return s;
   }
-  attn_kernel<T, D, NT><<<WORKERS, ATHREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
+  P.workers = Shape<D, NT>::WORKERS;
+  attn_kernel<T, D, NT><<<P.workers, Shape<D, NT>::THREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  // the join is launched while the units are at work, and waits for them
-  const int tile_rows = NT * 8, blocks = ((tile_rows < P.rows ? tile_rows : P.rows) + JR - 1) / JR;
-  const int64_t items = P.B * P.c.kv_heads * P.tiles * blocks;
-  // a chain to a warp, as far as one round of CTAs (one per SM) has the warps
+  // the join is launched while the units are at work, and waits for them.  A chain to a
+  // warp, as far as one round of CTAs (one per SM) has the warps; two rows to a warp, unless
+  // it has all their chains and there is room for a row to a warp in one round
+  const int tile_rows = NT * 8, rows = tile_rows < P.rows ? tile_rows : P.rows;
+  const int64_t entries = P.B * P.c.kv_heads * P.tiles, pairs = entries * ((rows + 1) / 2);
   int width = 1;
   while (width < JW && width < P.groups) width *= 2;
-  if (items * width > NUM_SMS * JW) width = width > JB && items * JB <= NUM_SMS * JW ? JB : 1;
-  const int64_t ctas = (items * width + JW - 1) / JW;
-  if (ctas >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n * q_heads is too large for one call");
+  if (pairs * width > NUM_SMS * JW) width = width > JB && pairs * JB <= NUM_SMS * JW ? JB : 1;
+  const bool single = width == 1 && entries * rows <= 2 * NUM_SMS * JW;
+  const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? 2 : 1);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
   cfg.blockDim = dim3(JW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -1263,7 +1268,7 @@ rlk_status launch_attn(const AttnParams& P, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, P, tile_rows, width, items);
+  e = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1> : join_kernel<T, D, 2>, P, tile_rows, width, items);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
