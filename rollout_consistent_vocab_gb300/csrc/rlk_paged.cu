@@ -45,35 +45,56 @@ struct AppendParams {
   const uint4* vsrc;
   rlk_bth_strides ks, vs;       // in 16-byte units
   int row16;                    // 16-byte pieces of a head row
-  int64_t total;                // B * n * kv_heads * row16
+  int pieces;                   // ... of a token
+  int per;                      // tokens of a block
+  int64_t tokens;               // B * n
 };
 
-// One thread per 16-byte piece of a new token's head row, keys and values.
-__global__ void append_kernel(const AppendParams P) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (t >= P.total) return;
-  const int piece = static_cast<int>(t % P.row16);
-  int64_t rest = t / P.row16;
-  const int h = static_cast<int>(rest % P.c.kv_heads);
-  rest /= P.c.kv_heads;
-  const int i = static_cast<int>(rest % P.c.n);
-  const int b = static_cast<int>(rest / P.c.n);
-  int len, nnew;
-  const bool first = piece == 0 && h == 0;
-  if (!seq_lens(P.c, b, len, nnew)) {
-    if (first && i == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    return;
+// A block copies the head rows of `per` tokens, a thread two pieces of 16 bytes of
+// the keys and of the values at once: all its loads are out before its first store.
+constexpr int APPEND_THREADS = 256, APPEND_PIECES = 2;
+__global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams P) {
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
+  const uint32_t n = P.c.n, b0 = static_cast<uint32_t>(t0 / n), i0 = static_cast<uint32_t>(t0 - static_cast<int64_t>(b0) * n);
+  const uint32_t tokens = static_cast<uint32_t>(min(static_cast<int64_t>(P.per), P.tokens - t0));
+  const uint32_t all = tokens * P.pieces;
+  for (uint32_t e0 = threadIdx.x; e0 < all; e0 += APPEND_THREADS * APPEND_PIECES) {
+    int64_t at[APPEND_PIECES];
+    bool there[APPEND_PIECES];
+    uint4 k[APPEND_PIECES], v[APPEND_PIECES];
+#pragma unroll
+    for (int j = 0; j < APPEND_PIECES; ++j) {
+      const uint32_t e = e0 + j * APPEND_THREADS;
+      there[j] = false;
+      if (e >= all) continue;
+      const uint32_t tok = e / P.pieces, h = (e - tok * P.pieces) / P.row16, piece = e % P.row16;
+      const uint32_t up = i0 + tok, b = b0 + up / n;
+      const int i = static_cast<int>(up % n);
+      const bool first = piece == 0 && h == 0;
+      int len, nnew;
+      if (!seq_lens(P.c, static_cast<int>(b), len, nnew)) {
+        if (first && i == 0 && P.c.err) atomicAdd(P.c.err, 1);
+        continue;
+      }
+      if (i >= nnew) continue;
+      const int pos = len - nnew + i, place = pos / P.c.page_size;
+      const int page = P.c.table[b * P.c.table_stride + place];
+      if (page < 0 || page >= P.c.num_pages) {
+        if (first && P.c.err) atomicAdd(P.c.err, 1);
+        continue;
+      }
+      at[j] = (page * P.c.page_stride + (pos - place * P.c.page_size) * P.c.token_stride + h * P.c.head_stride) / 8 + piece;
+      there[j] = true;
+      k[j] = __ldcs(P.ksrc + b * P.ks.batch + i * P.ks.token + h * P.ks.head + piece);
+      v[j] = __ldcs(P.vsrc + b * P.vs.batch + i * P.vs.token + h * P.vs.head + piece);
+    }
+#pragma unroll
+    for (int j = 0; j < APPEND_PIECES; ++j) {
+      if (!there[j]) continue;
+      reinterpret_cast<uint4*>(const_cast<void*>(P.c.k))[at[j]] = k[j];
+      reinterpret_cast<uint4*>(const_cast<void*>(P.c.v))[at[j]] = v[j];
+    }
   }
-  if (i >= nnew) return;
-  const int pos = len - nnew + i;
-  const int page = P.c.table[b * P.c.table_stride + pos / P.c.page_size];
-  if (page < 0 || page >= P.c.num_pages) {
-    if (first && P.c.err) atomicAdd(P.c.err, 1);
-    return;
-  }
-  const int64_t at = (page * P.c.page_stride + (pos % P.c.page_size) * P.c.token_stride + h * P.c.head_stride) / 8 + piece;
-  reinterpret_cast<uint4*>(const_cast<void*>(P.c.k))[at] = P.ksrc[b * P.ks.batch + i * P.ks.token + h * P.ks.head + piece];
-  reinterpret_cast<uint4*>(const_cast<void*>(P.c.v))[at] = P.vsrc[b * P.vs.batch + i * P.vs.token + h * P.vs.head + piece];
 }
 
 // ------------------------------------------------------------ attention
@@ -1301,10 +1322,12 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
   P.ks = {k_strides->batch / 8, k_strides->token / 8, k_strides->head / 8};
   P.vs = {v_strides->batch / 8, v_strides->token / 8, v_strides->head / 8};
   P.row16 = cache->head_dim / 8;
-  P.total = cache->B * cache->n * cache->kv_heads * P.row16;
-  const int64_t blocks = (P.total + 255) / 256;
+  P.pieces = cache->kv_heads * P.row16;
+  P.per = APPEND_THREADS * APPEND_PIECES / P.pieces > 0 ? APPEND_THREADS * APPEND_PIECES / P.pieces : 1;
+  P.tokens = cache->B * cache->n;
+  const int64_t blocks = (P.tokens + P.per - 1) / P.per;
   if (blocks >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n * kv_heads is too large for one call");
-  append_kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  append_kernel<<<static_cast<unsigned>(blocks), APPEND_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(P);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
