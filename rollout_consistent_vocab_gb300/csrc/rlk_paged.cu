@@ -126,7 +126,7 @@ constexpr int SL = 32;
 constexpr int HALF = SL / 2;
 template <int D, int NT>
 struct Shape {
-  static constexpr int CTAS = NT <= 2 ? 2 : 1;               // per SM
+  static constexpr int CTAS = NT == 1 ? 2 : 1;               // per SM
   static constexpr int WORKERS = NUM_SMS * CTAS;
   static constexpr int THREADS = (NT + 1) * AW * 32;
   // Registers of a thread: as many at the launch as an SM has for its CTAs, then what
@@ -138,7 +138,7 @@ struct Shape {
   static constexpr int PANEL = HALF * 128;
   static constexpr int KEYS = D / 64 * PANEL;
   static constexpr int STAGE = 2 * KEYS;
-  static constexpr int STAGES = CTAS == 1 ? 5 * 128 / D : D == 128 ? 3 : NT == 1 ? 6 : 5;
+  static constexpr int STAGES = NT > 1 ? 5 * 128 / D : D == 128 ? 3 : 6;
   static constexpr int SLOTS = D / 16;                       // fragments (four floats a thread) of a warp's result
   static constexpr int PASSES = D == 128 && NT % 2 == 0 ? 2 : 1;
   static constexpr int XCH = SLOTS / PASSES * AW * 512;      // ... of 8 rows, exchanged in so many passes
@@ -425,22 +425,27 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
   }
 }
 // the four working warps of the tile's rows 8 x .. 8 x + 7
-__device__ __forceinline__ void rows_sync(int x) { asm volatile("bar.sync %0, %1;" ::"r"(x + 1), "n"(AW * 32) : "memory"); }
+template <int NT>
+__device__ __forceinline__ void rows_sync(int x) {
+  if (NT <= 1 || (NT == 2 && x == 0)) asm volatile("bar.sync 1, %0;" ::"n"(AW * 32) : "memory");
+  else if (NT == 2) asm volatile("bar.sync 2, %0;" ::"n"(AW * 32) : "memory");
+  else asm volatile("bar.sync %0, %1;" ::"r"(x + 1), "n"(AW * 32) : "memory");
+}
 
 // A place in a worker's run: the sequence, kv head and tile, the unit in the
-// sequence's list, the slice in the unit.
+// sequence's list.
 struct Place {
   Seq s;
-  int b, head, tile, li, slice;
+  int b, head, tile, li;
   int left;                              // units of the run from this one on
 };
-// A warp's first slice of the unit from p.slice on that some new token sees, or false.
-__device__ __forceinline__ bool seek_slice(const AttnParams& P, Place& p) {
-  for (; p.slice < UNIT / SL; p.slice += AW) {
-    const int t0 = p.s.unit(p.li) * UNIT + p.slice * SL;
-    if (t0 < p.s.len && (t0 + SL > p.s.low || t0 < P.sinks)) return true;
-  }
-  return false;
+// The slices of a unit that some new token sees, by bits; a lane's are every fourth.
+__device__ __forceinline__ uint32_t slices_of(const AttnParams& P, const Place& p, int lane) {
+  constexpr int N = UNIT / SL;
+  const int t = p.s.unit(p.li) * UNIT;
+  const int end = min(N, (p.s.len - t + SL - 1) / SL), from = min(N, max(0, p.s.low - t) / SL);
+  const int sinks = min(N, (max(0, P.sinks - t) + SL - 1) / SL);
+  return ((1u << end) - 1u) & (((1u << N) - (1u << from)) | ((1u << sinks) - 1u)) & (0x1111u << lane);
 }
 // The next unit of the run; false at its end.
 __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
@@ -477,12 +482,14 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings' front held the block sums
   int page = 0, place = 0;
   bool seen = false;
+  uint32_t slices = slices_of(P, p, (threadIdx.x >> 5) % AW);
   auto seek = [&]() {
-    while (!seek_slice(P, p)) {
+    while (slices == 0) {
       if (!next_unit(P, p)) return false;
-      p.slice = (threadIdx.x >> 5) % AW;
+      slices = slices_of(P, p, (threadIdx.x >> 5) % AW);
     }
-    const int t = p.s.unit(p.li) * UNIT + p.slice * SL + lane;
+    const int t = p.s.unit(p.li) * UNIT + (__ffs(slices) - 1) * SL + lane;
+    slices &= slices - 1;
     seen = t < p.s.len && (t >= p.s.low || t < P.sinks);
     uint32_t n = __umulhi(static_cast<uint32_t>(t), P.page_magic);
     place = static_cast<int>(static_cast<uint32_t>(t) - n * static_cast<uint32_t>(P.c.page_size));
@@ -502,7 +509,6 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
     const bool copies = speaks && at >= 0 && at < P.c.num_pages;
     const bool bad = __any_sync(0xffffffffu, speaks && !copies);
     const uint32_t boxes = __ballot_sync(0xffffffffu, copies);
-    p.slice += AW;
     more = seek();
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
@@ -580,7 +586,6 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     cons.head = ht / P.tiles;
     cons.tile = ht - cons.head * P.tiles;
     cons.li = static_cast<int>(rest - static_cast<int64_t>(ht) * s.nu);
-    cons.slice = warp % AW;
   }
   const int w = warp % AW, x = warp / AW;      // the lane; the working warp's rows, 8 x .. 8 x + 7 of a tile
   const uint32_t ring = smem_addr(smem_raw) + w * (S_::STAGES * S_::STAGE);
@@ -608,49 +613,53 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
   uint2* const qsm = reinterpret_cast<uint2*>(smem_raw + S_::Q_AT) + x * KK * 32 + lane;       // [KK][thread]
   float o[DT][4], m[2], l[2];
   float4 gacc[MINE];
-  bool fresh_unit = true, fresh_head = true, fresh_group = true, folding = false, head_part = false, unit_bad = false, idle = false;
+  bool fresh_group = true, folding = false, head_part = false, idle = false;
+  int row0 = 0;
   uint32_t at = start;                   // the unit's number in the batch
+  // the queries of a kv head and tile, as B operands: loaded, and where the tile's warps share them, put down
+  uint32_t qr[S_::QS ? KK / AW : 1][2];
+  auto fetch_queries = [&]() {
+    row0 = (cons.tile * NT + x) * 8;
+    idle = row0 >= P.rows || query_of(P, row0) >= cons.s.nnew;
+    const int row = row0 + g8, i = query_of(P, row);
+    const bool real = row < P.rows && i < cons.s.nnew;
+    const T* qp = static_cast<const T*>(P.q) + cons.b * P.qs.batch + i * P.qs.token +
+                  (cons.head * P.group + (row - i * P.group)) * P.qs.head + t4 * 2;
+#pragma unroll
+    for (int k = 0; k < KK / (S_::QS ? AW : 1); ++k) {
+      const int c = (S_::QS ? k * AW + w : k) * 16;
+      const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + c)) ^ P.q_sign : 0u;
+      const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + c + 8)) ^ P.q_sign : 0u;
+      if constexpr (S_::QS) qr[k][0] = lo, qr[k][1] = hi;
+      else qf[k][0] = lo, qf[k][1] = hi;
+    }
+  };
+  auto put_queries = [&]() {
+#pragma unroll
+    for (int k = 0; k < KK / AW; ++k) qsm[(k * AW + w) * 32] = make_uint2(qr[k][0], qr[k][1]);
+  };
+  fetch_queries();
+  if constexpr (S_::QS) {
+    put_queries();
+    rows_sync<NT>(x);
+  }
   for (;;) {
     const int u = cons.s.unit(cons.li), g = u / GROUP;
-    const int row0 = (cons.tile * NT + x) * 8;
-    if (fresh_head) {
-      // the queries of this kv head and tile, as B operands
-      const T* qb = static_cast<const T*>(P.q) + cons.b * P.qs.batch + cons.head * P.group * P.qs.head;
-      idle = row0 >= P.rows || query_of(P, row0) >= cons.s.nnew;
-      const int row = row0 + g8, i = query_of(P, row);
-      const bool real = row < P.rows && i < cons.s.nnew;
-      const T* qp = qb + i * P.qs.token + (row - i * P.group) * P.qs.head + t4 * 2;
-      if (S_::QS) rows_sync(x);          // every warp is done with the head before
-#pragma unroll
-      for (int k = 0; k < KK; ++k) {
-        if (S_::QS && k % AW != w) continue;
-        const uint32_t lo = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.q_sign : 0u;
-        const uint32_t hi = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.q_sign : 0u;
-        if constexpr (S_::QS) qsm[k * 32] = make_uint2(lo, hi);
-        else qf[k][0] = lo, qf[k][1] = hi;
-      }
-      if (S_::QS) rows_sync(x);
-      fresh_head = false;
-    }
-    if (fresh_unit && fresh_group) {
+    if (fresh_group) {
       const int f = cons.s.first(g), e = cons.s.past(g);
       folding = cons.li == f && e - cons.li <= cons.left;
       head_part = start >= at - (cons.li - f);
 #pragma unroll
       for (int j = 0; j < MINE; ++j) gacc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    if (fresh_unit) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
-      m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
-      unit_bad = false;
-      fresh_unit = false;
-      cons.slice = w;
-    }
-
-    if (seek_slice(P, cons)) {
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+    m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
+    bool unit_bad = false;
+#pragma unroll 1
+    for (uint32_t slices = slices_of(P, cons, w); slices != 0; slices &= slices - 1) {
       // ---- one slice: its two halves, when they have landed
       uint32_t sk[2], done[2];
 #pragma unroll
@@ -662,8 +671,7 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       }
       unit_bad |= dead || bad_slice[w][number & 7] != 0;
       ++number;
-      const int t0 = u * UNIT + cons.slice * SL;
-      cons.slice += AW;
+      const int t0 = u * UNIT + (__ffs(slices) - 1) * SL;
       if (idle) {                        // no query among the warp's rows
         if (lane == 0) mbar_arrive(done[0]), mbar_arrive(done[1]);
         continue;
@@ -820,8 +828,17 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       }
       __syncwarp();                      // the stages may be filled again
       if (lane == 0) mbar_arrive(done[0]), mbar_arrive(done[1]);
-      continue;
     }
+
+    // ---- where the unit's result goes; on to the next unit, whose queries come meanwhile
+    const bool group_ends = cons.li + 1 == cons.s.past(g), store = !folding || group_ends;
+    const bool direct = folding && cons.s.past(g) - cons.s.first(g) == cons.s.nu;
+    const int64_t slot = folding ? (static_cast<int64_t>(cons.b) * HT + cons.head * P.tiles + cons.tile) * P.groups + g
+                                 : static_cast<int64_t>(me) * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
+    const int was_b = cons.b, was_head = cons.head, was_row0 = row0, was_nnew = cons.s.nnew;
+    const bool head_ends = cons.li + 1 == cons.s.nu, more = next_unit(P, cons);
+    if (head_ends && more) fetch_queries();
+    ++at;
 
     // ---- the unit's result: the lanes' shares brought to one maximum and summed in order
 #pragma unroll
@@ -842,14 +859,16 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     constexpr int PER_PASS = MINE / S_::PASSES;
 #pragma unroll
     for (int pass = 0; pass < S_::PASSES; ++pass) {
-      if (pass > 0) rows_sync(x);
+      if (pass > 0) rows_sync<NT>(x);
 #pragma unroll
       for (int f = 0; f < PER_PASS * AW; ++f) {
         const int d = pass * PER_PASS * AW + f;
         xch[(f * AW + w) * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
       }
-      rows_sync(x);
+      rows_sync<NT>(x);
       if (pass == 0) {
+        if constexpr (S_::QS)
+          if (head_ends && more) put_queries();        // every warp is done with the head before
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float2 h[AW];
@@ -882,15 +901,9 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
         uacc[pass * PER_PASS + j] = v;
       }
     }
-    rows_sync(x);                        // the shares may be written again
+    rows_sync<NT>(x);                        // the shares may be written again
 
     // ---- into the group, where this run holds all of it; otherwise out
-    const bool head_ends = cons.li + 1 == cons.s.nu;
-    const bool group_ends = cons.li + 1 == cons.s.past(g);
-    bool store = true, direct = false;
-    int64_t slot = static_cast<int64_t>(me) * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
-    float2* ml = P.unit_ml;
-    float* po = P.unit_o;
     if (folding) {
       Factors f[2];
 #pragma unroll
@@ -905,20 +918,17 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
         fold4(gacc[j], uacc[j], f[0], f[1]);
         uacc[j] = gacc[j];
       }
-      store = group_ends;
-      direct = cons.s.past(g) - cons.s.first(g) == cons.s.nu;
-      slot = (static_cast<int64_t>(cons.b) * HT + cons.head * P.tiles + cons.tile) * P.groups + g;
-      ml = P.group_ml;
-      po = P.group_o;
     }
     if (store) {
+      float2* const ml = folding ? P.group_ml : P.unit_ml;
+      float* const po = folding ? P.group_o : P.unit_o;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = x * 8 + 2 * t4 + e, row = row0 + 2 * t4 + e, i = query_of(P, row);
-        if (row >= P.rows || i >= cons.s.nnew) continue;
+        const int r = x * 8 + 2 * t4 + e, row = was_row0 + 2 * t4 + e, i = query_of(P, row);
+        if (row >= P.rows || i >= was_nnew) continue;
         const bool none = UL[e] == 0.0f;
-        const int hq = cons.head * P.group + (row - i * P.group);
-        T* op = static_cast<T*>(P.out) + cons.b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
+        const int hq = was_head * P.group + (row - i * P.group);
+        T* op = static_cast<T*>(P.out) + was_b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
         float* dst = po + (slot * (NT * 8) + r) * D + g8;
 #pragma unroll
         for (int j = 0; j < MINE; ++j) {
@@ -934,15 +944,12 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
         }
         if (w == 0 && g8 == 0) {
           if (!direct) ml[slot * (NT * 8) + r] = make_float2(UM[e], UL[e]);
-          else if (P.lse) P.lse[(static_cast<int64_t>(cons.b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(UM[e], UL[e]);
+          else if (P.lse) P.lse[(static_cast<int64_t>(was_b) * P.c.n + i) * P.q_heads + hq] = lse_of<T>(UM[e], UL[e]);
         }
       }
     }
-    fresh_unit = true;
     fresh_group = group_ends;
-    fresh_head = head_ends;
-    ++at;
-    if (!next_unit(P, cons)) break;
+    if (!more) break;
   }
 }
 
