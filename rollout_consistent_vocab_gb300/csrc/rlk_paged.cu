@@ -819,11 +819,14 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            uint32_t a[4];
-            ldsm_t(a, sk[y] + vswz[d % 4] + d / 4 * S_::PANEL);
-            E::mma(o[d], a, pf[y][2], pf[y][3]);
-            E::mma(o[d], a, pf[y][0], pf[y][1]);
+          for (int d = 0; d < DT; d += 4) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) ldsm_t(a[z], sk[y] + vswz[z] + d / 4 * S_::PANEL);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) E::mma(o[d + z], a[z], pf[y][2], pf[y][3]);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) E::mma(o[d + z], a[z], pf[y][0], pf[y][1]);
           }
       }
       __syncwarp();                      // the stages may be filled again
