@@ -176,6 +176,29 @@ def test_same_bits_in_any_batch_and_as_drafts():
         assert torch.equal(o, out) and torch.equal(z, lse)
 
 
+@pytest.mark.parametrize("n,group", [(1, 8), (3, 3), (2, 8), (1, 17), (4, 6), (5, 5), (4, 8), (11, 3), (9, 5), (1, 64)])
+@pytest.mark.parametrize("dim,dtype", [(128, "bf16"), (64, "f16")])
+def test_every_number_of_query_rows(n, group, dim, dtype):
+    """8 to 64 rows of a kv head, in tiles of 8, 16, 24 and 32, some of them without a query."""
+    lens = [n, 40 + n, 530, 1100]
+    new = [n, max(1, n // 2), 0, n]
+    c = make(lens, n, 2 * group, 2, dim, 16, dtype, seed=n * group)
+    out, lse = run(c, new)
+    compare(c, out, lse, new, dtype)
+    for b, i in ((0, n - 1), (1, 0), (3, n // 2)):             # decoded alone: the same bits
+        o, z = pkg.paged_attention(c["q"][b:b + 1, i:i + 1], c["k"], c["v"], c["table"][b:b + 1],
+                                   i32([lens[b] - new[b] + 1 + i]))
+        assert i >= new[b] or (torch.equal(o[0, 0], out[b, i]) and torch.equal(z[0, 0], lse[b, i]))
+    # an infinite value among the new tokens: it reaches the queries at and after it, and only them
+    t = lens[3] - 1 - n // 2
+    c["v"][int(c["table"][3, t // 16]), t % 16, 1] = math.inf
+    got, gl = run(c, new)
+    assert torch.equal(got[:3], out[:3]) and torch.equal(gl, lse)
+    first = n - 1 - n // 2
+    assert torch.equal(got[3, :first], out[3, :first]) and torch.equal(got[3, first:, :group], out[3, first:, :group])
+    assert torch.all(got[3, first:, group:] == math.inf)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_bad_values_in_masked_places_stay_there(dim):
     # a drafted token with NaN key and infinite value: only the queries that see it are NaN
