@@ -114,16 +114,19 @@ verify_draw_kernel(const DrawParams P) {
   __shared__ unsigned long long round_mass[ROUNDS];
   __shared__ unsigned long long shard_mass[2][NSHARD];
   __shared__ uint16_t list[SHARD_CHUNKS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const int r = static_cast<int>(cluster_rank());
   const int64_t b = blockIdx.x / NSHARD;
   const int n = P.ver.n;
+  // what the pass does not write is here before it is done
+  const int num_in = P.ver.num ? P.ver.num[b] : n;
+  const uint32_t accept0 = lane < n ? P.accept[b * n + lane] : 0u, draw = P.draw[b];
+  const float tau = P.tau_arr ? P.tau_arr[b] : P.tau_s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const VerifyMsg* rec = P.ver.rec + b * (n + 1);
   const VerifyMsg* recq = P.draft ? P.ver.rec_draft + b * n : nullptr;
 
   // ---- the first place that is not an accepted draft (every warp, the same)
-  const int num_in = P.ver.num ? P.ver.num[b] : n;
   bool bad = num_in < 0 || num_in > n;
   const int num = bad ? 0 : num_in;
   int a = num;
@@ -131,7 +134,7 @@ verify_draw_kernel(const DrawParams P) {
     const int i = i0 + lane;
     bool go_on = true;
     if (i < num) {
-      const float u = static_cast<float>(P.accept[b * n + i] >> 8) * 5.9604644775390625e-8f;
+      const float u = static_cast<float>((i0 == 0 ? accept0 : P.accept[b * n + i]) >> 8) * 5.9604644775390625e-8f;
       const bool ok = (rec[i].flags & VER_OK) && (!recq || (recq[i].flags & VER_OK));
       const float q = recq ? recq[i].p_t : 1.0f;
       go_on = ok && __fmul_rn(u, q) < rec[i].p_t;
@@ -194,7 +197,6 @@ verify_draw_kernel(const DrawParams P) {
   for (int i = tid; i < ROUNDS; i += VT) round_mass[i] = 0ull;
   __syncthreads();
   Masses m{};
-  const float tau = P.tau_arr ? P.tau_arr[b] : P.tau_s;
   m.M = rr.M;
   m.c = __fdiv_rn(LOG2E, tau);
   const float vmin = rr.min_key <= KEY_NEG_INF ? -INFINITY : key_value(rr.min_key);
@@ -256,7 +258,7 @@ verify_draw_kernel(const DrawParams P) {
   }
 
   // ---- the shard, the round, the chunk and the column that hold the draw
-  const unsigned long long t = scale_draw(P.draw[b], total);
+  const unsigned long long t = scale_draw(draw, total);
   if (t < prefix || t - prefix >= mine) return;      // another CTA's
   unsigned long long left = t - prefix;
   int round = 0;
