@@ -52,6 +52,9 @@ struct AppendParams {
 
 // A block copies the head rows of `per` tokens, a thread two pieces of 16 bytes of
 // the keys and of the values at once: all its loads are out before its first store.
+// Bound by memory: 16 x 2048 tokens (ragged) of 8 heads of 128 elements, 252 MB read
+// and written, 0.043 ms = 5.8 TB/s; with one piece to a thread and 64-bit places
+// 0.048 ms, with four pieces 0.043 ms, with eight 0.053 ms.
 constexpr int APPEND_THREADS = 256, APPEND_PIECES = 2;
 __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams P) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
@@ -113,7 +116,24 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // holds all of a group folds it itself, otherwise the units' results go to the
 // workspace and the join folds them, with the same arithmetic.  So no result
 // depends on the batch.
+//
+// What bounds it.  One new token: memory.  64 sequences of up to 8192 tokens, 32 query
+// heads on 8 of 128 elements, 0.69 GB of keys and values: 0.125 ms = 5.5 TB/s; 4 of up
+// to 131071, 1.28 GB: 0.206 ms = 6.2 TB/s.  Several new tokens (128 sequences of up to
+// 4096, 5 each, 0.65 GB): 0.172 ms = 3.8 TB/s, bound by the latency of the working
+// warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500).  A
+// window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.058 ms =
+// 2.3 TB/s, where the units are few and their ends count.
+//
+// Why mma.sync.  With 8 query rows to a tile the products are small: K and V pass
+// once through shared memory into registers, and a score never leaves the warp that
+// takes its exponential.  The same tree on tcgen05 (128 tokens as rows, 16 to 64 query
+// rows as columns, scores and results in tensor memory) took 0.172 ms where this takes
+// 0.125, 0.243 for 0.206, 0.330 for 0.172 and 0.125 for 0.058: the weights' way through
+// tensor memory and back lies between the two products, and its code (96 to 198 KB
+// against 73 to 82) ran into the instruction cache.
 
+// (units of 2048 tokens: 0.137 ms for 0.125 in the first case above, 0.274 for 0.253 in the third)
 constexpr int UNIT = 512;                // tokens of a unit
 constexpr int GROUP = 4;                 // units of a group
 constexpr int AW = 4;                    // lanes of a CTA: every fourth slice of a unit is one's
@@ -122,6 +142,9 @@ constexpr int NUM_SMS = 152;
 // Rows of a tile: the n * (q_heads / kv_heads) query rows of a kv head, in tiles of
 // 8 NT.  A lane is a copying warp and NT working warps of 8 rows each, which share
 // what it copies: slices of 32 tokens, in halves of 16, STAGES halves in its ring.
+// (One working warp with all the rows: 0.223 ms for 0.185 with 20 rows.)  Two CTAs to an
+// SM with 8 rows; from 16 rows on one, with the longer rings (16 rows, 64 sequences of
+// up to 4096 tokens: 0.097 ms with one CTA, 0.123 with two).
 constexpr int SL = 32;
 constexpr int HALF = SL / 2;
 template <int D, int NT>
@@ -1282,7 +1305,9 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them.  A chain to a
   // warp, as far as one round of CTAs (one per SM) has the warps; two rows to a warp, unless
-  // it has all their chains and there is room for a row to a warp in one round
+  // it has all their chains and there is room for a row to a warp in one round (the window's
+  // 4096 rows: 0.065 ms the call with two, 0.060 with one; the drafts' 20480, which take
+  // rounds: 0.188 with two, 0.195 with one)
   const int tile_rows = NT * 8, rows = tile_rows < P.rows ? tile_rows : P.rows;
   const int64_t entries = P.B * P.c.kv_heads * P.tiles, pairs = entries * ((rows + 1) / 2);
   int width = 1;

@@ -11,6 +11,12 @@
 // exact whatever their order: P_j = exp((x_j - M) / tau) 2^44, rounded, for the
 // support's columns.  A residual takes q_j in the same unit, Q_j = q_j Z_S 2^44
 // rounded, and the mass is max(P_j - Q_j, 0).
+//
+// The pass is the sampler's, and bound as that is: by the exchanges between a row's
+// eight CTAs.  128 sequences with 4 drafts of a draft model (1152 rows, 0.35 GB, top-k
+// 128): 0.0925 ms = 3.8 TB/s, the pass 0.083 of it.  The draw is latency: a thread takes
+// one marked chunk, and CTAs of 128 threads, many to an SM, wait beside each other
+// (with 512 threads and every chunk of the shard looked at: 0.150 ms the call).
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
