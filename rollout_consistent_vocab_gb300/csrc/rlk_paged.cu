@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // What bounds it.  One new token: memory.  64 sequences of up to 8192 tokens, 32 query
 // heads on 8 of 128 elements, 0.69 GB of keys and values: 0.125 ms = 5.5 TB/s; 4 of up
 // to 131071, 1.28 GB: 0.206 ms = 6.2 TB/s.  Several new tokens (128 sequences of up to
-// 4096, 5 each, 0.65 GB): 0.172 ms = 3.8 TB/s, bound by the latency of the working
+// 4096, 5 each, 0.65 GB): 0.169 ms = 3.8 TB/s, bound by the latency of the working
 // warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500).  A
 // window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.058 ms =
 // 2.3 TB/s, where the units are few and their ends count.
@@ -144,7 +144,7 @@ constexpr int NUM_SMS = 152;
 // what it copies: slices of 32 tokens, in halves of 16, STAGES halves in its ring.
 // (One working warp with all the rows: 0.223 ms for 0.185 with 20 rows.)  Two CTAs to an
 // SM with 8 rows; from 16 rows on one, with the longer rings (16 rows, 64 sequences of
-// up to 4096 tokens: 0.097 ms with one CTA, 0.123 with two).
+// up to 4096 tokens: 0.093 ms with one CTA, about 0.12 with two).
 constexpr int SL = 32;
 constexpr int HALF = SL / 2;
 template <int D, int NT>
@@ -952,7 +952,7 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       for (int e = 0; e < 2; ++e) {
         const int r = x * 8 + 2 * t4 + e, row = was_row0 + 2 * t4 + e, i = query_of(P, row);
         if (row >= P.rows || i >= was_nnew) continue;
-        const bool none = UL[e] == 0.0f;
+        const float inv = UL[e] == 0.0f ? 0.0f : __frcp_rn(UL[e]);       // (nothing seen: o is 0)
         const int hq = was_head * P.group + (row - i * P.group);
         T* op = static_cast<T*>(P.out) + was_b * P.os.batch + i * P.os.token + hq * P.os.head + g8;
         float* dst = po + (slot * (NT * 8) + r) * D + g8;
@@ -961,8 +961,8 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
           const int d = j * AW + w;
           const float lo = e ? uacc[j].y : uacc[j].x, hi = e ? uacc[j].w : uacc[j].z;
           if (direct) {
-            from_float(none ? 0.0f : __fdiv_rn(lo, UL[e]), op[d * 16]);
-            from_float(none ? 0.0f : __fdiv_rn(hi, UL[e]), op[d * 16 + 8]);
+            from_float(__fmul_rn(lo, inv), op[d * 16]);
+            from_float(__fmul_rn(hi, inv), op[d * 16 + 8]);
           } else {
             dst[d * 16] = lo;
             dst[d * 16 + 8] = hi;
@@ -1135,11 +1135,12 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
       }
       const int hq = (ht / P.tiles) * P.group + (row - i * P.group);
       const bool query = i < s.nnew;
+      const float inv = all.L == 0.0f ? 0.0f : __frcp_rn(all.L);
       const float nan = __int_as_float(0x7fc00000);
       T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        from_float(!s.ok ? nan : !query || all.L == 0.0f ? 0.0f : __fdiv_rn(all.o[e], all.L), op[e]);
+        from_float(!s.ok ? nan : !query ? 0.0f : __fmul_rn(all.o[e], inv), op[e]);
       if (P.lse && lane == 0)
         P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] =
             !s.ok ? nan : !query ? -INFINITY : lse_of<T>(all.M, all.L);
