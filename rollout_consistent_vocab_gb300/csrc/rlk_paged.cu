@@ -144,7 +144,7 @@ constexpr int NUM_SMS = 152;
 // what it copies: slices of 32 tokens, in halves of 16, STAGES halves in its ring.
 // (One working warp with all the rows: 0.223 ms for 0.185 with 20 rows.)  Two CTAs to an
 // SM with 8 rows; from 16 rows on one, with the longer rings (16 rows, 64 sequences of
-// up to 4096 tokens: 0.093 ms with one CTA, about 0.12 with two).
+// up to 4096 tokens: 0.089 ms with one CTA, about 0.12 with two).
 constexpr int SL = 32;
 constexpr int HALF = SL / 2;
 template <int D, int NT>
@@ -161,7 +161,8 @@ struct Shape {
   static constexpr int PANEL = HALF * 128;
   static constexpr int KEYS = D / 64 * PANEL;
   static constexpr int STAGE = 2 * KEYS;
-  static constexpr int STAGES = NT > 1 ? 5 * 128 / D : D == 128 ? 3 : 6;
+  // (as many as there is room for; with 10 of 64 elements 24 and 32 rows took half as long again, with 6 to 9 not)
+  static constexpr int STAGES = D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : NT == 1 ? 6 : 8;
   static constexpr int SLOTS = D / 16;                       // fragments (four floats a thread) of a warp's result
   static constexpr int PASSES = D == 128 && NT % 2 == 0 ? 2 : 1;
   static constexpr int XCH = SLOTS / PASSES * AW * 512;      // ... of 8 rows, exchanged in so many passes
