@@ -122,14 +122,14 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // to 131071, 1.28 GB: 0.206 ms = 6.2 TB/s.  Several new tokens (128 sequences of up to
 // 4096, 5 each, 0.65 GB): 0.169 ms = 3.8 TB/s, bound by the latency of the working
 // warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500).  A
-// window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.058 ms =
-// 2.3 TB/s, where the units are few and their ends count.
+// window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.051 ms =
+// 2.6 TB/s, where the units are few and their ends count.
 //
 // Why mma.sync.  With 8 query rows to a tile the products are small: K and V pass
 // once through shared memory into registers, and a score never leaves the warp that
 // takes its exponential.  The same tree on tcgen05 (128 tokens as rows, 16 to 64 query
 // rows as columns, scores and results in tensor memory) took 0.172 ms where this takes
-// 0.125, 0.243 for 0.206, 0.330 for 0.172 and 0.125 for 0.058: the weights' way through
+// 0.125, 0.243 for 0.206, 0.330 for 0.169 and 0.125 for 0.051: the weights' way through
 // tensor memory and back lies between the two products, and its code (96 to 198 KB
 // against 73 to 82) ran into the instruction cache.
 
@@ -161,7 +161,7 @@ struct Shape {
   static constexpr int PANEL = HALF * 128;
   static constexpr int KEYS = D / 64 * PANEL;
   static constexpr int STAGE = 2 * KEYS;
-  // (as many as there is room for; with 10 of 64 elements 24 and 32 rows took half as long again, with 6 to 9 not)
+  // (as many as there is room for; with 10 of 64 elements 24 and 32 rows took a fifth longer, with 6 to 9 not)
   static constexpr int STAGES = D == 128 ? (NT == 1 ? 3 : NT == 2 ? 6 : 5) : NT == 1 ? 6 : 8;
   static constexpr int SLOTS = D / 16;                       // fragments (four floats a thread) of a warp's result
   static constexpr int PASSES = D == 128 && NT % 2 == 0 ? 2 : 1;
@@ -797,6 +797,8 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 #pragma unroll 1
           for (int r = 0; r < SL; ++r) {
             const int t = t0 + r;
+            // (what lies in a place that nobody sees is of no account, whatever it is)
+            if (t >= cons.s.len || (t < cons.s.low && t >= P.sinks)) continue;
             const uint32_t row = (r < HALF ? sk[0] : sk[1]) + S_::KEYS + (r & (HALF - 1)) * 128;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
