@@ -467,8 +467,8 @@ struct Place {
 __device__ __forceinline__ uint32_t slices_of(const AttnParams& P, const Place& p, int lane) {
   constexpr int N = UNIT / SL;
   const int t = p.s.unit(p.li) * UNIT;
-  const int end = min(N, (p.s.len - t + SL - 1) / SL), from = min(N, max(0, p.s.low - t) / SL);
-  const int sinks = min(N, (max(0, P.sinks - t) + SL - 1) / SL);
+  const int end = (min(p.s.len - t, UNIT) + SL - 1) / SL, from = min(N, max(0, p.s.low - t) / SL);
+  const int sinks = (min(max(0, P.sinks - t), UNIT) + SL - 1) / SL;
   return ((1u << end) - 1u) & (((1u << N) - (1u << from)) | ((1u << sinks) - 1u)) & (0x1111u << lane);
 }
 // The next unit of the run; false at its end.

@@ -128,6 +128,35 @@ def test_window_and_sinks(window, sinks, dim, dtype):
     compare(c, out, lse, [6, 6], dtype, window=window, sinks=sinks)
 
 
+def test_the_largest_windows_and_sinks_hide_nothing():
+    c = make([1, 33, 700, 1300], 2, 8, 2, 64, 16, "bf16", seed=21, width=90)
+    c["lens"][0] = 2                                           # (both tokens in the first page)
+    c["k"][c["table"][0, 0].long(), 1] = 0.5
+    c["v"][c["table"][0, 0].long(), 1] = 0.25
+    out, lse = run(c)
+    top = 2**31 - 1
+    for window, sinks in ((top, 0), (top, top), (1, top), (5, 5000), (5, top)):
+        o, z = run(c, window=window, sinks=sinks)
+        assert torch.equal(o, out) and torch.equal(z, lse), (window, sinks)
+
+
+def test_garbage_in_unused_places_counts_for_nothing():
+    """Infinities and NaN past the end, before the window and between sinks and window."""
+    for dim, dtype in ((128, "bf16"), (64, "f16")):
+        c = make([77, 1500, 600], 3, 8, 2, dim, 24, dtype, seed=22)
+        clean = {k: c[k].clone() for k in ("k", "v")}
+        used = torch.zeros(c["k"].shape[:2], dtype=torch.bool, device=DEV)
+        for b, t in enumerate(c["lens"].tolist()):
+            for j in range(t):
+                used[c["table"][b, j // 24].long(), j % 24] = True
+        clean["k"][~used], clean["v"][~used] = 0.0, 0.0
+        z = dict(c, **clean)
+        for kw in ({}, {"window": 100, "sinks": 5}):
+            a, b = run(c, **kw), run(z, **kw)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            assert torch.isfinite(a[0]).all()
+
+
 def test_long_sequence_and_a_wide_table():
     c = make([40001, 20000, 3], 2, 4, 1, 64, 48, "bf16", seed=5, width=3000)
     out, lse = run(c)
