@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // What bounds it.  One new token: memory.  64 sequences of up to 8192 tokens, 32 query
 // heads on 8 of 128 elements, 0.69 GB of keys and values: 0.125 ms = 5.5 TB/s; 4 of up
 // to 131071, 1.28 GB: 0.206 ms = 6.2 TB/s.  Several new tokens (128 sequences of up to
-// 4096, 5 each, 0.65 GB): 0.169 ms = 3.8 TB/s, bound by the latency of the working
+// 4096, 5 each, 0.65 GB): 0.172 ms = 3.8 TB/s, bound by the latency of the working
 // warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500).  A
 // window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.051 ms =
 // 2.6 TB/s, where the units are few and their ends count.
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // once through shared memory into registers, and a score never leaves the warp that
 // takes its exponential.  The same tree on tcgen05 (128 tokens as rows, 16 to 64 query
 // rows as columns, scores and results in tensor memory) took 0.172 ms where this takes
-// 0.125, 0.243 for 0.206, 0.330 for 0.169 and 0.125 for 0.051: the weights' way through
+// 0.125, 0.243 for 0.206, 0.330 for 0.172 and 0.125 for 0.051: the weights' way through
 // tensor memory and back lies between the two products, and its code (96 to 198 KB
 // against 73 to 82) ran into the instruction cache.
 
@@ -219,6 +219,7 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
   Seq s;
   s.ok = seq_lens(P.c, b, s.len, s.nnew);
+  if (!s.ok) s.len = s.nnew = 0;
   s.low = s.us = s.ul = s.nu = 0;
   if (s.ok && s.nnew > 0) {
     if (P.window > 0) {
@@ -410,9 +411,6 @@ __device__ __forceinline__ uint32_t lds16(uint32_t at) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory");
-}
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -467,7 +465,7 @@ struct Place {
 __device__ __forceinline__ uint32_t slices_of(const AttnParams& P, const Place& p, int lane) {
   constexpr int N = UNIT / SL;
   const int t = p.s.unit(p.li) * UNIT;
-  const int end = (min(p.s.len - t, UNIT) + SL - 1) / SL, from = min(N, max(0, p.s.low - t) / SL);
+  const int end = (min(max(0, p.s.len - t), UNIT) + SL - 1) / SL, from = min(N, max(0, p.s.low - t) / SL);
   const int sinks = (min(max(0, P.sinks - t), UNIT) + SL - 1) / SL;
   return ((1u << end) - 1u) & (((1u << N) - (1u << from)) | ((1u << sinks) - 1u)) & (0x1111u << lane);
 }
@@ -479,10 +477,12 @@ __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
     if (++p.tile == P.tiles) p.tile = 0, ++p.head;
     if (p.head == P.c.kv_heads) {
       p.head = 0;
+      // (where the lengths changed under the call there may be none left: then units without
+      // tokens, so that every warp of a CTA goes through as many as the others)
       do {
-        if (++p.b >= P.B) return false;  // (the lengths changed under the call)
+        p.b = min(p.b + 1, static_cast<int>(P.B) - 1);
         p.s = load_seq(P, p.b);
-      } while (p.s.nu == 0);
+      } while (p.s.nu == 0 && p.b + 1 < P.B);
     }
   }
   return true;
@@ -602,14 +602,14 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       run += s.nu;
       s = load_seq(P, ++b);
     }
-    if (s.nu == 0) return;               // (the lengths changed under the call)
+    // (within bounds, should the lengths have changed)
     const int64_t rest = static_cast<int64_t>(start) - run * HT;
-    const int ht = static_cast<int>(rest / s.nu);
+    const int ht = min(static_cast<int>(rest / max(s.nu, 1)), HT - 1);
     cons.s = s;
     cons.b = b;
     cons.head = ht / P.tiles;
     cons.tile = ht - cons.head * P.tiles;
-    cons.li = static_cast<int>(rest - static_cast<int64_t>(ht) * s.nu);
+    cons.li = max(0, min(static_cast<int>(rest - static_cast<int64_t>(ht) * s.nu), s.nu - 1));
   }
   const int w = warp % AW, x = warp / AW;      // the lane; the working warp's rows, 8 x .. 8 x + 7 of a tile
   const uint32_t ring = smem_addr(smem_raw) + w * (S_::STAGES * S_::STAGE);
@@ -979,6 +979,14 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     }
     fresh_group = group_ends;
     if (!more) break;
+  }
+  // where a copy did not come in time, the CTA stays for the last ones, within limits
+  if (dead) {
+#pragma unroll 1
+    for (int i = 0; i < S_::STAGES; ++i) {
+      if (--use_stage < 0) use_stage = S_::STAGES - 1, use_phase ^= 1;
+      mbar_wait_phase(my_full + use_stage * 8, use_phase);
+    }
   }
 }
 
