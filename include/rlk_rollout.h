@@ -104,9 +104,10 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
  * sequence gets NaN in out and lse: for all its places if its lengths are at
  * fault (as in rlk_kv_append), for its places i < new_lens[b] if the page
  * number of a visible token is out of range.
- * Scores, softmax statistics and output sums are held in float32; the weights
- * exp(s_j - max) go into the product with V as the sum of two elements of the
- * cache's dtype (16 bits or more), and out is rounded once at the end. */
+ * Scores, softmax statistics and output sums are held in float32, and out is
+ * rounded once at the end.  The weights exp(s_j - max) go into the product with
+ * V as two elements of the cache's dtype: 16 bits in bf16, whatever their size;
+ * 22 bits in f16, but no finer than 2^-44 of the row's largest weight. */
 rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides,
                                int32_t q_heads, float scale, int32_t window, int32_t sinks, void* out,
                                const rlk_bth_strides* out_strides, float* out_lse, void* workspace,

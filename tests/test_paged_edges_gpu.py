@@ -1,0 +1,79 @@
+"""GPU: paged attention where single weights, values or lengths lie at the edge of their formats.
+
+Inputs, float64 results and tolerances as in test_paged_gpu.py; what a test adds to them
+is stated beside it.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rollout_consistent_vocab_gb300 as pkg
+from oracle import rollout as ro
+from test_paged_gpu import DEV, DT, U, i32, np64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from rollout_consistent_vocab_gb300.build import build_library
+    build_library()
+    pkg.load_library()
+
+
+def one_row(scores, values, dtype, dim=64, page=64):
+    """One query whose score of token j is scores[j] (scale 1), over values[j] in every place."""
+    n = len(scores)
+    pages = -(-n // page)
+    k = torch.zeros((pages * page, 1, dim), dtype=DT[dtype], device=DEV)
+    v = torch.full_like(k, math.nan)
+    k[:n, 0, 0] = torch.as_tensor(scores, device=DEV).to(DT[dtype])
+    v[:n, 0] = torch.as_tensor(values, device=DEV).to(DT[dtype])[:, None]
+    q = torch.zeros((1, 1, 1, dim), dtype=DT[dtype], device=DEV)
+    q[..., 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    out, lse = pkg.paged_attention(q, k.view(pages, page, 1, dim), v.view(pages, page, 1, dim), table, i32([n]), scale=1.0)
+    want, wl, (A, X) = ro.attend(np64(q)[0, 0, 0], np64(k)[:n, 0], np64(v)[:n, 0], 1.0)
+    ds = 2 * (dim + 4) * 2.0**-24 * X + 2.0**-18
+    tol = U[dtype] * np.abs(want) + (U[dtype] + ds) * A * (1 + 2.0**-7)
+    return np64(out)[0, 0, 0], want, tol, np64(v)[:n, 0]
+
+
+# f16: a weight is held to 22 bits, but to no less than 2^-44 of the row's largest
+STEP = 2.0**-44
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gap", [16.0, 20.75, 23.5, 27.0])
+@pytest.mark.parametrize("tokens", [40, 2000, 131071])
+def test_f16_weights_far_below_the_largest(tokens, gap, dim):
+    """A first token that takes all the weight and has no value: the result is the others'."""
+    rng = np.random.default_rng(tokens)
+    scores = np.concatenate([[0.0], -gap + rng.uniform(-0.5, 0.5, tokens - 1)])
+    values = np.concatenate([[0.0], rng.uniform(500.0, 1500.0, tokens - 1)])
+    got, want, tol, v = one_row(scores, values, "f16", dim)
+    tol = tol + 2.0**-24 + STEP * np.abs(v).sum(0)
+    assert np.all(np.abs(got - want) <= tol), (np.abs(got - want) / tol).max()
+
+
+def test_f16_values_near_the_largest_on_tokens_of_no_weight():
+    for gap in (25.0, 40.0, 60.0):
+        for n in (2, 33):
+            got, want, tol, v = one_row([0.0] + [-gap] * (n - 1), [1e-3] + [60000.0] * (n - 1), "f16")
+            tol = tol + 2.0**-24 + STEP * np.abs(v).sum(0)
+            assert np.all(np.abs(got - want) <= tol), (gap, n, got[0], want[0])
+
+
+def test_f16_infinite_values_in_the_middle_of_a_sequence():
+    """An infinite value that every query sees, at a token of ordinary weight."""
+    for at in (0, 1, 100, 700):
+        for bad in (math.inf, -math.inf):
+            values = np.ones(1500)
+            values[at] = bad
+            k = np.zeros(1500)
+            k[::3] = -3.0
+            got = one_row(k, values, "f16")[0]
+            assert np.all(got == bad), (at, bad, got[:4])
