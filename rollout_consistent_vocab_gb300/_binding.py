@@ -257,6 +257,21 @@ def _stream(stream):
     return raw(torch.cuda.current_device())
 
 
+def _new(shape, dtype, device, stream, returned=True):
+    """A tensor that a call on ``stream`` makes for itself.  It is that stream's own: its memory
+    is neither what other work on the current stream still uses, nor given to such work while
+    the call runs.  What the caller gets back is marked as used on the current stream too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and here != stream:
+        t.record_stream(here)
+    return t
+
+
 def _empty(T, dtype, like):
     return _torch().empty((T,), dtype=dtype, device=like.device)
 
@@ -929,18 +944,18 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
     shape = (B, n, heads, dim)
     qs = _bth(q, shape, k_cache.dtype, "q")
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _new(shape, q.dtype, q.device, stream)
         os_ = BTHStrides(n * heads * dim, heads * dim, dim)
     else:
         os_ = _bth(out, shape, q.dtype, "out")
     if out_lse is None:
-        out_lse = torch.empty((B, n, heads), dtype=torch.float32, device=q.device)
+        out_lse = _new((B, n, heads), torch.float32, q.device, stream)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
     need = paged_attention_workspace_bytes(B, n, heads, kv_heads, dim, c.max_pages * c.page_size) \
         if heads > 0 and heads % kv_heads == 0 else 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(need, torch.uint8, q.device, stream, returned=False)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
     check(lib.rlk_paged_attention(c, q.data_ptr(), qs, heads, dim ** -0.5 if scale is None else scale, window, sinks,
@@ -999,13 +1014,13 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
                                   (out_restr, (B, n + 1), torch.float32, "out_restr"),
                                   (out_full, (B, n + 1), torch.float32, "out_full")):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = _new(shape, dtype, dev, stream)
         elif t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
         outs.append(t)
     need = verify_workspace_bytes(B, n)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _new(need, torch.uint8, dev, stream, returned=False)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least verify_workspace_bytes(B, n) bytes")
     a = VerifyArgs(B, n, VOCAB_REAL, VOCAB_PADDED, logits.data_ptr() if B else None,
