@@ -272,8 +272,13 @@ def _new(shape, dtype, device, stream, returned=True):
     return t
 
 
-def _empty(T, dtype, like):
-    return _torch().empty((T,), dtype=dtype, device=like.device)
+def _elsewhere(stream) -> bool:
+    """Whether a call runs on another stream than the current one."""
+    return stream is not None and stream != _torch().cuda.current_stream(stream.device)
+
+
+def _empty(T, dtype, like, stream):
+    return _new((T,), dtype, like.device, stream)
 
 
 def logp_full(logits, target, temperature=1.0, *, out=None, err_count=None, stream=None):
@@ -281,7 +286,7 @@ def logp_full(logits, target, temperature=1.0, *, out=None, err_count=None, stre
     lib = load_library()
     torch = _torch()
     a = make_args(logits, target, temperature, 1.0, -1, err_count)
-    out = _empty(a.T, torch.float32, logits) if out is None else out
+    out = _empty(a.T, torch.float32, logits, stream) if out is None else out
     check(lib.rlk_logp_full(ctypes.byref(a), _ptr(out), _stream(stream)))
     return out
 
@@ -292,9 +297,9 @@ def logp_pair(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, out_full=
     lib = load_library()
     torch = _torch()
     a = make_args(logits, target, temperature, top_p, top_k, err_count)
-    out_full = _empty(a.T, torch.float32, logits) if out_full is None else out_full
-    out_restr = _empty(a.T, torch.float32, logits) if out_restr is None else out_restr
-    out_support = _empty(a.T, torch.int32, logits) if out_support is None else out_support
+    out_full = _empty(a.T, torch.float32, logits, stream) if out_full is None else out_full
+    out_restr = _empty(a.T, torch.float32, logits, stream) if out_restr is None else out_restr
+    out_support = _empty(a.T, torch.int32, logits, stream) if out_support is None else out_support
     check(lib.rlk_logp_pair(ctypes.byref(a), _ptr(out_full), _ptr(out_restr), _ptr(out_support),
                             _stream(stream)))
     return out_full, out_restr, out_support
@@ -306,8 +311,8 @@ def logp_restricted(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, out
     lib = load_library()
     torch = _torch()
     a = make_args(logits, target, temperature, top_p, top_k, err_count)
-    out = _empty(a.T, torch.float32, logits) if out is None else out
-    out_support = _empty(a.T, torch.int32, logits) if out_support is None else out_support
+    out = _empty(a.T, torch.float32, logits, stream) if out is None else out
+    out_support = _empty(a.T, torch.int32, logits, stream) if out_support is None else out_support
     check(lib.rlk_logp_restricted(ctypes.byref(a), _ptr(out), _ptr(out_support), _stream(stream)))
     return out, out_support
 
@@ -322,7 +327,7 @@ def logp_kl(logits, ref_logits, target, temperature=1.0, top_p=1.0, top_k=-1, *,
     a = make_args(logits, target, temperature, top_p, top_k, err_count)
     if ref_logits.dtype != torch.bfloat16 or ref_logits.shape[0] != a.T or ref_logits.stride(1) != 1:
         raise ValueError("ref_logits must be a bf16 [T, >=152576] tensor like logits")
-    outs = [o if o is not None else _empty(a.T, dt, logits) for o, dt in
+    outs = [o if o is not None else _empty(a.T, dt, logits, stream) for o, dt in
             ((out_full, torch.float32), (out_restr, torch.float32), (out_support, torch.int32),
              (out_full_ref, torch.float32), (out_kl, torch.float32))]
     check(lib.rlk_logp_kl(ctypes.byref(a), ref_logits.data_ptr() if a.T else None,
@@ -358,7 +363,7 @@ def logp_kl_host(logits, ref_logits, target, temperature=1.0, top_p=1.0, top_k=-
             ((out_full, torch.float32), (out_restr, torch.float32), (out_support, torch.int32),
              (out_full_ref, torch.float32), (out_kl, torch.float32))]
     if workspace is None:
-        workspace = torch.empty(logp_kl_host_workspace_bytes(a.T), dtype=torch.uint8, device=dev)
+        workspace = _new(logp_kl_host_workspace_bytes(a.T), torch.uint8, dev, stream, returned=False)
     if workspace.numel() * workspace.element_size() < logp_kl_host_workspace_bytes(a.T) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least logp_kl_host_workspace_bytes(T) bytes")
     check(lib.rlk_logp_kl_host(ctypes.byref(a), ref_logits.data_ptr() if a.T else None,
@@ -377,8 +382,8 @@ def logp_kl_ref(ref_logits, target, full_policy, temperature=1.0, *, out_full_re
     a = make_args(ref_logits, target, temperature, 1.0, -1, None)
     if full_policy.dtype != torch.float32 or full_policy.shape != (a.T,):
         raise ValueError("full_policy must be a float32 tensor of shape [T]")
-    out_full_ref = _empty(a.T, torch.float32, ref_logits) if out_full_ref is None else out_full_ref
-    out_kl = _empty(a.T, torch.float32, ref_logits) if out_kl is None else out_kl
+    out_full_ref = _empty(a.T, torch.float32, ref_logits, stream) if out_full_ref is None else out_full_ref
+    out_kl = _empty(a.T, torch.float32, ref_logits, stream) if out_kl is None else out_kl
     check(lib.rlk_logp_kl_ref(ctypes.byref(a), _ptr(full_policy), _ptr(out_full_ref), _ptr(out_kl),
                               _stream(stream)))
     return out_full_ref, out_kl
@@ -444,10 +449,10 @@ def logp_merge(maxes, sumexps, aux, target_logit, target, temperature=1.0, top_p
     tp, ts = _param(temperature, T, torch.float32, "temperature")
     pp, ps = _param(top_p, T, torch.float32, "top_p")
     kp, ks = _param(top_k, T, torch.int32, "top_k")
-    out_full = _empty(T, torch.float32, maxes) if out_full is None else out_full
+    out_full = _empty(T, torch.float32, maxes, stream) if out_full is None else out_full
     if counts is not None:
-        out_restr = _empty(T, torch.float32, maxes) if out_restr is None else out_restr
-        out_support = _empty(T, torch.int32, maxes) if out_support is None else out_support
+        out_restr = _empty(T, torch.float32, maxes, stream) if out_restr is None else out_restr
+        out_support = _empty(T, torch.int32, maxes, stream) if out_support is None else out_support
     nc = 0 if counts is None else counts.shape[0]
     check(lib.rlk_logp_merge(_ptr(maxes), _ptr(sumexps), _ptr(aux), _ptr(target_logit), T,
                              _ptr(target), tp, ts, pp, ps, kp, ks, _ptr(counts), nc,
@@ -503,6 +508,14 @@ def logp_sharded(shards, target, temperature=1.0, top_p=1.0, top_k=-1, *, restri
     resolved; without it such rows keep support -2.  Returns (full,) or
     (full, restricted, support)."""
     torch = _torch()
+    if _elsewhere(stream):                  # every part, and what it clears and allocates, in order there
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            outs = logp_sharded(shards, target, temperature, top_p, top_k, restricted=restricted,
+                                chunk_maxima=chunk_maxima, resolve=resolve, err_count=err_count)
+        for t in outs:
+            t.record_stream(here)
+        return outs
     if len(shards) != NUM_SHARDS:
         raise ValueError(f"expected {NUM_SHARDS} shard tensors")
     T = target.shape[0]
@@ -568,7 +581,7 @@ def logp_backward(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, grad_
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape [T]")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        out = torch.empty((a.T, VOCAB_PADDED), dtype=dtype, device=logits.device)
+        out = _new((a.T, VOCAB_PADDED), dtype, logits.device, stream)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.dim() != 2 or out.stride(1) != 1:
         raise ValueError("out must be a bf16 or float32 [T, >=152576] tensor with unit column stride")
     gd = RLK_GRAD_F32 if out.dtype == torch.float32 else RLK_GRAD_BF16
@@ -587,11 +600,11 @@ def logp_pair_save(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, out_
     lib = load_library()
     torch = _torch()
     a = make_args(logits, target, temperature, top_p, top_k, err_count)
-    out_full = _empty(a.T, torch.float32, logits) if out_full is None else out_full
-    out_restr = _empty(a.T, torch.float32, logits) if out_restr is None else out_restr
-    out_support = _empty(a.T, torch.int32, logits) if out_support is None else out_support
+    out_full = _empty(a.T, torch.float32, logits, stream) if out_full is None else out_full
+    out_restr = _empty(a.T, torch.float32, logits, stream) if out_restr is None else out_restr
+    out_support = _empty(a.T, torch.int32, logits, stream) if out_support is None else out_support
     if out_stats is None:
-        out_stats = torch.empty((a.T, 4), dtype=torch.float32, device=logits.device)
+        out_stats = _new((a.T, 4), torch.float32, logits.device, stream)
     check(lib.rlk_logp_pair_save(ctypes.byref(a), _ptr(out_full), _ptr(out_restr), _ptr(out_support),
                                  _ptr(out_stats), _stream(stream)))
     return out_full, out_restr, out_support, out_stats
@@ -611,7 +624,7 @@ def logp_backward_saved(logits, target, stats, temperature=1.0, *, grad_full=Non
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape [T]")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        out = torch.empty((a.T, VOCAB_PADDED), dtype=dtype, device=logits.device)
+        out = _new((a.T, VOCAB_PADDED), dtype, logits.device, stream)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.dim() != 2 or out.stride(1) != 1:
         raise ValueError("out must be a bf16 or float32 [T, >=152576] tensor with unit column stride")
     gd = RLK_GRAD_F32 if out.dtype == torch.float32 else RLK_GRAD_BF16
@@ -688,12 +701,12 @@ def sample(logits, temperature=1.0, top_p=1.0, top_k=-1, *, seed=0, counter=None
             raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor of shape [T]")
     if counter is None and uniform is None:
         raise ValueError("give counter (with seed) or uniform")
-    out_token = _empty(T, torch.int32, logits) if out_token is None else out_token
-    out_restr = _empty(T, torch.float32, logits) if out_restr is None else out_restr
-    out_full = _empty(T, torch.float32, logits) if out_full is None else out_full
-    out_support = _empty(T, torch.int32, logits) if out_support is None else out_support
+    out_token = _empty(T, torch.int32, logits, stream) if out_token is None else out_token
+    out_restr = _empty(T, torch.float32, logits, stream) if out_restr is None else out_restr
+    out_full = _empty(T, torch.float32, logits, stream) if out_full is None else out_full
+    out_support = _empty(T, torch.int32, logits, stream) if out_support is None else out_support
     if workspace is None:
-        workspace = torch.empty(sample_workspace_bytes(T), dtype=torch.uint8, device=logits.device)
+        workspace = _new(sample_workspace_bytes(T), torch.uint8, logits.device, stream, returned=False)
     if workspace.numel() * workspace.element_size() < sample_workspace_bytes(T) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least sample_workspace_bytes(T) bytes")
     check(lib.rlk_sample(ctypes.byref(a), int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(counter), _ptr(uniform),
@@ -724,9 +737,9 @@ def linear_logp(hidden, weight, target, temperature=1.0, *, out=None, workspace=
     if target.dtype != torch.int32 or target.shape != (T,) or not target.is_contiguous():
         raise ValueError("target must be a contiguous int32 tensor of shape [T]")
     tp, ts = _param(temperature, T, torch.float32, "temperature")
-    out = _empty(T, torch.float32, hidden) if out is None else out
+    out = _empty(T, torch.float32, hidden, stream) if out is None else out
     if workspace is None:
-        workspace = torch.empty(max(1, linear_workspace_bytes(T)), dtype=torch.uint8, device=hidden.device)
+        workspace = _new(max(1, linear_workspace_bytes(T)), torch.uint8, hidden.device, stream, returned=False)
     check(lib.rlk_linear_logp(hidden.data_ptr() if T else None, T, H, hidden.stride(0) if T else H,
                               weight.data_ptr(), weight.stride(0), _ptr(target), tp, ts, _ptr(out),
                               workspace.data_ptr(), _ptr(err_count), _stream(stream)))
@@ -756,12 +769,12 @@ def linear_logp_pair(hidden, weight, target, temperature=1.0, top_p=1.0, top_k=-
     tp, ts = _param(temperature, T, torch.float32, "temperature")
     pp, ps = _param(top_p, T, torch.float32, "top_p")
     kp, ks = _param(top_k, T, torch.int32, "top_k")
-    out_full = _empty(T, torch.float32, hidden) if out_full is None else out_full
-    out_restr = _empty(T, torch.float32, hidden) if out_restr is None else out_restr
-    out_support = _empty(T, torch.int32, hidden) if out_support is None else out_support
+    out_full = _empty(T, torch.float32, hidden, stream) if out_full is None else out_full
+    out_restr = _empty(T, torch.float32, hidden, stream) if out_restr is None else out_restr
+    out_support = _empty(T, torch.int32, hidden, stream) if out_support is None else out_support
     if workspace is None:
-        workspace = torch.empty(max(1, linear_pair_workspace_bytes(T)), dtype=torch.uint8,
-                                device=hidden.device)
+        workspace = _new(max(1, linear_pair_workspace_bytes(T)), torch.uint8, hidden.device, stream,
+                         returned=False)
     elif workspace.numel() * workspace.element_size() < linear_pair_workspace_bytes(T):
         raise ValueError("workspace must hold at least linear_pair_workspace_bytes(T) bytes")
     check(lib.rlk_linear_logp_pair(hidden.data_ptr() if T else None, T, H, hidden.stride(0) if T else H,
@@ -808,7 +821,7 @@ def sqnorm_finalize(bins, out=None, stream=None):
     """(sum of squares, norm) as a device float64 [2]."""
     lib = load_library()
     torch = _torch()
-    out = torch.empty(2, dtype=torch.float64, device=bins.device) if out is None else out
+    out = _new(2, torch.float64, bins.device, stream) if out is None else out
     check(lib.rlk_sqnorm_finalize(_ptr(bins), _ptr(out), _stream(stream)))
     return out
 
@@ -826,6 +839,13 @@ def grad_norm(tensors, *, distributed=False, group=None, bins=None, out=None, st
     the launch shape, or (with ``distributed``) the split across the ranks
     of ``group``.  Returns the device float64 [2] (sum of squares, norm)."""
     torch = _torch()
+    if _elsewhere(stream):                  # every part in order there, the clearing and the reduction too
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            got = grad_norm(tensors, distributed=distributed, group=group, bins=bins, out=out)
+        if out is None:
+            got.record_stream(here)
+        return got
     if isinstance(tensors, torch.Tensor):
         tensors = [tensors]
     tensors = list(tensors)

@@ -35,7 +35,60 @@ def verification():
     return lambda **kw: test_verify_gpu.run(c, 1.0, 0.95, 50, **kw), pkg.verify_workspace_bytes(5, 3)
 
 
-CALLS = [attention, verification]
+def _logits(T=6, seed=42):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = 4.0 * torch.randn((T, pkg.VOCAB_PADDED), generator=g, device=DEV)
+    return x.to(torch.bfloat16), torch.arange(T, dtype=torch.int32, device=DEV) * 1000
+
+
+def pair():
+    x, t = _logits()
+    return lambda **kw: pkg.logp_pair(x, t, 0.8, 0.9, 50, **kw), 256
+
+
+def backward():
+    x, t = _logits()
+    g = torch.linspace(-1.0, 1.0, 6, device=DEV)
+    return lambda **kw: pkg.logp_backward(x, t, 0.8, 0.9, 50, grad_full=g, grad_restr=g, **kw), 256
+
+
+def sampler():
+    x, t = _logits()
+    u = t * 12345                        # (made before the call: its stream does not wait for the current one)
+    return lambda **kw: pkg.sample(x, 0.8, 0.9, 50, uniform=u, **kw), pkg._binding.sample_workspace_bytes(6)
+
+
+def _head(H=128):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(43)
+    w, h = (0.3 * torch.randn((n, H), generator=g, device=DEV) for n in (pkg.VOCAB_PADDED, 6))
+    return h.to(torch.bfloat16), w.to(torch.bfloat16), torch.arange(6, dtype=torch.int32, device=DEV) * 1000
+
+
+def head():
+    h, w, t = _head()
+    return lambda **kw: pkg.linear_logp(h, w, t, 0.8, **kw), pkg._binding.linear_workspace_bytes(6)
+
+
+def head_pair():
+    h, w, t = _head()
+    return (lambda **kw: pkg.linear_logp_pair(h, w, t, 0.8, 0.9, 50, **kw),
+            pkg._binding.linear_pair_workspace_bytes(6))
+
+
+def sharded():
+    x, t = _logits()
+    shards = [x[:, r * pkg.SHARD_WIDTH:(r + 1) * pkg.SHARD_WIDTH].contiguous() for r in range(pkg.NUM_SHARDS)]
+    return lambda **kw: pkg.logp_sharded(shards, t, 0.8, 0.9, 50, **kw), 8 * 6 * 1024 * 4
+
+
+def norm():
+    x = [torch.linspace(-2.0, 3.0, n, device=DEV) for n in (1000, 77)]
+    return lambda **kw: pkg.grad_norm(x, **kw), 8 * pkg.NORM_BINS
+
+
+CALLS = [attention, verification, pair, backward, sampler, head, head_pair, sharded, norm]
 
 
 def outputs(got):
