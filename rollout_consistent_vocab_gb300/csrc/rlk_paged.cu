@@ -203,6 +203,9 @@ struct AttnMaps {
   CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
 };
 
+// Units of t tokens; t may be anything up to 2^31 - 1.
+__device__ __forceinline__ int units_of(int t) { return t / UNIT + (t % UNIT != 0); }
+
 // What of a sequence is visible to its new tokens: units [0, us) for the sinks
 // and [ul, ul + nu - us) up to the end.
 struct Seq {
@@ -225,9 +228,9 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
     if (P.window > 0) {
       s.low = max(0, s.len - s.nnew - P.window + 1);
       s.ul = s.low / UNIT;
-      s.us = min((min(P.sinks, s.len) + UNIT - 1) / UNIT, s.ul);
+      s.us = min(units_of(min(P.sinks, s.len)), s.ul);
     }
-    s.nu = s.us + (s.len + UNIT - 1) / UNIT - s.ul;
+    s.nu = s.us + units_of(s.len) - s.ul;
   }
   return s;
 }
@@ -755,18 +758,18 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
       // masks: the queries stand at p0 .. len - 1
       const int p0 = cons.s.len - cons.s.nnew;
       const bool masked = t0 + SL - 1 > p0 ||
-                          (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 + SL > P.sinks);
+                          (P.window > 0 && t0 <= cons.s.len - 1 - P.window && t0 > P.sinks - SL);
       uint32_t hidden = 0;               // bit 4 y + e (of the thread's scores)
       if (masked) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int pos = p0 + query_of(P, row0 + 2 * t4 + e);
+          const int i = query_of(P, row0 + 2 * t4 + e);        // at p0 + i, which 32 bits may not hold past the last token
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
               const int t = t0 + y * HALF + g8 + 8 * f;
-              if (t > pos || t >= cons.s.len || (P.window > 0 && t <= pos - P.window && t >= P.sinks)) {
+              if (t - p0 > i || t >= cons.s.len || (P.window > 0 && t - p0 <= i - P.window && t >= P.sinks)) {
                 s[y][2 * f + e] = -INFINITY;
                 hidden |= 1u << (y * 4 + 2 * f + e);
               }
@@ -843,8 +846,8 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
                 if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const int pos = p0 + query_of(P, row0 + 2 * t4 + e);
-                  if (t <= pos && !(P.window > 0 && t <= pos - P.window && t >= P.sinks)) o[d][2 * f + e] += E::value(bits);
+                  const int i = query_of(P, row0 + 2 * t4 + e);
+                  if (t - p0 <= i && !(P.window > 0 && t - p0 <= i - P.window && t >= P.sinks)) o[d][2 * f + e] += E::value(bits);
                 }
               }
           }

@@ -77,3 +77,47 @@ def test_f16_infinite_values_in_the_middle_of_a_sequence():
             k[::3] = -3.0
             got = one_row(k, values, "f16")[0]
             assert np.all(got == bad), (at, bad, got[:4])
+
+
+def test_the_longest_sequence():
+    """2^31 - 16 tokens, from one page that the table holds again and again."""
+    page, width, dim, n = 8176, 262657, 64, 2
+    length = page * width
+    assert length == 2**31 - 16
+    table = torch.zeros((1, width), dtype=torch.int32, device=DEV)
+    lens = i32([length])
+    g = torch.Generator(device=DEV)
+    g.manual_seed(30)
+    q = torch.randn((1, n, 2, dim), generator=g, device=DEV).to(torch.bfloat16)
+    k = torch.zeros((1, page, 1, dim), dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    for d in range(dim):
+        v[0, ::d + 2, 0, d] = 1.0
+    # all scores 0: the mean of the values.  Every partial sum is a whole number, exact in float32
+    # up to 2^24 of its units of 2048 and more
+    once = np64(v)[0, :, 0]
+    for kw in ({}, {"window": 5, "sinks": 2**31 - 1}):
+        out, lse = pkg.paged_attention(q, k, v, table, lens, **kw)
+        for i in range(n):
+            seen = length - n + 1 + i
+            want = (width * once.sum(0) - once[page - n + 1 + i:].sum(0)) / seen
+            assert np.all(np.abs(np64(out)[0, i] - want) <= (2 * U["bf16"] + 2.0**-20) * want)     # rounded once
+            assert np.all(np.abs(np64(lse)[0, i] - math.log(seen)) <= 2.0**-18 + 2.0**-23 * math.log(seen))
+    # a window at the end, and the first tokens
+    k.copy_(torch.randn(k.shape, generator=g, device=DEV))
+    v.copy_(torch.randn(v.shape, generator=g, device=DEV))
+    for window, sinks in ((1000, 4), (1, 0), (3000, 600)):
+        out, lse = pkg.paged_attention(q, k, v, table, lens, window=window, sinks=sinks)
+        for i in range(n):
+            pos = length - n + i
+            j = np.concatenate([np.arange(sinks), np.arange(pos - window + 1, pos + 1)]) % page
+            for h in range(2):
+                o, z, (A, X) = ro.attend(np64(q)[0, i, h], np64(k)[0, j, 0], np64(v)[0, j, 0], dim**-0.5)
+                ds = 2 * (dim + 4) * 2.0**-24 * X + 2.0**-18
+                tol = U["bf16"] * np.abs(o) + (U["bf16"] + ds) * A * (1 + 2.0**-7)
+                assert np.all(np.abs(np64(out)[0, i, h] - o) <= tol)
+                assert abs(float(lse[0, i, h]) - z) <= ds + 2.0**-23 * abs(z)
+    # the last token's place
+    new = torch.randn((1, 1, 1, dim), generator=g, device=DEV).to(torch.bfloat16)
+    pkg.kv_append(k, v, table, lens, new, -new)
+    assert torch.equal(k[0, page - 1, 0], new[0, 0, 0]) and torch.equal(v[0, page - 1, 0], -new[0, 0, 0])
