@@ -98,9 +98,10 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
  *     gives for max_tokens = max_pages * page_size, 16-byte aligned.  No
  *     contents are expected or kept; calls that overlap on the GPU need one
  *     each.
- * Places i >= new_lens[b], and queries that see no token, get out = 0 and
- * lse = -inf.  NaN and infinite keys, values or queries spread to the outputs
- * that see them only (the value of a masked token is never used).  A rejected
+ * Places i >= new_lens[b], and queries that see only tokens of score -inf, get
+ * out = 0 and lse = -inf.  NaN and infinite keys, values or queries spread to the
+ * outputs that see them only (the value of a masked token is never used; an
+ * infinite one at a weight that is 0 in float32 makes NaN).  A rejected
  * sequence gets NaN in out and lse: for all its places if its lengths are at
  * fault (as in rlk_kv_append), for its places i < new_lens[b] if the page
  * number of a visible token is out of range.

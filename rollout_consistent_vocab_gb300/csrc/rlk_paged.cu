@@ -324,10 +324,9 @@ __device__ __forceinline__ Factors fold_factors(float& M, float m) {
   M = mx;
   return f;
 }
-// (b = 0: the part weighs nothing beside what is there, or is left out; a is then 1)
-__device__ __forceinline__ float fold(float x, float part, Factors f) {
-  return f.b == 0.0f ? x : __fmaf_rn(part, f.b, __fmul_rn(x, f.a));
-}
+// (b = 0: the part weighs nothing beside what is there, or saw only scores of -inf; its sum
+// comes in all the same, so that values that are not finite are not lost)
+__device__ __forceinline__ float fold(float x, float part, Factors f) { return __fmaf_rn(part, f.b, __fmul_rn(x, f.a)); }
 // The part's maximum and sum into (M, L).
 __device__ __forceinline__ Factors add_part(float& M, float& L, float m, float l) {
   if (l == 0.0f) return Factors{1.0f, 0.0f};
@@ -908,10 +907,6 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int z = 4; z < 32; z <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], z);
-      if (l[e] == 0.0f) {                // nothing seen: no trace, whatever the values were
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d][e] = o[d][2 + e] = 0.0f;
-      }
       if (unit_bad) m[e] = 0.0f, l[e] = __int_as_float(0x7fc00000);
       if (g8 == 0) share[w][x * 8 + 2 * t4 + e] = make_float2(m[e], l[e]);
     }

@@ -24,7 +24,7 @@ def _library():
     pkg.load_library()
 
 
-def one_row(scores, values, dtype, dim=64, page=64):
+def row_of(scores, values, dtype, dim, page=64):
     """One query whose score of token j is scores[j] (scale 1), over values[j] in every place."""
     n = len(scores)
     pages = -(-n // page)
@@ -35,11 +35,22 @@ def one_row(scores, values, dtype, dim=64, page=64):
     q = torch.zeros((1, 1, 1, dim), dtype=DT[dtype], device=DEV)
     q[..., 0] = 1.0
     table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
-    out, lse = pkg.paged_attention(q, k.view(pages, page, 1, dim), v.view(pages, page, 1, dim), table, i32([n]), scale=1.0)
-    want, wl, (A, X) = ro.attend(np64(q)[0, 0, 0], np64(k)[:n, 0], np64(v)[:n, 0], 1.0)
+    got = pkg.paged_attention(q, k.view(pages, page, 1, dim), v.view(pages, page, 1, dim), table, i32([n]), scale=1.0)
+    return got, np64(q)[0, 0, 0], np64(k)[:n, 0], np64(v)[:n, 0]
+
+
+def attended(scores, values, dtype, dim=64):
+    (out, lse), _, _, _ = row_of(scores, values, dtype, dim)
+    return np64(out)[0, 0, 0], float(lse[0, 0, 0])
+
+
+def one_row(scores, values, dtype, dim=64):
+    """(result, float64 result, tolerance, values)"""
+    (out, _), q, k, v = row_of(scores, values, dtype, dim)
+    want, _, (A, X) = ro.attend(q, k, v, 1.0)
     ds = 2 * (dim + 4) * 2.0**-24 * X + 2.0**-18
     tol = U[dtype] * np.abs(want) + (U[dtype] + ds) * A * (1 + 2.0**-7)
-    return np64(out)[0, 0, 0], want, tol, np64(v)[:n, 0]
+    return np64(out)[0, 0, 0], want, tol, v
 
 
 # f16: a weight is held to 22 bits, but to no less than 2^-44 of the row's largest
@@ -121,3 +132,23 @@ def test_the_longest_sequence():
     new = torch.randn((1, 1, 1, dim), generator=g, device=DEV).to(torch.bfloat16)
     pkg.kv_append(k, v, table, lens, new, -new)
     assert torch.equal(k[0, page - 1, 0], new[0, 0, 0]) and torch.equal(v[0, page - 1, 0], -new[0, 0, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_values_that_are_not_finite_are_not_lost_for_their_weight(bad, dtype):
+    """At a token whose weight is 0 in float32, wherever it stands beside the weights that count."""
+    n = 9000
+    for low in (-400.0, -math.inf):
+        for at, heavy in ((0, 8999), (8999, 0), (600, 10), (10, 600), (3, 40), (40, 3), (2500, 100), (100, 2500), (33, 33 + 32)):
+            for every in (True, False):      # all the others as light, or only those around
+                scores = np.full(n, low) if every else np.zeros(n)
+                scores[at // 512 * 512:at // 512 * 512 + 512] = low
+                scores[heavy] = 0.0
+                values = np.ones(n)
+                clean, lse = attended(scores, values, dtype)
+                assert np.all(np.abs(clean - 1.0) <= 2 * U[dtype]), (low, at, heavy, every)
+                values[at] = bad
+                got, z = attended(scores, values, dtype)
+                assert not np.isfinite(got).any(), (low, at, heavy, every, got[:4])
+                assert z == lse
