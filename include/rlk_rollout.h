@@ -95,9 +95,9 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
  *   scale: finite.  window: 0 (off) or > 0.  sinks: >= 0, ignored without a
  *     window.
  *   workspace: device scratch of the size that rlk_paged_attention_workspace
- *     gives for max_tokens = max_pages * page_size, 16-byte aligned.  No
- *     contents are expected or kept; calls that overlap on the GPU need one
- *     each.
+ *     gives for max_tokens = max_pages * page_size, 16-byte aligned (NULL will
+ *     do where that is 0).  No contents are expected or kept; calls that
+ *     overlap on the GPU need one each.
  * Places i >= new_lens[b], and queries that see only tokens of score -inf, get
  * out = 0 and lse = -inf.  NaN and infinite keys, values or queries spread to the
  * outputs that see them only (the value of a masked token is never used; an

@@ -1433,7 +1433,6 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
   if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
   if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
   if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
-  if (!workspace) return fail(RLK_EINVAL, "workspace is NULL");
   if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
   const int group = q_heads / cache->kv_heads;
   const Tiling t = tiling_of(cache->n, group);
@@ -1442,6 +1441,7 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
     return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
   const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
                              static_cast<int64_t>(cache->max_pages) * cache->page_size);
+  if (!workspace && y.bytes > 0) return fail(RLK_EINVAL, "workspace is NULL");
   char* ws = static_cast<char*>(workspace);
   AttnParams P{};
   P.c = paged_params(cache);

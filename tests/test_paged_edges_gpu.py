@@ -152,3 +152,24 @@ def test_values_that_are_not_finite_are_not_lost_for_their_weight(bad, dtype):
                 got, z = attended(scores, values, dtype)
                 assert not np.isfinite(got).any(), (low, at, heavy, every, got[:4])
                 assert z == lse
+
+
+def test_a_page_table_without_pages():
+    """[B, 0]: every sequence is still empty."""
+    for pages in (4, 0):
+        k = torch.zeros((pages, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+        table = torch.zeros((3, 0), dtype=torch.int32, device=DEV)
+        q = torch.ones((3, 2, 8, 64), dtype=torch.bfloat16, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        pkg.kv_append(k, k, table, i32([0, 0, 0]), q[:, :, :2], q[:, :, :2], new_lens=i32([0, 0, 0]), err_count=err)
+        out, lse = pkg.paged_attention(q, k, k, table, i32([0, 0, 0]), new_lens=i32([0, 0, 0]), err_count=err)
+        assert not out.any() and torch.all(lse == -math.inf) and int(err) == 0
+        out, lse = pkg.paged_attention(q, k, k, table, i32([0, 1, 0]), new_lens=i32([0, 1, 0]), err_count=err)
+        assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all() and not out[[0, 2]].any() and int(err) >= 1
+
+
+def test_a_call_without_its_workspace_is_refused():
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+    q = torch.ones((1, 1, 8, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        pkg.paged_attention(q, k, k, i32([[0, 1]]), i32([3]), workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
