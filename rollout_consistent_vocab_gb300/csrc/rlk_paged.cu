@@ -469,20 +469,6 @@ __device__ __forceinline__ bool mbar_wait_phase(uint32_t bar, uint32_t parity) {
     if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
   return true;
 }
-// ... for a copying warp: it looks now and then, and leaves the issue slots to the
-// working ones.
-__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
-  unsigned long long t0 = 0;
-  for (;;) {
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    if (ok) return true;
-    if (t0 == 0) t0 = global_timer();
-    else if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
-    __nanosleep(100);
-  }
-}
 // the four working warps of the tile's rows 8 x .. 8 x + 7
 template <int NT>
 __device__ __forceinline__ void rows_sync(int x) {
