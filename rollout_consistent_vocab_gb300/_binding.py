@@ -210,16 +210,34 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _param(v, T, dtype, name):
-    """(device pointer or None, scalar) for a per-row tensor or a Python scalar."""
+def _param(v, T, dtype, name, dev=None):
+    """(device pointer or None, scalar) for a per-row tensor (on GPU ``dev``, if given) or a Python scalar."""
     torch = _torch()
     if isinstance(v, torch.Tensor):
         if v.dtype != dtype or v.dim() != 1 or v.shape[0] != T or not v.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{T}]")
         if not v.is_cuda:
             raise ValueError(f"{name} must live on the GPU")
+        if dev is not None:
+            _placed(v, dev, name)
         return v.data_ptr(), 0
     return None, v
+
+
+def _placed(t, dev, name):
+    """Refuses a tensor that is not on GPU ``dev``, where the call's others are."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on the GPU of the call's other tensors (cuda:{dev}), not on {t.device}")
+
+
+def _err_ptr(t, dev) -> int | None:
+    """A rollout call's counter of rejected sequences."""
+    if t is None:
+        return None
+    if t.dtype != _torch().int32 or t.numel() < 1:
+        raise ValueError("err_count must be an int32 tensor of one element")
+    _placed(t, dev, "err_count")
+    return t.data_ptr()
 
 
 def make_args(logits, target, temperature=1.0, top_p=1.0, top_k=-1, err_count=None) -> LogpArgs:
@@ -247,14 +265,20 @@ def make_args(logits, target, temperature=1.0, top_p=1.0, top_k=-1, err_count=No
     return a
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """The handle of the stream, or of the current one: on GPU ``dev``, if given."""
     if stream is not None:
+        if dev is not None and dev != stream.device.index:
+            raise ValueError(f"the call's tensors live on cuda:{dev}, its stream is {stream.device}'s")
         return stream.cuda_stream
     torch = _torch()
+    here = torch.cuda.current_device()
+    if dev is not None and dev != here:
+        raise ValueError(f"the call's tensors live on cuda:{dev}, the current GPU is cuda:{here}")
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the same handle, without building a Stream
     if raw is None:
         return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    return raw(here)
 
 
 def _new(shape, dtype, device, stream, returned=True):
@@ -864,10 +888,10 @@ def grad_norm(tensors, *, distributed=False, group=None, bins=None, out=None, st
 
 # ----------------------------------------------------------------- paged key-value cache
 
-def _bth(t, shape, dtype, name) -> BTHStrides:
+def _bth(t, shape, dtype, name, dev) -> BTHStrides:
     """Strides of a [B, n, heads, head_dim] tensor with unit stride in the last place."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on the cache's GPU, cuda:{dev}")
     sb, st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have unit stride in its last place")
@@ -882,8 +906,10 @@ def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> K
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim] tensors of one dtype")
     if strides[3] != 1 or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same strides, 1 in the last place")
-    if not (k_cache.is_cuda and v_cache.is_cuda):
+    dev = k_cache.get_device()
+    if dev < 0:
         raise ValueError("k_cache and v_cache must live on the GPU")
+    _placed(v_cache, dev, "v_cache")
     if dtype == torch.bfloat16:
         code = RLK_DT_BF16
     elif dtype == torch.float16:
@@ -891,23 +917,26 @@ def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> K
     else:
         raise ValueError(f"the cache's dtype {dtype} must be bfloat16 or float16")
     i32 = torch.int32
-    if lens.dtype != i32 or lens.dim() != 1 or not lens.is_contiguous() or not lens.is_cuda:
+    if lens.dtype != i32 or lens.dim() != 1 or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 CUDA tensor of shape [B]")
+    _placed(lens, dev, "lens")
     B = lens.shape[0]
-    if page_table.dtype != i32 or page_table.dim() != 2 or page_table.shape[0] != B or not page_table.is_cuda:
+    if page_table.dtype != i32 or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
+    _placed(page_table, dev, "page_table")
     width = page_table.shape[1]
     row, col = page_table.stride()
     if width > 1 and col != 1:
         raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
-    if new_lens is not None and (new_lens.dtype != i32 or new_lens.shape != (B,) or not new_lens.is_contiguous()
-                                 or not new_lens.is_cuda):
-        raise ValueError(f"new_lens must be a contiguous int32 CUDA tensor of shape [{B}]")
+    if new_lens is not None:
+        if new_lens.dtype != i32 or new_lens.shape != (B,) or not new_lens.is_contiguous():
+            raise ValueError(f"new_lens must be a contiguous int32 CUDA tensor of shape [{B}]")
+        _placed(new_lens, dev, "new_lens")
     pages, page_size, heads, dim = shape
     return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, strides[0] if pages > 1 else 0,
                    strides[1] if page_size > 1 else 0, strides[2] if heads > 1 else 0, page_size, heads, dim,
                    code, page_table.data_ptr(), row if B > 1 else width, width,
-                   B, lens.data_ptr(), _ptr(new_lens), n, _ptr(err_count))
+                   B, lens.data_ptr(), _ptr(new_lens), n, _err_ptr(err_count, dev))
 
 
 def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_count=None, stream=None):
@@ -917,16 +946,17 @@ def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_co
     strides (a transposed view for pages ordered by head), the same for both.
     page_table: int32 [B, pages per sequence]; lens: int32 [B], tokens of each
     sequence with the new ones; k, v: [B, n, kv_heads, head_dim], any strides;
-    new_lens: int32 [B] (None: n each), the tokens of k and v that count."""
+    new_lens: int32 [B] (None: n each), the tokens of k and v that count.
+    All of a call's tensors live on one GPU, the stream's."""
     lib = load_library()
     if k.dim() != 4:
         raise ValueError("k must be [B, n, kv_heads, head_dim]")
     n = k.shape[1]
     c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
-    shape, dtype = (c.B, n, c.kv_heads, c.head_dim), k_cache.dtype
-    ks = _bth(k, shape, dtype, "k")
-    vs = _bth(v, shape, dtype, "v")
-    check(lib.rlk_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)))
+    shape, dtype, dev = (c.B, n, c.kv_heads, c.head_dim), k_cache.dtype, k_cache.get_device()
+    ks = _bth(k, shape, dtype, "k", dev)
+    vs = _bth(v, shape, dtype, "v", dev)
+    check(lib.rlk_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream, dev)))
 
 
 def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -961,25 +991,29 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
     _, n, heads, _ = q.shape
     c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
     B, dim, kv_heads = c.B, c.head_dim, c.kv_heads
-    shape = (B, n, heads, dim)
-    qs = _bth(q, shape, k_cache.dtype, "q")
+    shape, dev = (B, n, heads, dim), k_cache.get_device()
+    qs = _bth(q, shape, k_cache.dtype, "q", dev)
     if out is None:
         out = _new(shape, q.dtype, q.device, stream)
         os_ = BTHStrides(n * heads * dim, heads * dim, dim)
     else:
-        os_ = _bth(out, shape, q.dtype, "out")
+        os_ = _bth(out, shape, q.dtype, "out", dev)
     if out_lse is None:
         out_lse = _new((B, n, heads), torch.float32, q.device, stream)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
+    else:
+        _placed(out_lse, dev, "out_lse")
     need = paged_attention_workspace_bytes(B, n, heads, kv_heads, dim, c.max_pages * c.page_size) \
         if heads > 0 and heads % kv_heads == 0 else 0
     if workspace is None:
         workspace = _new(need, torch.uint8, q.device, stream, returned=False)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
+    else:
+        _placed(workspace, dev, "workspace")
     check(lib.rlk_paged_attention(c, q.data_ptr(), qs, heads, dim ** -0.5 if scale is None else scale, window, sinks,
-                                  out.data_ptr(), os_, out_lse.data_ptr(), workspace.data_ptr(), _stream(stream)))
+                                  out.data_ptr(), os_, out_lse.data_ptr(), workspace.data_ptr(), _stream(stream, dev)))
     return out, out_lse
 
 
@@ -1011,44 +1045,49 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
     if draft_token.dim() != 2:
         raise ValueError("draft_token must be int32 [B, n]")
     B, n = draft_token.shape
+    dev = logits.get_device()
     for t, rows, name in ((logits, B * (n + 1), "logits"), (draft_logits, B * n, "draft_logits")):
         if t is not None and (t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != rows
-                              or t.shape[1] < VOCAB_PADDED or t.stride(1) != 1 or not t.is_cuda):
+                              or t.shape[1] < VOCAB_PADDED or t.stride(1) != 1 or t.get_device() != dev or dev < 0):
             raise ValueError(f"{name} must be a bf16 CUDA [{rows}, >={VOCAB_PADDED}] tensor with unit column stride")
     for t, shape, name in ((draft_token, (B, n), "draft_token"), (accept_uniform, (B, n), "accept_uniform"),
                            (draw_uniform, (B,), "draw_uniform"), (num_drafts, (B,), "num_drafts")):
         if t is None and name == "num_drafts":
             continue
-        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {list(shape)}")
-    tp, ts = _param(temperature, B, torch.float32, "temperature")
-    pp, ps = _param(top_p, B, torch.float32, "top_p")
-    kp, ks = _param(top_k, B, torch.int32, "top_k")
-    dtp, dts = (tp, ts) if draft_temperature is None else _param(draft_temperature, B, torch.float32, "draft_temperature")
-    dpp, dps = (pp, ps) if draft_top_p is None else _param(draft_top_p, B, torch.float32, "draft_top_p")
-    dkp, dks = (kp, ks) if draft_top_k is None else _param(draft_top_k, B, torch.int32, "draft_top_k")
-    dev = logits.device
+        _placed(t, dev, name)
+    tp, ts = _param(temperature, B, torch.float32, "temperature", dev)
+    pp, ps = _param(top_p, B, torch.float32, "top_p", dev)
+    kp, ks = _param(top_k, B, torch.int32, "top_k", dev)
+    dtp, dts = (tp, ts) if draft_temperature is None else _param(draft_temperature, B, torch.float32, "draft_temperature", dev)
+    dpp, dps = (pp, ps) if draft_top_p is None else _param(draft_top_p, B, torch.float32, "draft_top_p", dev)
+    dkp, dks = (kp, ks) if draft_top_k is None else _param(draft_top_k, B, torch.int32, "draft_top_k", dev)
     outs = []
     for t, shape, dtype, name in ((out_token, (B, n + 1), torch.int32, "out_token"),
                                   (out_accepted, (B,), torch.int32, "out_accepted"),
                                   (out_restr, (B, n + 1), torch.float32, "out_restr"),
                                   (out_full, (B, n + 1), torch.float32, "out_full")):
         if t is None:
-            t = _new(shape, dtype, dev, stream)
+            t = _new(shape, dtype, logits.device, stream)
         elif t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+        else:
+            _placed(t, dev, name)
         outs.append(t)
     need = verify_workspace_bytes(B, n)
     if workspace is None:
-        workspace = _new(need, torch.uint8, dev, stream, returned=False)
+        workspace = _new(need, torch.uint8, logits.device, stream, returned=False)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least verify_workspace_bytes(B, n) bytes")
+    else:
+        _placed(workspace, dev, "workspace")
     a = VerifyArgs(B, n, VOCAB_REAL, VOCAB_PADDED, logits.data_ptr() if B else None,
                    logits.stride(0) if B * (n + 1) > 1 else VOCAB_PADDED,
                    draft_logits.data_ptr() if draft_logits is not None and B * n else None,
                    draft_logits.stride(0) if draft_logits is not None and B * n > 1 else VOCAB_PADDED,
                    draft_token.data_ptr(), _ptr(num_drafts), tp, ts, pp, ps, kp, ks, dtp, dts, dpp, dps, dkp, dks,
-                   accept_uniform.data_ptr(), draw_uniform.data_ptr(), _ptr(err_count))
+                   accept_uniform.data_ptr(), draw_uniform.data_ptr(), _err_ptr(err_count, dev))
     check(lib.rlk_verify_drafts(a, *[t.data_ptr() for t in outs], workspace.data_ptr() if B else None,
-                                _stream(stream)))
+                                _stream(stream, dev)))
     return tuple(outs)
