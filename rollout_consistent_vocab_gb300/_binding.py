@@ -230,10 +230,8 @@ def _placed(t, dev, name):
         raise ValueError(f"{name} must live on the GPU of the call's other tensors (cuda:{dev}), not on {t.device}")
 
 
-def _err_ptr(t, dev) -> int | None:
+def _err_ptr(t, dev) -> int:
     """A rollout call's counter of rejected sequences."""
-    if t is None:
-        return None
     if t.dtype != _torch().int32 or t.numel() < 1:
         raise ValueError("err_count must be an int32 tensor of one element")
     _placed(t, dev, "err_count")
@@ -281,19 +279,23 @@ def _stream(stream, dev=None):
     return raw(here)
 
 
-def _new(shape, dtype, device, stream, returned=True):
-    """A tensor that a call on ``stream`` makes for itself.  It is that stream's own: its memory
-    is neither what other work on the current stream still uses, nor given to such work while
+def _maker(stream, returned=True):
+    """torch.empty for what a call on ``stream`` makes for itself.  A tensor is that stream's own: its
+    memory is neither what other work on the current stream still uses, nor given to such work while
     the call runs.  What the caller gets back is marked as used on the current stream too."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned and here != stream:
-        t.record_stream(here)
-    return t
+        return torch.empty
+
+    def empty(shape, *, dtype, device):
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        if returned and here != stream:
+            t.record_stream(here)
+        return t
+
+    return empty
 
 
 def _elsewhere(stream) -> bool:
@@ -302,7 +304,7 @@ def _elsewhere(stream) -> bool:
 
 
 def _empty(T, dtype, like, stream):
-    return _new((T,), dtype, like.device, stream)
+    return _maker(stream)((T,), dtype=dtype, device=like.device)
 
 
 def logp_full(logits, target, temperature=1.0, *, out=None, err_count=None, stream=None):
@@ -387,7 +389,7 @@ def logp_kl_host(logits, ref_logits, target, temperature=1.0, top_p=1.0, top_k=-
             ((out_full, torch.float32), (out_restr, torch.float32), (out_support, torch.int32),
              (out_full_ref, torch.float32), (out_kl, torch.float32))]
     if workspace is None:
-        workspace = _new(logp_kl_host_workspace_bytes(a.T), torch.uint8, dev, stream, returned=False)
+        workspace = _maker(stream, returned=False)(logp_kl_host_workspace_bytes(a.T), dtype=torch.uint8, device=dev)
     if workspace.numel() * workspace.element_size() < logp_kl_host_workspace_bytes(a.T) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least logp_kl_host_workspace_bytes(T) bytes")
     check(lib.rlk_logp_kl_host(ctypes.byref(a), ref_logits.data_ptr() if a.T else None,
@@ -605,7 +607,7 @@ def logp_backward(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, grad_
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape [T]")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        out = _new((a.T, VOCAB_PADDED), dtype, logits.device, stream)
+        out = _maker(stream)((a.T, VOCAB_PADDED), dtype=dtype, device=logits.device)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.dim() != 2 or out.stride(1) != 1:
         raise ValueError("out must be a bf16 or float32 [T, >=152576] tensor with unit column stride")
     gd = RLK_GRAD_F32 if out.dtype == torch.float32 else RLK_GRAD_BF16
@@ -628,7 +630,7 @@ def logp_pair_save(logits, target, temperature=1.0, top_p=1.0, top_k=-1, *, out_
     out_restr = _empty(a.T, torch.float32, logits, stream) if out_restr is None else out_restr
     out_support = _empty(a.T, torch.int32, logits, stream) if out_support is None else out_support
     if out_stats is None:
-        out_stats = _new((a.T, 4), torch.float32, logits.device, stream)
+        out_stats = _maker(stream)((a.T, 4), dtype=torch.float32, device=logits.device)
     check(lib.rlk_logp_pair_save(ctypes.byref(a), _ptr(out_full), _ptr(out_restr), _ptr(out_support),
                                  _ptr(out_stats), _stream(stream)))
     return out_full, out_restr, out_support, out_stats
@@ -648,7 +650,7 @@ def logp_backward_saved(logits, target, stats, temperature=1.0, *, grad_full=Non
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape [T]")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        out = _new((a.T, VOCAB_PADDED), dtype, logits.device, stream)
+        out = _maker(stream)((a.T, VOCAB_PADDED), dtype=dtype, device=logits.device)
     if out.dtype not in (torch.bfloat16, torch.float32) or out.dim() != 2 or out.stride(1) != 1:
         raise ValueError("out must be a bf16 or float32 [T, >=152576] tensor with unit column stride")
     gd = RLK_GRAD_F32 if out.dtype == torch.float32 else RLK_GRAD_BF16
@@ -730,7 +732,7 @@ def sample(logits, temperature=1.0, top_p=1.0, top_k=-1, *, seed=0, counter=None
     out_full = _empty(T, torch.float32, logits, stream) if out_full is None else out_full
     out_support = _empty(T, torch.int32, logits, stream) if out_support is None else out_support
     if workspace is None:
-        workspace = _new(sample_workspace_bytes(T), torch.uint8, logits.device, stream, returned=False)
+        workspace = _maker(stream, returned=False)(sample_workspace_bytes(T), dtype=torch.uint8, device=logits.device)
     if workspace.numel() * workspace.element_size() < sample_workspace_bytes(T) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least sample_workspace_bytes(T) bytes")
     check(lib.rlk_sample(ctypes.byref(a), int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(counter), _ptr(uniform),
@@ -763,7 +765,7 @@ def linear_logp(hidden, weight, target, temperature=1.0, *, out=None, workspace=
     tp, ts = _param(temperature, T, torch.float32, "temperature")
     out = _empty(T, torch.float32, hidden, stream) if out is None else out
     if workspace is None:
-        workspace = _new(max(1, linear_workspace_bytes(T)), torch.uint8, hidden.device, stream, returned=False)
+        workspace = _maker(stream, returned=False)(max(1, linear_workspace_bytes(T)), dtype=torch.uint8, device=hidden.device)
     check(lib.rlk_linear_logp(hidden.data_ptr() if T else None, T, H, hidden.stride(0) if T else H,
                               weight.data_ptr(), weight.stride(0), _ptr(target), tp, ts, _ptr(out),
                               workspace.data_ptr(), _ptr(err_count), _stream(stream)))
@@ -797,8 +799,8 @@ def linear_logp_pair(hidden, weight, target, temperature=1.0, top_p=1.0, top_k=-
     out_restr = _empty(T, torch.float32, hidden, stream) if out_restr is None else out_restr
     out_support = _empty(T, torch.int32, hidden, stream) if out_support is None else out_support
     if workspace is None:
-        workspace = _new(max(1, linear_pair_workspace_bytes(T)), torch.uint8, hidden.device, stream,
-                         returned=False)
+        workspace = _maker(stream, returned=False)(max(1, linear_pair_workspace_bytes(T)), dtype=torch.uint8,
+                                                    device=hidden.device)
     elif workspace.numel() * workspace.element_size() < linear_pair_workspace_bytes(T):
         raise ValueError("workspace must hold at least linear_pair_workspace_bytes(T) bytes")
     check(lib.rlk_linear_logp_pair(hidden.data_ptr() if T else None, T, H, hidden.stride(0) if T else H,
@@ -845,7 +847,7 @@ def sqnorm_finalize(bins, out=None, stream=None):
     """(sum of squares, norm) as a device float64 [2]."""
     lib = load_library()
     torch = _torch()
-    out = _new(2, torch.float64, bins.device, stream) if out is None else out
+    out = _maker(stream)(2, dtype=torch.float64, device=bins.device) if out is None else out
     check(lib.rlk_sqnorm_finalize(_ptr(bins), _ptr(out), _stream(stream)))
     return out
 
@@ -909,7 +911,6 @@ def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> K
     dev = k_cache.get_device()
     if dev < 0:
         raise ValueError("k_cache and v_cache must live on the GPU")
-    _placed(v_cache, dev, "v_cache")
     if dtype == torch.bfloat16:
         code = RLK_DT_BF16
     elif dtype == torch.float16:
@@ -919,11 +920,9 @@ def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> K
     i32 = torch.int32
     if lens.dtype != i32 or lens.dim() != 1 or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 CUDA tensor of shape [B]")
-    _placed(lens, dev, "lens")
     B = lens.shape[0]
     if page_table.dtype != i32 or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be an int32 [B, pages] CUDA tensor with unit column stride")
-    _placed(page_table, dev, "page_table")
     width = page_table.shape[1]
     row, col = page_table.stride()
     if width > 1 and col != 1:
@@ -931,12 +930,16 @@ def _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count) -> K
     if new_lens is not None:
         if new_lens.dtype != i32 or new_lens.shape != (B,) or not new_lens.is_contiguous():
             raise ValueError(f"new_lens must be a contiguous int32 CUDA tensor of shape [{B}]")
-        _placed(new_lens, dev, "new_lens")
+        if new_lens.get_device() != dev:
+            _placed(new_lens, dev, "new_lens")
+    if v_cache.get_device() != dev or page_table.get_device() != dev or lens.get_device() != dev:
+        for t, name in ((v_cache, "v_cache"), (page_table, "page_table"), (lens, "lens")):
+            _placed(t, dev, name)
     pages, page_size, heads, dim = shape
     return KVCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, strides[0] if pages > 1 else 0,
                    strides[1] if page_size > 1 else 0, strides[2] if heads > 1 else 0, page_size, heads, dim,
                    code, page_table.data_ptr(), row if B > 1 else width, width,
-                   B, lens.data_ptr(), _ptr(new_lens), n, _err_ptr(err_count, dev))
+                   B, lens.data_ptr(), _ptr(new_lens), n, None if err_count is None else _err_ptr(err_count, dev))
 
 
 def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_count=None, stream=None):
@@ -993,13 +996,14 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
     B, dim, kv_heads = c.B, c.head_dim, c.kv_heads
     shape, dev = (B, n, heads, dim), k_cache.get_device()
     qs = _bth(q, shape, k_cache.dtype, "q", dev)
+    new = torch.empty if stream is None else _maker(stream)
     if out is None:
-        out = _new(shape, q.dtype, q.device, stream)
+        out = new(shape, dtype=q.dtype, device=q.device)
         os_ = BTHStrides(n * heads * dim, heads * dim, dim)
     else:
         os_ = _bth(out, shape, q.dtype, "out", dev)
     if out_lse is None:
-        out_lse = _new((B, n, heads), torch.float32, q.device, stream)
+        out_lse = new((B, n, heads), dtype=torch.float32, device=q.device)
     elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
     else:
@@ -1007,7 +1011,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
     need = paged_attention_workspace_bytes(B, n, heads, kv_heads, dim, c.max_pages * c.page_size) \
         if heads > 0 and heads % kv_heads == 0 else 0
     if workspace is None:
-        workspace = _new(need, torch.uint8, q.device, stream, returned=False)
+        workspace = (new if stream is None else _maker(stream, returned=False))(need, dtype=torch.uint8, device=q.device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least paged_attention_workspace_bytes(...) bytes")
     else:
@@ -1054,22 +1058,22 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
                            (draw_uniform, (B,), "draw_uniform"), (num_drafts, (B,), "num_drafts")):
         if t is None and name == "num_drafts":
             continue
-        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {list(shape)}")
-        _placed(t, dev, name)
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on the logits' GPU")
     tp, ts = _param(temperature, B, torch.float32, "temperature", dev)
     pp, ps = _param(top_p, B, torch.float32, "top_p", dev)
     kp, ks = _param(top_k, B, torch.int32, "top_k", dev)
     dtp, dts = (tp, ts) if draft_temperature is None else _param(draft_temperature, B, torch.float32, "draft_temperature", dev)
     dpp, dps = (pp, ps) if draft_top_p is None else _param(draft_top_p, B, torch.float32, "draft_top_p", dev)
     dkp, dks = (kp, ks) if draft_top_k is None else _param(draft_top_k, B, torch.int32, "draft_top_k", dev)
+    new, device = torch.empty if stream is None else _maker(stream), logits.device
     outs = []
     for t, shape, dtype, name in ((out_token, (B, n + 1), torch.int32, "out_token"),
                                   (out_accepted, (B,), torch.int32, "out_accepted"),
                                   (out_restr, (B, n + 1), torch.float32, "out_restr"),
                                   (out_full, (B, n + 1), torch.float32, "out_full")):
         if t is None:
-            t = _new(shape, dtype, logits.device, stream)
+            t = new(shape, dtype=dtype, device=device)
         elif t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
         else:
@@ -1077,7 +1081,7 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
         outs.append(t)
     need = verify_workspace_bytes(B, n)
     if workspace is None:
-        workspace = _new(need, torch.uint8, logits.device, stream, returned=False)
+        workspace = (new if stream is None else _maker(stream, returned=False))(need, dtype=torch.uint8, device=device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor of at least verify_workspace_bytes(B, n) bytes")
     else:
@@ -1087,7 +1091,8 @@ def verify_drafts(logits, draft_token, temperature=1.0, top_p=1.0, top_k=-1, *, 
                    draft_logits.data_ptr() if draft_logits is not None and B * n else None,
                    draft_logits.stride(0) if draft_logits is not None and B * n > 1 else VOCAB_PADDED,
                    draft_token.data_ptr(), _ptr(num_drafts), tp, ts, pp, ps, kp, ks, dtp, dts, dpp, dps, dkp, dks,
-                   accept_uniform.data_ptr(), draw_uniform.data_ptr(), _err_ptr(err_count, dev))
+                   accept_uniform.data_ptr(), draw_uniform.data_ptr(),
+                   None if err_count is None else _err_ptr(err_count, dev))
     check(lib.rlk_verify_drafts(a, *[t.data_ptr() for t in outs], workspace.data_ptr() if B else None,
                                 _stream(stream, dev)))
     return tuple(outs)
