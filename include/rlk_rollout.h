@@ -105,6 +105,8 @@ rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth
  * sequence gets NaN in out and lse: for all its places if its lengths are at
  * fault (as in rlk_kv_append), for its places i < new_lens[b] if the page
  * number of a visible token is out of range.
+ * The call's cost goes by n, and by the keys and values that a sequence's new
+ * tokens see together: prompts and single tokens want calls of their own.
  * Scores, softmax statistics and output sums are held in float32, and out is
  * rounded once at the end.  The weights exp(s_j - max) go into the product with
  * V as two elements of the cache's dtype: 16 bits in bf16, whatever their size;

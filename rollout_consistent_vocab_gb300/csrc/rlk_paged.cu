@@ -118,22 +118,27 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // depends on the batch.
 //
 // What bounds it.  One new token: memory.  64 sequences of up to 8192 tokens, 32 query
-// heads on 8 of 128 elements, 0.69 GB of keys and values: 0.125 ms = 5.5 TB/s; 4 of up
-// to 131071, 1.28 GB: 0.206 ms = 6.2 TB/s.  Several new tokens (128 sequences of up to
-// 4096, 5 each, 0.65 GB): 0.172 ms = 3.8 TB/s, bound by the latency of the working
-// warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500).  A
-// window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.051 ms =
+// heads on 8 of 128 elements, 0.69 GB of keys and values: 0.123 ms = 5.6 TB/s; 4 of up
+// to 131071, 1.28 GB: 0.203 ms = 6.3 TB/s.  Several new tokens (128 sequences of up to
+// 4096, 5 each, 0.65 GB): 0.170 ms = 3.8 TB/s, bound by the latency of the working
+// warps' instructions (a slice takes one about 1800 cycles, a unit's sum 3500; with 24
+// and 32 rows of 128 elements they also spill, 100 and 220 bytes a thread).  A
+// window of 1024 (64 sequences, 64 heads on 8 of 64 elements, f16, 0.13 GB): 0.050 ms =
 // 2.6 TB/s, where the units are few and their ends count.
+// The extent of the work is the sequence's and the call's, not the tile's: every tile of
+// n's rows goes over all that the sequence's new tokens see.  So prompts pay for their
+// masked half (4 of 2048 tokens: 2.8 ms), and single tokens beside a prompt for its tiles.
 //
 // Why mma.sync.  With 8 query rows to a tile the products are small: K and V pass
 // once through shared memory into registers, and a score never leaves the warp that
 // takes its exponential.  The same tree on tcgen05 (128 tokens as rows, 16 to 64 query
 // rows as columns, scores and results in tensor memory) took 0.172 ms where this takes
-// 0.125, 0.243 for 0.206, 0.330 for 0.172 and 0.125 for 0.051: the weights' way through
+// 0.123, 0.243 for 0.203, 0.330 for 0.170 and 0.125 for 0.050: the weights' way through
 // tensor memory and back lies between the two products, and its code (96 to 198 KB
 // against 73 to 82) ran into the instruction cache.
 
-// (units of 2048 tokens: 0.137 ms for 0.125 in the first case above, 0.274 for 0.253 in the third)
+// (units of 2048 tokens: 0.137 ms for 0.125 in the first case above, 0.274 for 0.253 in the third,
+// when they were chosen; requests of a few units were not compared)
 constexpr int UNIT = 512;                // tokens of a unit
 constexpr int GROUP = 4;                 // units of a group
 constexpr int AW = 4;                    // lanes of a CTA: every fourth slice of a unit is one's

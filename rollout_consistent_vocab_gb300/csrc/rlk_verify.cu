@@ -16,7 +16,9 @@
 // eight CTAs.  128 sequences with 4 drafts of a draft model (1152 rows, 0.35 GB, top-k
 // 128): 0.0925 ms = 3.8 TB/s, the pass 0.083 of it.  The draw is latency: a thread takes
 // one marked chunk, and CTAs of 128 threads, many to an SM, wait beside each other
-// (with 512 threads and every chunk of the shard looked at: 0.150 ms the call).
+// (with 512 threads and every chunk of the shard looked at: 0.150 ms the call).  Rows
+// without a bitmap (unfiltered, or nuclei of thousands) are read in full: the same call
+// unfiltered takes 0.177 ms, with top-p 0.95 alone 0.164.
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
