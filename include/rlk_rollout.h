@@ -82,6 +82,49 @@ typedef struct rlk_bth_strides {
 rlk_status rlk_kv_append(const rlk_kv_cache* cache, const void* k, const rlk_bth_strides* k_strides,
                          const void* v, const rlk_bth_strides* v_strides, void* stream);
 
+/* A rotation of heads by position.  Pair j of a head, j < rot_dim / 2, turns by
+ *   angle = positions[pair_axis[j]][b][i] * inv_freq[j]:
+ *   (x, y) -> (x cos - y sin, x sin + y cos);
+ * its elements are j and j + rot_dim / 2, or with `interleaved` 2 j and 2 j + 1.
+ * Elements from rot_dim on pass through.  Angles are reduced to a turn exactly
+ * (64 bits of a turn), whatever the position; products are taken in float32 and
+ * rounded to the dtype once. */
+#define RLK_ROPE_MAX_DIM 256
+#define RLK_ROPE_MAX_AXES 4
+typedef struct rlk_rope_args {
+  const double* inv_freq;       /* HOST [rot_dim / 2], radians a position; finite; read during the call */
+  const uint8_t* pair_axis;     /* HOST [rot_dim / 2], the axis that each pair turns with, or NULL: axis 0 */
+  int32_t rot_dim;              /* a multiple of 16, 16 .. the head's dimension (at most RLK_ROPE_MAX_DIM) */
+  int32_t interleaved;          /* 0 or 1 */
+  const int32_t* positions;     /* device [axes][B][n], any int32 */
+  int32_t axes;                 /* 1 .. RLK_ROPE_MAX_AXES */
+} rlk_rope_args;
+
+/* out = x turned by its positions, or with `inverse` turned back: the gradient
+ * of x where x is the gradient of out.
+ *   x, out: [B][n][heads][head_dim] of dtype RLK_DT_F32, _BF16 or _F16, 16-byte
+ *     aligned, strides of multiples of 16 bytes; out may be x itself (the same
+ *     pointer and strides), otherwise they do not overlap.
+ *   head_dim: a multiple of 16, at most RLK_ROPE_MAX_DIM.  B, n and heads: >= 0,
+ *     B * n below 2^32.  Nothing but out is written. */
+rlk_status rlk_rope(const rlk_rope_args* rope, int64_t B, int64_t n, int32_t heads, int32_t head_dim, int32_t dtype,
+                    const void* x, const rlk_bth_strides* x_strides, void* out, const rlk_bth_strides* out_strides,
+                    int32_t inverse, void* stream);
+
+/* rlk_kv_append with the keys turned on the way, and the queries that go with
+ * them turned into q_out.  positions NULL: a token's place in its sequence, on
+ * every axis.  rot_dim is at most the cache's head_dim.
+ *   q, q_out: [B][n][q_heads][head_dim] of the cache's dtype, or NULL with
+ *     q_heads 0; q_out may be q itself (the same pointer and strides).
+ * A turned head has rlk_rope's bits.  Places i >= new_lens[b] get q_out = 0, and
+ * nothing of them is written to the cache.  A sequence that rlk_kv_append
+ * rejects gets q_out = NaN in all its places; a token whose page number is out
+ * of range is left out of the cache and counted, and its queries are turned. */
+rlk_status rlk_kv_append_rope(const rlk_kv_cache* cache, const rlk_rope_args* rope, const void* k,
+                              const rlk_bth_strides* k_strides, const void* v, const rlk_bth_strides* v_strides,
+                              const void* q, const rlk_bth_strides* q_strides, int32_t q_heads, void* q_out,
+                              const rlk_bth_strides* q_out_strides, void* stream);
+
 /* Attention of the new tokens over the cache (which already holds them).
  * Query i of sequence b stands at pos = lens[b] - new_lens[b] + i and sees the
  * tokens j <= pos; with window > 0 only those with j > pos - window, and the

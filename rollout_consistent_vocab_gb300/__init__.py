@@ -12,7 +12,7 @@ from ._binding import (VOCAB_PADDED, VOCAB_REAL, NUM_SHARDS, SHARD_WIDTH, RlkErr
                        shard_counts, logp_merge, logp_sharded, shard_counts_window,
                        logp_merge_resumable, merge_state, sample, linear_logp, linear_logp_pair,
                        NORM_BINS, norm_bins, sqnorm_accumulate, sqnorm_finalize, reduce_bins_,
-                       grad_norm, KVCache, BTHStrides, kv_append, paged_attention,
+                       grad_norm, KVCache, BTHStrides, RopeArgs, rope, rope_autograd, kv_append, kv_append_rope, paged_attention,
                        paged_attention_workspace_bytes, VerifyArgs, verify_drafts, verify_workspace_bytes)
 
 __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError", "LogpArgs",
@@ -22,5 +22,5 @@ __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError"
            "logp_backward", "logp_pair_save", "logp_backward_saved", "logp_autograd", "shard_summary", "shard_counts", "logp_merge", "shard_counts_window", "logp_merge_resumable", "merge_state",
            "logp_sharded", "sample", "linear_logp", "linear_logp_pair", "NORM_BINS", "norm_bins", "sqnorm_accumulate",
            "sqnorm_finalize", "reduce_bins_", "grad_norm",
-           "KVCache", "BTHStrides", "kv_append", "paged_attention", "paged_attention_workspace_bytes",
+           "KVCache", "BTHStrides", "RopeArgs", "rope", "rope_autograd", "kv_append", "kv_append_rope", "paged_attention", "paged_attention_workspace_bytes",
            "VerifyArgs", "verify_drafts", "verify_workspace_bytes"]

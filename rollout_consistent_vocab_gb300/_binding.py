@@ -91,6 +91,18 @@ class BTHStrides(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
+class RopeArgs(ctypes.Structure):
+    """rlk_rope_args."""
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+        ("axes", ctypes.c_int32),
+    ]
+
+
 class VerifyArgs(ctypes.Structure):
     """rlk_verify_args."""
     _fields_ = [
@@ -129,7 +141,7 @@ COMPUTE = ("rlk_logp_full", "rlk_logp_restricted", "rlk_logp_pair", "rlk_logp_kl
            "rlk_logp_shard_summary", "rlk_logp_shard_counts", "rlk_logp_merge",
            "rlk_logp_merge_resumable", "rlk_logp_shard_counts_window",
            "rlk_sqnorm_accumulate", "rlk_sqnorm_finalize", "rlk_grad_norm",
-           "rlk_kv_append", "rlk_paged_attention", "rlk_paged_attention_workspace", "rlk_verify_drafts")
+           "rlk_rope", "rlk_kv_append", "rlk_kv_append_rope", "rlk_paged_attention", "rlk_paged_attention_workspace", "rlk_verify_drafts")
 RLK_GRAD_BF16, RLK_GRAD_F32 = 0, 1
 EXPORTS = COMPUTE + ("rlk_status_string", "rlk_last_error", "rlk_abi_version")
 
@@ -176,6 +188,9 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.rlk_grad_norm.argtypes = [VP, i64, i32, VP, VP, VP]
     KC, BS = P(KVCache), P(BTHStrides)
     lib.rlk_kv_append.argtypes = [KC, VP, BS, VP, BS, VP]
+    RA = P(RopeArgs)
+    lib.rlk_rope.argtypes = [RA, i64, i64, i32, i32, i32, VP, BS, VP, BS, i32, VP]
+    lib.rlk_kv_append_rope.argtypes = [KC, RA, VP, BS, VP, BS, VP, BS, i32, VP, BS, VP]
     lib.rlk_paged_attention.argtypes = [KC, VP, BS, i32, f32, i32, i32, VP, BS, VP, VP, VP]
     lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i32, i64, P(ctypes.c_size_t)]
     lib.rlk_verify_drafts.argtypes = [P(VerifyArgs), VP, VP, VP, VP, VP, VP]
@@ -893,7 +908,7 @@ def grad_norm(tensors, *, distributed=False, group=None, bins=None, out=None, st
 def _bth(t, shape, dtype, name, dev) -> BTHStrides:
     """Strides of a [B, n, heads, head_dim] tensor with unit stride in the last place."""
     if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on the cache's GPU, cuda:{dev}")
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on the GPU of the call's other tensors, cuda:{dev}")
     sb, st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have unit stride in its last place")
@@ -961,6 +976,142 @@ def kv_append(k_cache, v_cache, page_table, lens, k, v, *, new_lens=None, err_co
     vs = _bth(v, shape, dtype, "v", dev)
     check(lib.rlk_kv_append(c, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream, dev)))
 
+
+# ----------------------------------------------------------------- rotation by position
+
+def _rope_args(inv_freq, pair_axis, interleaved, positions, B, n, dev) -> RopeArgs:
+    """The rotation of [B, n, ...] heads on GPU ``dev``; its CPU tensors are read during the call."""
+    torch = _torch()
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.get_device() >= 0:
+        raise ValueError("inv_freq must be a contiguous float64 CPU tensor of shape [rot_dim / 2]")
+    pairs = inv_freq.shape[0]
+    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or pair_axis.shape != (pairs,) or
+                                  not pair_axis.is_contiguous() or pair_axis.get_device() >= 0):
+        raise ValueError(f"pair_axis must be a contiguous uint8 CPU tensor of shape [{pairs}]")
+    axes = 4
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.dim() not in (2, 3) or tuple(positions.shape[-2:]) != (B, n) \
+                or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of shape [{B}, {n}] or [axes, {B}, {n}]")
+        _placed(positions, dev, "positions")
+        axes = positions.shape[0] if positions.dim() == 3 else 1
+    return RopeArgs(inv_freq.data_ptr(), _ptr(pair_axis), 2 * pairs, 1 if interleaved else 0, _ptr(positions), axes)
+
+
+def rope(x, inv_freq, positions, *, pair_axis=None, interleaved=False, inverse=False, out=None, stream=None):
+    """Heads turned by their positions; with ``inverse`` turned back, which is the gradient
+    of x for a gradient of the result.
+
+    x: float32, bf16 or f16 [B, n, heads, head_dim], any strides of multiples of 16 bytes.
+    inv_freq: float64 [rot_dim / 2] on the CPU, radians a position: pair j of a head, its
+    elements j and j + rot_dim / 2 (``interleaved``: 2 j and 2 j + 1), turns by
+    positions[pair_axis[j], b, i] * inv_freq[j]; elements from rot_dim on pass through.
+    positions: int32 [B, n], or [axes, B, n] with the axis of each pair in ``pair_axis``
+    (uint8 [rot_dim / 2] on the CPU; None: all turn with axis 0).  ``out`` may be x."""
+    lib = load_library()
+    torch = _torch()
+    if x.dim() != 4:
+        raise ValueError("x must be [B, n, heads, head_dim]")
+    B, n, heads, dim = shape = x.shape
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must live on the GPU")
+    if x.dtype == torch.bfloat16:
+        code = RLK_DT_BF16
+    elif x.dtype == torch.float16:
+        code = RLK_DT_F16
+    elif x.dtype == torch.float32:
+        code = RLK_DT_F32
+    else:
+        raise ValueError(f"the dtype {x.dtype} must be float32, bfloat16 or float16")
+    if positions is None:
+        raise ValueError("positions must be given")
+    a = _rope_args(inv_freq, pair_axis, interleaved, positions, B, n, dev)
+    xs = _bth(x, shape, x.dtype, "x", dev)
+    if out is None:
+        out = (torch.empty if stream is None else _maker(stream))(shape, dtype=x.dtype, device=x.device)
+    os_ = _bth(out, shape, x.dtype, "out", dev)
+    check(lib.rlk_rope(a, B, n, heads, dim, code, x.data_ptr(), xs, out.data_ptr(), os_, 1 if inverse else 0,
+                       _stream(stream, dev)))
+    return out
+
+
+def _rope_function():
+    torch = _torch()
+
+    class _Rope(torch.autograd.Function):
+        """rope, differentiable with respect to x: the backward is the same kernel, turning back."""
+
+        @staticmethod
+        def forward(ctx, x, inv_freq, positions, pair_axis, interleaved):
+            ctx.save_for_backward(inv_freq, positions, pair_axis)
+            ctx.interleaved = interleaved
+            return rope(x, inv_freq, positions, pair_axis=pair_axis, interleaved=interleaved)
+
+        @staticmethod
+        def backward(ctx, grad):
+            inv_freq, positions, pair_axis = ctx.saved_tensors
+            # a gradient may come expanded or as a view of anything
+            size, strides = grad.element_size(), zip(grad.stride()[:-1], grad.shape)
+            if grad.stride(-1) != 1 or grad.data_ptr() % 16 or any(s * size % 16 for s, m in strides if m > 1):
+                grad = grad.clone(memory_format=torch.contiguous_format)
+            grad = rope(grad, inv_freq, positions, pair_axis=pair_axis, interleaved=ctx.interleaved, inverse=True)
+            return grad, None, None, None, None
+
+    return _Rope
+
+
+_ROPE_FN = None
+
+
+def rope_autograd(x, inv_freq, positions, *, pair_axis=None, interleaved=False):
+    """rope as a differentiable torch output."""
+    global _ROPE_FN
+    if _ROPE_FN is None:
+        _ROPE_FN = _rope_function()
+    return _ROPE_FN.apply(x, inv_freq, positions, pair_axis, interleaved)
+
+
+def kv_append_rope(k_cache, v_cache, page_table, lens, k, v, inv_freq, *, q=None, q_out=None, positions=None,
+                   pair_axis=None, interleaved=False, new_lens=None, err_count=None, stream=None):
+    """kv_append with the keys turned by their positions on the way (rope's bits), and the
+    queries that go with them turned into ``q_out``.
+
+    inv_freq, pair_axis, interleaved: as in rope; positions: as there, or None: a token's
+    place in its sequence.  q: [B, n, q_heads, head_dim] of the cache's dtype, any strides;
+    q_out: where they go (q itself will do), allocated here if not given.  Places
+    i >= new_lens[b] get q_out = 0.  Returns q_out (None without q)."""
+    lib = load_library()
+    if k.dim() != 4:
+        raise ValueError("k must be [B, n, kv_heads, head_dim]")
+    n = k.shape[1]
+    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
+    B, dim, dtype, dev = c.B, c.head_dim, k_cache.dtype, k_cache.get_device()
+    shape = (B, n, c.kv_heads, dim)
+    ks = _bth(k, shape, dtype, "k", dev)
+    vs = _bth(v, shape, dtype, "v", dev)
+    a = _rope_args(inv_freq, pair_axis, interleaved, positions, B, n, dev)
+    heads, qs, os_ = 0, None, None
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if q.dim() != 4:
+            raise ValueError("q must be [B, n, q_heads, head_dim]")
+        heads = q.shape[2]
+        shape = (B, n, heads, dim)
+        qs = _bth(q, shape, dtype, "q", dev)
+        if q_out is None:
+            q_out = (_torch().empty if stream is None else _maker(stream))(shape, dtype=dtype, device=q.device)
+            os_ = BTHStrides(n * heads * dim, heads * dim, dim)
+        else:
+            os_ = _bth(q_out, shape, dtype, "q_out", dev)
+    check(lib.rlk_kv_append_rope(c, a, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads, _ptr(q_out), os_,
+                                 _stream(stream, dev)))
+    return q_out
+
+
+# ----------------------------------------------------------------- paged attention
 
 def paged_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int, head_dim: int,
                                     max_tokens: int) -> int:
