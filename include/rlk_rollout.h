@@ -163,6 +163,44 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
 rlk_status rlk_paged_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                          int64_t max_tokens, size_t* bytes);
 
+/* Groups of sequences that begin with the same tokens, as the samples of one
+ * prompt do: sequences group_start[g] .. group_start[g + 1] - 1 have the keys and
+ * values of their first shared_lens[g] tokens in common.  Sequences before
+ * group_start[0] and from group_start[groups] on are in no group. */
+typedef struct rlk_prefix_groups {
+  const int32_t* group_start;   /* device [groups + 1], never decreasing, 0 .. B */
+  const int32_t* shared_lens;   /* device [groups], 0 .. max_shared */
+  int32_t groups;               /* 0 .. 65535 */
+  int32_t max_shared;           /* at most max_pages * page_size; the workspace goes by it */
+} rlk_prefix_groups;
+
+/* rlk_paged_attention (without a window) of a batch whose groups share a prefix:
+ * the shared tokens are read once for all of a group's queries, through the page
+ * table's row of the group's first sequence; every sequence's other tokens
+ * through its own.  The rows may name the same pages or copies of them: the
+ * pages of the shared tokens, but for the last 31 of them at most, are looked up
+ * in the first sequence's row alone, whether or not it has new tokens.
+ * Every new token comes after the shared ones: a sequence with new tokens and
+ * lens[b] - new_lens[b] < shared_lens[g] is rejected, and so are all of a group
+ * whose shared length is out of range, and all of a call whose group_start is at
+ * fault (NaN for all their places, as in rlk_paged_attention, *err_count raised).
+ * A shared token's page number out of range rejects the group's new tokens.
+ * A sequence's result depends on its own tokens and its shared length, not on
+ * what else is in its group or the batch; one in no group, or that shares fewer
+ * than 32 tokens, has rlk_paged_attention's bits.
+ * Precision is that of rlk_paged_attention, but for the weights of shared tokens
+ * in f16: 22 bits, no finer than 2^-37 of the row's largest weight among up to
+ * 2048 tokens.
+ *   workspace: of rlk_prefix_attention_workspace's size for max_tokens =
+ *     max_pages * page_size, 16-byte aligned; not kept. */
+rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_groups* groups, const void* q,
+                                const rlk_bth_strides* q_strides, int32_t q_heads, float scale, void* out,
+                                const rlk_bth_strides* out_strides, float* out_lse, void* workspace, void* stream);
+
+/* *bytes = the scratch that rlk_prefix_attention needs for these sizes. */
+rlk_status rlk_prefix_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                          int64_t max_tokens, int32_t groups, int32_t max_shared, size_t* bytes);
+
 /* Verification of drafted tokens by rejection sampling: what comes out is
  * distributed as the target's own tokens, whatever the draft model.
  *

@@ -13,7 +13,8 @@ from ._binding import (VOCAB_PADDED, VOCAB_REAL, NUM_SHARDS, SHARD_WIDTH, RlkErr
                        logp_merge_resumable, merge_state, sample, linear_logp, linear_logp_pair,
                        NORM_BINS, norm_bins, sqnorm_accumulate, sqnorm_finalize, reduce_bins_,
                        grad_norm, KVCache, BTHStrides, RopeArgs, rope, rope_autograd, kv_append, kv_append_rope, paged_attention,
-                       paged_attention_workspace_bytes, VerifyArgs, verify_drafts, verify_workspace_bytes)
+                       paged_attention_workspace_bytes, PrefixGroups, prefix_attention, prefix_attention_workspace_bytes,
+                       VerifyArgs, verify_drafts, verify_workspace_bytes)
 
 __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError", "LogpArgs",
            "ShardArgs",
@@ -23,4 +24,4 @@ __all__ = ["VOCAB_PADDED", "VOCAB_REAL", "NUM_SHARDS", "SHARD_WIDTH", "RlkError"
            "logp_sharded", "sample", "linear_logp", "linear_logp_pair", "NORM_BINS", "norm_bins", "sqnorm_accumulate",
            "sqnorm_finalize", "reduce_bins_", "grad_norm",
            "KVCache", "BTHStrides", "RopeArgs", "rope", "rope_autograd", "kv_append", "kv_append_rope", "paged_attention", "paged_attention_workspace_bytes",
-           "VerifyArgs", "verify_drafts", "verify_workspace_bytes"]
+           "PrefixGroups", "prefix_attention", "prefix_attention_workspace_bytes", "VerifyArgs", "verify_drafts", "verify_workspace_bytes"]

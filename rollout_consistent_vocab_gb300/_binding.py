@@ -103,6 +103,16 @@ class RopeArgs(ctypes.Structure):
     ]
 
 
+class PrefixGroups(ctypes.Structure):
+    """rlk_prefix_groups."""
+    _fields_ = [
+        ("group_start", ctypes.c_void_p),
+        ("shared_lens", ctypes.c_void_p),
+        ("groups", ctypes.c_int32),
+        ("max_shared", ctypes.c_int32),
+    ]
+
+
 class VerifyArgs(ctypes.Structure):
     """rlk_verify_args."""
     _fields_ = [
@@ -141,7 +151,8 @@ COMPUTE = ("rlk_logp_full", "rlk_logp_restricted", "rlk_logp_pair", "rlk_logp_kl
            "rlk_logp_shard_summary", "rlk_logp_shard_counts", "rlk_logp_merge",
            "rlk_logp_merge_resumable", "rlk_logp_shard_counts_window",
            "rlk_sqnorm_accumulate", "rlk_sqnorm_finalize", "rlk_grad_norm",
-           "rlk_rope", "rlk_kv_append", "rlk_kv_append_rope", "rlk_paged_attention", "rlk_paged_attention_workspace", "rlk_verify_drafts")
+           "rlk_rope", "rlk_kv_append", "rlk_kv_append_rope", "rlk_paged_attention", "rlk_paged_attention_workspace",
+           "rlk_prefix_attention", "rlk_prefix_attention_workspace", "rlk_verify_drafts")
 RLK_GRAD_BF16, RLK_GRAD_F32 = 0, 1
 EXPORTS = COMPUTE + ("rlk_status_string", "rlk_last_error", "rlk_abi_version")
 
@@ -193,6 +204,8 @@ def load_library(path: str = LIB) -> ctypes.CDLL:
     lib.rlk_kv_append_rope.argtypes = [KC, RA, VP, BS, VP, BS, VP, BS, i32, VP, BS, VP]
     lib.rlk_paged_attention.argtypes = [KC, VP, BS, i32, f32, i32, i32, VP, BS, VP, VP, VP]
     lib.rlk_paged_attention_workspace.argtypes = [i64, i32, i32, i32, i32, i64, P(ctypes.c_size_t)]
+    lib.rlk_prefix_attention.argtypes = [KC, P(PrefixGroups), VP, BS, i32, f32, VP, BS, VP, VP, VP]
+    lib.rlk_prefix_attention_workspace.argtypes = [i64, i32, i32, i32, i32, i64, i32, i32, P(ctypes.c_size_t)]
     lib.rlk_verify_drafts.argtypes = [P(VerifyArgs), VP, VP, VP, VP, VP, VP]
     for f in COMPUTE:
         getattr(lib, f).restype = ctypes.c_int
@@ -1169,6 +1182,80 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, *, new_lens=None, sca
         _placed(workspace, dev, "workspace")
     check(lib.rlk_paged_attention(c, q.data_ptr(), qs, heads, dim ** -0.5 if scale is None else scale, window, sinks,
                                   out.data_ptr(), os_, out_lse.data_ptr(), workspace.data_ptr(), _stream(stream, dev)))
+    return out, out_lse
+
+
+# ----------------------------------------------------------------- attention over a shared prefix
+
+def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
+                                     groups: int, max_shared: int) -> int:
+    """rlk_prefix_attention_workspace: scratch bytes for max_tokens = pages per sequence * page_size."""
+    if B == 0 or n == 0 or q_heads == 0:
+        return 0
+    pieces = 0
+    for top in (min(max_shared, 8191), min(max_shared, 32767), max_shared):
+        size = 512 if top < 8192 else 1024 if top < 32768 else 2048
+        pieces = max(pieces, -(-(top // 32 * 32) // size))
+
+    def lined(x):
+        return (x + 127) // 128 * 128
+
+    rows = B * n * q_heads
+    return 128 + lined(4 * B) + lined(16 * groups) + lined(4 * groups) + lined(4 * (groups + 1)) \
+        + lined(8 * rows * pieces) + lined(4 * rows * pieces * head_dim) \
+        + paged_attention_workspace_bytes(B, n, q_heads, kv_heads, head_dim, max_tokens)
+
+
+def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_lens, *, new_lens=None, max_shared=None,
+                     scale=None, out=None, out_lse=None, workspace=None, err_count=None, stream=None):
+    """paged_attention of a batch whose groups of sequences begin with the same tokens (the
+    samples of one prompt), which are read once for all of a group's queries.
+
+    group_start: int32 [groups + 1], never decreasing: sequences group_start[g] up to
+    group_start[g + 1] are a group, and those outside of all are on their own;
+    shared_lens: int32 [groups], the tokens that a group's sequences have in common (their
+    pages are looked up in its first sequence's row of page_table).  Every new token comes
+    after them.  ``max_shared``: what no shared length exceeds (None: what the page table
+    holds); the scratch's size goes by it.  The rest as in paged_attention; ``workspace``:
+    uint8 [prefix_attention_workspace_bytes(...)].  A sequence's result does not depend on
+    what else is in its group or the batch."""
+    lib = load_library()
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, q_heads, head_dim]")
+    _, n, heads, _ = q.shape
+    c = _make_cache(k_cache, v_cache, page_table, lens, new_lens, n, err_count)
+    B, dim, kv_heads = c.B, c.head_dim, c.kv_heads
+    shape, dev = (B, n, heads, dim), k_cache.get_device()
+    groups, tokens = shared_lens.shape[0] if shared_lens.dim() == 1 else -1, c.max_pages * c.page_size
+    for t, m, name in ((shared_lens, groups, "shared_lens"), (group_start, groups + 1, "group_start")):
+        if t.dtype != torch.int32 or t.shape != (m,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor: shared_lens [groups], group_start [groups + 1]")
+        _placed(t, dev, name)
+    pg = PrefixGroups(group_start.data_ptr(), shared_lens.data_ptr(), groups, tokens if max_shared is None else max_shared)
+    qs = _bth(q, shape, k_cache.dtype, "q", dev)
+    new = torch.empty if stream is None else _maker(stream)
+    if out is None:
+        out = new(shape, dtype=q.dtype, device=q.device)
+        os_ = BTHStrides(n * heads * dim, heads * dim, dim)
+    else:
+        os_ = _bth(out, shape, q.dtype, "out", dev)
+    if out_lse is None:
+        out_lse = new((B, n, heads), dtype=torch.float32, device=q.device)
+    elif out_lse.dtype != torch.float32 or out_lse.shape != (B, n, heads) or not out_lse.is_contiguous():
+        raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
+    else:
+        _placed(out_lse, dev, "out_lse")
+    need = prefix_attention_workspace_bytes(B, n, heads, kv_heads, dim, tokens, groups, max(pg.max_shared, 0)) \
+        if heads > 0 and heads % kv_heads == 0 and pg.max_shared <= tokens else 0
+    if workspace is None:
+        workspace = (new if stream is None else _maker(stream, returned=False))(need, dtype=torch.uint8, device=q.device)
+    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor of at least prefix_attention_workspace_bytes(...) bytes")
+    else:
+        _placed(workspace, dev, "workspace")
+    check(lib.rlk_prefix_attention(c, pg, q.data_ptr(), qs, heads, dim ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                   out_lse.data_ptr(), workspace.data_ptr(), _stream(stream, dev)))
     return out, out_lse
 
 

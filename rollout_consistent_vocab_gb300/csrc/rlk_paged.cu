@@ -182,6 +182,7 @@ struct AttnParams {
   uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
   uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
+  PrefixParts pre;              // first NULL: none
 };
 struct AttnMaps {
   CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
@@ -206,6 +207,8 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
   Seq s;
   s.ok = seq_lens(P.c, b, s.len, s.nnew);
+  const int first = P.pre.first ? P.pre.first[b] : 0;
+  s.ok &= first >= 0;
   if (!s.ok) s.len = s.nnew = 0;
   s.low = s.us = s.ul = s.nu = 0;
   if (s.ok && s.nnew > 0) {
@@ -213,6 +216,9 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
       s.low = max(0, s.len - s.nnew - P.window + 1);
       s.ul = s.low / UNIT;
       s.us = min(units_of(min(P.sinks, s.len)), s.ul);
+    } else if (first > 0) {              // (no window with parts)
+      s.low = min(first, s.len - 1);
+      s.ul = s.low / UNIT;
     }
     s.nu = s.us + units_of(s.len) - s.ul;
   }
@@ -864,7 +870,7 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 
     // ---- where the unit's result goes; on to the next unit, whose queries come meanwhile
     const bool group_ends = cons.li + 1 == cons.s.past(g), store = !folding || group_ends;
-    const bool direct = folding && cons.s.past(g) - cons.s.first(g) == cons.s.nu;
+    const bool direct = folding && !P.pre.first && cons.s.past(g) - cons.s.first(g) == cons.s.nu;
     const int64_t slot = folding ? (static_cast<int64_t>(cons.b) * HT + cons.head * P.tiles + cons.tile) * P.groups + g
                                  : static_cast<int64_t>(me) * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
     const int was_b = cons.b, was_head = cons.head, was_row0 = row0, was_nnew = cons.s.nnew;
@@ -1021,7 +1027,7 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
   }
 }
 
-template <class T, int D, int JR>        // JR: rows that a warp joins at once
+template <class T, int D, int JR, bool PRE>      // JR: rows that a warp joins at once; PRE: with parts of a prefix
 __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
   constexpr int E = D / 32;
   __shared__ int64_t scan[JW * 32 + 1];
@@ -1047,7 +1053,7 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
     const Seq s = load_seq(P, b);
     const uint32_t u0 = static_cast<uint32_t>(units_before<JW * 32>(P, scan, b) * HT) + static_cast<uint32_t>(ht) * s.nu;
     const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
-    const bool direct = s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
+    const bool direct = !PRE && s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
     const bool work = mine && !(direct && s.nnew == P.c.n);
     if (mine && !s.ok && ht == 0 && r0 == 0 && w0 == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1128,6 +1134,25 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
       const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
       if (row >= P.rows || (direct && i < s.nnew)) continue;
       JoinRow<D> all, part;
+      if (PRE && s.ok && i < s.nnew) {   // the prefix's parts in order, eight under way at once
+        const int parts = pieces_of(P.pre.first[b]);
+        const int64_t from = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + row;
+        const float2* ml = P.pre.ml + from * P.pre.pieces;
+        const float* po = P.pre.o + from * P.pre.pieces * D + lane * E;
+        for (int c0 = 0; c0 < parts; c0 += 8) {
+          float2 h[8];
+          float v[8][E];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int at = min(c0 + c, parts - 1);
+            h[c] = ml[at];
+            load_row<E>(po + static_cast<int64_t>(at) * D, v[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c0 + c < parts) all.add(h[c].x, h[c].y, v[c]);
+        }
+      }
       for (int c = 0; c < width; ++c) {
         float v[E];
 #pragma unroll
@@ -1335,7 +1360,9 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1> : join_kernel<T, D, 2>, P, tile_rows, width, items);
+  auto* const join = P.pre.first ? (single ? join_kernel<T, D, 1, true> : join_kernel<T, D, 2, true>)
+                                 : (single ? join_kernel<T, D, 1, false> : join_kernel<T, D, 2, false>);
+  e = cudaLaunchKernelEx(&cfg, join, P, tile_rows, width, items);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
@@ -1347,6 +1374,64 @@ rlk_status launch_rows(const AttnParams& P, int nt, cudaStream_t st) {
     case 3: return launch_attn<T, D, 3>(P, st);
     default: return launch_attn<T, D, 4>(P, st);
   }
+}
+
+rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides, int32_t q_heads,
+                           float scale, int32_t window, int32_t sinks, void* out, const rlk_bth_strides* out_strides,
+                           float* out_lse, void* workspace, const PrefixParts* parts, void* stream) {
+  rlk_status s = check_cache(cache);
+  if (s != RLK_OK) return s;
+  if (q_heads < 1 || q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads)
+    return fail(RLK_EINVAL, "q_heads %d must be 1 to 128 times kv_heads %d", q_heads, cache->kv_heads);
+  if (!isfinite(scale)) return fail(RLK_EINVAL, "scale %g must be finite", (double)scale);
+  if (window < 0 || sinks < 0) return fail(RLK_EINVAL, "window %d and sinks %d must be >= 0", window, sinks);
+  if (cache->B == 0 || cache->n == 0) return RLK_OK;
+  if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
+  if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
+  if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
+  if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
+  const int group = q_heads / cache->kv_heads;
+  const Tiling t = tiling_of(cache->n, group);
+  const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
+  if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
+    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
+  const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
+                             static_cast<int64_t>(cache->max_pages) * cache->page_size);
+  if (!workspace && y.bytes > 0) return fail(RLK_EINVAL, "workspace is NULL");
+  char* ws = static_cast<char*>(workspace);
+  AttnParams P{};
+  P.c = paged_params(cache);
+  P.q = q;
+  P.out = out;
+  P.qs = *q_strides;
+  P.os = *out_strides;
+  P.q_heads = q_heads;
+  P.group = group;
+  P.rows = t.rows;
+  P.tiles = t.tiles;
+  P.B = cache->B;
+  P.c2 = fabsf(scale) * 1.4426950408889634f;
+  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+  P.window = window;
+  P.sinks = window > 0 ? sinks : 0;
+  P.lse = out_lse;
+  if (parts) P.pre = *parts;
+  P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
+  P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
+  P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
+  P.group_o = reinterpret_cast<float*>(ws + y.group_o);
+  P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
+                                       : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
+  P.groups = static_cast<int>(y.groups);
+  P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
+  P.box = 1;
+  while (P.box < HALF && cache->page_size % (2 * P.box) == 0) P.box *= 2;
+  P.head_first = cache->kv_heads > 1 && (cache->page_size == 1 || cache->head_stride < cache->token_stride);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == RLK_DT_BF16;
+  if (cache->head_dim == 128)
+    return bf ? launch_rows<__nv_bfloat16, 128>(P, t.nt, st) : launch_rows<__half, 128>(P, t.nt, st);
+  return bf ? launch_rows<__nv_bfloat16, 64>(P, t.nt, st) : launch_rows<__half, 64>(P, t.nt, st);
 }
 
 }  // namespace rlk
@@ -1393,58 +1478,7 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
                                int32_t q_heads, float scale, int32_t window, int32_t sinks, void* out,
                                const rlk_bth_strides* out_strides, float* out_lse, void* workspace,
                                void* stream) {
-  rlk_status s = check_cache(cache);
-  if (s != RLK_OK) return s;
-  if (q_heads < 1 || q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads)
-    return fail(RLK_EINVAL, "q_heads %d must be 1 to 128 times kv_heads %d", q_heads, cache->kv_heads);
-  if (!isfinite(scale)) return fail(RLK_EINVAL, "scale %g must be finite", (double)scale);
-  if (window < 0 || sinks < 0) return fail(RLK_EINVAL, "window %d and sinks %d must be >= 0", window, sinks);
-  if (cache->B == 0 || cache->n == 0) return RLK_OK;
-  if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
-  if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
-  if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
-  if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
-  const int group = q_heads / cache->kv_heads;
-  const Tiling t = tiling_of(cache->n, group);
-  const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
-  if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
-    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
-  const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
-                             static_cast<int64_t>(cache->max_pages) * cache->page_size);
-  if (!workspace && y.bytes > 0) return fail(RLK_EINVAL, "workspace is NULL");
-  char* ws = static_cast<char*>(workspace);
-  AttnParams P{};
-  P.c = paged_params(cache);
-  P.q = q;
-  P.out = out;
-  P.qs = *q_strides;
-  P.os = *out_strides;
-  P.q_heads = q_heads;
-  P.group = group;
-  P.rows = t.rows;
-  P.tiles = t.tiles;
-  P.B = cache->B;
-  P.c2 = fabsf(scale) * 1.4426950408889634f;
-  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
-  P.window = window;
-  P.sinks = window > 0 ? sinks : 0;
-  P.lse = out_lse;
-  P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
-  P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
-  P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
-  P.group_o = reinterpret_cast<float*>(ws + y.group_o);
-  P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
-                                       : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
-  P.groups = static_cast<int>(y.groups);
-  P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
-  P.box = 1;
-  while (P.box < HALF && cache->page_size % (2 * P.box) == 0) P.box *= 2;
-  P.head_first = cache->kv_heads > 1 && (cache->page_size == 1 || cache->head_stride < cache->token_stride);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = cache->dtype == RLK_DT_BF16;
-  if (cache->head_dim == 128)
-    return bf ? launch_rows<__nv_bfloat16, 128>(P, t.nt, st) : launch_rows<__half, 128>(P, t.nt, st);
-  return bf ? launch_rows<__nv_bfloat16, 64>(P, t.nt, st) : launch_rows<__half, 64>(P, t.nt, st);
+  return paged_attention(cache, q, q_strides, q_heads, scale, window, sinks, out, out_strides, out_lse, workspace, nullptr, stream);
 }
 
 }  // extern "C"

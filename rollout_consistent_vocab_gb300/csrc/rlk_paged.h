@@ -31,6 +31,28 @@ __device__ __forceinline__ bool seq_lens(const PagedParams& P, int b, int& len, 
          len <= static_cast<int64_t>(P.max_pages) * P.page_size;
 }
 
+// Attention over the first tokens of each sequence, done before: what paged attention
+// over the rest joins to its own.
+struct PrefixParts {
+  const int32_t* first;         // [B] tokens that the parts cover, a multiple of 32; -1: the sequence is rejected
+  const float2* ml;             // [B][kv_heads][n * group][pieces]: maximum (base 2), sum
+  const float* o;               // ... and the weighted sum of values [head_dim]
+  int pieces;
+};
+// Tokens of a part.  By the covered length alone, so that a sequence's result does not
+// depend on its batch: more parts where there are few tokens (one to an SM), fewer
+// where there are many (a part's result is as much to write and read as 64 tokens are).
+__host__ __device__ __forceinline__ int piece_tokens(int covered) { return covered < 8192 ? 512 : covered < 32768 ? 1024 : 2048; }
+__host__ __device__ __forceinline__ int pieces_of(int covered) {
+  const int t = piece_tokens(covered);
+  return covered / t + (covered % t != 0);
+}
+
+// rlk_paged_attention, without the tokens that `parts` (NULL: none) covers.
+rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides, int32_t q_heads,
+                           float scale, int32_t window, int32_t sinks, void* out, const rlk_bth_strides* out_strides,
+                           float* out_lse, void* workspace, const PrefixParts* parts, void* stream);
+
 rlk_status check_cache(const rlk_kv_cache* c);
 rlk_status check_bth(const void* p, const rlk_bth_strides* s, const char* what);
 PagedParams paged_params(const rlk_kv_cache* c);
