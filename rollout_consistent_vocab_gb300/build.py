@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("rlk_logp.cu", "rlk_shard.cu", "rlk_grad.cu", "rlk_noalloc.cu",
                                           "rlk_linear.cu", "rlk_norm.cu", "rlk_host_io.cu", "rlk_paged.cu", "rlk_verify.cu", "rlk_rope.cu", "rlk_prefix.cu")]
-HEADERS = [os.path.join(CSRC, "rlk_device.cuh"), os.path.join(CSRC, "rlk_host.h"), os.path.join(CSRC, "rlk_paged.h")]
+HEADERS = [os.path.join(CSRC, "rlk_device.cuh"), os.path.join(CSRC, "rlk_host.h"), os.path.join(CSRC, "rlk_paged.h"),
+           os.path.join(CSRC, "rlk_tcgen05.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "librlk_logp.so")

@@ -45,6 +45,7 @@
 #include "rlk_logp.h"
 #include "rlk_device.cuh"
 #include "rlk_host.h"
+#include "rlk_tcgen05.cuh"
 
 namespace rlk {
 
@@ -158,22 +159,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-               :: "r"(dst_smem), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
 // D[tmem] (+)= A[smem] . B[smem]^T, one elected thread
 __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t accumulate) {
@@ -181,19 +166,6 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(accumulate), "r"(LIN_IDESC) : "memory");
-}
-// arrive on a barrier once every tcgen05 operation this thread issued is done
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(bar) : "memory");
-}
-// Shared-memory matrix descriptor of a K-major tile in the 128-byte swizzle
-// layout: start address >> 4 (bits 0-13), leading byte offset 16 B (unused by
-// swizzled K-major tiles), stride byte offset 1024 B = 8 rows x 128 B (bits
-// 32-45), descriptor version 1 (bit 46), layout 128-byte swizzle (2 at bit 61).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
 }
 // 32 TMEM lanes x 32 columns of 32-bit values: thread i of the warp gets lane
 // (base lane + i), columns col .. col + 31.
@@ -215,10 +187,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 }
 
 // ------------------------------------------------------------ kernels
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
 
 // Persistent: one CTA per SM walks the tiles tile = blockIdx.x + i * gridDim.x
 // (row tiles fastest, so the CTAs running at one time share a vocabulary tile

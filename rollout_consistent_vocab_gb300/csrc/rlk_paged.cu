@@ -13,6 +13,7 @@
 #include "rlk_device.cuh"
 #include "rlk_host.h"
 #include "rlk_paged.h"
+#include "rlk_tcgen05.cuh"
 
 namespace rlk {
 
@@ -178,7 +179,7 @@ struct AttnParams {
   float* unit_o;                // ... and the weighted sum of values [D]
   float2* group_ml;             // [B * kv_heads * tiles * groups][8 NT]
   float* group_o;
-  uint32_t page_magic;          // 2^32 / page_size, rounded up (page_size 1: 2^32 - 1)
+  uint32_t page_magic;
   uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
   uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
@@ -443,14 +444,6 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap& map, int c0, int c1, int c2, int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Waits for a phase of a barrier, at most TIMEOUT_NS twice over.
 __device__ __forceinline__ bool mbar_wait_phase(uint32_t bar, uint32_t parity) {
   if (mbar_try(bar, parity)) return true;
@@ -528,10 +521,7 @@ __device__ __forceinline__ void copy_run(const AttnParams& P, const AttnMaps& ma
     const int t = p.s.unit(p.li) * UNIT + (__ffs(slices) - 1) * SL + lane;
     slices &= slices - 1;
     seen = t < p.s.len && (t >= p.s.low || t < P.sinks);
-    uint32_t n = __umulhi(static_cast<uint32_t>(t), P.page_magic);
-    place = static_cast<int>(static_cast<uint32_t>(t) - n * static_cast<uint32_t>(P.c.page_size));
-    if (place < 0) place += P.c.page_size, --n;            // the quotient is one off at most
-    if (place >= P.c.page_size) place -= P.c.page_size, ++n;
+    const uint32_t n = page_of(P.c, P.page_magic, t, place);
     page = seen ? __ldg(P.c.table + p.b * P.c.table_stride + n) : -1;
     return true;
   };
@@ -1292,10 +1282,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The cache's keys or values as a tensor of (element, token of the page, head, page),
-// the middle two in the order of their strides; a copy takes 64 elements of
-// P.box tokens of a head.
-rlk_status map_cache(CUtensorMap* map, const AttnParams& P, const void* base, int D, bool bf16) {
+rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box_tokens, bool head_first, int D, bool bf16) {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -1307,14 +1294,14 @@ rlk_status map_cache(CUtensorMap* map, const AttnParams& P, const void* base, in
   }
   // a place of extent 1 is never stepped over: any stride does
   const cuuint64_t any = static_cast<cuuint64_t>(D) * 2;
-  const cuuint64_t token = P.c.page_size > 1 ? static_cast<cuuint64_t>(P.c.token_stride) * 2 : any;
-  const cuuint64_t head = P.c.kv_heads > 1 ? static_cast<cuuint64_t>(P.c.head_stride) * 2 : any;
-  const cuuint64_t page = P.c.num_pages > 1 ? static_cast<cuuint64_t>(P.c.page_stride) * 2 : any;
-  const cuuint64_t tokens = P.c.page_size, heads = P.c.kv_heads, pages = P.c.num_pages;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), P.head_first ? heads : tokens, P.head_first ? tokens : heads, pages};
-  const cuuint64_t strides[3] = {P.head_first ? head : token, P.head_first ? token : head, page};
-  const cuuint32_t box = static_cast<cuuint32_t>(P.box);
-  const cuuint32_t boxes[4] = {64, P.head_first ? 1 : box, P.head_first ? box : 1, 1}, ones[4] = {1, 1, 1, 1};
+  const cuuint64_t token = c.page_size > 1 ? static_cast<cuuint64_t>(c.token_stride) * 2 : any;
+  const cuuint64_t head = c.kv_heads > 1 ? static_cast<cuuint64_t>(c.head_stride) * 2 : any;
+  const cuuint64_t page = c.num_pages > 1 ? static_cast<cuuint64_t>(c.page_stride) * 2 : any;
+  const cuuint64_t tokens = c.page_size, heads = c.kv_heads, pages = c.num_pages;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), head_first ? heads : tokens, head_first ? tokens : heads, pages};
+  const cuuint64_t strides[3] = {head_first ? head : token, head_first ? token : head, page};
+  const cuuint32_t box = static_cast<cuuint32_t>(box_tokens);
+  const cuuint32_t boxes[4] = {64, head_first ? 1 : box, head_first ? box : 1, 1}, ones[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                         const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1332,8 +1319,8 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   AttnMaps maps;
   constexpr bool bf16 = sizeof(T) == 2 && Elem<T>::EXP == 0x7F807F80u;
   if (P.c.num_pages > 0) {
-    if ((s = map_cache(&maps.k, P, P.c.k, D, bf16)) != RLK_OK) return s;
-    if ((s = map_cache(&maps.v, P, P.c.v, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf16)) != RLK_OK) return s;
   }
   P.workers = Shape<D, NT>::WORKERS;
   attn_kernel<T, D, NT><<<P.workers, Shape<D, NT>::THREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
@@ -1420,13 +1407,11 @@ rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_b
   P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
   P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
   P.group_o = reinterpret_cast<float*>(ws + y.group_o);
-  P.page_magic = static_cast<uint32_t>(cache->page_size == 1 ? 0xFFFFFFFFull
-                                       : ((1ull << 32) + cache->page_size - 1) / cache->page_size);
+  P.page_magic = page_magic(cache->page_size);
   P.groups = static_cast<int>(y.groups);
   P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
-  P.box = 1;
-  while (P.box < HALF && cache->page_size % (2 * P.box) == 0) P.box *= 2;
-  P.head_first = cache->kv_heads > 1 && (cache->page_size == 1 || cache->head_stride < cache->token_stride);
+  P.box = box_of(cache->page_size, HALF);
+  P.head_first = heads_first(cache);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == RLK_DT_BF16;
   if (cache->head_dim == 128)

@@ -2,6 +2,7 @@
 // translation units that work on it share.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,6 +31,33 @@ __device__ __forceinline__ bool seq_lens(const PagedParams& P, int b, int& len, 
   return nnew >= 0 && nnew <= P.n && len >= nnew &&
          len <= static_cast<int64_t>(P.max_pages) * P.page_size;
 }
+
+// 2^32 / page_size, rounded up (page_size 1: 2^32 - 1), and by it the page of token t in its
+// sequence's list, with its place in the page.
+inline uint32_t page_magic(int page_size) {
+  return static_cast<uint32_t>(page_size == 1 ? 0xFFFFFFFFull : ((1ull << 32) + page_size - 1) / page_size);
+}
+__device__ __forceinline__ uint32_t page_of(const PagedParams& P, uint32_t magic, int t, int& place) {
+  uint32_t n = __umulhi(static_cast<uint32_t>(t), magic);
+  place = static_cast<int>(static_cast<uint32_t>(t) - n * static_cast<uint32_t>(P.page_size));
+  if (place < 0) place += P.page_size, --n;                // the quotient is one off at most
+  if (place >= P.page_size) place -= P.page_size, ++n;
+  return n;
+}
+// Tokens of a copy: the largest power of 2, up to `most`, that divides the page.
+inline int box_of(int page_size, int most) {
+  int box = 1;
+  while (box < most && page_size % (2 * box) == 0) box *= 2;
+  return box;
+}
+// Whether the tensor maps' second place is the head, not the token.
+inline bool heads_first(const rlk_kv_cache* c) {
+  return c->kv_heads > 1 && (c->page_size == 1 || c->head_stride < c->token_stride);
+}
+// The cache's keys or values as a tensor of (element, token of the page, head, page),
+// the middle two in the order of their strides; a copy takes 64 elements of
+// `box` tokens of a head.
+rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box, bool head_first, int D, bool bf16);
 
 // Attention over the first tokens of each sequence, done before: what paged attention
 // over the rest joins to its own.

@@ -6,6 +6,7 @@
 // (maximum, sum, weighted sum of values of each query row) goes to the workspace.  Then
 // paged attention takes every sequence's other tokens, and its join adds the pieces first.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,6 +17,7 @@
 #include "rlk_device.cuh"
 #include "rlk_host.h"
 #include "rlk_paged.h"
+#include "rlk_tcgen05.cuh"
 
 namespace rlk {
 
@@ -40,10 +42,20 @@ struct PrefixParams {
   int q_heads, group;           // group: query heads of a kv head
   int rows;                     // n * group: of a sequence and kv head
   int max_pieces;
-  float c2;                     // scale * log2(e)
+  float c2;                     // |scale| * log2(e)
+  uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
+  int box;                      // tokens of a copy
+  bool head_first;
+  uint32_t page_magic;
   float2* ml;
   float* o;
 };
+
+// Items of a group: its pieces, for every kv head and block of 256 query rows.
+__device__ __forceinline__ uint32_t items_of(const PrefixParams& P, const GroupPlan& p) {
+  const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows;
+  return (rows + 255u) / 256u * P.c.kv_heads * p.pieces;
+}
 
 // ------------------------------------------------------------ the plan
 
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
       p.pieces = pieces_of(p.shared);
     }
     P.plan[g] = p;
-    mine += p.pieces;
+    mine += items_of(P, p);
   }
   scan[tid] = mine;
   __syncthreads();
@@ -107,65 +119,561 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
   uint32_t run = scan[tid] - mine;
   for (int g = g0; g < g1; ++g) {
     P.base[g] = run;
-    run += P.plan[g].pieces;
+    run += items_of(P, P.plan[g]);
   }
   if (tid == PLAN_THREADS - 1) P.base[G] = run;
 }
 
 // ------------------------------------------------------------ the shared tokens
+//
+// S = Q K^T and O += P V run on tcgen05: 128 query rows as the accumulator's rows, 128
+// tokens a tile, everything between in tensor memory.  A CTA has two streams of tiles, each
+// with scores (128 columns of tensor memory) and a result (head_dim columns) of its own:
+// while a stream's warps take the exponentials of one tile, the tensor cores are at the
+// other stream's.  A group with up to 128 query rows per kv head gives its streams pieces
+// of their own; with more, both streams take the same piece, with 128 rows each, and
+// every tile of keys and values is read once for 256 rows.
+//
+//   warps 0-3, 4-7   a stream's: a thread to a query row.  It reads its 128 scores, keeps
+//                    a reference maximum (which follows the row's maximum where that runs
+//                    SLACK ahead; then the result so far is scaled in tensor memory) and
+//                    the sum, and writes the weights over the scores as two elements
+//                    of the cache's dtype each (hi, then what hi dropped): an operand of
+//                    the second product as it lies.  At a piece's end it takes the result out.
+//   warp 8           one thread issues the products
+//   warp 9           copies keys and values, in the order in which they are needed, into one
+//                    ring of tiles (TMA boxes of as many tokens as lie together in a page)
+//
+// Shared tokens come in multiples of 32, so that a piece's last tile needs no masks: the
+// scores of what is not there are not read, and the second product ends before it.
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <class T> struct WeightUnit;    // paged attention's: weights are in units of 2^-OFF of the reference
-template <> struct WeightUnit<__nv_bfloat16> { static constexpr float OFF = 0.0f; };
-template <> struct WeightUnit<__half> { static constexpr float OFF = 8.0f; };
+using bf16_t = __nv_bfloat16;
 
-// A warp per query row and piece, one token after the other.
-template <class T, int D>
-__global__ void __launch_bounds__(256) prefix_kernel(const PrefixParams P) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int g = 0; g < P.groups; ++g) {
-    const GroupPlan pl = P.plan[g];
+template <class T> struct Weights;
+template <> struct Weights<bf16_t> {
+  static constexpr uint32_t FORMAT = 1;            // of the instruction descriptor
+  // weights are in units of 2^-OFF of the reference, so below 2^(OFF + SLACK); the pieces' in paged attention's
+  static constexpr float OFF = 0.0f, SLACK = 8.0f, TO_PIECES = 1.0f;
+  // hi is cut off; lo is the rest and 2^-22 of the weight, so that both parts of a weight
+  // above 0 are above 0, and an infinite value comes through as itself
+  static constexpr float MORE = 1.0f + 2.384185791015625e-07f;
+  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    hi = __byte_perm(x, y, 0x7632);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(a, MORE, -__uint_as_float(x & 0xFFFF0000u)),
+                                                   __fmaf_rn(b, MORE, -__uint_as_float(y & 0xFFFF0000u)));
+    lo = *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+// f16: 22 bits of a weight, and steps of 2^-24 below: 2^-37 of the reference.  (Paged attention
+// gives the low parts a scale and an accumulator of their own; here tensor memory has no
+// room for one, so the reference stays close to the maximum and the unit is as small as it can be.)
+template <> struct Weights<__half> {
+  static constexpr uint32_t FORMAT = 0;
+  static constexpr float OFF = 13.0f, SLACK = 2.0f, TO_PIECES = 1.0f / 32.0f;
+  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16
+  static __device__ __forceinline__ float rest(float a, float h) {
+    const float r = __fsub_rn(a, h);
+    return a >= TINY ? fmaxf(r, TINY) : r;
+  }
+  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const __half2 r = __floats2half2_rn(rest(a, h.x), rest(b, h.y));
+    lo = *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+
+constexpr int PTILE = 128;               // tokens of a tile, and rows
+constexpr int PROWS = 2 * PTILE;         // query rows of a CTA
+constexpr int PTHREADS = 320;
+template <int D>
+struct PShape {
+  static constexpr int PANEL = PTILE * 128;        // 64 elements of every row, 128-byte swizzle
+  static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int BARS = 2 * STAGES + 2 * 4 + 1;
+  static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BARS * 8 + 16;
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
+struct PrefixMaps { CUtensorMap k, v; };
+
+// The items in equal runs, the first ones one longer.
+__device__ __forceinline__ uint32_t run_start(uint32_t items, uint32_t workers, uint32_t k) {
+  const uint32_t len = items / workers, more = items - len * workers;
+  return k * len + min(k, more);
+}
+
+// What the two streams take side by side: a piece each of a group's kv head, or one piece
+// with rows of their own.
+struct Step {
+  int seq0, seqs, head, rb, piece;
+  int t0, size;                          // the first piece's first token, tokens of a full piece
+  int len0, len1;                        // tokens of the streams' pieces (0: none)
+  bool both;                             // the same piece
+  __device__ __forceinline__ int tokens(int s) const { return s ? len1 : len0; }
+  __device__ __forceinline__ int tiles(int s) const { return (tokens(s) + PTILE - 1) / PTILE; }
+  __device__ __forceinline__ int from(int s) const { return both || s == 0 ? t0 : t0 + size; }
+  __device__ __forceinline__ int piece_of(int s) const { return both || s == 0 ? piece : piece + 1; }
+};
+// The rows that a stream has the queries of.
+struct Rows {
+  int seq0 = -1, head = 0, rb = 0;
+  __device__ __forceinline__ bool of(const Step& x) const { return seq0 == x.seq0 && head == x.head && rb == x.rb; }
+  __device__ __forceinline__ void take(const Step& x) { seq0 = x.seq0, head = x.head, rb = x.rb; }
+};
+// A tile's product: of a stream's step, tokens t .. t + count - 1.
+struct Tile {
+  int seq0, head, t, count;
+  bool both, first, last;                // of its piece
+};
+// A CTA's way through its run of items: an item is a piece of a group, kv head and block of rows.
+struct Way {
+  uint32_t at, end;
+  int g, head, rb, piece, rows, rbs;
+  GroupPlan pl;
+  __device__ __forceinline__ void load(const PrefixParams& P) {
+    pl = P.plan[g];
+    rows = pl.seqs * P.rows;
+    rbs = (rows + PROWS - 1) / PROWS;
+  }
+  __device__ __forceinline__ void find(const PrefixParams& P) {        // the group that holds item `at`
+    int lo = g, hi = P.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (P.base[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    g = lo;
+    load(P);
+  }
+  __device__ __forceinline__ Way(const PrefixParams& P, uint32_t a, uint32_t e) : at(a), end(e), g(0) {
+    find(P);
+    const uint32_t rest = a - P.base[g], pieces = max(pl.pieces, 1), x = rest / pieces;
+    piece = static_cast<int>(rest - x * pieces);
+    head = static_cast<int>(x / max(rbs, 1));
+    rb = static_cast<int>(x - static_cast<uint32_t>(head) * max(rbs, 1));
+  }
+  // The next step; false at the run's end.
+  __device__ __forceinline__ bool next(const PrefixParams& P, Step& s) {
+    if (at >= end) return false;
     const int size = piece_tokens(pl.shared);
-    const int64_t all = static_cast<int64_t>(pl.seqs) * P.c.kv_heads * P.rows * pl.pieces;
-    for (int64_t w = blockIdx.x * 8ll + threadIdx.x / 32; w < all; w += warps) {
-      const int piece = static_cast<int>(w % pl.pieces);
-      int64_t rest = w / pl.pieces;
-      const int row = static_cast<int>(rest % P.rows);
-      rest /= P.rows;
-      const int h = static_cast<int>(rest % P.c.kv_heads), b = pl.seq0 + static_cast<int>(rest / P.c.kv_heads);
-      const int i = row / P.group, nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
-      if (P.first[b] < 0 || i >= nnew) continue;
-      const T* q = static_cast<const T*>(P.q) + b * P.qs.batch + i * P.qs.token + (h * P.group + row % P.group) * P.qs.head + lane * E;
-      float qv[E], o[E] = {}, m = -INFINITY, l = 0.0f;
-      for (int e = 0; e < E; ++e) qv[e] = to_float(q[e]);
-      for (int t = piece * size; t < min(pl.shared, (piece + 1) * size); ++t) {
-        const int page = P.c.table[pl.seq0 * P.c.table_stride + t / P.c.page_size];
-        if (page < 0 || page >= P.c.num_pages) {
-          l = NAN;
-          if (lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-          break;
-        }
-        const int64_t at = page * P.c.page_stride + t % P.c.page_size * P.c.token_stride + h * P.c.head_stride + lane * E;
-        const T* k = static_cast<const T*>(P.c.k) + at;
-        const T* v = static_cast<const T*>(P.c.v) + at;
-        float x = 0.0f;
-        for (int e = 0; e < E; ++e) x += qv[e] * to_float(k[e]);
-        for (int z = 16; z > 0; z >>= 1) x += __shfl_xor_sync(0xffffffffu, x, z);
-        x *= P.c2;
-        const float top = fmaxf(m, x);
-        const float old = m == -INFINITY ? 0.0f : exp2f(m - top), wt = exp2f(x - (top == -INFINITY ? 0.0f : top) + WeightUnit<T>::OFF);
-        m = top;
-        l = l * old + wt;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * old + wt * to_float(v[e]);
+    s.seq0 = pl.seq0, s.seqs = pl.seqs, s.head = head, s.rb = rb, s.piece = piece, s.t0 = piece * size, s.size = size;
+    s.both = rows - rb * PROWS > PTILE;
+    const bool pair = !s.both && piece + 1 < pl.pieces && at + 1 < end;
+    s.len0 = min(size, pl.shared - s.t0);
+    s.len1 = s.both ? s.len0 : pair ? min(size, pl.shared - s.t0 - size) : 0;
+    const int used = pair ? 2 : 1;
+    at += used;
+    piece += used;
+    if (piece >= pl.pieces && at < end) {
+      piece = 0;
+      if (++rb == rbs) rb = 0, ++head;
+      if (head == P.c.kv_heads) {
+        head = 0;
+        ++g;
+        load(P);
+        if (pl.pieces == 0) find(P);
       }
-      const int64_t slot = ((static_cast<int64_t>(b) * P.c.kv_heads + h) * P.rows + row) * P.max_pieces + piece;
-      if (lane == 0) P.ml[slot] = make_float2(m, l);
-      for (int e = 0; e < E; ++e) P.o[slot * D + lane * E + e] = o[e];
+    }
+    return true;
+  }
+  // Every product of the run in order: qk(s, tile, asks) for scores (asks: the stream's queries are other
+  // ones than before), pv(s, tile) for results.
+  template <class QK, class PV>
+  __device__ __forceinline__ void walk(const PrefixParams& P, QK qk, PV pv) {
+    Step cur, nxt;
+    Rows held[2];
+    bool have = next(P, cur);
+    for (int j = -1; have; j = 0) {
+      const bool more = next(P, nxt);
+      const int tiles = max(cur.tiles(0), cur.tiles(1));
+#pragma unroll 1
+      for (; j < tiles; ++j) {
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const int mine = cur.tiles(s), t0 = cur.from(s);
+          if (j >= 0 && j < mine)
+            pv(s, Tile{cur.seq0, cur.head, t0 + j * PTILE, min(PTILE, cur.tokens(s) - j * PTILE), cur.both, j == 0, j + 1 == mine});
+          const bool here = j + 1 < mine;
+          if (!here && !(j + 1 == tiles && more && nxt.tokens(s) > 0)) continue;
+          Rows want;
+          want.take(here ? cur : nxt);
+          Rows& old = held[s];
+          const bool asks = old.seq0 != want.seq0 || old.head != want.head || old.rb != want.rb;
+          old = want;
+          if (here)
+            qk(s, Tile{cur.seq0, cur.head, t0 + (j + 1) * PTILE, min(PTILE, cur.tokens(s) - (j + 1) * PTILE), cur.both, j < 0, false}, asks);
+          else
+            qk(s, Tile{nxt.seq0, nxt.head, nxt.from(s), min(PTILE, nxt.tokens(s)), nxt.both, true, false}, asks);
+        }
+      }
+      cur = nxt;
+      have = more;
     }
   }
+};
+
+// D[tmem] (+)= A . B^T, one thread: A in shared or in tensor memory
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}"
+               :: "r"(d), "l"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(idesc) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}"
+               :: "r"(d), "r"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(idesc) : "memory");
+}
+// 32 columns of the warp's 32 lanes of tensor memory, a lane to a thread; what is loaded is there after the wait
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (keeps uses of the registers behind the wait)
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
+  asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                    "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+      :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) a[j] = r[j], b[j] = r[16 + j];
+  tmem_st16(taddr, a);
+  tmem_st16(taddr + 16, b);
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The descriptor of the values' tile as the operand whose rows are the tokens (128-byte
+// swizzle): 64 elements of 8 tokens are an atom of 1024 bytes, 8 tokens further on is
+// 1024 bytes on, the next 64 elements a panel on.
+__device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t panel) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(panel >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+__device__ __forceinline__ void store8(float* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(PTHREADS, 1)
+prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps maps) {
+  using S_ = PShape<D>;
+  using W = Weights<T>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t raw = smem_addr(smem_raw), queries = (raw + 1023u) & ~1023u, ring = queries + 2 * S_::TILE;
+  const uint32_t bars = ring + S_::STAGES * S_::TILE;
+  const uint32_t full = bars, empty = bars + 8 * S_::STAGES, streams = empty + 8 * S_::STAGES;
+  const uint32_t scored = streams, weighed = streams + 16, summed = streams + 32, asked = streams + 48, last = streams + 64;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 72 - raw));
+  volatile uint32_t* const dead = slot + 1;        // a wait gave up: everything ends, within limits
+  const uint32_t items = P.base[P.groups], workers = min(items, gridDim.x);
+  if (blockIdx.x >= workers) return;
+  if (tid == 0) {
+    for (int s = 0; s < S_::STAGES; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(scored + 8 * s, 1);
+      mbar_init(weighed + 8 * s, 4);
+      mbar_init(summed + 8 * s, 1);
+      mbar_init(asked + 8 * s, 4);
+    }
+    mbar_init(last, 1);
+    *dead = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  Way way(P, run_start(items, workers, blockIdx.x), run_start(items, workers, blockIdx.x + 1));
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (mbar_try(bar, parity & 1)) return true;
+    const unsigned long long t0 = global_timer();
+    while (!mbar_try(bar, parity & 1)) {
+      if (*dead) return false;
+      if (global_timer() - t0 > 2 * TIMEOUT_NS) {
+        *dead = 1u;
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp == 9) {
+    // ---- copies
+    uint32_t n = 0;                      // tiles so far
+    auto fill = [&](const CUtensorMap& map, const Tile& x) {
+      const uint32_t stage = n % S_::STAGES, bar = full + 8 * stage, dst = ring + stage * S_::TILE + lane * 128;
+      uint32_t page[4], boxes = 0;       // of tokens lane, lane + 32, ..; whether the lane speaks for a box there
+      int place[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int in = y * 32 + lane;
+        bool there = in % P.box == 0 && in < x.count;
+        if (there) {
+          const uint32_t number = page_of(P.c, P.page_magic, x.t + in, place[y]);
+          page[y] = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
+          there = page[y] < P.c.num_pages;
+        }
+        boxes |= (there ? 1u : 0u) << y;
+      }
+      const uint32_t all = __reduce_add_sync(0xffffffffu, __popc(boxes));
+      const bool go = n < S_::STAGES || wait(empty + 8 * stage, n / S_::STAGES - 1);
+      ++n;
+      if (__any_sync(0xffffffffu, !go)) return;
+      if (lane == 0) mbar_arrive_expect_tx(bar, all * P.box * D * 2);
+      __syncwarp();
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (!((boxes >> y) & 1u)) continue;
+        const int c1 = P.head_first ? x.head : place[y], c2 = P.head_first ? place[y] : x.head;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) copy_box(dst + c * S_::PANEL + y * 32 * 128, map, c * 64, c1, c2, page[y], bar);
+      }
+    };
+    way.walk(P, [&](int s, const Tile& x, bool) { if (!(x.both && s == 1)) fill(maps.k, x); },
+             [&](int s, const Tile& x) { if (!(x.both && s == 1)) fill(maps.v, x); });
+    // where the products ended early, the CTA stays for its last copies
+    if (*dead)
+      for (uint32_t k = n > S_::STAGES ? n - S_::STAGES : 0; k < n; ++k) {
+        const unsigned long long t0 = global_timer();
+        while (!mbar_try(full + 8 * (k % S_::STAGES), (k / S_::STAGES) & 1) && global_timer() - t0 < TIMEOUT_NS) {}
+      }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      // ---- products
+      constexpr uint32_t IDESC = (1u << 4) | (W::FORMAT << 7) | (W::FORMAT << 10) | (static_cast<uint32_t>(PTILE >> 4) << 24);
+      constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE >> 3) << 17);
+      constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
+      uint32_t n = 0, key_stage = 0, value_stage = 0;
+      uint32_t weights0 = 0, weights1 = 0, asked0 = 0, asked1 = 0;   // waits so far
+      way.walk(P,
+          [&](int s, const Tile& x, bool asks) {
+            if (asks) wait(asked + 8 * s, s ? asked1++ : asked0++);
+            if (!(x.both && s == 1)) {
+              key_stage = n % S_::STAGES;
+              wait(full + 8 * key_stage, n / S_::STAGES);
+              ++n;
+            }
+            if (*dead) return;
+            tc_fence_after();
+            const uint64_t a = sw128_desc(queries + s * S_::TILE), b = sw128_desc(ring + key_stage * S_::TILE);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k / 4 * S_::PANEL + k % 4 * 32) >> 4;
+              umma_ss(tmem + s * PTILE, a + off, b + off, IDESC_QK, k > 0);
+            }
+            if (!(x.both && s == 0)) umma_commit(empty + 8 * key_stage);
+            umma_commit(scored + 8 * s);
+          },
+          [&](int s, const Tile& x) {
+            if (!(x.both && s == 1)) {
+              value_stage = n % S_::STAGES;
+              wait(full + 8 * value_stage, n / S_::STAGES);
+              ++n;
+            }
+            wait(weighed + 8 * s, s ? weights1++ : weights0++);
+            if (*dead) return;
+            tc_fence_after();
+            const uint64_t b = values_desc(ring + value_stage * S_::TILE, S_::PANEL);
+            const uint32_t d = tmem + 2 * PTILE + s * 128, a = tmem + s * PTILE;
+            const int steps = x.count / 16;
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) umma_ts(d, a + k / 2 * 32 + 16 + k % 2 * 8, b + 128 * k, IDESC_PV, !x.first || k > 0);
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) umma_ts(d, a + k / 2 * 32 + k % 2 * 8, b + 128 * k, IDESC_PV, true);
+            if (!(x.both && s == 0)) umma_commit(empty + 8 * value_stage);
+            if (x.last) umma_commit(summed + 8 * s);
+          });
+      umma_commit(last);                 // nothing is left under way when tensor memory is given back
+      const unsigned long long t0 = global_timer();
+      while (!mbar_try(last, 0) && global_timer() - t0 < TIMEOUT_NS) {}
+    }
+    __syncwarp();
+  } else {
+    // ---- exponentials: a thread to a query row
+    const int s = warp >> 2, row = tid & (PTILE - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t scores = tmem + s * PTILE + lanes, result = tmem + 2 * PTILE + s * 128 + lanes;
+    uint32_t tiles = 0, pieces = 0;      // waits so far
+    Step st, nxt;
+    Rows held;
+    bool have = way.next(P, st);
+    int64_t out = -1;                    // the row's first part, in parts; -1: no query
+    auto ask = [&](const Step& x) {      // the queries of the stream's rows of x
+      held.take(x);
+      const int at = x.rb * PROWS + (x.both ? s * PTILE : 0) + row, k = at / P.rows, r = at - k * P.rows, i = r / P.group, b = x.seq0 + k;
+      out = -1;
+      const uint4* src = nullptr;
+      if (k < x.seqs) {
+        const int nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
+        if (P.first[b] >= 0 && i < nnew) {
+          out = ((static_cast<int64_t>(b) * P.c.kv_heads + x.head) * P.rows + r) * P.max_pieces;
+          src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + b * P.qs.batch + i * P.qs.token +
+                                               (x.head * P.group + (r - i * P.group)) * P.qs.head);
+        }
+      }
+      const uint32_t dst = queries + s * S_::TILE + row * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 v = src ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        v.x ^= P.q_sign, v.y ^= P.q_sign, v.z ^= P.q_sign, v.w ^= P.q_sign;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(dst + c / 8 * S_::PANEL + ((c & 7) ^ (row & 7)) * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(asked + 8 * s);
+    };
+    for (; have; st = nxt) {
+      const bool more = way.next(P, nxt);
+      const int all = st.tokens(s);
+      if (all > 0) {
+        if (!held.of(st)) ask(st);
+        // whether all the piece's pages are there
+        bool bad = false;
+        {
+          int place;
+          const int to = static_cast<int>(page_of(P.c, P.page_magic, st.from(s) + all - 1, place));
+          for (int p = static_cast<int>(page_of(P.c, P.page_magic, st.from(s), place)) + lane; p <= to; p += 32) {
+            const int page = __ldg(P.c.table + st.seq0 * P.c.table_stride + p);
+            bad |= page < 0 || page >= P.c.num_pages;
+          }
+          bad = __any_sync(0xffffffffu, bad);
+        }
+        const int64_t slot_at = out + st.piece_of(s);
+        const bool query = out >= 0;
+        float m = -INFINITY, l = 0.0f;
+        const int count = st.tiles(s);
+#pragma unroll 1
+        for (int j = 0; j < count; ++j) {
+          const int chunks = min(PTILE, all - j * PTILE) / 32;
+          wait(scored + 8 * s, tiles++);
+          __syncwarp();
+          tc_fence_after();
+          // the scores are read twice, 64 at a time: once for the maximum, once for the weights
+          float top = -INFINITY;
+#pragma unroll
+          for (int c0 = 0; c0 < 4; c0 += 2) {
+            if (c0 >= chunks) break;
+            uint32_t x[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld32_async(scores + 32 * (c0 + c), x[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_loaded(x[c]);
+              if (c0 + c < chunks) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+              }
+            }
+          }
+          top *= P.c2;
+          float fac = 1.0f;
+          if (top > m + W::SLACK) {
+            if (m != -INFINITY) fac = ex2(m - top);
+            m = top;
+          }
+          if (__any_sync(0xffffffffu, fac != 1.0f)) {
+            l *= fac;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t y[32];
+              tmem_ld32_async(result + 32 * c, y);
+              tmem_wait_ld();
+              tmem_loaded(y);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fac);
+              tmem_st32(result + 32 * c, y);
+            }
+          }
+          const float sub = m == -INFINITY ? W::OFF : W::OFF - m;
+          float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int c0 = 0; c0 < 4; c0 += 2) {
+            if (c0 >= chunks) break;
+            uint32_t x[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld32_async(scores + 32 * (c0 + c), x[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_loaded(x[c]);
+              if (c0 + c < chunks) {
+                // 32 scores become 16 words of hi and 16 of lo, in their place
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float a = ex2(__fmaf_rn(__uint_as_float(x[c][2 * e]), P.c2, sub));
+                  const float b = ex2(__fmaf_rn(__uint_as_float(x[c][2 * e + 1]), P.c2, sub));
+                  sum[0] += a;
+                  sum[1] += b;
+                  W::split(a, b, hi[e], lo[e]);
+                }
+                tmem_st16(scores + 32 * (c0 + c), hi);
+                tmem_st16(scores + 32 * (c0 + c) + 16, lo);
+              }
+            }
+          }
+          l += sum[0] + sum[1];
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(weighed + 8 * s);
+        }
+        if (more && nxt.tokens(s) > 0 && !held.of(nxt)) ask(nxt);        // (all products with the old ones are done)
+        bad |= !wait(summed + 8 * s, pieces++) || *dead != 0u;
+        bad = __any_sync(0xffffffffu, bad);
+        tc_fence_after();
+        if (bad && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t y[32];
+          tmem_ld32_async(result + 32 * c, y);
+          tmem_wait_ld();
+          tmem_loaded(y);
+          if (query) {
+            if constexpr (W::TO_PIECES != 1.0f) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * W::TO_PIECES);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store8(P.o + slot_at * D + 32 * c + e, y + e);
+          }
+          __syncwarp();
+        }
+        if (query) P.ml[slot_at] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
+      }
+      have = more;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------ host side
@@ -175,6 +683,26 @@ struct PrefixLayout {
   size_t first, plan, busy, base, ml, o, rest, bytes;
   int pieces;
 };
+template <class T, int D>
+static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cudaStream_t st) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
+    e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<D>::SMEM);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+  }
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "function attributes: %s", cudaGetErrorString(e));
+  PrefixMaps maps{};
+  rlk_status s;
+  if (P.c.num_pages > 0) {
+    const bool bf = cache->dtype == RLK_DT_BF16;
+    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, D, bf)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf)) != RLK_OK) return s;
+  }
+  prefix_kernel<T, D><<<152, PTHREADS, PShape<D>::SMEM, st>>>(P, maps);
+  return RLK_OK;
+}
 static size_t lined(size_t x) { return (x + 127) / 128 * 128; }
 static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t head_dim, int groups, int max_shared, size_t rest) {
   PrefixLayout y{};
@@ -231,6 +759,9 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   if (cache->B == 0 || cache->n == 0) return RLK_OK;
   if (groups->groups > 0 && (!groups->group_start || !groups->shared_lens))
     return fail(RLK_EINVAL, "group_start or shared_lens is NULL");
+  const double rows = static_cast<double>(cache->B) * cache->n * (q_heads / cache->kv_heads);
+  if (rows >= 2147483392.0 || (rows / 256 + groups->groups) * cache->kv_heads * (groups->max_shared / 512 + 1.0) >= 2147483648.0)
+    return fail(RLK_EINVAL, "too many query rows and shared tokens for one call");
   if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
   if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
   if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
@@ -258,18 +789,21 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.group = q_heads / cache->kv_heads;
   P.rows = cache->n * P.group;
   P.max_pieces = y.pieces;
-  P.c2 = scale * 1.4426950408889634f;
+  P.c2 = fabsf(scale) * 1.4426950408889634f;
+  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+  P.box = box_of(cache->page_size, PTILE);
+  P.head_first = heads_first(cache);
+  P.page_magic = page_magic(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   plan_kernel<<<1, PLAN_THREADS, 0, st>>>(P);
   if (y.pieces > 0 && groups->groups > 0) {
     const bool bf = cache->dtype == RLK_DT_BF16;
     if (cache->head_dim == 128) {
-      if (bf) prefix_kernel<__nv_bfloat16, 128><<<152 * 8, 256, 0, st>>>(P);
-      else prefix_kernel<__half, 128><<<152 * 8, 256, 0, st>>>(P);
+      s = bf ? launch_prefix<bf16_t, 128>(P, cache, st) : launch_prefix<__half, 128>(P, cache, st);
     } else {
-      if (bf) prefix_kernel<__nv_bfloat16, 64><<<152 * 8, 256, 0, st>>>(P);
-      else prefix_kernel<__half, 64><<<152 * 8, 256, 0, st>>>(P);
+      s = bf ? launch_prefix<bf16_t, 64>(P, cache, st) : launch_prefix<__half, 64>(P, cache, st);
     }
+    if (s != RLK_OK) return s;
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
