@@ -1193,9 +1193,8 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     if B == 0 or n == 0 or q_heads == 0:
         return 0
     pieces = 0
-    for top in (min(max_shared, 8191), min(max_shared, 32767), max_shared):
-        size = 512 if top < 8192 else 1024 if top < 32768 else 2048
-        pieces = max(pieces, -(-(top // 32 * 32) // size))
+    for top in (min(max_shared, 8191), max_shared):
+        pieces = max(pieces, -(-(top // 32 * 32) // (512 if top < 8192 else 1024)))
 
     def lined(x):
         return (x + 127) // 128 * 128

@@ -184,6 +184,7 @@ struct AttnParams {
   uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
   PrefixParts pre;              // first NULL: none
+  int chains;                   // groups, or pieces of a prefix, whichever are more
 };
 struct AttnMaps {
   CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
@@ -975,6 +976,8 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     fresh_group = group_ends;
     if (!more) break;
   }
+  // behind a prefix's kernel this one may be launched early; the join goes by its end alone
+  if (P.pre.pieces > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   // where a copy did not come in time, the CTA stays for the last ones, within limits
   if (dead) {
 #pragma unroll 1
@@ -1027,7 +1030,7 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
   const int HT = P.c.kv_heads * P.tiles;
   const int blocks = (min(tile_rows, P.rows) + JR - 1) / JR;
 
-  const bool chainwise = P.groups <= width || width == JW;
+  const bool chainwise = P.chains <= width || width == JW;
   const int w0 = warp % width;           // this warp's first chain
   const int64_t total = unit_sums<JW * 32>(P, scan);
   const RunOf runs(static_cast<uint32_t>(total * HT), P.workers);
@@ -1054,9 +1057,33 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
     const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
     JoinRow<D> acc[JR], blk[JR];
     if (work && !direct) {
-      const int chains = chainwise ? 1 : JW / width;
-      for (int c = w0 * chains; c < (w0 + 1) * chains && c <= glast; ++c) {     // (chainwise: chain w0)
+      const int chains = chainwise ? 1 : JW / width, pieces = PRE && s.nnew > 0 ? pieces_of(P.pre.first[b]) : 0;
+      const int clast = PRE ? max(glast, pieces - 1) : glast;
+      for (int c = w0 * chains; c < (w0 + 1) * chains && c <= clast; ++c) {     // (chainwise: chain w0)
         JoinRow<D> chain[JR];
+        if constexpr (PRE) {             // the prefix's pieces c, c + 16, .., as many at a time as a group has units
+          const int64_t row = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + (ht % P.tiles) * tile_rows + r0;
+          for (int p0 = c; p0 < pieces; p0 += JW * GROUP) {
+            float2 h[GROUP][JR];
+            float v[GROUP][JR][E];
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k)
+#pragma unroll
+              for (int j = 0; j < JR; ++j) {
+                // (past the last piece, or row: one that is there again)
+                const int p = p0 + k * JW < pieces ? p0 + k * JW : p0, in = (ht % P.tiles) * tile_rows + r0 + j < P.rows ? j : 0;
+                const int64_t at = (row + in) * P.pre.pieces + p;
+                h[k][j] = P.pre.ml[at];
+                load_row<E>(P.pre.o + at * D + lane * E, v[k][j]);
+              }
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k)
+              if (p0 + k * JW < pieces) {
+#pragma unroll
+                for (int j = 0; j < JR; ++j) chain[j].add(h[k][j].x, h[k][j].y, v[k][j]);
+              }
+          }
+        }
         for (int g = c; g <= glast; g += JW) {
           if (g >= gs && g < gl) {
             g += (gl - g + JW - 1) / JW * JW;
@@ -1103,7 +1130,7 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
             acc[j] = chain[j];
           } else {
             blk[j].add(chain[j]);
-            if (c % JB == JB - 1 || c == glast) {
+            if (c % JB == JB - 1 || c == clast) {
               acc[j].add(blk[j]);
               blk[j] = JoinRow<D>();
             }
@@ -1124,25 +1151,6 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
       const int row = (ht % P.tiles) * tile_rows + r0 + j, i = query_of(P, row);
       if (row >= P.rows || (direct && i < s.nnew)) continue;
       JoinRow<D> all, part;
-      if (PRE && s.ok && i < s.nnew) {   // the prefix's parts in order, eight under way at once
-        const int parts = pieces_of(P.pre.first[b]);
-        const int64_t from = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + row;
-        const float2* ml = P.pre.ml + from * P.pre.pieces;
-        const float* po = P.pre.o + from * P.pre.pieces * D + lane * E;
-        for (int c0 = 0; c0 < parts; c0 += 8) {
-          float2 h[8];
-          float v[8][E];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int at = min(c0 + c, parts - 1);
-            h[c] = ml[at];
-            load_row<E>(po + static_cast<int64_t>(at) * D, v[c]);
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c0 + c < parts) all.add(h[c].x, h[c].y, v[c]);
-        }
-      }
       for (int c = 0; c < width; ++c) {
         float v[E];
 #pragma unroll
@@ -1323,8 +1331,18 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
     if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf16)) != RLK_OK) return s;
   }
   P.workers = Shape<D, NT>::WORKERS;
-  attn_kernel<T, D, NT><<<P.workers, Shape<D, NT>::THREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(P.workers);
+  cfg.blockDim = dim3(Shape<D, NT>::THREADS);
+  cfg.dynamicSmemBytes = Shape<D, NT>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  // (behind a prefix's kernel: on the SMs that it leaves one by one)
+  cfg.numAttrs = P.pre.first && P.pre.pieces > 0 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, D, NT>, P, maps);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them.  A chain to a
   // warp, as far as one round of CTAs (one per SM) has the warps; two rows to a warp, unless
@@ -1334,18 +1352,13 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   const int tile_rows = NT * 8, rows = tile_rows < P.rows ? tile_rows : P.rows;
   const int64_t entries = P.B * P.c.kv_heads * P.tiles, pairs = entries * ((rows + 1) / 2);
   int width = 1;
-  while (width < JW && width < P.groups) width *= 2;
+  while (width < JW && width < P.chains) width *= 2;
   if (pairs * width > NUM_SMS * JW) width = width > JB && pairs * JB <= NUM_SMS * JW ? JB : 1;
   const bool single = width == 1 && entries * rows <= 2 * NUM_SMS * JW;
   const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? 2 : 1);
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
   cfg.blockDim = dim3(JW * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   auto* const join = P.pre.first ? (single ? join_kernel<T, D, 1, true> : join_kernel<T, D, 2, true>)
                                  : (single ? join_kernel<T, D, 1, false> : join_kernel<T, D, 2, false>);
@@ -1402,7 +1415,11 @@ rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_b
   P.window = window;
   P.sinks = window > 0 ? sinks : 0;
   P.lse = out_lse;
-  if (parts) P.pre = *parts;
+  P.chains = static_cast<int>(y.groups);
+  if (parts) {
+    P.pre = *parts;
+    if (parts->pieces > P.chains) P.chains = parts->pieces;
+  }
   P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
   P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
   P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);

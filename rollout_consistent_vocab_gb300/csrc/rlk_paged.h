@@ -65,12 +65,12 @@ struct PrefixParts {
   const int32_t* first;         // [B] tokens that the parts cover, a multiple of 32; -1: the sequence is rejected
   const float2* ml;             // [B][kv_heads][n * group][pieces]: maximum (base 2), sum
   const float* o;               // ... and the weighted sum of values [head_dim]
-  int pieces;
+  int pieces;                   // at most, of a sequence; 0: no kernel for them was launched
 };
 // Tokens of a part.  By the covered length alone, so that a sequence's result does not
 // depend on its batch: more parts where there are few tokens (one to an SM), fewer
-// where there are many (a part's result is as much to write and read as 64 tokens are).
-__host__ __device__ __forceinline__ int piece_tokens(int covered) { return covered < 8192 ? 512 : covered < 32768 ? 1024 : 2048; }
+// where there are many (the parts' results are a read and a write of 128 tokens' size for 128 rows).
+__host__ __device__ __forceinline__ int piece_tokens(int covered) { return covered < 8192 ? 512 : 1024; }
 __host__ __device__ __forceinline__ int pieces_of(int covered) {
   const int t = piece_tokens(covered);
   return covered / t + (covered % t != 0);

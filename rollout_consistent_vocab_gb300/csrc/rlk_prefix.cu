@@ -51,6 +51,12 @@ struct PrefixParams {
   float* o;
 };
 
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // Items of a group: its pieces, for every kv head and block of 256 query rows.
 __device__ __forceinline__ uint32_t items_of(const PrefixParams& P, const GroupPlan& p) {
   const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows;
@@ -64,6 +70,7 @@ constexpr int PLAN_THREADS = 1024;
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P) {
   __shared__ uint32_t scan[PLAN_THREADS];
   const int tid = threadIdx.x, G = P.groups;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t tokens = static_cast<int64_t>(P.c.max_pages) * P.c.page_size;
   bool fault = false;
   for (int g = tid; g < G; g += PLAN_THREADS) {
@@ -141,8 +148,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
 //                    of the cache's dtype each (hi, then what hi dropped): an operand of
 //                    the second product as it lies.  At a piece's end it takes the result out.
 //   warp 8           one thread issues the products
-//   warp 9           copies keys and values, in the order in which they are needed, into one
-//                    ring of tiles (TMA boxes of as many tokens as lie together in a page)
+//   warps 9, 10      copy keys and values into one ring of tiles, in the order in which they are
+//                    needed (TMA boxes of as many tokens as lie together in a page)
 //
 // Shared tokens come in multiples of 32, so that a piece's last tile needs no masks: the
 // scores of what is not there are not read, and the second product ends before it.
@@ -160,8 +167,10 @@ template <> struct Weights<bf16_t> {
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
     const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
     hi = __byte_perm(x, y, 0x7632);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(a, MORE, -__uint_as_float(x & 0xFFFF0000u)),
-                                                   __fmaf_rn(b, MORE, -__uint_as_float(y & 0xFFFF0000u)));
+    float c, d;
+    unpack2(fma2(pack2(a, b), pack2(MORE, MORE), pack2(__uint_as_float((x & 0xFFFF0000u) ^ 0x80000000u),
+                                                       __uint_as_float((y & 0xFFFF0000u) ^ 0x80000000u))), c, d);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(c, d);
     lo = *reinterpret_cast<const uint32_t*>(&r);
   }
 };
@@ -186,7 +195,7 @@ template <> struct Weights<__half> {
 
 constexpr int PTILE = 128;               // tokens of a tile, and rows
 constexpr int PROWS = 2 * PTILE;         // query rows of a CTA
-constexpr int PTHREADS = 320;
+constexpr int PTHREADS = 352;
 template <int D>
 struct PShape {
   static constexpr int PANEL = PTILE * 128;        // 64 elements of every row, 128-byte swizzle
@@ -248,6 +257,7 @@ struct Way {
     load(P);
   }
   __device__ __forceinline__ Way(const PrefixParams& P, uint32_t a, uint32_t e) : at(a), end(e), g(0) {
+    if (a >= e) return;
     find(P);
     const uint32_t rest = a - P.base[g], pieces = max(pl.pieces, 1), x = rest / pieces;
     piece = static_cast<int>(rest - x * pieces);
@@ -290,22 +300,23 @@ struct Way {
       const int tiles = max(cur.tiles(0), cur.tiles(1));
 #pragma unroll 1
       for (; j < tiles; ++j) {
-#pragma unroll 1
+#pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int mine = cur.tiles(s), t0 = cur.from(s);
-          if (j >= 0 && j < mine)
-            pv(s, Tile{cur.seq0, cur.head, t0 + j * PTILE, min(PTILE, cur.tokens(s) - j * PTILE), cur.both, j == 0, j + 1 == mine});
-          const bool here = j + 1 < mine;
+          const int left = cur.tokens(s) - j * PTILE;            // of the stream's piece, from this tile on
+          if (j >= 0 && left > 0)
+            pv(s, Tile{cur.seq0, cur.head, cur.from(s) + j * PTILE, min(PTILE, left), cur.both, j == 0, left <= PTILE});
+          // the scores of its next tile, here or in the next step
+          const bool here = left > PTILE;
           if (!here && !(j + 1 == tiles && more && nxt.tokens(s) > 0)) continue;
-          Rows want;
-          want.take(here ? cur : nxt);
-          Rows& old = held[s];
-          const bool asks = old.seq0 != want.seq0 || old.head != want.head || old.rb != want.rb;
-          old = want;
-          if (here)
-            qk(s, Tile{cur.seq0, cur.head, t0 + (j + 1) * PTILE, min(PTILE, cur.tokens(s) - (j + 1) * PTILE), cur.both, j < 0, false}, asks);
-          else
-            qk(s, Tile{nxt.seq0, nxt.head, nxt.from(s), min(PTILE, nxt.tokens(s)), nxt.both, true, false}, asks);
+          const Tile x{here ? cur.seq0 : nxt.seq0, here ? cur.head : nxt.head, here ? cur.from(s) + (j + 1) * PTILE : nxt.from(s),
+                       min(PTILE, here ? left - PTILE : nxt.tokens(s)), here ? cur.both : nxt.both, !here || j < 0, false};
+          bool asks = false;
+          if (x.first) {
+            const int rb = here ? cur.rb : nxt.rb;
+            asks = held[s].seq0 != x.seq0 || held[s].head != x.head || held[s].rb != rb;
+            held[s].seq0 = x.seq0, held[s].head = x.head, held[s].rb = rb;
+          }
+          qk(s, x, asks);
         }
       }
       cur = nxt;
@@ -314,6 +325,12 @@ struct Way {
   }
 };
 
+// true in one thread of a warp that is together
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
 // D[tmem] (+)= A . B^T, one thread: A in shared or in tensor memory
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}"
@@ -384,8 +401,6 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   const uint32_t scored = streams, weighed = streams + 16, summed = streams + 32, asked = streams + 48, last = streams + 64;
   uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 72 - raw));
   volatile uint32_t* const dead = slot + 1;        // a wait gave up: everything ends, within limits
-  const uint32_t items = P.base[P.groups], workers = min(items, gridDim.x);
-  if (blockIdx.x >= workers) return;
   if (tid == 0) {
     for (int s = 0; s < S_::STAGES; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
     for (int s = 0; s < 2; ++s) {
@@ -407,7 +422,12 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  Way way(P, run_start(items, workers, blockIdx.x), run_start(items, workers, blockIdx.x + 1));
+  asm volatile("griddepcontrol.wait;" ::: "memory");           // the plan
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t items = P.base[P.groups], workers = max(1u, min(items, gridDim.x));
+  // (a CTA without items goes through with an empty run)
+  const uint32_t me = min(blockIdx.x, workers);
+  Way way(P, run_start(items, workers, me), run_start(items, workers, min(me + 1, workers)));
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_try(bar, parity & 1)) return true;
     const unsigned long long t0 = global_timer();
@@ -421,40 +441,60 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     return true;
   };
 
-  if (warp == 9) {
-    // ---- copies
-    uint32_t n = 0;                      // tiles so far
-    auto fill = [&](const CUtensorMap& map, const Tile& x) {
-      const uint32_t stage = n % S_::STAGES, bar = full + 8 * stage, dst = ring + stage * S_::TILE + lane * 128;
-      uint32_t page[4], boxes = 0;       // of tokens lane, lane + 32, ..; whether the lane speaks for a box there
-      int place[4];
+  if (warp >= 9) {
+    // ---- copies: keys by warp 9, values by warp 10.  A tile's pages are looked up while the
+    // one before it waits for its place.
+    const bool keys = warp == 9;
+    const CUtensorMap& map = keys ? maps.k : maps.v;
+    uint32_t n = 0, ahead = 0;           // tiles of both so far; the one that is looked up
+    uint32_t page[4], boxes = 0;         // of tokens lane, lane + 32, ..; whether the lane speaks for a box there
+    int place[4], head = 0;
+    bool waiting = false;
+    auto copy = [&]() {                  // the tile that is looked up
+      const uint32_t stage = ahead % S_::STAGES, bar = full + 8 * stage, dst = ring + stage * S_::TILE + lane * 128;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int in = y * 32 + lane;
-        bool there = in % P.box == 0 && in < x.count;
-        if (there) {
-          const uint32_t number = page_of(P.c, P.page_magic, x.t + in, place[y]);
-          page[y] = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
-          there = page[y] < P.c.num_pages;
-        }
-        boxes |= (there ? 1u : 0u) << y;
-      }
+      for (int y = 0; y < 4; ++y)
+        if (page[y] >= P.c.num_pages) boxes &= ~(1u << y);
       const uint32_t all = __reduce_add_sync(0xffffffffu, __popc(boxes));
-      const bool go = n < S_::STAGES || wait(empty + 8 * stage, n / S_::STAGES - 1);
-      ++n;
+      const bool go = ahead < S_::STAGES || wait(empty + 8 * stage, ahead / S_::STAGES - 1);
       if (__any_sync(0xffffffffu, !go)) return;
       if (lane == 0) mbar_arrive_expect_tx(bar, all * P.box * D * 2);
       __syncwarp();
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         if (!((boxes >> y) & 1u)) continue;
-        const int c1 = P.head_first ? x.head : place[y], c2 = P.head_first ? place[y] : x.head;
+        const int c1 = P.head_first ? head : place[y], c2 = P.head_first ? place[y] : head;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) copy_box(dst + c * S_::PANEL + y * 32 * 128, map, c * 64, c1, c2, page[y], bar);
       }
     };
-    way.walk(P, [&](int s, const Tile& x, bool) { if (!(x.both && s == 1)) fill(maps.k, x); },
-             [&](int s, const Tile& x) { if (!(x.both && s == 1)) fill(maps.v, x); });
+    auto fill = [&](int s, const Tile& x, bool mine) {
+      if (x.both && s == 1) return;
+      const uint32_t at = n++;
+      if (!mine) return;
+      uint32_t next_page[4], next_boxes = 0;
+      int next_place[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int in = y * 32 + lane;
+        next_page[y] = 0;
+        next_place[y] = 0;
+        if ((in & (P.box - 1)) == 0 && in < x.count) {
+          const uint32_t number = page_of(P.c, P.page_magic, x.t + in, next_place[y]);
+          next_page[y] = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
+          next_boxes |= 1u << y;
+        }
+      }
+      if (waiting) copy();
+      waiting = true;
+      ahead = at;
+      boxes = next_boxes;
+      head = x.head;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) page[y] = next_page[y], place[y] = next_place[y];
+    };
+    way.walk(P, [&](int s, const Tile& x, bool) { fill(s, x, keys); }, [&](int s, const Tile& x) { fill(s, x, !keys); });
+    if (waiting) copy();
     // where the products ended early, the CTA stays for its last copies
     if (*dead)
       for (uint32_t k = n > S_::STAGES ? n - S_::STAGES : 0; k < n; ++k) {
@@ -462,24 +502,25 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         while (!mbar_try(full + 8 * (k % S_::STAGES), (k / S_::STAGES) & 1) && global_timer() - t0 < TIMEOUT_NS) {}
       }
   } else if (warp == 8) {
-    if (lane == 0) {
-      // ---- products
-      constexpr uint32_t IDESC = (1u << 4) | (W::FORMAT << 7) | (W::FORMAT << 10) | (static_cast<uint32_t>(PTILE >> 4) << 24);
-      constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE >> 3) << 17);
-      constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
-      uint32_t n = 0, key_stage = 0, value_stage = 0;
-      uint32_t weights0 = 0, weights1 = 0, asked0 = 0, asked1 = 0;   // waits so far
-      way.walk(P,
-          [&](int s, const Tile& x, bool asks) {
-            if (asks) wait(asked + 8 * s, s ? asked1++ : asked0++);
-            if (!(x.both && s == 1)) {
-              key_stage = n % S_::STAGES;
-              wait(full + 8 * key_stage, n / S_::STAGES);
-              ++n;
-            }
-            if (*dead) return;
-            tc_fence_after();
-            const uint64_t a = sw128_desc(queries + s * S_::TILE), b = sw128_desc(ring + key_stage * S_::TILE);
+    // ---- products: the warp goes together, one thread issues
+    constexpr uint32_t IDESC = (1u << 4) | (W::FORMAT << 7) | (W::FORMAT << 10) | (static_cast<uint32_t>(PTILE >> 4) << 24);
+    constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE >> 3) << 17);
+    constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
+    uint32_t n = 0, key_stage = 0, value_stage = 0;
+    uint32_t weights0 = 0, weights1 = 0, asked0 = 0, asked1 = 0;   // waits so far
+    way.walk(P,
+        [&](int s, const Tile& x, bool asks) {
+          if (asks) wait(asked + 8 * s, s ? asked1++ : asked0++);
+          if (!(x.both && s == 1)) {
+            key_stage = n % S_::STAGES;
+            wait(full + 8 * key_stage, n / S_::STAGES);
+            ++n;
+          }
+          __syncwarp();
+          if (*dead) return;
+          tc_fence_after();
+          const uint64_t a = sw128_desc(queries + s * S_::TILE), b = sw128_desc(ring + key_stage * S_::TILE);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k / 4 * S_::PANEL + k % 4 * 32) >> 4;
@@ -487,30 +528,40 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
             }
             if (!(x.both && s == 0)) umma_commit(empty + 8 * key_stage);
             umma_commit(scored + 8 * s);
-          },
-          [&](int s, const Tile& x) {
-            if (!(x.both && s == 1)) {
-              value_stage = n % S_::STAGES;
-              wait(full + 8 * value_stage, n / S_::STAGES);
-              ++n;
-            }
-            wait(weighed + 8 * s, s ? weights1++ : weights0++);
-            if (*dead) return;
-            tc_fence_after();
-            const uint64_t b = values_desc(ring + value_stage * S_::TILE, S_::PANEL);
-            const uint32_t d = tmem + 2 * PTILE + s * 128, a = tmem + s * PTILE;
-            const int steps = x.count / 16;
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k) umma_ts(d, a + k / 2 * 32 + 16 + k % 2 * 8, b + 128 * k, IDESC_PV, !x.first || k > 0);
-#pragma unroll 1
-            for (int k = 0; k < steps; ++k) umma_ts(d, a + k / 2 * 32 + k % 2 * 8, b + 128 * k, IDESC_PV, true);
+          }
+          __syncwarp();
+        },
+        [&](int s, const Tile& x) {
+          if (!(x.both && s == 1)) {
+            value_stage = n % S_::STAGES;
+            wait(full + 8 * value_stage, n / S_::STAGES);
+            ++n;
+          }
+          wait(weighed + 8 * s, s ? weights1++ : weights0++);
+          __syncwarp();
+          if (*dead) return;
+          tc_fence_after();
+          const uint64_t b = values_desc(ring + value_stage * S_::TILE, S_::PANEL);
+          const uint32_t d = tmem + 2 * PTILE + s * 128, a = tmem + s * PTILE;
+          if (elect_one()) {
+            // the low parts, then the high ones; two products of 16 tokens at a time
+#pragma unroll
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int c = 0; c < PTILE / 32; ++c)
+                if (c * 32 < x.count) {
+                  umma_ts(d, a + c * 32 + part * 16, b + 256 * c, IDESC_PV, !x.first || part == 0 || c > 0);
+                  umma_ts(d, a + c * 32 + part * 16 + 8, b + 256 * c + 128, IDESC_PV, true);
+                }
             if (!(x.both && s == 0)) umma_commit(empty + 8 * value_stage);
             if (x.last) umma_commit(summed + 8 * s);
-          });
-      umma_commit(last);                 // nothing is left under way when tensor memory is given back
-      const unsigned long long t0 = global_timer();
-      while (!mbar_try(last, 0) && global_timer() - t0 < TIMEOUT_NS) {}
-    }
+          }
+          __syncwarp();
+        });
+    if (elect_one()) umma_commit(last);  // nothing is left under way when tensor memory is given back
+    __syncwarp();
+    const unsigned long long t0 = global_timer();
+    while (!mbar_try(last, 0) && global_timer() - t0 < TIMEOUT_NS) {}
     __syncwarp();
   } else {
     // ---- exponentials: a thread to a query row
@@ -573,23 +624,28 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           wait(scored + 8 * s, tiles++);
           __syncwarp();
           tc_fence_after();
-          // the scores are read twice, 64 at a time: once for the maximum, once for the weights
-          float top = -INFINITY;
-#pragma unroll
-          for (int c0 = 0; c0 < 4; c0 += 2) {
-            if (c0 >= chunks) break;
-            uint32_t x[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld32_async(scores + 32 * (c0 + c), x[c]);
+          // The scores are read 64 at a time: for the maximum, and again for the weights, the last
+          // 64 first, which are still there.
+          const int batches = (chunks + 1) / 2;
+          uint32_t x[2][32];
+          auto load = [&](int at) {
+            tmem_ld32_async(scores + 64 * at, x[0]);
+            tmem_ld32_async(scores + 64 * at + 32, x[1]);
             tmem_wait_ld();
+            tmem_loaded(x[0]);
+            tmem_loaded(x[1]);
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int y = 0; y < batches; ++y) {
+            load(y);
+            float t2 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_loaded(x[c]);
-              if (c0 + c < chunks) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
-              }
+            for (int e = 0; e < 32; e += 2) {
+              top = fmaxf(top, fmaxf(__uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1])));
+              t2 = fmaxf(t2, fmaxf(__uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1])));
             }
+            if (2 * y + 1 < chunks) top = fmaxf(top, t2);
           }
           top *= P.c2;
           float fac = 1.0f;
@@ -611,34 +667,33 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
             }
           }
           const float sub = m == -INFINITY ? W::OFF : W::OFF - m;
-          float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int c0 = 0; c0 < 4; c0 += 2) {
-            if (c0 >= chunks) break;
-            uint32_t x[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld32_async(scores + 32 * (c0 + c), x[c]);
-            tmem_wait_ld();
+          const uint64_t sub2 = pack2(sub, sub), c22 = pack2(P.c2, P.c2);
+          uint64_t sum2 = 0;
+#pragma unroll 1
+          for (int y = batches - 1;;) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              tmem_loaded(x[c]);
-              if (c0 + c < chunks) {
-                // 32 scores become 16 words of hi and 16 of lo, in their place
-                uint32_t hi[16], lo[16];
+              if (c == 1 && 2 * y + 1 >= chunks) continue;
+              // 32 scores become 16 words of hi and 16 of lo, in their place
+              uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float a = ex2(__fmaf_rn(__uint_as_float(x[c][2 * e]), P.c2, sub));
-                  const float b = ex2(__fmaf_rn(__uint_as_float(x[c][2 * e + 1]), P.c2, sub));
-                  sum[0] += a;
-                  sum[1] += b;
-                  W::split(a, b, hi[e], lo[e]);
-                }
-                tmem_st16(scores + 32 * (c0 + c), hi);
-                tmem_st16(scores + 32 * (c0 + c) + 16, lo);
+              for (int e = 0; e < 16; ++e) {
+                float a, b;
+                unpack2(fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), c22, sub2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum2 = add2(sum2, pack2(a, b));
+                W::split(a, b, hi[e], lo[e]);
               }
+              tmem_st16(scores + 64 * y + 32 * c, hi);
+              tmem_st16(scores + 64 * y + 32 * c + 16, lo);
             }
+            if (--y < 0) break;
+            load(y);
           }
-          l += sum[0] + sum[1];
+          float sum0, sum1;
+          unpack2(sum2, sum0, sum1);
+          l += sum0 + sum1;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -700,13 +755,25 @@ static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cuda
     if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, D, bf)) != RLK_OK) return s;
     if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf)) != RLK_OK) return s;
   }
-  prefix_kernel<T, D><<<152, PTHREADS, PShape<D>::SMEM, st>>>(P, maps);
+  // launched while the plan is made, for which it waits
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(152);
+  cfg.blockDim = dim3(PTHREADS);
+  cfg.dynamicSmemBytes = PShape<D>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefix_kernel<T, D>, P, maps);
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
 static size_t lined(size_t x) { return (x + 127) / 128 * 128; }
 static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t head_dim, int groups, int max_shared, size_t rest) {
   PrefixLayout y{};
-  for (const int top : {max_shared < 8191 ? max_shared : 8191, max_shared < 32767 ? max_shared : 32767, max_shared}) {
+  for (const int top : {max_shared < 8191 ? max_shared : 8191, max_shared}) {
     const int pieces = pieces_of(top / PREFIX_STEP * PREFIX_STEP);
     y.pieces = pieces > y.pieces ? pieces : y.pieces;
   }
@@ -796,7 +863,8 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.page_magic = page_magic(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   plan_kernel<<<1, PLAN_THREADS, 0, st>>>(P);
-  if (y.pieces > 0 && groups->groups > 0) {
+  const bool any = y.pieces > 0 && groups->groups > 0;
+  if (any) {
     const bool bf = cache->dtype == RLK_DT_BF16;
     if (cache->head_dim == 128) {
       s = bf ? launch_prefix<bf16_t, 128>(P, cache, st) : launch_prefix<__half, 128>(P, cache, st);
@@ -807,7 +875,7 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  const PrefixParts parts{P.first, P.ml, P.o, y.pieces};
+  const PrefixParts parts{P.first, P.ml, P.o, any ? y.pieces : 0};
   return paged_attention(cache, q, q_strides, q_heads, scale, 0, 0, out, out_strides, out_lse, ws + y.rest, &parts, stream);
 }
 
