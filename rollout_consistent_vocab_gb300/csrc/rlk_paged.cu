@@ -184,7 +184,7 @@ struct AttnParams {
   uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
   PrefixParts pre;              // first NULL: none
-  int chains;                   // groups, or pieces of a prefix, whichever are more
+  int chains;                   // as many as there are groups; four at least with a prefix
 };
 struct AttnMaps {
   CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
@@ -996,7 +996,8 @@ constexpr int JB = 4;                    // chains of a block
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, a chain folds its groups in order, a block its four chains,
 // and the row its four blocks.  By how many rows there are, a chain, a block or
-// a row is a warp's; it is the same tree.  The join also fills the rows without
+// a row is a warp's; it is the same tree.  The pieces of a prefix come first in the first four
+// chains, piece mod 4 to a chain.  The join also fills the rows without
 // a query, and those of rejected sequences.
 template <int D>
 struct JoinRow {
@@ -1021,7 +1022,7 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
 }
 
 template <class T, int D, int JR, bool PRE>      // JR: rows that a warp joins at once; PRE: with parts of a prefix
-__global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
+__global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
   constexpr int E = D / 32;
   __shared__ int64_t scan[JW * 32 + 1];
   __shared__ float2 chain_ml[JW][JR];
@@ -1058,27 +1059,28 @@ __global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams 
     JoinRow<D> acc[JR], blk[JR];
     if (work && !direct) {
       const int chains = chainwise ? 1 : JW / width, pieces = PRE && s.nnew > 0 ? pieces_of(P.pre.first[b]) : 0;
-      const int clast = PRE ? max(glast, pieces - 1) : glast;
+      const int clast = PRE ? max(glast, min(pieces, JB) - 1) : glast;
       for (int c = w0 * chains; c < (w0 + 1) * chains && c <= clast; ++c) {     // (chainwise: chain w0)
         JoinRow<D> chain[JR];
-        if constexpr (PRE) {             // the prefix's pieces c, c + 16, .., as many at a time as a group has units
-          const int64_t row = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + (ht % P.tiles) * tile_rows + r0;
-          for (int p0 = c; p0 < pieces; p0 += JW * GROUP) {
-            float2 h[GROUP][JR];
-            float v[GROUP][JR][E];
+        if constexpr (PRE) {             // a quarter of the prefix's pieces, several under way at once
+          constexpr int U = 8 / JR;
+          const int row = (ht % P.tiles) * tile_rows + r0;
+          const int64_t from = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + row;
+          for (int p0 = c; c < JB && p0 < pieces; p0 += JB * U) {
+            float2 h[U][JR];
+            float v[U][JR][E];
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k)
+            for (int k = 0; k < U; ++k)
 #pragma unroll
               for (int j = 0; j < JR; ++j) {
-                // (past the last piece, or row: one that is there again)
-                const int p = p0 + k * JW < pieces ? p0 + k * JW : p0, in = (ht % P.tiles) * tile_rows + r0 + j < P.rows ? j : 0;
-                const int64_t at = (row + in) * P.pre.pieces + p;
+                // (past the last piece, or row: one that is there)
+                const int64_t at = (from + (row + j < P.rows ? j : 0)) * P.pre.pieces + (p0 + k * JB < pieces ? p0 + k * JB : p0);
                 h[k][j] = P.pre.ml[at];
                 load_row<E>(P.pre.o + at * D + lane * E, v[k][j]);
               }
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k)
-              if (p0 + k * JW < pieces) {
+            for (int k = 0; k < U; ++k)
+              if (p0 + k * JB < pieces) {
 #pragma unroll
                 for (int j = 0; j < JR; ++j) chain[j].add(h[k][j].x, h[k][j].y, v[k][j]);
               }
@@ -1290,7 +1292,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box_tokens, bool head_first, int D, bool bf16) {
+rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box_tokens, bool head_first, int panels, int D,
+                     bool bf16) {
   static EncodeTiledFn fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -1306,11 +1309,12 @@ rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, i
   const cuuint64_t head = c.kv_heads > 1 ? static_cast<cuuint64_t>(c.head_stride) * 2 : any;
   const cuuint64_t page = c.num_pages > 1 ? static_cast<cuuint64_t>(c.page_stride) * 2 : any;
   const cuuint64_t tokens = c.page_size, heads = c.kv_heads, pages = c.num_pages;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), head_first ? heads : tokens, head_first ? tokens : heads, pages};
-  const cuuint64_t strides[3] = {head_first ? head : token, head_first ? token : head, page};
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(D / panels), head_first ? heads : tokens, head_first ? tokens : heads, pages,
+                              static_cast<cuuint64_t>(panels)};
+  const cuuint64_t strides[4] = {head_first ? head : token, head_first ? token : head, page, 128};
   const cuuint32_t box = static_cast<cuuint32_t>(box_tokens);
-  const cuuint32_t boxes[4] = {64, head_first ? 1 : box, head_first ? box : 1, 1}, ones[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  const cuuint32_t boxes[5] = {64, head_first ? 1 : box, head_first ? box : 1, 1, static_cast<cuuint32_t>(panels)}, ones[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, panels > 1 ? 5 : 4,
                         const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
@@ -1327,8 +1331,8 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   AttnMaps maps;
   constexpr bool bf16 = sizeof(T) == 2 && Elem<T>::EXP == 0x7F807F80u;
   if (P.c.num_pages > 0) {
-    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, D, bf16)) != RLK_OK) return s;
-    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, 1, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, 1, D, bf16)) != RLK_OK) return s;
   }
   P.workers = Shape<D, NT>::WORKERS;
   cudaLaunchConfig_t cfg{};
@@ -1354,8 +1358,9 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   int width = 1;
   while (width < JW && width < P.chains) width *= 2;
   if (pairs * width > NUM_SMS * JW) width = width > JB && pairs * JB <= NUM_SMS * JW ? JB : 1;
-  const bool single = width == 1 && entries * rows <= 2 * NUM_SMS * JW;
-  const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? 2 : 1);
+  const int joins = P.pre.first ? 1 : 2;       // CTAs of a row to a warp that an SM has room for
+  const bool single = width == 1 && entries * rows <= joins * NUM_SMS * JW;
+  const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? joins : 1);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
   cfg.blockDim = dim3(JW * 32);
   cfg.dynamicSmemBytes = 0;
@@ -1418,7 +1423,7 @@ rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_b
   P.chains = static_cast<int>(y.groups);
   if (parts) {
     P.pre = *parts;
-    if (parts->pieces > P.chains) P.chains = parts->pieces;
+    if (P.chains < JB) P.chains = JB;
   }
   P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
   P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);

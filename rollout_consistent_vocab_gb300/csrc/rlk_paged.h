@@ -56,8 +56,9 @@ inline bool heads_first(const rlk_kv_cache* c) {
 }
 // The cache's keys or values as a tensor of (element, token of the page, head, page),
 // the middle two in the order of their strides; a copy takes 64 elements of
-// `box` tokens of a head.
-rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box, bool head_first, int D, bool bf16);
+// `box` tokens of a head; with panels = 2 all 128 elements, the second 64 of every token
+// behind the first 64 (a fifth place).
+rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box, bool head_first, int panels, int D, bool bf16);
 
 // Attention over the first tokens of each sequence, done before: what paged attention
 // over the rest joins to its own.

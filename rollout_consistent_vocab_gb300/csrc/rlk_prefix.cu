@@ -44,7 +44,8 @@ struct PrefixParams {
   int max_pieces;
   float c2;                     // |scale| * log2(e)
   uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
-  int box;                      // tokens of a copy
+  int box;                      // tokens of a copy: the largest power of 2, up to 64, that divides page_size
+  bool merged;                  // a copy takes all 128 elements of its tokens (64 of them)
   bool head_first;
   uint32_t page_magic;
   float2* ml;
@@ -135,20 +136,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
 //
 // S = Q K^T and O += P V run on tcgen05: 128 query rows as the accumulator's rows, 128
 // tokens a tile, everything between in tensor memory.  A CTA has two streams of tiles, each
-// with scores (128 columns of tensor memory) and a result (head_dim columns) of its own:
-// while a stream's warps take the exponentials of one tile, the tensor cores are at the
-// other stream's.  A group with up to 128 query rows per kv head gives its streams pieces
+// with scores (128 columns of tensor memory) and a result (head_dim columns) of its own.
+// The scores of a tile's halves come and go by themselves: while a stream's warps take the
+// exponentials of one half, the tensor cores are at its other half, or at the other stream.
+// A group with up to 128 query rows per kv head gives its streams pieces
 // of their own; with more, both streams take the same piece, with 128 rows each, and
 // every tile of keys and values is read once for 256 rows.
 //
-//   warps 0-3, 4-7   a stream's: a thread to a query row.  It reads its 128 scores, keeps
+//   warps 0-3, 4-7   a stream's: a thread to a query row.  It reads 64 of its scores, keeps
 //                    a reference maximum (which follows the row's maximum where that runs
 //                    SLACK ahead; then the result so far is scaled in tensor memory) and
 //                    the sum, and writes the weights over the scores as two elements
 //                    of the cache's dtype each (hi, then what hi dropped): an operand of
 //                    the second product as it lies.  At a piece's end it takes the result out.
-//   warp 8           one thread issues the products
-//   warps 9, 10      copy keys and values into one ring of tiles, in the order in which they are
+//   warps 8, 9       a stream's: one thread issues the products
+//   warps 10, 11     copy keys and values, half a tile each, into one ring of tiles, in the order in which they are
 //                    needed (TMA boxes of as many tokens as lie together in a page)
 //
 // Shared tokens come in multiples of 32, so that a piece's last tile needs no masks: the
@@ -195,13 +197,14 @@ template <> struct Weights<__half> {
 
 constexpr int PTILE = 128;               // tokens of a tile, and rows
 constexpr int PROWS = 2 * PTILE;         // query rows of a CTA
-constexpr int PTHREADS = 352;
+constexpr int PTHREADS = 384;
 template <int D>
 struct PShape {
   static constexpr int PANEL = PTILE * 128;        // 64 elements of every row, 128-byte swizzle
   static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int HALF = TILE / 2;            // keys and values: 64 tokens' panels, then the others'
   static constexpr int STAGES = D == 128 ? 5 : 10;
-  static constexpr int BARS = 2 * STAGES + 2 * 4 + 1;
+  static constexpr int BARS = 2 * STAGES + 2 * 6 + 1;
   static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BARS * 8 + 16;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
@@ -231,10 +234,10 @@ struct Rows {
   __device__ __forceinline__ bool of(const Step& x) const { return seq0 == x.seq0 && head == x.head && rb == x.rb; }
   __device__ __forceinline__ void take(const Step& x) { seq0 = x.seq0, head = x.head, rb = x.rb; }
 };
-// A tile's product: of a stream's step, tokens t .. t + count - 1.
+// A stream's tile: tokens t .. t + count - 1 of a kv head; first: of its piece.
 struct Tile {
   int seq0, head, t, count;
-  bool both, first, last;                // of its piece
+  bool both, first;
 };
 // A CTA's way through its run of items: an item is a piece of a group, kv head and block of rows.
 struct Way {
@@ -288,10 +291,11 @@ struct Way {
     }
     return true;
   }
-  // Every product of the run in order: qk(s, tile, asks) for scores (asks: the stream's queries are other
-  // ones than before), pv(s, tile) for results.
-  template <class QK, class PV>
-  __device__ __forceinline__ void walk(const PrefixParams& P, QK qk, PV pv) {
+  // The products of the run in order: op(s, cur, next, asks) takes stream s from its tile cur to its tile
+  // next (count 0: none).  The results of cur and the scores of next go together; asks: next's
+  // queries are other ones than the stream had.
+  template <class Op>
+  __device__ __forceinline__ void walk(const PrefixParams& P, Op op) {
     Step cur, nxt;
     Rows held[2];
     bool have = next(P, cur);
@@ -303,20 +307,17 @@ struct Way {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int left = cur.tokens(s) - j * PTILE;            // of the stream's piece, from this tile on
-          if (j >= 0 && left > 0)
-            pv(s, Tile{cur.seq0, cur.head, cur.from(s) + j * PTILE, min(PTILE, left), cur.both, j == 0, left <= PTILE});
-          // the scores of its next tile, here or in the next step
-          const bool here = left > PTILE;
-          if (!here && !(j + 1 == tiles && more && nxt.tokens(s) > 0)) continue;
-          const Tile x{here ? cur.seq0 : nxt.seq0, here ? cur.head : nxt.head, here ? cur.from(s) + (j + 1) * PTILE : nxt.from(s),
-                       min(PTILE, here ? left - PTILE : nxt.tokens(s)), here ? cur.both : nxt.both, !here || j < 0, false};
+          const Tile x{cur.seq0, cur.head, cur.from(s) + j * PTILE, j < 0 ? 0 : max(0, min(PTILE, left)), cur.both, j == 0};
+          const bool here = left > PTILE, there = !here && j + 1 == tiles && more && nxt.tokens(s) > 0;
+          const Tile y{here ? cur.seq0 : nxt.seq0, here ? cur.head : nxt.head, here ? cur.from(s) + (j + 1) * PTILE : nxt.from(s),
+                       here ? min(PTILE, left - PTILE) : there ? min(PTILE, nxt.tokens(s)) : 0, here ? cur.both : nxt.both, !here || j < 0};
           bool asks = false;
-          if (x.first) {
+          if (y.first && y.count > 0) {
             const int rb = here ? cur.rb : nxt.rb;
-            asks = held[s].seq0 != x.seq0 || held[s].head != x.head || held[s].rb != rb;
-            held[s].seq0 = x.seq0, held[s].head = x.head, held[s].rb = rb;
+            asks = held[s].seq0 != y.seq0 || held[s].head != y.head || held[s].rb != rb;
+            held[s].seq0 = y.seq0, held[s].head = y.head, held[s].rb = rb;
           }
-          qk(s, x, asks);
+          if (x.count > 0 || y.count > 0) op(s, x, y, asks);
         }
       }
       cur = nxt;
@@ -398,18 +399,18 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   const uint32_t raw = smem_addr(smem_raw), queries = (raw + 1023u) & ~1023u, ring = queries + 2 * S_::TILE;
   const uint32_t bars = ring + S_::STAGES * S_::TILE;
   const uint32_t full = bars, empty = bars + 8 * S_::STAGES, streams = empty + 8 * S_::STAGES;
-  const uint32_t scored = streams, weighed = streams + 16, summed = streams + 32, asked = streams + 48, last = streams + 64;
-  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 72 - raw));
+  // of stream s: half h of a tile has scores, or weights, at 16 s + 8 h; a half's result is in, queries are there, at 8 s
+  const uint32_t scored = streams, weighed = streams + 32, summed = streams + 64, asked = streams + 80, last = streams + 96;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 104 - raw));
   volatile uint32_t* const dead = slot + 1;        // a wait gave up: everything ends, within limits
   if (tid == 0) {
-    for (int s = 0; s < S_::STAGES; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
+    for (int s = 0; s < S_::STAGES; ++s) mbar_init(full + 8 * s, 2), mbar_init(empty + 8 * s, 2);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(scored + 8 * s, 1);
-      mbar_init(weighed + 8 * s, 4);
+      for (int h = 0; h < 2; ++h) mbar_init(scored + 16 * s + 8 * h, 1), mbar_init(weighed + 16 * s + 8 * h, 4);
       mbar_init(summed + 8 * s, 1);
       mbar_init(asked + 8 * s, 4);
     }
-    mbar_init(last, 1);
+    mbar_init(last, 2);
     *dead = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -441,59 +442,82 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     return true;
   };
 
-  if (warp >= 9) {
-    // ---- copies: keys by warp 9, values by warp 10.  A tile's pages are looked up while the
-    // one before it waits for its place.
-    const bool keys = warp == 9;
-    const CUtensorMap& map = keys ? maps.k : maps.v;
-    uint32_t n = 0, ahead = 0;           // tiles of both so far; the one that is looked up
-    uint32_t page[4], boxes = 0;         // of tokens lane, lane + 32, ..; whether the lane speaks for a box there
-    int place[4], head = 0;
-    bool waiting = false;
-    auto copy = [&]() {                  // the tile that is looked up
-      const uint32_t stage = ahead % S_::STAGES, bar = full + 8 * stage, dst = ring + stage * S_::TILE + lane * 128;
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        if (page[y] >= P.c.num_pages) boxes &= ~(1u << y);
-      const uint32_t all = __reduce_add_sync(0xffffffffu, __popc(boxes));
-      const bool go = ahead < S_::STAGES || wait(empty + 8 * stage, ahead / S_::STAGES - 1);
-      if (__any_sync(0xffffffffu, !go)) return;
-      if (lane == 0) mbar_arrive_expect_tx(bar, all * P.box * D * 2);
-      __syncwarp();
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if (!((boxes >> y) & 1u)) continue;
-        const int c1 = P.head_first ? head : place[y], c2 = P.head_first ? place[y] : head;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) copy_box(dst + c * S_::PANEL + y * 32 * 128, map, c * 64, c1, c2, page[y], bar);
+  if (warp >= 10) {
+    // ---- copies: each of the two warps has half of the copies of every tile, a lane one of them: a box of
+    // tokens and 64 of their elements, or all (P.merged).  Its page is looked up while the tile before
+    // waits for its place.
+    const int panels = P.merged ? 1 : D / 64, copies = PTILE / P.box * panels;
+    const uint32_t pages = static_cast<uint32_t>(P.c.num_pages), bytes = P.box * (P.merged ? 256 : 128);
+    auto token_of = [&](int e) { return (D == 64 || P.merged ? e : e >> 1) * P.box; };
+    auto panel_of = [&](int e) { return D == 64 || P.merged ? 0 : e & 1; };
+    auto place_of = [&](int e) {         // of copy e in a tile: halves of 64 tokens, then panels of 64 elements
+      const int token = token_of(e);
+      return (token >> 6) * S_::HALF + panel_of(e) * (64 * 128) + (token & 63) * 128;
+    };
+    const int first = lane * 2 + (warp - 10), my_token = first < copies ? token_of(first) : PTILE, my_x = panel_of(first) * 64;
+    const uint32_t my_place = ring + place_of(first);
+    uint32_t stage = 0, phase = 1, n = 0;                // n: tiles so far
+    uint32_t page = ~0u;
+    int place = 0;
+    Tile now{};
+    bool values = false, waiting = false;
+    // where a token of a tile lies (a page number past the last: nothing to copy)
+    auto look = [&](const Tile& x, int token, uint32_t& pg, int& pl) {
+      pg = ~0u;
+      if (token < x.count) {
+        const uint32_t number = page_of(P.c, P.page_magic, x.t + token, pl);
+        pg = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
       }
     };
-    auto fill = [&](int s, const Tile& x, bool mine) {
-      if (x.both && s == 1) return;
-      const uint32_t at = n++;
-      if (!mine) return;
-      uint32_t next_page[4], next_boxes = 0;
-      int next_place[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int in = y * 32 + lane;
-        next_page[y] = 0;
-        next_place[y] = 0;
-        if ((in & (P.box - 1)) == 0 && in < x.count) {
-          const uint32_t number = page_of(P.c, P.page_magic, x.t + in, next_place[y]);
-          next_page[y] = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
-          next_boxes |= 1u << y;
+    auto copy = [&]() {                  // the tile that is looked up
+      const uint32_t bar = full + 8 * stage;
+      const CUtensorMap& map = values ? maps.v : maps.k;
+      const bool there = page < pages;
+      uint32_t all = __popc(__ballot_sync(0xffffffffu, there));
+      if (copies > 64)                   // (boxes of 1 or 2 tokens)
+        for (int e = first + 64; e < copies; e += 64) {
+          uint32_t pg;
+          int pl;
+          look(now, token_of(e), pg, pl);
+          all += __popc(__ballot_sync(0xffffffffu, pg < pages));
         }
+      const bool go = wait(empty + 8 * stage, phase);
+      if (__all_sync(0xffffffffu, go)) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, all * bytes);
+        __syncwarp();
+        if (there) {
+          const int c1 = P.head_first ? now.head : place, c2 = P.head_first ? place : now.head;
+          if (P.merged) copy_box5(my_place + stage * S_::TILE, map, c1, c2, page, bar);
+          else copy_box(my_place + stage * S_::TILE, map, my_x, c1, c2, page, bar);
+        }
+        if (copies > 64)
+          for (int e = first + 64; e < copies; e += 64) {
+            look(now, token_of(e), page, place);
+            if (page < pages)
+              copy_box(ring + stage * S_::TILE + place_of(e), map, panel_of(e) * 64, P.head_first ? now.head : place,
+                       P.head_first ? place : now.head, page, bar);
+          }
+        __syncwarp();
       }
+      ++n;
+      if (++stage == S_::STAGES) stage = 0, phase ^= 1;
+    };
+    auto fill = [&](int s, const Tile& x, bool of_values) {
+      if (x.both && s == 1) return;
+      uint32_t next_page;
+      int next_place = 0;
+      look(x, my_token, next_page, next_place);
       if (waiting) copy();
       waiting = true;
-      ahead = at;
-      boxes = next_boxes;
-      head = x.head;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) page[y] = next_page[y], place[y] = next_place[y];
+      now = x;
+      values = of_values;
+      page = next_page;
+      place = next_place;
     };
-    way.walk(P, [&](int s, const Tile& x, bool) { fill(s, x, keys); }, [&](int s, const Tile& x) { fill(s, x, !keys); });
+    way.walk(P, [&](int s, const Tile& x, const Tile& y, bool) {
+      if (x.count > 0) fill(s, x, true);
+      if (y.count > 0) fill(s, y, false);
+    });
     if (waiting) copy();
     // where the products ended early, the CTA stays for its last copies
     if (*dead)
@@ -501,63 +525,80 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         const unsigned long long t0 = global_timer();
         while (!mbar_try(full + 8 * (k % S_::STAGES), (k / S_::STAGES) & 1) && global_timer() - t0 < TIMEOUT_NS) {}
       }
-  } else if (warp == 8) {
-    // ---- products: the warp goes together, one thread issues
+  } else if (warp >= 8) {
+    // ---- a stream's products: the warp goes together, one thread issues
     constexpr uint32_t IDESC = (1u << 4) | (W::FORMAT << 7) | (W::FORMAT << 10) | (static_cast<uint32_t>(PTILE >> 4) << 24);
-    constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE >> 3) << 17);
+    constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE / 2 >> 3) << 17);
     constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
-    uint32_t n = 0, key_stage = 0, value_stage = 0;
-    uint32_t weights0 = 0, weights1 = 0, asked0 = 0, asked1 = 0;   // waits so far
-    way.walk(P,
-        [&](int s, const Tile& x, bool asks) {
-          if (asks) wait(asked + 8 * s, s ? asked1++ : asked0++);
-          if (!(x.both && s == 1)) {
-            key_stage = n % S_::STAGES;
-            wait(full + 8 * key_stage, n / S_::STAGES);
-            ++n;
-          }
-          __syncwarp();
-          if (*dead) return;
-          tc_fence_after();
-          const uint64_t a = sw128_desc(queries + s * S_::TILE), b = sw128_desc(ring + key_stage * S_::TILE);
-          if (elect_one()) {
+    const int mine = warp - 8;
+    const uint32_t scores = tmem + mine * PTILE, result = tmem + 2 * PTILE + mine * 128;
+    uint32_t n = 0, value_at = 0, key_at = 0, uses[2] = {0, 0}, blocks = 0;        // tiles, waits so far
+    // Both streams' warps go by every tile, so that neither is ever more than one round of the ring
+    // behind: a stage is free when both have let it go, at once where the tile is the other's.
+    auto take = [&](int s, const Tile& x, uint32_t& at) {
+      if (!(x.both && s == 1)) at = n++;
+      if (s != mine && x.both) return;
+      wait(full + 8 * (at % S_::STAGES), at / S_::STAGES);
+      __syncwarp();
+      if (s != mine && lane == 0) mbar_arrive(empty + 8 * (at % S_::STAGES));
+    };
+    way.walk(P, [&](int s, const Tile& x, const Tile& y, bool asks) {
+      if (s != mine) {
+        if (x.count > 0) take(s, x, value_at);
+        if (y.count > 0) take(s, y, key_at);
+        return;
+      }
+      if (x.count > 0) take(s, x, value_at);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k / 4 * S_::PANEL + k % 4 * 32) >> 4;
-              umma_ss(tmem + s * PTILE, a + off, b + off, IDESC_QK, k > 0);
+      for (int h = 0; h < 2; ++h) {
+        // the results of half a tile
+        if (h * 64 < x.count) {
+          wait(weighed + 16 * mine + 8 * h, uses[h]++);
+          __syncwarp();
+          if (!*dead) {
+            tc_fence_after();
+            const uint64_t b = values_desc(ring + value_at % S_::STAGES * S_::TILE + h * S_::HALF, 64 * 128);
+            if (elect_one()) {
+              // the low parts, then the high ones; two products of 16 tokens at a time
+#pragma unroll
+              for (int part = 1; part >= 0; --part)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (h * 64 + c * 32 < x.count) {
+                    const uint32_t a = scores + h * 64 + c * 32 + part * 16;
+                    umma_ts(result, a, b + 256 * c, IDESC_PV, !x.first || h > 0 || part == 0 || c > 0);
+                    umma_ts(result, a + 8, b + 256 * c + 128, IDESC_PV, true);
+                  }
+              umma_commit(summed + 8 * mine);
+              if (x.count <= h * 64 + 64) umma_commit(empty + 8 * (value_at % S_::STAGES));
             }
-            if (!(x.both && s == 0)) umma_commit(empty + 8 * key_stage);
-            umma_commit(scored + 8 * s);
+            __syncwarp();
           }
-          __syncwarp();
-        },
-        [&](int s, const Tile& x) {
-          if (!(x.both && s == 1)) {
-            value_stage = n % S_::STAGES;
-            wait(full + 8 * value_stage, n / S_::STAGES);
-            ++n;
+        }
+        // the scores of half of the next, in the place of what was just used
+        if (h * 64 < y.count) {
+          if (h == 0) {
+            take(s, y, key_at);
+            if (asks) wait(asked + 8 * mine, blocks++);
+            __syncwarp();
           }
-          wait(weighed + 8 * s, s ? weights1++ : weights0++);
-          __syncwarp();
-          if (*dead) return;
-          tc_fence_after();
-          const uint64_t b = values_desc(ring + value_stage * S_::TILE, S_::PANEL);
-          const uint32_t d = tmem + 2 * PTILE + s * 128, a = tmem + s * PTILE;
-          if (elect_one()) {
-            // the low parts, then the high ones; two products of 16 tokens at a time
+          if (!*dead) {
+            tc_fence_after();
+            const uint64_t a = sw128_desc(queries + mine * S_::TILE), b = sw128_desc(ring + key_at % S_::STAGES * S_::TILE + h * S_::HALF);
+            if (elect_one()) {
 #pragma unroll
-            for (int part = 1; part >= 0; --part)
-#pragma unroll
-              for (int c = 0; c < PTILE / 32; ++c)
-                if (c * 32 < x.count) {
-                  umma_ts(d, a + c * 32 + part * 16, b + 256 * c, IDESC_PV, !x.first || part == 0 || c > 0);
-                  umma_ts(d, a + c * 32 + part * 16 + 8, b + 256 * c + 128, IDESC_PV, true);
-                }
-            if (!(x.both && s == 0)) umma_commit(empty + 8 * value_stage);
-            if (x.last) umma_commit(summed + 8 * s);
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = k % 4 * 32 >> 4;
+                umma_ss(scores + h * 64, a + off + (k / 4 * S_::PANEL >> 4), b + off + (k / 4 * 64 * 128 >> 4), IDESC_QK, k > 0);
+              }
+              umma_commit(scored + 16 * mine + 8 * h);
+              if (y.count <= h * 64 + 64) umma_commit(empty + 8 * (key_at % S_::STAGES));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        });
+        }
+      }
+    });
     if (elect_one()) umma_commit(last);  // nothing is left under way when tensor memory is given back
     __syncwarp();
     const unsigned long long t0 = global_timer();
@@ -568,10 +609,10 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     const int s = warp >> 2, row = tid & (PTILE - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scores = tmem + s * PTILE + lanes, result = tmem + 2 * PTILE + s * 128 + lanes;
-    uint32_t tiles = 0, pieces = 0;      // waits so far
+    uint32_t used0 = 0, used1 = 0, total = 0, seen = 0;    // waits so far; halves of tiles so far, and those whose results are in
     Step st, nxt;
     Rows held;
-    bool have = way.next(P, st);
+    bool have = way.next(P, st), dry = true;
     int64_t out = -1;                    // the row's first part, in parts; -1: no query
     auto ask = [&](const Step& x) {      // the queries of the stream's rows of x
       held.take(x);
@@ -617,44 +658,43 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         const int64_t slot_at = out + st.piece_of(s);
         const bool query = out >= 0;
         float m = -INFINITY, l = 0.0f;
-        const int count = st.tiles(s);
+        const int halves = (all + 63) / 64;
+        // (the first tile's scores are a while in coming: half a tile without any in the meantime, into the
+        // result's place, which brings the instructions)
 #pragma unroll 1
-        for (int j = 0; j < count; ++j) {
-          const int chunks = min(PTILE, all - j * PTILE) / 32;
-          wait(scored + 8 * s, tiles++);
+        for (int h = dry ? -1 : 0; h < halves; ++h, dry = false) {
+          const bool two = dry || all - h * 64 > 32;             // 64 tokens, not 32
+          const uint32_t at = dry ? result : scores + (h & 1) * 64;
+          if (!dry) {
+            if (h & 1) wait(scored + 16 * s + 8, used1++);
+            else wait(scored + 16 * s, used0++);
+          }
           __syncwarp();
           tc_fence_after();
-          // The scores are read 64 at a time: for the maximum, and again for the weights, the last
-          // 64 first, which are still there.
-          const int batches = (chunks + 1) / 2;
           uint32_t x[2][32];
-          auto load = [&](int at) {
-            tmem_ld32_async(scores + 64 * at, x[0]);
-            tmem_ld32_async(scores + 64 * at + 32, x[1]);
-            tmem_wait_ld();
-            tmem_loaded(x[0]);
-            tmem_loaded(x[1]);
-          };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int y = 0; y < batches; ++y) {
-            load(y);
-            float t2 = -INFINITY;
+          tmem_ld32_async(at, x[0]);
+          tmem_ld32_async(at + 32, x[1]);
+          tmem_wait_ld();
+          tmem_loaded(x[0]);
+          tmem_loaded(x[1]);
+          float top = -INFINITY, t2 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              top = fmaxf(top, fmaxf(__uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1])));
-              t2 = fmaxf(t2, fmaxf(__uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1])));
-            }
-            if (2 * y + 1 < chunks) top = fmaxf(top, t2);
+          for (int e = 0; e < 32; e += 2) {
+            top = fmaxf(top, fmaxf(__uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1])));
+            t2 = fmaxf(t2, fmaxf(__uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1])));
           }
+          if (two) top = fmaxf(top, t2);
           top *= P.c2;
           float fac = 1.0f;
           if (top > m + W::SLACK) {
             if (m != -INFINITY) fac = ex2(m - top);
             m = top;
           }
-          if (__any_sync(0xffffffffu, fac != 1.0f)) {
+          if (__any_sync(0xffffffffu, fac != 1.0f) && !dry) {
             l *= fac;
+            if (seen < total) wait(summed + 8 * s, seen++);
+            __syncwarp();
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t y[32];
@@ -669,27 +709,22 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           const float sub = m == -INFINITY ? W::OFF : W::OFF - m;
           const uint64_t sub2 = pack2(sub, sub), c22 = pack2(P.c2, P.c2);
           uint64_t sum2 = 0;
-#pragma unroll 1
-          for (int y = batches - 1;;) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c == 1 && 2 * y + 1 >= chunks) continue;
-              // 32 scores become 16 words of hi and 16 of lo, in their place
-              uint32_t hi[16], lo[16];
+          for (int c = 0; c < 2; ++c) {
+            if (c == 1 && !two) continue;
+            // 32 scores become 16 words of hi and 16 of lo, in their place
+            uint32_t hi[16], lo[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float a, b;
-                unpack2(fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), c22, sub2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum2 = add2(sum2, pack2(a, b));
-                W::split(a, b, hi[e], lo[e]);
-              }
-              tmem_st16(scores + 64 * y + 32 * c, hi);
-              tmem_st16(scores + 64 * y + 32 * c + 16, lo);
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), c22, sub2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum2 = add2(sum2, pack2(a, b));
+              W::split(a, b, hi[e], lo[e]);
             }
-            if (--y < 0) break;
-            load(y);
+            tmem_st16(at + 32 * c, hi);
+            tmem_st16(at + 32 * c + 16, lo);
           }
           float sum0, sum1;
           unpack2(sum2, sum0, sum1);
@@ -697,10 +732,20 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(weighed + 8 * s);
+          if (dry) {
+            m = -INFINITY;
+            l = 0.0f;
+          } else {
+            // (one half at a time is under way to the result, so that no wait is ever two behind)
+            if (seen < total) wait(summed + 8 * s, seen++);
+            __syncwarp();
+            ++total;
+            if (lane == 0) mbar_arrive(weighed + 16 * s + 8 * (h & 1));
+          }
+          __syncwarp();
         }
         if (more && nxt.tokens(s) > 0 && !held.of(nxt)) ask(nxt);        // (all products with the old ones are done)
-        bad |= !wait(summed + 8 * s, pieces++) || *dead != 0u;
+        bad |= !wait(summed + 8 * s, seen++) || *dead != 0u;
         bad = __any_sync(0xffffffffu, bad);
         tc_fence_after();
         if (bad && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
@@ -752,8 +797,8 @@ static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cuda
   rlk_status s;
   if (P.c.num_pages > 0) {
     const bool bf = cache->dtype == RLK_DT_BF16;
-    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, D, bf)) != RLK_OK) return s;
-    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, D, bf)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, P.merged ? 2 : 1, D, bf)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, P.merged ? 2 : 1, D, bf)) != RLK_OK) return s;
   }
   // launched while the plan is made, for which it waits
   cudaLaunchConfig_t cfg{};
@@ -858,7 +903,8 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.max_pieces = y.pieces;
   P.c2 = fabsf(scale) * 1.4426950408889634f;
   P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
-  P.box = box_of(cache->page_size, PTILE);
+  P.box = box_of(cache->page_size, PTILE / 2);
+  P.merged = P.box == 64 && cache->head_dim == 128;
   P.head_first = heads_first(cache);
   P.page_magic = page_magic(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -136,6 +136,27 @@ def test_a_very_long_prefix():
     compare(c, out, lse, [1, 1])
 
 
+RUNS = [
+    # more pieces than CTAs: runs that hold pieces side by side, end anywhere, and go from group to group
+    ([(2, 4600), (1, 4100), (3, 2080), (0, 700), (2, 5000), (1, 0), (2, 4608), (1, 3000)], 8, 8, 64, 16, "bf16"),
+    ([(3, 4600), (2, 1570), (4, 3300), (3, 4096), (1, 9000)], 16, 8, 128, 64, "f16"),
+    ([(40, 1700), (2, 2300), (33, 1600), (1, 4500), (70, 1100), (2, 4200)], 16, 4, 64, 64, "bf16"),    # one tile of rows and two
+    ([(33, 2600), (3, 9300), (34, 2000), (1, 8900), (33, 1700), (2, 3000)], 32, 8, 128, 24, "bf16"),
+    ([(1, 32 + 544 * (i % 9)) for i in range(40)], 8, 8, 128, 128, "bf16"),
+]
+
+
+@pytest.mark.parametrize("groups,heads,kv_heads,dim,page,dtype", RUNS)
+def test_runs_of_many_pieces(groups, heads, kv_heads, dim, page, dtype):
+    tails = [1 + (7 * i) % 40 for i in range(sum(m for m, _ in groups))]
+    c = make(groups, tails, 1, heads, kv_heads, dim, page, dtype, seed=30)
+    out, lse = run(c)
+    compare(c, out, lse, [1] * len(tails))
+    for _ in range(5):
+        o, z = run(c)
+        assert torch.equal(o, out) and torch.equal(z, lse)
+
+
 def test_sequences_without_queries_and_fewer_new_tokens():
     c = make([(5, 700), (3, 300)], [4, 9, 4, 30, 5, 4, 4, 4, 7, 9], 4, 8, 2, 128, 24, "bf16", seed=7, before=1)
     new = [3, 4, 0, 1, 2, 4, 0, 0, 0, 4]
