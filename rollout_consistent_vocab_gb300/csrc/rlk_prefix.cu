@@ -36,7 +36,7 @@ struct PrefixParams {
   int32_t* first;               // [B], as in PrefixParts
   GroupPlan* plan;              // [groups]
   int32_t* busy;                // [groups] whether a sequence has new tokens
-  uint32_t* base;               // [groups + 1] items before each group
+  uint32_t* base;               // [groups + 1] units of work before each group
   const void* q;
   rlk_bth_strides qs;
   int q_heads, group;           // group: query heads of a kv head
@@ -58,26 +58,38 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
-// Items of a group: its pieces, for every kv head and block of 256 query rows.
-__device__ __forceinline__ uint32_t items_of(const PrefixParams& P, const GroupPlan& p) {
-  const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows;
-  return (rows + 255u) / 256u * P.c.kv_heads * p.pieces;
+// The work of a group in units: 512 shared tokens of a kv head for up to 128 query rows.  An
+// item, a piece of a kv head for a block of up to 256 query rows, is so many of them.
+constexpr int PIECE_UNIT = 512, PROWS = 256;
+__device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const GroupPlan& p) {
+  const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows, full = rows / PROWS, rest = rows - full * PROWS;
+  return (2u * full + (rest > PROWS / 2 ? 2u : rest > 0 ? 1u : 0u)) * p.pieces * (piece_tokens(p.shared) / PIECE_UNIT);
 }
 
 // ------------------------------------------------------------ the plan
 
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 1024, PLAN_GROUPS = 2048;         // groups that are kept in shared memory
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P) {
-  __shared__ uint32_t scan[PLAN_THREADS];
-  const int tid = threadIdx.x, G = P.groups;
+  __shared__ int32_t near_start[PLAN_GROUPS + 1], near_shared[PLAN_GROUPS], near_busy[PLAN_GROUPS];
+  __shared__ uint32_t scan[PLAN_THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, G = P.groups;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t tokens = static_cast<int64_t>(P.c.max_pages) * P.c.page_size;
+  const bool near = G <= PLAN_GROUPS;
+  const int32_t* const start = near ? near_start : P.group_start;
+  const int32_t* const shared = near ? near_shared : P.shared_lens;
+  int32_t* const busy = near ? near_busy : P.busy;
   bool fault = false;
   for (int g = tid; g < G; g += PLAN_THREADS) {
     const int a = P.group_start[g], e = P.group_start[g + 1];
     fault |= a < 0 || e < a || e > P.B;
-    P.busy[g] = 0;
+    busy[g] = 0;
+    if (near) {
+      near_start[g] = a;
+      near_shared[g] = P.shared_lens[g];
+      if (g == G - 1) near_start[G] = e;
+    }
   }
   fault = __syncthreads_or(fault);
   for (int b = tid; b < P.B; b += PLAN_THREADS) {
@@ -87,16 +99,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
       int lo = -1, hi = G;
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (P.group_start[mid] <= b) lo = mid;
+        if (start[mid] <= b) lo = mid;
         else hi = mid;
       }
-      if (lo < 0 || b >= P.group_start[lo + 1]) {
+      if (lo < 0 || b >= start[lo + 1]) {
         first = 0;
       } else {
-        const int shared = P.shared_lens[lo];
-        if (shared >= 0 && shared <= P.max_shared && shared <= tokens && (nnew == 0 || len - nnew >= shared)) {
-          first = shared / PREFIX_STEP * PREFIX_STEP;
-          if (nnew > 0 && first > 0) P.busy[lo] = 1;
+        const int in = shared[lo];
+        if (in >= 0 && in <= P.max_shared && in <= tokens && (nnew == 0 || len - nnew >= in)) {
+          first = in / PREFIX_STEP * PREFIX_STEP;
+          if (nnew > 0 && first > 0) busy[lo] = 1;
         }
       }
     }
@@ -107,27 +119,37 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
   uint32_t mine = 0;
   for (int g = g0; g < g1; ++g) {
     GroupPlan p{0, 0, 0, 0};
-    if (!fault && P.busy[g]) {
-      p.seq0 = P.group_start[g];
-      p.seqs = P.group_start[g + 1] - p.seq0;
-      p.shared = min(max(P.shared_lens[g], 0), P.max_shared) / PREFIX_STEP * PREFIX_STEP;
+    if (!fault && busy[g]) {
+      p.seq0 = start[g];
+      p.seqs = start[g + 1] - p.seq0;
+      p.shared = min(max(shared[g], 0), P.max_shared) / PREFIX_STEP * PREFIX_STEP;
       p.pieces = pieces_of(p.shared);
     }
     P.plan[g] = p;
-    mine += items_of(P, p);
+    mine += units_of_head(P, p) * P.c.kv_heads;
   }
-  scan[tid] = mine;
+  uint32_t run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += x;
+  }
+  if (lane == 31) scan[tid / 32] = run;
   __syncthreads();
-  for (int o = 1; o < PLAN_THREADS; o <<= 1) {
-    const uint32_t x = tid >= o ? scan[tid - o] : 0u;
-    __syncthreads();
-    scan[tid] += x;
-    __syncthreads();
+  if (tid < 32) {
+    uint32_t sum = scan[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    scan[lane] = sum;
   }
-  uint32_t run = scan[tid] - mine;
+  __syncthreads();
+  run += (tid >= 32 ? scan[tid / 32 - 1] : 0u) - mine;
   for (int g = g0; g < g1; ++g) {
     P.base[g] = run;
-    run += items_of(P, P.plan[g]);
+    run += units_of_head(P, P.plan[g]) * P.c.kv_heads;
   }
   if (tid == PLAN_THREADS - 1) P.base[G] = run;
 }
@@ -196,7 +218,7 @@ template <> struct Weights<__half> {
 };
 
 constexpr int PTILE = 128;               // tokens of a tile, and rows
-constexpr int PROWS = 2 * PTILE;         // query rows of a CTA
+static_assert(PROWS == 2 * PTILE, "query rows of a CTA");
 constexpr int PTHREADS = 384;
 template <int D>
 struct PShape {
@@ -210,9 +232,9 @@ struct PShape {
 };
 struct PrefixMaps { CUtensorMap k, v; };
 
-// The items in equal runs, the first ones one longer.
-__device__ __forceinline__ uint32_t run_start(uint32_t items, uint32_t workers, uint32_t k) {
-  const uint32_t len = items / workers, more = items - len * workers;
+// The units in equal runs, the first ones one longer.  An item is the CTA's whose run holds its first unit.
+__device__ __forceinline__ uint32_t run_start(uint32_t units, uint32_t workers, uint32_t k) {
+  const uint32_t len = units / workers, more = units - len * workers;
   return k * len + min(k, more);
 }
 
@@ -239,17 +261,18 @@ struct Tile {
   int seq0, head, t, count;
   bool both, first;
 };
-// A CTA's way through its run of items: an item is a piece of a group, kv head and block of rows.
+// A CTA's way through its run: `at` is the first unit of the item that is next.
 struct Way {
   uint32_t at, end;
-  int g, head, rb, piece, rows, rbs;
+  int g, head, rb, piece, rows, rbs, size;
   GroupPlan pl;
   __device__ __forceinline__ void load(const PrefixParams& P) {
     pl = P.plan[g];
     rows = pl.seqs * P.rows;
     rbs = (rows + PROWS - 1) / PROWS;
+    size = piece_tokens(pl.shared);
   }
-  __device__ __forceinline__ void find(const PrefixParams& P) {        // the group that holds item `at`
+  __device__ __forceinline__ void find(const PrefixParams& P) {        // the group that holds unit `at`
     int lo = g, hi = P.groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -259,36 +282,48 @@ struct Way {
     g = lo;
     load(P);
   }
-  __device__ __forceinline__ Way(const PrefixParams& P, uint32_t a, uint32_t e) : at(a), end(e), g(0) {
+  __device__ __forceinline__ bool both() const { return rows - rb * PROWS > PTILE; }
+  __device__ __forceinline__ uint32_t weight() const { return (both() ? 2u : 1u) * (size / PIECE_UNIT); }
+  // where the pieces of a block end, the next block, head or group (with another item: at < end)
+  __device__ __forceinline__ void settle(const PrefixParams& P) {
+    if (piece < pl.pieces || at >= end) return;
+    piece = 0;
+    if (++rb == rbs) rb = 0, ++head;
+    if (head == P.c.kv_heads) {
+      head = 0;
+      ++g;
+      load(P);
+      if (pl.pieces == 0) find(P);
+    }
+  }
+  __device__ __forceinline__ void begin(const PrefixParams& P, uint32_t a, uint32_t e) {
+    at = a, end = e, g = 0;
     if (a >= e) return;
     find(P);
-    const uint32_t rest = a - P.base[g], pieces = max(pl.pieces, 1), x = rest / pieces;
-    piece = static_cast<int>(rest - x * pieces);
-    head = static_cast<int>(x / max(rbs, 1));
-    rb = static_cast<int>(x - static_cast<uint32_t>(head) * max(rbs, 1));
+    const uint32_t whole = units_of_head(P, pl), block = 2u * pl.pieces * (size / PIECE_UNIT);
+    uint32_t rest = a - P.base[g];
+    head = static_cast<int>(rest / whole);
+    rest -= head * whole;
+    rb = static_cast<int>(min(rest / block, static_cast<uint32_t>(rbs - 1)));
+    rest -= rb * block;
+    const uint32_t w = weight();
+    piece = static_cast<int>((rest + w - 1) / w);
+    at += piece * w - rest;
+    settle(P);
   }
   // The next step; false at the run's end.
   __device__ __forceinline__ bool next(const PrefixParams& P, Step& s) {
     if (at >= end) return false;
-    const int size = piece_tokens(pl.shared);
     s.seq0 = pl.seq0, s.seqs = pl.seqs, s.head = head, s.rb = rb, s.piece = piece, s.t0 = piece * size, s.size = size;
-    s.both = rows - rb * PROWS > PTILE;
-    const bool pair = !s.both && piece + 1 < pl.pieces && at + 1 < end;
+    s.both = both();
+    const uint32_t w = weight();
+    const bool pair = !s.both && piece + 1 < pl.pieces && at + w < end;
     s.len0 = min(size, pl.shared - s.t0);
     s.len1 = s.both ? s.len0 : pair ? min(size, pl.shared - s.t0 - size) : 0;
     const int used = pair ? 2 : 1;
-    at += used;
+    at += used * w;
     piece += used;
-    if (piece >= pl.pieces && at < end) {
-      piece = 0;
-      if (++rb == rbs) rb = 0, ++head;
-      if (head == P.c.kv_heads) {
-        head = 0;
-        ++g;
-        load(P);
-        if (pl.pieces == 0) find(P);
-      }
-    }
+    settle(P);
     return true;
   }
   // The products of the run in order: op(s, cur, next, asks) takes stream s from its tile cur to its tile
@@ -423,12 +458,14 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");           // the plan
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t items = P.base[P.groups], workers = max(1u, min(items, gridDim.x));
-  // (a CTA without items goes through with an empty run)
-  const uint32_t me = min(blockIdx.x, workers);
-  Way way(P, run_start(items, workers, me), run_start(items, workers, min(me + 1, workers)));
+  Way way;
+  auto begin = [&]() {                   // the plan is made
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (a CTA without items goes through with an empty run)
+    const uint32_t units = P.base[P.groups], workers = max(1u, min(units, gridDim.x)), me = min(blockIdx.x, workers);
+    way.begin(P, run_start(units, workers, me), run_start(units, workers, min(me + 1, workers)));
+  };
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_try(bar, parity & 1)) return true;
     const unsigned long long t0 = global_timer();
@@ -446,6 +483,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     // ---- copies: each of the two warps has half of the copies of every tile, a lane one of them: a box of
     // tokens and 64 of their elements, or all (P.merged).  Its page is looked up while the tile before
     // waits for its place.
+    begin();
     const int panels = P.merged ? 1 : D / 64, copies = PTILE / P.box * panels;
     const uint32_t pages = static_cast<uint32_t>(P.c.num_pages), bytes = P.box * (P.merged ? 256 : 128);
     auto token_of = [&](int e) { return (D == 64 || P.merged ? e : e >> 1) * P.box; };
@@ -457,11 +495,10 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     const int first = lane * 2 + (warp - 10), my_token = first < copies ? token_of(first) : PTILE, my_x = panel_of(first) * 64;
     const uint32_t my_place = ring + place_of(first);
     uint32_t stage = 0, phase = 1, n = 0;                // n: tiles so far
-    uint32_t page = ~0u;
-    int place = 0;
-    Tile now{};
-    bool values = false, waiting = false;
-    // where a token of a tile lies (a page number past the last: nothing to copy)
+    // of the streams' last tile of keys, whose values come next: the page and place of this lane's copy (a page
+    // number past the last: nothing to copy), and how many copies of the warp there are
+    uint32_t page[2] = {~0u, ~0u}, count[2] = {0, 0};
+    int place[2] = {0, 0};
     auto look = [&](const Tile& x, int token, uint32_t& pg, int& pl) {
       pg = ~0u;
       if (token < x.count) {
@@ -469,56 +506,52 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         pg = static_cast<uint32_t>(__ldg(P.c.table + x.seq0 * P.c.table_stride + number));
       }
     };
-    auto copy = [&]() {                  // the tile that is looked up
+    auto copy = [&](const CUtensorMap& map, const Tile& x, uint32_t pg, int pl, uint32_t all) {
       const uint32_t bar = full + 8 * stage;
-      const CUtensorMap& map = values ? maps.v : maps.k;
-      const bool there = page < pages;
-      uint32_t all = __popc(__ballot_sync(0xffffffffu, there));
       if (copies > 64)                   // (boxes of 1 or 2 tokens)
         for (int e = first + 64; e < copies; e += 64) {
-          uint32_t pg;
-          int pl;
-          look(now, token_of(e), pg, pl);
-          all += __popc(__ballot_sync(0xffffffffu, pg < pages));
+          uint32_t p2;
+          int l2;
+          look(x, token_of(e), p2, l2);
+          all += __popc(__ballot_sync(0xffffffffu, p2 < pages));
         }
       const bool go = wait(empty + 8 * stage, phase);
       if (__all_sync(0xffffffffu, go)) {
         if (lane == 0) mbar_arrive_expect_tx(bar, all * bytes);
         __syncwarp();
-        if (there) {
-          const int c1 = P.head_first ? now.head : place, c2 = P.head_first ? place : now.head;
-          if (P.merged) copy_box5(my_place + stage * S_::TILE, map, c1, c2, page, bar);
-          else copy_box(my_place + stage * S_::TILE, map, my_x, c1, c2, page, bar);
+        if (pg < pages) {
+          const int c1 = P.head_first ? x.head : pl, c2 = P.head_first ? pl : x.head;
+          if (P.merged) copy_box5(my_place + stage * S_::TILE, map, c1, c2, pg, bar);
+          else copy_box(my_place + stage * S_::TILE, map, my_x, c1, c2, pg, bar);
         }
         if (copies > 64)
           for (int e = first + 64; e < copies; e += 64) {
-            look(now, token_of(e), page, place);
-            if (page < pages)
-              copy_box(ring + stage * S_::TILE + place_of(e), map, panel_of(e) * 64, P.head_first ? now.head : place,
-                       P.head_first ? place : now.head, page, bar);
+            uint32_t p2;
+            int l2;
+            look(x, token_of(e), p2, l2);
+            if (p2 < pages)
+              copy_box(ring + stage * S_::TILE + place_of(e), map, panel_of(e) * 64, P.head_first ? x.head : l2,
+                       P.head_first ? l2 : x.head, p2, bar);
           }
         __syncwarp();
       }
       ++n;
       if (++stage == S_::STAGES) stage = 0, phase ^= 1;
     };
-    auto fill = [&](int s, const Tile& x, bool of_values) {
-      if (x.both && s == 1) return;
-      uint32_t next_page;
-      int next_place = 0;
-      look(x, my_token, next_page, next_place);
-      if (waiting) copy();
-      waiting = true;
-      now = x;
-      values = of_values;
-      page = next_page;
-      place = next_place;
-    };
     way.walk(P, [&](int s, const Tile& x, const Tile& y, bool) {
-      if (x.count > 0) fill(s, x, true);
-      if (y.count > 0) fill(s, y, false);
+      // the next keys are looked up while the values before them are copied
+      const bool keys = y.count > 0 && !(y.both && s == 1);
+      uint32_t pg = ~0u;
+      int pl = 0;
+      if (keys) look(y, my_token, pg, pl);
+      if (x.count > 0 && !(x.both && s == 1)) copy(maps.v, x, page[s], place[s], count[s]);
+      if (keys) {
+        page[s] = pg;
+        place[s] = pl;
+        count[s] = __popc(__ballot_sync(0xffffffffu, pg < pages));
+        copy(maps.k, y, pg, pl, count[s]);
+      }
     });
-    if (waiting) copy();
     // where the products ended early, the CTA stays for its last copies
     if (*dead)
       for (uint32_t k = n > S_::STAGES ? n - S_::STAGES : 0; k < n; ++k) {
@@ -530,6 +563,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     constexpr uint32_t IDESC = (1u << 4) | (W::FORMAT << 7) | (W::FORMAT << 10) | (static_cast<uint32_t>(PTILE >> 4) << 24);
     constexpr uint32_t IDESC_QK = IDESC | (static_cast<uint32_t>(PTILE / 2 >> 3) << 17);
     constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
+    begin();
     const int mine = warp - 8;
     const uint32_t scores = tmem + mine * PTILE, result = tmem + 2 * PTILE + mine * 128;
     uint32_t n = 0, value_at = 0, key_at = 0, uses[2] = {0, 0}, blocks = 0;        // tiles, waits so far
@@ -612,7 +646,10 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     uint32_t used0 = 0, used1 = 0, total = 0, seen = 0;    // waits so far; halves of tiles so far, and those whose results are in
     Step st, nxt;
     Rows held;
-    bool have = way.next(P, st), dry = true;
+    // Before the plan is made, half a tile without scores in the result's place: it brings the instructions,
+    // which would be 3 us of the first half's 4.
+    bool have = true, dry = true;
+    st.len0 = st.len1 = 64;
     int64_t out = -1;                    // the row's first part, in parts; -1: no query
     auto ask = [&](const Step& x) {      // the queries of the stream's rows of x
       held.take(x);
@@ -640,13 +677,13 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
       if (lane == 0) mbar_arrive(asked + 8 * s);
     };
     for (; have; st = nxt) {
-      const bool more = way.next(P, nxt);
+      const bool more = !dry && way.next(P, nxt);
       const int all = st.tokens(s);
       if (all > 0) {
-        if (!held.of(st)) ask(st);
+        if (!dry && !held.of(st)) ask(st);
         // whether all the piece's pages are there
         bool bad = false;
-        {
+        if (!dry) {
           int place;
           const int to = static_cast<int>(page_of(P.c, P.page_magic, st.from(s) + all - 1, place));
           for (int p = static_cast<int>(page_of(P.c, P.page_magic, st.from(s), place)) + lane; p <= to; p += 32) {
@@ -659,11 +696,9 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         const bool query = out >= 0;
         float m = -INFINITY, l = 0.0f;
         const int halves = (all + 63) / 64;
-        // (the first tile's scores are a while in coming: half a tile without any in the meantime, into the
-        // result's place, which brings the instructions)
 #pragma unroll 1
-        for (int h = dry ? -1 : 0; h < halves; ++h, dry = false) {
-          const bool two = dry || all - h * 64 > 32;             // 64 tokens, not 32
+        for (int h = 0; h < halves; ++h) {
+          const bool two = all - h * 64 > 32;                    // 64 tokens, not 32
           const uint32_t at = dry ? result : scores + (h & 1) * 64;
           if (!dry) {
             if (h & 1) wait(scored + 16 * s + 8, used1++);
@@ -732,10 +767,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (dry) {
-            m = -INFINITY;
-            l = 0.0f;
-          } else {
+          if (!dry) {
             // (one half at a time is under way to the result, so that no wait is ever two behind)
             if (seen < total) wait(summed + 8 * s, seen++);
             __syncwarp();
@@ -743,6 +775,12 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
             if (lane == 0) mbar_arrive(weighed + 16 * s + 8 * (h & 1));
           }
           __syncwarp();
+        }
+        if (dry) {
+          dry = false;
+          begin();
+          have = way.next(P, nxt);
+          continue;
         }
         if (more && nxt.tokens(s) > 0 && !held.of(nxt)) ask(nxt);        // (all products with the old ones are done)
         bad |= !wait(summed + 8 * s, seen++) || *dead != 0u;
