@@ -226,7 +226,7 @@ struct PShape {
   static constexpr int TILE = D / 64 * PANEL;
   static constexpr int HALF = TILE / 2;            // keys and values: 64 tokens' panels, then the others'
   static constexpr int STAGES = D == 128 ? 5 : 10;
-  static constexpr int BARS = 2 * STAGES + 2 * 6 + 1;
+  static constexpr int BARS = 2 * STAGES + 2 * 7 + 1;
   static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BARS * 8 + 16;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
@@ -272,14 +272,15 @@ struct Way {
     rbs = (rows + PROWS - 1) / PROWS;
     size = piece_tokens(pl.shared);
   }
-  __device__ __forceinline__ void find(const PrefixParams& P) {        // the group that holds unit `at`
-    int lo = g, hi = P.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (P.base[mid] <= at) lo = mid;
-      else hi = mid;
+  // the group that holds unit `at`, from g on; the whole warp
+  __device__ __forceinline__ void find(const PrefixParams& P) {
+    int hi = P.groups;
+    while (hi - g > 1) {
+      const int step = (hi - g + 31) / 32, mine = g + static_cast<int>(threadIdx.x & 31) * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, mine < hi && P.base[mine] <= at);      // (of g it is)
+      g += (31 - __clz(below)) * step;
+      hi = min(hi, g + step);
     }
-    g = lo;
     load(P);
   }
   __device__ __forceinline__ bool both() const { return rows - rb * PROWS > PTILE; }
@@ -434,15 +435,14 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   const uint32_t raw = smem_addr(smem_raw), queries = (raw + 1023u) & ~1023u, ring = queries + 2 * S_::TILE;
   const uint32_t bars = ring + S_::STAGES * S_::TILE;
   const uint32_t full = bars, empty = bars + 8 * S_::STAGES, streams = empty + 8 * S_::STAGES;
-  // of stream s: half h of a tile has scores, or weights, at 16 s + 8 h; a half's result is in, queries are there, at 8 s
-  const uint32_t scored = streams, weighed = streams + 32, summed = streams + 64, asked = streams + 80, last = streams + 96;
-  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 104 - raw));
+  // of stream s, at 16 s + 8 h: half h of a tile has scores, or weights, an even or odd half's result is in; at 8 s: queries
+  const uint32_t scored = streams, weighed = streams + 32, summed = streams + 64, asked = streams + 96, last = streams + 112;
+  uint32_t* const slot = reinterpret_cast<uint32_t*>(smem_raw + (streams + 120 - raw));
   volatile uint32_t* const dead = slot + 1;        // a wait gave up: everything ends, within limits
   if (tid == 0) {
     for (int s = 0; s < S_::STAGES; ++s) mbar_init(full + 8 * s, 2), mbar_init(empty + 8 * s, 2);
     for (int s = 0; s < 2; ++s) {
-      for (int h = 0; h < 2; ++h) mbar_init(scored + 16 * s + 8 * h, 1), mbar_init(weighed + 16 * s + 8 * h, 4);
-      mbar_init(summed + 8 * s, 1);
+      for (int h = 0; h < 2; ++h) mbar_init(scored + 16 * s + 8 * h, 1), mbar_init(weighed + 16 * s + 8 * h, 4), mbar_init(summed + 16 * s + 8 * h, 1);
       mbar_init(asked + 8 * s, 4);
     }
     mbar_init(last, 2);
@@ -494,6 +494,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     };
     const int first = lane * 2 + (warp - 10), my_token = first < copies ? token_of(first) : PTILE, my_x = panel_of(first) * 64;
     const uint32_t my_place = ring + place_of(first);
+    // (keys and values go first when the L2 is full: the pieces' results are to stay there for the join)
+    const uint64_t policy = evict_first_policy();
     uint32_t stage = 0, phase = 1, n = 0;                // n: tiles so far
     // of the streams' last tile of keys, whose values come next: the page and place of this lane's copy (a page
     // number past the last: nothing to copy), and how many copies of the warp there are
@@ -521,8 +523,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         __syncwarp();
         if (pg < pages) {
           const int c1 = P.head_first ? x.head : pl, c2 = P.head_first ? pl : x.head;
-          if (P.merged) copy_box5(my_place + stage * S_::TILE, map, c1, c2, pg, bar);
-          else copy_box(my_place + stage * S_::TILE, map, my_x, c1, c2, pg, bar);
+          if (P.merged) copy_box5(my_place + stage * S_::TILE, map, c1, c2, pg, bar, policy);
+          else copy_box(my_place + stage * S_::TILE, map, my_x, c1, c2, pg, bar, policy);
         }
         if (copies > 64)
           for (int e = first + 64; e < copies; e += 64) {
@@ -531,7 +533,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
             look(x, token_of(e), p2, l2);
             if (p2 < pages)
               copy_box(ring + stage * S_::TILE + place_of(e), map, panel_of(e) * 64, P.head_first ? x.head : l2,
-                       P.head_first ? l2 : x.head, p2, bar);
+                       P.head_first ? l2 : x.head, p2, bar, policy);
           }
         __syncwarp();
       }
@@ -566,7 +568,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     begin();
     const int mine = warp - 8;
     const uint32_t scores = tmem + mine * PTILE, result = tmem + 2 * PTILE + mine * 128;
-    uint32_t n = 0, value_at = 0, key_at = 0, uses[2] = {0, 0}, blocks = 0;        // tiles, waits so far
+    uint32_t n = 0, value_at = 0, key_at = 0, uses[2] = {0, 0}, blocks = 0, halves = 0;   // tiles, waits, halves of tiles so far
     // Both streams' warps go by every tile, so that neither is ever more than one round of the ring
     // behind: a stage is free when both have let it go, at once where the tile is the other's.
     auto take = [&](int s, const Tile& x, uint32_t& at) {
@@ -603,11 +605,12 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
                     umma_ts(result, a, b + 256 * c, IDESC_PV, !x.first || h > 0 || part == 0 || c > 0);
                     umma_ts(result, a + 8, b + 256 * c + 128, IDESC_PV, true);
                   }
-              umma_commit(summed + 8 * mine);
+              umma_commit(summed + 16 * mine + 8 * (halves & 1));
               if (x.count <= h * 64 + 64) umma_commit(empty + 8 * (value_at % S_::STAGES));
             }
             __syncwarp();
           }
+          ++halves;
         }
         // the scores of half of the next, in the place of what was just used
         if (h * 64 < y.count) {
@@ -643,7 +646,10 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     const int s = warp >> 2, row = tid & (PTILE - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scores = tmem + s * PTILE + lanes, result = tmem + 2 * PTILE + s * 128 + lanes;
-    uint32_t used0 = 0, used1 = 0, total = 0, seen = 0;    // waits so far; halves of tiles so far, and those whose results are in
+    uint32_t used0 = 0, used1 = 0, total = 0;              // waits so far; halves of tiles so far
+    // Half n's part of the result.  Even and odd halves have a barrier each: when a half has its scores, the
+    // result of the one before the last is in, so that no wait is two rounds behind, whichever are left out.
+    auto result_in = [&](uint32_t n) { return wait(summed + 16 * s + 8 * (n & 1), n >> 1); };
     Step st, nxt;
     Rows held;
     // Before the plan is made, half a tile without scores in the result's place: it brings the instructions,
@@ -727,7 +733,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           }
           if (__any_sync(0xffffffffu, fac != 1.0f) && !dry) {
             l *= fac;
-            if (seen < total) wait(summed + 8 * s, seen++);
+            result_in(total - 1);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -768,9 +774,6 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           tc_fence_before();
           __syncwarp();
           if (!dry) {
-            // (one half at a time is under way to the result, so that no wait is ever two behind)
-            if (seen < total) wait(summed + 8 * s, seen++);
-            __syncwarp();
             ++total;
             if (lane == 0) mbar_arrive(weighed + 16 * s + 8 * (h & 1));
           }
@@ -783,7 +786,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           continue;
         }
         if (more && nxt.tokens(s) > 0 && !held.of(nxt)) ask(nxt);        // (all products with the old ones are done)
-        bad |= !wait(summed + 8 * s, seen++) || *dead != 0u;
+        bad |= !result_in(total - 1) || *dead != 0u;
         bad = __any_sync(0xffffffffu, bad);
         tc_fence_after();
         if (bad && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);

@@ -45,11 +45,17 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap& map, i
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
 }
-// ... of a 5-dimensional one, from the beginning of its first and last place
-__device__ __forceinline__ void copy_box5(uint32_t dst, const CUtensorMap& map, int c1, int c2, int c3, uint32_t bar) {
+// ... with a cache policy
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap& map, int c0, int c1, int c2, int c3, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %2}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy) : "memory");
+}
+// ... of a 5-dimensional one, from the beginning of its first and last place
+__device__ __forceinline__ void copy_box5(uint32_t dst, const CUtensorMap& map, int c1, int c2, int c3, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %2}], [%6], %7;"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy) : "memory");
 }
 
 }  // namespace rlk
