@@ -184,40 +184,45 @@ __device__ __forceinline__ void load_factors(const Turns& t, const float* cs, in
 }
 
 template <class T>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 2 : 3) rope_kernel(const __grid_constant__ RopeParams P) {
   __shared__ __align__(16) float cs[ROPE_TOKENS * RLK_ROPE_MAX_DIM];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(P.per), P.tokens - t0));
-  block_turns(P.t, cs, tokens, nullptr, t0);
-  __syncthreads();
   // the threads as [head][token][item]
   const int row = tokens * P.items, slots = ROPE_THREADS / row;
   const int h0 = threadIdx.x / row, rest = threadIdx.x - h0 * row, k = rest / P.items, it = rest - k * P.items;
-  if (h0 >= slots) return;
   const Item e = item_of(P.t, it);
-  if (!e.turns && P.in_place) return;
-  float c[8], s[8];
-  if (e.turns) load_factors(P.t, cs, k, it, c, s);
+  const bool works = h0 < slots && (e.turns || !P.in_place);
   const uint64_t at = static_cast<uint64_t>(t0) + k, b = at / P.n, i = at - b * P.n;
   const char* src = P.x.p + b * P.x.batch + i * P.x.token;
   char* dst = const_cast<char*>(P.out.p) + b * P.out.batch + i * P.out.token;
-  for (int h = h0; h < P.heads; h += slots * ROPE_AHEAD) {
-    Eight<T> lo[ROPE_AHEAD], hi[ROPE_AHEAD];
+  const int heads = works ? P.heads : 0;
+  Eight<T> lo[ROPE_AHEAD], hi[ROPE_AHEAD];
+  auto load = [&](int h) {
 #pragma unroll
     for (int j = 0; j < ROPE_AHEAD; ++j)
-      if (h + j * slots < P.heads) {
+      if (h + j * slots < heads) {
         const char* p = src + (h + j * slots) * P.x.head;
         lo[j].load(p + e.lo * sizeof(T));
         hi[j].load(p + e.hi * sizeof(T));
       }
+  };
+  load(h0);                              // (under way while the angles are taken)
+  block_turns(P.t, cs, tokens, nullptr, t0);
+  __syncthreads();
+  float c[8], s[8];
+  if (e.turns && works) load_factors(P.t, cs, k, it, c, s);
+  for (int h = h0; h < heads;) {
 #pragma unroll
     for (int j = 0; j < ROPE_AHEAD; ++j)
-      if (h + j * slots < P.heads) {
+      if (h + j * slots < heads) {
         if (e.turns) turn(lo[j], hi[j], c, s, P.t.interleaved);
         char* p = dst + (h + j * slots) * P.out.head;
         lo[j].store(p + e.lo * sizeof(T));
         hi[j].store(p + e.hi * sizeof(T));
       }
+    h += slots * ROPE_AHEAD;
+    load(h);
   }
 }
 
@@ -232,96 +237,87 @@ struct AppendRopeParams {
 };
 
 template <class T>
-__global__ void __launch_bounds__(ROPE_THREADS) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
-  enum : int { THERE = 0, NO_PAGE = 1, NO_TOKEN = 2, REJECTED = 3 };
+__global__ void __launch_bounds__(ROPE_THREADS, 3) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
   __shared__ __align__(16) float cs[ROPE_TOKENS * RLK_ROPE_MAX_DIM];
-  __shared__ int64_t place[ROPE_TOKENS];           // of the token's first head in the cache, in elements
-  __shared__ int position[ROPE_TOKENS], state[ROPE_TOKENS];
+  __shared__ int64_t place[ROPE_TOKENS];           // of the token's first head in the cache, in elements; -1: none
+  __shared__ int position[ROPE_TOKENS];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(P.per), P.tokens - t0));
-  const uint32_t n = P.c.n;
-  if (threadIdx.x < tokens) {
-    const uint64_t at = static_cast<uint64_t>(t0) + threadIdx.x;
-    const int b = static_cast<int>(at / n), i = static_cast<int>(at - static_cast<uint64_t>(b) * n);
-    int len, nnew, st = THERE, pos = 0;
-    int64_t to = 0;
-    if (!seq_lens(P.c, b, len, nnew)) {
-      st = REJECTED;
-      if (i == 0 && P.c.err) atomicAdd(P.c.err, 1);
-    } else if (i >= nnew) {
-      st = NO_TOKEN;
-    } else {
-      pos = len - nnew + i;
-      const int number = pos / P.c.page_size;
-      const int page = P.c.table[b * P.c.table_stride + number];
-      if (page < 0 || page >= P.c.num_pages) {
-        st = NO_PAGE;
-        if (P.c.err) atomicAdd(P.c.err, 1);
-      } else {
-        to = page * P.c.page_stride + (pos - number * P.c.page_size) * P.c.token_stride;
-      }
-    }
-    place[threadIdx.x] = to;
-    position[threadIdx.x] = pos;
-    state[threadIdx.x] = st;
-  }
-  __syncthreads();
-  block_turns(P.t, cs, tokens, position, t0);
-  __syncthreads();
+  // the threads as [head][token][item]
   const int row = tokens * P.items, slots = ROPE_THREADS / row;
   const int h0 = threadIdx.x / row, rest = threadIdx.x - h0 * row, k = rest / P.items, it = rest - k * P.items;
-  if (h0 >= slots) return;
   const Item e = item_of(P.t, it);
-  const int st = state[k];
-  float c[8], s[8];
-  if (e.turns) load_factors(P.t, cs, k, it, c, s);
-  const uint64_t at = static_cast<uint64_t>(t0) + k, b = at / n, i = at - b * n;
-  const int heads = P.q_heads + 2 * P.c.kv_heads;        // queries, keys, values
+  const uint32_t n = P.c.n;
+  const uint64_t at = static_cast<uint64_t>(t0) + k;
+  const int b = static_cast<int>(at / n), i = static_cast<int>(at - static_cast<uint64_t>(b) * n);
+  int len, nnew;
+  const bool fine = seq_lens(P.c, b, len, nnew), there = fine && i < nnew;
+  // queries, keys, values; of a place without a token only the queries' places are written
+  const int heads = h0 >= slots ? 0 : there ? P.q_heads + 2 * P.c.kv_heads : P.q_heads;
   const bool in_place = P.q.p == P.q_out.p;
   const int64_t lo_at = e.lo * static_cast<int64_t>(sizeof(T)), hi_at = e.hi * static_cast<int64_t>(sizeof(T));
-  for (int h = h0; h < heads; h += slots * ROPE_AHEAD) {
-    Eight<T> lo[ROPE_AHEAD], hi[ROPE_AHEAD];
-    char* dst[ROPE_AHEAD];
-    bool turns[ROPE_AHEAD];
+  Eight<T> lo[ROPE_AHEAD], hi[ROPE_AHEAD];
+  auto load = [&](int h) {
 #pragma unroll
     for (int j = 0; j < ROPE_AHEAD; ++j) {
       const int g = h + j * slots;
-      dst[j] = nullptr;
-      if (g >= heads) continue;
-      const char* src;
-      if (g < P.q_heads) {
-        dst[j] = const_cast<char*>(P.q_out.p) + b * P.q_out.batch + i * P.q_out.token + g * P.q_out.head;
-        turns[j] = e.turns;
-        if (st >= NO_TOKEN) {
-          lo[j].fill(st == REJECTED ? __int_as_float(0x7fc00000) : 0.0f);
-          hi[j] = lo[j];
-          turns[j] = false;
-          continue;
-        }
-        if (!e.turns && in_place) {
-          dst[j] = nullptr;
-          continue;
-        }
-        src = P.q.p + b * P.q.batch + i * P.q.token + g * P.q.head;
-      } else {
-        if (st != THERE) continue;
-        const bool key = g < P.q_heads + P.c.kv_heads;
-        const int z = key ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
-        const HeadRows& r = key ? P.k : P.v;
-        src = r.p + b * r.batch + i * r.token + z * r.head;
-        dst[j] = static_cast<char*>(const_cast<void*>(key ? P.c.k : P.c.v)) + (place[k] + z * P.c.head_stride) * static_cast<int64_t>(sizeof(T));
-        turns[j] = key && e.turns;
-      }
-      lo[j].load(src + lo_at);
-      hi[j].load(src + hi_at);
+      if (g >= heads || !there) continue;
+      const int z = g < P.q_heads ? g : g < P.q_heads + P.c.kv_heads ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
+      const HeadRows& r = g < P.q_heads ? P.q : g < P.q_heads + P.c.kv_heads ? P.k : P.v;
+      const char* p = r.p + b * r.batch + i * r.token + z * r.head;
+      lo[j].load(p + lo_at);
+      hi[j].load(p + hi_at);
     }
+  };
+  load(h0);                              // (under way while places and angles are looked up)
+  if (threadIdx.x < row && it == 0) {
+    int64_t to = -1;
+    int pos = 0;
+    if (there) {
+      pos = len - nnew + i;
+      const int number = pos / P.c.page_size;
+      const int page = P.c.table[b * P.c.table_stride + number];
+      if (page >= 0 && page < P.c.num_pages)
+        to = page * P.c.page_stride + (pos - number * P.c.page_size) * P.c.token_stride;
+    }
+    place[k] = to;
+    position[k] = pos;
+    if (P.c.err && (fine ? there && to < 0 : i == 0)) atomicAdd(P.c.err, 1);
+  }
+  if (!P.t.positions) __syncthreads();
+  block_turns(P.t, cs, tokens, position, t0);
+  __syncthreads();
+  float c[8], s[8];
+  if (e.turns && heads > 0) load_factors(P.t, cs, k, it, c, s);
+  const int64_t to = place[k];
+  for (int h = h0; h < heads;) {
 #pragma unroll
     for (int j = 0; j < ROPE_AHEAD; ++j) {
-      if (!dst[j]) continue;
-      if (turns[j]) turn(lo[j], hi[j], c, s, P.t.interleaved);
-      lo[j].store(dst[j] + lo_at);
-      hi[j].store(dst[j] + hi_at);
+      const int g = h + j * slots;
+      if (g >= heads) continue;
+      char* dst;
+      if (g < P.q_heads) {
+        if (!there) {
+          lo[j].fill(fine ? 0.0f : __int_as_float(0x7fc00000));
+          hi[j] = lo[j];
+        } else if (e.turns) {
+          turn(lo[j], hi[j], c, s, P.t.interleaved);
+        } else if (in_place) {
+          continue;
+        }
+        dst = const_cast<char*>(P.q_out.p) + b * P.q_out.batch + i * P.q_out.token + g * P.q_out.head;
+      } else {
+        if (to < 0) continue;
+        const bool key = g < P.q_heads + P.c.kv_heads;
+        const int z = key ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
+        if (key && e.turns) turn(lo[j], hi[j], c, s, P.t.interleaved);
+        dst = static_cast<char*>(const_cast<void*>(key ? P.c.k : P.c.v)) + (to + z * P.c.head_stride) * static_cast<int64_t>(sizeof(T));
+      }
+      lo[j].store(dst + lo_at);
+      hi[j].store(dst + hi_at);
     }
+    h += slots * ROPE_AHEAD;
+    load(h);
   }
 }
 
@@ -359,12 +355,12 @@ static HeadRows head_rows(const void* p, const rlk_bth_strides* s, int size) {
   return {static_cast<const char*>(p), s->batch * size, s->token * size, s->head * size};
 }
 
-// Tokens of a block: the more, the fewer the heads that a thread goes over one after the
-// other; but as many blocks as two to an SM, where there are as many tokens.
+// Tokens of a block: as many as leave a thread no more heads than it loads at once, but as many
+// blocks as two to an SM, where there are as many tokens.
 static int tokens_per_block(int64_t tokens, int items, int heads) {
   int per = 1;
   while (per < ROPE_TOKENS && 2 * per * items <= ROPE_THREADS &&
-         ROPE_THREADS / (per * items) * ROPE_AHEAD > heads && tokens > 2 * 152 * 2 * per)
+         ROPE_THREADS / (2 * per * items) * ROPE_AHEAD >= heads && tokens > 2 * 152 * 2 * per)
     per *= 2;
   return per;
 }
