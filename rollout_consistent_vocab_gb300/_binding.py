@@ -1003,11 +1003,12 @@ def _rope_args(inv_freq, pair_axis, interleaved, positions, B, n, dev) -> RopeAr
         raise ValueError(f"pair_axis must be a contiguous uint8 CPU tensor of shape [{pairs}]")
     axes = 4
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.dim() not in (2, 3) or tuple(positions.shape[-2:]) != (B, n) \
-                or not positions.is_contiguous():
+        shape = positions.shape
+        if positions.dtype != torch.int32 or (shape != (B, n) if len(shape) != 3 else shape[1:] != (B, n)) or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 tensor of shape [{B}, {n}] or [axes, {B}, {n}]")
-        _placed(positions, dev, "positions")
-        axes = positions.shape[0] if positions.dim() == 3 else 1
+        if positions.get_device() != dev:
+            _placed(positions, dev, "positions")
+        axes = shape[0] if len(shape) == 3 else 1
     return RopeArgs(inv_freq.data_ptr(), _ptr(pair_axis), 2 * pairs, 1 if interleaved else 0, _ptr(positions), axes)
 
 
@@ -1029,21 +1030,24 @@ def rope(x, inv_freq, positions, *, pair_axis=None, interleaved=False, inverse=F
     dev = x.get_device()
     if dev < 0:
         raise ValueError("x must live on the GPU")
-    if x.dtype == torch.bfloat16:
+    dtype = x.dtype
+    if dtype == torch.bfloat16:
         code = RLK_DT_BF16
-    elif x.dtype == torch.float16:
+    elif dtype == torch.float16:
         code = RLK_DT_F16
-    elif x.dtype == torch.float32:
+    elif dtype == torch.float32:
         code = RLK_DT_F32
     else:
-        raise ValueError(f"the dtype {x.dtype} must be float32, bfloat16 or float16")
+        raise ValueError(f"the dtype {dtype} must be float32, bfloat16 or float16")
     if positions is None:
         raise ValueError("positions must be given")
     a = _rope_args(inv_freq, pair_axis, interleaved, positions, B, n, dev)
     xs = _bth(x, shape, x.dtype, "x", dev)
     if out is None:
         out = (torch.empty if stream is None else _maker(stream))(shape, dtype=x.dtype, device=x.device)
-    os_ = _bth(out, shape, x.dtype, "out", dev)
+        os_ = BTHStrides(n * heads * dim, heads * dim, dim)
+    else:
+        os_ = _bth(out, shape, x.dtype, "out", dev)
     check(lib.rlk_rope(a, B, n, heads, dim, code, x.data_ptr(), xs, out.data_ptr(), os_, 1 if inverse else 0,
                        _stream(stream, dev)))
     return out

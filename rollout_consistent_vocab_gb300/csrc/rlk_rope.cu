@@ -7,9 +7,12 @@
 // 32 bits, taken to the nearest quarter turn, leave at most an eighth: sine and
 // cosine of that, to float32's accuracy, then the quarters by exchange and sign.
 //
-// A block takes a few tokens: one sine and cosine per token and pair, by all threads
-// into shared memory; then each thread holds the eight pairs of its 16 elements in
-// registers and goes over the token's heads, several heads' loads under way at once.
+// A block takes a few tokens: a thread has the same 16 elements of a few of their heads, whose loads go out
+// first; meanwhile all threads take one sine and cosine per token and pair into shared memory,
+// and those of the cache's places are looked up.  Bound by memory: 4 x 4096 tokens of 32 heads of 128
+// elements, bf16, 268 MB, 0.041 ms = 6.5 TB/s; three axes, 28 heads, 117 MB, 0.0174 ms = 6.7 TB/s;
+// append of 16 x 2048 tokens, 32 query heads on 8, 755 MB, 0.127 ms = 5.9 TB/s.  Blocks of 256 threads:
+// 0.041, 0.0185, 0.141 ms; loads behind the angles: 0.047, 0.025, 0.160.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,8 +26,9 @@
 
 namespace rlk {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_AHEAD = 4;            // heads of a thread whose loads are under way together
+constexpr int ROPE_THREADS = 128;
+// heads of a thread whose loads are under way together: alone, and in the append
+constexpr int ROPE_AHEAD = 4, APPEND_AHEAD = 3;
 constexpr int ROPE_TOKENS = 8;           // of a block, at most
 
 struct Turns {
@@ -75,7 +79,9 @@ template <> struct Eight<float> {
 };
 struct Eight16 {
   uint4 w;
+  // (read once; but the append of 16 x 2048 tokens takes 0.132 ms with loads that leave the caches first, 0.127 without)
   __device__ __forceinline__ void load(const char* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_kept(const char* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint4*>(p) = w; }
 };
 template <> struct Eight<__nv_bfloat16> : Eight16 {
@@ -157,11 +163,12 @@ struct RopeParams {
   bool in_place;
 };
 
-// The cosines and sines of a block's tokens, [token][cos, sin][pair].
-__device__ __forceinline__ void block_turns(const Turns& t, float* cs, int tokens, const int* place, int64_t t0) {
+// The cosines and sines of a block's tokens, [token][cos, sin][pair]; place(token) is where positions has none.
+template <class Place>
+__device__ __forceinline__ void block_turns(const Turns& t, float* cs, int tokens, int64_t t0, Place place) {
   for (int e = threadIdx.x; e < tokens * t.pairs; e += ROPE_THREADS) {
     const int k = e / t.pairs, j = e - k * t.pairs;
-    const int position = t.positions ? t.positions[t.axis[j] * t.axis_stride + t0 + k] : place[k];
+    const int position = t.positions ? __ldg(t.positions + t.axis[j] * t.axis_stride + t0 + k) : place(k);
     const float2 v = cos_sin(t.turn[j], position);
     cs[k * (2 * t.pairs) + j] = v.x;
     cs[k * (2 * t.pairs) + t.pairs + j] = t.inverse ? -v.y : v.y;
@@ -184,7 +191,7 @@ __device__ __forceinline__ void load_factors(const Turns& t, const float* cs, in
 }
 
 template <class T>
-__global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 2 : 3) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 4 : 6) rope_kernel(const __grid_constant__ RopeParams P) {
   __shared__ __align__(16) float cs[ROPE_TOKENS * RLK_ROPE_MAX_DIM];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(P.per), P.tokens - t0));
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 2 : 3) rope_ker
   const int h0 = threadIdx.x / row, rest = threadIdx.x - h0 * row, k = rest / P.items, it = rest - k * P.items;
   const Item e = item_of(P.t, it);
   const bool works = h0 < slots && (e.turns || !P.in_place);
-  const uint64_t at = static_cast<uint64_t>(t0) + k, b = at / P.n, i = at - b * P.n;
+  const uint32_t at = static_cast<uint32_t>(t0) + k, b = at / P.n, i = at - b * P.n;     // (B * n is below 2^32)
   const char* src = P.x.p + b * P.x.batch + i * P.x.token;
   char* dst = const_cast<char*>(P.out.p) + b * P.out.batch + i * P.out.token;
   const int heads = works ? P.heads : 0;
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 2 : 3) rope_ker
       }
   };
   load(h0);                              // (under way while the angles are taken)
-  block_turns(P.t, cs, tokens, nullptr, t0);
+  block_turns(P.t, cs, tokens, t0, [](int) { return 0; });
   __syncthreads();
   float c[8], s[8];
   if (e.turns && works) load_factors(P.t, cs, k, it, c, s);
@@ -237,10 +244,9 @@ struct AppendRopeParams {
 };
 
 template <class T>
-__global__ void __launch_bounds__(ROPE_THREADS, 3) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
+__global__ void __launch_bounds__(ROPE_THREADS, 8) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
   __shared__ __align__(16) float cs[ROPE_TOKENS * RLK_ROPE_MAX_DIM];
   __shared__ int64_t place[ROPE_TOKENS];           // of the token's first head in the cache, in elements; -1: none
-  __shared__ int position[ROPE_TOKENS];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(P.per), P.tokens - t0));
   // the threads as [head][token][item]
@@ -248,51 +254,51 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) append_rope_kernel(const __gr
   const int h0 = threadIdx.x / row, rest = threadIdx.x - h0 * row, k = rest / P.items, it = rest - k * P.items;
   const Item e = item_of(P.t, it);
   const uint32_t n = P.c.n;
-  const uint64_t at = static_cast<uint64_t>(t0) + k;
-  const int b = static_cast<int>(at / n), i = static_cast<int>(at - static_cast<uint64_t>(b) * n);
+  const uint32_t at = static_cast<uint32_t>(t0) + k;       // (B * n is below 2^32)
+  const int b = static_cast<int>(at / n), i = static_cast<int>(at - b * n);
   int len, nnew;
   const bool fine = seq_lens(P.c, b, len, nnew), there = fine && i < nnew;
   // queries, keys, values; of a place without a token only the queries' places are written
   const int heads = h0 >= slots ? 0 : there ? P.q_heads + 2 * P.c.kv_heads : P.q_heads;
   const bool in_place = P.q.p == P.q_out.p;
   const int64_t lo_at = e.lo * static_cast<int64_t>(sizeof(T)), hi_at = e.hi * static_cast<int64_t>(sizeof(T));
-  Eight<T> lo[ROPE_AHEAD], hi[ROPE_AHEAD];
+  Eight<T> lo[APPEND_AHEAD], hi[APPEND_AHEAD];
   auto load = [&](int h) {
 #pragma unroll
-    for (int j = 0; j < ROPE_AHEAD; ++j) {
+    for (int j = 0; j < APPEND_AHEAD; ++j) {
       const int g = h + j * slots;
       if (g >= heads || !there) continue;
       const int z = g < P.q_heads ? g : g < P.q_heads + P.c.kv_heads ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
       const HeadRows& r = g < P.q_heads ? P.q : g < P.q_heads + P.c.kv_heads ? P.k : P.v;
       const char* p = r.p + b * r.batch + i * r.token + z * r.head;
-      lo[j].load(p + lo_at);
-      hi[j].load(p + hi_at);
+      lo[j].load_kept(p + lo_at);
+      hi[j].load_kept(p + hi_at);
     }
   };
   load(h0);                              // (under way while places and angles are looked up)
   if (threadIdx.x < row && it == 0) {
     int64_t to = -1;
-    int pos = 0;
     if (there) {
-      pos = len - nnew + i;
-      const int number = pos / P.c.page_size;
+      const int pos = len - nnew + i, number = pos / P.c.page_size;
       const int page = P.c.table[b * P.c.table_stride + number];
       if (page >= 0 && page < P.c.num_pages)
         to = page * P.c.page_stride + (pos - number * P.c.page_size) * P.c.token_stride;
     }
     place[k] = to;
-    position[k] = pos;
     if (P.c.err && (fine ? there && to < 0 : i == 0)) atomicAdd(P.c.err, 1);
   }
-  if (!P.t.positions) __syncthreads();
-  block_turns(P.t, cs, tokens, position, t0);
+  block_turns(P.t, cs, tokens, t0, [&](int z) {
+    const uint32_t u = static_cast<uint32_t>(t0) + z, s = u / n;
+    int l, m;
+    return seq_lens(P.c, static_cast<int>(s), l, m) ? l - m + static_cast<int>(u - s * n) : 0;
+  });
   __syncthreads();
   float c[8], s[8];
   if (e.turns && heads > 0) load_factors(P.t, cs, k, it, c, s);
   const int64_t to = place[k];
   for (int h = h0; h < heads;) {
 #pragma unroll
-    for (int j = 0; j < ROPE_AHEAD; ++j) {
+    for (int j = 0; j < APPEND_AHEAD; ++j) {
       const int g = h + j * slots;
       if (g >= heads) continue;
       char* dst;
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 3) append_rope_kernel(const __gr
       lo[j].store(dst + lo_at);
       hi[j].store(dst + hi_at);
     }
-    h += slots * ROPE_AHEAD;
+    h += slots * APPEND_AHEAD;
     load(h);
   }
 }
@@ -357,10 +363,10 @@ static HeadRows head_rows(const void* p, const rlk_bth_strides* s, int size) {
 
 // Tokens of a block: as many as leave a thread no more heads than it loads at once, but as many
 // blocks as two to an SM, where there are as many tokens.
-static int tokens_per_block(int64_t tokens, int items, int heads) {
+static int tokens_per_block(int64_t tokens, int items, int heads, int ahead) {
   int per = 1;
   while (per < ROPE_TOKENS && 2 * per * items <= ROPE_THREADS &&
-         ROPE_THREADS / (2 * per * items) * ROPE_AHEAD >= heads && tokens > 2 * 152 * 2 * per)
+         ROPE_THREADS / (2 * per * items) * ahead >= heads && tokens > 2 * 152 * 2 * per)
     per *= 2;
   return per;
 }
@@ -405,7 +411,7 @@ rlk_status rlk_rope(const rlk_rope_args* rope, int64_t B, int64_t n, int32_t hea
   P.n = static_cast<uint32_t>(n);
   P.heads = heads;
   P.items = head_dim / 16;
-  P.per = tokens_per_block(P.tokens, P.items, heads);
+  P.per = tokens_per_block(P.tokens, P.items, heads, ROPE_AHEAD);
   const int64_t blocks = (P.tokens + P.per - 1) / P.per;
   if (blocks >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n is too large for one call");
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -445,7 +451,7 @@ rlk_status rlk_kv_append_rope(const rlk_kv_cache* cache, const rlk_rope_args* ro
   P.tokens = cache->B * cache->n;
   P.q_heads = q_heads;
   P.items = cache->head_dim / 16;
-  P.per = tokens_per_block(P.tokens, P.items, q_heads + 2 * cache->kv_heads);
+  P.per = tokens_per_block(P.tokens, P.items, q_heads + 2 * cache->kv_heads, APPEND_AHEAD);
   const int64_t blocks = (P.tokens + P.per - 1) / P.per;
   if (blocks >= (int64_t(1) << 31)) return fail(RLK_EINVAL, "B * n is too large for one call");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
