@@ -1197,16 +1197,13 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     if B == 0 or n == 0 or q_heads == 0:
         return 0
     pieces = 0
-    for top in (min(max_shared, 8191), max_shared):
+    for top in (min(max_shared, 8191), max_shared) if groups else ():
         pieces = max(pieces, -(-(top // 32 * 32) // (512 if top < 8192 else 1024)))
-
-    def lined(x):
-        return (x + 127) // 128 * 128
-
+    tails = -(-max_tokens // 256) if max_tokens < 8192 else 32 if max_tokens <= 2**30 else 64
     rows = B * n * q_heads
-    return 128 + lined(4 * B) + lined(16 * groups) + lined(4 * groups) + lined(4 * (groups + 1)) \
-        + lined(8 * rows * pieces) + lined(4 * rows * pieces * head_dim) \
-        + paged_attention_workspace_bytes(B, n, q_heads, kv_heads, head_dim, max_tokens)
+    return 128 + sum((x + 127) // 128 * 128 for x in (
+        4 * B, 4 * (B + 1), 16 * groups, 4 * groups, 4 * (groups + 1), 8 * rows * pieces, 8 * rows * tails,
+        4 * rows * pieces * head_dim, 4 * rows * tails * head_dim))
 
 
 def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_lens, *, new_lens=None, max_shared=None,

@@ -12,6 +12,7 @@
 #include "rlk_rollout.h"
 #include "rlk_device.cuh"
 #include "rlk_host.h"
+#include "rlk_attn.cuh"
 #include "rlk_paged.h"
 #include "rlk_tcgen05.cuh"
 
@@ -183,8 +184,6 @@ struct AttnParams {
   uint32_t group_magic;         // 2^32 / group, rounded up (group 1: 0)
   uint32_t workers;             // CTAs of the main kernel
   int groups;                   // groups of the longest sequence that the table can hold
-  PrefixParts pre;              // first NULL: none
-  int chains;                   // as many as there are groups; four at least with a prefix
 };
 struct AttnMaps {
   CUtensorMap k, v;             // (element, token of the page, head, page), or the head before the token
@@ -209,8 +208,6 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
   Seq s;
   s.ok = seq_lens(P.c, b, s.len, s.nnew);
-  const int first = P.pre.first ? P.pre.first[b] : 0;
-  s.ok &= first >= 0;
   if (!s.ok) s.len = s.nnew = 0;
   s.low = s.us = s.ul = s.nu = 0;
   if (s.ok && s.nnew > 0) {
@@ -218,9 +215,6 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b) {
       s.low = max(0, s.len - s.nnew - P.window + 1);
       s.ul = s.low / UNIT;
       s.us = min(units_of(min(P.sinks, s.len)), s.ul);
-    } else if (first > 0) {              // (no window with parts)
-      s.low = min(first, s.len - 1);
-      s.ul = s.low / UNIT;
     }
     s.nu = s.us + units_of(s.len) - s.ul;
   }
@@ -299,159 +293,12 @@ __device__ __forceinline__ int query_of(const AttnParams& P, int row) {
   return P.group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), P.group_magic)) : row;
 }
 
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// One more part of a row, of maximum m: the factors of what is there and of the
-// part, with the new maximum in M.  A part that saw nothing (its sum is 0, since
-// a part's largest weight is 1) is left out; one whose scores are all NaN has a
-// NaN sum and m = -inf, and stays NaN.
-struct Factors { float a, b; };
-__device__ __forceinline__ Factors fold_factors(float& M, float m) {
-  const float mx = fmaxf(M, m);
-  const Factors f{M == -INFINITY ? 0.0f : ex2f(M - mx), ex2f(m - mx)};
-  M = mx;
-  return f;
-}
-// (b = 0: the part weighs nothing beside what is there, or saw only scores of -inf; its sum
-// comes in all the same, so that values that are not finite are not lost)
-__device__ __forceinline__ float fold(float x, float part, Factors f) { return __fmaf_rn(part, f.b, __fmul_rn(x, f.a)); }
-// The part's maximum and sum into (M, L).
-__device__ __forceinline__ Factors add_part(float& M, float& L, float m, float l) {
-  if (l == 0.0f) return Factors{1.0f, 0.0f};
-  Factors f = fold_factors(M, m);
-  if (l != l) f.b = l;
-  L = fold(L, l, f);
-  return f;
-}
 // Four elements of a fragment: two each of its rows of even and odd number.
 __device__ __forceinline__ void fold4(float4& x, const float4& part, Factors even, Factors odd) {
   x.x = fold(x.x, part.x, even);
   x.y = fold(x.y, part.y, odd);
   x.z = fold(x.z, part.z, even);
   x.w = fold(x.w, part.w, odd);
-}
-template <uint32_t EXP, uint32_t ONE>
-struct OddElem {                         // which of a pair of elements are not finite: bits 15 and 31
-  static __device__ __forceinline__ uint32_t of(uint32_t w) { return ((w & EXP) + ONE) & 0x80008000u; }
-  static __device__ __forceinline__ bool odd(const uint4& w) { return (of(w.x) | of(w.y) | of(w.z) | of(w.w)) != 0; }
-  static __device__ __forceinline__ void clear_odd(uint32_t (&a)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] &= ~((of(a[j]) >> 15) * 0xFFFFu);
-  }
-};
-template <class T> struct Elem;
-template <> struct Elem<__nv_bfloat16> : OddElem<0x7F807F80u, 0x00800080u> {
-  static constexpr float OFF = 0.0f, SLACK = 8.0f;
-  static constexpr uint32_t EXP = 0x7F807F80u;
-  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
-  static constexpr float MORE = 1.0f + 2.384185791015625e-07f;   // 1 + 2^-22
-  // The weights (a, b) >= 0 as the sum of two pairs of elements: hi is cut off, lo
-  // is the rest and 2^-22 of the weight, a bias far below the result's own
-  // rounding.  So both parts of a weight above 0 are above 0, and an infinite value
-  // comes through as itself.
-  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-    hi = __byte_perm(x, y, 0x7632);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(a, MORE, -__uint_as_float(x & 0xFFFF0000u)),
-                                                   __fmaf_rn(b, MORE, -__uint_as_float(y & 0xFFFF0000u)));
-    lo = *reinterpret_cast<const uint32_t*>(&r);
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-  // The values of N fragments times the weights (tokens 0-7 and 8-15: hi, then lo).
-  template <int N>
-  static __device__ __forceinline__ void weigh(float (*o)[4], const uint32_t (&a)[N][4], const uint32_t (&p)[4]) {
-#pragma unroll
-    for (int z = 0; z < N; ++z) mma(o[z], a[z], p[2], p[3]);
-#pragma unroll
-    for (int z = 0; z < N; ++z) mma(o[z], a[z], p[0], p[1]);
-  }
-};
-// f16: a weight's high part in units of 2^-8 of the row's reference, cut off, and the
-// rest of it 2^12 times larger, whose products are scaled back as they join the others'.
-// So a weight has 22 bits, down to 2^-44 of the reference; below that it is rounded to a
-// multiple of it (with one scale for both that would be 2^-32, N 2^-33 of the values of N
-// tokens).  The high part is below 2^15 and its rest below 2^3: both fit.
-template <> struct Elem<__half> : OddElem<0x7C007C00u, 0x04000400u> {
-  static constexpr float OFF = 8.0f, SLACK = 6.0f;
-  static constexpr uint32_t EXP = 0x7C007C00u;
-  static __device__ __forceinline__ float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
-  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16
-  static constexpr float UP = 4096.0f, DOWN = 1.0f / 4096.0f;
-  // The rest of a weight with a high part is never 0 (at most one step of the rest too
-  // much), so that an infinite value comes through as itself.
-  static __device__ __forceinline__ float rest(float a, float h) {
-    const float r = __fmul_rn(__fsub_rn(a, h), UP);
-    return a >= TINY ? fmaxf(r, TINY) : r;
-  }
-  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    const __half2 r = __floats2half2_rn(rest(a, h.x), rest(b, h.y));
-    lo = *reinterpret_cast<const uint32_t*>(&r);
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-  template <int N>
-  static __device__ __forceinline__ void weigh(float (*o)[4], const uint32_t (&a)[N][4], const uint32_t (&p)[4]) {
-    constexpr int M = N > 2 ? 2 : N;     // (all four at once: 0.120 ms for 0.115, 20 rows, 64 sequences of up to 4096 tokens)
-#pragma unroll
-    for (int z0 = 0; z0 < N; z0 += M) {
-      float low[M][4] = {};
-#pragma unroll
-      for (int z = 0; z < M; ++z) mma(low[z], a[z0 + z], p[2], p[3]);
-#pragma unroll
-      for (int z = 0; z < M; ++z) mma(o[z0 + z], a[z0 + z], p[0], p[1]);
-#pragma unroll
-      for (int z = 0; z < M; ++z)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[z0 + z][e] = __fmaf_rn(low[z][e], DOWN, o[z0 + z][e]);
-    }
-  }
-};
-__device__ __forceinline__ void from_float(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_float(float x, __half& y) { y = __float2half_rn(x); }
-
-__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t movm(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// Waits for a phase of a barrier, at most TIMEOUT_NS twice over.
-__device__ __forceinline__ bool mbar_wait_phase(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = global_timer();
-  while (!mbar_try(bar, parity))
-    if (global_timer() - t0 > 2 * TIMEOUT_NS) return false;
-  return true;
 }
 // the four working warps of the tile's rows 8 x .. 8 x + 7
 template <int NT>
@@ -493,13 +340,6 @@ __device__ __forceinline__ bool next_unit(const AttnParams& P, Place& p) {
     }
   }
   return true;
-}
-
-// Where the result of a row goes: out and lse, from the weighted sum o (this
-// lane's share), the sum l and the maximum m (base 2).
-template <class T>
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m + (log2f(l) - Elem<T>::OFF)) * 0.6931471805599453f;
 }
 
 // A copying warp: the slices of its lane, by halves of 16 tokens, each half
@@ -861,7 +701,7 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 
     // ---- where the unit's result goes; on to the next unit, whose queries come meanwhile
     const bool group_ends = cons.li + 1 == cons.s.past(g), store = !folding || group_ends;
-    const bool direct = folding && !P.pre.first && cons.s.past(g) - cons.s.first(g) == cons.s.nu;
+    const bool direct = folding && cons.s.past(g) - cons.s.first(g) == cons.s.nu;
     const int64_t slot = folding ? (static_cast<int64_t>(cons.b) * HT + cons.head * P.tiles + cons.tile) * P.groups + g
                                  : static_cast<int64_t>(me) * (2 * GROUP) + (head_part ? 0 : GROUP) + u % GROUP;
     const int was_b = cons.b, was_head = cons.head, was_row0 = row0, was_nnew = cons.s.nnew;
@@ -976,8 +816,6 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
     fresh_group = group_ends;
     if (!more) break;
   }
-  // behind a prefix's kernel this one may be launched early; the join goes by its end alone
-  if (P.pre.pieces > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   // where a copy did not come in time, the CTA stays for the last ones, within limits
   if (dead) {
 #pragma unroll 1
@@ -996,33 +834,10 @@ constexpr int JB = 4;                    // chains of a block
 // A row of a sequence whose groups are not all in one run: group g goes to
 // chain g mod 16, a chain folds its groups in order, a block its four chains,
 // and the row its four blocks.  By how many rows there are, a chain, a block or
-// a row is a warp's; it is the same tree.  The pieces of a prefix come first in the first four
-// chains, piece mod 4 to a chain.  The join also fills the rows without
+// a row is a warp's; it is the same tree.  The join also fills the rows without
 // a query, and those of rejected sequences.
-template <int D>
-struct JoinRow {
-  static constexpr int E = D / 32;       // elements of a lane
-  float M = -INFINITY, L = 0.0f, o[E] = {};
-  __device__ __forceinline__ void add(float m, float l, const float (&v)[E]) {
-    const Factors f = add_part(M, L, m, l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fold(o[e], v[e], f);
-  }
-  __device__ __forceinline__ void add(const JoinRow& r) { add(r.M, r.L, r.o); }
-};
-template <int E>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
-  if constexpr (E == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(p);
-    v[0] = x.x, v[1] = x.y;
-  }
-}
-
-template <class T, int D, int JR, bool PRE>      // JR: rows that a warp joins at once; PRE: with parts of a prefix
-__global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
+template <class T, int D, int JR>        // JR: rows that a warp joins at once
+__global__ void __launch_bounds__(JW * 32, 3 - JR) join_kernel(const AttnParams P, int tile_rows, int width, int64_t items) {
   constexpr int E = D / 32;
   __shared__ int64_t scan[JW * 32 + 1];
   __shared__ float2 chain_ml[JW][JR];
@@ -1031,7 +846,7 @@ __global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const A
   const int HT = P.c.kv_heads * P.tiles;
   const int blocks = (min(tile_rows, P.rows) + JR - 1) / JR;
 
-  const bool chainwise = P.chains <= width || width == JW;
+  const bool chainwise = P.groups <= width || width == JW;
   const int w0 = warp % width;           // this warp's first chain
   const int64_t total = unit_sums<JW * 32>(P, scan);
   const RunOf runs(static_cast<uint32_t>(total * HT), P.workers);
@@ -1047,7 +862,7 @@ __global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const A
     const Seq s = load_seq(P, b);
     const uint32_t u0 = static_cast<uint32_t>(units_before<JW * 32>(P, scan, b) * HT) + static_cast<uint32_t>(ht) * s.nu;
     const int glast = s.nu > 0 ? s.unit(s.nu - 1) / GROUP : -1;
-    const bool direct = !PRE && s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
+    const bool direct = s.nu > 0 && s.first(glast) == 0 && runs.of(u0) == runs.of(u0 + s.nu - 1);
     const bool work = mine && !(direct && s.nnew == P.c.n);
     if (mine && !s.ok && ht == 0 && r0 == 0 && w0 == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1058,34 +873,9 @@ __global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const A
     const int gl = s.ul / GROUP, gs = (s.us + GROUP - 1) / GROUP;            // groups [0, gs) and [gl, glast]
     JoinRow<D> acc[JR], blk[JR];
     if (work && !direct) {
-      const int chains = chainwise ? 1 : JW / width, pieces = PRE && s.nnew > 0 ? pieces_of(P.pre.first[b]) : 0;
-      const int clast = PRE ? max(glast, min(pieces, JB) - 1) : glast;
-      for (int c = w0 * chains; c < (w0 + 1) * chains && c <= clast; ++c) {     // (chainwise: chain w0)
+      const int chains = chainwise ? 1 : JW / width;
+      for (int c = w0 * chains; c < (w0 + 1) * chains && c <= glast; ++c) {     // (chainwise: chain w0)
         JoinRow<D> chain[JR];
-        if constexpr (PRE) {             // a quarter of the prefix's pieces, several under way at once
-          constexpr int U = 8 / JR;
-          const int row = (ht % P.tiles) * tile_rows + r0;
-          const int64_t from = (static_cast<int64_t>(b) * P.c.kv_heads + ht / P.tiles) * P.rows + row;
-          for (int p0 = c; c < JB && p0 < pieces; p0 += JB * U) {
-            float2 h[U][JR];
-            float v[U][JR][E];
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-#pragma unroll
-              for (int j = 0; j < JR; ++j) {
-                // (past the last piece, or row: one that is there)
-                const int64_t at = (from + (row + j < P.rows ? j : 0)) * P.pre.pieces + (p0 + k * JB < pieces ? p0 + k * JB : p0);
-                h[k][j] = P.pre.ml[at];
-                load_row<E>(P.pre.o + at * D + lane * E, v[k][j]);
-              }
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-              if (p0 + k * JB < pieces) {
-#pragma unroll
-                for (int j = 0; j < JR; ++j) chain[j].add(h[k][j].x, h[k][j].y, v[k][j]);
-              }
-          }
-        }
         for (int g = c; g <= glast; g += JW) {
           if (g >= gs && g < gl) {
             g += (gl - g + JW - 1) / JW * JW;
@@ -1132,7 +922,7 @@ __global__ void __launch_bounds__(JW * 32, PRE ? 1 : 3 - JR) join_kernel(const A
             acc[j] = chain[j];
           } else {
             blk[j].add(chain[j]);
-            if (c % JB == JB - 1 || c == clast) {
+            if (c % JB == JB - 1 || c == glast) {
               acc[j].add(blk[j]);
               blk[j] = JoinRow<D>();
             }
@@ -1335,18 +1125,8 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
     if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, 1, D, bf16)) != RLK_OK) return s;
   }
   P.workers = Shape<D, NT>::WORKERS;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(P.workers);
-  cfg.blockDim = dim3(Shape<D, NT>::THREADS);
-  cfg.dynamicSmemBytes = Shape<D, NT>::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  // (behind a prefix's kernel: on the SMs that it leaves one by one)
-  cfg.numAttrs = P.pre.first && P.pre.pieces > 0 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kernel<T, D, NT>, P, maps);
+  attn_kernel<T, D, NT><<<P.workers, Shape<D, NT>::THREADS, Shape<D, NT>::SMEM, st>>>(P, maps);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   // the join is launched while the units are at work, and waits for them.  A chain to a
   // warp, as far as one round of CTAs (one per SM) has the warps; two rows to a warp, unless
@@ -1356,18 +1136,20 @@ rlk_status launch_attn(AttnParams P, cudaStream_t st) {
   const int tile_rows = NT * 8, rows = tile_rows < P.rows ? tile_rows : P.rows;
   const int64_t entries = P.B * P.c.kv_heads * P.tiles, pairs = entries * ((rows + 1) / 2);
   int width = 1;
-  while (width < JW && width < P.chains) width *= 2;
+  while (width < JW && width < P.groups) width *= 2;
   if (pairs * width > NUM_SMS * JW) width = width > JB && pairs * JB <= NUM_SMS * JW ? JB : 1;
-  const int joins = P.pre.first ? 1 : 2;       // CTAs of a row to a warp that an SM has room for
-  const bool single = width == 1 && entries * rows <= joins * NUM_SMS * JW;
-  const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? joins : 1);
+  const bool single = width == 1 && entries * rows <= 2 * NUM_SMS * JW;
+  const int64_t items = single ? entries * rows : pairs, ctas = (items * width + JW - 1) / JW, most = NUM_SMS * (single ? 2 : 1);
+  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
   cfg.blockDim = dim3(JW * 32);
-  cfg.dynamicSmemBytes = 0;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto* const join = P.pre.first ? (single ? join_kernel<T, D, 1, true> : join_kernel<T, D, 2, true>)
-                                 : (single ? join_kernel<T, D, 1, false> : join_kernel<T, D, 2, false>);
-  e = cudaLaunchKernelEx(&cfg, join, P, tile_rows, width, items);
+  e = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1> : join_kernel<T, D, 2>, P, tile_rows, width, items);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
@@ -1379,66 +1161,6 @@ rlk_status launch_rows(const AttnParams& P, int nt, cudaStream_t st) {
     case 3: return launch_attn<T, D, 3>(P, st);
     default: return launch_attn<T, D, 4>(P, st);
   }
-}
-
-rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides, int32_t q_heads,
-                           float scale, int32_t window, int32_t sinks, void* out, const rlk_bth_strides* out_strides,
-                           float* out_lse, void* workspace, const PrefixParts* parts, void* stream) {
-  rlk_status s = check_cache(cache);
-  if (s != RLK_OK) return s;
-  if (q_heads < 1 || q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads)
-    return fail(RLK_EINVAL, "q_heads %d must be 1 to 128 times kv_heads %d", q_heads, cache->kv_heads);
-  if (!isfinite(scale)) return fail(RLK_EINVAL, "scale %g must be finite", (double)scale);
-  if (window < 0 || sinks < 0) return fail(RLK_EINVAL, "window %d and sinks %d must be >= 0", window, sinks);
-  if (cache->B == 0 || cache->n == 0) return RLK_OK;
-  if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
-  if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
-  if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
-  if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
-  const int group = q_heads / cache->kv_heads;
-  const Tiling t = tiling_of(cache->n, group);
-  const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
-  if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
-    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
-  const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
-                             static_cast<int64_t>(cache->max_pages) * cache->page_size);
-  if (!workspace && y.bytes > 0) return fail(RLK_EINVAL, "workspace is NULL");
-  char* ws = static_cast<char*>(workspace);
-  AttnParams P{};
-  P.c = paged_params(cache);
-  P.q = q;
-  P.out = out;
-  P.qs = *q_strides;
-  P.os = *out_strides;
-  P.q_heads = q_heads;
-  P.group = group;
-  P.rows = t.rows;
-  P.tiles = t.tiles;
-  P.B = cache->B;
-  P.c2 = fabsf(scale) * 1.4426950408889634f;
-  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
-  P.window = window;
-  P.sinks = window > 0 ? sinks : 0;
-  P.lse = out_lse;
-  P.chains = static_cast<int>(y.groups);
-  if (parts) {
-    P.pre = *parts;
-    if (P.chains < JB) P.chains = JB;
-  }
-  P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
-  P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
-  P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
-  P.group_o = reinterpret_cast<float*>(ws + y.group_o);
-  P.page_magic = page_magic(cache->page_size);
-  P.groups = static_cast<int>(y.groups);
-  P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
-  P.box = box_of(cache->page_size, HALF);
-  P.head_first = heads_first(cache);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = cache->dtype == RLK_DT_BF16;
-  if (cache->head_dim == 128)
-    return bf ? launch_rows<__nv_bfloat16, 128>(P, t.nt, st) : launch_rows<__half, 128>(P, t.nt, st);
-  return bf ? launch_rows<__nv_bfloat16, 64>(P, t.nt, st) : launch_rows<__half, 64>(P, t.nt, st);
 }
 
 }  // namespace rlk
@@ -1485,7 +1207,56 @@ rlk_status rlk_paged_attention(const rlk_kv_cache* cache, const void* q, const r
                                int32_t q_heads, float scale, int32_t window, int32_t sinks, void* out,
                                const rlk_bth_strides* out_strides, float* out_lse, void* workspace,
                                void* stream) {
-  return paged_attention(cache, q, q_strides, q_heads, scale, window, sinks, out, out_strides, out_lse, workspace, nullptr, stream);
+  rlk_status s = check_cache(cache);
+  if (s != RLK_OK) return s;
+  if (q_heads < 1 || q_heads % cache->kv_heads || q_heads > 128 * cache->kv_heads)
+    return fail(RLK_EINVAL, "q_heads %d must be 1 to 128 times kv_heads %d", q_heads, cache->kv_heads);
+  if (!isfinite(scale)) return fail(RLK_EINVAL, "scale %g must be finite", (double)scale);
+  if (window < 0 || sinks < 0) return fail(RLK_EINVAL, "window %d and sinks %d must be >= 0", window, sinks);
+  if (cache->B == 0 || cache->n == 0) return RLK_OK;
+  if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
+  if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
+  if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
+  if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
+  const int group = q_heads / cache->kv_heads;
+  const Tiling t = tiling_of(cache->n, group);
+  const int64_t max_units = (static_cast<int64_t>(cache->max_pages) * cache->page_size + UNIT - 1) / UNIT;
+  if (static_cast<double>(cache->B) * cache->kv_heads * t.tiles * max_units >= 2147483648.0)
+    return fail(RLK_EINVAL, "too many tokens for one call: B * kv_heads * row tiles * max_pages * page_size / 512 must be below 2^31");
+  const Layout y = layout_of(cache->B, cache->n, cache->kv_heads, group, cache->head_dim,
+                             static_cast<int64_t>(cache->max_pages) * cache->page_size);
+  if (!workspace && y.bytes > 0) return fail(RLK_EINVAL, "workspace is NULL");
+  char* ws = static_cast<char*>(workspace);
+  AttnParams P{};
+  P.c = paged_params(cache);
+  P.q = q;
+  P.out = out;
+  P.qs = *q_strides;
+  P.os = *out_strides;
+  P.q_heads = q_heads;
+  P.group = group;
+  P.rows = t.rows;
+  P.tiles = t.tiles;
+  P.B = cache->B;
+  P.c2 = fabsf(scale) * 1.4426950408889634f;
+  P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+  P.window = window;
+  P.sinks = window > 0 ? sinks : 0;
+  P.lse = out_lse;
+  P.unit_ml = reinterpret_cast<float2*>(ws + y.unit_ml);
+  P.unit_o = reinterpret_cast<float*>(ws + y.unit_o);
+  P.group_ml = reinterpret_cast<float2*>(ws + y.group_ml);
+  P.group_o = reinterpret_cast<float*>(ws + y.group_o);
+  P.page_magic = page_magic(cache->page_size);
+  P.groups = static_cast<int>(y.groups);
+  P.group_magic = static_cast<uint32_t>(group == 1 ? 0 : ((1ull << 32) + group - 1) / group);
+  P.box = box_of(cache->page_size, HALF);
+  P.head_first = heads_first(cache);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == RLK_DT_BF16;
+  if (cache->head_dim == 128)
+    return bf ? launch_rows<__nv_bfloat16, 128>(P, t.nt, st) : launch_rows<__half, 128>(P, t.nt, st);
+  return bf ? launch_rows<__nv_bfloat16, 64>(P, t.nt, st) : launch_rows<__half, 64>(P, t.nt, st);
 }
 
 }  // extern "C"

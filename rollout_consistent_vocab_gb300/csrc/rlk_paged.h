@@ -60,27 +60,52 @@ inline bool heads_first(const rlk_kv_cache* c) {
 // behind the first 64 (a fifth place).
 rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box, bool head_first, int panels, int D, bool bf16);
 
-// Attention over the first tokens of each sequence, done before: what paged attention
-// over the rest joins to its own.
-struct PrefixParts {
-  const int32_t* first;         // [B] tokens that the parts cover, a multiple of 32; -1: the sequence is rejected
-  const float2* ml;             // [B][kv_heads][n * group][pieces]: maximum (base 2), sum
-  const float* o;               // ... and the weighted sum of values [head_dim]
-  int pieces;                   // at most, of a sequence; 0: no kernel for them was launched
-};
-// Tokens of a part.  By the covered length alone, so that a sequence's result does not
-// depend on its batch: more parts where there are few tokens (one to an SM), fewer
-// where there are many (the parts' results are a read and a write of 128 tokens' size for 128 rows).
-__host__ __device__ __forceinline__ int piece_tokens(int covered) { return covered < 8192 ? 512 : 1024; }
-__host__ __device__ __forceinline__ int pieces_of(int covered) {
-  const int t = piece_tokens(covered);
-  return covered / t + (covered % t != 0);
+// Attention over a shared prefix is taken in parts: of the shared tokens, that a group's
+// queries go over together, and of each sequence's other ones.  How they are cut goes by a
+// sequence's own lengths alone, so that its result does not depend on its batch.
+//
+// Tokens of a part of the shared ones: more parts where there are few tokens (one to an
+// SM), fewer where there are many (the parts' results are a read and a write of 128 tokens'
+// size for 128 rows).
+__host__ __device__ __forceinline__ int piece_tokens(int shared) { return shared < 8192 ? 512 : 1024; }
+__host__ __device__ __forceinline__ int pieces_of(int shared) {
+  const int t = piece_tokens(shared);
+  return shared / t + (shared % t != 0);
 }
+// Tokens of a part of a sequence's other ones, at most TAIL_PARTS parts (from 2^30 tokens on, 2 TAIL_PARTS).
+constexpr int TAIL_PARTS = 32;
+__host__ __device__ __forceinline__ int tail_tokens(int tokens) {
+  int t = 256;
+  while (t < (1 << 25) && tokens > TAIL_PARTS * t) t *= 2;
+  return t;
+}
+// What both kernels and the join go by.
+struct PrefixParts {
+  PagedParams c;
+  const void* q;
+  void* out;
+  rlk_bth_strides qs, os;       // elements
+  int64_t B;
+  int q_heads, group;           // group: query heads of a kv head
+  int rows;                     // n * group: of a sequence and kv head
+  float c2;                     // |scale| * log2(e)
+  uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
+  uint32_t page_magic;
+  bool head_first;              // the tensor maps' second place is the head, not the token
+  float* lse;
+  const int32_t* first;         // [B] tokens of the sequence that are taken as shared, a multiple of 32; -1: rejected
+  const uint32_t* tail_base;    // [B + 1] steps of 16 other tokens (of a kv head) before each sequence
+  float2* piece_ml;             // [B][kv_heads][rows][pieces]: maximum (base 2), sum
+  float* piece_o;               // ... and the weighted sum of values [head_dim]
+  int pieces;                   // at most, of a sequence
+  float2* tail_ml;              // [B][kv_heads][rows][tails]
+  float* tail_o;
+  int tails;
+};
 
-// rlk_paged_attention, without the tokens that `parts` (NULL: none) covers.
-rlk_status paged_attention(const rlk_kv_cache* cache, const void* q, const rlk_bth_strides* q_strides, int32_t q_heads,
-                           float scale, int32_t window, int32_t sinks, void* out, const rlk_bth_strides* out_strides,
-                           float* out_lse, void* workspace, const PrefixParts* parts, void* stream);
+// The sequences' other tokens, and the join of all parts; the launches follow the shared tokens'
+// kernel, or where there is none (`alone`) the plan's.
+rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool alone, cudaStream_t stream);
 
 rlk_status check_cache(const rlk_kv_cache* c);
 rlk_status check_bth(const void* p, const rlk_bth_strides* s, const char* what);

@@ -3,8 +3,8 @@
 //
 // plan_kernel looks the groups and lengths over.  The shared tokens of a group, rounded
 // down to 32, go in pieces of a length that depends on theirs alone; a piece's result
-// (maximum, sum, weighted sum of values of each query row) goes to the workspace.  Then
-// paged attention takes every sequence's other tokens, and its join adds the pieces first.
+// (maximum, sum, weighted sum of values of each query row) goes to the workspace.  Every
+// sequence's other tokens, and the join of all, are a kernel each of rlk_tail.cu.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -27,29 +27,17 @@ constexpr int PREFIX_STEP = 32;          // shared tokens come in multiples of t
 // their pieces (0: nothing to do).
 struct alignas(16) GroupPlan { int seq0, seqs, shared, pieces; };
 
-struct PrefixParams {
-  PagedParams c;
+struct PrefixParams : PrefixParts {
   const int32_t* group_start;
   const int32_t* shared_lens;
   int groups, max_shared;
-  int64_t B;
-  int32_t* first;               // [B], as in PrefixParts
+  int32_t* plan_first;          // as in PrefixParts, for the plan to write
+  uint32_t* plan_tails;
   GroupPlan* plan;              // [groups]
   int32_t* busy;                // [groups] whether a sequence has new tokens
   uint32_t* base;               // [groups + 1] units of work before each group
-  const void* q;
-  rlk_bth_strides qs;
-  int q_heads, group;           // group: query heads of a kv head
-  int rows;                     // n * group: of a sequence and kv head
-  int max_pieces;
-  float c2;                     // |scale| * log2(e)
-  uint32_t q_sign;              // 0x80008000: the queries change sign (scale < 0)
   int box;                      // tokens of a copy: the largest power of 2, up to 64, that divides page_size
   bool merged;                  // a copy takes all 128 elements of its tokens (64 of them)
-  bool head_first;
-  uint32_t page_magic;
-  float2* ml;
-  float* o;
 };
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -70,10 +58,35 @@ __device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const G
 
 constexpr int PLAN_THREADS = 1024, PLAN_GROUPS = 2048;         // groups that are kept in shared memory
 
+// The sum of the values of the threads before this one; the whole CTA.
+__device__ __forceinline__ uint32_t sum_before(uint32_t mine, uint32_t* scan) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += x;
+  }
+  __syncthreads();
+  if (lane == 31) scan[warp] = run;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t sum = scan[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    scan[lane] = sum;
+  }
+  __syncthreads();
+  return run - mine + (warp > 0 ? scan[warp - 1] : 0u);
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P) {
   __shared__ int32_t near_start[PLAN_GROUPS + 1], near_shared[PLAN_GROUPS], near_busy[PLAN_GROUPS];
   __shared__ uint32_t scan[PLAN_THREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, G = P.groups;
+  const int tid = threadIdx.x, G = P.groups;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t tokens = static_cast<int64_t>(P.c.max_pages) * P.c.page_size;
   const bool near = G <= PLAN_GROUPS;
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
         }
       }
     }
-    P.first[b] = first;
+    P.plan_first[b] = first;
   }
   __syncthreads();
   const int per = (G + PLAN_THREADS - 1) / PLAN_THREADS, g0 = min(G, tid * per), g1 = min(G, g0 + per);
@@ -128,30 +141,28 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
     P.plan[g] = p;
     mine += units_of_head(P, p) * P.c.kv_heads;
   }
-  uint32_t run = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += x;
-  }
-  if (lane == 31) scan[tid / 32] = run;
-  __syncthreads();
-  if (tid < 32) {
-    uint32_t sum = scan[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += x;
-    }
-    scan[lane] = sum;
-  }
-  __syncthreads();
-  run += (tid >= 32 ? scan[tid / 32 - 1] : 0u) - mine;
+  uint32_t run = sum_before(mine, scan);
   for (int g = g0; g < g1; ++g) {
     P.base[g] = run;
     run += units_of_head(P, P.plan[g]) * P.c.kv_heads;
   }
   if (tid == PLAN_THREADS - 1) P.base[G] = run;
+  // the steps of 16 tokens that the sequences have behind the shared ones
+  const int seqs = static_cast<int>((P.B + PLAN_THREADS - 1) / PLAN_THREADS);
+  const int b0 = static_cast<int>(min(P.B, static_cast<int64_t>(tid) * seqs)), b1 = static_cast<int>(min(P.B, static_cast<int64_t>(b0) + seqs));
+  auto steps = [&](int b) {
+    const int first = P.plan_first[b];
+    int len, nnew;
+    return first >= 0 && seq_lens(P.c, b, len, nnew) && nnew > 0 && len > first ? static_cast<uint32_t>((len - first + 15) / 16) : 0u;
+  };
+  mine = 0;
+  for (int b = b0; b < b1; ++b) mine += steps(b);
+  run = sum_before(mine, scan);
+  for (int b = b0; b < b1; ++b) {
+    P.plan_tails[b] = run;
+    run += steps(b);
+  }
+  if (tid == PLAN_THREADS - 1) P.plan_tails[P.B] = run;
 }
 
 // ------------------------------------------------------------ the shared tokens
@@ -665,7 +676,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
       if (k < x.seqs) {
         const int nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
         if (P.first[b] >= 0 && i < nnew) {
-          out = ((static_cast<int64_t>(b) * P.c.kv_heads + x.head) * P.rows + r) * P.max_pieces;
+          out = ((static_cast<int64_t>(b) * P.c.kv_heads + x.head) * P.rows + r) * P.pieces;
           src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + b * P.qs.batch + i * P.qs.token +
                                                (x.head * P.group + (r - i * P.group)) * P.qs.head);
         }
@@ -802,11 +813,11 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
               for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * W::TO_PIECES);
             }
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) store8(P.o + slot_at * D + 32 * c + e, y + e);
+            for (int e = 0; e < 32; e += 8) store8(P.piece_o + slot_at * D + 32 * c + e, y + e);
           }
           __syncwarp();
         }
-        if (query) P.ml[slot_at] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
+        if (query) P.piece_ml[slot_at] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
       }
       have = more;
     }
@@ -819,11 +830,6 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
 
 // ------------------------------------------------------------ host side
 
-// The workspace, in this order; each part on a line of its own.
-struct PrefixLayout {
-  size_t first, plan, busy, base, ml, o, rest, bytes;
-  int pieces;
-};
 template <class T, int D>
 static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cudaStream_t st) {
   static bool done[64] = {};
@@ -856,22 +862,39 @@ static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cuda
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;
 }
+
 static size_t lined(size_t x) { return (x + 127) / 128 * 128; }
-static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t head_dim, int groups, int max_shared, size_t rest) {
+
+// The workspace, in this order; each part on a line of its own.
+struct PrefixLayout {
+  size_t first, tails_at, plan, busy, base, piece_ml, tail_ml, piece_o, tail_o, bytes;
+  int pieces, tails;
+};
+static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t head_dim, int64_t max_tokens, int groups, int max_shared) {
   PrefixLayout y{};
   for (const int top : {max_shared < 8191 ? max_shared : 8191, max_shared}) {
     const int pieces = pieces_of(top / PREFIX_STEP * PREFIX_STEP);
     y.pieces = pieces > y.pieces ? pieces : y.pieces;
   }
-  const size_t slots = static_cast<size_t>(B) * n * q_heads * y.pieces;
-  y.first = 0;
-  y.plan = y.first + lined(static_cast<size_t>(B) * 4);
-  y.busy = y.plan + lined(static_cast<size_t>(groups) * sizeof(GroupPlan));
-  y.base = y.busy + lined(static_cast<size_t>(groups) * 4);
-  y.ml = y.base + lined(static_cast<size_t>(groups + 1) * 4);
-  y.o = y.ml + lined(slots * 8);
-  y.rest = y.o + lined(slots * head_dim * 4);
-  y.bytes = y.rest + rest + 128;         // (the caller's memory may begin between two lines)
+  if (groups == 0) y.pieces = 0;
+  y.tails = static_cast<int>(max_tokens >= TAIL_PARTS * 256 ? max_tokens > (int64_t(1) << 30) ? 2 * TAIL_PARTS : TAIL_PARTS : (max_tokens + 255) / 256);
+  const size_t rows = static_cast<size_t>(B) * n * q_heads, pieces = rows * y.pieces, tails = rows * y.tails;
+  size_t at = 0;
+  auto next = [&](size_t bytes) {
+    const size_t here = at;
+    at += lined(bytes);
+    return here;
+  };
+  y.first = next(static_cast<size_t>(B) * 4);
+  y.tails_at = next(static_cast<size_t>(B + 1) * 4);
+  y.plan = next(static_cast<size_t>(groups) * sizeof(GroupPlan));
+  y.busy = next(static_cast<size_t>(groups) * 4);
+  y.base = next(static_cast<size_t>(groups + 1) * 4);
+  y.piece_ml = next(pieces * 8);
+  y.tail_ml = next(tails * 8);
+  y.piece_o = next(pieces * head_dim * 4);
+  y.tail_o = next(tails * head_dim * 4);
+  y.bytes = at + 128;                    // (the caller's memory may begin between two lines)
   return y;
 }
 
@@ -883,13 +906,13 @@ extern "C" {
 
 rlk_status rlk_prefix_attention_workspace(int64_t B, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                           int64_t max_tokens, int32_t groups, int32_t max_shared, size_t* bytes) {
-  size_t rest = 0;
-  const rlk_status s = rlk_paged_attention_workspace(B, n, q_heads, kv_heads, head_dim, max_tokens, bytes ? &rest : nullptr);
-  if (s != RLK_OK) return s;
+  if (B < 0 || n < 0 || q_heads < 0 || head_dim < 0 || max_tokens < 0) return fail(RLK_EINVAL, "a size is negative");
+  if (!bytes) return fail(RLK_EINVAL, "bytes is NULL");
+  if (kv_heads < 1 || q_heads % kv_heads) return fail(RLK_EINVAL, "q_heads %d must be a multiple of kv_heads %d", q_heads, kv_heads);
   if (groups < 0 || groups >= (1 << 16)) return fail(RLK_EINVAL, "groups %d must be in 0..65535", groups);
   if (max_shared < 0 || max_shared > max_tokens)
     return fail(RLK_EINVAL, "max_shared %d must be in 0..%lld", max_shared, (long long)max_tokens);
-  *bytes = B == 0 || n == 0 || q_heads == 0 ? 0 : prefix_layout(B, n, q_heads, head_dim, groups, max_shared, rest).bytes;
+  *bytes = B == 0 || n == 0 || q_heads == 0 ? 0 : prefix_layout(B, n, q_heads, head_dim, max_tokens, groups, max_shared).bytes;
   return RLK_OK;
 }
 
@@ -903,7 +926,7 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
     return fail(RLK_EINVAL, "q_heads %d must be 1 to 128 times kv_heads %d", q_heads, cache->kv_heads);
   if (!isfinite(scale)) return fail(RLK_EINVAL, "scale %g must be finite", (double)scale);
   const int64_t tokens = static_cast<int64_t>(cache->max_pages) * cache->page_size;
-  size_t rest = 0, bytes = 0;
+  size_t bytes = 0;
   if ((s = rlk_prefix_attention_workspace(cache->B, cache->n, q_heads, cache->kv_heads, cache->head_dim, tokens, groups->groups,
                                           groups->max_shared, &bytes)) != RLK_OK)
     return s;
@@ -913,15 +936,15 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   if (groups->groups > 0 && (!groups->group_start || !groups->shared_lens))
     return fail(RLK_EINVAL, "group_start or shared_lens is NULL");
   const double rows = static_cast<double>(cache->B) * cache->n * (q_heads / cache->kv_heads);
-  if (rows >= 2147483392.0 || (rows / 256 + groups->groups) * cache->kv_heads * (groups->max_shared / 512 + 1.0) >= 2147483648.0)
-    return fail(RLK_EINVAL, "too many query rows and shared tokens for one call");
+  if (rows >= 2147483392.0 || (rows / 128 + groups->groups) * cache->kv_heads * (groups->max_shared / 512 + 2.0) >= 2147483648.0 ||
+      static_cast<double>(cache->B) * (tokens / 16 + 1.0) >= 2147483648.0)
+    return fail(RLK_EINVAL, "too many query rows or tokens for one call");
   if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;
   if ((s = check_bth(out, out_strides, "out")) != RLK_OK) return s;
   if ((s = check_out(out_lse, "out_lse", false)) != RLK_OK) return s;
   if (!workspace) return fail(RLK_EINVAL, "workspace is NULL");
   if (!aligned(workspace, 16)) return fail(RLK_EALIGN, "workspace is not 16-byte aligned");
-  rlk_paged_attention_workspace(cache->B, cache->n, q_heads, cache->kv_heads, cache->head_dim, tokens, &rest);
-  const PrefixLayout y = prefix_layout(cache->B, cache->n, q_heads, cache->head_dim, groups->groups, groups->max_shared, rest);
+  const PrefixLayout y = prefix_layout(cache->B, cache->n, q_heads, cache->head_dim, tokens, groups->groups, groups->max_shared);
   char* ws = reinterpret_cast<char*>(lined(reinterpret_cast<size_t>(workspace)));
   PrefixParams P{};
   P.c = paged_params(cache);
@@ -930,18 +953,27 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.groups = groups->groups;
   P.max_shared = groups->max_shared;
   P.B = cache->B;
-  P.first = reinterpret_cast<int32_t*>(ws + y.first);
+  P.plan_first = reinterpret_cast<int32_t*>(ws + y.first);
+  P.plan_tails = reinterpret_cast<uint32_t*>(ws + y.tails_at);
+  P.first = P.plan_first;
+  P.tail_base = P.plan_tails;
   P.plan = reinterpret_cast<GroupPlan*>(ws + y.plan);
   P.busy = reinterpret_cast<int32_t*>(ws + y.busy);
   P.base = reinterpret_cast<uint32_t*>(ws + y.base);
-  P.ml = reinterpret_cast<float2*>(ws + y.ml);
-  P.o = reinterpret_cast<float*>(ws + y.o);
+  P.piece_ml = reinterpret_cast<float2*>(ws + y.piece_ml);
+  P.piece_o = reinterpret_cast<float*>(ws + y.piece_o);
+  P.tail_ml = reinterpret_cast<float2*>(ws + y.tail_ml);
+  P.tail_o = reinterpret_cast<float*>(ws + y.tail_o);
+  P.pieces = y.pieces;
+  P.tails = y.tails;
   P.q = q;
   P.qs = *q_strides;
+  P.out = out;
+  P.os = *out_strides;
+  P.lse = out_lse;
   P.q_heads = q_heads;
   P.group = q_heads / cache->kv_heads;
   P.rows = cache->n * P.group;
-  P.max_pieces = y.pieces;
   P.c2 = fabsf(scale) * 1.4426950408889634f;
   P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
   P.box = box_of(cache->page_size, PTILE / 2);
@@ -949,21 +981,16 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.head_first = heads_first(cache);
   P.page_magic = page_magic(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == RLK_DT_BF16;
   plan_kernel<<<1, PLAN_THREADS, 0, st>>>(P);
-  const bool any = y.pieces > 0 && groups->groups > 0;
-  if (any) {
-    const bool bf = cache->dtype == RLK_DT_BF16;
-    if (cache->head_dim == 128) {
-      s = bf ? launch_prefix<bf16_t, 128>(P, cache, st) : launch_prefix<__half, 128>(P, cache, st);
-    } else {
-      s = bf ? launch_prefix<bf16_t, 64>(P, cache, st) : launch_prefix<__half, 64>(P, cache, st);
-    }
-    if (s != RLK_OK) return s;
-  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  const PrefixParts parts{P.first, P.ml, P.o, any ? y.pieces : 0};
-  return paged_attention(cache, q, q_strides, q_heads, scale, 0, 0, out, out_strides, out_lse, ws + y.rest, &parts, stream);
+  if (y.pieces > 0) {
+    if (cache->head_dim == 128) s = bf ? launch_prefix<bf16_t, 128>(P, cache, st) : launch_prefix<__half, 128>(P, cache, st);
+    else s = bf ? launch_prefix<bf16_t, 64>(P, cache, st) : launch_prefix<__half, 64>(P, cache, st);
+    if (s != RLK_OK) return s;
+  }
+  return attend_tails(P, cache->head_dim, bf, y.pieces == 0, st);
 }
 
 }  // extern "C"

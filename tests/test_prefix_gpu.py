@@ -242,18 +242,30 @@ def test_drafted_tokens_have_the_bits_of_single_ones():
         assert torch.equal(bits(o[:, 0]), bits(out[:, i])) and torch.equal(bits(z[:, 0]), bits(lse[:, i]))
 
 
-def test_without_a_prefix_the_bits_are_paged_attentions():
-    c = make([(2, 31), (3, 0), (2, 640)], [600, 1, 5000, 3, 9, 2, 2, 77, 1234], 2, 8, 2, 128, 16, "bf16", seed=16, before=1)
+def test_a_sequence_in_no_group():
+    c = make([(2, 31), (3, 0), (2, 640)], [600, 1, 5000, 3, 9, 2, 2, 77, 9234], 2, 8, 2, 128, 16, "bf16", seed=16, before=1)
     new = [2, 1, 2, 2, 2, 2, 2, 2, 2]
     out, lse = run(c, new)
-    o, z = pkg.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], new_lens=i32(new))
-    for b in (0, 1, 2, 3, 4, 5, 8):
-        assert torch.equal(bits(o[b]), bits(out[b])) and torch.equal(bits(z[b]), bits(lse[b])), b
     compare(c, out, lse, new)
-    # no groups at all, and groups that share nothing a call knows of
+    # without any groups: the bits of those that share nothing a call knows of
     d = dict(c, start=i32([0]), shared=i32([]))
     p, y = run(d, new)
-    assert torch.equal(bits(p), bits(o)) and torch.equal(bits(y), bits(z))
+    compare(c, p, y, new)
+    for b in (0, 1, 2, 3, 4, 5, 8):
+        assert torch.equal(bits(p[b]), bits(out[b])) and torch.equal(bits(y[b]), bits(lse[b])), b
+    # alone, in a wider table
+    wide = torch.full((1, c["table"].shape[1] + 300), -7, dtype=torch.int32, device=DEV)
+    wide[:, :c["table"].shape[1]] = c["table"][8:]
+    p, y = run(dict(c, q=c["q"][8:], table=wide, lens=c["lens"][8:], start=i32([0]), shared=i32([])))
+    assert torch.equal(bits(p[0]), bits(out[8])) and torch.equal(bits(y[0]), bits(lse[8]))
+
+
+@pytest.mark.parametrize("dtype,dim,n", [("bf16", 128, 1), ("f16", 64, 3), ("bf16", 64, 9), ("f16", 128, 5)])
+def test_long_tails(dtype, dim, n):
+    """Parts of more than 256 tokens, one of them with a single token."""
+    c = make([(2, 64)], [8193 + 256, 4096, 16385 - 64, 300], n, 4, 2, dim, 24, dtype, seed=27)
+    out, lse = run(c)
+    compare(c, out, lse, [n] * 4)
 
 
 # ------------------------------------------------------------ what is not finite, what is rejected
