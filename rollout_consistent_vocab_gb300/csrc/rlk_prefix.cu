@@ -215,16 +215,15 @@ template <> struct Weights<bf16_t> {
 template <> struct Weights<__half> {
   static constexpr uint32_t FORMAT = 0;
   static constexpr float OFF = 13.0f, SLACK = 2.0f, TO_PIECES = 1.0f / 32.0f;
-  static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16
-  static __device__ __forceinline__ float rest(float a, float h) {
-    const float r = __fsub_rn(a, h);
-    return a >= TINY ? fmaxf(r, TINY) : r;
-  }
+  // The rest of a weight with a high part is never 0 (at most one step of 2^-24 too much), so that an
+  // infinite value comes through as itself; the words of numbers >= 0 are in their order.
   static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
     const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    const __half2 r = __floats2half2_rn(rest(a, h.x), rest(b, h.y));
-    lo = *reinterpret_cast<const uint32_t*>(&r);
+    float c, d;
+    unpack2(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), pack2(a, b)), c, d);
+    const __half2 r = __floats2half2_rn(c, d);
+    lo = __vmaxu2(*reinterpret_cast<const uint32_t*>(&r), __vminu2(hi, 0x00010001u));
   }
 };
 
@@ -279,6 +278,9 @@ struct Way {
   GroupPlan pl;
   __device__ __forceinline__ void load(const PrefixParams& P) {
     pl = P.plan[g];
+    size_up(P);
+  }
+  __device__ __forceinline__ void size_up(const PrefixParams& P) {
     rows = pl.seqs * P.rows;
     rbs = (rows + PROWS - 1) / PROWS;
     size = piece_tokens(pl.shared);
@@ -308,12 +310,31 @@ struct Way {
       if (pl.pieces == 0) find(P);
     }
   }
-  __device__ __forceinline__ void begin(const PrefixParams& P, uint32_t a, uint32_t e) {
-    at = a, end = e, g = 0;
-    if (a >= e) return;
-    find(P);
+  // The CTA's run, of equal ones; the whole warp.
+  __device__ __forceinline__ void begin(const PrefixParams& P) {
+    const int lane = threadIdx.x & 31, G = P.groups;
+    g = 0;
+    const bool few = G < 32;             // all of them are looked at at once
+    uint32_t before = ~0u;
+    GroupPlan mine{0, 0, 0, 0};
+    if (few && lane <= G) before = P.base[lane];
+    if (few && lane < G) mine = P.plan[lane];
+    const uint32_t units = few ? __shfl_sync(0xffffffffu, before, G) : P.base[G];
+    const uint32_t workers = max(1u, min(units, gridDim.x)), me = min(blockIdx.x, workers);
+    at = run_start(units, workers, me), end = run_start(units, workers, min(me + 1, workers));
+    if (at >= end) return;               // (a CTA without items goes through with an empty run)
+    uint32_t rest = at;
+    if (few) {
+      g = 31 - __clz(__ballot_sync(0xffffffffu, lane < G && before <= at));
+      pl = GroupPlan{__shfl_sync(0xffffffffu, mine.seq0, g), __shfl_sync(0xffffffffu, mine.seqs, g),
+                     __shfl_sync(0xffffffffu, mine.shared, g), __shfl_sync(0xffffffffu, mine.pieces, g)};
+      rest -= __shfl_sync(0xffffffffu, before, g);
+      size_up(P);
+    } else {
+      find(P);
+      rest -= P.base[g];
+    }
     const uint32_t whole = units_of_head(P, pl), block = 2u * pl.pieces * (size / PIECE_UNIT);
-    uint32_t rest = a - P.base[g];
     head = static_cast<int>(rest / whole);
     rest -= head * whole;
     rb = static_cast<int>(min(rest / block, static_cast<uint32_t>(rbs - 1)));
@@ -473,9 +494,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
   auto begin = [&]() {                   // the plan is made
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // (a CTA without items goes through with an empty run)
-    const uint32_t units = P.base[P.groups], workers = max(1u, min(units, gridDim.x)), me = min(blockIdx.x, workers);
-    way.begin(P, run_start(units, workers, me), run_start(units, workers, min(me + 1, workers)));
+    way.begin(P);
   };
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_try(bar, parity & 1)) return true;
