@@ -1057,13 +1057,14 @@ def _rope_function():
     torch = _torch()
 
     class _Rope(torch.autograd.Function):
-        """rope, differentiable with respect to x: the backward is the same kernel, turning back."""
+        """rope, differentiable with respect to x: the backward is the same kernel, turning the other
+        way, and differentiable again."""
 
         @staticmethod
-        def forward(ctx, x, inv_freq, positions, pair_axis, interleaved):
+        def forward(ctx, x, inv_freq, positions, pair_axis, interleaved, inverse):
             ctx.save_for_backward(inv_freq, positions, pair_axis)
-            ctx.interleaved = interleaved
-            return rope(x, inv_freq, positions, pair_axis=pair_axis, interleaved=interleaved)
+            ctx.interleaved, ctx.inverse = interleaved, inverse
+            return rope(x, inv_freq, positions, pair_axis=pair_axis, interleaved=interleaved, inverse=inverse)
 
         @staticmethod
         def backward(ctx, grad):
@@ -1072,8 +1073,8 @@ def _rope_function():
             size, strides = grad.element_size(), zip(grad.stride()[:-1], grad.shape)
             if grad.stride(-1) != 1 or grad.data_ptr() % 16 or any(s * size % 16 for s, m in strides if m > 1):
                 grad = grad.clone(memory_format=torch.contiguous_format)
-            grad = rope(grad, inv_freq, positions, pair_axis=pair_axis, interleaved=ctx.interleaved, inverse=True)
-            return grad, None, None, None, None
+            grad = _Rope.apply(grad, inv_freq, positions, pair_axis, ctx.interleaved, not ctx.inverse)
+            return grad, None, None, None, None, None
 
     return _Rope
 
@@ -1082,11 +1083,22 @@ _ROPE_FN = None
 
 
 def rope_autograd(x, inv_freq, positions, *, pair_axis=None, interleaved=False):
-    """rope as a differentiable torch output."""
+    """rope as a differentiable torch output.  Not to be captured into a graph while a backward
+    graph of the same leaf x, made on another stream, lives: refused (RuntimeError) where that one
+    came from here too."""
     global _ROPE_FN
+    torch = _torch()
     if _ROPE_FN is None:
         _ROPE_FN = _rope_function()
-    return _ROPE_FN.apply(x, inv_freq, positions, pair_axis, interleaved)
+    node = None
+    if x.is_leaf and x.requires_grad and x.is_cuda and torch.is_grad_enabled():
+        # torch adds a leaf's gradient up on the stream that its first graph was made on, while any lives,
+        # and a capture that has to wait for another stream's work ends the process.
+        node = torch.autograd.graph.get_gradient_edge(x).node
+        here = torch.cuda.current_stream(x.device).cuda_stream
+        if node.metadata.setdefault("rlk_stream", here) != here and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("x is a leaf of a backward graph made on another stream: drop that one before the capture")
+    return _ROPE_FN.apply(x, inv_freq, positions, pair_axis, interleaved, False)
 
 
 def kv_append_rope(k_cache, v_cache, page_table, lens, k, v, inv_freq, *, q=None, q_out=None, positions=None,
