@@ -1214,7 +1214,7 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     tails = -(-max_tokens // 256) if max_tokens < 8192 else 32 if max_tokens <= 2**30 else 64
     rows = B * n * q_heads
     return 128 + sum((x + 127) // 128 * 128 for x in (
-        4 * B, 4 * (B + 1), 16 * groups, 4 * groups, 4 * (groups + 1), 8 * rows * pieces, 8 * rows * tails,
+        4 * B, 4 * (B + 1), 16 * groups, 4 * groups, 4 * (groups + 3), 8 * rows * pieces, 8 * rows * tails,
         4 * rows * pieces * head_dim, 4 * rows * tails * head_dim))
 
 

@@ -79,6 +79,12 @@ __host__ __device__ __forceinline__ int tail_tokens(int tokens) {
   while (t < (1 << 25) && tokens > TAIL_PARTS * t) t *= 2;
   return t;
 }
+// Their query rows go in tiles of 8 nt: as few as hold the rows in 24 each, then as narrow as they can be.
+struct TailTiles { int tiles, nt; };
+inline TailTiles tail_tiles(int rows) {
+  const int tiles = (rows + 23) / 24;
+  return {tiles, (rows + 8 * tiles - 1) / (8 * tiles)};
+}
 // What both kernels and the join go by.
 struct PrefixParts {
   PagedParams c;
@@ -95,6 +101,7 @@ struct PrefixParts {
   float* lse;
   const int32_t* first;         // [B] tokens of the sequence that are taken as shared, a multiple of 32; -1: rejected
   const uint32_t* tail_base;    // [B + 1] steps of 16 other tokens (of a kv head) before each sequence
+  uint32_t* taken;              // chunks of those steps that warps have taken
   float2* piece_ml;             // [B][kv_heads][rows][pieces]: maximum (base 2), sum
   float* piece_o;               // ... and the weighted sum of values [head_dim]
   int pieces;                   // at most, of a sequence

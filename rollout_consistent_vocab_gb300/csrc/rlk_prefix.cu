@@ -35,7 +35,8 @@ struct PrefixParams : PrefixParts {
   uint32_t* plan_tails;
   GroupPlan* plan;              // [groups]
   int32_t* busy;                // [groups] whether a sequence has new tokens
-  uint32_t* base;               // [groups + 1] units of work before each group
+  uint32_t* base;               // units of work before each of [groups + 1], then the CTAs that share them
+  uint32_t tail_cost;           // of 16 own tokens of a sequence, against a unit's UNIT_COST
   int box;                      // tokens of a copy: the largest power of 2, up to 64, that divides page_size
   bool merged;                  // a copy takes all 128 elements of its tokens (64 of them)
 };
@@ -49,6 +50,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // The work of a group in units: 512 shared tokens of a kv head for up to 128 query rows.  An
 // item, a piece of a kv head for a block of up to 256 query rows, is so many of them.
 constexpr int PIECE_UNIT = 512, PROWS = 256;
+// What one costs, in steps of 16 own tokens for 8 query rows (a unit by itself is some 9 us of an SM, a step
+// 0.2; 48 gave 16 groups of 16 samples 160 us, 96 157, 192 160, and 16 x 8 drafts 154, 127, 142).
+constexpr uint32_t UNIT_COST = 96;
+constexpr int PSMS = 152;
 __device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const GroupPlan& p) {
   const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows, full = rows / PROWS, rest = rows - full * PROWS;
   return (2u * full + (rest > PROWS / 2 ? 2u : rest > 0 ? 1u : 0u)) * p.pieces * (piece_tokens(p.shared) / PIECE_UNIT);
@@ -146,6 +151,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
     P.base[g] = run;
     run += units_of_head(P, P.plan[g]) * P.c.kv_heads;
   }
+  const uint32_t units = run;            // (of the last thread: all)
   if (tid == PLAN_THREADS - 1) P.base[G] = run;
   // the steps of 16 tokens that the sequences have behind the shared ones
   const int seqs = static_cast<int>((P.B + PLAN_THREADS - 1) / PLAN_THREADS);
@@ -162,7 +168,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
     P.plan_tails[b] = run;
     run += steps(b);
   }
-  if (tid == PLAN_THREADS - 1) P.plan_tails[P.B] = run;
+  if (tid == PLAN_THREADS - 1) {
+    P.plan_tails[P.B] = run;
+    // Shared tokens keep the tensor cores and exponentials busy, the others memory: the SMs are shared out
+    // by the work that they are, so that both go on side by side to the end (16 groups of 16 samples took
+    // 177 us one after the other).  Runs are of pairs of units, for the two streams.
+    const uint64_t of_shared = static_cast<uint64_t>(units) * UNIT_COST, of_all = of_shared + static_cast<uint64_t>(run) * P.tail_cost;
+    uint32_t ctas = static_cast<uint32_t>((PSMS * of_shared + of_all) / (of_all + 1));
+    ctas = max(1u, min(ctas, static_cast<uint32_t>(PSMS)));
+    if (units > ctas) {
+      const uint32_t per = ((units + ctas - 1) / ctas + 1) & ~1u;
+      ctas = (units + per - 1) / per;
+    }
+    P.base[G + 1] = max(1u, min(units, ctas));
+    *P.taken = 0u;
+  }
 }
 
 // ------------------------------------------------------------ the shared tokens
@@ -242,7 +262,7 @@ struct PShape {
 };
 struct PrefixMaps { CUtensorMap k, v; };
 
-// The units in equal runs, the first ones one longer.  An item is the CTA's whose run holds its first unit.
+// The units in equal runs, the first ones one longer (the CTAs without one make room at once).  An item is the CTA's whose run holds its first unit.
 __device__ __forceinline__ uint32_t run_start(uint32_t units, uint32_t workers, uint32_t k) {
   const uint32_t len = units / workers, more = units - len * workers;
   return k * len + min(k, more);
@@ -314,13 +334,13 @@ struct Way {
   __device__ __forceinline__ void begin(const PrefixParams& P) {
     const int lane = threadIdx.x & 31, G = P.groups;
     g = 0;
-    const bool few = G < 32;             // all of them are looked at at once
+    const bool few = G < 31;             // all of them are looked at at once
     uint32_t before = ~0u;
     GroupPlan mine{0, 0, 0, 0};
-    if (few && lane <= G) before = P.base[lane];
+    if (few && lane <= G + 1) before = P.base[lane];
     if (few && lane < G) mine = P.plan[lane];
     const uint32_t units = few ? __shfl_sync(0xffffffffu, before, G) : P.base[G];
-    const uint32_t workers = max(1u, min(units, gridDim.x)), me = min(blockIdx.x, workers);
+    const uint32_t workers = few ? __shfl_sync(0xffffffffu, before, G + 1) : P.base[G + 1], me = min(blockIdx.x, workers);
     at = run_start(units, workers, me), end = run_start(units, workers, min(me + 1, workers));
     if (at >= end) return;               // (a CTA without items goes through with an empty run)
     uint32_t rest = at;
@@ -868,7 +888,7 @@ static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cuda
   }
   // launched while the plan is made, for which it waits
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(152);
+  cfg.gridDim = dim3(PSMS);
   cfg.blockDim = dim3(PTHREADS);
   cfg.dynamicSmemBytes = PShape<D>::SMEM;
   cfg.stream = st;
@@ -908,7 +928,7 @@ static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t
   y.tails_at = next(static_cast<size_t>(B + 1) * 4);
   y.plan = next(static_cast<size_t>(groups) * sizeof(GroupPlan));
   y.busy = next(static_cast<size_t>(groups) * 4);
-  y.base = next(static_cast<size_t>(groups + 1) * 4);
+  y.base = next((static_cast<size_t>(groups) + 3) * 4);
   y.piece_ml = next(pieces * 8);
   y.tail_ml = next(tails * 8);
   y.piece_o = next(pieces * head_dim * 4);
@@ -979,6 +999,7 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.plan = reinterpret_cast<GroupPlan*>(ws + y.plan);
   P.busy = reinterpret_cast<int32_t*>(ws + y.busy);
   P.base = reinterpret_cast<uint32_t*>(ws + y.base);
+  P.taken = P.base + groups->groups + 2;
   P.piece_ml = reinterpret_cast<float2*>(ws + y.piece_ml);
   P.piece_o = reinterpret_cast<float*>(ws + y.piece_o);
   P.tail_ml = reinterpret_cast<float2*>(ws + y.tail_ml);
@@ -995,6 +1016,8 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.rows = cache->n * P.group;
   P.c2 = fabsf(scale) * 1.4426950408889634f;
   P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+  const TailTiles tt = tail_tiles(P.rows);
+  P.tail_cost = static_cast<uint32_t>(tt.tiles) * tt.nt * cache->kv_heads;
   P.box = box_of(cache->page_size, PTILE / 2);
   P.merged = P.box == 64 && cache->head_dim == 128;
   P.head_first = heads_first(cache);

@@ -2,12 +2,14 @@
 // the join with the shared tokens' parts.
 //
 // Own tokens are many short runs: hundreds of samples, each with some hundred tokens
-// per kv head.  So a warp goes by itself: it has a run of parts (up to 256 tokens of a
-// sequence and kv head, more for long ones), brings its keys and values by TMA into a ring
-// of its own, 16 tokens at a time, and meets no barrier but the ring's.  S^T = K Q^T and
+// per kv head.  So a warp goes by itself: it takes a chunk of parts at a time (up to 256
+// tokens of a sequence and kv head, more for long ones), brings its keys and values by TMA
+// into a ring of its own, 16 tokens at a time, and meets no barrier but the ring's.  S^T = K Q^T and
 // O^T += V^T P^T run on mma.sync with 16 tokens (or elements) as rows and 8 query rows as
 // columns, up to three tiles of 8 rows on the same copy.  A part's maximum, sum and
-// weighted sum of values go to the workspace; runs are equal in steps of 16 tokens.
+// weighted sum of values go to the workspace, so that it is of no account which warp has it.
+// The kernel's CTAs come to the SMs that the shared tokens' kernel leaves free, some at once
+// and the others when it ends; chunks go to whoever is there.
 //
 // Bound by memory where rows are few.
 
@@ -45,11 +47,11 @@ struct TailParams {
 };
 struct TailMaps { CUtensorMap k, v; };
 
-// A place in a warp's run: a part of a sequence, kv head and row tile, tokens t .. end - 1.
+// A place in a warp's chunk: a part of a sequence, kv head and row tile, tokens t .. end - 1.
 struct TailPlace {
   int b, ht, part, t, end;
   int len, nnew, first, size;   // of the sequence: its lengths, where its own tokens begin, tokens of a part
-  int64_t left;                 // steps of the run from this part's begin on (the part is the run's if there are any)
+  int64_t left;                 // steps of the chunk from this part's begin on (the part is the chunk's if there are any)
   __device__ __forceinline__ void load(const PrefixParts& P) {
     nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
     first = P.first[b];
@@ -63,7 +65,7 @@ struct TailPlace {
   }
 };
 
-// The next part; false at the run's end.
+// The next part; false at the chunk's end.
 __device__ __forceinline__ bool next_part(const TailParams& P, TailPlace& x, int HT) {
   do {
     x.left -= (x.end - (x.first + x.part * x.size) + TSTEP - 1) / TSTEP;
@@ -106,14 +108,20 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
   }
   __syncwarp();
 
-  // ---- the warp's run: steps [from, to) of all, the parts that begin there
   const int HT = P.p.c.kv_heads * P.tiles;
   const int64_t total = static_cast<int64_t>(P.p.tail_base[P.p.B]) * HT;
-  const int64_t runs = TSMS * TWARPS, me = blockIdx.x + static_cast<int64_t>(warp) * TSMS;
-  const int64_t from = total * me / runs, to = total * (me + 1) / runs;
+  // A chunk: a quarter of an equal share (half of one is slower by a twentieth, an eighth no faster), but a
+  // part's 16 steps where that is less, and a share where there are not so many.
+  const int64_t each = total / (TSMS * TWARPS);
+  const int64_t chunk = max(each / 4, min(max(each, static_cast<int64_t>(1)), static_cast<int64_t>(256 / TSTEP)));
   TailPlace load_at, work_at;
-  bool have = from < to;
-  if (have) {
+  bool have = false;
+  // ---- the next chunk of all steps that no warp has: the parts that begin there.  False where none is left.
+  auto take = [&]() {
+    uint32_t k = 0;
+    if (lane == 0) k = atomicAdd(P.p.taken, 1u);
+    const int64_t from = __shfl_sync(0xffffffffu, k, 0) * chunk, to = min(total, from + chunk);
+    if (from >= to) return false;
     // the last sequence that begins at or before it
     const uint32_t at = static_cast<uint32_t>(from / HT);
     int lo = 0, hi = static_cast<int>(P.p.B);
@@ -132,18 +140,19 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
     const int64_t in = rest - x.ht * steps;
     x.part = static_cast<int>(min(in / (x.size / TSTEP), static_cast<int64_t>(TAIL_PARTS * 2)));
     const int64_t over = in - static_cast<int64_t>(x.part) * (x.size / TSTEP);
-    x.left = to - from + over;           // (from where the part begins that holds the run's first step)
+    x.left = to - from + over;           // (from where the part begins that holds the chunk's first step)
     if (static_cast<int64_t>(x.first) + static_cast<int64_t>(x.part) * x.size >= x.len) x.part = 0;
     x.cut();
-    if (over > 0 || x.t >= x.end) have = next_part(P, x, HT);
+    have = over > 0 || x.t >= x.end ? next_part(P, x, HT) : true;
     work_at = load_at = x;
-  }
+    return true;
+  };
 
   // ---- copies: a step's pages are looked up while the step before is worked on.  Lanes 0-15 have the
   // tokens' keys, 16-31 their values; the first of a box speaks for it.
   constexpr int PANELS = D / 64;
   const uint64_t policy = evict_first_policy();            // (read once)
-  bool more = have;
+  bool more = false;
   int page = -1, place = 0;
   bool speaks = false;
   auto look = [&]() {
@@ -178,11 +187,6 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
     if (load_at.t >= load_at.end) more = next_part(P, load_at, HT);
     look();
   };
-  look();
-#pragma unroll 1
-  for (int i = 0; i < S_::STAGES - 1; ++i)
-    if (more) copy();
-
   const int g8 = lane >> 2, t4 = lane & 3;
   const uint32_t klane = (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
   const uint32_t vlane = ((lane >> 4) * 8 + (lane & 7)) * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
@@ -191,204 +195,217 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
   int held_b = -1, held_ht = -1;
   uint32_t qf[NT][KK][2];
 #pragma unroll 1
-  while (have) {
-    const int head = work_at.ht / P.tiles, row0 = (work_at.ht - head * P.tiles) * (8 * NT);
-    if (work_at.b != held_b || work_at.ht != held_ht) {
-      held_b = work_at.b, held_ht = work_at.ht;
+  while (take()) {
+    more = have && !dead;
+    look();
+#pragma unroll 1
+    for (int i = 0; i < S_::STAGES - 1; ++i)
+      if (more) copy();
+#pragma unroll 1
+    while (have) {
+      const int head = work_at.ht / P.tiles, row0 = (work_at.ht - head * P.tiles) * (8 * NT);
+      if (work_at.b != held_b || work_at.ht != held_ht) {
+        held_b = work_at.b, held_ht = work_at.ht;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          const int row = row0 + x * 8 + g8, i = row_query(P.p, row);
+          const bool real = row < P.p.rows && i < work_at.nnew;
+          const T* qp = static_cast<const T*>(P.p.q) + work_at.b * P.p.qs.batch + i * P.p.qs.token +
+                        (head * P.p.group + (row - i * P.p.group)) * P.p.qs.head + t4 * 2;
+#pragma unroll
+          for (int k = 0; k < KK; ++k) {
+            qf[x][k][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.p.q_sign : 0u;
+            qf[x][k][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.p.q_sign : 0u;
+          }
+        }
+      }
+      float o[NT][DT][4], m[NT][2], l[NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
-        const int row = row0 + x * 8 + g8, i = row_query(P.p, row);
-        const bool real = row < P.p.rows && i < work_at.nnew;
-        const T* qp = static_cast<const T*>(P.p.q) + work_at.b * P.p.qs.batch + i * P.p.qs.token +
-                      (head * P.p.group + (row - i * P.p.group)) * P.p.qs.head + t4 * 2;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[x][d][e] = 0.0f;
+        m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
+      }
+      bool part_bad = false;
+      const int p0 = work_at.len - work_at.nnew;             // the queries stand at p0 .. len - 1
+#pragma unroll 1
+      for (int t0 = work_at.t; t0 < work_at.end; t0 += TSTEP) {
+        if (more) copy();
+        if (!dead && !mbar_wait_phase(full + get * 8, phase)) {
+          dead = true;
+          more = false;
+        }
+        part_bad |= dead || ((bad_stages >> get) & 1u);
+        const uint32_t sk = ring + get * S_::STAGE, sv = sk + S_::KEYS;
+        if (!dead) {                       // (else it stays, for the end)
+          --under_way;
+          if (++get == S_::STAGES) get = 0, phase ^= 1;
+        }
+        __syncwarp();
+        float s[NT][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
-          qf[x][k][0] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16)) ^ P.p.q_sign : 0u;
-          qf[x][k][1] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + k * 16 + 8)) ^ P.p.q_sign : 0u;
+          uint32_t a[4];
+          ldsm(a, sk + (klane ^ (32 * (k % 4))) + k / 4 * S_::PANEL);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) E::mma(s[x], a, qf[x][k][0], qf[x][k][1]);
         }
-      }
-    }
-    float o[NT][DT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int x = 0; x < NT; ++x) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][d][e] = 0.0f;
-      m[x][0] = m[x][1] = -INFINITY, l[x][0] = l[x][1] = 0.0f;
-    }
-    bool part_bad = false;
-    const int p0 = work_at.len - work_at.nnew;             // the queries stand at p0 .. len - 1
-#pragma unroll 1
-    for (int t0 = work_at.t; t0 < work_at.end; t0 += TSTEP) {
-      if (more) copy();
-      if (!dead && !mbar_wait_phase(full + get * 8, phase)) {
-        dead = true;
-        more = false;
-      }
-      part_bad |= dead || ((bad_stages >> get) & 1u);
-      const uint32_t sk = ring + get * S_::STAGE, sv = sk + S_::KEYS;
-      if (!dead) {                       // (else it stays, for the end)
-        --under_way;
-        if (++get == S_::STAGES) get = 0, phase ^= 1;
-      }
-      __syncwarp();
-      float s[NT][4];
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KK; ++k) {
-        uint32_t a[4];
-        ldsm(a, sk + (klane ^ (32 * (k % 4))) + k / 4 * S_::PANEL);
-#pragma unroll
-        for (int x = 0; x < NT; ++x) E::mma(s[x], a, qf[x][k][0], qf[x][k][1]);
-      }
-      const bool masked = t0 + TSTEP - 1 > p0;
-      bool odd = false;                  // values that are not finite among a masked step's
-      if (masked) {
-#pragma unroll
-        for (int z = lane * 16; z < S_::KEYS; z += 512) odd |= E::odd(lds128(sv + z));
-        odd = __any_sync(0xffffffffu, odd);
-      }
-      uint32_t pf[NT][4];                // weights: tokens 0-7 and 8-15, then what the dtype dropped of them
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        uint32_t hidden = 0;             // bit e (of the thread's scores)
+        const bool masked = t0 + TSTEP - 1 > p0;
+        bool odd = false;                  // values that are not finite among a masked step's
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = row_query(P.p, row0 + x * 8 + 2 * t4 + e);           // at p0 + i, which 32 bits may not hold past the last token
+          for (int z = lane * 16; z < S_::KEYS; z += 512) odd |= E::odd(lds128(sv + z));
+          odd = __any_sync(0xffffffffu, odd);
+        }
+        uint32_t pf[NT][4];                // weights: tokens 0-7 and 8-15, then what the dtype dropped of them
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int t = t0 + g8 + 8 * f;
-              if (t - p0 > i || t >= work_at.end) {
-                s[x][2 * f + e] = -INFINITY;
-                hidden |= 1u << (2 * f + e);
+        for (int x = 0; x < NT; ++x) {
+          uint32_t hidden = 0;             // bit e (of the thread's scores)
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = row_query(P.p, row0 + x * 8 + 2 * t4 + e);           // at p0 + i, which 32 bits may not hold past the last token
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const int t = t0 + g8 + 8 * f;
+                if (t - p0 > i || t >= work_at.end) {
+                  s[x][2 * f + e] = -INFINITY;
+                  hidden |= 1u << (2 * f + e);
+                }
               }
             }
           }
-        }
-        // the reference m follows the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
-        float top[2];
-        bool ahead = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(s[x][e], s[x][2 + e]) * P.p.c2;
-          ahead |= top[e] > m[x][e] + E::SLACK;
-        }
-        if (__any_sync(0xffffffffu, ahead)) {
-          bool scaled = false;
-          float fac[2];
+          // the reference m follows the row's maximum where that runs SLACK ahead, so weights stay below 2^SLACK
+          float top[2];
+          bool ahead = false;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = top[e];
+            top[e] = fmaxf(s[x][e], s[x][2 + e]) * P.p.c2;
+            ahead |= top[e] > m[x][e] + E::SLACK;
+          }
+          if (__any_sync(0xffffffffu, ahead)) {
+            bool scaled = false;
+            float fac[2];
 #pragma unroll
-            for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
-            fac[e] = 1.0f;
-            if (mx > m[x][e] + E::SLACK) {
-              if (m[x][e] != -INFINITY) {
-                fac[e] = ex2f(m[x][e] - mx);
-                scaled = true;
+            for (int e = 0; e < 2; ++e) {
+              float mx = top[e];
+#pragma unroll
+              for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+              fac[e] = 1.0f;
+              if (mx > m[x][e] + E::SLACK) {
+                if (m[x][e] != -INFINITY) {
+                  fac[e] = ex2f(m[x][e] - mx);
+                  scaled = true;
+                }
+                m[x][e] = mx;
               }
-              m[x][e] = mx;
             }
-          }
-          if (__any_sync(0xffffffffu, scaled)) {
-            l[x][0] *= fac[0], l[x][1] *= fac[1];
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[x][d][e] *= fac[e & 1];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float sub = m[x][e] == -INFINITY ? E::OFF : E::OFF - m[x][e];
-#pragma unroll
-          for (int f = 0; f < 4; f += 2) s[x][f + e] = ex2f(__fmaf_rn(s[x][f + e], P.p.c2, sub));
-        }
-        // A masked token's value must not come in even as 0 * inf: values that are not finite go straight
-        // into the rows that see them (which they leave infinite or NaN), and the product takes zeros for them.
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((hidden >> e) & 1u) s[x][e] = 0.0f;
-          if (odd) {
-#pragma unroll 1
-            for (int r = 0; r < TSTEP; ++r) {
-              const int t = t0 + r;
-              if (t >= work_at.end) break;                       // (what lies in a place that nobody sees is of no account)
+            if (__any_sync(0xffffffffu, scaled)) {
+              l[x][0] *= fac[0], l[x][1] *= fac[1];
 #pragma unroll
               for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const uint32_t bits = lds16(sv + r * 128 + d / 4 * S_::PANEL + (((2 * (d % 4) + f) ^ (r & 7)) * 16) + g8 * 2);
-                  if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
+                for (int e = 0; e < 4; ++e) o[x][d][e] *= fac[e & 1];
+            }
+          }
 #pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (t - p0 <= row_query(P.p, row0 + x * 8 + 2 * t4 + e)) o[x][d][2 * f + e] += E::value(bits);
+          for (int e = 0; e < 2; ++e) {
+            const float sub = m[x][e] == -INFINITY ? E::OFF : E::OFF - m[x][e];
+#pragma unroll
+            for (int f = 0; f < 4; f += 2) s[x][f + e] = ex2f(__fmaf_rn(s[x][f + e], P.p.c2, sub));
+          }
+          // A masked token's value must not come in even as 0 * inf: values that are not finite go straight
+          // into the rows that see them (which they leave infinite or NaN), and the product takes zeros for them.
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((hidden >> e) & 1u) s[x][e] = 0.0f;
+            if (odd) {
+#pragma unroll 1
+              for (int r = 0; r < TSTEP; ++r) {
+                const int t = t0 + r;
+                if (t >= work_at.end) break;                       // (what lies in a place that nobody sees is of no account)
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                  for (int f = 0; f < 2; ++f) {
+                    const uint32_t bits = lds16(sv + r * 128 + d / 4 * S_::PANEL + (((2 * (d % 4) + f) ^ (r & 7)) * 16) + g8 * 2);
+                    if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (t - p0 <= row_query(P.p, row0 + x * 8 + 2 * t4 + e)) o[x][d][2 * f + e] += E::value(bits);
+                  }
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[x][e] += s[x][e] + s[x][2 + e];
+          E::split(s[x][0], s[x][1], pf[x][0], pf[x][2]);
+          E::split(s[x][2], s[x][3], pf[x][1], pf[x][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
+        }
+        if (odd) {
+#pragma unroll 1
+          for (int d4 = 0; d4 < DT; d4 += 4) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              uint32_t a[1][4];
+              ldsm_t(a[0], sv + (vlane ^ (32 * z)) + d4 / 4 * S_::PANEL);
+              E::clear_odd(a[0]);
+#pragma unroll
+              for (int d = 0; d < DT; d += 4)
+                if (d == d4) {
+#pragma unroll
+                  for (int x = 0; x < NT; ++x) E::weigh(o[x] + d + z, a, pf[x]);
                 }
             }
           }
-        }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) l[x][e] += s[x][e] + s[x][2 + e];
-        E::split(s[x][0], s[x][1], pf[x][0], pf[x][2]);
-        E::split(s[x][2], s[x][3], pf[x][1], pf[x][3]);
+          for (int d = 0; d < DT; d += 4) {
+            uint32_t a[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pf[x][e] = movm(pf[x][e]);
-      }
-      if (odd) {
-#pragma unroll 1
-        for (int d4 = 0; d4 < DT; d4 += 4) {
+            for (int z = 0; z < 4; ++z) ldsm_t(a[z], sv + (vlane ^ (32 * z)) + d / 4 * S_::PANEL);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            uint32_t a[1][4];
-            ldsm_t(a[0], sv + (vlane ^ (32 * z)) + d4 / 4 * S_::PANEL);
-            E::clear_odd(a[0]);
-#pragma unroll
-            for (int d = 0; d < DT; d += 4)
-              if (d == d4) {
-#pragma unroll
-                for (int x = 0; x < NT; ++x) E::weigh(o[x] + d + z, a, pf[x]);
-              }
+            for (int x = 0; x < NT; ++x) E::weigh(o[x] + d, a, pf[x]);
           }
         }
-      } else {
-#pragma unroll
-        for (int d = 0; d < DT; d += 4) {
-          uint32_t a[4][4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) ldsm_t(a[z], sv + (vlane ^ (32 * z)) + d / 4 * S_::PANEL);
-#pragma unroll
-          for (int x = 0; x < NT; ++x) E::weigh(o[x] + d, a, pf[x]);
-        }
+        __syncwarp();                      // the stage may be filled again
       }
-      __syncwarp();                      // the stage may be filled again
+      // ---- the part's result
+      if (part_bad && lane == 0 && P.p.c.err) atomicAdd(P.p.c.err, 1);
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[x][e];
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+          const int row = row0 + x * 8 + 2 * t4 + e, i = row_query(P.p, row);
+          if (row >= P.p.rows || i >= work_at.nnew) continue;
+          const int64_t slot = ((static_cast<int64_t>(work_at.b) * P.p.c.kv_heads + head) * P.p.rows + row) * P.p.tails + work_at.part;
+          float* dst = P.p.tail_o + slot * D + g8;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            dst[d * 16] = o[x][d][e];
+            dst[d * 16 + 8] = o[x][d][2 + e];
+          }
+          if (g8 == 0) P.p.tail_ml[slot] = part_bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m[x][e], sum);
+        }
+      have = next_part(P, work_at, HT);
     }
-    // ---- the part's result
-    if (part_bad && lane == 0 && P.p.c.err) atomicAdd(P.p.c.err, 1);
-#pragma unroll
-    for (int x = 0; x < NT; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[x][e];
-#pragma unroll
-        for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
-        const int row = row0 + x * 8 + 2 * t4 + e, i = row_query(P.p, row);
-        if (row >= P.p.rows || i >= work_at.nnew) continue;
-        const int64_t slot = ((static_cast<int64_t>(work_at.b) * P.p.c.kv_heads + head) * P.p.rows + row) * P.p.tails + work_at.part;
-        float* dst = P.p.tail_o + slot * D + g8;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          dst[d * 16] = o[x][d][e];
-          dst[d * 16 + 8] = o[x][d][2 + e];
-        }
-        if (g8 == 0) P.p.tail_ml[slot] = part_bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m[x][e], sum);
-      }
-    have = next_part(P, work_at, HT);
+#pragma unroll 1
+    for (; !dead && under_way > 0; --under_way) {            // (only should the lengths have changed)
+      mbar_wait_phase(full + get * 8, phase);
+      if (++get == S_::STAGES) get = 0, phase ^= 1;
+    }
   }
   // Copies that nobody waited for (one did not come in time, or the lengths changed under the call): the
   // warp stays for them, within limits.
@@ -501,9 +518,9 @@ static rlk_status launch_tail_rows(const TailParams& P, const TailMaps& maps, in
 rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool alone, cudaStream_t stream) {
   TailParams P{};
   P.p = parts;
-  // as few tiles as hold the rows in 24 each, then as narrow as they can be
-  P.tiles = (parts.rows + 23) / 24;
-  const int nt = (parts.rows + 8 * P.tiles - 1) / (8 * P.tiles);
+  const TailTiles tt = tail_tiles(parts.rows);
+  P.tiles = tt.tiles;
+  const int nt = tt.nt;
   P.box = box_of(parts.c.page_size, TSTEP);
   P.merged = P.box == TSTEP && head_dim == 128;
   TailMaps maps{};
