@@ -1209,8 +1209,8 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     if B == 0 or n == 0 or q_heads == 0:
         return 0
     pieces = 0
-    for top in (min(max_shared, 8191), max_shared) if groups else ():
-        pieces = max(pieces, -(-(top // 32 * 32) // (512 if top < 8192 else 1024)))
+    for top in (min(max_shared, 1023), min(max_shared, 16383), max_shared) if groups else ():
+        pieces = max(pieces, -(-(top // 32 * 32) // (512 if top < 1024 else 1024 if top < 16384 else 2048)))
     tails = -(-max_tokens // 256) if max_tokens < 8192 else 32 if max_tokens <= 2**30 else 64
     rows = B * n * q_heads
     return 128 + sum((x + 127) // 128 * 128 for x in (

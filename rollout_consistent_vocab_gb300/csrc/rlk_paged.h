@@ -64,10 +64,14 @@ rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, i
 // queries go over together, and of each sequence's other ones.  How they are cut goes by a
 // sequence's own lengths alone, so that its result does not depend on its batch.
 //
-// Tokens of a part of the shared ones: more parts where there are few tokens (one to an
-// SM), fewer where there are many (the parts' results are a read and a write of 128 tokens'
-// size for 128 rows).
-__host__ __device__ __forceinline__ int piece_tokens(int shared) { return shared < 8192 ? 512 : 1024; }
+// Tokens of a part of the shared ones: the fewer the longer, since a part costs as much as three tiles of
+// 128 tokens, and a write and a read of 128 tokens' size for 128 rows; but as many as there are SMs, for a
+// group or two (1 x 64 samples of 8190 tokens: parts of 1024 58 us, of 2048 71; 2 x 32 of 131071 tokens:
+// parts of 1024 232 us, of 2048 213).
+constexpr int PIECES_1024 = 1024, PIECES_2048 = 16384;     // shared tokens from which on parts are so long
+__host__ __device__ __forceinline__ int piece_tokens(int shared) {
+  return shared < PIECES_1024 ? 512 : shared < PIECES_2048 ? 1024 : 2048;
+}
 __host__ __device__ __forceinline__ int pieces_of(int shared) {
   const int t = piece_tokens(shared);
   return shared / t + (shared % t != 0);
@@ -102,10 +106,11 @@ struct PrefixParts {
   const int32_t* first;         // [B] tokens of the sequence that are taken as shared, a multiple of 32; -1: rejected
   const uint32_t* tail_base;    // [B + 1] steps of 16 other tokens (of a kv head) before each sequence
   uint32_t* taken;              // chunks of those steps that warps have taken
-  float2* piece_ml;             // [B][kv_heads][rows][pieces]: maximum (base 2), sum
-  float* piece_o;               // ... and the weighted sum of values [head_dim]
+  float2* piece_ml;             // [B][kv_heads][pieces][rows]: maximum (base 2), sum
+  float* piece_o;               // ... and the weighted sum of values [B][kv_heads][pieces][head_dim / 8][rows][8]: a warp with a
+                                // thread to a row has few lines to write at a time
   int pieces;                   // at most, of a sequence
-  float2* tail_ml;              // [B][kv_heads][rows][tails]
+  float2* tail_ml;              // the same of the tails
   float* tail_o;
   int tails;
 };

@@ -50,9 +50,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // The work of a group in units: 512 shared tokens of a kv head for up to 128 query rows.  An
 // item, a piece of a kv head for a block of up to 256 query rows, is so many of them.
 constexpr int PIECE_UNIT = 512, PROWS = 256;
-// What one costs, in steps of 16 own tokens for 8 query rows (a unit by itself is some 9 us of an SM, a step
-// 0.2; 48 gave 16 groups of 16 samples 160 us, 96 157, 192 160, and 16 x 8 drafts 154, 127, 142).
-constexpr uint32_t UNIT_COST = 96;
+// What one costs, in steps of 16 own tokens for 8 query rows (a unit by itself is some 8 us of an SM, a step
+// 0.2 on the way through memory; 48 and 144 are slower by a tenth and more where neither is little).
+constexpr uint32_t UNIT_COST = 72;
 constexpr int PSMS = 152;
 __device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const GroupPlan& p) {
   const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows, full = rows / PROWS, rest = rows - full * PROWS;
@@ -706,7 +706,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
     // which would be 3 us of the first half's 4.
     bool have = true, dry = true;
     st.len0 = st.len1 = 64;
-    int64_t out = -1;                    // the row's first part, in parts; -1: no query
+    int64_t out = -1;                    // the first part of the row's sequence and kv head, in rows; -1: no query
+    int row_in = 0;                      // the row in its sequence
     auto ask = [&](const Step& x) {      // the queries of the stream's rows of x
       held.take(x);
       const int at = x.rb * PROWS + (x.both ? s * PTILE : 0) + row, k = at / P.rows, r = at - k * P.rows, i = r / P.group, b = x.seq0 + k;
@@ -715,7 +716,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
       if (k < x.seqs) {
         const int nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
         if (P.first[b] >= 0 && i < nnew) {
-          out = ((static_cast<int64_t>(b) * P.c.kv_heads + x.head) * P.rows + r) * P.pieces;
+          out = (static_cast<int64_t>(b) * P.c.kv_heads + x.head) * P.pieces * P.rows;
+          row_in = r;
           src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + b * P.qs.batch + i * P.qs.token +
                                                (x.head * P.group + (r - i * P.group)) * P.qs.head);
         }
@@ -732,24 +734,21 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
       __syncwarp();
       if (lane == 0) mbar_arrive(asked + 8 * s);
     };
+    auto missing = [&](const Step& x) {  // whether one of the stream's pages of x that the lane looks at is not there
+      bool bad = false;
+      int place;
+      const int to = static_cast<int>(page_of(P.c, P.page_magic, x.from(s) + x.tokens(s) - 1, place));
+      for (int p = static_cast<int>(page_of(P.c, P.page_magic, x.from(s), place)) + lane; p <= to; p += 32) {
+        const int page = __ldg(P.c.table + x.seq0 * P.c.table_stride + p);
+        bad |= page < 0 || page >= P.c.num_pages;
+      }
+      return bad;
+    };
+    bool bad = false;
     for (; have; st = nxt) {
-      const bool more = !dry && way.next(P, nxt);
+      bool more = false;
       const int all = st.tokens(s);
       if (all > 0) {
-        if (!dry && !held.of(st)) ask(st);
-        // whether all the piece's pages are there
-        bool bad = false;
-        if (!dry) {
-          int place;
-          const int to = static_cast<int>(page_of(P.c, P.page_magic, st.from(s) + all - 1, place));
-          for (int p = static_cast<int>(page_of(P.c, P.page_magic, st.from(s), place)) + lane; p <= to; p += 32) {
-            const int page = __ldg(P.c.table + st.seq0 * P.c.table_stride + p);
-            bad |= page < 0 || page >= P.c.num_pages;
-          }
-          bad = __any_sync(0xffffffffu, bad);
-        }
-        const int64_t slot_at = out + st.piece_of(s);
-        const bool query = out >= 0;
         float m = -INFINITY, l = 0.0f;
         const int halves = (all + 63) / 64;
 #pragma unroll 1
@@ -829,17 +828,33 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           }
           __syncwarp();
         }
+        const int64_t slot_at = out + static_cast<int64_t>(st.piece_of(s)) * P.rows;
+        const bool query = out >= 0;
+        const int r = row_in;
         if (dry) {
           dry = false;
           begin();
           have = way.next(P, nxt);
+          if (have && nxt.tokens(s) > 0) {
+            ask(nxt);
+            bad = missing(nxt);
+          }
           continue;
         }
-        if (more && nxt.tokens(s) > 0 && !held.of(nxt)) ask(nxt);        // (all products with the old ones are done)
+        // What the next piece needs is looked up before this one's result goes out: a load waits for the stores
+        // before it (2 us of them here).  All products with the queries of this one are done.
+        more = way.next(P, nxt);
+        bool bad_next = false;
+        if (more && nxt.tokens(s) > 0) {
+          if (!held.of(nxt)) ask(nxt);
+          bad_next = missing(nxt);
+        }
         bad |= !result_in(total - 1) || *dead != 0u;
         bad = __any_sync(0xffffffffu, bad);
         tc_fence_after();
         if (bad && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+        const int64_t step = 8 * static_cast<int64_t>(P.rows);
+        float* const to = P.piece_o + slot_at * D + 8 * static_cast<int64_t>(r);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t y[32];
@@ -852,11 +867,18 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
               for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * W::TO_PIECES);
             }
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) store8(P.piece_o + slot_at * D + 32 * c + e, y + e);
+            for (int e = 0; e < 32; e += 8) store8(to + (4 * c + e / 8) * step, y + e);
           }
           __syncwarp();
         }
-        if (query) P.piece_ml[slot_at] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
+        if (query) P.piece_ml[slot_at + r] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
+        bad = bad_next;
+      } else {
+        more = way.next(P, nxt);
+        if (more && nxt.tokens(s) > 0) {
+          if (!held.of(nxt)) ask(nxt);
+          bad = missing(nxt);
+        }
       }
       have = more;
     }
@@ -911,8 +933,8 @@ struct PrefixLayout {
 };
 static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t head_dim, int64_t max_tokens, int groups, int max_shared) {
   PrefixLayout y{};
-  for (const int top : {max_shared < 8191 ? max_shared : 8191, max_shared}) {
-    const int pieces = pieces_of(top / PREFIX_STEP * PREFIX_STEP);
+  for (const int most : {PIECES_1024 - 1, PIECES_2048 - 1, 0x7fffffff}) {
+    const int pieces = pieces_of((max_shared < most ? max_shared : most) / PREFIX_STEP * PREFIX_STEP);
     y.pieces = pieces > y.pieces ? pieces : y.pieces;
   }
   if (groups == 0) y.pieces = 0;
@@ -975,7 +997,7 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   if (groups->groups > 0 && (!groups->group_start || !groups->shared_lens))
     return fail(RLK_EINVAL, "group_start or shared_lens is NULL");
   const double rows = static_cast<double>(cache->B) * cache->n * (q_heads / cache->kv_heads);
-  if (rows >= 2147483392.0 || (rows / 128 + groups->groups) * cache->kv_heads * (groups->max_shared / 512 + 2.0) >= 2147483648.0 ||
+  if (rows >= 2147483392.0 || (rows / 128 + groups->groups) * cache->kv_heads * (groups->max_shared / 512 + 4.0) >= 2147483648.0 ||
       static_cast<double>(cache->B) * (tokens / 16 + 1.0) >= 2147483648.0)
     return fail(RLK_EINVAL, "too many query rows or tokens for one call");
   if ((s = check_bth(q, q_strides, "q")) != RLK_OK) return s;

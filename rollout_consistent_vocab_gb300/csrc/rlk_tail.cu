@@ -390,14 +390,15 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
           for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
           const int row = row0 + x * 8 + 2 * t4 + e, i = row_query(P.p, row);
           if (row >= P.p.rows || i >= work_at.nnew) continue;
-          const int64_t slot = ((static_cast<int64_t>(work_at.b) * P.p.c.kv_heads + head) * P.p.rows + row) * P.p.tails + work_at.part;
-          float* dst = P.p.tail_o + slot * D + g8;
+          const int64_t slot = ((static_cast<int64_t>(work_at.b) * P.p.c.kv_heads + head) * P.p.tails + work_at.part) * P.p.rows;
+          float* dst = P.p.tail_o + slot * D + row * 8LL + g8;
+          const int64_t chunk8 = P.p.rows * 8LL;
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            dst[d * 16] = o[x][d][e];
-            dst[d * 16 + 8] = o[x][d][2 + e];
+            dst[2 * d * chunk8] = o[x][d][e];
+            dst[(2 * d + 1) * chunk8] = o[x][d][2 + e];
           }
-          if (g8 == 0) P.p.tail_ml[slot] = part_bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m[x][e], sum);
+          if (g8 == 0) P.p.tail_ml[slot + row] = part_bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m[x][e], sum);
         }
       have = next_part(P, work_at, HT);
     }
@@ -414,60 +415,60 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
     mbar_wait_phase(full + get * 8, phase);
     if (++get == S_::STAGES) get = 0, phase ^= 1;
   }
-  // (launched over the end of the shared tokens' kernel: the join goes by the end of this one alone)
+  // (launched beside the shared tokens' kernel: the join goes by the end of this one alone)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------ the join
 
-// A warp to a row: its parts, the shared tokens' first, go to four chains in turn, whose sums are
-// joined in order.
-constexpr int TJOIN = 8;                 // warps of a CTA
-template <class T, int D>
-__global__ void __launch_bounds__(TJOIN * 32) tail_join_kernel(const __grid_constant__ PrefixParts P) {
-  constexpr int E = D / 32, AT_ONCE = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t entry = blockIdx.x * static_cast<int64_t>(TJOIN) + (threadIdx.x >> 5);
-  const int64_t bh = entry / P.rows;
-  const int row = static_cast<int>(entry - bh * P.rows), i = row / P.group;
+// A thread to four elements of a row, in the order in which the parts lie: they go to two chains in
+// turn, the shared tokens' first, whose sums are joined.  Bound by the latency of reads, of which each thread
+// has a chain.  With more threads than are on the GPU at once each has two parts under way, and few registers;
+// with fewer, eight (16 x 8 sequences with drafts, 655,360 threads: 14 us after the last part, with eight 24;
+// 2 x 32 with 131,071 shared tokens, 65,536 threads: 15, with two 27).
+constexpr int TJOIN = 256, JOIN_MANY = TSMS * 1024;        // threads of a CTA, and of all with two parts each
+template <class T, int D, int AT_ONCE>
+__global__ void __launch_bounds__(TJOIN, AT_ONCE == 2 ? 4 : 2) tail_join_kernel(const __grid_constant__ PrefixParts P) {
+  const int64_t id = blockIdx.x * static_cast<int64_t>(TJOIN) + threadIdx.x, each = P.rows * static_cast<int64_t>(D / 4), bh = id / each;
+  const uint32_t in = static_cast<uint32_t>(id - bh * each), two = in >> 1;        // (pairs of threads: 8 elements)
+  const int d8 = two / P.rows, row = two - d8 * P.rows, i = row / P.group, half = (in & 1) * 4;
   const int b = static_cast<int>(bh / P.c.kv_heads), head = static_cast<int>(bh - static_cast<int64_t>(b) * P.c.kv_heads);
   if (b >= P.B) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int first = P.first[b], nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
+  const int first = P.first[b], nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n, own = P.c.lens[b] - first;
   const bool ok = first >= 0, query = ok && i < nnew;
-  if (!ok && row == 0 && head == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
-  JoinRow<D> chain[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!ok && in == 0 && head == 0 && P.c.err) atomicAdd(P.c.err, 1);
+  JoinRow<128> chain[2];
   if (query) {
-    const int own = P.c.lens[b] - first, size = tail_tokens(own);
+    const int size = tail_tokens(own);
     const int pieces = min(pieces_of(first), P.pieces), parts = pieces + min(own / size + (own % size != 0), P.tails);
+    const int64_t shared = bh * P.pieces, tails = bh * P.tails - pieces;
     for (int p0 = 0; p0 < parts; p0 += AT_ONCE) {
       float2 h[AT_ONCE];
-      float v[AT_ONCE][E];
+      float v[AT_ONCE][4];
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k) {
         const int p = min(p0 + k, parts - 1);              // (past the last one: it again)
         const bool of_shared = p < pieces;
-        const int64_t at = of_shared ? entry * P.pieces + p : entry * P.tails + (p - pieces);
-        h[k] = (of_shared ? P.piece_ml : P.tail_ml)[at];
-        load_row<E>((of_shared ? P.piece_o : P.tail_o) + at * D + lane * E, v[k]);
+        const int64_t at = ((of_shared ? shared : tails) + p) * P.rows;
+        h[k] = (of_shared ? P.piece_ml : P.tail_ml)[at + row];
+        load_row<4>((of_shared ? P.piece_o : P.tail_o) + at * D + in * 4LL, v[k]);
       }
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k)
-        if (p0 + k < parts) chain[k % 4].add(h[k].x, h[k].y, v[k]);
+        if (p0 + k < parts) chain[k % 2].add(h[k].x, h[k].y, v[k]);
     }
-#pragma unroll
-    for (int k = 1; k < 4; ++k) chain[0].add(chain[k]);
+    chain[0].add(chain[1]);
   }
-  const JoinRow<D>& all = chain[0];
+  const JoinRow<128>& all = chain[0];
   const float inv = all.L == 0.0f ? 0.0f : __frcp_rn(all.L), nan = __int_as_float(0x7fc00000);
   const int hq = head * P.group + (row - i * P.group);
-  T r[E];
+  T r[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) from_float(!ok ? nan : !query ? 0.0f : __fmul_rn(all.o[e], inv), r[e]);
-  T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + lane * E;
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(op) = *reinterpret_cast<const uint2*>(r);
-  else *reinterpret_cast<uint32_t*>(op) = *reinterpret_cast<const uint32_t*>(r);
-  if (P.lse && lane == 0)
+  for (int e = 0; e < 4; ++e) from_float(!ok ? nan : !query ? 0.0f : __fmul_rn(all.o[e], inv), r[e]);
+  T* op = static_cast<T*>(P.out) + b * P.os.batch + i * P.os.token + hq * P.os.head + d8 * 8 + half;
+  *reinterpret_cast<uint2*>(op) = *reinterpret_cast<const uint2*>(r);
+  if (P.lse && d8 == 0 && half == 0)
     P.lse[(static_cast<int64_t>(b) * P.c.n + i) * P.q_heads + hq] = !ok ? nan : !query ? -INFINITY : lse_of<T>(all.M, all.L);
 }
 
@@ -492,16 +493,16 @@ static rlk_status launch_tails(const TailParams& P, const TailMaps& maps, bool a
   cfg.dynamicSmemBytes = TShape<D>::SMEM;
   cfg.stream = st;
   cfg.attrs = &attr;
-  // (behind the shared tokens' kernel, which has waited for the plan: on the SMs that it leaves one by one)
+  // (beside the shared tokens' kernel, which has waited for the plan)
   cfg.numAttrs = alone ? 0 : 1;
   e = cudaLaunchKernelEx(&cfg, tail_kernel<T, D, NT>, P, maps);
   if (e == cudaSuccess) {
-    const int64_t rows = P.p.B * P.p.c.kv_heads * P.p.rows;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + TJOIN - 1) / TJOIN));
-    cfg.blockDim = dim3(TJOIN * 32);
+    const int64_t threads = P.p.B * P.p.c.kv_heads * P.p.rows * (D / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>((threads + TJOIN - 1) / TJOIN));
+    cfg.blockDim = dim3(TJOIN);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tail_join_kernel<T, D>, P.p);
+    e = threads > JOIN_MANY ? cudaLaunchKernelEx(&cfg, tail_join_kernel<T, D, 2>, P.p) : cudaLaunchKernelEx(&cfg, tail_join_kernel<T, D, 8>, P.p);
   }
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
   return RLK_OK;

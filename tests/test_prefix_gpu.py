@@ -143,6 +143,7 @@ RUNS = [
     ([(40, 1700), (2, 2300), (33, 1600), (1, 4500), (70, 1100), (2, 4200)], 16, 4, 64, 64, "bf16"),    # one tile of rows and two
     ([(33, 2600), (3, 9300), (34, 2000), (1, 8900), (33, 1700), (2, 3000)], 32, 8, 128, 24, "bf16"),
     ([(1, 32 + 544 * (i % 9)) for i in range(40)], 8, 8, 128, 128, "bf16"),
+    ([(40, 20000), (2, 16384), (3, 1500), (33, 33000), (1, 700), (2, 16383), (5, 1024), (4, 1023)], 16, 4, 64, 64, "bf16"),    # of all lengths
 ]
 
 
@@ -422,6 +423,20 @@ def test_many_small_groups():
     c = make(members, tails, 1, 2, 1, 64, 16, "bf16", seed=25)
     out, lse = run(c)
     compare(c, out, lse, [1] * len(tails))
+
+
+def test_many_own_tokens_in_a_large_batch():
+    # more chunks of own tokens than warps, and more elements of the result than threads at once: the bits are
+    # those of each sequence alone
+    tails = [1 + (211 * i) % 2900 for i in range(200)]
+    c = make([(9, 1500), (120, 600)], tails, 1, 64, 2, 64, 16, "bf16", seed=31, before=3)
+    out, lse = run(c)
+    compare(c, out, lse, [1] * 200, rows=slice(0, 200, 9))
+    assert bool(torch.isfinite(out).all())
+    for b in (0, 3, 11, 70, 131, 199):
+        d = dict(c, q=c["q"][b:b + 1], table=c["table"][b:b + 1], lens=c["lens"][b:b + 1], start=i32([0, 1]), shared=i32([c["of"][b]]))
+        o, z = run(d)
+        assert torch.equal(bits(o[0]), bits(out[b])) and torch.equal(bits(z[0]), bits(lse[b])), b
 
 
 def test_a_cache_past_32_bits():
