@@ -36,7 +36,7 @@ struct PrefixParams : PrefixParts {
   GroupPlan* plan;              // [groups]
   int32_t* busy;                // [groups] whether a sequence has new tokens
   uint32_t* base;               // units of work before each of [groups + 1], then the CTAs that share them
-  uint32_t tail_cost;           // of 16 own tokens of a sequence, against a unit's UNIT_COST
+  uint32_t unit_cost, tail_cost;         // of a unit, and of 16 own tokens of a sequence
   int box;                      // tokens of a copy: the largest power of 2, up to 64, that divides page_size
   bool merged;                  // a copy takes all 128 elements of its tokens (64 of them)
 };
@@ -51,8 +51,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // item, a piece of a kv head for a block of up to 256 query rows, is so many of them.
 constexpr int PIECE_UNIT = 512, PROWS = 256;
 // What one costs, in steps of 16 own tokens for 8 query rows (a unit by itself is some 8 us of an SM, a step
-// 0.2 on the way through memory; 48 and 144 are slower by a tenth and more where neither is little).
-constexpr uint32_t UNIT_COST = 72;
+// 0.2 on the way through memory; 48 and 144 are slower by a tenth and more where neither is little;
+// a step of 64 elements is half as many bytes, a unit of them nearly as many exponentials.)
+constexpr uint32_t UNIT_COST_128 = 72, UNIT_COST_64 = 100;
 constexpr int PSMS = 152;
 __device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const GroupPlan& p) {
   const uint32_t rows = static_cast<uint32_t>(p.seqs) * P.rows, full = rows / PROWS, rest = rows - full * PROWS;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
     // Shared tokens keep the tensor cores and exponentials busy, the others memory: the SMs are shared out
     // by the work that they are, so that both go on side by side to the end (16 groups of 16 samples took
     // 177 us one after the other).  Runs are of pairs of units, for the two streams.
-    const uint64_t of_shared = static_cast<uint64_t>(units) * UNIT_COST, of_all = of_shared + static_cast<uint64_t>(run) * P.tail_cost;
+    const uint64_t of_shared = static_cast<uint64_t>(units) * P.unit_cost, of_all = of_shared + static_cast<uint64_t>(run) * P.tail_cost;
     uint32_t ctas = static_cast<uint32_t>((PSMS * of_shared + of_all) / (of_all + 1));
     ctas = max(1u, min(ctas, static_cast<uint32_t>(PSMS)));
     if (units > ctas) {
@@ -1039,6 +1040,7 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.c2 = fabsf(scale) * 1.4426950408889634f;
   P.q_sign = scale < 0.0f ? 0x80008000u : 0u;
   const TailTiles tt = tail_tiles(P.rows);
+  P.unit_cost = cache->head_dim == 128 ? UNIT_COST_128 : UNIT_COST_64;
   P.tail_cost = static_cast<uint32_t>(tt.tiles) * tt.nt * cache->kv_heads;
   P.box = box_of(cache->page_size, PTILE / 2);
   P.merged = P.box == 64 && cache->head_dim == 128;
