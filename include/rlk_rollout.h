@@ -1,12 +1,14 @@
 /*
  * rlk_rollout.h -- C ABI of the rollout's serving operators for GB300
  * (sm_103a), part of librlk_logp.so: the paged key-value cache (append, and
- * the attention of new tokens over it) and the verification of drafted
- * tokens.  One speculative rollout step is
+ * the attention of new tokens over it), the rotation of heads by position, and
+ * the verification of drafted tokens.  One speculative rollout step is
  *
  *   rlk_kv_append -> rlk_paged_attention -> the rest of the model's layers,
  *   the LM head -> rlk_verify_drafts,
  *
+ * or, of a model whose heads turn with their positions and for many samples of
+ * each prompt, rlk_kv_append_rope -> rlk_prefix_attention in place of the first two,
  * whose emitted tokens and logprobs are the rollout side that rlk_logp_pair
  * reproduces at training time ("Configurable H100 consistency runs": the
  * rollout engine's decode, sampling flags and logprobs).
@@ -186,11 +188,17 @@ typedef struct rlk_prefix_groups {
  * fault (NaN for all their places, as in rlk_paged_attention, *err_count raised).
  * A shared token's page number out of range rejects the group's new tokens.
  * A sequence's result depends on its own tokens and its shared length, not on
- * what else is in its group or the batch; one in no group, or that shares fewer
- * than 32 tokens, has rlk_paged_attention's bits.
+ * what else is in its group or the batch (the bits are not rlk_paged_attention's:
+ * its tokens are cut otherwise).
  * Precision is that of rlk_paged_attention, but for the weights of shared tokens
  * in f16: 22 bits, no finer than 2^-37 of the row's largest weight among up to
  * 2048 tokens.
+ * n new tokens of all of a group's sequences are taken together, so that its
+ * shared tokens are read once for 256 query rows of a kv head (n times the
+ * query heads of one, times the sequences).  The sizes are limited:
+ * max_pages * page_size below 2^31 - 64, B times that below 2^35, query rows (B * n * q_heads / kv_heads)
+ * below 2^31, and those over 128, plus the groups, times kv_heads and
+ * max_shared / 512 + 4 below 2^31.
  *   workspace: of rlk_prefix_attention_workspace's size for max_tokens =
  *     max_pages * page_size, 16-byte aligned; not kept. */
 rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_groups* groups, const void* q,

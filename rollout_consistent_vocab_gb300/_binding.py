@@ -1230,7 +1230,8 @@ def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_
     after them.  ``max_shared``: what no shared length exceeds (None: what the page table
     holds); the scratch's size goes by it.  The rest as in paged_attention; ``workspace``:
     uint8 [prefix_attention_workspace_bytes(...)].  A sequence's result does not depend on
-    what else is in its group or the batch."""
+    what else is in its group or the batch.  Worth its four launches from groups of two on
+    where the batch is large, and of eight where there is one group alone."""
     lib = load_library()
     torch = _torch()
     if q.dim() != 4:

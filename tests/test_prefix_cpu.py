@@ -39,6 +39,9 @@ def test_call_is_checked(lib):
     for kw in (dict(start=0xA0002), dict(shared=0xB0001), dict(q=0x60008), dict(out=0x70004), dict(lse=0x90002), dict(ws=0x80008),
                dict(os=b.BTHStrides(512, 256, 130))):
         assert attend(lib, **kw) == b.RLK_EALIGN, kw
+    # places a step past the last token are still of 32 bits; so are the steps of all sequences
+    for c in (cache(page_size=1, max_pages=2**31 - 64, table_stride=2**31), cache(page_size=1 << 20, max_pages=2047, B=65535, table_stride=2048)):
+        assert attend(lib, c=c) == b.RLK_EINVAL
     for c in (cache(B=0), cache(n=0), cache(B=0, k=None, lens=None, page_table=None)):
         assert attend(lib, c=c, q=None, qs=None, out=None, os=None, ws=None, start=None, shared=None) == b.RLK_OK
 
