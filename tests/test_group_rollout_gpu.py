@@ -230,6 +230,44 @@ def test_outputs_dropped_while_the_current_stream_reads_them(make):
     ts.test_outputs_dropped_while_the_current_stream_reads_them(make)
 
 
+# ------------------------------------------------------------ few and many
+
+@pytest.mark.parametrize("B,n", [(0, 1), (0, 0), (3, 0)])
+def test_nothing_to_do(B, n):
+    k, v = (tr.rand((4, 16, 2, 64), "bf16", s) for s in (19, 20))
+    table, lens = torch.zeros((B, 2), dtype=torch.int32, device=DEV), torch.full((B,), 5, dtype=torch.int32, device=DEV)
+    q, kn = tr.rand((B, n, 4, 64), "bf16", 21), tr.rand((B, n, 2, 64), "bf16", 22)
+    before = k.clone()
+    assert pkg.kv_append_rope(k, v, table, lens, kn, kn, tr.freq_of(64), q=q).shape == q.shape
+    out, lse = pkg.prefix_attention(q, k, v, table, lens, i32([0, B]), i32([5]))
+    assert out.shape == q.shape and lse.shape == (B, n, 4) and torch.equal(k, before)
+
+
+def test_no_groups_and_one_page():
+    # all on their own; and a cache of a single page, which the shared and the own tokens are in
+    c = tp.make([], [1, 40, 300, 17], 1, 8, 2, 128, 16, "bf16", seed=23)
+    tp.compare(c, *tp.run(c), [1] * 4)
+    tp.compare(c, *tp.run(c, max_shared=0), [1] * 4)
+    k, v = (tr.rand((1, 200, 2, 64), "f16", s) for s in (24, 25))
+    q = tr.rand((1, 2, 8, 64), "f16", 26)
+    d = dict(q=q, k=k, v=v, table=i32([[0]]), whole=torch.zeros((1, 1), dtype=torch.int32), lens=i32([190]), start=i32([0, 1]),
+             shared=i32([170]), of=[170], dtype="f16")
+    tp.compare(d, *tp.run(d), [2])
+
+
+def test_thousands_of_groups():
+    members = [(1 + i % 2, 32 * (i % 4)) for i in range(2500)]
+    tails = [1 + (7 * i) % 20 for i in range(sum(m for m, _ in members))]
+    c = tp.make(members, tails, 1, 2, 1, 64, 16, "bf16", seed=27)
+    err = i32([0])
+    out, lse = tp.run(c, err_count=err)
+    assert int(err) == 0
+    tp.compare(c, out, lse, [1] * len(tails))
+    c["start"][1700] += 4000                                     # (past the next one's begin)
+    out, lse = tp.run(c, err_count=err)
+    assert int(err) >= len(tails) and bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
 # ------------------------------------------------------------ gradients
 
 def test_a_captured_gradient():
