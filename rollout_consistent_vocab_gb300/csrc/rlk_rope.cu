@@ -11,8 +11,10 @@
 // first; meanwhile all threads take one sine and cosine per token and pair into shared memory,
 // and those of the cache's places are looked up.  Bound by memory: 4 x 4096 tokens of 32 heads of 128
 // elements, bf16, 268 MB, 0.041 ms = 6.5 TB/s; three axes, 28 heads, 117 MB, 0.0174 ms = 6.7 TB/s;
-// append of 16 x 2048 tokens, 32 query heads on 8, 755 MB, 0.127 ms = 5.9 TB/s.  Blocks of 256 threads:
-// 0.041, 0.0185, 0.141 ms; loads behind the angles: 0.047, 0.025, 0.160.
+// append of 16 x 2048 tokens, 32 query heads on 8, 755 MB, 0.1175 ms = 6.4 TB/s.  Blocks of 256 threads:
+// 0.041, 0.0185, 0.141 ms; loads behind the angles: 0.047, 0.025, 0.160.  The append's loads wait in shared
+// memory: in registers three heads of a thread were under way, and it took 0.127 ms; 3, 4, 5, 6, 8 and 10 heads there
+// 0.121, 0.123, 0.125, 0.1175, 0.1185, 0.125.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +30,7 @@ namespace rlk {
 
 constexpr int ROPE_THREADS = 128;
 // heads of a thread whose loads are under way together: alone, and in the append
-constexpr int ROPE_AHEAD = 4, APPEND_AHEAD = 3;
+constexpr int ROPE_AHEAD = 4, APPEND_AHEAD = 6;
 constexpr int ROPE_TOKENS = 8;           // of a block, at most
 
 struct Turns {
@@ -75,13 +77,10 @@ template <> struct Eight<float> {
     a = make_float4(v[0], v[1], v[2], v[3]);
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
-  __device__ __forceinline__ void fill(float x) { a = b = make_float4(x, x, x, x); }
 };
 struct Eight16 {
   uint4 w;
-  // (read once; but the append of 16 x 2048 tokens takes 0.132 ms with loads that leave the caches first, 0.127 without)
   __device__ __forceinline__ void load(const char* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void load_kept(const char* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint4*>(p) = w; }
 };
 template <> struct Eight<__nv_bfloat16> : Eight16 {
@@ -235,6 +234,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, sizeof(T) == 4 ? 4 : 6) rope_ker
 
 // ------------------------------------------------------------ append
 
+// 16 bytes on their way into shared memory, for the thread itself.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct AppendRopeParams {
   Turns t;
   PagedParams c;
@@ -244,8 +249,9 @@ struct AppendRopeParams {
 };
 
 template <class T>
-__global__ void __launch_bounds__(ROPE_THREADS, 8) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
-  __shared__ __align__(16) float cs[ROPE_TOKENS * RLK_ROPE_MAX_DIM];
+__global__ void __launch_bounds__(ROPE_THREADS, 7) append_rope_kernel(const __grid_constant__ AppendRopeParams P) {
+  __shared__ uint4 under_way[APPEND_AHEAD][2][ROPE_THREADS];       // each thread's own
+  __shared__ __align__(16) float cs[ROPE_TOKENS * 128];         // (a cache's heads have up to 128 elements)
   __shared__ int64_t place[ROPE_TOKENS];           // of the token's first head in the cache, in elements; -1: none
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.per;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(P.per), P.tokens - t0));
@@ -262,17 +268,16 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) append_rope_kernel(const __gr
   const int heads = h0 >= slots ? 0 : there ? P.q_heads + 2 * P.c.kv_heads : P.q_heads;
   const bool in_place = P.q.p == P.q_out.p;
   const int64_t lo_at = e.lo * static_cast<int64_t>(sizeof(T)), hi_at = e.hi * static_cast<int64_t>(sizeof(T));
-  Eight<T> lo[APPEND_AHEAD], hi[APPEND_AHEAD];
   auto load = [&](int h) {
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < APPEND_AHEAD; ++j) {
       const int g = h + j * slots;
       if (g >= heads || !there) continue;
       const int z = g < P.q_heads ? g : g < P.q_heads + P.c.kv_heads ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
       const HeadRows& r = g < P.q_heads ? P.q : g < P.q_heads + P.c.kv_heads ? P.k : P.v;
       const char* p = r.p + b * r.batch + i * r.token + z * r.head;
-      lo[j].load_kept(p + lo_at);
-      hi[j].load_kept(p + hi_at);
+      copy16(&under_way[j][0][threadIdx.x], p + lo_at);
+      copy16(&under_way[j][1][threadIdx.x], p + hi_at);
     }
   };
   load(h0);                              // (under way while places and angles are looked up)
@@ -297,17 +302,20 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) append_rope_kernel(const __gr
   if (e.turns && heads > 0) load_factors(P.t, cs, k, it, c, s);
   const int64_t to = place[k];
   for (int h = h0; h < heads;) {
-#pragma unroll
+    copies_wait();
+#pragma unroll 1
     for (int j = 0; j < APPEND_AHEAD; ++j) {
       const int g = h + j * slots;
-      if (g >= heads) continue;
+      if (g >= heads) break;
+      Eight<T> lo, hi;
+      if (there) lo.w = under_way[j][0][threadIdx.x], hi.w = under_way[j][1][threadIdx.x];
       char* dst;
       if (g < P.q_heads) {
         if (!there) {
-          lo[j].fill(fine ? 0.0f : __int_as_float(0x7fc00000));
-          hi[j] = lo[j];
+          lo.fill(fine ? 0.0f : __int_as_float(0x7fc00000));
+          hi = lo;
         } else if (e.turns) {
-          turn(lo[j], hi[j], c, s, P.t.interleaved);
+          turn(lo, hi, c, s, P.t.interleaved);
         } else if (in_place) {
           continue;
         }
@@ -316,11 +324,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 8) append_rope_kernel(const __gr
         if (to < 0) continue;
         const bool key = g < P.q_heads + P.c.kv_heads;
         const int z = key ? g - P.q_heads : g - P.q_heads - P.c.kv_heads;
-        if (key && e.turns) turn(lo[j], hi[j], c, s, P.t.interleaved);
+        if (key && e.turns) turn(lo, hi, c, s, P.t.interleaved);
         dst = static_cast<char*>(const_cast<void*>(key ? P.c.k : P.c.v)) + (to + z * P.c.head_stride) * static_cast<int64_t>(sizeof(T));
       }
-      lo[j].store(dst + lo_at);
-      hi[j].store(dst + hi_at);
+      lo.store(dst + lo_at);
+      hi.store(dst + hi_at);
     }
     h += slots * APPEND_AHEAD;
     load(h);
