@@ -1209,13 +1209,17 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     if B == 0 or n == 0 or q_heads == 0:
         return 0
     pieces = 0
-    for top in (min(max_shared, 1023), min(max_shared, 16383), max_shared) if groups else ():
-        pieces = max(pieces, -(-(top // 32 * 32) // (512 if top < 1024 else 1024 if top < 16384 else 2048)))
+    if groups:
+        pieces = -(-(min(max_shared, 1023) // 32 * 32) // 512)
+        if max_shared >= 1024:
+            pieces = max(pieces, -(-(min(max_shared, 16383) // 32 * 32) // 1024))
+        if max_shared >= 16384:
+            pieces = max(pieces, -(-(max_shared // 32 * 32) // 2048))
     tails = -(-max_tokens // 256) if max_tokens < 8192 else 32 if max_tokens <= 2**30 else 64
     rows = B * n * q_heads
-    return 128 + sum((x + 127) // 128 * 128 for x in (
-        4 * B, 4 * (B + 1), 16 * groups, 4 * groups, 4 * (groups + 3), 8 * rows * pieces, 8 * rows * tails,
-        4 * rows * pieces * head_dim, 4 * rows * tails * head_dim))
+    p, t, d = 4 * rows * pieces, 4 * rows * tails, head_dim         # (each part of it in whole lines)
+    return (128 + (4 * B + 127 & -128) + (4 * B + 131 & -128) + (16 * groups + 127 & -128) + (4 * groups + 127 & -128) +
+            (4 * groups + 139 & -128) + (2 * p + 127 & -128) + (2 * t + 127 & -128) + (p * d + 127 & -128) + (t * d + 127 & -128))
 
 
 def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_lens, *, new_lens=None, max_shared=None,
@@ -1241,10 +1245,13 @@ def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_
     B, dim, kv_heads = c.B, c.head_dim, c.kv_heads
     shape, dev = (B, n, heads, dim), k_cache.get_device()
     groups, tokens = shared_lens.shape[0] if shared_lens.dim() == 1 else -1, c.max_pages * c.page_size
-    for t, m, name in ((shared_lens, groups, "shared_lens"), (group_start, groups + 1, "group_start")):
-        if t.dtype != torch.int32 or t.shape != (m,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor: shared_lens [groups], group_start [groups + 1]")
-        _placed(t, dev, name)
+    i32 = torch.int32
+    if (shared_lens.dtype != i32 or groups < 0 or not shared_lens.is_contiguous() or
+            group_start.dtype != i32 or group_start.shape != (groups + 1,) or not group_start.is_contiguous()):
+        raise ValueError("shared_lens [groups] and group_start [groups + 1] must be contiguous int32 tensors")
+    if shared_lens.get_device() != dev or group_start.get_device() != dev:
+        _placed(shared_lens, dev, "shared_lens")
+        _placed(group_start, dev, "group_start")
     pg = PrefixGroups(group_start.data_ptr(), shared_lens.data_ptr(), groups, tokens if max_shared is None else max_shared)
     qs = _bth(q, shape, k_cache.dtype, "q", dev)
     new = torch.empty if stream is None else _maker(stream)
