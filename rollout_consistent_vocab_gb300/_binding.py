@@ -1215,11 +1215,12 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
             pieces = max(pieces, -(-(min(max_shared, 16383) // 32 * 32) // 1024))
         if max_shared >= 16384:
             pieces = max(pieces, -(-(max_shared // 32 * 32) // 2048))
-    tails = -(-max_tokens // 256) if max_tokens < 8192 else 32 if max_tokens <= 2**30 else 64
+    level = max(0, (max_tokens - 1).bit_length() - 14)
+    tails = (max_tokens - 1 >> 8 + level) + 32 * level + 1 if max_tokens else 0
     rows = B * n * q_heads
     p, t, d = 4 * rows * pieces, 4 * rows * tails, head_dim         # (each part of it in whole lines)
-    return (128 + (4 * B + 127 & -128) + (4 * B + 131 & -128) + (16 * groups + 127 & -128) + (4 * groups + 127 & -128) +
-            (4 * groups + 139 & -128) + (2 * p + 127 & -128) + (2 * t + 127 & -128) + (p * d + 127 & -128) + (t * d + 127 & -128))
+    return (128 + (4 * B + 127 & -128) + ((4 * B + 4) * (level + 1) + 127 & -128) + (16 * groups + 127 & -128) + (4 * groups + 127 & -128) +
+            (4 * groups + 143 & -128) + (2 * p + 127 & -128) + (2 * t + 127 & -128) + (p * d + 127 & -128) + (t * d + 127 & -128))
 
 
 def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_lens, *, new_lens=None, max_shared=None,

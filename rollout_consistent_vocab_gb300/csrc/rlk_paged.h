@@ -61,8 +61,9 @@ inline bool heads_first(const rlk_kv_cache* c) {
 rlk_status map_cache(CUtensorMap* map, const PagedParams& c, const void* base, int box, bool head_first, int panels, int D, bool bf16);
 
 // Attention over a shared prefix is taken in parts: of the shared tokens, that a group's
-// queries go over together, and of each sequence's other ones.  How they are cut goes by a
-// sequence's own lengths alone, so that its result does not depend on its batch.
+// queries go over together, and of each sequence's other ones.  How the shared ones are cut goes by
+// their number alone, and how the others are by nothing but how far behind them each is: a token's
+// result does not depend on its batch, nor on how many new tokens come with it.
 //
 // Tokens of a part of the shared ones: the fewer the longer, since a part costs as much as three tiles of
 // 128 tokens, and a write and a read of 128 tokens' size for 128 rows; but as many as there are SMs, for a
@@ -76,13 +77,31 @@ __host__ __device__ __forceinline__ int pieces_of(int shared) {
   const int t = piece_tokens(shared);
   return shared / t + (shared % t != 0);
 }
-// Tokens of a part of a sequence's other ones, at most TAIL_PARTS parts (from 2^30 tokens on, 2 TAIL_PARTS).
-constexpr int TAIL_PARTS = 32;
-__host__ __device__ __forceinline__ int tail_tokens(int tokens) {
-  int t = 256;
-  while (t < (1 << 25) && tokens > TAIL_PARTS * t) t *= 2;
-  return t;
+// The parts of a sequence's other tokens: 64 of 256 tokens, then 32 to each doubling (of 512 from token 16384 on,
+// of 1024 from 32768 on).  (Lengths that went by the number of all tokens made a token's bits depend on the
+// drafts behind it.)  With half as many of twice the length from token 8192 on, 2 sequences of 500,000 tokens took
+// 992 us for 710, 1 of 16,000 53 for 42; 64 of 16,000 672 for 684, whose results are half as many.
+constexpr int TAIL_PART = 256;
+__host__ __device__ __forceinline__ int tail_level(int64_t token) {    // parts are TAIL_PART << level tokens
+  int level = 0;
+  while (token >> (13 + level) > 1) ++level;
+  return level;
 }
+__host__ __device__ __forceinline__ int tail_part_of(int64_t token) {
+  const int level = tail_level(token);
+  return static_cast<int>(token >> (8 + level)) + 32 * level;
+}
+__host__ __device__ __forceinline__ int tail_parts(int64_t tokens) { return tokens > 0 ? tail_part_of(tokens - 1) + 1 : 0; }
+__host__ __device__ __forceinline__ int tail_part_level(int part) { return part < 64 ? 0 : part / 32 - 1; }
+__host__ __device__ __forceinline__ int tail_part_from(int part) {
+  const int level = tail_part_level(part);
+  return (part - 32 * level) << (8 + level);
+}
+__host__ __device__ __forceinline__ int tail_part_tokens(int part) { return TAIL_PART << tail_part_level(part); }
+// The parts of one length: the first of them, the token that it begins with, and the tokens of all.
+__host__ __device__ __forceinline__ int tail_level_part(int level) { return level == 0 ? 0 : 32 + 32 * level; }
+__host__ __device__ __forceinline__ int tail_level_from(int level) { return level == 0 ? 0 : 8192 << level; }
+__host__ __device__ __forceinline__ int tail_level_tokens(int level) { return level == 0 ? 16384 : 8192 << level; }
 // Their query rows go in tiles of 8 nt: as few as hold the rows in 24 each, then as narrow as they can be.
 struct TailTiles { int tiles, nt; };
 inline TailTiles tail_tiles(int rows) {
@@ -104,8 +123,9 @@ struct PrefixParts {
   bool head_first;              // the tensor maps' second place is the head, not the token
   float* lse;
   const int32_t* first;         // [B] tokens of the sequence that are taken as shared, a multiple of 32; -1: rejected
-  const uint32_t* tail_base;    // [B + 1] steps of 16 other tokens (of a kv head) before each sequence
-  uint32_t* taken;              // chunks of those steps that warps have taken
+  // By the length of their parts, the level: steps of 16 other tokens (of a kv head) before each sequence
+  const uint32_t* tail_base;    // [levels][B + 1]
+  uint32_t* taken;              // chunks of those steps that warps have taken; then the highest level that there is
   float2* piece_ml;             // [B][kv_heads][pieces][rows]: maximum (base 2), sum
   float* piece_o;               // ... and the weighted sum of values [B][kv_heads][pieces][head_dim / 8][rows][8]: a warp with a
                                 // thread to a row has few lines to write at a time

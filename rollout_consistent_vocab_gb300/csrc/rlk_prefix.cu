@@ -37,7 +37,7 @@ struct PrefixParams : PrefixParts {
   uint32_t* plan_tails;
   GroupPlan* plan;              // [groups]
   int32_t* busy;                // [groups] whether a sequence has new tokens
-  uint32_t* base;               // units of work before each of [groups + 1], then the CTAs that share them
+  uint32_t* base;               // units of work before each of [groups + 1], then the CTAs that share them (and `taken`)
   uint32_t unit_cost, tail_cost;         // of a unit, and of 16 own tokens of a sequence
   int box;                      // tokens of a copy: the largest power of 2, up to 64, that divides page_size
   bool merged;                  // a copy takes all 128 elements of its tokens (64 of them)
@@ -94,6 +94,7 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t mine, uint32_t* scan) {
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P) {
   __shared__ int32_t near_start[PLAN_GROUPS + 1], near_shared[PLAN_GROUPS], near_busy[PLAN_GROUPS];
   __shared__ uint32_t scan[PLAN_THREADS / 32];
+  __shared__ int most_own;               // tokens behind the shared ones, of the sequence with the most
   const int tid = threadIdx.x, G = P.groups;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t tokens = static_cast<int64_t>(P.c.max_pages) * P.c.page_size;
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
   const int32_t* const shared = near ? near_shared : P.shared_lens;
   int32_t* const busy = near ? near_busy : P.busy;
   bool fault = false;
+  if (tid == 0) most_own = 0;
   for (int g = tid; g < G; g += PLAN_THREADS) {
     const int a = P.group_start[g], e = P.group_start[g + 1];
     fault |= a < 0 || e < a || e > P.B;
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
           if (nnew > 0 && first > 0) busy[lo] = 1;
         }
       }
+      if (first >= 0 && nnew > 0) atomicMax(&most_own, len - first);
     }
     P.plan_first[b] = first;
   }
@@ -156,27 +159,35 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
   }
   const uint32_t units = run;            // (of the last thread: all)
   if (tid == PLAN_THREADS - 1) P.base[G] = run;
-  // the steps of 16 tokens that the sequences have behind the shared ones
+  // the steps of 16 tokens that the sequences have behind the shared ones, by the length of their parts
   const int seqs = static_cast<int>((P.B + PLAN_THREADS - 1) / PLAN_THREADS);
   const int b0 = static_cast<int>(min(P.B, static_cast<int64_t>(tid) * seqs)), b1 = static_cast<int>(min(P.B, static_cast<int64_t>(b0) + seqs));
-  auto steps = [&](int b) {
+  auto steps = [&](int b, int level) {
     const int first = P.plan_first[b];
     int len, nnew;
-    return first >= 0 && seq_lens(P.c, b, len, nnew) && nnew > 0 && len > first ? (static_cast<uint32_t>(len - first) + 15u) / 16u : 0u;
+    if (first < 0 || !seq_lens(P.c, b, len, nnew) || nnew == 0) return 0u;
+    const int in = min(len - first - tail_level_from(level), tail_level_tokens(level));
+    return in > 0 ? (static_cast<uint32_t>(in) + 15u) / 16u : 0u;
   };
-  mine = 0;
-  for (int b = b0; b < b1; ++b) mine += steps(b);
-  run = sum_before(mine, scan);
-  for (int b = b0; b < b1; ++b) {
-    P.plan_tails[b] = run;
-    run += steps(b);
+  const int top = tail_level(max(most_own, 1) - 1);
+  uint32_t own_steps = 0;                // (of the last thread)
+  for (int level = 0; level <= top; ++level) {
+    uint32_t* const base = P.plan_tails + level * (P.B + 1);
+    mine = 0;
+    for (int b = b0; b < b1; ++b) mine += steps(b, level);
+    run = sum_before(mine, scan);
+    for (int b = b0; b < b1; ++b) {
+      base[b] = run;
+      run += steps(b, level);
+    }
+    if (tid == PLAN_THREADS - 1) base[P.B] = run;
+    own_steps += run;
   }
   if (tid == PLAN_THREADS - 1) {
-    P.plan_tails[P.B] = run;
     // Shared tokens keep the tensor cores and exponentials busy, the others memory: the SMs are shared out
     // by the work that they are, so that both go on side by side to the end (16 groups of 16 samples took
     // 177 us one after the other).  Runs are of pairs of units, for the two streams.
-    const uint64_t of_shared = static_cast<uint64_t>(units) * P.unit_cost, of_all = of_shared + static_cast<uint64_t>(run) * P.tail_cost;
+    const uint64_t of_shared = static_cast<uint64_t>(units) * P.unit_cost, of_all = of_shared + static_cast<uint64_t>(own_steps) * P.tail_cost;
     uint32_t ctas = static_cast<uint32_t>((PSMS * of_shared + of_all) / (of_all + 1));
     ctas = max(1u, min(ctas, static_cast<uint32_t>(PSMS)));
     if (units > ctas) {
@@ -184,7 +195,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
       ctas = (units + per - 1) / per;
     }
     P.base[G + 1] = max(1u, min(units, ctas));
-    *P.taken = 0u;
+    P.taken[0] = 0u;
+    P.taken[1] = static_cast<uint32_t>(top);
   }
 }
 
@@ -947,7 +959,7 @@ static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t
     y.pieces = pieces > y.pieces ? pieces : y.pieces;
   }
   if (groups == 0) y.pieces = 0;
-  y.tails = static_cast<int>(max_tokens >= TAIL_PARTS * 256 ? max_tokens > (int64_t(1) << 30) ? 2 * TAIL_PARTS : TAIL_PARTS : (max_tokens + 255) / 256);
+  y.tails = tail_parts(max_tokens);
   const size_t rows = static_cast<size_t>(B) * n * q_heads, pieces = rows * y.pieces, tails = rows * y.tails;
   size_t at = 0;
   auto next = [&](size_t bytes) {
@@ -956,10 +968,10 @@ static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t
     return here;
   };
   y.first = next(static_cast<size_t>(B) * 4);
-  y.tails_at = next(static_cast<size_t>(B + 1) * 4);
+  y.tails_at = next(static_cast<size_t>(B + 1) * 4 * (tail_level(max_tokens > 0 ? max_tokens - 1 : 0) + 1));
   y.plan = next(static_cast<size_t>(groups) * sizeof(GroupPlan));
   y.busy = next(static_cast<size_t>(groups) * 4);
-  y.base = next((static_cast<size_t>(groups) + 3) * 4);
+  y.base = next((static_cast<size_t>(groups) + 4) * 4);
   y.piece_ml = next(pieces * 8);
   y.tail_ml = next(tails * 8);
   y.piece_o = next(pieces * head_dim * 4);
