@@ -1220,7 +1220,7 @@ def prefix_attention_workspace_bytes(B: int, n: int, q_heads: int, kv_heads: int
     rows = B * n * q_heads
     p, t, d = 4 * rows * pieces, 4 * rows * tails, head_dim         # (each part of it in whole lines)
     return (128 + (4 * B + 127 & -128) + ((4 * B + 4) * (level + 1) + 127 & -128) + (16 * groups + 127 & -128) + (4 * groups + 127 & -128) +
-            (4 * groups + 143 & -128) + (2 * p + 127 & -128) + (2 * t + 127 & -128) + (p * d + 127 & -128) + (t * d + 127 & -128))
+            (4 * groups + 147 & -128) + (2 * p + 127 & -128) + (2 * t + 127 & -128) + (p * d + 127 & -128) + (t * d + 127 & -128))
 
 
 def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_lens, *, new_lens=None, max_shared=None,

@@ -82,16 +82,16 @@ __host__ __device__ __forceinline__ int pieces_of(int shared) {
 // drafts behind it.)  With half as many of twice the length from token 8192 on, 2 sequences of 500,000 tokens took
 // 992 us for 710, 1 of 16,000 53 for 42; 64 of 16,000 672 for 684, whose results are half as many.
 constexpr int TAIL_PART = 256;
-__host__ __device__ __forceinline__ int tail_level(int64_t token) {    // parts are TAIL_PART << level tokens
+__host__ __device__ __forceinline__ int tail_level(int token) {        // parts are TAIL_PART << level tokens
   int level = 0;
   while (token >> (13 + level) > 1) ++level;
   return level;
 }
-__host__ __device__ __forceinline__ int tail_part_of(int64_t token) {
+__host__ __device__ __forceinline__ int tail_part_of(int token) {
   const int level = tail_level(token);
-  return static_cast<int>(token >> (8 + level)) + 32 * level;
+  return (token >> (8 + level)) + 32 * level;
 }
-__host__ __device__ __forceinline__ int tail_parts(int64_t tokens) { return tokens > 0 ? tail_part_of(tokens - 1) + 1 : 0; }
+__host__ __device__ __forceinline__ int tail_parts(int tokens) { return tokens > 0 ? tail_part_of(tokens - 1) + 1 : 0; }
 __host__ __device__ __forceinline__ int tail_part_level(int part) { return part < 64 ? 0 : part / 32 - 1; }
 __host__ __device__ __forceinline__ int tail_part_from(int part) {
   const int level = tail_part_level(part);
@@ -125,7 +125,7 @@ struct PrefixParts {
   const int32_t* first;         // [B] tokens of the sequence that are taken as shared, a multiple of 32; -1: rejected
   // By the length of their parts, the level: steps of 16 other tokens (of a kv head) before each sequence
   const uint32_t* tail_base;    // [levels][B + 1]
-  uint32_t* taken;              // chunks of those steps that warps have taken; then the highest level that there is
+  uint32_t* taken;              // chunks of those steps that warps have taken; then the highest level that there is, and all steps
   float2* piece_ml;             // [B][kv_heads][pieces][rows]: maximum (base 2), sum
   float* piece_o;               // ... and the weighted sum of values [B][kv_heads][pieces][head_dim / 8][rows][8]: a warp with a
                                 // thread to a row has few lines to write at a time

@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PrefixParams P
     P.base[G + 1] = max(1u, min(units, ctas));
     P.taken[0] = 0u;
     P.taken[1] = static_cast<uint32_t>(top);
+    P.taken[2] = own_steps;
   }
 }
 
@@ -959,7 +960,8 @@ static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t
     y.pieces = pieces > y.pieces ? pieces : y.pieces;
   }
   if (groups == 0) y.pieces = 0;
-  y.tails = tail_parts(max_tokens);
+  const int tokens = static_cast<int>(max_tokens < 0x7fffffff ? max_tokens : 0x7fffffff);
+  y.tails = tail_parts(tokens);
   const size_t rows = static_cast<size_t>(B) * n * q_heads, pieces = rows * y.pieces, tails = rows * y.tails;
   size_t at = 0;
   auto next = [&](size_t bytes) {
@@ -968,10 +970,10 @@ static PrefixLayout prefix_layout(int64_t B, int64_t n, int64_t q_heads, int64_t
     return here;
   };
   y.first = next(static_cast<size_t>(B) * 4);
-  y.tails_at = next(static_cast<size_t>(B + 1) * 4 * (tail_level(max_tokens > 0 ? max_tokens - 1 : 0) + 1));
+  y.tails_at = next(static_cast<size_t>(B + 1) * 4 * (tail_level(tokens > 0 ? tokens - 1 : 0) + 1));
   y.plan = next(static_cast<size_t>(groups) * sizeof(GroupPlan));
   y.busy = next(static_cast<size_t>(groups) * 4);
-  y.base = next((static_cast<size_t>(groups) + 4) * 4);
+  y.base = next((static_cast<size_t>(groups) + 5) * 4);
   y.piece_ml = next(pieces * 8);
   y.tail_ml = next(tails * 8);
   y.piece_o = next(pieces * head_dim * 4);

@@ -55,30 +55,28 @@ struct TailMaps { CUtensorMap k, v; };
 struct TailPlace {
   int b, ht, part, t, end;
   int len, nnew, first;         // of the sequence: its lengths, where its own tokens begin
-  int level, stop;              // the level of the parts, where the sequence's last of it ends
-  int64_t left;                 // steps of the chunk from this part's begin on (the part is the chunk's if there are any)
+  int left;                     // steps of the chunk from this part's begin on (the part is the chunk's if there are any)
   __device__ __forceinline__ void load(const PrefixParts& P) {
     nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n;
     first = P.first[b];
     // (within bounds, should the lengths have changed since they were looked over)
     len = max(first, min(P.c.lens[b], static_cast<int>(min(static_cast<int64_t>(P.c.max_pages) * P.c.page_size, static_cast<int64_t>(0x7fffffff)))));
-    const int in = len - first - tail_level_from(level);
-    stop = in > tail_level_tokens(level) ? len - in + tail_level_tokens(level) : len;
   }
-  __device__ __forceinline__ int from() const { return first + tail_part_from(part); }
-  __device__ __forceinline__ void cut() {
-    t = from();
+  __device__ __forceinline__ void cut(int from) {
+    t = from;
     end = min(len, t + min(tail_part_tokens(part), len - t));
   }
 };
 
-// The next part; false at the chunk's end.  The longest parts come first, so that none is begun when the others end
-// (4 sequences of 100,000 tokens, parts of up to 4096 tokens: 380 us in the order of their places, 327 so).
+// The next part; false at the chunk's end.  The longest parts come first,
+// so that none is begun when the others end (4 sequences of 100,000 tokens, parts of up to 4096 tokens: 380 us in the
+// order of their places, 327 so).
 __device__ __forceinline__ bool next_part(const TailParams& P, TailPlace& x, int HT) {
   do {
-    x.left -= (x.end - x.from() + TSTEP - 1) / TSTEP;
+    x.left -= (x.end - x.first - tail_part_from(x.part) + TSTEP - 1) / TSTEP;
     if (x.left <= 0) return false;
-    if (x.end < x.stop) {
+    int level = tail_part_level(x.part), from = x.end;
+    if (x.end < x.len && tail_part_level(x.part + 1) == level) {
       ++x.part;
     } else {
       if (++x.ht == HT) {
@@ -86,17 +84,18 @@ __device__ __forceinline__ bool next_part(const TailParams& P, TailPlace& x, int
         const uint32_t* base;
         do {
           if (++x.b >= P.p.B) {
-            if (x.level == 0) return false;
-            --x.level;
+            if (level == 0) return false;
+            --level;
             x.b = 0;
           }
-          base = P.p.tail_base + x.level * (P.p.B + 1) + x.b;
+          base = P.p.tail_base + level * (P.p.B + 1) + x.b;
         } while (base[1] == base[0]);
         x.load(P.p);
       }
-      x.part = tail_level_part(x.level);
+      x.part = tail_level_part(level);
+      from = x.first + tail_level_from(level);
     }
-    x.cut();
+    x.cut(from);
   } while (x.t >= x.end);                // (only should the lengths have changed)
   return true;
 }
@@ -123,25 +122,23 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
   __syncwarp();
 
   const int HT = P.p.c.kv_heads * P.tiles;
-  const int top = static_cast<int>(P.p.taken[1]);
-  int64_t total = 0;
-  for (int level = 0; level <= top; ++level) total += P.p.tail_base[level * (P.p.B + 1) + P.p.B];
-  total *= HT;
   // A chunk: a quarter of an equal share (half of one is slower by a twentieth, an eighth no faster), but a
   // part's 16 steps where that is less, and a share where there are not so many.
-  const int64_t each = total / (TSMS * TWARPS);
-  const int64_t chunk = max(each / 4, min(max(each, static_cast<int64_t>(1)), static_cast<int64_t>(256 / TSTEP)));
+  const int64_t each = static_cast<int64_t>(P.p.taken[2]) * HT / (TSMS * TWARPS);
+  const int chunk = static_cast<int>(min(max(each / 4, min(max(each, static_cast<int64_t>(1)), static_cast<int64_t>(256 / TSTEP))), static_cast<int64_t>(1) << 29));
   TailPlace load_at, work_at;
   bool have = false;
   // ---- the next chunk of all steps that no warp has: the parts that begin there.  False where none is left.
   auto take = [&]() {
     uint32_t k = 0;
+    // (looked up while the counter is; they would be in the products' way)
+    int level = static_cast<int>(P.p.taken[1]);
+    const uint32_t all = P.p.taken[2];
     if (lane == 0) k = atomicAdd(P.p.taken, 1u);
-    const int64_t from = __shfl_sync(0xffffffffu, k, 0) * chunk, to = min(total, from + chunk);
+    const int64_t from = static_cast<int64_t>(__shfl_sync(0xffffffffu, k, 0)) * chunk, to = min(static_cast<int64_t>(all) * HT, from + chunk);
     if (from >= to) return false;
     // the last sequence that begins at or before it
     int64_t rest = from;
-    int level = top;
     const uint32_t* base = P.p.tail_base + level * (P.p.B + 1);
     for (; level > 0 && rest >= static_cast<int64_t>(base[P.p.B]) * HT; --level, base -= P.p.B + 1) rest -= static_cast<int64_t>(base[P.p.B]) * HT;
     const uint32_t at = static_cast<uint32_t>(rest / HT);
@@ -154,17 +151,16 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
     }
     TailPlace x;
     x.b = lo;
-    x.level = level;
     x.load(P.p);
     const int64_t steps = base[lo + 1] - base[lo];
     rest -= static_cast<int64_t>(base[lo]) * HT;
     x.ht = static_cast<int>(min(rest / max(steps, static_cast<int64_t>(1)), static_cast<int64_t>(HT - 1)));
     const int64_t in = rest - x.ht * steps + tail_level_from(level) / TSTEP;
     // (within its tokens, should the lengths have changed)
-    x.part = tail_part_of(min(in * TSTEP, static_cast<int64_t>(max(x.len - x.first, 1) - 1)));
-    const int64_t over = in - tail_part_from(x.part) / TSTEP;
-    x.left = to - from + over;           // (from where the part begins that holds the chunk's first step)
-    x.cut();
+    x.part = tail_part_of(static_cast<int>(min(in * TSTEP, static_cast<int64_t>(max(x.len - x.first, 1) - 1))));
+    const int over = static_cast<int>(in - tail_part_from(x.part) / TSTEP);
+    x.left = static_cast<int>(to - from) + over;           // (from where the part begins that holds the chunk's first step)
+    x.cut(x.first + tail_part_from(x.part));
     have = over > 0 || x.t >= x.end ? next_part(P, x, HT) : true;
     work_at = load_at = x;
     return true;
