@@ -3,7 +3,8 @@
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn a position, so that
 // position * frequency in 64-bit arithmetic is the angle modulo a turn, exact
-// but for the frequency's own rounding (2^-53 of it) whatever the position.  Its upper
+// but for the frequency's own rounding (2^-52 of it: a rounded constant and a rounded product;
+// a negative one is the positive one's complement) whatever the position.  Its upper
 // 32 bits, taken to the nearest quarter turn, leave at most an eighth: sine and
 // cosine of that, to float32's accuracy, then the quarters by exchange and sign.
 //
@@ -350,10 +351,11 @@ static rlk_status make_turns(const rlk_rope_args* r, int dim, int64_t B, int64_t
   if (!aligned(r->positions, 4)) return fail(RLK_EALIGN, "positions is not 4-byte aligned");
   t->pairs = r->rot_dim / 2;
   for (int j = 0; j < t->pairs; ++j) {
-    const double f = r->inv_freq[j] * 0.15915494309189535;     // 1 / (2 pi)
+    const double f = fabs(r->inv_freq[j]) * 0.15915494309189535;         // 1 / (2 pi)
     if (!isfinite(f)) return fail(RLK_EINVAL, "inv_freq[%d] must be finite", j);
-    const double part = f - floor(f);                          // in [0, 1]: 1 where a tiny negative f is rounded
-    t->turn[j] = part >= 1.0 ? 0ull : static_cast<unsigned long long>(part * 18446744073709551616.0);
+    // (exact, in [0, 1); a small negative one's fraction would be a rounded number next to 1)
+    const unsigned long long part = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
+    t->turn[j] = r->inv_freq[j] < 0.0 ? 0ull - part : part;
     t->axis[j] = r->pair_axis ? r->pair_axis[j] : 0;
     if (t->axis[j] >= r->axes) return fail(RLK_EINVAL, "pair_axis[%d] = %d must be below axes %d", j, t->axis[j], r->axes);
   }

@@ -24,7 +24,5 @@ def test_small_negative_frequencies_at_far_positions():
     x = rand((1, 8, 3, 64), "f32", 21)
     for first, last in ((-1.0, -3.0), (-3.0, -6.0), (-6.0, -12.0)):
         freq = -torch.logspace(first, last, 32, dtype=torch.float64)
-        got = pkg.rope(x, freq, pos)
-        compare(got, x, freq, pos, "f32")
-        # a turn by -f is the turn back by f
-        assert torch.equal(got, pkg.rope(x, -freq, pos, inverse=True))
+        compare(pkg.rope(x, freq, pos), x, freq, pos, "f32")
+        compare(pkg.rope(x, freq, pos, inverse=True), x, freq, pos, "f32", inverse=True)
