@@ -186,7 +186,8 @@ typedef struct rlk_prefix_groups {
  * lens[b] - new_lens[b] < shared_lens[g] is rejected, and so are all of a group
  * whose shared length is out of range, and all of a call whose group_start is at
  * fault (NaN for all their places, as in rlk_paged_attention, *err_count raised).
- * A shared token's page number out of range rejects the group's new tokens.
+ * A shared token's page number out of range rejects all of the group's sequences
+ * with new tokens; each is counted.
  * A sequence's result depends on its own tokens and its shared length, not on
  * what else is in its group or the batch (the bits are not rlk_paged_attention's:
  * its tokens are cut otherwise).

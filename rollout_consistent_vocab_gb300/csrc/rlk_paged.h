@@ -135,6 +135,10 @@ struct PrefixParts {
   int tails;
 };
 
+// What is written of a part with a page that is not there: a sum that stays NaN, and a maximum that
+// no other part has.
+__device__ __forceinline__ float2 bad_part() { return make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)); }
+
 // The sequences' other tokens, and the join of all parts; the launches follow the shared tokens'
 // kernel, or where there is none (`alone`) the plan's.
 rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool alone, cudaStream_t stream);

@@ -874,7 +874,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
         bad |= !result_in(total - 1) || *dead != 0u;
         bad = __any_sync(0xffffffffu, bad);
         tc_fence_after();
-        if (bad && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);
+        if (*dead && (warp & 3) == 0 && lane == 0 && P.c.err) atomicAdd(P.c.err, 1);         // (missing pages are the join's to count)
         const int64_t step = 8 * static_cast<int64_t>(P.rows);
         float* const to = P.piece_o + slot_at * D + 8 * static_cast<int64_t>(r);
 #pragma unroll 1
@@ -893,7 +893,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
           }
           __syncwarp();
         }
-        if (query) P.piece_ml[slot_at + r] = bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m, l * W::TO_PIECES);
+        if (query) P.piece_ml[slot_at + r] = bad ? bad_part() : make_float2(m, l * W::TO_PIECES);
         bad = bad_next;
       } else {
         more = way.next(P, nxt);

@@ -398,7 +398,7 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
         __syncwarp();                      // the stage may be filled again
       }
       // ---- the part's result
-      if (part_bad && lane == 0 && P.p.c.err) atomicAdd(P.p.c.err, 1);
+      if (dead && lane == 0 && P.p.c.err) atomicAdd(P.p.c.err, 1);         // (missing pages are the join's to count)
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -416,7 +416,7 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMa
             dst[2 * d * chunk8] = o[x][d][e];
             dst[(2 * d + 1) * chunk8] = o[x][d][2 + e];
           }
-          if (g8 == 0) P.p.tail_ml[slot + row] = part_bad ? make_float2(0.0f, __int_as_float(0x7fc00000)) : make_float2(m[x][e], sum);
+          if (g8 == 0) P.p.tail_ml[slot + row] = part_bad ? bad_part() : make_float2(m[x][e], sum);
         }
       have = next_part(P, work_at, HT);
     }
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(TJOIN, AT_ONCE == 2 ? 4 : 2) tail_join_kernel(
   const int first = P.first[b], nnew = P.c.new_lens ? P.c.new_lens[b] : P.c.n, own = P.c.lens[b] - first;
   const bool ok = first >= 0, query = ok && i < nnew;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!ok && in == 0 && head == 0 && P.c.err) atomicAdd(P.c.err, 1);
   JoinRow<128> chain[2];
+  bool bad = !ok;
   if (query) {
     const int pieces = min(pieces_of(first), P.pieces), parts = pieces + min(tail_parts(own), P.tails);
     const int64_t shared = bh * P.pieces, tails = bh * P.tails - pieces;
@@ -473,10 +473,11 @@ __global__ void __launch_bounds__(TJOIN, AT_ONCE == 2 ? 4 : 2) tail_join_kernel(
       }
 #pragma unroll
       for (int k = 0; k < AT_ONCE; ++k)
-        if (p0 + k < parts) chain[k % 2].add(h[k].x, h[k].y, v[k]);
+        if (p0 + k < parts) chain[k % 2].add(h[k].x, h[k].y, v[k]), bad |= h[k].x != h[k].x;
     }
     chain[0].add(chain[1]);
   }
+  if (bad && in == 0 && head == 0 && P.c.err) atomicAdd(P.c.err, 1);       // a rejected sequence, once
   const JoinRow<128>& all = chain[0];
   const float inv = all.L == 0.0f ? 0.0f : __frcp_rn(all.L), nan = __int_as_float(0x7fc00000);
   const int hq = head * P.group + (row - i * P.group);

@@ -36,3 +36,31 @@ def test_drafted_tokens_have_the_bits_of_single_ones_where_parts_grow(dtype, dim
     # the first three alone, in a call with room for five
     o, z = run(dict(c, lens=c["lens"] - 2), [3] * len(OWN))
     assert torch.equal(bits(o[:, :3]), bits(out[:, :3])) and torch.equal(bits(z[:, :3]), bits(lse[:, :3]))
+
+
+def test_every_sequence_that_a_missing_page_rejects_is_counted():
+    c = make([(20, 64), (3, 64)], [9] * 24, 1, 1, 1, 64, 16, "bf16", seed=42)
+    err, pages = i32([0]), c["k"].shape[0]
+
+    def count(d, new=None):
+        err.zero_()
+        out, lse = run(d, new, err_count=err)
+        nan = torch.isnan(out).flatten(1).all(1)
+        assert torch.equal(nan, torch.isnan(lse).flatten(1).all(1)) and torch.equal(nan, torch.isnan(out).flatten(1).any(1))
+        return int(err), int(nan.sum())
+
+    assert count(c) == (0, 0)
+    for page in (-1, pages, 2**31 - 1):
+        table = c["table"].clone()
+        table[0, 1] = page                                       # a shared one
+        raised, rejected = count(dict(c, table=table))
+        assert rejected == 20 and raised >= 20
+        table = c["table"].clone()
+        table[21, 4] = table[23, 0] = page                       # own ones
+        raised, rejected = count(dict(c, table=table))
+        assert rejected == 2 and raised >= 2
+    # sequences without new tokens have nothing to reject
+    table = c["table"].clone()
+    table[0, 1] = -1
+    raised, rejected = count(dict(c, table=table), [1 if b % 2 else 0 for b in range(24)])
+    assert rejected == 10 and raised >= 10
