@@ -139,9 +139,11 @@ struct PrefixParts {
 // no other part has.
 __device__ __forceinline__ float2 bad_part() { return make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)); }
 
-// The sequences' other tokens, and the join of all parts; the launches follow the shared tokens'
-// kernel, or where there is none (`alone`) the plan's.
-rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool alone, cudaStream_t stream);
+// The sequences' other tokens, and the join of all parts.  What can be refused is looked at before anything is
+// launched (`prepare`); the launches follow the shared tokens' kernel, or where there is none (`alone`) the plan's.
+struct CacheMaps { CUtensorMap k, v; };
+enum class Tails { prepare, beside, alone };
+rlk_status attend_tails(const PrefixParts& parts, CacheMaps& maps, int head_dim, bool bf16, Tails what, cudaStream_t stream);
 
 rlk_status check_cache(const rlk_kv_cache* c);
 rlk_status check_bth(const void* p, const rlk_bth_strides* s, const char* what);

@@ -282,7 +282,6 @@ struct PShape {
   static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BARS * 8 + 16;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
-struct PrefixMaps { CUtensorMap k, v; };
 
 // The units in equal runs, the first ones one longer (the CTAs without one make room at once).  An item is the CTA's whose run holds its first unit.
 __device__ __forceinline__ uint32_t run_start(uint32_t units, uint32_t workers, uint32_t k) {
@@ -501,7 +500,7 @@ __device__ __forceinline__ void store8(float* p, const uint32_t* r) {
 
 template <class T, int D>
 __global__ void __launch_bounds__(PTHREADS, 1)
-prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ PrefixMaps maps) {
+prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ CacheMaps maps) {
   using S_ = PShape<D>;
   using W = Weights<T>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -913,23 +912,29 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Pr
 
 // ------------------------------------------------------------ host side
 
+// The four launches, with all that can be refused before the first of them.
 template <class T, int D>
-static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cudaStream_t st) {
+static rlk_status launch_prefix(const PrefixParams& P, bool bf16, cudaStream_t st) {
   static bool done[64] = {};
+  const bool shared = P.pieces > 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
+  if (e == cudaSuccess && shared && (dev >= 64 || !done[dev])) {
     e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PShape<D>::SMEM);
     if (e == cudaSuccess && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return fail(RLK_ECUDA, "function attributes: %s", cudaGetErrorString(e));
-  PrefixMaps maps{};
+  CacheMaps maps{}, tail_maps{};
   rlk_status s;
-  if (P.c.num_pages > 0) {
-    const bool bf = cache->dtype == RLK_DT_BF16;
-    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, P.merged ? 2 : 1, D, bf)) != RLK_OK) return s;
-    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, P.merged ? 2 : 1, D, bf)) != RLK_OK) return s;
+  if (shared && P.c.num_pages > 0) {
+    if ((s = map_cache(&maps.k, P.c, P.c.k, P.box, P.head_first, P.merged ? 2 : 1, D, bf16)) != RLK_OK) return s;
+    if ((s = map_cache(&maps.v, P.c, P.c.v, P.box, P.head_first, P.merged ? 2 : 1, D, bf16)) != RLK_OK) return s;
   }
+  if ((s = attend_tails(P, tail_maps, D, bf16, Tails::prepare, st)) != RLK_OK) return s;
+  plan_kernel<<<1, PLAN_THREADS, 0, st>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
+  if (!shared) return attend_tails(P, tail_maps, D, bf16, Tails::alone, st);
   // launched while the plan is made, for which it waits
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(PSMS);
@@ -943,7 +948,7 @@ static rlk_status launch_prefix(PrefixParams& P, const rlk_kv_cache* cache, cuda
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, prefix_kernel<T, D>, P, maps);
   if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  return RLK_OK;
+  return attend_tails(P, tail_maps, D, bf16, Tails::beside, st);
 }
 
 static size_t lined(size_t x) { return (x + 127) / 128 * 128; }
@@ -1071,15 +1076,8 @@ rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_grou
   P.page_magic = page_magic(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == RLK_DT_BF16;
-  plan_kernel<<<1, PLAN_THREADS, 0, st>>>(P);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(RLK_ECUDA, "kernel launch: %s", cudaGetErrorString(e));
-  if (y.pieces > 0) {
-    if (cache->head_dim == 128) s = bf ? launch_prefix<bf16_t, 128>(P, cache, st) : launch_prefix<__half, 128>(P, cache, st);
-    else s = bf ? launch_prefix<bf16_t, 64>(P, cache, st) : launch_prefix<__half, 64>(P, cache, st);
-    if (s != RLK_OK) return s;
-  }
-  return attend_tails(P, cache->head_dim, bf, y.pieces == 0, st);
+  if (cache->head_dim == 128) return bf ? launch_prefix<bf16_t, 128>(P, bf, st) : launch_prefix<__half, 128>(P, bf, st);
+  return bf ? launch_prefix<bf16_t, 64>(P, bf, st) : launch_prefix<__half, 64>(P, bf, st);
 }
 
 }  // extern "C"

@@ -49,7 +49,6 @@ struct TailParams {
   int tiles, box;               // row tiles of 8 NT rows; tokens of a copy: the largest power of 2, up to 16, in a page
   bool merged;                  // a copy takes all 128 elements of its 16 tokens
 };
-struct TailMaps { CUtensorMap k, v; };
 
 // A place in a warp's chunk: a part of a sequence, kv head and row tile, tokens t .. end - 1.
 struct TailPlace {
@@ -104,7 +103,7 @@ __device__ __forceinline__ int row_query(const PrefixParts& P, int row) { return
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(TWARPS * 32, 1)
-tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ TailMaps maps) {
+tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ CacheMaps maps) {
   using S_ = TShape<D>;
   using E = Elem<T>;
   constexpr int KK = D / 16, DT = D / 16;
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(TJOIN, AT_ONCE == 2 ? 4 : 2) tail_join_kernel(
 // ------------------------------------------------------------ host side
 
 template <class T, int D, int NT>
-static rlk_status launch_tails(const TailParams& P, const TailMaps& maps, bool alone, cudaStream_t st) {
+static rlk_status launch_tails(const TailParams& P, const CacheMaps& maps, Tails what, cudaStream_t st) {
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -502,6 +501,7 @@ static rlk_status launch_tails(const TailParams& P, const TailMaps& maps, bool a
     if (e == cudaSuccess && dev < 64) done[dev] = true;
   }
   if (e != cudaSuccess) return fail(RLK_ECUDA, "function attributes: %s", cudaGetErrorString(e));
+  if (what == Tails::prepare) return RLK_OK;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -512,7 +512,7 @@ static rlk_status launch_tails(const TailParams& P, const TailMaps& maps, bool a
   cfg.stream = st;
   cfg.attrs = &attr;
   // (beside the shared tokens' kernel, which has waited for the plan)
-  cfg.numAttrs = alone ? 0 : 1;
+  cfg.numAttrs = what == Tails::alone ? 0 : 1;
   e = cudaLaunchKernelEx(&cfg, tail_kernel<T, D, NT>, P, maps);
   if (e == cudaSuccess) {
     const int64_t threads = P.p.B * P.p.c.kv_heads * P.p.rows * (D / 4);
@@ -526,15 +526,15 @@ static rlk_status launch_tails(const TailParams& P, const TailMaps& maps, bool a
   return RLK_OK;
 }
 template <class T, int D>
-static rlk_status launch_tail_rows(const TailParams& P, const TailMaps& maps, int nt, bool alone, cudaStream_t st) {
+static rlk_status launch_tail_rows(const TailParams& P, const CacheMaps& maps, int nt, Tails what, cudaStream_t st) {
   switch (nt) {
-    case 1: return launch_tails<T, D, 1>(P, maps, alone, st);
-    case 2: return launch_tails<T, D, 2>(P, maps, alone, st);
-    default: return launch_tails<T, D, 3>(P, maps, alone, st);
+    case 1: return launch_tails<T, D, 1>(P, maps, what, st);
+    case 2: return launch_tails<T, D, 2>(P, maps, what, st);
+    default: return launch_tails<T, D, 3>(P, maps, what, st);
   }
 }
 
-rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool alone, cudaStream_t stream) {
+rlk_status attend_tails(const PrefixParts& parts, CacheMaps& maps, int head_dim, bool bf16, Tails what, cudaStream_t stream) {
   TailParams P{};
   P.p = parts;
   const TailTiles tt = tail_tiles(parts.rows);
@@ -542,15 +542,14 @@ rlk_status attend_tails(const PrefixParts& parts, int head_dim, bool bf16, bool 
   const int nt = tt.nt;
   P.box = box_of(parts.c.page_size, TSTEP);
   P.merged = P.box == TSTEP && head_dim == 128;
-  TailMaps maps{};
   rlk_status s;
-  if (parts.c.num_pages > 0) {
+  if (what == Tails::prepare && parts.c.num_pages > 0) {
     if ((s = map_cache(&maps.k, parts.c, parts.c.k, P.box, parts.head_first, P.merged ? 2 : 1, head_dim, bf16)) != RLK_OK) return s;
     if ((s = map_cache(&maps.v, parts.c, parts.c.v, P.box, parts.head_first, P.merged ? 2 : 1, head_dim, bf16)) != RLK_OK) return s;
   }
   if (head_dim == 128)
-    return bf16 ? launch_tail_rows<__nv_bfloat16, 128>(P, maps, nt, alone, stream) : launch_tail_rows<__half, 128>(P, maps, nt, alone, stream);
-  return bf16 ? launch_tail_rows<__nv_bfloat16, 64>(P, maps, nt, alone, stream) : launch_tail_rows<__half, 64>(P, maps, nt, alone, stream);
+    return bf16 ? launch_tail_rows<__nv_bfloat16, 128>(P, maps, nt, what, stream) : launch_tail_rows<__half, 128>(P, maps, nt, what, stream);
+  return bf16 ? launch_tail_rows<__nv_bfloat16, 64>(P, maps, nt, what, stream) : launch_tail_rows<__half, 64>(P, maps, nt, what, stream);
 }
 
 }  // namespace rlk

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import rollout_consistent_vocab_gb300 as pkg
+from rollout_consistent_vocab_gb300 import _binding as b
 from test_prefix_gpu import DEV, bits, compare, i32, make, run
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +65,25 @@ def test_every_sequence_that_a_missing_page_rejects_is_counted():
     table[0, 1] = -1
     raised, rejected = count(dict(c, table=table), [1 if b % 2 else 0 for b in range(24)])
     assert rejected == 10 and raised >= 10
+
+
+@pytest.mark.parametrize("dim,most,page", [(128, 64, 64), (64, 64, 16), (128, 0, 16)])
+def test_a_refused_cache_leaves_the_workspace_alone(dim, most, page):
+    # strides of 2^39 elements have no tensor map: nothing may be under way when the call says so
+    c = make([(3, 64)], [9, 9, 9], 1, 4, 2, dim, page, "bf16", seed=43)
+    tokens = page * c["table"].shape[1]
+    ws = torch.full((pkg.prefix_attention_workspace_bytes(3, 1, 4, 2, dim, tokens, 1, most),), 255, dtype=torch.uint8, device=DEV)
+    cache = b._make_cache(c["k"], c["v"], c["table"], c["lens"], None, 1, None)
+    groups = b.PrefixGroups(c["start"].data_ptr(), c["shared"].data_ptr(), 1, most)
+    out, strides = torch.zeros_like(c["q"]), b.BTHStrides(4 * dim, 0, dim)
+
+    def call():
+        status = pkg.load_library().rlk_prefix_attention(cache, groups, c["q"].data_ptr(), strides, 4, 0.1, out.data_ptr(), strides, None,
+                                                         ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        return status
+
+    cache.page_stride, stride = 2**40, cache.page_stride
+    assert call() == b.RLK_EINVAL and bool((ws == 255).all()) and not out.any()
+    cache.page_stride = stride
+    assert call() == b.RLK_OK and not bool((ws == 255).all())
