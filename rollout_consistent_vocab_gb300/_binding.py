@@ -1253,7 +1253,9 @@ def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_
     if shared_lens.get_device() != dev or group_start.get_device() != dev:
         _placed(shared_lens, dev, "shared_lens")
         _placed(group_start, dev, "group_start")
-    pg = PrefixGroups(group_start.data_ptr(), shared_lens.data_ptr(), groups, tokens if max_shared is None else max_shared)
+    # (a number that 32 bits do not hold is refused as the next one that they do hold)
+    most = tokens if max_shared is None else max(-1, min(max_shared, 2**31 - 1))
+    pg = PrefixGroups(group_start.data_ptr(), shared_lens.data_ptr(), groups, most)
     qs = _bth(q, shape, k_cache.dtype, "q", dev)
     new = torch.empty if stream is None else _maker(stream)
     if out is None:
@@ -1267,8 +1269,8 @@ def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_
         raise ValueError("out_lse must be a contiguous float32 tensor of shape [B, n, q_heads]")
     else:
         _placed(out_lse, dev, "out_lse")
-    need = prefix_attention_workspace_bytes(B, n, heads, kv_heads, dim, tokens, groups, max(pg.max_shared, 0)) \
-        if heads > 0 and heads % kv_heads == 0 and pg.max_shared <= tokens else 0
+    need = prefix_attention_workspace_bytes(B, n, heads, kv_heads, dim, tokens, groups, max(most, 0)) \
+        if heads > 0 and heads % kv_heads == 0 and most <= tokens else 0
     if workspace is None:
         workspace = (new if stream is None else _maker(stream, returned=False))(need, dtype=torch.uint8, device=q.device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():

@@ -87,3 +87,10 @@ def test_a_refused_cache_leaves_the_workspace_alone(dim, most, page):
     assert call() == b.RLK_EINVAL and bool((ws == 255).all()) and not out.any()
     cache.page_stride = stride
     assert call() == b.RLK_OK and not bool((ws == 255).all())
+
+
+def test_a_bound_past_32_bits_is_refused():
+    c = make([(2, 64)], [3, 4], 1, 4, 2, 64, 16, "bf16", seed=44)
+    for most in (2**31, 2**32, 2**32 + 64, -2**32 + 64, -2**63):
+        with pytest.raises(pkg.RlkError):
+            run(c, max_shared=most)
