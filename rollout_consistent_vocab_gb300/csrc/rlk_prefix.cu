@@ -638,6 +638,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Ca
     constexpr uint32_t IDESC_PV = IDESC | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17);
     begin();
     const int mine = warp - 8;
+    // whether a wait gave up: one answer for all lanes, which go on together
+    auto ended = [&]() { return __any_sync(0xffffffffu, *dead != 0u) != 0; };
     const uint32_t scores = tmem + mine * PTILE, result = tmem + 2 * PTILE + mine * 128;
     uint32_t n = 0, value_at = 0, key_at = 0, uses[2] = {0, 0}, blocks = 0, halves = 0;   // tiles, waits, halves of tiles so far
     // Both streams' warps go by every tile, so that neither is ever more than one round of the ring
@@ -661,8 +663,7 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Ca
         // the results of half a tile
         if (h * 64 < x.count) {
           wait(weighed + 16 * mine + 8 * h, uses[h]++);
-          __syncwarp();
-          if (!*dead) {
+          if (!ended()) {
             tc_fence_after();
             const uint64_t b = values_desc(ring + value_at % S_::STAGES * S_::TILE + h * S_::HALF, 64 * 128);
             if (elect_one()) {
@@ -688,9 +689,8 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Ca
           if (h == 0) {
             take(s, y, key_at);
             if (asks) wait(asked + 8 * mine, blocks++);
-            __syncwarp();
           }
-          if (!*dead) {
+          if (!ended()) {
             tc_fence_after();
             const uint64_t a = sw128_desc(queries + mine * S_::TILE), b = sw128_desc(ring + key_at % S_::STAGES * S_::TILE + h * S_::HALF);
             if (elect_one()) {

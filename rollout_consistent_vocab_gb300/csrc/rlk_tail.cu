@@ -250,7 +250,8 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ CacheM
 #pragma unroll 1
       for (int t0 = work_at.t; t0 < work_at.end; t0 += TSTEP) {
         if (more) copy();
-        if (!dead && !mbar_wait_phase(full + get * 8, phase)) {
+        // (one answer for all lanes: with some given up and some not, the next exchange would find no end)
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait_phase(full + get * 8, phase))) {
           dead = true;
           more = false;
         }
