@@ -1084,20 +1084,20 @@ _ROPE_FN = None
 
 def rope_autograd(x, inv_freq, positions, *, pair_axis=None, interleaved=False):
     """rope as a differentiable torch output.  Not to be captured into a graph while a backward
-    graph of the same leaf x, made on another stream, lives: refused (RuntimeError) where that one
-    came from here too."""
+    graph of the same leaf x, made on the default stream, lives (or its accumulation node is kept):
+    refused (RuntimeError) where that one came from here too."""
     global _ROPE_FN
     torch = _torch()
     if _ROPE_FN is None:
         _ROPE_FN = _rope_function()
     node = None
     if x.is_leaf and x.requires_grad and x.is_cuda and torch.is_grad_enabled():
-        # torch adds a leaf's gradient up on the stream that its first graph was made on, while any lives,
-        # and a capture that has to wait for another stream's work ends the process.
+        # torch adds a leaf's gradient up on the stream that its first graph was made on, while any lives.
+        # Any other stream joins a capture for that; the default one cannot, which ends the capture or the process.
         node = torch.autograd.graph.get_gradient_edge(x).node
-        here = torch.cuda.current_stream(x.device).cuda_stream
-        if node.metadata.setdefault("rlk_stream", here) != here and torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("x is a leaf of a backward graph made on another stream: drop that one before the capture")
+        first = node.metadata.setdefault("rlk_stream", torch.cuda.current_stream(x.device).cuda_stream)
+        if torch.cuda.is_current_stream_capturing() and first == torch.cuda.default_stream(x.device).cuda_stream:
+            raise RuntimeError("x is a leaf of a backward graph made on the default stream: drop that one before the capture")
     return _ROPE_FN.apply(x, inv_freq, positions, pair_axis, interleaved, False)
 
 
