@@ -4,12 +4,14 @@ cut into, and what a call that fails leaves behind.
 Inputs, float64 results and tolerances as in test_prefix_gpu.py; bits are compared as bits.
 """
 
+import math
+
 import pytest
 import torch
 
 import rollout_consistent_vocab_gb300 as pkg
 from rollout_consistent_vocab_gb300 import _binding as b
-from test_prefix_gpu import DEV, bits, compare, i32, make, run
+from test_prefix_gpu import DEV, DT, U, bits, compare, i32, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +96,51 @@ def test_a_bound_past_32_bits_is_refused():
     for most in (2**31, 2**32, 2**32 + 64, -2**32 + 64, -2**63):
         with pytest.raises(pkg.RlkError):
             run(c, max_shared=most)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_values_that_are_not_finite_are_not_lost_for_their_weight(bad, dtype):
+    """At a token whose weight is 0 in float32, shared or not, wherever it stands beside the weights that count."""
+    shared, n, page, dim = 5000, 9000, 64, 64
+    k = torch.zeros((-(-n // page) * page, 1, dim), dtype=DT[dtype], device=DEV)
+    table, q = torch.arange(k.shape[0] // page, dtype=torch.int32, device=DEV)[None], torch.zeros((1, 1, 1, dim), dtype=DT[dtype], device=DEV)
+    q[..., 0] = 1.0
+
+    def attended(scores, values):
+        k[:n, 0, 0] = scores.to(DT[dtype])
+        v = torch.ones_like(k)
+        v[:n, 0] = values.to(DT[dtype])[:, None]
+        out, lse = pkg.prefix_attention(q, k.view(-1, page, 1, dim), v.view(-1, page, 1, dim), table, i32([n]), i32([0, 1]), i32([shared]),
+                                        scale=1.0)
+        return out[0, 0, 0], lse[0, 0, 0]
+
+    for low in (-400.0, -math.inf):
+        for at, heavy in ((0, 8999), (8999, 0), (600, 10), (10, 600), (3, 40), (40, 3), (2500, 100), (4990, 5010), (5300, 8000), (6000, 5998)):
+            for every in (True, False):                          # all the others as light, or only those around
+                scores, values = torch.full((n,), low if every else 0.0, device=DEV), torch.ones(n, device=DEV)
+                scores[at // 512 * 512:at // 512 * 512 + 512] = low
+                scores[heavy] = 0.0
+                clean, lse = attended(scores, values)
+                assert bool(((clean - 1.0).abs() <= 2 * U[dtype]).all()), (low, at, heavy, every)
+                values[at] = bad
+                got, z = attended(scores, values)
+                assert not bool(torch.isfinite(got).any()), (low, at, heavy, every)
+                assert torch.equal(bits(z), bits(lse))
+
+
+def test_prompts_behind_a_shared_prefix():
+    """Hundreds of new tokens of each sequence, some of their rows against the oracle, and the bits of all."""
+    n, new = 300, [300, 277, 0, 1]
+    c = make([(3, 700)], [300, 310, 5, 2], n, 8, 2, 64, 16, "bf16", seed=45)
+    c["lens"] = i32([700 + 300, 700 + 310, 700 + 5, 2])
+    out, lse = run(c, new)
+    for b in (0, 1, 3):
+        for i in sorted({0, new[b] // 2, new[b] - 1}):
+            lens = c["lens"][b:b + 1] - new[b] + 1 + i
+            d = dict(c, q=c["q"][b:b + 1, i:i + 1], table=c["whole"][b:b + 1].to(DEV), whole=c["whole"][b:b + 1], lens=lens, start=i32([0, 1]),
+                     shared=i32([c["of"][b]]), of=c["of"][b:b + 1])
+            o, z = run(d)
+            compare(d, o, z, [1])
+            assert torch.equal(bits(o[0, 0]), bits(out[b, i])) and torch.equal(bits(z[0, 0]), bits(lse[b, i])), (b, i)
+        assert not out[b, new[b]:].any()
