@@ -146,7 +146,8 @@ rlk_status rlk_kv_append_rope(const rlk_kv_cache* cache, const rlk_rope_args* ro
  * Places i >= new_lens[b], and queries that see only tokens of score -inf, get
  * out = 0 and lse = -inf.  NaN and infinite keys, values or queries spread to the
  * outputs that see them only (the value of a masked token is never used; an
- * infinite one at a weight that is 0 in float32 makes NaN).  A rejected
+ * infinite one at a weight that is 0 in float32, or in f16 below 2^-32 of the
+ * row's largest, makes NaN).  A rejected
  * sequence gets NaN in out and lse: for all its places if its lengths are at
  * fault (as in rlk_kv_append), for its places i < new_lens[b] if the page
  * number of a visible token is out of range.
@@ -193,7 +194,7 @@ typedef struct rlk_prefix_groups {
  * its tokens are cut otherwise).
  * Precision is that of rlk_paged_attention, but for the weights of shared tokens
  * in f16: 22 bits, no finer than 2^-37 of the row's largest weight among up to
- * 2048 tokens.
+ * 2048 tokens (an infinite value at one below 2^-37 makes NaN).
  * n new tokens of all of a group's sequences are taken together, so that its
  * shared tokens are read once for 256 query rows of a kv head (n times the
  * query heads of one, times the sequences).  The sizes are limited:

@@ -52,6 +52,8 @@ template <> struct Elem<__nv_bfloat16> : OddElem<0x7F807F80u, 0x00800080u> {
   static constexpr float OFF = 0.0f, SLACK = 8.0f;
   static constexpr uint32_t EXP = 0x7F807F80u;
   static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
+  // whether both parts of a weight are above 0 (NaN's are not): a value that is not finite comes through as itself
+  static __device__ __forceinline__ bool counts(float w) { return w > 0.0f; }
   static constexpr float MORE = 1.0f + 2.384185791015625e-07f;   // 1 + 2^-22
   // The weights (a, b) >= 0 as the sum of two pairs of elements: hi is cut off, lo
   // is the rest and 2^-22 of the weight, a bias far below the result's own
@@ -89,6 +91,7 @@ template <> struct Elem<__half> : OddElem<0x7C007C00u, 0x04000400u> {
   static __device__ __forceinline__ float value(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
   static constexpr float TINY = 5.960464477539063e-08f;      // 2^-24, the smallest f16
   static constexpr float UP = 4096.0f, DOWN = 1.0f / 4096.0f;
+  static __device__ __forceinline__ bool counts(float w) { return w >= TINY; }
   // The rest of a weight with a high part is never 0 (at most one step of the rest too
   // much), so that an infinite value comes through as itself.
   static __device__ __forceinline__ float rest(float a, float h) {

@@ -625,8 +625,8 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
           for (int f = 0; f < 4; f += 2) s[y][f + e] = ex2f(__fmaf_rn(s[y][f + e], P.c2, sub));
       }
       // A masked token's value must not come in even as 0 * inf: where a masked slice
-      // holds values that are not finite, they go straight into the rows that see them
-      // (which they leave infinite or NaN), and the product takes zeros for them.
+      // holds values that are not finite, they go straight into the rows that see them, as
+      // the product would leave them (infinite, or NaN at a weight of 0), and it takes zeros for them.
       bool odd = false;
       if (masked) {
 #pragma unroll
@@ -644,6 +644,12 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
             // (what lies in a place that nobody sees is of no account, whatever it is)
             if (t >= cons.s.len || (t < cons.s.low && t >= P.sinks)) continue;
             const uint32_t row = (r < HALF ? sk[0] : sk[1]) + S_::KEYS + (r & (HALF - 1)) * 128;
+            bool w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float lo = r < HALF ? s[0][e] : s[1][e], hi = r < HALF ? s[0][2 + e] : s[1][2 + e];
+              w[e] = E::counts(__shfl_sync(0xffffffffu, (r & 8) == 0 ? lo : hi, (r & 7) * 4 + t4));
+            }
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -653,7 +659,7 @@ attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ AttnMa
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int i = query_of(P, row0 + 2 * t4 + e);
-                  if (t - p0 <= i && !(P.window > 0 && t - p0 <= i - P.window && t >= P.sinks)) o[d][2 * f + e] += E::value(bits);
+                  if (t - p0 <= i && !(P.window > 0 && t - p0 <= i - P.window && t >= P.sinks)) o[d][2 * f + e] += w[e] ? E::value(bits) : __int_as_float(0x7fc00000);
                 }
               }
           }

@@ -339,7 +339,8 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ CacheM
             for (int f = 0; f < 4; f += 2) s[x][f + e] = ex2f(__fmaf_rn(s[x][f + e], P.p.c2, sub));
           }
           // A masked token's value must not come in even as 0 * inf: values that are not finite go straight
-          // into the rows that see them (which they leave infinite or NaN), and the product takes zeros for them.
+          // into the rows that see them, as the product would leave them (infinite, or NaN at a weight of 0), and
+          // the product takes zeros for them.
           if (masked) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -349,6 +350,9 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ CacheM
               for (int r = 0; r < TSTEP; ++r) {
                 const int t = t0 + r;
                 if (t >= work_at.end) break;                       // (what lies in a place that nobody sees is of no account)
+                bool w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) w[e] = E::counts(__shfl_sync(0xffffffffu, r < 8 ? s[x][e] : s[x][2 + e], (r & 7) * 4 + t4));
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -357,7 +361,7 @@ tail_kernel(const __grid_constant__ TailParams P, const __grid_constant__ CacheM
                     if ((bits & E::EXP & 0xFFFFu) != (E::EXP & 0xFFFFu)) continue;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if (t - p0 <= row_query(P.p, row0 + x * 8 + 2 * t4 + e)) o[x][d][2 * f + e] += E::value(bits);
+                      if (t - p0 <= row_query(P.p, row0 + x * 8 + 2 * t4 + e)) o[x][d][2 * f + e] += w[e] ? E::value(bits) : __int_as_float(0x7fc00000);
                   }
               }
             }
