@@ -202,7 +202,10 @@ typedef struct rlk_prefix_groups {
  * below 2^31, and those over 128, plus the groups, times kv_heads and
  * max_shared / 512 + 4 below 2^31.
  *   workspace: of rlk_prefix_attention_workspace's size for max_tokens =
- *     max_pages * page_size, 16-byte aligned; not kept. */
+ *     max_pages * page_size, 16-byte aligned; not kept.  Every query row has room for
+ *     the result of each part of max_shared and of max_tokens tokens, 4 * head_dim + 8
+ *     bytes: 32 heads of 128 and a table of 8192 tokens, 256 sequences with one new
+ *     token 0.2 GB, 32 with 256 each 5.5 GB, with 2048 each 44 GB. */
 rlk_status rlk_prefix_attention(const rlk_kv_cache* cache, const rlk_prefix_groups* groups, const void* q,
                                 const rlk_bth_strides* q_strides, int32_t q_heads, float scale, void* out,
                                 const rlk_bth_strides* out_strides, float* out_lse, void* workspace, void* stream);

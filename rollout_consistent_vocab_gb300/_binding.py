@@ -1234,9 +1234,15 @@ def prefix_attention(q, k_cache, v_cache, page_table, lens, group_start, shared_
     pages are looked up in its first sequence's row of page_table).  Every new token comes
     after them.  ``max_shared``: what no shared length exceeds (None: what the page table
     holds); the scratch's size goes by it.  The rest as in paged_attention; ``workspace``:
-    uint8 [prefix_attention_workspace_bytes(...)].  A sequence's result does not depend on
-    what else is in its group or the batch.  Worth its four launches from groups of two on
-    where the batch is large, and of eight where there is one group alone."""
+    uint8 [prefix_attention_workspace_bytes(...)], which is allocated for the call if not
+    given: every new token has room for each part of as many tokens as the page table's rows
+    hold, several GB for hundreds of new tokens a sequence.  A sequence's result does not depend
+    on what else is in its group or the batch.
+
+    Worth its four launches where some 250 MB of keys and values need not be read again:
+    (members - 1) times the shared tokens' bytes, summed over the groups (8 heads of 128: one
+    group of 64 from 1024 shared tokens on, of 16 from 4096, of 8 from 8192; 16 groups of 16 from
+    256, of 4 from 1024, of 2 from 4096).  Below that paged_attention is up to a third faster."""
     lib = load_library()
     torch = _torch()
     if q.dim() != 4:

@@ -52,9 +52,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // The work of a group in units: 512 shared tokens of a kv head for up to 128 query rows.  An
 // item, a piece of a kv head for a block of up to 256 query rows, is so many of them.
 constexpr int PIECE_UNIT = 512, PROWS = 256;
-// What one costs, in steps of 16 own tokens for 8 query rows (a unit by itself is some 8 us of an SM, a step
-// 0.2 on the way through memory; 48 and 144 are slower by a tenth and more where neither is little;
-// a step of 64 elements is half as many bytes, a unit of them nearly as many exponentials.)
+// What one costs, in steps of 16 own tokens for 8 query rows (a step of 64 elements is half as many bytes, a unit
+// of them nearly as many exponentials).  By the times of 48, 72, 96 and 144: 8 x 16 samples with drafts 131, 112,
+// 123, 123 us, in f16 143, 123, 134, 134; 16 x 16 samples 150, 150, 150, 150, in f16 160, 153, 151, 154; 8 x 4 with
+// drafts and up to 20,000 own tokens 305, 245, 239, 236.  Of 60, 100, 140 and 200: uneven groups of 64 elements 166, 141, 143, 143.
 constexpr uint32_t UNIT_COST_128 = 72, UNIT_COST_64 = 100;
 constexpr int PSMS = 152;
 __device__ __forceinline__ uint32_t units_of_head(const PrefixParams& P, const GroupPlan& p) {
@@ -532,7 +533,9 @@ prefix_kernel(const __grid_constant__ PrefixParams P, const __grid_constant__ Ca
   tc_fence_after();
   const uint32_t tmem = *slot;
   Way way;
-  auto begin = [&]() {                   // the plan is made
+  // The plan is made.  (tail_kernel and the join read it without a wait of their own: they are launched by this
+  // kernel's signal, which must not come before the wait.)
+  auto begin = [&]() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     way.begin(P);
