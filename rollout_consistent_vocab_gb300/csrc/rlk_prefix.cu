@@ -5,8 +5,8 @@
 // down to 32, go in pieces of a length that depends on theirs alone; a piece's result
 // (maximum, sum, weighted sum of values of each query row) goes to the workspace.  Every
 // sequence's other tokens, and the join of all, are a kernel each of rlk_tail.cu.  16 prompts
-// of up to 8192 tokens with 16 samples each of up to 2048 more, 32 heads on 8 of 128: 786 MB, 148 us
-// = 5.3 TB/s; 2 of up to 131071 with 32 samples each: 999 MB, 215 us = 4.6 TB/s.
+// of up to 8192 tokens with 16 samples each of up to 2048 more, 32 heads on 8 of 128: 786 MB, 150 us
+// = 5.2 TB/s; 2 of up to 131071 with 32 samples each: 999 MB, 218 us = 4.6 TB/s (242 on another GB300).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
