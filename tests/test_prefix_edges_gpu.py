@@ -144,3 +144,39 @@ def test_prompts_behind_a_shared_prefix():
             compare(d, o, z, [1])
             assert torch.equal(bits(o[0, 0]), bits(out[b, i])) and torch.equal(bits(z[0, 0]), bits(lse[b, i])), (b, i)
         assert not out[b, new[b]:].any()
+
+
+def test_many_sequences_with_a_few_long_ones():
+    """More sequences than the plan has threads, own parts of three lengths, a workspace of just the size."""
+    B, page, dim = 1500, 64, 64
+    long = {0: 40000, 7: 16384, 8: 16385, 700: 33000, 1023: 32768, 1024: 32769, 1499: 20000}
+    tails = [long.get(b, 1 + (37 * b) % 90) for b in range(B)]
+    c = make([(700, 640), (500, 100)], tails, 1, 4, 2, dim, page, "bf16", seed=46, before=5)
+    need = pkg.prefix_attention_workspace_bytes(B, 1, 4, 2, dim, page * c["table"].shape[1], 2, 640)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+    out, lse = run(c, workspace=ws[:need], max_shared=640)
+    assert bool((ws[need:] == 255).all()) and bool(torch.isfinite(out).all())
+    compare(c, out, lse, [1] * B, rows=slice(0, B, 150))
+    for b in (0, 5, 7, 8, 700, 1023, 1024, 1200, 1499):
+        d = dict(c, q=c["q"][b:b + 1], table=c["whole"][b:b + 1].to(DEV), whole=c["whole"][b:b + 1], lens=c["lens"][b:b + 1], start=i32([0, 1]),
+                 shared=i32([c["of"][b]]), of=c["of"][b:b + 1])
+        o, z = run(d)
+        compare(d, o, z, [1])
+        assert torch.equal(bits(o[0]), bits(out[b])) and torch.equal(bits(z[0]), bits(lse[b])), b
+
+
+def test_a_captured_step_that_grows_past_a_length_of_parts():
+    c = make([(2, 64)], [16390, 32775, 16384], 2, 8, 2, 64, 16, "f16", seed=47)
+    lens = c["lens"].clone()
+    out, lse = run(c)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        run(c, out=out, out_lse=lse)
+    for back in (20, 8, 5, 2, 0, 16300, 1):
+        c["lens"].copy_(lens - back)
+        g.replay()
+        want, z = run(c)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want)) and torch.equal(bits(lse), bits(z))
+        compare(c, out, lse, [2] * 3)
